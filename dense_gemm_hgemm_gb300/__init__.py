@@ -27,6 +27,7 @@ __all__ = [
     "gemm_select_config", "gemm_tile_coords", "gemm_workspace_bytes", "gemm_status_string",
     "gemm_abi_version", "gemm_launch_empty", "gemm_run_splitk_noalloc", "gemm_noalloc_check",
     "gemm_noalloc_set_wait_test", "gemm_probe_mma_rate", "library", "DTYPES",
+    "ELEMS", "NormPlan", "EmbedPlan", "DistillPlan",
 ]
 
 GEMM_F16, GEMM_BF16, GEMM_I8_I32 = 0, 1, 2
@@ -38,7 +39,7 @@ STATUS_NAMES = {
     0: "GEMM_OK", 1: "GEMM_ERR_INVALID_ARG", 2: "GEMM_ERR_UNSUPPORTED", 3: "GEMM_ERR_ALIGNMENT",
     4: "GEMM_ERR_NO_DEVICE", 5: "GEMM_ERR_ARCH", 6: "GEMM_ERR_OOM", 7: "GEMM_ERR_TENSORMAP",
     8: "GEMM_ERR_LAUNCH", 9: "GEMM_ERR_DEVICE_TIMEOUT", 10: "GEMM_ERR_CUDA",
-    11: "GEMM_ERR_SCRATCH_LIMIT",
+    11: "GEMM_ERR_SCRATCH_LIMIT", 12: "GEMM_ERR_INDEX",
 }
 
 
@@ -111,6 +112,7 @@ def library() -> ctypes.CDLL:
                 "gemm_probe_mma_rate": ([i32, i32, vp, vp, vp, vp], i32),
                 "tma_intensity_run": ([i32, i32, ctypes.c_float, ctypes.c_float, vp, vp, i64, i32,
                                        vp, vp], i32),
+                **train.signatures(),
             }
             for name, (args, res) in sig.items():
                 fn = getattr(lib, name)
@@ -392,3 +394,7 @@ class Plan:
             self.close()
         except Exception:
             pass
+
+
+from . import train   # noqa: E402  (needs the names above)
+from .train import ELEMS, DistillPlan, EmbedPlan, NormPlan   # noqa: E402

@@ -834,6 +834,7 @@ const char* gemm_status_string(gemm_status_t s) {
         case GEMM_ERR_SCRATCH_LIMIT:
             return "GEMM_ERR_SCRATCH_LIMIT: split-K partials exceed the fixed 16 MiB scratch of "
                    "gemm_run_splitk_noalloc";
+        case GEMM_ERR_INDEX: return "GEMM_ERR_INDEX: a kernel met an id outside its range";
         default: return "unknown gemm_status_t";
     }
 }

@@ -1,0 +1,157 @@
+// train_common.cuh -- what the kernels of gemm_train.h share: element types,
+// reductions, the launch (programmatic dependent launch on the caller's stream)
+// and the host-side checks.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gemm_train.h"
+
+namespace gbt {
+
+// ---- element types ------------------------------------------------------------
+
+template <typename T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) {
+    return __bfloat162float(v);
+}
+
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+
+// An element of a matrix whose type is known at run time (small operands only).
+__device__ __forceinline__ float load_elem(const void* p, int64_t i, int elem) {
+    if (elem == GEMM_ELEM_F32) return static_cast<const float*>(p)[i];
+    if (elem == GEMM_ELEM_F16) return __half2float(static_cast<const __half*>(p)[i]);
+    return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+__device__ __forceinline__ int64_t load_index(const void* p, int64_t i, int type) {
+    return type == GEMM_INDEX_I64 ? static_cast<const int64_t*>(p)[i]
+                                  : static_cast<int64_t>(static_cast<const int32_t*>(p)[i]);
+}
+
+// ---- reductions ---------------------------------------------------------------
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// The previous kernel of the stream has finished and its writes are visible.
+__device__ __forceinline__ void wait_for_previous_kernel() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// The next kernel of the stream may be brought up (it waits as above itself).
+__device__ __forceinline__ void let_next_kernel_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ---- host ---------------------------------------------------------------------
+
+inline bool valid_elem(gemm_elem_t e) { return e >= GEMM_ELEM_F16 && e <= GEMM_ELEM_F32; }
+inline int elem_bytes(gemm_elem_t e) { return e == GEMM_ELEM_F32 ? 4 : 2; }
+inline bool valid_index(gemm_index_t t) { return t == GEMM_INDEX_I32 || t == GEMM_INDEX_I64; }
+inline int index_bytes(gemm_index_t t) { return t == GEMM_INDEX_I64 ? 8 : 4; }
+inline bool aligned(const void* p, int bytes) {
+    return (reinterpret_cast<uintptr_t>(p) & static_cast<uintptr_t>(bytes - 1)) == 0;
+}
+
+// The current device, which has to be an sm_103 part.
+inline gemm_status_t current_device(int* device, int* num_sms) {
+    int dev = -1, major = 0, minor = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_NO_DEVICE;
+    }
+    if (major != 10 || minor != 3) return GEMM_ERR_ARCH;
+    *device = dev;
+    return GEMM_OK;
+}
+
+inline gemm_status_t check_device(int device) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_NO_DEVICE;
+    }
+    return dev == device ? GEMM_OK : GEMM_ERR_INVALID_ARG;
+}
+
+inline gemm_status_t allocate(void** p, size_t bytes) {
+    if (cudaMalloc(p, bytes) == cudaSuccess) return GEMM_OK;
+    cudaGetLastError();
+    *p = nullptr;
+    return GEMM_ERR_OOM;
+}
+
+// Synchronise, then read and clear an error word that the kernels set to 1.
+inline gemm_status_t check_error_word(int32_t* word, void* stream_ptr) {
+    int32_t value = 0;
+    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream_ptr)) != cudaSuccess ||
+        cudaMemcpy(&value, word, sizeof(value), cudaMemcpyDeviceToHost) != cudaSuccess ||
+        (value != 0 && cudaMemset(word, 0, sizeof(value)) != cudaSuccess)) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    return value != 0 ? GEMM_ERR_INDEX : GEMM_OK;
+}
+
+// Launch with programmatic dependent launch: the kernel starts its first
+// instructions while the stream's previous kernel ends, and calls
+// wait_for_previous_kernel before it touches memory.
+template <typename... P, typename... A>
+gemm_status_t launch(void (*kernel)(P...), int64_t grid, int block, size_t smem, void* stream,
+                     int cluster, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(block));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cluster > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
+}
+
+// Calls f with a value of the element type.
+template <typename F>
+gemm_status_t with_elem(gemm_elem_t e, F f) {
+    if (e == GEMM_ELEM_F16) return f(__half());
+    if (e == GEMM_ELEM_BF16) return f(__nv_bfloat16());
+    return f(float());
+}
+
+}  // namespace gbt

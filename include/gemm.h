@@ -79,7 +79,8 @@ typedef enum {
     GEMM_ERR_LAUNCH = 8,          /* kernel launch failed */
     GEMM_ERR_DEVICE_TIMEOUT = 9,  /* a kernel wait ran out (reported by gemm_plan_check) */
     GEMM_ERR_CUDA = 10,           /* any other CUDA runtime error */
-    GEMM_ERR_SCRATCH_LIMIT = 11   /* gemm_run_splitk_noalloc: problem exceeds its fixed scratch */
+    GEMM_ERR_SCRATCH_LIMIT = 11,  /* gemm_run_splitk_noalloc: problem exceeds its fixed scratch */
+    GEMM_ERR_INDEX = 12           /* a kernel met an id outside its range (gemm_train.h's checks) */
 } gemm_status_t;
 
 /*
