@@ -39,6 +39,76 @@ __device__ __forceinline__ int64_t load_index(const void* p, int64_t i, int type
                                   : static_cast<int64_t>(static_cast<const int32_t*>(p)[i]);
 }
 
+// ---- packs: VEC elements that move as one access --------------------------------
+
+template <int BYTES> struct RawOf;
+template <> struct RawOf<16> { using type = uint4; };
+template <> struct RawOf<8> { using type = uint2; };
+template <> struct RawOf<4> { using type = uint32_t; };
+template <> struct RawOf<2> { using type = uint16_t; };
+
+template <typename T, int VEC>
+struct Pack {
+    typename RawOf<static_cast<int>(sizeof(T)) * VEC>::type raw;
+    __device__ __forceinline__ float get(int i) const {
+        return to_f32(reinterpret_cast<const T*>(&raw)[i]);
+    }
+    __device__ __forceinline__ void set(int i, float v) {
+        reinterpret_cast<T*>(&raw)[i] = from_f32<T>(v);
+    }
+    __device__ __forceinline__ void set_raw(int i, T v) { reinterpret_cast<T*>(&raw)[i] = v; }
+};
+
+// The first n of VEC elements at p (the rest zeros); p is aligned to the pack.
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> load_pack(const T* p, int64_t n) {
+    using Raw = decltype(Pack<T, VEC>::raw);
+    Pack<T, VEC> r;
+    if (n >= VEC) {
+        r.raw = *reinterpret_cast<const Raw*>(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) r.set_raw(i, i < n ? p[i] : from_f32<T>(0.f));
+    }
+    return r;
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void store_pack(T* p, int64_t n, const Pack<T, VEC>& v) {
+    using Raw = decltype(Pack<T, VEC>::raw);
+    if (n >= VEC) {
+        *reinterpret_cast<Raw*>(p) = v.raw;
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (i < n) p[i] = reinterpret_cast<const T*>(&v.raw)[i];
+    }
+}
+
+// VEC fp32 values as elements of G (several accesses where they are wider than 16 bytes).
+template <typename G, int VEC>
+__device__ __forceinline__ void load_values(const G* p, int64_t n, float (&v)[VEC]) {
+    constexpr int kPer = VEC * static_cast<int>(sizeof(G)) > 16 ? 16 / static_cast<int>(sizeof(G)) : VEC;
+#pragma unroll
+    for (int k = 0; k < VEC; k += kPer) {
+        const Pack<G, kPer> q = load_pack<G, kPer>(p + k, n - k);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) v[k + i] = q.get(i);
+    }
+}
+
+template <typename G, int VEC>
+__device__ __forceinline__ void store_values(G* p, int64_t n, const float (&v)[VEC]) {
+    constexpr int kPer = VEC * static_cast<int>(sizeof(G)) > 16 ? 16 / static_cast<int>(sizeof(G)) : VEC;
+#pragma unroll
+    for (int k = 0; k < VEC; k += kPer) {
+        Pack<G, kPer> q;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) q.set(i, v[k + i]);
+        store_pack<G, kPer>(p + k, n - k, q);
+    }
+}
+
 // ---- reductions ---------------------------------------------------------------
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -114,6 +184,11 @@ inline gemm_status_t check_error_word(int32_t* word, void* stream_ptr) {
         return GEMM_ERR_CUDA;
     }
     return value != 0 ? GEMM_ERR_INDEX : GEMM_OK;
+}
+
+// Rows of a matrix start at multiples of 16 bytes (so whole packs can move).
+inline bool rows_aligned(const void* p, int64_t ld, int bytes) {
+    return aligned(p, 16) && (ld * bytes) % 16 == 0;
 }
 
 // Launch with programmatic dependent launch: the kernel starts its first
