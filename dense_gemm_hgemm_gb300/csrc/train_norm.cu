@@ -7,12 +7,298 @@ struct gemm_norm_plan {
     int64_t max_rows, cols;
     gemm_elem_t elem, weight_elem;
     int device, num_sms;
+    float* partial;      // [2][blocks][cols] sums of the weight gradients
 };
 
 namespace gbt {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;      // of the kernels that loop over a row or a column
+constexpr int kMaxLanes = 1024;
+constexpr int kLaneCols = 16;      // columns a lane keeps in registers
+
+// ---- rows in registers ----------------------------------------------------------
+//
+// `lanes` threads (32 to 1024, a power of two) keep one row, kLaneCols columns each:
+// PACKS packs of VEC elements, pack k of lane l at column (k * lanes + l) * VEC.  A
+// block has BLOCK / lanes such groups, each with its own rows, and asks for its next
+// row before it works on the present one.  So a row is read once, and its statistics
+// are exact two-pass ones at no further traffic.
+
+template <typename T, int VEC, int PACKS>
+struct RowPacks {
+    Pack<T, VEC> p[PACKS];
+    __device__ __forceinline__ void load(const T* row, int lane, int lanes, int cols) {
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k) {
+            const int c = (k * lanes + lane) * VEC;
+            p[k] = load_pack<T, VEC>(row + c, cols - c);
+        }
+    }
+};
+
+// Sums over a group, in every lane: shuffles in the warp, then one exchange in shared
+// memory behind the group's own barrier.  Two exchange buffers in turn: a warp that is
+// a sum ahead has passed the barrier that the others reach only after their reads.
+template <int N>
+struct GroupSum {
+    float (*part)[N][32];    // [2][N][32] of the group
+    int lanes, barrier, turn;
+    __device__ __forceinline__ void operator()(float (&v)[N], int lane) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+        if (lanes == 32) return;
+        const int warps = lanes / 32, l = lane % 32;
+        if (l == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) part[turn][i][lane / 32] = v[i];
+        }
+        asm volatile("bar.sync %0, %1;" :: "r"(barrier), "r"(lanes) : "memory");
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = warp_sum(l < warps ? part[turn][i][l] : 0.f);
+        turn ^= 1;
+    }
+};
+
+template <typename T, typename W>
+struct ForwardArgs {
+    const T* x;
+    const W* gamma;
+    const W* beta;
+    T* y;
+    float* mean;
+    float* rstd;
+    int64_t ldx, ldy, rows;
+    float eps;
+    int cols, lanes;
+};
+
+// KEEP: gamma and beta stay in registers over the rows (else they are read for each
+// row, where the block's registers would not suffice).
+template <typename T, typename W, int VEC, int BLOCK, bool KEEP>
+__global__ void __launch_bounds__(BLOCK) norm_forward_kernel(const ForwardArgs<T, W> a) {
+    constexpr int PACKS = kLaneCols / VEC;
+    __shared__ float part[BLOCK / 32][2][1][32];
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    const int lanes = a.lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * (BLOCK / lanes);
+    int64_t row = static_cast<int64_t>(blockIdx.x) * (BLOCK / lanes) + group;
+    if (row >= a.rows) return;
+    GroupSum<1> sum{part[group], lanes, 1 + group, 0};
+    RowPacks<T, VEC, PACKS> next;
+    next.load(a.x + row * a.ldx, lane, lanes, a.cols);
+    float gamma[PACKS][VEC], beta[PACKS][VEC];
+    const auto load_weights = [&] {
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k) {
+            const int c = (k * lanes + lane) * VEC;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                gamma[k][i] = 1.f;
+                beta[k][i] = 0.f;
+            }
+            if (a.gamma) load_values<W, VEC>(a.gamma + c, a.cols - c, gamma[k]);
+            if (a.beta) load_values<W, VEC>(a.beta + c, a.cols - c, beta[k]);
+        }
+    };
+    if (KEEP) load_weights();
+    const float n = static_cast<float>(a.cols);
+    for (; row < a.rows; row += step) {
+        float v[PACKS][VEC];
+        float s[1] = {0.f};
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                v[k][i] = next.p[k].get(i);      // (columns past the row's end are zeros)
+                s[0] += v[k][i];
+            }
+        }
+        if (row + step < a.rows) next.load(a.x + (row + step) * a.ldx, lane, lanes, a.cols);
+        sum(s, lane);
+        const float mu = s[0] / n;
+        s[0] = 0.f;
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k) {
+            const int left = a.cols - (k * lanes + lane) * VEC;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                v[k][i] -= mu;
+                if (i < left) s[0] += v[k][i] * v[k][i];
+            }
+        }
+        sum(s, lane);
+        const float r = 1.f / sqrtf(s[0] / n + a.eps);
+        if (!KEEP) load_weights();
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k) {
+            const int c = (k * lanes + lane) * VEC;
+            Pack<T, VEC> out;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) out.set(i, v[k][i] * r * gamma[k][i] + beta[k][i]);
+            store_pack<T, VEC>(a.y + row * a.ldy + c, a.cols - c, out);
+        }
+        if (lane == 0) {
+            if (a.mean) a.mean[row] = mu;
+            if (a.rstd) a.rstd[row] = r;
+        }
+    }
+}
+
+template <typename T, typename W>
+struct BackwardArgs {
+    const T* x;
+    const W* gamma;
+    const float* mean;
+    const float* rstd;
+    const T* dy;
+    T* dx;
+    float* partial;      // [2][gridDim.x][cols]
+    int64_t ldx, lddy, lddx, rows;
+    int cols, lanes;
+    bool weights;        // dgamma or dbeta is wanted
+};
+
+// dx of each row, and the block's sums of dy * xh and dy over its rows: each lane adds
+// up its own columns, in registers (SHARED: in shared memory, where a block of 1024
+// threads has no registers left for them); the groups of a block are joined at the end.
+template <typename T, typename W, int VEC, int BLOCK, bool SHARED>
+__global__ void __launch_bounds__(BLOCK) norm_backward_kernel(const BackwardArgs<T, W> a) {
+    constexpr int PACKS = kLaneCols / VEC;
+    extern __shared__ float join[];      // [2][lanes * kLaneCols]
+    __shared__ float part[BLOCK / 32][2][2][32];
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    const int lanes = a.lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+    const int groups = BLOCK / lanes;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group;
+    GroupSum<2> sum{part[group], lanes, 1 + group, 0};
+    float dg[PACKS][VEC], db[PACKS][VEC], gamma[PACKS][VEC];
+    // sum `which` of the lane's column i of pack k
+    const auto mine = [&](int which, int k, int i) -> float& {
+        return join[(which * kLaneCols + k * VEC + i) * lanes + lane];
+    };
+#pragma unroll
+    for (int k = 0; k < PACKS; ++k) {
+        const int c = (k * lanes + lane) * VEC;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            gamma[k][i] = 1.f;
+            if (SHARED)
+                mine(0, k, i) = mine(1, k, i) = 0.f;
+            else
+                dg[k][i] = db[k][i] = 0.f;
+        }
+        if (!SHARED && a.gamma) load_values<W, VEC>(a.gamma + c, a.cols - c, gamma[k]);
+    }
+    RowPacks<T, VEC, PACKS> next_x, next_dy;
+    float next_mean = 0.f, next_rstd = 0.f;
+    const auto ask = [&](int64_t r) {
+        next_x.load(a.x + r * a.ldx, lane, lanes, a.cols);
+        next_dy.load(a.dy + r * a.lddy, lane, lanes, a.cols);
+        next_mean = a.mean[r];
+        next_rstd = a.rstd[r];
+    };
+    if (row < a.rows) ask(row);
+    const float n = static_cast<float>(a.cols);
+    for (; row < a.rows; row += step) {
+        const RowPacks<T, VEC, PACKS> x = next_x, dy = next_dy;
+        const float mu = next_mean, r = next_rstd;
+        if (row + step < a.rows) ask(row + step);
+        if (SHARED && a.gamma) {
+#pragma unroll
+            for (int k = 0; k < PACKS; ++k) {
+                const int c = (k * lanes + lane) * VEC;
+                load_values<W, VEC>(a.gamma + c, a.cols - c, gamma[k]);
+            }
+        }
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                // past the row's end dy, and so every sum's term, is zero
+                const float hat = (x.p[k].get(i) - mu) * r, d = dy.p[k].get(i), g = d * gamma[k][i];
+                s[0] += g;
+                s[1] += g * hat;
+                if (SHARED) {
+                    mine(0, k, i) += d * hat;
+                    mine(1, k, i) += d;
+                } else {
+                    dg[k][i] += d * hat;
+                    db[k][i] += d;
+                }
+            }
+        }
+        if (!a.dx) continue;
+        sum(s, lane);
+        const float mean_g = s[0] / n, mean_gx = s[1] / n;
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k) {
+            const int c = (k * lanes + lane) * VEC;
+            Pack<T, VEC> out;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const float hat = (x.p[k].get(i) - mu) * r, g = dy.p[k].get(i) * gamma[k][i];
+                out.set(i, r * (g - mean_g - hat * mean_gx));
+            }
+            store_pack<T, VEC>(a.dx + row * a.lddx + c, a.cols - c, out);
+        }
+    }
+    if (!a.weights) return;
+    if (!SHARED) {
+        for (int g = 0; g < groups; ++g) {       // the groups in turn
+            if (group == g) {
+#pragma unroll
+                for (int k = 0; k < PACKS; ++k) {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        mine(0, k, i) = g == 0 ? dg[k][i] : mine(0, k, i) + dg[k][i];
+                        mine(1, k, i) = g == 0 ? db[k][i] : mine(1, k, i) + db[k][i];
+                    }
+                }
+            }
+            __syncthreads();
+        }
+    } else {
+        __syncthreads();
+    }
+    for (int which = 0; which < 2; ++which) {
+        float* out = a.partial + (static_cast<int64_t>(which) * gridDim.x + blockIdx.x) * a.cols;
+        for (int c = threadIdx.x; c < a.cols; c += BLOCK) {
+            const int pack = c / VEC;            // column c is element c % VEC of this pack
+            out[c] = join[(which * kLaneCols + pack / lanes * VEC + c % VEC) * lanes + pack % lanes];
+        }
+    }
+}
+
+// The blocks' sums of 32 columns: eight warps take every eighth block, then join.
+template <typename W>
+__global__ void __launch_bounds__(kThreads)
+norm_weight_join_kernel(const float* partial, int blocks, int cols, W* dgamma, W* dbeta) {
+    __shared__ float part[kThreads / 32][32];
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    const int tiles = (cols + 31) / 32;
+    const int which = blockIdx.x / tiles;
+    W* out = which == 0 ? dgamma : dbeta;
+    if (!out) return;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t c = static_cast<int64_t>(blockIdx.x % tiles) * 32 + lane;
+    float s = 0.f;
+    if (c < cols)
+        for (int b = warp; b < blocks; b += kThreads / 32)
+            s += partial[(static_cast<int64_t>(which) * blocks + b) * cols + c];
+    part[warp][lane] = s;
+    __syncthreads();
+    if (warp != 0 || c >= cols) return;
+    for (int w = 1; w < kThreads / 32; ++w) s += part[w][lane];
+    out[c] = from_f32<W>(s);
+}
+
+// ---- rows too wide for the registers of a block ------------------------------------
 
 // The sum over the block, in every thread.
 __device__ float block_sum(float v) {
@@ -28,77 +314,72 @@ __device__ float block_sum(float v) {
 
 // One block a row: three passes over the row (sum, squares about the mean, result).
 template <typename T, typename W>
-__global__ void __launch_bounds__(kThreads)
-norm_forward_kernel(const T* x, int64_t ldx, const W* gamma, const W* beta, float eps, T* y,
-                    int64_t ldy, float* mean, float* rstd, int cols) {
+__global__ void __launch_bounds__(kThreads) norm_forward_wide_kernel(const ForwardArgs<T, W> a) {
     wait_for_previous_kernel();
     const int64_t row = blockIdx.x;
-    const T* xr = x + row * ldx;
-    T* yr = y + row * ldy;
+    const T* x = a.x + row * a.ldx;
+    T* y = a.y + row * a.ldy;
     float s = 0.f;
-    for (int c = threadIdx.x; c < cols; c += kThreads) s += to_f32(xr[c]);
-    const float mu = block_sum(s) / static_cast<float>(cols);
+    for (int c = threadIdx.x; c < a.cols; c += kThreads) s += to_f32(x[c]);
+    const float mu = block_sum(s) / static_cast<float>(a.cols);
     s = 0.f;
-    for (int c = threadIdx.x; c < cols; c += kThreads) {
-        const float d = to_f32(xr[c]) - mu;
+    for (int c = threadIdx.x; c < a.cols; c += kThreads) {
+        const float d = to_f32(x[c]) - mu;
         s += d * d;
     }
-    const float r = 1.f / sqrtf(block_sum(s) / static_cast<float>(cols) + eps);
-    for (int c = threadIdx.x; c < cols; c += kThreads) {
-        const float g = gamma ? to_f32(gamma[c]) : 1.f, b = beta ? to_f32(beta[c]) : 0.f;
-        yr[c] = from_f32<T>((to_f32(xr[c]) - mu) * r * g + b);
+    const float r = 1.f / sqrtf(block_sum(s) / static_cast<float>(a.cols) + a.eps);
+    for (int c = threadIdx.x; c < a.cols; c += kThreads) {
+        const float g = a.gamma ? to_f32(a.gamma[c]) : 1.f, b = a.beta ? to_f32(a.beta[c]) : 0.f;
+        y[c] = from_f32<T>((to_f32(x[c]) - mu) * r * g + b);
     }
     if (threadIdx.x == 0) {
-        if (mean) mean[row] = mu;
-        if (rstd) rstd[row] = r;
+        if (a.mean) a.mean[row] = mu;
+        if (a.rstd) a.rstd[row] = r;
     }
 }
 
 // One block a row: the row's two sums, then dx.
 template <typename T, typename W>
-__global__ void __launch_bounds__(kThreads)
-norm_dx_kernel(const T* x, int64_t ldx, const W* gamma, const float* mean, const float* rstd,
-               const T* dy, int64_t lddy, T* dx, int64_t lddx, int cols) {
+__global__ void __launch_bounds__(kThreads) norm_dx_wide_kernel(const BackwardArgs<T, W> a) {
     wait_for_previous_kernel();
     const int64_t row = blockIdx.x;
-    const T* xr = x + row * ldx;
-    const T* dyr = dy + row * lddy;
-    const float mu = mean[row], r = rstd[row];
+    const T* x = a.x + row * a.ldx;
+    const T* dy = a.dy + row * a.lddy;
+    const float mu = a.mean[row], r = a.rstd[row];
     float sg = 0.f, sgx = 0.f;
-    for (int c = threadIdx.x; c < cols; c += kThreads) {
-        const float g = to_f32(dyr[c]) * (gamma ? to_f32(gamma[c]) : 1.f);
+    for (int c = threadIdx.x; c < a.cols; c += kThreads) {
+        const float g = to_f32(dy[c]) * (a.gamma ? to_f32(a.gamma[c]) : 1.f);
         sg += g;
-        sgx += g * ((to_f32(xr[c]) - mu) * r);
+        sgx += g * ((to_f32(x[c]) - mu) * r);
     }
-    sg = block_sum(sg) / static_cast<float>(cols);
-    sgx = block_sum(sgx) / static_cast<float>(cols);
-    for (int c = threadIdx.x; c < cols; c += kThreads) {
-        const float g = to_f32(dyr[c]) * (gamma ? to_f32(gamma[c]) : 1.f);
-        dx[row * lddx + c] = from_f32<T>(r * (g - sg - (to_f32(xr[c]) - mu) * r * sgx));
+    sg = block_sum(sg) / static_cast<float>(a.cols);
+    sgx = block_sum(sgx) / static_cast<float>(a.cols);
+    for (int c = threadIdx.x; c < a.cols; c += kThreads) {
+        const float g = to_f32(dy[c]) * (a.gamma ? to_f32(a.gamma[c]) : 1.f);
+        a.dx[row * a.lddx + c] = from_f32<T>(r * (g - sg - (to_f32(x[c]) - mu) * r * sgx));
     }
 }
 
 // One block per 32 columns: eight warps take every eighth row, then join.
 template <typename T, typename W>
 __global__ void __launch_bounds__(kThreads)
-norm_weight_grad_kernel(const T* x, int64_t ldx, const float* mean, const float* rstd, const T* dy,
-                        int64_t lddy, int64_t rows, int cols, W* dgamma, W* dbeta) {
+norm_weight_grad_wide_kernel(const BackwardArgs<T, W> a, W* dgamma, W* dbeta) {
     __shared__ float part[2][kThreads / 32][32];
     wait_for_previous_kernel();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     float dg = 0.f, db = 0.f;
-    if (c < cols) {
-        for (int64_t row = warp; row < rows; row += kThreads / 32) {
-            const float d = to_f32(dy[row * lddy + c]);
-            dg += d * ((to_f32(x[row * ldx + c]) - mean[row]) * rstd[row]);
+    if (c < a.cols) {
+        for (int64_t row = warp; row < a.rows; row += kThreads / 32) {
+            const float d = to_f32(a.dy[row * a.lddy + c]);
+            dg += d * ((to_f32(a.x[row * a.ldx + c]) - a.mean[row]) * a.rstd[row]);
             db += d;
         }
     }
     part[0][warp][lane] = dg;
     part[1][warp][lane] = db;
     __syncthreads();
-    if (warp == 0 && c < cols) {
+    if (warp == 0 && c < a.cols) {
         dg = db = 0.f;
         for (int w = 0; w < kThreads / 32; ++w) {
             dg += part[0][w][lane];
@@ -107,6 +388,61 @@ norm_weight_grad_kernel(const T* x, int64_t ldx, const float* mean, const float*
         if (dgamma) dgamma[c] = from_f32<W>(dg);
         if (dbeta) dbeta[c] = from_f32<W>(db);
     }
+}
+
+// ---- launches ----------------------------------------------------------------------
+
+// Lanes that keep a row of `cols` columns.
+int lanes_for(int64_t cols) {
+    int lanes = 32;
+    while (static_cast<int64_t>(lanes) * kLaneCols < cols) lanes *= 2;
+    return lanes;
+}
+
+bool in_registers(int64_t cols) { return cols <= static_cast<int64_t>(kMaxLanes) * kLaneCols; }
+
+template <typename T, typename W, int VEC, int BLOCK, bool KEEP>
+gemm_status_t forward_rows(const ForwardArgs<T, W>& a, int sms, void* stream) {
+    const auto kernel = norm_forward_kernel<T, W, VEC, BLOCK, KEEP>;
+    const int groups = BLOCK / a.lanes;
+    const int64_t blocks = (a.rows + groups - 1) / groups;
+    const int64_t most = static_cast<int64_t>(sms) * (2048 / BLOCK);
+    return launch(kernel, blocks < most ? blocks : most, BLOCK, 0, stream, 1, a);
+}
+
+template <typename T, typename W, int VEC>
+gemm_status_t forward_vec(const ForwardArgs<T, W>& a, int sms, void* stream) {
+    if (a.lanes <= 256) return forward_rows<T, W, VEC, 256, true>(a, sms, stream);
+    if (a.lanes == 512) return forward_rows<T, W, VEC, 512, true>(a, sms, stream);
+    return forward_rows<T, W, VEC, 1024, false>(a, sms, stream);
+}
+
+template <typename T, typename W, int VEC, int BLOCK, bool SHARED>
+gemm_status_t backward_rows(const BackwardArgs<T, W>& a, int blocks, void* stream) {
+    const auto kernel = norm_backward_kernel<T, W, VEC, BLOCK, SHARED>;
+    const size_t smem = a.weights ? static_cast<size_t>(a.lanes) * kLaneCols * 2 * sizeof(float) : 0;
+    // (SHARED keeps its sums there whether they are wanted or not)
+    const size_t want = SHARED ? static_cast<size_t>(a.lanes) * kLaneCols * 2 * sizeof(float) : smem;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(want)) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return launch(kernel, blocks, BLOCK, want, stream, 1, a);
+}
+
+// Blocks of a backward launch over `rows` rows, and the block size for `lanes`.
+int backward_block(int lanes) { return lanes <= 512 ? 512 : 1024; }
+int64_t backward_blocks(int64_t rows, int lanes, int sms) {
+    const int groups = backward_block(lanes) / lanes;
+    const int64_t blocks = (rows + groups - 1) / groups;
+    return blocks < sms ? blocks : sms;
+}
+
+template <typename T, typename W, int VEC>
+gemm_status_t backward_vec(const BackwardArgs<T, W>& a, int blocks, void* stream) {
+    if (a.lanes <= 512) return backward_rows<T, W, VEC, 512, false>(a, blocks, stream);
+    return backward_rows<T, W, VEC, 1024, true>(a, blocks, stream);
 }
 
 // Calls f with values of the plan's element and weight types.
@@ -134,8 +470,18 @@ gemm_status_t gemm_norm_plan_create(int64_t max_rows, int64_t cols, gemm_elem_t 
     int device = 0, sms = 0;
     const gemm_status_t st = gbt::current_device(&device, &sms);
     if (st != GEMM_OK) return st;
+    void* partial = nullptr;
+    if (max_rows > 0 && gbt::in_registers(cols)) {
+        const int64_t blocks = gbt::backward_blocks(max_rows, gbt::lanes_for(cols), sms);
+        const gemm_status_t room = gbt::allocate(&partial, static_cast<size_t>(blocks * cols) * 2 * sizeof(float));
+        if (room != GEMM_OK) return room;
+    }
     gemm_norm_plan* p = new (std::nothrow) gemm_norm_plan();
-    if (!p) return GEMM_ERR_OOM;
+    if (!p) {
+        cudaFree(partial);
+        return GEMM_ERR_OOM;
+    }
+    p->partial = static_cast<float*>(partial);
     p->max_rows = max_rows;
     p->cols = cols;
     p->elem = elem;
@@ -160,10 +506,17 @@ gemm_status_t gemm_norm_forward(gemm_norm_plan_t p, int64_t rows, const void* x,
     return gbt::with_types(p, [&](auto t, auto v) {
         using T = decltype(t);
         using W = decltype(v);
-        return gbt::launch(gbt::norm_forward_kernel<T, W>, rows, gbt::kThreads, 0, stream, 1,
-                           static_cast<const T*>(x), ldx, static_cast<const W*>(gamma),
-                           static_cast<const W*>(beta), eps, static_cast<T*>(y), ldy, mean, rstd,
-                           static_cast<int>(p->cols));
+        const gbt::ForwardArgs<T, W> a{static_cast<const T*>(x), static_cast<const W*>(gamma),
+                                       static_cast<const W*>(beta), static_cast<T*>(y), mean, rstd,
+                                       ldx, ldy, rows, eps, static_cast<int>(p->cols),
+                                       gbt::lanes_for(p->cols)};
+        if (!gbt::in_registers(p->cols))
+            return gbt::launch(gbt::norm_forward_wide_kernel<T, W>, rows, gbt::kThreads, 0, stream, 1, a);
+        const bool vec = gbt::rows_aligned(x, ldx, e) && gbt::rows_aligned(y, ldy, e) &&
+                         gbt::aligned(gamma, 16) && gbt::aligned(beta, 16);
+        constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+        return vec ? gbt::forward_vec<T, W, kVec>(a, p->num_sms, stream)
+                   : gbt::forward_vec<T, W, 1>(a, p->num_sms, stream);
     });
 }
 
@@ -185,25 +538,44 @@ gemm_status_t gemm_norm_backward(gemm_norm_plan_t p, int64_t rows, const void* x
     return gbt::with_types(p, [&](auto t, auto v) {
         using T = decltype(t);
         using W = decltype(v);
+        W* dg = static_cast<W*>(dgamma);
+        W* db = static_cast<W*>(dbeta);
+        const int lanes = gbt::lanes_for(p->cols);
+        gbt::BackwardArgs<T, W> a{static_cast<const T*>(x), static_cast<const W*>(gamma), mean, rstd,
+                                  static_cast<const T*>(dy), static_cast<T*>(dx), p->partial, ldx,
+                                  lddy, lddx, rows, static_cast<int>(p->cols), lanes, dg || db};
+        const int tiles = static_cast<int>((p->cols + 31) / 32);
         gemm_status_t s = GEMM_OK;
-        // (the weight's gradients first: dx may overwrite dy or x)
-        if (dgamma || dbeta)
-            s = gbt::launch(gbt::norm_weight_grad_kernel<T, W>, (p->cols + 31) / 32, gbt::kThreads,
-                            0, stream, 1, static_cast<const T*>(x), ldx, mean, rstd,
-                            static_cast<const T*>(dy), lddy, rows, static_cast<int>(p->cols),
-                            static_cast<W*>(dgamma), static_cast<W*>(dbeta));
-        if (s == GEMM_OK && dx && rows > 0)
-            s = gbt::launch(gbt::norm_dx_kernel<T, W>, rows, gbt::kThreads, 0, stream, 1,
-                            static_cast<const T*>(x), ldx, static_cast<const W*>(gamma), mean, rstd,
-                            static_cast<const T*>(dy), lddy, static_cast<T*>(dx), lddx,
-                            static_cast<int>(p->cols));
+        if (!gbt::in_registers(p->cols)) {
+            // (the weight's gradients first: dx may overwrite dy or x)
+            if (a.weights)
+                s = gbt::launch(gbt::norm_weight_grad_wide_kernel<T, W>, tiles, gbt::kThreads, 0, stream,
+                                1, a, dg, db);
+            if (s == GEMM_OK && dx && rows > 0)
+                s = gbt::launch(gbt::norm_dx_wide_kernel<T, W>, rows, gbt::kThreads, 0, stream, 1, a);
+            return s;
+        }
+        const int blocks = static_cast<int>(gbt::backward_blocks(rows, lanes, p->num_sms));
+        if (blocks > 0) {
+            const bool vec = gbt::rows_aligned(x, ldx, e) && gbt::rows_aligned(dy, lddy, e) &&
+                             (!dx || gbt::rows_aligned(dx, lddx, e)) && gbt::aligned(gamma, 16);
+            constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+            s = vec ? gbt::backward_vec<T, W, kVec>(a, blocks, stream)
+                    : gbt::backward_vec<T, W, 1>(a, blocks, stream);
+        }
+        if (s == GEMM_OK && a.weights)
+            s = gbt::launch(gbt::norm_weight_join_kernel<W>, 2 * tiles, gbt::kThreads, 0, stream, 1,
+                            p->partial, blocks, static_cast<int>(p->cols), dg, db);
         return s;
     });
 }
 
 gemm_status_t gemm_norm_plan_destroy(gemm_norm_plan_t p) {
+    if (!p) return GEMM_OK;
+    const gemm_status_t st = cudaFree(p->partial) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+    if (st != GEMM_OK) cudaGetLastError();
     delete p;
-    return GEMM_OK;
+    return st;
 }
 
 }  // extern "C"
