@@ -109,6 +109,13 @@ __device__ __forceinline__ void store_values(G* p, int64_t n, const float (&v)[V
     }
 }
 
+// 2^v to two units in the last place (results below 2^-126 are zero).
+__device__ __forceinline__ float exp2_fast(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // ---- reductions ---------------------------------------------------------------
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -174,7 +181,11 @@ inline gemm_status_t allocate(void** p, size_t bytes) {
     return GEMM_ERR_OOM;
 }
 
-// Synchronise, then read and clear an error word that the kernels set to 1.
+// Bits of an error word.
+constexpr int32_t kErrorIndex = 1;
+constexpr int32_t kErrorTimeout = 2;
+
+// Synchronise, then read and clear an error word.
 inline gemm_status_t check_error_word(int32_t* word, void* stream_ptr) {
     int32_t value = 0;
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream_ptr)) != cudaSuccess ||
@@ -183,6 +194,7 @@ inline gemm_status_t check_error_word(int32_t* word, void* stream_ptr) {
         cudaGetLastError();
         return GEMM_ERR_CUDA;
     }
+    if (value & kErrorTimeout) return GEMM_ERR_DEVICE_TIMEOUT;
     return value != 0 ? GEMM_ERR_INDEX : GEMM_OK;
 }
 

@@ -17,8 +17,15 @@ namespace gbt {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTop = 1024;
+constexpr int kMaxCluster = 8;                 // blocks that share a row
+constexpr int kPieceBytes = 32 * 1024;         // of a row that a block aims to hold
+constexpr int kMostPieceBytes = 200 * 1024;    // ... and can hold
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+enum Mode { kForward = 1, kBackward = 2, kBoth = 3 };
 
 struct Teacher {
     const void* ids;
@@ -28,134 +35,436 @@ struct Teacher {
     int top, id_type, value_elem;
 };
 
-// A row's teacher entries in shared memory: ids (-1 = no entry), log2 of the
-// probabilities and the probabilities; `mass` is their sum.
-struct Entries {
-    int32_t id[kMaxTop];
-    float log2p[kMaxTop];
-    float p[kMaxTop];
-    float part[kThreads / 32];
-    float mass;
+template <typename T>
+struct Args {
+    const T* logits;
+    T* dlogits;
+    const float* dloss;
+    float* loss;
+    float* lse;
+    int32_t* error;
+    Teacher teacher;
+    int64_t ldl, ldd;
+    float temperature;
+    int vocab, piece;      // elements; a piece is a multiple of the pack
+    int pieces;            // of a row: blocks that share it
 };
 
-__device__ float block_reduce(float v, bool is_max, float* part) {
-    v = is_max ? warp_max(v) : warp_sum(v);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
-    __syncthreads();
-    v = part[0];
-    for (int w = 1; w < kThreads / 32; ++w) v = is_max ? fmaxf(v, part[w]) : v + part[w];
-    return v;
+// ---- asynchronous copies ----------------------------------------------------------
+
+__device__ __forceinline__ uint32_t shared_address(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-// Scaled logits are kept as log2 values: c = log2(e) / temperature.
-__device__ void load_entries(Entries& en, const Teacher& t, int64_t row, float c, int64_t vocab,
-                             int32_t* error) {
+// Waits for a phase of the barrier, at most about two seconds.
+__device__ bool wait_phase(uint64_t* barrier, uint32_t parity) {
+    const uint32_t at = shared_address(barrier);
+    long long began = 0;
+    for (uint32_t tries = 0;; ++tries) {
+        uint32_t done;
+        asm volatile(
+            "{\n.reg .pred p;\n"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+            "selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(done) : "r"(at), "r"(parity) : "memory");
+        if (done) return true;
+        long long now;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        if (tries == 0) began = now;
+        if (now - began > 2000000000ll) return false;
+    }
+}
+
+// The elements of [src, src + n) into shared memory at dst, which has src's offset
+// from a 16-byte boundary: one thread starts a bulk copy of the whole 16-byte units
+// (counted on the barrier), all threads copy the ragged ends.  Past the ends, up to
+// the 16-byte boundaries, go -infinities.
+template <typename T>
+__device__ __forceinline__ void start_copy(T* dst, const T* src, int n, uint64_t* barrier) {
+    constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15u) / sizeof(T));
+    int head = (VEC - off) % VEC;                    // elements before the first boundary
+    if (head > n) head = n;
+    const int body = (n - head) / VEC * VEC, tail = n - head - body;
+    if (threadIdx.x == 0) {
+        const uint32_t bytes = static_cast<uint32_t>(body * static_cast<int>(sizeof(T)));
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
+                     :: "r"(shared_address(barrier)), "r"(bytes) : "memory");
+        if (bytes > 0)
+            asm volatile(
+                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                :: "r"(shared_address(dst + head)), "l"(src + head), "r"(bytes),
+                   "r"(shared_address(barrier)) : "memory");
+    }
+    if (threadIdx.x < VEC) {
+        const int i = threadIdx.x;
+        if (i < head) dst[i] = src[i];
+        if (i < tail) dst[head + body + i] = src[head + body + i];
+        if (i < off) dst[i - off] = from_f32<T>(-INFINITY);
+        const int end = off + n, fill = (VEC - end % VEC) % VEC;
+        if (i < fill) dst[n + i] = from_f32<T>(-INFINITY);
+    }
+}
+
+// ---- the teacher's entries ----------------------------------------------------------
+
+// In shared memory, `top` each: ids (-1 = no entry), log2 of the probabilities, and the
+// probabilities.
+struct Entries {
+    int32_t* id;
+    float* log2p;
+    float* p;
+};
+
+// One warp: a row's entries; returns the mass.  Logits are scaled to log2 values by
+// c = log2(e) / temperature.
+__device__ float load_entries(const Entries& en, const Teacher& t, int64_t row, float c, int vocab,
+                              int32_t* error) {
+    const int lane = threadIdx.x % 32;
     float high = -INFINITY, sum = 0.f;
-    for (int j = threadIdx.x; j < t.top; j += kThreads) {
+    for (int j = lane; j < t.top; j += 32) {
         int64_t id = load_index(t.ids, row * t.ld_ids + j, t.id_type);
+        float v = load_elem(t.values, row * t.ld_values + j, t.value_elem) * c;
         if (id >= vocab) {
-            *error = 1;
+            atomicOr(error, kErrorIndex);
             id = -1;
         }
-        const float v = id < 0 ? -INFINITY : load_elem(t.values, row * t.ld_values + j, t.value_elem) * c;
+        if (id < 0) v = -INFINITY;
         en.id[j] = id < 0 ? -1 : static_cast<int32_t>(id);
         en.log2p[j] = v;
         high = fmaxf(high, v);
     }
-    high = block_reduce(high, true, en.part);
     float norm;
     if (t.lse) {
         norm = t.lse[row] * kLog2e;
     } else {
-        for (int j = threadIdx.x; j < t.top; j += kThreads)
-            sum += en.log2p[j] == -INFINITY ? 0.f : exp2f(en.log2p[j] - high);
-        norm = high + log2f(block_reduce(sum, false, en.part));
+        high = warp_max(high);
+        for (int j = lane; j < t.top; j += 32)
+            sum += en.log2p[j] == -INFINITY ? 0.f : exp2_fast(en.log2p[j] - high);
+        norm = high + log2f(warp_sum(sum));
     }
     sum = 0.f;
-    for (int j = threadIdx.x; j < t.top; j += kThreads) {
+    for (int j = lane; j < t.top; j += 32) {
         const float l = en.log2p[j] == -INFINITY ? -INFINITY : en.log2p[j] - norm;
         en.log2p[j] = l;
-        en.p[j] = exp2f(l);
+        en.p[j] = exp2_fast(l);
         sum += en.p[j];
     }
-    sum = block_reduce(sum, false, en.part);
-    if (threadIdx.x == 0) en.mass = sum;
-    __syncthreads();
+    return warp_sum(sum);
 }
 
-// One block a row: the row's maximum, the sum, the loss over the teacher's entries.
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-distill_forward_kernel(const T* logits, int64_t ldl, Teacher t, float temperature, int vocab,
-                       float* loss, float* lse, int32_t* error) {
-    __shared__ Entries en;
+// ---- running maximum and sum ----------------------------------------------------------
+
+__device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
+
+// sum exp2((x - m) c) over two sets with maxima m, m2.
+__device__ __forceinline__ void merge(float& m, float& s, float m2, float s2, float c) {
+    const float high = fmaxf(m, m2), base = finite_base(high);
+    s = s * exp2_fast((m - base) * c) + s2 * exp2_fast((m2 - base) * c);
+    m = high;
+}
+
+// ---- the kernel ------------------------------------------------------------------------
+//
+// A block holds one piece of a row's logits in shared memory.  Forward: the blocks of a
+// row form a cluster; each finds its piece's maximum m and sum of exp2((s - m) c) in one
+// pass, and they exchange those and their parts of the loss.  Backward: the gradient of
+// the piece, from the piece.  Both: the piece is read from memory once.
+// Differences s - m are taken before the scaling, so masks of the type's lowest value do
+// not overflow.
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kThreads, 5) distill_kernel(const Args<T> a) {
+    constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+    constexpr bool kLoss = (MODE & kForward) != 0, kGrad = (MODE & kBackward) != 0;
+    extern __shared__ __align__(16) uint8_t memory[];
+    __shared__ uint64_t barrier;
+    __shared__ float4 exchange[kMaxCluster];     // a block's m, sum, loss part, mass part
+    __shared__ float part[2][kWarps];
+    __shared__ float row_mass;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int64_t row = blockIdx.x / static_cast<unsigned>(a.pieces);
+    const int rank = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.pieces));
+    const int top = a.teacher.top;
+    const bool shared_row = kLoss && a.pieces > 1;
+    Entries en;
+    en.id = reinterpret_cast<int32_t*>(memory);
+    en.log2p = reinterpret_cast<float*>(en.id + top);
+    en.p = en.log2p + top;
+    // behind the entries, one pack of room before and after the piece
+    T* const room = reinterpret_cast<T*>(memory + (top * 12 + 15) / 16 * 16);
+    if (tid == 0) {
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" :: "r"(shared_address(&barrier)));
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (shared_row) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     wait_for_previous_kernel();
-    const int64_t row = blockIdx.x;
-    const T* s = logits + row * ldl;
-    const float c = kLog2e / temperature;
-    load_entries(en, t, row, c, vocab, error);
-    if (en.mass == 0.f) {
-        if (threadIdx.x == 0) {
-            loss[row] = 0.f;
-            lse[row] = -INFINITY;
+    let_next_kernel_start();
+
+    const float c = kLog2e / a.temperature;
+    if (warp == 0) {
+        const float mass = load_entries(en, a.teacher, row, c, a.vocab, a.error);
+        if (lane == 0) row_mass = mass;
+    }
+    float given_lse = 0.f;
+    if (MODE == kBackward) given_lse = a.lse[row];
+    __syncthreads();
+    const float mass = row_mass;
+    const bool out = mass == 0.f || (MODE == kBackward && given_lse == -INFINITY);
+    const int begin = rank * a.piece;
+    const int n = min(a.piece, a.vocab - begin);         // (at least one: pieces are not empty)
+    T* d = nullptr;
+    if (kGrad) d = a.dlogits + row * a.ldd + begin;
+
+    float top_m = 0.f, log2_sum = 0.f;                   // of the whole row
+    bool empty = out;
+    const T* src = a.logits + row * a.ldl + begin;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15u) / sizeof(T));
+    T* const s = room + off;
+    const int packs = (off + n + VEC - 1) / VEC;         // from room on
+    bool arrived = true;
+    if (!out) {
+        start_copy(s, src, n, &barrier);
+        arrived = wait_phase(&barrier, 0);
+        if (!arrived) atomicOr(a.error, kErrorTimeout);
+        __syncthreads();                                 // the ragged ends
+    }
+    if (kLoss) {
+        float m = -INFINITY, sum = 0.f;
+        if (!out) {
+            constexpr int kBatch = 2;
+            for (int k = tid; k < packs; k += kBatch * kThreads) {
+                float v[kBatch][VEC];
+                float high = m;
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    const int at = k + b * kThreads;
+                    Pack<T, VEC> q;
+                    if (at < packs) q = load_pack<T, VEC>(room + at * VEC, VEC);
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        v[b][i] = at < packs ? q.get(i) : -INFINITY;
+                        high = fmaxf(high, v[b][i]);
+                    }
+                }
+                const float base = finite_base(high);
+                sum *= exp2_fast((m - base) * c);
+                m = high;
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) sum += exp2_fast((v[b][i] - base) * c);
+                }
+            }
         }
-        return;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            merge(m, sum, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, sum, o), c);
+        if (lane == 0) {
+            part[0][warp] = m;
+            part[1][warp] = sum;
+        }
+        __syncthreads();
+        m = part[0][0];
+        sum = part[1][0];
+        for (int w = 1; w < kWarps; ++w) merge(m, sum, part[0][w], part[1][w], c);
+        // the entries in the piece: p (log2 p - (s - m) c), and their mass
+        if (warp == 0) {
+            float terms = 0.f, here = 0.f;
+            if (!out) {
+                const float base = finite_base(m);
+                for (int j = lane; j < top; j += 32) {
+                    const int at = en.id[j] - begin;
+                    if (en.id[j] >= 0 && at >= 0 && at < n && !(en.p[j] == 0.f)) {
+                        terms += en.p[j] * (en.log2p[j] - (to_f32(s[at]) - base) * c);
+                        here += en.p[j];
+                    }
+                }
+                terms = warp_sum(terms);
+                here = warp_sum(here);
+            }
+            const float4 mine = make_float4(m, sum, terms, here);
+            if (shared_row) {
+                __syncwarp();
+                // every block has started: put this block's numbers into each one's memory
+                asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+                if (lane < a.pieces) {
+                    uint32_t remote;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                                 : "=r"(remote) : "r"(shared_address(&exchange[rank])), "r"(lane));
+                    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};"
+                                 :: "r"(remote), "f"(mine.x), "f"(mine.y), "f"(mine.z), "f"(mine.w)
+                                 : "memory");
+                }
+            } else if (lane == 0) {
+                exchange[0] = mine;
+            }
+        } else if (shared_row) {
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        }
+        if (shared_row) {
+            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        } else {
+            __syncthreads();
+        }
+        top_m = exchange[0].x;
+        float all = exchange[0].y;
+        for (int r = 1; r < a.pieces; ++r) merge(top_m, all, exchange[r].x, exchange[r].y, c);
+        top_m = finite_base(top_m);
+        empty = out || all == 0.f;
+        log2_sum = log2f(all);
+        if (rank == 0 && tid == 0) {
+            float total = mass * log2_sum;
+            for (int r = 0; r < a.pieces; ++r)
+                total += exchange[r].z + (exchange[r].w == 0.f ? 0.f : exchange[r].w * (top_m - finite_base(exchange[r].x)) * c);
+            a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * total;
+            a.lse[row] = empty ? -INFINITY : top_m / a.temperature + kLn2 * log2_sum;
+        }
     }
-    float high = -INFINITY, sum = 0.f;
-    for (int i = threadIdx.x; i < vocab; i += kThreads) high = fmaxf(high, to_f32(s[i]));
-    high = block_reduce(high, true, en.part);
-    const float base = high == -INFINITY ? 0.f : high * c;
-    for (int i = threadIdx.x; i < vocab; i += kThreads) sum += exp2f(to_f32(s[i]) * c - base);
-    sum = block_reduce(sum, false, en.part);
-    const float l2 = base + log2f(sum);
+    if (!kGrad) return;
+
+    const bool same = (reinterpret_cast<uintptr_t>(d) & 15u) == (reinterpret_cast<uintptr_t>(src) & 15u);
+    const float scale = a.temperature * (a.dloss ? a.dloss[row] : 1.f);
+    const float q_scale = scale * mass, inverse = 1.f / a.temperature;
+    // log2 q
+    const auto log2q = [&](float x) {
+        return MODE == kBoth ? (x - top_m) * c - log2_sum : (x * inverse - given_lse) * kLog2e;
+    };
+    for (int k = tid; k < packs; k += kThreads) {
+        Pack<T, VEC> g;
+        if (empty) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) g.set(i, 0.f);
+        } else {
+            const Pack<T, VEC> q = load_pack<T, VEC>(room + k * VEC, VEC);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) g.set(i, q_scale * exp2_fast(log2q(q.get(i))));
+        }
+        const int at = k * VEC - off;                    // the pack's first element in the piece
+        if (same && at >= 0 && at + VEC <= n) {
+            store_pack<T, VEC>(d + at, VEC, g);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (at + i >= 0 && at + i < n) d[at + i] = reinterpret_cast<const T*>(&g.raw)[i];
+        }
+    }
+    if (!empty) {
+        __syncthreads();                                 // the stores above come first
+        for (int j = tid; j < top; j += kThreads) {
+            const int id = en.id[j], at = id - begin;
+            if (id < 0 || at < 0 || at >= n) continue;
+            float p = 0.f;
+            bool first = true;                           // of equal ids the first writes for all
+            for (int k = 0; k < top; ++k) {
+                if (en.id[k] != id) continue;
+                p += en.p[k];
+                first = first && k >= j;
+            }
+            if (first) d[at] = from_f32<T>(scale * (mass * exp2_fast(log2q(to_f32(s[at]))) - p));
+        }
+    }
+    if (!arrived) wait_phase(&barrier, 0);               // no copy may land in a finished block's memory
+}
+
+// Forward over rows that no cluster can hold: one block a row, a pass for the maximum
+// and one for the sum.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) distill_forward_wide_kernel(const Args<T> a) {
+    extern __shared__ __align__(16) uint8_t memory[];
+    __shared__ float part[2][kWarps];
+    __shared__ float row_mass;
+    const int top = a.teacher.top, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    Entries en;
+    en.id = reinterpret_cast<int32_t*>(memory);
+    en.log2p = reinterpret_cast<float*>(en.id + top);
+    en.p = en.log2p + top;
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    const int64_t row = blockIdx.x;
+    const T* s = a.logits + row * a.ldl;
+    const float c = kLog2e / a.temperature;
+    if (warp == 0) {
+        const float mass = load_entries(en, a.teacher, row, c, a.vocab, a.error);
+        if (lane == 0) row_mass = mass;
+    }
+    __syncthreads();
+    const float mass = row_mass;
+    float m = -INFINITY, sum = 0.f;
+    if (mass != 0.f) {
+        for (int i = threadIdx.x; i < a.vocab; i += kThreads) m = fmaxf(m, to_f32(s[i]));
+        const float base = finite_base(m);
+        for (int i = threadIdx.x; i < a.vocab; i += kThreads) sum += exp2_fast((to_f32(s[i]) - base) * c);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        merge(m, sum, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, sum, o), c);
+    if (lane == 0) {
+        part[0][warp] = m;
+        part[1][warp] = sum;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    m = part[0][0];
+    sum = part[1][0];
+    for (int w = 1; w < kWarps; ++w) merge(m, sum, part[0][w], part[1][w], c);
+    m = finite_base(m);
+    const bool empty = mass == 0.f || sum == 0.f;
+    const float log2_sum = log2f(sum);
     float total = 0.f;
-    for (int j = threadIdx.x; j < t.top; j += kThreads)
-        if (!(en.p[j] == 0.f)) total += en.p[j] * (en.log2p[j] - to_f32(s[en.id[j]]) * c + l2);
-    total = block_reduce(total, false, en.part);
-    if (threadIdx.x == 0) {
-        const bool empty = sum == 0.f;
-        loss[row] = empty ? 0.f : temperature * temperature * total / kLog2e;
-        lse[row] = empty ? -INFINITY : l2 / kLog2e;
+    if (!empty)
+        for (int j = lane; j < top; j += 32)
+            if (!(en.p[j] == 0.f)) total += en.p[j] * (en.log2p[j] - (to_f32(s[en.id[j]]) - m) * c + log2_sum);
+    total = warp_sum(total);
+    if (lane == 0) {
+        a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * total;
+        a.lse[row] = empty ? -INFINITY : m / a.temperature + kLn2 * log2_sum;
     }
 }
 
-// One block a row: P * q over the row, then the teacher's entries.
+// How a row is cut: pieces of about kPieceBytes, more and smaller ones where there are
+// too few rows to fill the GPU, at most `most`.
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
-distill_backward_kernel(const T* logits, int64_t ldl, Teacher t, float temperature, int vocab,
-                        const float* lse, const float* dloss, T* dlogits, int64_t ldd,
-                        int32_t* error) {
-    __shared__ Entries en;
-    wait_for_previous_kernel();
-    const int64_t row = blockIdx.x;
-    const T* s = logits + row * ldl;
-    T* d = dlogits + row * ldd;
-    const float c = kLog2e / temperature;
-    load_entries(en, t, row, c, vocab, error);
-    const float l2 = lse[row] * kLog2e;
-    if (en.mass == 0.f || l2 == -INFINITY) {
-        for (int i = threadIdx.x; i < vocab; i += kThreads) d[i] = from_f32<T>(0.f);
-        return;
-    }
-    const float scale = temperature * (dloss ? dloss[row] : 1.f);
-    // the entries' own gradients, before dlogits overwrites the logits: the first
-    // entry of each id takes them all
-    __shared__ float own[kMaxTop];
-    for (int j = threadIdx.x; j < t.top; j += kThreads) {
-        if (en.id[j] < 0) continue;
-        float p = 0.f;
-        for (int k = 0; k < t.top; ++k)
-            if (en.id[k] == en.id[j]) p += en.p[k];
-        own[j] = scale * (en.mass * exp2f(to_f32(s[en.id[j]]) * c - l2) - p);
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < vocab; i += kThreads)
-        d[i] = from_f32<T>(scale * en.mass * exp2f(to_f32(s[i]) * c - l2));
-    __syncthreads();
-    for (int j = threadIdx.x; j < t.top; j += kThreads)
-        if (en.id[j] >= 0) d[en.id[j]] = from_f32<T>(own[j]);   // equal ids write equal values
+void cut_row(Args<T>& a, int64_t rows, int sms, int64_t most) {
+    constexpr int64_t kVec = 16 / sizeof(T);
+    const int64_t bytes = static_cast<int64_t>(a.vocab) * static_cast<int64_t>(sizeof(T));
+    int64_t pieces = 1;
+    while (pieces < most && bytes > pieces * kPieceBytes) pieces *= 2;
+    while (pieces < most && pieces < kMaxCluster && rows * pieces < 2 * sms && bytes > pieces * 8192) pieces *= 2;
+    const int64_t packs = (a.vocab + kVec - 1) / kVec;
+    const int64_t each = (packs + pieces - 1) / pieces;
+    a.piece = static_cast<int>(each * kVec);
+    a.pieces = static_cast<int>((packs + each - 1) / each);
 }
+
+template <typename T, int MODE>
+gemm_status_t run(Args<T> a, int64_t rows, int sms, void* stream) {
+    cut_row(a, rows, sms, MODE == kBackward ? INT32_MAX : kMaxCluster);
+    const size_t smem = (a.teacher.top * 12 + 15) / 16 * 16 + a.piece * sizeof(T) + 32;
+    return launch(distill_kernel<T, MODE>, rows * a.pieces, kThreads, smem, stream,
+                  MODE == kBackward ? 1 : a.pieces, a);
+}
+
+// Lets the kernels have as much shared memory as the largest launch asks for.
+template <typename T>
+gemm_status_t prepare() {
+    const int most = kMaxTop * 12 + kMostPieceBytes + 32;
+    const auto allow = [&](auto kernel) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) == cudaSuccess;
+    };
+    if (allow(distill_kernel<T, kForward>) && allow(distill_kernel<T, kBackward>) && allow(distill_kernel<T, kBoth>))
+        return GEMM_OK;
+    cudaGetLastError();
+    return GEMM_ERR_LAUNCH;
+}
+
+template <typename T>
+gemm_status_t run_forward_wide(const Args<T>& a, int64_t rows, void* stream) {
+    return launch(distill_forward_wide_kernel<T>, rows, kThreads, a.teacher.top * 12, stream, 1, a);
+}
+
+// Whether a cluster can hold a row.
+bool fits(int64_t vocab, int bytes) { return vocab * bytes <= int64_t{kMaxCluster} * kMostPieceBytes; }
 
 gemm_status_t check_call(const gemm_distill_plan* p, int64_t rows, const void* logits, int64_t ldl,
                          const gemm_teacher_t* t, float temperature) {
@@ -172,11 +481,24 @@ gemm_status_t check_call(const gemm_distill_plan* p, int64_t rows, const void* l
     return check_device(p->device);
 }
 
-Teacher device_teacher(const gemm_teacher_t* t) {
-    return Teacher{t->ids,       t->values,
-                   t->lse,       t->ld_ids,
-                   t->ld_values, static_cast<int>(t->top),
-                   static_cast<int>(t->id_type), static_cast<int>(t->value_elem)};
+template <typename T>
+Args<T> arguments(const gemm_distill_plan* p, const void* logits, int64_t ldl, const gemm_teacher_t* t,
+                  float temperature) {
+    Args<T> a = {};
+    a.logits = static_cast<const T*>(logits);
+    a.ldl = ldl;
+    a.teacher = Teacher{t->ids,
+                        t->values,
+                        t->lse,
+                        t->ld_ids,
+                        t->ld_values,
+                        static_cast<int>(t->top),
+                        static_cast<int>(t->id_type),
+                        static_cast<int>(t->value_elem)};
+    a.temperature = temperature;
+    a.vocab = static_cast<int>(p->vocab);
+    a.error = p->error_word;
+    return a;
 }
 
 }  // namespace
@@ -194,6 +516,8 @@ gemm_status_t gemm_distill_plan_create(int64_t max_rows, int64_t vocab, int64_t 
         return GEMM_ERR_INVALID_ARG;
     int device = 0, sms = 0;
     gemm_status_t st = gbt::current_device(&device, &sms);
+    if (st != GEMM_OK) return st;
+    st = gbt::with_elem(elem, [](auto v) { return gbt::prepare<decltype(v)>(); });
     if (st != GEMM_OK) return st;
     void* word = nullptr;
     st = gbt::allocate(&word, 256);
@@ -227,9 +551,11 @@ gemm_status_t gemm_distill_forward(gemm_distill_plan_t p, int64_t rows, const vo
     if (rows == 0) return GEMM_OK;
     return gbt::with_elem(p->elem, [&](auto v) {
         using T = decltype(v);
-        return gbt::launch(gbt::distill_forward_kernel<T>, rows, gbt::kThreads, 0, stream, 1,
-                           static_cast<const T*>(logits), ldl, gbt::device_teacher(teacher),
-                           temperature, static_cast<int>(p->vocab), loss, lse, p->error_word);
+        auto a = gbt::arguments<T>(p, logits, ldl, teacher, temperature);
+        a.loss = loss;
+        a.lse = lse;
+        return gbt::fits(p->vocab, sizeof(T)) ? gbt::run<T, gbt::kForward>(a, rows, p->num_sms, stream)
+                                              : gbt::run_forward_wide(a, rows, stream);
     });
 }
 
@@ -246,10 +572,12 @@ gemm_status_t gemm_distill_backward(gemm_distill_plan_t p, int64_t rows, const v
     if (rows == 0) return GEMM_OK;
     return gbt::with_elem(p->elem, [&](auto v) {
         using T = decltype(v);
-        return gbt::launch(gbt::distill_backward_kernel<T>, rows, gbt::kThreads, 0, stream, 1,
-                           static_cast<const T*>(logits), ldl, gbt::device_teacher(teacher),
-                           temperature, static_cast<int>(p->vocab), lse, dloss,
-                           static_cast<T*>(dlogits), ldd, p->error_word);
+        auto a = gbt::arguments<T>(p, logits, ldl, teacher, temperature);
+        a.lse = const_cast<float*>(lse);     // (read only)
+        a.dloss = dloss;
+        a.dlogits = static_cast<T*>(dlogits);
+        a.ldd = ldd;
+        return gbt::run<T, gbt::kBackward>(a, rows, p->num_sms, stream);
     });
 }
 
@@ -264,11 +592,19 @@ gemm_status_t gemm_distill_forward_backward(gemm_distill_plan_t p, int64_t rows,
     if (!gbt::aligned(loss, 4) || !gbt::aligned(lse, 4) || !gbt::aligned(dloss, 4) ||
         !gbt::aligned(dlogits, gbt::elem_bytes(p->elem)))
         return GEMM_ERR_ALIGNMENT;
-    const gemm_status_t first =
-        gemm_distill_forward(p, rows, logits, ldl, teacher, temperature, loss, lse, stream);
-    if (first != GEMM_OK) return first;
-    return gemm_distill_backward(p, rows, logits, ldl, teacher, temperature, lse, dloss, dlogits,
-                                 ldd, stream);
+    if (rows == 0) return GEMM_OK;
+    return gbt::with_elem(p->elem, [&](auto v) {
+        using T = decltype(v);
+        auto a = gbt::arguments<T>(p, logits, ldl, teacher, temperature);
+        a.loss = loss;
+        a.lse = lse;
+        a.dloss = dloss;
+        a.dlogits = static_cast<T*>(dlogits);
+        a.ldd = ldd;
+        if (gbt::fits(p->vocab, sizeof(T))) return gbt::run<T, gbt::kBoth>(a, rows, p->num_sms, stream);
+        const gemm_status_t first = gbt::run_forward_wide(a, rows, stream);
+        return first == GEMM_OK ? gbt::run<T, gbt::kBackward>(a, rows, p->num_sms, stream) : first;
+    });
 }
 
 gemm_status_t gemm_distill_plan_check(gemm_distill_plan_t p, void* stream) {

@@ -420,15 +420,24 @@ gemm_status_t forward_vec(const ForwardArgs<T, W>& a, int sms, void* stream) {
 template <typename T, typename W, int VEC, int BLOCK, bool SHARED>
 gemm_status_t backward_rows(const BackwardArgs<T, W>& a, int blocks, void* stream) {
     const auto kernel = norm_backward_kernel<T, W, VEC, BLOCK, SHARED>;
-    const size_t smem = a.weights ? static_cast<size_t>(a.lanes) * kLaneCols * 2 * sizeof(float) : 0;
     // (SHARED keeps its sums there whether they are wanted or not)
-    const size_t want = SHARED ? static_cast<size_t>(a.lanes) * kLaneCols * 2 * sizeof(float) : smem;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(want)) != cudaSuccess) {
-        cudaGetLastError();
-        return GEMM_ERR_LAUNCH;
-    }
-    return launch(kernel, blocks, BLOCK, want, stream, 1, a);
+    const size_t smem = SHARED || a.weights ? static_cast<size_t>(a.lanes) * kLaneCols * 2 * sizeof(float) : 0;
+    return launch(kernel, blocks, BLOCK, smem, stream, 1, a);
+}
+
+// Lets the kernels have as much shared memory as their largest launch asks for.
+template <typename T, typename W>
+gemm_status_t prepare() {
+    constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+    const auto allow = [](auto kernel, int lanes) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    lanes * kLaneCols * 2 * static_cast<int>(sizeof(float))) == cudaSuccess;
+    };
+    if (allow(norm_backward_kernel<T, W, kVec, 512, false>, 512) && allow(norm_backward_kernel<T, W, 1, 512, false>, 512) &&
+        allow(norm_backward_kernel<T, W, kVec, 1024, true>, 1024) && allow(norm_backward_kernel<T, W, 1, 1024, true>, 1024))
+        return GEMM_OK;
+    cudaGetLastError();
+    return GEMM_ERR_LAUNCH;
 }
 
 // Blocks of a backward launch over `rows` rows, and the block size for `lanes`.
@@ -481,13 +490,20 @@ gemm_status_t gemm_norm_plan_create(int64_t max_rows, int64_t cols, gemm_elem_t 
         cudaFree(partial);
         return GEMM_ERR_OOM;
     }
-    p->partial = static_cast<float*>(partial);
     p->max_rows = max_rows;
     p->cols = cols;
     p->elem = elem;
     p->weight_elem = weight_elem;
     p->device = device;
     p->num_sms = sms;
+    p->partial = static_cast<float*>(partial);
+    const gemm_status_t ready =
+        gbt::with_types(p, [](auto t, auto v) { return gbt::prepare<decltype(t), decltype(v)>(); });
+    if (ready != GEMM_OK) {
+        cudaFree(partial);
+        delete p;
+        return ready;
+    }
     *plan = p;
     return GEMM_OK;
 }

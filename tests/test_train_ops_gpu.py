@@ -306,7 +306,8 @@ def test_embedding_one_token_many_times(gemm_lib):
 # ---------------------------------------------------------------- distillation
 
 DISTILL_SIZES = [(1, 1, 1), (1, 8, 3), (3, 7, 7), (5, 100, 1), (2, 1000, 64), (40, 333, 20), (3, 4096, 200), (2, 8200, 33),
-                 (7, 20011, 16), (2, 50021, 1024), (1, 131072, 64), (400, 136, 5), (2, 300000, 8)]
+                 (7, 20011, 16), (2, 50021, 1024), (1, 131072, 64), (400, 136, 5), (2, 300000, 8),
+                 (1, 850000, 4)]
 
 
 def _distill_case(rows, vocab, top, elem, value, index, pad, offset, given, tau, mask=True):
