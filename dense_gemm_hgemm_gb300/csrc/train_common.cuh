@@ -140,6 +140,12 @@ __device__ __forceinline__ void let_next_kernel_start() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// All threads of the cluster; writes before it, to global memory too, are visible after it.
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // ---- host ---------------------------------------------------------------------
 
 inline bool valid_elem(gemm_elem_t e) { return e >= GEMM_ELEM_F16 && e <= GEMM_ELEM_F32; }

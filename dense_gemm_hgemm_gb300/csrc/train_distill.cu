@@ -6,11 +6,21 @@
 
 #include "train_common.cuh"
 
+namespace gbt {
+// How the pipeline over rows cuts a row and fills the GPU (see distill_stream_kernel).
+struct StreamShape {
+    int pieces, piece, stages;
+    int clusters;            // resident at once; 0 = not used
+    size_t smem;
+};
+}  // namespace gbt
+
 struct gemm_distill_plan {
     int64_t max_rows, vocab, max_top;
     gemm_elem_t elem;
     int device, num_sms;
     int32_t* error_word;
+    gbt::StreamShape forward, both;
 };
 
 namespace gbt {
@@ -22,6 +32,8 @@ constexpr int kMaxTop = 1024;
 constexpr int kMaxCluster = 8;                 // blocks that share a row
 constexpr int kPieceBytes = 32 * 1024;         // of a row that a block aims to hold
 constexpr int kMostPieceBytes = 200 * 1024;    // ... and can hold
+constexpr int kMostShared = 224 * 1024;        // dynamic shared memory of any launch
+constexpr long long kWaitNs = 2000000000ll;     // the longest wait in a kernel
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -71,7 +83,7 @@ __device__ bool wait_phase(uint64_t* barrier, uint32_t parity) {
         long long now;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
         if (tries == 0) began = now;
-        if (now - began > 2000000000ll) return false;
+        if (now - began > kWaitNs) return false;
     }
 }
 
@@ -108,12 +120,13 @@ __device__ __forceinline__ void start_copy(T* dst, const T* src, int n, uint64_t
 
 // ---- the teacher's entries ----------------------------------------------------------
 
-// In shared memory, `top` each: ids (-1 = no entry), log2 of the probabilities, and the
+// In shared memory, `top` each: ids (-1 = no entry), log2 of the probabilities, the
 // probabilities.
 struct Entries {
     int32_t* id;
     float* log2p;
     float* p;
+    float* x;      // the student's logits at the ids (where a kernel fetches them)
 };
 
 // One warp: a row's entries; returns the mass.  Logits are scaled to log2 values by
@@ -367,6 +380,349 @@ __global__ void __launch_bounds__(kThreads, 5) distill_kernel(const Args<T> a) {
     if (!arrived) wait_phase(&barrier, 0);               // no copy may land in a finished block's memory
 }
 
+// ---- many rows: a pipeline over rows -----------------------------------------------------
+//
+// A block (or a cluster, each block with its part of the row) goes through rows, with
+// three kinds of warps: one copies the logits into a ring of kStageBytes stages, as far
+// ahead as there is room; one prepares the teacher's entries of the next row; the others
+// compute.  Forward frees a stage as soon as it is summed; both directions together keep
+// the row's stages until its gradient is written, and copy the next row into those that
+// are free.  So memory is busy while a row is reduced, and no block starts or ends per row.
+
+constexpr int kStageBytes = 8192;
+constexpr int kMostStages = 25;
+constexpr int kComputeWarps = 8;
+constexpr int kComputeThreads = kComputeWarps * 32;
+constexpr int kStreamThreads = 64 + kComputeThreads;
+
+struct StreamBarriers {
+    uint64_t full[kMostStages], empty[kMostStages];
+    uint64_t entries_full[2], entries_empty[2];
+    uint64_t exchanged[2];
+    float4 exchange[2][kMaxCluster];
+    float part[2][2][kComputeWarps];
+    float mass[2];
+    int dead;                // a wait ran out: nothing waits any more
+};
+
+// As wait_phase; when it runs out (or another wait has) it returns at once from then on.
+__device__ __forceinline__ void wait_or_die(uint64_t* barrier, uint32_t parity, int* dead, int32_t* error) {
+    const uint32_t at = shared_address(barrier);
+    long long began = 0;
+    for (uint32_t tries = 0;; ++tries) {
+        uint32_t done;
+        asm volatile(
+            "{\n.reg .pred p;\n"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            "selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(done) : "r"(at), "r"(parity) : "memory");
+        if (done || *static_cast<volatile int*>(dead)) return;
+        long long now;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        if (tries == 0) began = now;
+        if (now - began > kWaitNs) {
+            *static_cast<volatile int*>(dead) = 1;
+            atomicOr(error, kErrorTimeout);
+            return;
+        }
+    }
+}
+
+__device__ __forceinline__ void init_barrier(uint64_t* barrier, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(shared_address(barrier)), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void arrive(uint64_t* barrier) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(shared_address(barrier)) : "memory");
+}
+
+__device__ __forceinline__ void compute_barrier() {
+    asm volatile("bar.sync 1, %0;" :: "n"(kComputeThreads) : "memory");
+}
+
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const Args<T> a, int64_t rows, int stages) {
+    constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+    constexpr int kStage = kStageBytes / static_cast<int>(sizeof(T));     // elements
+    constexpr bool kGrad = MODE == kBoth;
+    extern __shared__ __align__(16) uint8_t memory[];
+    __shared__ StreamBarriers sh;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int rank = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.pieces));
+    const int64_t first = blockIdx.x / static_cast<unsigned>(a.pieces);
+    const int64_t step = gridDim.x / static_cast<unsigned>(a.pieces);
+    const int top = a.teacher.top;
+    T* const ring = reinterpret_cast<T*>(memory);
+    const auto entries = [&](int slot) {
+        float* at = reinterpret_cast<float*>(memory + stages * kStageBytes) + slot * 4 * top;
+        return Entries{reinterpret_cast<int32_t*>(at), at + top, at + 2 * top, at + 3 * top};
+    };
+    const int begin = rank * a.piece;
+    const int n = min(a.piece, a.vocab - begin);
+    const float c = kLog2e / a.temperature;
+    if (tid == 0) {
+        for (int k = 0; k < stages; ++k) {
+            init_barrier(&sh.full[k], 1);
+            init_barrier(&sh.empty[k], kComputeWarps);
+        }
+        for (int k = 0; k < 2; ++k) {
+            init_barrier(&sh.entries_full[k], 1);
+            init_barrier(&sh.entries_empty[k], kComputeWarps + 1);
+            init_barrier(&sh.exchanged[k], 1);
+        }
+        sh.dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    if (a.pieces > 1) cluster_barrier();                 // the others' barriers exist
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+
+    if (warp == 0) {                                     // copies
+        uint32_t stage = 0, round = 0;
+        int64_t k = 0;
+        for (int64_t row = first; row < rows; row += step, ++k) {
+            const int slot = k & 1;
+            wait_or_die(&sh.entries_full[slot], (k >> 1) & 1, &sh.dead, a.error);
+            const bool out = sh.mass[slot] == 0.f;
+            __syncwarp();
+            if (lane == 0) arrive(&sh.entries_empty[slot]);
+            if (out) continue;
+            const T* src = a.logits + row * a.ldl + begin;
+            const int off = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15u) / sizeof(T));
+            const T* base = src - off;                   // the 16-byte boundary at or before src
+            const int end = off + n;                     // positions count from there
+            const int head_end = min((off + VEC - 1) / VEC * VEC, end);
+            const int tail_begin = max(end / VEC * VEC, head_end);
+            T head = from_f32<T>(-INFINITY), tail = head;
+            if (lane < VEC) {                            // the ragged ends, by plain loads
+                if (off > 0 && lane >= off && lane < head_end) head = base[lane];
+                if (tail_begin + lane < end) tail = base[tail_begin + lane];
+            }
+            for (int at = 0; at < end; at += kStage) {
+                wait_or_die(&sh.empty[stage], (round & 1) ^ 1, &sh.dead, a.error);
+                T* const to = ring + stage * kStage;
+                const int lo = at == 0 ? head_end : at, hi = min(at + kStage, tail_begin);
+                const bool first_pack = at == 0 && off > 0;
+                const bool last_pack = tail_begin < end && tail_begin >= at && tail_begin < at + kStage;
+                if (first_pack || last_pack) {
+                    if (first_pack && lane < VEC) to[lane] = head;
+                    if (last_pack && lane < VEC) to[tail_begin - at + lane] = tail;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                __syncwarp();
+                if (lane == 0 && !*static_cast<volatile int*>(&sh.dead)) {
+                    const uint32_t bytes = hi > lo ? static_cast<uint32_t>((hi - lo) * static_cast<int>(sizeof(T))) : 0;
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
+                                 :: "r"(shared_address(&sh.full[stage])), "r"(bytes) : "memory");
+                    if (bytes > 0)
+                        asm volatile(
+                            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                            :: "r"(shared_address(to + (lo - at))), "l"(base + lo), "r"(bytes),
+                               "r"(shared_address(&sh.full[stage])) : "memory");
+                }
+                if (++stage == static_cast<uint32_t>(stages)) {
+                    stage = 0;
+                    ++round;
+                }
+            }
+        }
+        // A wait that ran out may have left copies behind: let them land (bounded).
+        if (*static_cast<volatile int*>(&sh.dead)) {
+            for (int s = 0; s < stages; ++s) {
+                const uint32_t issued = round + (static_cast<uint32_t>(s) < stage ? 1 : 0);
+                if (issued > 0) wait_phase(&sh.full[s], (issued - 1) & 1);
+            }
+        }
+    } else if (warp == 1) {                              // the teacher's entries
+        int64_t k = 0;
+        for (int64_t row = first; row < rows; row += step, ++k) {
+            const int slot = k & 1;
+            wait_or_die(&sh.entries_empty[slot], ((k >> 1) & 1) ^ 1, &sh.dead, a.error);
+            const Entries en = entries(slot);
+            const float mass = load_entries(en, a.teacher, row, c, a.vocab, a.error);
+            if (mass != 0.f)
+                for (int j = lane; j < top; j += 32)
+                    en.x[j] = en.id[j] >= 0 ? to_f32(a.logits[row * a.ldl + en.id[j]]) : 0.f;
+            if (lane == 0) sh.mass[slot] = mass;
+            __syncwarp();
+            if (lane == 0) arrive(&sh.entries_full[slot]);
+        }
+    } else {                                             // the arithmetic
+        const int thread = tid - 64, worker = warp - 2;
+        uint32_t stage = 0, round = 0, exchanges = 0;
+        int64_t k = 0;
+        for (int64_t row = first; row < rows; row += step, ++k) {
+            const int slot = k & 1;
+            wait_or_die(&sh.entries_full[slot], (k >> 1) & 1, &sh.dead, a.error);
+            const float mass = sh.mass[slot];
+            const Entries en = entries(slot);
+            const bool out = mass == 0.f;
+            const T* src = a.logits + row * a.ldl + begin;
+            const int off = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15u) / sizeof(T));
+            const int packs = (off + n + VEC - 1) / VEC;
+            const uint32_t row_stage = stage, row_round = round;
+            bool empty = out;
+            float top_m = 0.f, log2_sum = 0.f;
+            if (!out) {
+                float m = -INFINITY, sum = 0.f;
+                for (int p0 = 0; p0 < packs; p0 += kStage / VEC) {
+                    wait_or_die(&sh.full[stage], round & 1, &sh.dead, a.error);
+                    const T* from = ring + stage * kStage;
+                    const int here = min(packs - p0, kStage / VEC);
+                    constexpr int kBatch = kStage / VEC / kComputeThreads;
+                    Pack<T, VEC> q[kBatch];
+                    float v[kBatch][VEC];
+                    float high = m;
+#pragma unroll
+                    for (int b = 0; b < kBatch; ++b) {
+                        const int at = thread + b * kComputeThreads;
+                        if (at < here) q[b] = load_pack<T, VEC>(from + at * VEC, VEC);
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) {
+                            v[b][i] = at < here ? q[b].get(i) : -INFINITY;
+                            high = fmaxf(high, v[b][i]);
+                        }
+                    }
+                    if (!kGrad) {
+                        __syncwarp();
+                        if (lane == 0) arrive(&sh.empty[stage]);
+                    }
+                    const float base = finite_base(high);
+                    sum *= exp2_fast((m - base) * c);
+                    m = high;
+#pragma unroll
+                    for (int b = 0; b < kBatch; ++b) {
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) sum += exp2_fast((v[b][i] - base) * c);
+                    }
+                    if (++stage == static_cast<uint32_t>(stages)) {
+                        stage = 0;
+                        ++round;
+                    }
+                }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    merge(m, sum, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, sum, o), c);
+                const int turn = exchanges & 1;
+                if (lane == 0) {
+                    sh.part[turn][0][worker] = m;
+                    sh.part[turn][1][worker] = sum;
+                }
+                compute_barrier();
+                m = sh.part[turn][0][lane % kComputeWarps];
+                sum = sh.part[turn][1][lane % kComputeWarps];
+#pragma unroll
+                for (int o = kComputeWarps / 2; o > 0; o >>= 1)
+                    merge(m, sum, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, sum, o), c);
+                if (a.pieces > 1) {
+                    if (worker == 0) {
+                        if (lane == 0)
+                            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
+                                         :: "r"(shared_address(&sh.exchanged[turn])), "r"(a.pieces * 8) : "memory");
+                        if (lane < a.pieces) {           // this block's numbers, to each block of the row
+                            uint32_t slot_at, barrier_at;
+                            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                                         : "=r"(slot_at) : "r"(shared_address(&sh.exchange[turn][rank])), "r"(lane));
+                            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                                         : "=r"(barrier_at) : "r"(shared_address(&sh.exchanged[turn])), "r"(lane));
+                            asm volatile(
+                                "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];"
+                                :: "r"(slot_at), "f"(m), "f"(sum), "r"(barrier_at) : "memory");
+                        }
+                        __syncwarp();
+                    }
+                    wait_or_die(&sh.exchanged[turn], (exchanges >> 1) & 1, &sh.dead, a.error);
+                    m = sh.exchange[turn][0].x;
+                    sum = sh.exchange[turn][0].y;
+                    for (int r = 1; r < a.pieces; ++r)
+                        merge(m, sum, sh.exchange[turn][r].x, sh.exchange[turn][r].y, c);
+                }
+                ++exchanges;
+                top_m = finite_base(m);
+                empty = sum == 0.f;
+                log2_sum = log2f(sum);
+            }
+            if (rank == 0 && worker == 0) {
+                float total = 0.f;
+                if (!empty)
+                    for (int j = lane; j < top; j += 32)
+                        if (!(en.p[j] == 0.f)) total += en.p[j] * (en.log2p[j] - (en.x[j] - top_m) * c + log2_sum);
+                total = warp_sum(total);
+                if (lane == 0) {
+                    a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * total;
+                    a.lse[row] = empty ? -INFINITY : top_m / a.temperature + kLn2 * log2_sum;
+                }
+            }
+            if (kGrad) {
+                T* const d = a.dlogits + row * a.ldd + begin;
+                const bool same = (reinterpret_cast<uintptr_t>(d) & 15u) == (reinterpret_cast<uintptr_t>(src) & 15u);
+                const float scale = a.temperature * (a.dloss ? a.dloss[row] : 1.f);
+                const float q_scale = scale * mass;
+                stage = row_stage;
+                round = row_round;
+                for (int p0 = 0; p0 < packs; p0 += kStage / VEC) {
+                    const T* from = ring + stage * kStage;
+                    const int here = min(packs - p0, kStage / VEC);
+#pragma unroll
+                    for (int b = 0; b < kStage / VEC / kComputeThreads; ++b) {
+                        const int mine = thread + b * kComputeThreads;
+                        if (mine >= here) continue;
+                        Pack<T, VEC> g;
+                        if (empty) {
+#pragma unroll
+                            for (int i = 0; i < VEC; ++i) g.set(i, 0.f);
+                        } else {
+                            const Pack<T, VEC> q = load_pack<T, VEC>(from + mine * VEC, VEC);
+#pragma unroll
+                            for (int i = 0; i < VEC; ++i)
+                                g.set(i, q_scale * exp2_fast((q.get(i) - top_m) * c - log2_sum));
+                        }
+                        const int at = (p0 + mine) * VEC - off;
+                        if (same && at >= 0 && at + VEC <= n) {
+                            store_pack<T, VEC>(d + at, VEC, g);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < VEC; ++i)
+                                if (at + i >= 0 && at + i < n) d[at + i] = reinterpret_cast<const T*>(&g.raw)[i];
+                        }
+                    }
+                    if (!out) {
+                        __syncwarp();
+                        if (lane == 0) arrive(&sh.empty[stage]);
+                        if (++stage == static_cast<uint32_t>(stages)) {
+                            stage = 0;
+                            ++round;
+                        }
+                    }
+                }
+                if (!empty) {
+                    compute_barrier();                   // the stores above come first
+                    for (int j = thread; j < top; j += kComputeThreads) {
+                        const int id = en.id[j], at = id - begin;
+                        if (id < 0 || at < 0 || at >= n) continue;
+                        float p = 0.f;
+                        bool leads = true;               // of equal ids the first writes for all
+                        for (int i = 0; i < top; ++i) {
+                            if (en.id[i] != id) continue;
+                            p += en.p[i];
+                            leads = leads && i >= j;
+                        }
+                        if (leads)
+                            d[at] = from_f32<T>(scale * (mass * exp2_fast((en.x[j] - top_m) * c - log2_sum) - p));
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) arrive(&sh.entries_empty[slot]);
+        }
+    }
+    __syncthreads();
+    if (a.pieces > 1) cluster_barrier();                 // no block leaves while others write to it
+}
+
+// ---- rows that no cluster can hold ---------------------------------------------------------
+
 // Forward over rows that no cluster can hold: one block a row, a pass for the maximum
 // and one for the sum.
 template <typename T>
@@ -448,14 +804,65 @@ gemm_status_t run(Args<T> a, int64_t rows, int sms, void* stream) {
 // Lets the kernels have as much shared memory as the largest launch asks for.
 template <typename T>
 gemm_status_t prepare() {
-    const int most = kMaxTop * 12 + kMostPieceBytes + 32;
-    const auto allow = [&](auto kernel) {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) == cudaSuccess;
+    const auto allow = [](auto kernel) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared) == cudaSuccess;
     };
-    if (allow(distill_kernel<T, kForward>) && allow(distill_kernel<T, kBackward>) && allow(distill_kernel<T, kBoth>))
+    if (allow(distill_stream_kernel<T, kForward>) && allow(distill_stream_kernel<T, kBoth>) &&
+        allow(distill_kernel<T, kForward>) && allow(distill_kernel<T, kBackward>) && allow(distill_kernel<T, kBoth>))
         return GEMM_OK;
     cudaGetLastError();
     return GEMM_ERR_LAUNCH;
+}
+
+template <typename T, int MODE>
+gemm_status_t run_stream(Args<T> a, const StreamShape& shape, int64_t rows, void* stream) {
+    a.piece = shape.piece;
+    a.pieces = shape.pieces;
+    const int64_t clusters = rows < shape.clusters ? rows : shape.clusters;
+    return launch(distill_stream_kernel<T, MODE>, clusters * a.pieces, kStreamThreads, shape.smem, stream,
+                  a.pieces, a, rows, shape.stages);
+}
+
+// The pipeline's shape for a plan; clusters == 0 where it does not suit.
+template <typename T, int MODE>
+StreamShape stream_shape(int64_t vocab, int64_t max_top) {
+    constexpr int64_t kVec = 16 / sizeof(T);
+    const int64_t bytes = vocab * static_cast<int64_t>(sizeof(T)), entries = max_top * 32;
+    const int64_t room = (kMostShared - entries) / kStageBytes;
+    StreamShape shape = {};
+    shape.pieces = 1;
+    int64_t stages = 6;
+    if (MODE == kBoth) {
+        while (shape.pieces < kMaxCluster && bytes > shape.pieces * int64_t{64 * 1024}) shape.pieces *= 2;
+        const int64_t packs = (vocab + kVec - 1) / kVec;
+        const int64_t each = (packs + shape.pieces - 1) / shape.pieces;
+        shape.piece = static_cast<int>(each * kVec);
+        shape.pieces = static_cast<int>((packs + each - 1) / each);
+        const int64_t need = ((each + 1) * 16 + kStageBytes - 1) / kStageBytes;
+        stages = need <= 4 ? 7 : need <= 10 ? 13 : kMostStages;
+        if (stages > room) stages = room;
+        if (need > stages) return shape;
+    } else {
+        shape.piece = static_cast<int>(vocab);
+    }
+    shape.stages = static_cast<int>(stages);
+    shape.smem = static_cast<size_t>(stages * kStageBytes + entries);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(shape.pieces * 1024));
+    cfg.blockDim = dim3(kStreamThreads);
+    cfg.dynamicSmemBytes = shape.smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(shape.pieces);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&shape.clusters, distill_stream_kernel<T, MODE>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        shape.clusters = 0;
+    }
+    return shape;
 }
 
 template <typename T>
@@ -537,6 +944,11 @@ gemm_status_t gemm_distill_plan_create(int64_t max_rows, int64_t vocab, int64_t 
     p->device = device;
     p->num_sms = sms;
     p->error_word = static_cast<int32_t*>(word);
+    gbt::with_elem(elem, [&](auto v) {
+        p->forward = gbt::stream_shape<decltype(v), gbt::kForward>(vocab, max_top);
+        p->both = gbt::stream_shape<decltype(v), gbt::kBoth>(vocab, max_top);
+        return GEMM_OK;
+    });
     *plan = p;
     return GEMM_OK;
 }
@@ -554,6 +966,8 @@ gemm_status_t gemm_distill_forward(gemm_distill_plan_t p, int64_t rows, const vo
         auto a = gbt::arguments<T>(p, logits, ldl, teacher, temperature);
         a.loss = loss;
         a.lse = lse;
+        if (p->forward.clusters > 0 && rows >= p->forward.clusters)
+            return gbt::run_stream<T, gbt::kForward>(a, p->forward, rows, stream);
         return gbt::fits(p->vocab, sizeof(T)) ? gbt::run<T, gbt::kForward>(a, rows, p->num_sms, stream)
                                               : gbt::run_forward_wide(a, rows, stream);
     });
@@ -601,6 +1015,8 @@ gemm_status_t gemm_distill_forward_backward(gemm_distill_plan_t p, int64_t rows,
         a.dloss = dloss;
         a.dlogits = static_cast<T*>(dlogits);
         a.ldd = ldd;
+        if (p->both.clusters > 0 && rows >= p->both.clusters)
+            return gbt::run_stream<T, gbt::kBoth>(a, p->both, rows, stream);
         if (gbt::fits(p->vocab, sizeof(T))) return gbt::run<T, gbt::kBoth>(a, rows, p->num_sms, stream);
         const gemm_status_t first = gbt::run_forward_wide(a, rows, stream);
         return first == GEMM_OK ? gbt::run<T, gbt::kBackward>(a, rows, p->num_sms, stream) : first;

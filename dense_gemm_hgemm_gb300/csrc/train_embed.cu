@@ -88,12 +88,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 
-// All threads of the cluster; writes before it, to global memory too, are visible after it.
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // A word of the same shared-memory variable in block `rank` of the cluster.
 __device__ __forceinline__ uint32_t load_of_rank(const uint32_t* p, uint32_t rank) {
     const uint32_t local = static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -307,7 +307,7 @@ def test_embedding_one_token_many_times(gemm_lib):
 
 DISTILL_SIZES = [(1, 1, 1), (1, 8, 3), (3, 7, 7), (5, 100, 1), (2, 1000, 64), (40, 333, 20), (3, 4096, 200), (2, 8200, 33),
                  (7, 20011, 16), (2, 50021, 1024), (1, 131072, 64), (400, 136, 5), (2, 300000, 8),
-                 (1, 850000, 4)]
+                 (1, 850000, 4), (1000, 333, 20), (600, 4500, 7), (480, 20011, 9), (160, 66000, 64)]
 
 
 def _distill_case(rows, vocab, top, elem, value, index, pad, offset, given, tau, mask=True):
@@ -368,11 +368,11 @@ def test_distillation(gemm_lib, rows, vocab, top, elem, value, index, pad, offse
         plan.check()
 
 
-@pytest.mark.parametrize("vocab", [24, 1000, 50000, 150001])
+@pytest.mark.parametrize("rows,vocab", [(6, 24), (6, 1000), (6, 50000), (6, 150001), (700, 1000), (500, 9001), (160, 70000)])
 @pytest.mark.parametrize("call", ["backward", "forward_backward"])
-def test_distillation_in_place_and_without_dloss(gemm_lib, vocab, call):
-    c = _distill_case(6, vocab, 9, "bf16", "f32", "i32", 0, 0, False, 1.5)
-    with gemm_lib.DistillPlan(6, vocab, 9, "bf16") as plan:
+def test_distillation_in_place_and_without_dloss(gemm_lib, rows, vocab, call):
+    c = _distill_case(rows, vocab, 9, "bf16", "f32", "i32", 0, 0, False, 1.5)
+    with gemm_lib.DistillPlan(rows, vocab, 9, "bf16") as plan:
         over = c["logits"].clone()
         if call == "backward":
             plan.forward(over, c["ids"], c["values"], c["loss"], c["lse"], temperature=1.5)
@@ -383,8 +383,8 @@ def test_distillation_in_place_and_without_dloss(gemm_lib, vocab, call):
         _check_distill(c, "bf16", 1.5, dloss=False)
 
 
-@pytest.mark.parametrize("vocab", [40, 3000, 70000])
-def test_distillation_odd_rows(gemm_lib, vocab):
+@pytest.mark.parametrize("vocab,times", [(40, 1), (3000, 1), (70000, 1), (40, 100), (1003, 60), (17000, 30)])
+def test_distillation_odd_rows(gemm_lib, vocab, times):
     """Rows whose masks leave nothing, infinities and NaN, equal ids: each stays in its row."""
     c = _distill_case(9, vocab, 6, "f32", "f32", "i64", 0, 0, False, 1.0, mask=False)
     ids, values, logits = c["ids"], c["values"], c["logits"]
@@ -403,7 +403,10 @@ def test_distillation_odd_rows(gemm_lib, vocab):
     logits[7, :] = torch.finfo(torch.float32).min
     logits[7, ids[7, 0]] = 0.0             # a mask of the type's lowest value
     ids[7, 1:] = -1
-    with gemm_lib.DistillPlan(9, vocab, 6, "f32") as plan:
+    for k in ("loss", "lse", "dlogits", "logits", "ids", "values", "dloss"):     # the same rows many times
+        c[k] = c[k].repeat(times, *[1] * (c[k].dim() - 1))
+    ids, values, logits = c["ids"], c["values"], c["logits"]
+    with gemm_lib.DistillPlan(9 * times, vocab, 6, "f32") as plan:
         for both in (False, True):
             for k in ("loss", "lse", "dlogits"):
                 c[k].fill_(5.0)
@@ -414,11 +417,11 @@ def test_distillation_odd_rows(gemm_lib, vocab):
                 plan.backward(logits, ids, values, c["lse"], c["dlogits"], dloss=c["dloss"])
             loss, lse, grad = (c[k].clone() for k in ("loss", "lse", "dlogits"))
             for r in (0, 1, 2):
-                assert loss[r] == 0 and lse[r] == -math.inf and not bool(grad[r].any()), r
+                assert not bool(loss[r::9].any()) and bool((lse[r::9] == -math.inf).all()) and not bool(grad[r::9].any()), r
             for r in (3, 7):
-                assert abs(loss[r]) < 1e-6 and not bool((grad[r].abs() > 1e-6).any()), r
-            assert bool(torch.isnan(loss[6])) and bool(torch.isnan(lse[6])) and bool(torch.isnan(grad[6]).all())
-            some = [4, 5, 8]
+                assert bool((loss[r::9].abs() < 1e-6).all()) and not bool((grad[r::9].abs() > 1e-6).any()), r
+            assert all(bool(torch.isnan(t[6::9]).all()) for t in (loss, lse, grad))
+            some = torch.tensor([r for r in range(9 * times) if r % 9 in (4, 5, 8)], device="cuda")
             part = {k: c[k][some] for k in ("logits", "ids", "values", "dloss", "loss", "lse", "dlogits")}
             part["given"] = None
             _check_distill(part, "f32", 1.0, what="both %s: " % both)
