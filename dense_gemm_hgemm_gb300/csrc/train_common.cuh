@@ -59,6 +59,104 @@ struct Pack {
     __device__ __forceinline__ void set_raw(int i, T v) { reinterpret_cast<T*>(&raw)[i] = v; }
 };
 
+// ---- pairs of fp32 values, which one instruction works on -------------------------
+
+struct Pair {
+    uint64_t bits;
+    __device__ __forceinline__ Pair() {}
+    __device__ __forceinline__ Pair(float lo, float hi) {
+        asm("mov.b64 %0, {%1, %2};" : "=l"(bits) : "f"(lo), "f"(hi));
+    }
+    __device__ __forceinline__ void get(float& lo, float& hi) const {
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(bits));
+    }
+};
+
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.bits) : "l"(a.bits), "l"(b.bits), "l"(c.bits));
+    return d;
+}
+
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.bits) : "l"(a.bits), "l"(b.bits));
+    return d;
+}
+
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.bits) : "l"(a.bits), "l"(b.bits));
+    return d;
+}
+
+// Elements 2j and 2j + 1 of a pack, and back (rounded once).
+template <int VEC>
+__device__ __forceinline__ Pair pair_of(const Pack<float, VEC>& q, int j) {
+    const float* f = reinterpret_cast<const float*>(&q.raw);
+    return Pair(f[2 * j], f[2 * j + 1]);
+}
+template <int VEC>
+__device__ __forceinline__ Pair pair_of(const Pack<__half, VEC>& q, int j) {
+    const float2 f = __half22float2(reinterpret_cast<const __half2*>(&q.raw)[j]);
+    return Pair(f.x, f.y);
+}
+template <int VEC>
+__device__ __forceinline__ Pair pair_of(const Pack<__nv_bfloat16, VEC>& q, int j) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(&q.raw)[j];
+    return Pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+template <int VEC>
+__device__ __forceinline__ void set_pair(Pack<float, VEC>& q, int j, Pair v) {
+    float* f = reinterpret_cast<float*>(&q.raw);
+    v.get(f[2 * j], f[2 * j + 1]);
+}
+template <int VEC>
+__device__ __forceinline__ void set_pair(Pack<__half, VEC>& q, int j, Pair v) {
+    float lo, hi;
+    v.get(lo, hi);
+    reinterpret_cast<__half2*>(&q.raw)[j] = __floats2half2_rn(lo, hi);
+}
+template <int VEC>
+__device__ __forceinline__ void set_pair(Pack<__nv_bfloat16, VEC>& q, int j, Pair v) {
+    float lo, hi;
+    v.get(lo, hi);
+    reinterpret_cast<__nv_bfloat162*>(&q.raw)[j] = __floats2bfloat162_rn(lo, hi);
+}
+
+// The largest of some packs' elements (NaN aside).
+template <int VEC, int N>
+__device__ __forceinline__ float pack_max(const Pack<float, VEC> (&q)[N]) {
+    float m = reinterpret_cast<const float*>(&q[0].raw)[0];
+#pragma unroll
+    for (int b = 0; b < N; ++b) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) m = fmaxf(m, reinterpret_cast<const float*>(&q[b].raw)[i]);
+    }
+    return m;
+}
+template <typename T2, int WORDS, typename P, int N>
+__device__ __forceinline__ T2 word_max(const P (&q)[N]) {
+    T2 m = reinterpret_cast<const T2*>(&q[0].raw)[0];
+#pragma unroll
+    for (int b = 0; b < N; ++b) {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) m = __hmax2(m, reinterpret_cast<const T2*>(&q[b].raw)[i]);
+    }
+    return m;
+}
+template <int VEC, int N>
+__device__ __forceinline__ float pack_max(const Pack<__half, VEC> (&q)[N]) {
+    const float2 f = __half22float2(word_max<__half2, VEC / 2>(q));
+    return fmaxf(f.x, f.y);
+}
+template <int VEC, int N>
+__device__ __forceinline__ float pack_max(const Pack<__nv_bfloat16, VEC> (&q)[N]) {
+    const float2 f = __bfloat1622float2(word_max<__nv_bfloat162, VEC / 2>(q));
+    return fmaxf(f.x, f.y);
+}
+
 // The first n of VEC elements at p (the rest zeros); p is aligned to the pack.
 template <typename T, int VEC>
 __device__ __forceinline__ Pack<T, VEC> load_pack(const T* p, int64_t n) {

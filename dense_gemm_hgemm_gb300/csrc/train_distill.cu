@@ -167,26 +167,84 @@ __device__ float load_entries(const Entries& en, const Teacher& t, int64_t row, 
 }
 
 // ---- running maximum and sum ----------------------------------------------------------
+//
+// Of a set of logits s: k = max s c, in log2 units, and sum exp2(s c - k).  The reference
+// k is rounded once and subtracted exactly from then on, so it costs no accuracy.  A
+// reference below kMasked is that of masked logits only (-infinity, or a type's lowest
+// value, whose scaled value may leave fp32): their sum counts from zero and is zero.
 
-__device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
+constexpr float kMasked = -1e30f;
 
-// sum exp2((x - m) c) over two sets with maxima m, m2.
-__device__ __forceinline__ void merge(float& m, float& s, float m2, float s2, float c) {
-    const float high = fmaxf(m, m2), base = finite_base(high);
-    s = s * exp2_fast((m - base) * c) + s2 * exp2_fast((m2 - base) * c);
-    m = high;
+__device__ __forceinline__ float finite_base(float k) { return k < kMasked ? 0.f : k; }
+
+__device__ __forceinline__ void merge(float& k, float& s, float k2, float s2) {
+    const float high = fmaxf(k, k2), base = finite_base(high);
+    s = s * exp2_fast(k - base) + s2 * exp2_fast(k2 - base);
+    k = high;
+}
+
+template <typename T>
+struct Running {
+    static constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+    float k = -INFINITY;
+    Pair sum = Pair(0.f, 0.f), sum_b = Pair(0.f, 0.f);
+
+    template <int N>
+    __device__ __forceinline__ void add(const Pack<T, VEC> (&q)[N], float c) {
+        const float high = fmaxf(k, pack_max(q) * c), base = finite_base(high);
+        const float shrink = exp2_fast(k - base);
+        k = high;
+        sum = mul2(sum, Pair(shrink, shrink));
+        sum_b = mul2(sum_b, Pair(shrink, shrink));
+        const Pair c2(c, c), base2(-base, -base);
+#pragma unroll
+        for (int b = 0; b < N; ++b) {
+#pragma unroll
+            for (int j = 0; j < VEC / 2; ++j) {
+                float lo, hi;
+                fma2(pair_of(q[b], j), c2, base2).get(lo, hi);
+                Pair& to = j & 1 ? sum_b : sum;
+                to = add2(to, Pair(exp2_fast(lo), exp2_fast(hi)));
+            }
+        }
+    }
+    __device__ __forceinline__ float total() const {
+        float lo, hi;
+        add2(sum, sum_b).get(lo, hi);
+        return lo + hi;
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ Pack<T, 16 / sizeof(T)> all_masked() {
+    Pack<T, 16 / static_cast<int>(sizeof(T))> q;
+#pragma unroll
+    for (int i = 0; i < 16 / static_cast<int>(sizeof(T)); ++i) q.set(i, -INFINITY);
+    return q;
+}
+
+// scale * exp2(s c - log2_all) of each element of a pack.
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> gradient(const Pack<T, VEC>& q, float c, float log2_all, float scale) {
+    Pack<T, VEC> g;
+    const Pair c2(c, c), all2(-log2_all, -log2_all), scale2(scale, scale);
+#pragma unroll
+    for (int j = 0; j < VEC / 2; ++j) {
+        float lo, hi;
+        fma2(pair_of(q, j), c2, all2).get(lo, hi);
+        set_pair(g, j, mul2(scale2, Pair(exp2_fast(lo), exp2_fast(hi))));
+    }
+    return g;
 }
 
 // ---- the kernel ------------------------------------------------------------------------
 //
 // A block holds one piece of a row's logits in shared memory.  Forward: the blocks of a
-// row form a cluster; each finds its piece's maximum m and sum of exp2((s - m) c) in one
-// pass, and they exchange those and their parts of the loss.  Backward: the gradient of
-// the piece, from the piece.  Both: the piece is read from memory once.
-// Differences s - m are taken before the scaling, so masks of the type's lowest value do
-// not overflow.
+// row form a cluster; each finds its piece's k and sum in one pass, and they exchange
+// those and their parts of the loss.  Backward: the gradient of the piece, from the
+// piece.  Both: the piece is read from memory once.
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kThreads, 5) distill_kernel(const Args<T> a) {
+__global__ void __launch_bounds__(kThreads, 4) distill_kernel(const Args<T> a) {
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     constexpr bool kLoss = (MODE & kForward) != 0, kGrad = (MODE & kBackward) != 0;
     extern __shared__ __align__(16) uint8_t memory[];
@@ -228,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_kernel(const Args<T> a) {
     T* d = nullptr;
     if (kGrad) d = a.dlogits + row * a.ldd + begin;
 
-    float top_m = 0.f, log2_sum = 0.f;                   // of the whole row
+    float log2_all = given_lse * kLog2e;                 // log-sum-exp of the whole row, in log2 units
     bool empty = out;
     const T* src = a.logits + row * a.ldl + begin;
     const int off = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15u) / sizeof(T));
@@ -242,60 +300,46 @@ __global__ void __launch_bounds__(kThreads, 5) distill_kernel(const Args<T> a) {
         __syncthreads();                                 // the ragged ends
     }
     if (kLoss) {
-        float m = -INFINITY, sum = 0.f;
+        Running<T> run;
         if (!out) {
             constexpr int kBatch = 2;
-            for (int k = tid; k < packs; k += kBatch * kThreads) {
-                float v[kBatch][VEC];
-                float high = m;
+            for (int at = tid; at < packs; at += kBatch * kThreads) {
+                Pack<T, VEC> q[kBatch];
 #pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                    const int at = k + b * kThreads;
-                    Pack<T, VEC> q;
-                    if (at < packs) q = load_pack<T, VEC>(room + at * VEC, VEC);
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        v[b][i] = at < packs ? q.get(i) : -INFINITY;
-                        high = fmaxf(high, v[b][i]);
-                    }
-                }
-                const float base = finite_base(high);
-                sum *= exp2_fast((m - base) * c);
-                m = high;
-#pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) sum += exp2_fast((v[b][i] - base) * c);
-                }
+                for (int b = 0; b < kBatch; ++b)
+                    q[b] = at + b * kThreads < packs ? load_pack<T, VEC>(room + (at + b * kThreads) * VEC, VEC)
+                                                     : all_masked<T>();
+                run.add(q, c);
             }
         }
+        float k = run.k, sum = run.total();
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
-            merge(m, sum, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, sum, o), c);
+            merge(k, sum, __shfl_xor_sync(0xffffffffu, k, o), __shfl_xor_sync(0xffffffffu, sum, o));
         if (lane == 0) {
-            part[0][warp] = m;
+            part[0][warp] = k;
             part[1][warp] = sum;
         }
         __syncthreads();
-        m = part[0][0];
+        k = part[0][0];
         sum = part[1][0];
-        for (int w = 1; w < kWarps; ++w) merge(m, sum, part[0][w], part[1][w], c);
-        // the entries in the piece: p (log2 p - (s - m) c), and their mass
+        for (int w = 1; w < kWarps; ++w) merge(k, sum, part[0][w], part[1][w]);
+        // the entries in the piece: p (log2 p - (s c - k)), and their mass
         if (warp == 0) {
             float terms = 0.f, here = 0.f;
             if (!out) {
-                const float base = finite_base(m);
+                const float base = finite_base(k);
                 for (int j = lane; j < top; j += 32) {
                     const int at = en.id[j] - begin;
                     if (en.id[j] >= 0 && at >= 0 && at < n && !(en.p[j] == 0.f)) {
-                        terms += en.p[j] * (en.log2p[j] - (to_f32(s[at]) - base) * c);
+                        terms += en.p[j] * (en.log2p[j] - (to_f32(s[at]) * c - base));
                         here += en.p[j];
                     }
                 }
                 terms = warp_sum(terms);
                 here = warp_sum(here);
             }
-            const float4 mine = make_float4(m, sum, terms, here);
+            const float4 mine = make_float4(k, sum, terms, here);
             if (shared_row) {
                 __syncwarp();
                 // every block has started: put this block's numbers into each one's memory
@@ -320,38 +364,32 @@ __global__ void __launch_bounds__(kThreads, 5) distill_kernel(const Args<T> a) {
         } else {
             __syncthreads();
         }
-        top_m = exchange[0].x;
-        float all = exchange[0].y;
-        for (int r = 1; r < a.pieces; ++r) merge(top_m, all, exchange[r].x, exchange[r].y, c);
-        top_m = finite_base(top_m);
+        float high = exchange[0].x, all = exchange[0].y;
+        for (int r = 1; r < a.pieces; ++r) merge(high, all, exchange[r].x, exchange[r].y);
+        high = finite_base(high);
         empty = out || all == 0.f;
-        log2_sum = log2f(all);
+        const float log2_sum = log2f(all);
+        log2_all = high + log2_sum;
         if (rank == 0 && tid == 0) {
             float total = mass * log2_sum;
             for (int r = 0; r < a.pieces; ++r)
-                total += exchange[r].z + (exchange[r].w == 0.f ? 0.f : exchange[r].w * (top_m - finite_base(exchange[r].x)) * c);
+                total += exchange[r].z + (exchange[r].w == 0.f ? 0.f : exchange[r].w * (high - finite_base(exchange[r].x)));
             a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * total;
-            a.lse[row] = empty ? -INFINITY : top_m / a.temperature + kLn2 * log2_sum;
+            a.lse[row] = empty ? -INFINITY : kLn2 * log2_all;
         }
     }
     if (!kGrad) return;
 
     const bool same = (reinterpret_cast<uintptr_t>(d) & 15u) == (reinterpret_cast<uintptr_t>(src) & 15u);
     const float scale = a.temperature * (a.dloss ? a.dloss[row] : 1.f);
-    const float q_scale = scale * mass, inverse = 1.f / a.temperature;
-    // log2 q
-    const auto log2q = [&](float x) {
-        return MODE == kBoth ? (x - top_m) * c - log2_sum : (x * inverse - given_lse) * kLog2e;
-    };
+    const float q_scale = scale * mass;
     for (int k = tid; k < packs; k += kThreads) {
         Pack<T, VEC> g;
         if (empty) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) g.set(i, 0.f);
         } else {
-            const Pack<T, VEC> q = load_pack<T, VEC>(room + k * VEC, VEC);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) g.set(i, q_scale * exp2_fast(log2q(q.get(i))));
+            g = gradient(load_pack<T, VEC>(room + k * VEC, VEC), c, log2_all, q_scale);
         }
         const int at = k * VEC - off;                    // the pack's first element in the piece
         if (same && at >= 0 && at + VEC <= n) {
@@ -374,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 5) distill_kernel(const Args<T> a) {
                 p += en.p[k];
                 first = first && k >= j;
             }
-            if (first) d[at] = from_f32<T>(scale * (mass * exp2_fast(log2q(to_f32(s[at]))) - p));
+            if (first) d[at] = from_f32<T>(scale * (mass * exp2_fast(to_f32(s[at]) * c - log2_all) - p));
         }
     }
     if (!arrived) wait_phase(&barrier, 0);               // no copy may land in a finished block's memory
@@ -445,6 +483,7 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     constexpr int kStage = kStageBytes / static_cast<int>(sizeof(T));     // elements
     constexpr bool kGrad = MODE == kBoth;
+    constexpr int kBatch = kStage / VEC / kComputeThreads;                // packs a thread takes of a stage
     extern __shared__ __align__(16) uint8_t memory[];
     __shared__ StreamBarriers sh;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
@@ -563,58 +602,48 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
             const int packs = (off + n + VEC - 1) / VEC;
             const uint32_t row_stage = stage, row_round = round;
             bool empty = out;
-            float top_m = 0.f, log2_sum = 0.f;
+            float log2_all = 0.f;                        // the row's log-sum-exp, in log2 units
             if (!out) {
-                float m = -INFINITY, sum = 0.f;
+                Running<T> run;
                 for (int p0 = 0; p0 < packs; p0 += kStage / VEC) {
                     wait_or_die(&sh.full[stage], round & 1, &sh.dead, a.error);
-                    const T* from = ring + stage * kStage;
-                    const int here = min(packs - p0, kStage / VEC);
-                    constexpr int kBatch = kStage / VEC / kComputeThreads;
+                    const T* from = ring + stage * kStage + thread * VEC;
                     Pack<T, VEC> q[kBatch];
-                    float v[kBatch][VEC];
-                    float high = m;
+                    if (packs - p0 >= kStage / VEC) {
 #pragma unroll
-                    for (int b = 0; b < kBatch; ++b) {
-                        const int at = thread + b * kComputeThreads;
-                        if (at < here) q[b] = load_pack<T, VEC>(from + at * VEC, VEC);
+                        for (int b = 0; b < kBatch; ++b) q[b] = load_pack<T, VEC>(from + b * kComputeThreads * VEC, VEC);
+                    } else {
 #pragma unroll
-                        for (int i = 0; i < VEC; ++i) {
-                            v[b][i] = at < here ? q[b].get(i) : -INFINITY;
-                            high = fmaxf(high, v[b][i]);
-                        }
+                        for (int b = 0; b < kBatch; ++b)
+                            q[b] = p0 + thread + b * kComputeThreads < packs
+                                       ? load_pack<T, VEC>(from + b * kComputeThreads * VEC, VEC)
+                                       : all_masked<T>();
                     }
                     if (!kGrad) {
                         __syncwarp();
                         if (lane == 0) arrive(&sh.empty[stage]);
                     }
-                    const float base = finite_base(high);
-                    sum *= exp2_fast((m - base) * c);
-                    m = high;
-#pragma unroll
-                    for (int b = 0; b < kBatch; ++b) {
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) sum += exp2_fast((v[b][i] - base) * c);
-                    }
+                    run.add(q, c);
                     if (++stage == static_cast<uint32_t>(stages)) {
                         stage = 0;
                         ++round;
                     }
                 }
+                float k = run.k, sum = run.total();
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1)
-                    merge(m, sum, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, sum, o), c);
+                    merge(k, sum, __shfl_xor_sync(0xffffffffu, k, o), __shfl_xor_sync(0xffffffffu, sum, o));
                 const int turn = exchanges & 1;
                 if (lane == 0) {
-                    sh.part[turn][0][worker] = m;
+                    sh.part[turn][0][worker] = k;
                     sh.part[turn][1][worker] = sum;
                 }
                 compute_barrier();
-                m = sh.part[turn][0][lane % kComputeWarps];
+                k = sh.part[turn][0][lane % kComputeWarps];
                 sum = sh.part[turn][1][lane % kComputeWarps];
 #pragma unroll
                 for (int o = kComputeWarps / 2; o > 0; o >>= 1)
-                    merge(m, sum, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, sum, o), c);
+                    merge(k, sum, __shfl_xor_sync(0xffffffffu, k, o), __shfl_xor_sync(0xffffffffu, sum, o));
                 if (a.pieces > 1) {
                     if (worker == 0) {
                         if (lane == 0)
@@ -628,30 +657,29 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
                                          : "=r"(barrier_at) : "r"(shared_address(&sh.exchanged[turn])), "r"(lane));
                             asm volatile(
                                 "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];"
-                                :: "r"(slot_at), "f"(m), "f"(sum), "r"(barrier_at) : "memory");
+                                :: "r"(slot_at), "f"(k), "f"(sum), "r"(barrier_at) : "memory");
                         }
                         __syncwarp();
                     }
                     wait_or_die(&sh.exchanged[turn], (exchanges >> 1) & 1, &sh.dead, a.error);
-                    m = sh.exchange[turn][0].x;
+                    k = sh.exchange[turn][0].x;
                     sum = sh.exchange[turn][0].y;
                     for (int r = 1; r < a.pieces; ++r)
-                        merge(m, sum, sh.exchange[turn][r].x, sh.exchange[turn][r].y, c);
+                        merge(k, sum, sh.exchange[turn][r].x, sh.exchange[turn][r].y);
                 }
                 ++exchanges;
-                top_m = finite_base(m);
                 empty = sum == 0.f;
-                log2_sum = log2f(sum);
+                log2_all = finite_base(k) + log2f(sum);
             }
             if (rank == 0 && worker == 0) {
                 float total = 0.f;
                 if (!empty)
                     for (int j = lane; j < top; j += 32)
-                        if (!(en.p[j] == 0.f)) total += en.p[j] * (en.log2p[j] - (en.x[j] - top_m) * c + log2_sum);
+                        if (!(en.p[j] == 0.f)) total += en.p[j] * (en.log2p[j] - (en.x[j] * c - log2_all));
                 total = warp_sum(total);
                 if (lane == 0) {
                     a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * total;
-                    a.lse[row] = empty ? -INFINITY : top_m / a.temperature + kLn2 * log2_sum;
+                    a.lse[row] = empty ? -INFINITY : kLn2 * log2_all;
                 }
             }
             if (kGrad) {
@@ -663,28 +691,31 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
                 round = row_round;
                 for (int p0 = 0; p0 < packs; p0 += kStage / VEC) {
                     const T* from = ring + stage * kStage;
-                    const int here = min(packs - p0, kStage / VEC);
+                    const int at0 = (p0 + thread) * VEC - off;       // of the first pack, in the piece
+                    if (!empty && same && p0 * VEC >= off && p0 * VEC - off + kStage <= n) {
 #pragma unroll
-                    for (int b = 0; b < kStage / VEC / kComputeThreads; ++b) {
-                        const int mine = thread + b * kComputeThreads;
-                        if (mine >= here) continue;
-                        Pack<T, VEC> g;
-                        if (empty) {
+                        for (int b = 0; b < kBatch; ++b)
+                            store_pack<T, VEC>(d + at0 + b * kComputeThreads * VEC, VEC,
+                                               gradient(load_pack<T, VEC>(from + (thread + b * kComputeThreads) * VEC, VEC),
+                                                        c, log2_all, q_scale));
+                    } else {
+                        for (int b = 0; b < kBatch; ++b) {
+                            const int mine = thread + b * kComputeThreads, at = at0 + b * kComputeThreads * VEC;
+                            if (p0 + mine >= packs) break;
+                            Pack<T, VEC> g;
+                            if (empty) {
 #pragma unroll
-                            for (int i = 0; i < VEC; ++i) g.set(i, 0.f);
-                        } else {
-                            const Pack<T, VEC> q = load_pack<T, VEC>(from + mine * VEC, VEC);
+                                for (int i = 0; i < VEC; ++i) g.set(i, 0.f);
+                            } else {
+                                g = gradient(load_pack<T, VEC>(from + mine * VEC, VEC), c, log2_all, q_scale);
+                            }
+                            if (same && at >= 0 && at + VEC <= n) {
+                                store_pack<T, VEC>(d + at, VEC, g);
+                            } else {
 #pragma unroll
-                            for (int i = 0; i < VEC; ++i)
-                                g.set(i, q_scale * exp2_fast((q.get(i) - top_m) * c - log2_sum));
-                        }
-                        const int at = (p0 + mine) * VEC - off;
-                        if (same && at >= 0 && at + VEC <= n) {
-                            store_pack<T, VEC>(d + at, VEC, g);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < VEC; ++i)
-                                if (at + i >= 0 && at + i < n) d[at + i] = reinterpret_cast<const T*>(&g.raw)[i];
+                                for (int i = 0; i < VEC; ++i)
+                                    if (at + i >= 0 && at + i < n) d[at + i] = reinterpret_cast<const T*>(&g.raw)[i];
+                            }
                         }
                     }
                     if (!out) {
@@ -709,7 +740,7 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
                             leads = leads && i >= j;
                         }
                         if (leads)
-                            d[at] = from_f32<T>(scale * (mass * exp2_fast((en.x[j] - top_m) * c - log2_sum) - p));
+                            d[at] = from_f32<T>(scale * (mass * exp2_fast(en.x[j] * c - log2_all) - p));
                     }
                 }
             }
@@ -746,35 +777,34 @@ __global__ void __launch_bounds__(kThreads) distill_forward_wide_kernel(const Ar
     }
     __syncthreads();
     const float mass = row_mass;
-    float m = -INFINITY, sum = 0.f;
+    float k = -INFINITY, sum = 0.f;
     if (mass != 0.f) {
-        for (int i = threadIdx.x; i < a.vocab; i += kThreads) m = fmaxf(m, to_f32(s[i]));
-        const float base = finite_base(m);
-        for (int i = threadIdx.x; i < a.vocab; i += kThreads) sum += exp2_fast((to_f32(s[i]) - base) * c);
+        for (int i = threadIdx.x; i < a.vocab; i += kThreads) k = fmaxf(k, to_f32(s[i]) * c);
+        const float base = finite_base(k);
+        for (int i = threadIdx.x; i < a.vocab; i += kThreads) sum += exp2_fast(to_f32(s[i]) * c - base);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
-        merge(m, sum, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, sum, o), c);
+        merge(k, sum, __shfl_xor_sync(0xffffffffu, k, o), __shfl_xor_sync(0xffffffffu, sum, o));
     if (lane == 0) {
-        part[0][warp] = m;
+        part[0][warp] = k;
         part[1][warp] = sum;
     }
     __syncthreads();
     if (warp != 0) return;
-    m = part[0][0];
+    k = part[0][0];
     sum = part[1][0];
-    for (int w = 1; w < kWarps; ++w) merge(m, sum, part[0][w], part[1][w], c);
-    m = finite_base(m);
+    for (int w = 1; w < kWarps; ++w) merge(k, sum, part[0][w], part[1][w]);
     const bool empty = mass == 0.f || sum == 0.f;
-    const float log2_sum = log2f(sum);
+    const float log2_all = finite_base(k) + log2f(sum);
     float total = 0.f;
     if (!empty)
         for (int j = lane; j < top; j += 32)
-            if (!(en.p[j] == 0.f)) total += en.p[j] * (en.log2p[j] - (to_f32(s[en.id[j]]) - m) * c + log2_sum);
+            if (!(en.p[j] == 0.f)) total += en.p[j] * (en.log2p[j] - (to_f32(s[en.id[j]]) * c - log2_all));
     total = warp_sum(total);
     if (lane == 0) {
         a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * total;
-        a.lse[row] = empty ? -INFINITY : m / a.temperature + kLn2 * log2_sum;
+        a.lse[row] = empty ? -INFINITY : kLn2 * log2_all;
     }
 }
 

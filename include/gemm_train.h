@@ -180,7 +180,8 @@ gemm_status_t gemm_distill_plan_create(int64_t max_rows, int64_t vocab, int64_t 
  *     loss = tau^2 * sum_j p_j * (log p_j - log q_{ids_j})     (0 where p_j = 0)
  * A row is left out where the teacher has no mass (no entry, or -infinity values
  * only) or where no logit is above -infinity: loss 0, lse -infinity, gradient 0.
- * Logits of -infinity (masked tokens) have q = 0; NaN logits give NaN.
+ * Logits of -infinity (masked tokens) have q = 0, and a logit below -1e30 * tau
+ * counts as one (masks of a type's lowest value); NaN logits give NaN.
  * temperature > 0.  An id >= vocab is reported by gemm_distill_plan_check and
  * taken as no entry.
  */
