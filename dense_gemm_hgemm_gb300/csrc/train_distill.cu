@@ -9,7 +9,7 @@
 namespace gbt {
 // How the pipeline over rows cuts a row and fills the GPU (see distill_stream_kernel).
 struct StreamShape {
-    int pieces, piece, stages;
+    int pieces, piece, stages, slots;
     int clusters;            // resident at once; 0 = not used
     size_t smem;
 };
@@ -127,30 +127,53 @@ struct Entries {
     float* log2p;
     float* p;
     float* x;      // the student's logits at the ids (where a kernel fetches them)
+    float* own;    // sum of p over an id's equals at its first entry, -1 at the others
 };
 
 // One warp: a row's entries; returns the mass.  Logits are scaled to log2 values by
-// c = log2(e) / temperature.
-__device__ float load_entries(const Entries& en, const Teacher& t, int64_t row, float c, int vocab,
-                              int32_t* error) {
+// c = log2(e) / temperature.  `logits`: the row's, whose values at the ids go to en.x, or
+// null.  The loads of kBatch * 32 entries are in flight together.
+template <typename T>
+__device__ float load_entries(const Entries& en, const Teacher& t, int64_t row, const T* logits, float c,
+                              int vocab, int32_t* error) {
+    constexpr int kBatch = 4;
     const int lane = threadIdx.x % 32;
+    const float given = t.lse ? t.lse[row] * kLog2e : 0.f;
     float high = -INFINITY, sum = 0.f;
-    for (int j = lane; j < t.top; j += 32) {
-        int64_t id = load_index(t.ids, row * t.ld_ids + j, t.id_type);
-        float v = load_elem(t.values, row * t.ld_values + j, t.value_elem) * c;
-        if (id >= vocab) {
-            atomicOr(error, kErrorIndex);
-            id = -1;
+    for (int j0 = lane; j0 < t.top; j0 += 32 * kBatch) {
+        int64_t id[kBatch];
+        float v[kBatch], x[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int j = j0 + u * 32;
+            id[u] = j < t.top ? load_index(t.ids, row * t.ld_ids + j, t.id_type) : -1;
         }
-        if (id < 0) v = -INFINITY;
-        en.id[j] = id < 0 ? -1 : static_cast<int32_t>(id);
-        en.log2p[j] = v;
-        high = fmaxf(high, v);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int j = j0 + u * 32;
+            v[u] = j < t.top ? load_elem(t.values, row * t.ld_values + j, t.value_elem) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            if (id[u] >= vocab) {
+                atomicOr(error, kErrorIndex);
+                id[u] = -1;
+            }
+            x[u] = logits && id[u] >= 0 ? to_f32(logits[id[u]]) : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int j = j0 + u * 32;
+            if (j >= t.top) break;
+            const float l = id[u] < 0 ? -INFINITY : v[u] * c;
+            en.id[j] = id[u] < 0 ? -1 : static_cast<int32_t>(id[u]);
+            en.log2p[j] = l;
+            if (logits) en.x[j] = x[u];
+            high = fmaxf(high, l);
+        }
     }
-    float norm;
-    if (t.lse) {
-        norm = t.lse[row] * kLog2e;
-    } else {
+    float norm = given;
+    if (!t.lse) {
         high = warp_max(high);
         for (int j = lane; j < t.top; j += 32)
             sum += en.log2p[j] == -INFINITY ? 0.f : exp2_fast(en.log2p[j] - high);
@@ -164,6 +187,46 @@ __device__ float load_entries(const Entries& en, const Teacher& t, int64_t row, 
         sum += en.p[j];
     }
     return warp_sum(sum);
+}
+
+// Asks L2 for a row's entries.
+__device__ void prefetch_entries(const Teacher& t, int64_t row) {
+    const auto ask = [](const void* p, int64_t offset, int bytes) {
+        for (int b = threadIdx.x % 32 * 128; b < bytes; b += 32 * 128)
+            asm volatile("prefetch.global.L2 [%0];" :: "l"(static_cast<const uint8_t*>(p) + offset + b));
+    };
+    const int id_bytes = t.id_type == GEMM_INDEX_I64 ? 8 : 4, value_bytes = t.value_elem == GEMM_ELEM_F32 ? 4 : 2;
+    ask(t.ids, row * t.ld_ids * id_bytes, t.top * id_bytes);
+    ask(t.values, row * t.ld_values * value_bytes, t.top * value_bytes);
+}
+
+// One warp, after load_entries: fills `own`.  Ids are compared four at a time; equal
+// ones are rare.
+__device__ void join_equal_ids(const Entries& en, int top) {
+    __syncwarp();
+    for (int j = threadIdx.x % 32; j < top; j += 32) {
+        const int id = en.id[j];
+        float p = en.p[j];
+        if (id >= 0) {
+            bool equal = false;
+            for (int k = 0; k < top; k += 4) {
+                const int4 v = *reinterpret_cast<const int4*>(en.id + k);   // (16-byte aligned)
+                equal = equal || (v.x == id && k != j) || (v.y == id && k + 1 != j && k + 1 < top) ||
+                        (v.z == id && k + 2 != j && k + 2 < top) || (v.w == id && k + 3 != j && k + 3 < top);
+            }
+            if (equal) {
+                bool leads = true;
+                p = 0.f;
+                for (int k = 0; k < top; ++k) {
+                    if (en.id[k] != id) continue;
+                    p += en.p[k];
+                    leads = leads && k >= j;
+                }
+                if (!leads) p = -1.f;
+            }
+        }
+        en.own[j] = id >= 0 ? p : -1.f;
+    }
 }
 
 // ---- running maximum and sum ----------------------------------------------------------
@@ -273,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const Args<T> a) {
 
     const float c = kLog2e / a.temperature;
     if (warp == 0) {
-        const float mass = load_entries(en, a.teacher, row, c, a.vocab, a.error);
+        const float mass = load_entries<T>(en, a.teacher, row, nullptr, c, a.vocab, a.error);
         if (lane == 0) row_mass = mass;
     }
     float given_lse = 0.f;
@@ -421,26 +484,43 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const Args<T> a) {
 // ---- many rows: a pipeline over rows -----------------------------------------------------
 //
 // A block (or a cluster, each block with its part of the row) goes through rows, with
-// three kinds of warps: one copies the logits into a ring of kStageBytes stages, as far
-// ahead as there is room; one prepares the teacher's entries of the next row; the others
-// compute.  Forward frees a stage as soon as it is summed; both directions together keep
+// three kinds of warps: one copies the logits into a ring of stages, as far
+// ahead as there is room; some prepare the teacher's entries of the next rows (each is a
+// chain of loads, which take some microseconds behind the copies); the others compute.  Forward frees a stage as soon as it is summed; both directions together keep
 // the row's stages until its gradient is written, and copy the next row into those that
 // are free.  So memory is busy while a row is reduced, and no block starts or ends per row.
 
-constexpr int kStageBytes = 8192;
-constexpr int kMostStages = 25;
+template <int MODE> constexpr int kStageBytesOf = MODE == kBoth ? 16384 : 8192;
+constexpr int kMostStages = 16;
+constexpr int kEntryWords = 5;     // arrays of Entries
 constexpr int kComputeWarps = 8;
 constexpr int kComputeThreads = kComputeWarps * 32;
-constexpr int kStreamThreads = 64 + kComputeThreads;
+constexpr int kEntryWarps = 3;     // each prepares every third row's entries
+constexpr int kMostSlots = 2 * kEntryWarps;
+constexpr int kFirstCompute = 32 * (1 + kEntryWarps);
+constexpr int kStreamThreads = kFirstCompute + kComputeThreads;
 
 struct StreamBarriers {
     uint64_t full[kMostStages], empty[kMostStages];
-    uint64_t entries_full[2], entries_empty[2];
+    uint64_t entries_full[kMostSlots], entries_empty[kMostSlots];
     uint64_t exchanged[2];
     float4 exchange[2][kMaxCluster];
-    float part[2][2][kComputeWarps];
-    float mass[2];
+    float part[2][3][kComputeWarps];
+    float mass[kMostSlots], scale[kMostSlots];
     int dead;                // a wait ran out: nothing waits any more
+};
+
+// A place in a ring of buffers, and how often it has been passed.
+struct Turn {
+    int at;
+    uint32_t round;
+    __device__ __forceinline__ void next(int by, int size) {
+        at += by;
+        if (at >= size) {
+            at -= size;
+            ++round;
+        }
+    }
 };
 
 // As wait_phase; when it runs out (or another wait has) it returns at once from then on.
@@ -479,8 +559,9 @@ __device__ __forceinline__ void compute_barrier() {
 }
 
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const Args<T> a, int64_t rows, int stages) {
+__global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+    constexpr int kStageBytes = kStageBytesOf<MODE>;
     constexpr int kStage = kStageBytes / static_cast<int>(sizeof(T));     // elements
     constexpr bool kGrad = MODE == kBoth;
     constexpr int kBatch = kStage / VEC / kComputeThreads;                // packs a thread takes of a stage
@@ -491,10 +572,12 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
     const int64_t first = blockIdx.x / static_cast<unsigned>(a.pieces);
     const int64_t step = gridDim.x / static_cast<unsigned>(a.pieces);
     const int top = a.teacher.top;
+    const int padded_top = (top + 3) / 4 * 4;
     T* const ring = reinterpret_cast<T*>(memory);
     const auto entries = [&](int slot) {
-        float* at = reinterpret_cast<float*>(memory + stages * kStageBytes) + slot * 4 * top;
-        return Entries{reinterpret_cast<int32_t*>(at), at + top, at + 2 * top, at + 3 * top};
+        float* at = reinterpret_cast<float*>(memory + stages * kStageBytes) + slot * kEntryWords * padded_top;
+        return Entries{reinterpret_cast<int32_t*>(at), at + padded_top, at + 2 * padded_top, at + 3 * padded_top,
+                       at + 4 * padded_top};
     };
     const int begin = rank * a.piece;
     const int n = min(a.piece, a.vocab - begin);
@@ -504,11 +587,11 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
             init_barrier(&sh.full[k], 1);
             init_barrier(&sh.empty[k], kComputeWarps);
         }
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < slots; ++k) {
             init_barrier(&sh.entries_full[k], 1);
             init_barrier(&sh.entries_empty[k], kComputeWarps + 1);
-            init_barrier(&sh.exchanged[k], 1);
         }
+        for (int k = 0; k < 2; ++k) init_barrier(&sh.exchanged[k], 1);
         sh.dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -518,11 +601,10 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
     let_next_kernel_start();
 
     if (warp == 0) {                                     // copies
-        uint32_t stage = 0, round = 0;
-        int64_t k = 0;
-        for (int64_t row = first; row < rows; row += step, ++k) {
-            const int slot = k & 1;
-            wait_or_die(&sh.entries_full[slot], (k >> 1) & 1, &sh.dead, a.error);
+        Turn stage{0, 0}, turn{0, 0};
+        for (int64_t row = first; row < rows; row += step, turn.next(1, slots)) {
+            const int slot = turn.at;
+            wait_or_die(&sh.entries_full[slot], turn.round & 1, &sh.dead, a.error);
             const bool out = sh.mass[slot] == 0.f;
             __syncwarp();
             if (lane == 0) arrive(&sh.entries_empty[slot]);
@@ -539,8 +621,8 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
                 if (tail_begin + lane < end) tail = base[tail_begin + lane];
             }
             for (int at = 0; at < end; at += kStage) {
-                wait_or_die(&sh.empty[stage], (round & 1) ^ 1, &sh.dead, a.error);
-                T* const to = ring + stage * kStage;
+                wait_or_die(&sh.empty[stage.at], (stage.round & 1) ^ 1, &sh.dead, a.error);
+                T* const to = ring + stage.at * kStage;
                 const int lo = at == 0 ? head_end : at, hi = min(at + kStage, tail_begin);
                 const bool first_pack = at == 0 && off > 0;
                 const bool last_pack = tail_begin < end && tail_begin >= at && tail_begin < at + kStage;
@@ -553,61 +635,64 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
                 if (lane == 0 && !*static_cast<volatile int*>(&sh.dead)) {
                     const uint32_t bytes = hi > lo ? static_cast<uint32_t>((hi - lo) * static_cast<int>(sizeof(T))) : 0;
                     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
-                                 :: "r"(shared_address(&sh.full[stage])), "r"(bytes) : "memory");
+                                 :: "r"(shared_address(&sh.full[stage.at])), "r"(bytes) : "memory");
                     if (bytes > 0)
                         asm volatile(
                             "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                             :: "r"(shared_address(to + (lo - at))), "l"(base + lo), "r"(bytes),
-                               "r"(shared_address(&sh.full[stage])) : "memory");
+                               "r"(shared_address(&sh.full[stage.at])) : "memory");
                 }
-                if (++stage == static_cast<uint32_t>(stages)) {
-                    stage = 0;
-                    ++round;
-                }
+                stage.next(1, stages);
             }
         }
         // A wait that ran out may have left copies behind: let them land (bounded).
         if (*static_cast<volatile int*>(&sh.dead)) {
             for (int s = 0; s < stages; ++s) {
-                const uint32_t issued = round + (static_cast<uint32_t>(s) < stage ? 1 : 0);
+                const uint32_t issued = stage.round + (s < stage.at ? 1 : 0);
                 if (issued > 0) wait_phase(&sh.full[s], (issued - 1) & 1);
             }
         }
-    } else if (warp == 1) {                              // the teacher's entries
-        int64_t k = 0;
-        for (int64_t row = first; row < rows; row += step, ++k) {
-            const int slot = k & 1;
-            wait_or_die(&sh.entries_empty[slot], ((k >> 1) & 1) ^ 1, &sh.dead, a.error);
+    } else if (warp <= kEntryWarps) {                    // the teacher's entries
+        Turn turn{warp - 1, 0};
+        for (int64_t row = first + (warp - 1) * step; row < rows;
+             row += kEntryWarps * step, turn.next(kEntryWarps, slots)) {
+            const int slot = turn.at;
+            wait_or_die(&sh.entries_empty[slot], (turn.round & 1) ^ 1, &sh.dead, a.error);
             const Entries en = entries(slot);
-            const float mass = load_entries(en, a.teacher, row, c, a.vocab, a.error);
-            if (mass != 0.f)
-                for (int j = lane; j < top; j += 32)
-                    en.x[j] = en.id[j] >= 0 ? to_f32(a.logits[row * a.ldl + en.id[j]]) : 0.f;
-            if (lane == 0) sh.mass[slot] = mass;
+            if (row + kEntryWarps * step < rows) prefetch_entries(a.teacher, row + kEntryWarps * step);
+            const float dloss = kGrad && a.dloss ? a.dloss[row] : 1.f;
+            const float mass = load_entries<T>(en, a.teacher, row, kGrad ? nullptr : a.logits + row * a.ldl, c,
+                                              a.vocab, a.error);
+            if (kGrad) join_equal_ids(en, top);
+            if (lane == 0) {
+                sh.mass[slot] = mass;
+                if (kGrad) sh.scale[slot] = a.temperature * dloss;
+            }
             __syncwarp();
             if (lane == 0) arrive(&sh.entries_full[slot]);
         }
     } else {                                             // the arithmetic
-        const int thread = tid - 64, worker = warp - 2;
-        uint32_t stage = 0, round = 0, exchanges = 0;
-        int64_t k = 0;
-        for (int64_t row = first; row < rows; row += step, ++k) {
-            const int slot = k & 1;
-            wait_or_die(&sh.entries_full[slot], (k >> 1) & 1, &sh.dead, a.error);
+        const int thread = tid - kFirstCompute, worker = warp - kFirstCompute / 32;
+        uint32_t exchanges = 0;
+        Turn stage{0, 0}, entry{0, 0};
+        for (int64_t row = first; row < rows; row += step, entry.next(1, slots)) {
+            const int slot = entry.at;
+            wait_or_die(&sh.entries_full[slot], entry.round & 1, &sh.dead, a.error);
             const float mass = sh.mass[slot];
             const Entries en = entries(slot);
             const bool out = mass == 0.f;
             const T* src = a.logits + row * a.ldl + begin;
             const int off = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15u) / sizeof(T));
             const int packs = (off + n + VEC - 1) / VEC;
-            const uint32_t row_stage = stage, row_round = round;
+            const Turn row_stage = stage;
             bool empty = out;
             float log2_all = 0.f;                        // the row's log-sum-exp, in log2 units
+            float terms = 0.f;                           // of the loss: sum p (log2 p - x c)
             if (!out) {
                 Running<T> run;
                 for (int p0 = 0; p0 < packs; p0 += kStage / VEC) {
-                    wait_or_die(&sh.full[stage], round & 1, &sh.dead, a.error);
-                    const T* from = ring + stage * kStage + thread * VEC;
+                    wait_or_die(&sh.full[stage.at], stage.round & 1, &sh.dead, a.error);
+                    const T* from = ring + stage.at * kStage + thread * VEC;
                     Pack<T, VEC> q[kBatch];
                     if (packs - p0 >= kStage / VEC) {
 #pragma unroll
@@ -621,34 +706,47 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
                     }
                     if (!kGrad) {
                         __syncwarp();
-                        if (lane == 0) arrive(&sh.empty[stage]);
+                        if (lane == 0) arrive(&sh.empty[stage.at]);
                     }
                     run.add(q, c);
-                    if (++stage == static_cast<uint32_t>(stages)) {
-                        stage = 0;
-                        ++round;
+                    stage.next(1, stages);
+                }
+                // the entries of this part (forward: of the row, by the row's first block)
+                for (int j = thread; j < top; j += kComputeThreads) {
+                    const int at = en.id[j] - begin;
+                    if (en.id[j] < 0 || (kGrad ? at < 0 || at >= n : rank != 0)) continue;
+                    if (kGrad) {                         // the row's stages still hold its logits
+                        int s = row_stage.at + (off + at) / kStage;
+                        if (s >= stages) s -= stages;
+                        en.x[j] = to_f32(ring[s * kStage + (off + at) % kStage]);
                     }
+                    if (!(en.p[j] == 0.f)) terms += en.p[j] * (en.log2p[j] - en.x[j] * c);
                 }
                 float k = run.k, sum = run.total();
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1)
                     merge(k, sum, __shfl_xor_sync(0xffffffffu, k, o), __shfl_xor_sync(0xffffffffu, sum, o));
+                terms = warp_sum(terms);
                 const int turn = exchanges & 1;
                 if (lane == 0) {
                     sh.part[turn][0][worker] = k;
                     sh.part[turn][1][worker] = sum;
+                    sh.part[turn][2][worker] = terms;
                 }
                 compute_barrier();
                 k = sh.part[turn][0][lane % kComputeWarps];
                 sum = sh.part[turn][1][lane % kComputeWarps];
+                terms = sh.part[turn][2][lane % kComputeWarps];
 #pragma unroll
-                for (int o = kComputeWarps / 2; o > 0; o >>= 1)
+                for (int o = kComputeWarps / 2; o > 0; o >>= 1) {
                     merge(k, sum, __shfl_xor_sync(0xffffffffu, k, o), __shfl_xor_sync(0xffffffffu, sum, o));
+                    terms += __shfl_xor_sync(0xffffffffu, terms, o);
+                }
                 if (a.pieces > 1) {
                     if (worker == 0) {
                         if (lane == 0)
                             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
-                                         :: "r"(shared_address(&sh.exchanged[turn])), "r"(a.pieces * 8) : "memory");
+                                         :: "r"(shared_address(&sh.exchanged[turn])), "r"(a.pieces * 16) : "memory");
                         if (lane < a.pieces) {           // this block's numbers, to each block of the row
                             uint32_t slot_at, barrier_at;
                             asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
@@ -656,41 +754,37 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
                             asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
                                          : "=r"(barrier_at) : "r"(shared_address(&sh.exchanged[turn])), "r"(lane));
                             asm volatile(
-                                "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];"
-                                :: "r"(slot_at), "f"(k), "f"(sum), "r"(barrier_at) : "memory");
+                                "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, "
+                                "[%5];"
+                                :: "r"(slot_at), "f"(k), "f"(sum), "f"(terms), "f"(0.f), "r"(barrier_at) : "memory");
                         }
                         __syncwarp();
                     }
                     wait_or_die(&sh.exchanged[turn], (exchanges >> 1) & 1, &sh.dead, a.error);
                     k = sh.exchange[turn][0].x;
                     sum = sh.exchange[turn][0].y;
-                    for (int r = 1; r < a.pieces; ++r)
+                    terms = sh.exchange[turn][0].z;
+                    for (int r = 1; r < a.pieces; ++r) {
                         merge(k, sum, sh.exchange[turn][r].x, sh.exchange[turn][r].y);
+                        terms += sh.exchange[turn][r].z;
+                    }
                 }
                 ++exchanges;
                 empty = sum == 0.f;
                 log2_all = finite_base(k) + log2f(sum);
             }
-            if (rank == 0 && worker == 0) {
-                float total = 0.f;
-                if (!empty)
-                    for (int j = lane; j < top; j += 32)
-                        if (!(en.p[j] == 0.f)) total += en.p[j] * (en.log2p[j] - (en.x[j] * c - log2_all));
-                total = warp_sum(total);
-                if (lane == 0) {
-                    a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * total;
-                    a.lse[row] = empty ? -INFINITY : kLn2 * log2_all;
-                }
+            if (rank == 0 && thread == 0) {
+                a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * (terms + mass * log2_all);
+                a.lse[row] = empty ? -INFINITY : kLn2 * log2_all;
             }
             if (kGrad) {
                 T* const d = a.dlogits + row * a.ldd + begin;
                 const bool same = (reinterpret_cast<uintptr_t>(d) & 15u) == (reinterpret_cast<uintptr_t>(src) & 15u);
-                const float scale = a.temperature * (a.dloss ? a.dloss[row] : 1.f);
+                const float scale = sh.scale[slot];
                 const float q_scale = scale * mass;
                 stage = row_stage;
-                round = row_round;
                 for (int p0 = 0; p0 < packs; p0 += kStage / VEC) {
-                    const T* from = ring + stage * kStage;
+                    const T* from = ring + stage.at * kStage;
                     const int at0 = (p0 + thread) * VEC - off;       // of the first pack, in the piece
                     if (!empty && same && p0 * VEC >= off && p0 * VEC - off + kStage <= n) {
 #pragma unroll
@@ -720,26 +814,16 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
                     }
                     if (!out) {
                         __syncwarp();
-                        if (lane == 0) arrive(&sh.empty[stage]);
-                        if (++stage == static_cast<uint32_t>(stages)) {
-                            stage = 0;
-                            ++round;
-                        }
+                        if (lane == 0) arrive(&sh.empty[stage.at]);
+                        stage.next(1, stages);
                     }
                 }
                 if (!empty) {
                     compute_barrier();                   // the stores above come first
                     for (int j = thread; j < top; j += kComputeThreads) {
-                        const int id = en.id[j], at = id - begin;
-                        if (id < 0 || at < 0 || at >= n) continue;
-                        float p = 0.f;
-                        bool leads = true;               // of equal ids the first writes for all
-                        for (int i = 0; i < top; ++i) {
-                            if (en.id[i] != id) continue;
-                            p += en.p[i];
-                            leads = leads && i >= j;
-                        }
-                        if (leads)
+                        const float p = en.own[j];
+                        const int at = en.id[j] - begin;
+                        if (p >= 0.f && at >= 0 && at < n)
                             d[at] = from_f32<T>(scale * (mass * exp2_fast(en.x[j] * c - log2_all) - p));
                     }
                 }
@@ -772,7 +856,7 @@ __global__ void __launch_bounds__(kThreads) distill_forward_wide_kernel(const Ar
     const T* s = a.logits + row * a.ldl;
     const float c = kLog2e / a.temperature;
     if (warp == 0) {
-        const float mass = load_entries(en, a.teacher, row, c, a.vocab, a.error);
+        const float mass = load_entries<T>(en, a.teacher, row, nullptr, c, a.vocab, a.error);
         if (lane == 0) row_mass = mass;
     }
     __syncthreads();
@@ -850,16 +934,20 @@ gemm_status_t run_stream(Args<T> a, const StreamShape& shape, int64_t rows, void
     a.pieces = shape.pieces;
     const int64_t clusters = rows < shape.clusters ? rows : shape.clusters;
     return launch(distill_stream_kernel<T, MODE>, clusters * a.pieces, kStreamThreads, shape.smem, stream,
-                  a.pieces, a, rows, shape.stages);
+                  a.pieces, a, rows, shape.stages, shape.slots);
 }
 
 // The pipeline's shape for a plan; clusters == 0 where it does not suit.
 template <typename T, int MODE>
 StreamShape stream_shape(int64_t vocab, int64_t max_top) {
     constexpr int64_t kVec = 16 / sizeof(T);
-    const int64_t bytes = vocab * static_cast<int64_t>(sizeof(T)), entries = max_top * 32;
-    const int64_t room = (kMostShared - entries) / kStageBytes;
+    constexpr int64_t kStageBytes = kStageBytesOf<MODE>;
+    const int64_t bytes = vocab * static_cast<int64_t>(sizeof(T));
     StreamShape shape = {};
+    const int64_t slot = kEntryWords * sizeof(float) * ((max_top + 3) / 4 * 4);
+    shape.slots = slot * kMostSlots <= 16 * 1024 ? kMostSlots : kEntryWarps;
+    const int64_t entries = slot * shape.slots;
+    const int64_t room = (kMostShared - entries) / kStageBytes;
     shape.pieces = 1;
     int64_t stages = 6;
     if (MODE == kBoth) {
@@ -869,7 +957,7 @@ StreamShape stream_shape(int64_t vocab, int64_t max_top) {
         shape.piece = static_cast<int>(each * kVec);
         shape.pieces = static_cast<int>((packs + each - 1) / each);
         const int64_t need = ((each + 1) * 16 + kStageBytes - 1) / kStageBytes;
-        stages = need <= 4 ? 7 : need <= 10 ? 13 : kMostStages;
+        stages = need <= 2 ? 4 : need <= 4 ? 6 : 13;
         if (stages > room) stages = room;
         if (need > stages) return shape;
     } else {
