@@ -836,6 +836,94 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
     if (a.pieces > 1) cluster_barrier();                 // no block leaves while others write to it
 }
 
+// ---- short rows ---------------------------------------------------------------------------
+//
+// A warp keeps a whole row in registers, PACKS packs a lane, and asks for it before it
+// prepares the teacher's entries.  No block-wide step: for rows of some hundred logits the
+// blocks' and barriers' time of the other kernels is several times that of the memory.
+template <typename T, int MODE, int PACKS>
+__global__ void __launch_bounds__(kThreads) distill_short_kernel(const Args<T> a, int64_t rows) {
+    constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+    constexpr bool kLoss = (MODE & kForward) != 0, kGrad = (MODE & kBackward) != 0;
+    extern __shared__ __align__(16) uint8_t memory[];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    const int top = a.teacher.top, padded_top = (top + 3) / 4 * 4, n = a.vocab;
+    float* const mine = reinterpret_cast<float*>(memory) + warp * kEntryWords * padded_top;
+    const Entries en{reinterpret_cast<int32_t*>(mine), mine + padded_top, mine + 2 * padded_top,
+                     mine + 3 * padded_top, mine + 4 * padded_top};
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    if (row >= rows) return;
+    const T* src = a.logits + row * a.ldl;
+    const int off = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15u) / sizeof(T));
+    Pack<T, VEC> q[PACKS];
+#pragma unroll
+    for (int b = 0; b < PACKS; ++b) {
+        const int at = (b * 32 + lane) * VEC - off;      // the pack's first element in the row
+        if (at >= 0 && at + VEC <= n) {
+            q[b] = load_pack<T, VEC>(src + at, VEC);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                q[b].set_raw(i, at + i >= 0 && at + i < n ? src[at + i] : from_f32<T>(-INFINITY));
+        }
+    }
+    const float given = MODE == kBackward ? a.lse[row] : 0.f;
+    const float scale = kGrad ? a.temperature * (a.dloss ? a.dloss[row] : 1.f) : 0.f;
+    const float c = kLog2e / a.temperature;
+    const float mass = load_entries(en, a.teacher, row, src, c, n, a.error);
+    if (kGrad) join_equal_ids(en, top);
+    bool empty = mass == 0.f || (MODE == kBackward && given == -INFINITY);
+    float log2_all = given * kLog2e;
+    if (kLoss) {
+        Running<T> run;
+        run.add(q, c);
+        float k = run.k, sum = run.total(), terms = 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            merge(k, sum, __shfl_xor_sync(0xffffffffu, k, o), __shfl_xor_sync(0xffffffffu, sum, o));
+        empty = empty || sum == 0.f;
+        log2_all = finite_base(k) + log2f(sum);
+        if (!empty)
+            for (int j = lane; j < top; j += 32)
+                if (!(en.p[j] == 0.f)) terms += en.p[j] * (en.log2p[j] - (en.x[j] * c - log2_all));
+        terms = warp_sum(terms);
+        if (lane == 0) {
+            a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * terms;
+            a.lse[row] = empty ? -INFINITY : kLn2 * log2_all;
+        }
+    }
+    if (!kGrad) return;
+    T* const d = a.dlogits + row * a.ldd;
+    const bool same = (reinterpret_cast<uintptr_t>(d) & 15u) == (reinterpret_cast<uintptr_t>(src) & 15u);
+    const float q_scale = empty ? 0.f : scale * mass;
+    __syncwarp();                                        // the row has been read: d may be the logits
+#pragma unroll
+    for (int b = 0; b < PACKS; ++b) {
+        const int at = (b * 32 + lane) * VEC - off;
+        Pack<T, VEC> g;
+        if (empty) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) g.set(i, 0.f);
+        } else {
+            g = gradient(q[b], c, log2_all, q_scale);
+        }
+        if (same && at >= 0 && at + VEC <= n) {
+            store_pack<T, VEC>(d + at, VEC, g);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (at + i >= 0 && at + i < n) d[at + i] = reinterpret_cast<const T*>(&g.raw)[i];
+        }
+    }
+    if (empty) return;
+    __syncwarp();                                        // the stores above come first
+    for (int j = lane; j < top; j += 32)
+        if (en.own[j] >= 0.f)
+            d[en.id[j]] = from_f32<T>(scale * (mass * exp2_fast(en.x[j] * c - log2_all) - en.own[j]));
+}
+
 // ---- rows that no cluster can hold ---------------------------------------------------------
 
 // Forward over rows that no cluster can hold: one block a row, a pass for the maximum
@@ -907,8 +995,27 @@ void cut_row(Args<T>& a, int64_t rows, int sms, int64_t most) {
     a.pieces = static_cast<int>((packs + each - 1) / each);
 }
 
+// Rows that a warp's registers hold: up to 16 packs a lane, wherever the row begins.
+template <typename T>
+bool is_short(int64_t vocab) {
+    return vocab + 16 / static_cast<int>(sizeof(T)) - 1 <= 16 * 32 * (16 / static_cast<int>(sizeof(T)));
+}
+
+template <typename T, int MODE>
+gemm_status_t run_short(const Args<T>& a, int64_t rows, void* stream) {
+    constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+    const int lanes = (a.vocab + VEC - 1 + VEC - 1) / VEC;        // packs of a row, wherever it begins
+    const int64_t blocks = (rows + kWarps - 1) / kWarps;
+    const size_t smem = kWarps * kEntryWords * sizeof(float) * ((a.teacher.top + 3) / 4 * 4);
+    if (lanes <= 2 * 32) return launch(distill_short_kernel<T, MODE, 2>, blocks, kThreads, smem, stream, 1, a, rows);
+    if (lanes <= 4 * 32) return launch(distill_short_kernel<T, MODE, 4>, blocks, kThreads, smem, stream, 1, a, rows);
+    if (lanes <= 8 * 32) return launch(distill_short_kernel<T, MODE, 8>, blocks, kThreads, smem, stream, 1, a, rows);
+    return launch(distill_short_kernel<T, MODE, 16>, blocks, kThreads, smem, stream, 1, a, rows);
+}
+
 template <typename T, int MODE>
 gemm_status_t run(Args<T> a, int64_t rows, int sms, void* stream) {
+    if (is_short<T>(a.vocab)) return run_short<T, MODE>(a, rows, stream);
     cut_row(a, rows, sms, MODE == kBackward ? INT32_MAX : kMaxCluster);
     const size_t smem = (a.teacher.top * 12 + 15) / 16 * 16 + a.piece * sizeof(T) + 32;
     return launch(distill_kernel<T, MODE>, rows * a.pieces, kThreads, smem, stream,
@@ -916,12 +1023,23 @@ gemm_status_t run(Args<T> a, int64_t rows, int sms, void* stream) {
 }
 
 // Lets the kernels have as much shared memory as the largest launch asks for.
+template <typename T, int MODE>
+bool prepare_short() {
+    const int most = kWarps * kEntryWords * static_cast<int>(sizeof(float)) * kMaxTop;
+    const auto allow = [&](auto kernel) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) == cudaSuccess;
+    };
+    return allow(distill_short_kernel<T, MODE, 2>) && allow(distill_short_kernel<T, MODE, 4>) &&
+           allow(distill_short_kernel<T, MODE, 8>) && allow(distill_short_kernel<T, MODE, 16>);
+}
+
 template <typename T>
 gemm_status_t prepare() {
     const auto allow = [](auto kernel) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared) == cudaSuccess;
     };
-    if (allow(distill_stream_kernel<T, kForward>) && allow(distill_stream_kernel<T, kBoth>) &&
+    if (prepare_short<T, kForward>() && prepare_short<T, kBackward>() && prepare_short<T, kBoth>() &&
+        allow(distill_stream_kernel<T, kForward>) && allow(distill_stream_kernel<T, kBoth>) &&
         allow(distill_kernel<T, kForward>) && allow(distill_kernel<T, kBackward>) && allow(distill_kernel<T, kBoth>))
         return GEMM_OK;
     cudaGetLastError();
@@ -944,6 +1062,7 @@ StreamShape stream_shape(int64_t vocab, int64_t max_top) {
     constexpr int64_t kStageBytes = kStageBytesOf<MODE>;
     const int64_t bytes = vocab * static_cast<int64_t>(sizeof(T));
     StreamShape shape = {};
+    if (is_short<T>(vocab)) return shape;
     const int64_t slot = kEntryWords * sizeof(float) * ((max_top + 3) / 4 * 4);
     shape.slots = slot * kMostSlots <= 16 * 1024 ? kMostSlots : kEntryWarps;
     const int64_t entries = slot * shape.slots;
