@@ -22,6 +22,8 @@ from __future__ import annotations
 
 import ctypes
 
+import dense_gemm_hgemm_gb300 as _base   # (its C entry points are there once the library is loaded)
+
 from . import GemmError, _check, _stream, library
 
 __all__ = ["GEMM_ELEM_F16", "GEMM_ELEM_BF16", "GEMM_ELEM_F32", "GEMM_INDEX_I32", "GEMM_INDEX_I64",
@@ -133,6 +135,9 @@ class _Plan:
 
     _destroy = ""
 
+    def _drop(self):
+        """Forget the C entry points: they hold the plan's handle."""
+
     def _create(self, name, *args):
         _torch_types()
         self.handle = None
@@ -140,7 +145,33 @@ class _Plan:
         _check(getattr(library(), name)(*args, ctypes.byref(h)), name)
         self.handle = h.value
 
+    def _entry(self, kind, name, elem, weight, cols, rows=0):
+        """The C entry point of one call of this plan, which checks the arguments and
+        marshals them (the general path below each method does the same in Python and
+        says what is wrong); None where the C module could not be built."""
+        call = getattr(_base._pycall, "TrainCall", None)
+        if call is None:
+            return None
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            raw = lambda device: torch.cuda.current_stream(device).cuda_stream  # noqa: E731
+        kinds = (torch.float16, torch.bfloat16, torch.float32)
+        return call(kind, ctypes.cast(getattr(library(), name), ctypes.c_void_p).value, self.handle, kinds[elem],
+                    kinds[weight], (*kinds, torch.int32, torch.int64), cols, rows, torch.cuda.current_device(), raw)
+
+    @staticmethod
+    def _taken(entry, name, args) -> bool:
+        """Whether the C entry point took the call."""
+        if entry is None:
+            return False
+        status = entry(*args)
+        if status > 0:
+            raise GemmError(status, name)
+        return status == 0
+
     def close(self) -> None:
+        self._drop()
         handle, self.handle = getattr(self, "handle", None), None
         if handle:
             _check(getattr(library(), self._destroy)(handle), self._destroy)
@@ -168,10 +199,17 @@ class NormPlan(_Plan):
         self._elem = _elem(dtype)
         self._weight = self._elem if weight is None else _elem(weight)
         self._create("gemm_norm_plan_create", max_rows, cols, self._elem, self._weight)
+        self._forward = self._entry(0, "gemm_norm_forward", self._elem, self._weight, cols)
+        self._backward = self._entry(1, "gemm_norm_backward", self._elem, self._weight, cols)
+
+    def _drop(self):
+        self._forward = self._backward = None
 
     def forward(self, x, gamma, beta, y, mean=None, rstd=None, eps: float = 1e-5,
                 stream=None) -> None:
         """y = (x - mean) * rstd * gamma + beta; mean and rstd (fp32) are kept for backward."""
+        if self._taken(self._forward, "gemm_norm_forward", (x, gamma, beta, y, mean, rstd, eps, stream)):
+            return
         rows, cols = x.shape[0], self.cols
         px, ldx = _matrix(x, rows, cols, self._elem, "x")
         py, ldy = _matrix(y, rows, cols, self._elem, "y")
@@ -184,6 +222,9 @@ class NormPlan(_Plan):
     def backward(self, x, gamma, mean, rstd, dy, dx=None, dgamma=None, dbeta=None,
                  stream=None) -> None:
         """Gradients of x, gamma and beta (each optional) from dy."""
+        if self._taken(self._backward, "gemm_norm_backward",
+                       (x, gamma, mean, rstd, dy, dx, dgamma, dbeta, stream)):
+            return
         rows, cols = x.shape[0], self.cols
         px, ldx = _matrix(x, rows, cols, self._elem, "x")
         pdy, lddy = _matrix(dy, rows, cols, self._elem, "dy")
@@ -206,9 +247,16 @@ class EmbedPlan(_Plan):
         self._elem = _elem(dtype)
         self._grad = self._elem if grad is None else _elem(grad)
         self._create("gemm_embed_plan_create", vocab, dim, max_tokens, self._elem, self._grad)
+        self._forward = self._entry(2, "gemm_embed_forward", self._elem, self._grad, dim, vocab)
+        self._backward = self._entry(3, "gemm_embed_backward", self._elem, self._grad, dim, vocab)
+
+    def _drop(self):
+        self._forward = self._backward = None
 
     def forward(self, ids, table, out, scale: float = 1.0, padding: int = -1, stream=None) -> None:
         """out[t] = scale * table[ids[t]]; rows of padding tokens are zeros."""
+        if self._taken(self._forward, "gemm_embed_forward", (ids, table, out, scale, padding, stream)):
+            return
         n = ids.shape[0]
         pt, ldt = _matrix(table, self.vocab, self.dim, self._elem, "table")
         po, ldo = _matrix(out, n, self.dim, self._elem, "out")
@@ -219,6 +267,9 @@ class EmbedPlan(_Plan):
     def backward(self, ids, dout, dtable, scale: float = 1.0, padding: int = -1,
                  accumulate: bool = False, stream=None) -> None:
         """The table's gradient: written whole, or added to dtable where `accumulate`."""
+        if self._taken(self._backward, "gemm_embed_backward",
+                       (ids, dout, dtable, scale, padding, accumulate, stream)):
+            return
         n = ids.shape[0]
         pd, ldo = _matrix(dout, n, self.dim, self._elem, "dout")
         pt, ldt = _matrix(dtable, self.vocab, self.dim, self._grad, "dtable")
@@ -242,6 +293,13 @@ class DistillPlan(_Plan):
         self.max_rows, self.vocab, self.max_top = max_rows, vocab, max_top
         self._elem = _elem(dtype)
         self._create("gemm_distill_plan_create", max_rows, vocab, max_top, self._elem)
+        self._forward, self._backward, self._both = (
+            self._entry(kind, name, self._elem, self._elem, vocab)
+            for kind, name in ((4, "gemm_distill_forward"), (5, "gemm_distill_backward"),
+                               (6, "gemm_distill_forward_backward")))
+
+    def _drop(self):
+        self._forward = self._backward = self._both = None
 
     def _teacher(self, rows, ids, values, lse):
         top = ids.shape[1]
@@ -253,6 +311,9 @@ class DistillPlan(_Plan):
     def forward(self, logits, ids, values, loss, lse, temperature: float = 1.0, teacher_lse=None,
                 stream=None) -> None:
         """Each row's loss and the logits' log-sum-exp at the temperature (fp32)."""
+        if self._taken(self._forward, "gemm_distill_forward",
+                       (logits, ids, values, loss, lse, temperature, teacher_lse, stream)):
+            return
         rows = logits.shape[0]
         pl, ldl = _matrix(logits, rows, self.vocab, self._elem, "logits")
         teacher = self._teacher(rows, ids, values, teacher_lse)
@@ -264,6 +325,9 @@ class DistillPlan(_Plan):
     def backward(self, logits, ids, values, lse, dlogits, dloss=None, temperature: float = 1.0,
                  teacher_lse=None, stream=None) -> None:
         """The logits' gradient from forward's lse and each row's upstream gradient (None: ones)."""
+        if self._taken(self._backward, "gemm_distill_backward",
+                       (logits, ids, values, lse, dlogits, dloss, temperature, teacher_lse, stream)):
+            return
         rows = logits.shape[0]
         pl, ldl = _matrix(logits, rows, self.vocab, self._elem, "logits")
         pd, ldd = _matrix(dlogits, rows, self.vocab, self._elem, "dlogits")
@@ -277,6 +341,9 @@ class DistillPlan(_Plan):
     def forward_backward(self, logits, ids, values, loss, lse, dlogits, dloss=None,
                          temperature: float = 1.0, teacher_lse=None, stream=None) -> None:
         """Loss, lse and gradient in one call."""
+        if self._taken(self._both, "gemm_distill_forward_backward",
+                       (logits, ids, values, loss, lse, dlogits, dloss, temperature, teacher_lse, stream)):
+            return
         rows = logits.shape[0]
         pl, ldl = _matrix(logits, rows, self.vocab, self._elem, "logits")
         pd, ldd = _matrix(dlogits, rows, self.vocab, self._elem, "dlogits")
