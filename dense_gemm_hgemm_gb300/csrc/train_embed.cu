@@ -19,19 +19,79 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// One block a token.
-template <typename T>
+// ---- lookup ---------------------------------------------------------------------
+//
+// A group of `lanes` threads (a power of two, 8 to kThreads) takes TOKENS tokens: it loads
+// their ids, then PACKS packs of each one's row in every thread, so that two chained loads
+// serve TOKENS * PACKS * 16 bytes a thread.
+
+struct LookupParams {
+    const void* ids;
+    int id_type;
+    int64_t padding, tokens, vocab, ldt, ldo;
+    float scale;
+    int dim, lanes;
+    int32_t* error;
+};
+
+template <typename T, int VEC, int PACKS, int TOKENS>
 __global__ void __launch_bounds__(kThreads)
-embed_forward_kernel(const void* ids, int id_type, int64_t padding, const T* table, int64_t ldt,
-                     float scale, T* out, int64_t ldo, int64_t vocab, int dim, int32_t* error) {
+embed_forward_kernel(const LookupParams p, const T* __restrict__ table, T* __restrict__ out) {
     wait_for_previous_kernel();
-    const int64_t t = blockIdx.x;
-    const int64_t id = load_index(ids, t, id_type);
-    const bool inside = id >= 0 && id < vocab;
-    if (!inside && id != padding && threadIdx.x == 0) *error = 1;
-    const bool take = inside && id != padding;
-    for (int c = threadIdx.x; c < dim; c += kThreads)
-        out[t * ldo + c] = from_f32<T>(take ? scale * to_f32(table[id * ldt + c]) : 0.f);
+    let_next_kernel_start();
+    const int lane = threadIdx.x % p.lanes;
+    const int64_t first = (static_cast<int64_t>(blockIdx.x) * (kThreads / p.lanes) + threadIdx.x / p.lanes) * TOKENS;
+    int64_t id[TOKENS];
+#pragma unroll
+    for (int u = 0; u < TOKENS; ++u)
+        id[u] = first + u < p.tokens ? load_index(p.ids, first + u, p.id_type) : p.padding;
+#pragma unroll
+    for (int u = 0; u < TOKENS; ++u) {
+        if (id[u] == p.padding) {
+            id[u] = -1;
+        } else if (id[u] < 0 || id[u] >= p.vocab) {
+            *p.error = kErrorIndex;
+            id[u] = -1;
+        }
+    }
+    for (int c0 = lane * VEC; c0 < p.dim; c0 += p.lanes * VEC * PACKS) {
+        Pack<T, VEC> q[TOKENS][PACKS];
+#pragma unroll
+        for (int u = 0; u < TOKENS; ++u) {
+#pragma unroll
+            for (int k = 0; k < PACKS; ++k) {
+                const int c = c0 + k * p.lanes * VEC;
+                if (id[u] >= 0 && c < p.dim) q[u][k] = load_pack<T, VEC>(table + id[u] * p.ldt + c, p.dim - c);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < TOKENS; ++u) {
+            if (first + u >= p.tokens) return;
+#pragma unroll
+            for (int k = 0; k < PACKS; ++k) {
+                const int c = c0 + k * p.lanes * VEC;
+                if (c >= p.dim) break;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) q[u][k].set(i, id[u] >= 0 ? p.scale * q[u][k].get(i) : 0.f);
+                store_pack<T, VEC>(out + (first + u) * p.ldo + c, p.dim - c, q[u][k]);
+            }
+        }
+    }
+}
+
+template <typename T, int VEC>
+gemm_status_t lookup(LookupParams p, int sms, const T* table, T* out, void* stream) {
+    constexpr int PACKS = 2;
+    const int64_t packs = (static_cast<int64_t>(p.dim) + VEC - 1) / VEC;
+    p.lanes = 8;
+    while (p.lanes < kThreads && p.lanes * PACKS < packs) p.lanes *= 2;
+    const int groups = kThreads / p.lanes;
+    // four tokens a group where that leaves enough blocks to fill the GPU
+    if (p.tokens >= int64_t{4} * 8 * sms * groups)
+        return launch(embed_forward_kernel<T, VEC, PACKS, 4>, (p.tokens + 4 * groups - 1) / (4 * groups), kThreads,
+                      0, stream, 1, p, table, out);
+    return launch(embed_forward_kernel<T, VEC, PACKS, 1>, (p.tokens + groups - 1) / groups, kThreads, 0, stream, 1,
+                  p, table, out);
 }
 
 // ---- the table's gradient -------------------------------------------------------
@@ -102,7 +162,7 @@ __device__ __forceinline__ uint32_t key_of(const SortParams& p, int64_t t, bool 
     const int64_t id = load_index(p.ids, t, p.id_type);
     if (id == p.padding) return p.vocab;
     if (id >= 0 && id < static_cast<int64_t>(p.vocab)) return static_cast<uint32_t>(id);
-    if (report) *p.error = 1;
+    if (report) *p.error = kErrorIndex;
     return p.vocab;
 }
 
@@ -448,12 +508,16 @@ gemm_status_t gemm_embed_forward(gemm_embed_plan_t p, int64_t tokens, const void
         return GEMM_ERR_ALIGNMENT;
     const gemm_status_t st = gbt::check_device(p->device);
     if (st != GEMM_OK || tokens == 0) return st;
+    const gbt::LookupParams q{ids,  static_cast<int>(id_type), padding, tokens, p->vocab, ldt, ldo, scale,
+                              static_cast<int>(p->dim), 0, p->error_word};
+    const bool vec = gbt::rows_aligned(table, ldt, e) && gbt::rows_aligned(out, ldo, e);
     return gbt::with_elem(p->elem, [&](auto t) {
         using T = decltype(t);
-        return gbt::launch(gbt::embed_forward_kernel<T>, tokens, gbt::kThreads, 0, stream, 1, ids,
-                           static_cast<int>(id_type), padding, static_cast<const T*>(table), ldt,
-                           scale, static_cast<T*>(out), ldo, p->vocab, static_cast<int>(p->dim),
-                           p->error_word);
+        constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+        const T* from = static_cast<const T*>(table);
+        T* to = static_cast<T*>(out);
+        return vec ? gbt::lookup<T, kVec>(q, p->num_sms, from, to, stream)
+                   : gbt::lookup<T, 1>(q, p->num_sms, from, to, stream);
     });
 }
 
