@@ -125,6 +125,41 @@ __device__ __forceinline__ void set_pair(Pack<__nv_bfloat16, VEC>& q, int j, Pai
     reinterpret_cast<__nv_bfloat162*>(&q.raw)[j] = __floats2bfloat162_rn(lo, hi);
 }
 
+// All elements of some packs as pairs, and back (an even number of packs of one element
+// each, else pairs within the packs).
+template <typename T, int VEC, int PACKS>
+__device__ __forceinline__ void to_pairs(const Pack<T, VEC> (&p)[PACKS], Pair (&v)[PACKS * VEC / 2]) {
+    if constexpr (VEC == 1) {
+#pragma unroll
+        for (int j = 0; j < PACKS / 2; ++j) v[j] = Pair(p[2 * j].get(0), p[2 * j + 1].get(0));
+    } else {
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k) {
+#pragma unroll
+            for (int j = 0; j < VEC / 2; ++j) v[k * (VEC / 2) + j] = pair_of(p[k], j);
+        }
+    }
+}
+
+template <typename T, int VEC, int PACKS>
+__device__ __forceinline__ void from_pairs(const Pair (&v)[PACKS * VEC / 2], Pack<T, VEC> (&p)[PACKS]) {
+    if constexpr (VEC == 1) {
+#pragma unroll
+        for (int j = 0; j < PACKS / 2; ++j) {
+            float lo, hi;
+            v[j].get(lo, hi);
+            p[2 * j].set(0, lo);
+            p[2 * j + 1].set(0, hi);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k) {
+#pragma unroll
+            for (int j = 0; j < VEC / 2; ++j) set_pair(p[k], j, v[k * (VEC / 2) + j]);
+        }
+    }
+}
+
 // The largest of some packs' elements (NaN aside).
 template <int VEC, int N>
 __device__ __forceinline__ float pack_max(const Pack<float, VEC> (&q)[N]) {

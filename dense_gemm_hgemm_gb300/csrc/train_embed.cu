@@ -34,6 +34,22 @@ struct LookupParams {
     int32_t* error;
 };
 
+// A pack times a number, or zeros.
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> scaled(const Pack<T, VEC>& q, float scale, bool take) {
+    Pack<T, VEC> r;
+    if (!take) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) r.set_raw(i, from_f32<T>(0.f));
+    } else if constexpr (VEC == 1) {
+        r.set(0, scale * q.get(0));
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) set_pair(r, j, mul2(Pair(scale, scale), pair_of(q, j)));
+    }
+    return r;
+}
+
 template <typename T, int VEC, int PACKS, int TOKENS>
 __global__ void __launch_bounds__(kThreads)
 embed_forward_kernel(const LookupParams p, const T* __restrict__ table, T* __restrict__ out) {
@@ -71,9 +87,7 @@ embed_forward_kernel(const LookupParams p, const T* __restrict__ table, T* __res
             for (int k = 0; k < PACKS; ++k) {
                 const int c = c0 + k * p.lanes * VEC;
                 if (c >= p.dim) break;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) q[u][k].set(i, id[u] >= 0 ? p.scale * q[u][k].get(i) : 0.f);
-                store_pack<T, VEC>(out + (first + u) * p.ldo + c, p.dim - c, q[u][k]);
+                store_pack<T, VEC>(out + (first + u) * p.ldo + c, p.dim - c, scaled(q[u][k], p.scale, id[u] >= 0));
             }
         }
     }

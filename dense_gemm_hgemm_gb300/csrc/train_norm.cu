@@ -25,8 +25,9 @@ constexpr int kLaneCols = 16;      // columns a lane keeps in registers
 // row before it works on the present one.  So a row is read once, and its statistics
 // are exact two-pass ones at no further traffic.
 
-template <typename T, int VEC, int PACKS>
+template <typename T, int VEC>
 struct RowPacks {
+    static constexpr int PACKS = kLaneCols / VEC;
     Pack<T, VEC> p[PACKS];
     __device__ __forceinline__ void load(const T* row, int lane, int lanes, int cols) {
 #pragma unroll
@@ -35,7 +36,44 @@ struct RowPacks {
             p[k] = load_pack<T, VEC>(row + c, cols - c);
         }
     }
+    __device__ __forceinline__ void store(T* row, int lane, int lanes, int cols) const {
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k) {
+            const int c = (k * lanes + lane) * VEC;
+            store_pack<T, VEC>(row + c, cols - c, p[k]);
+        }
+    }
 };
+
+constexpr int kPairs = kLaneCols / 2;
+
+// A lane's columns of a weight vector (`other` without one, and past the row's end).
+template <typename W, int VEC>
+__device__ __forceinline__ void load_weights(const W* w, float other, int lane, int lanes, int cols, Pair (&v)[kPairs]) {
+    constexpr int PACKS = kLaneCols / VEC;
+    float f[kLaneCols];
+#pragma unroll
+    for (int k = 0; k < PACKS; ++k) {
+        const int c = (k * lanes + lane) * VEC;
+        float part[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) part[i] = other;
+        if (w) load_values<W, VEC>(w + c, cols - c, part);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) f[k * VEC + i] = part[i];
+    }
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) v[j] = Pair(f[2 * j], f[2 * j + 1]);
+}
+
+__device__ __forceinline__ float sum_of(const Pair (&v)[kPairs]) {
+    Pair s = add2(v[0], v[1]);
+#pragma unroll
+    for (int j = 2; j < kPairs; ++j) s = add2(s, v[j]);
+    float lo, hi;
+    s.get(lo, hi);
+    return lo + hi;
+}
 
 // Sums over a group, in every lane: shuffles in the warp, then one exchange in shared
 // memory behind the group's own barrier.  Two exchange buffers in turn: a warp that is
@@ -77,7 +115,6 @@ struct ForwardArgs {
 // row, where the block's registers would not suffice).
 template <typename T, typename W, int VEC, int BLOCK, bool KEEP>
 __global__ void __launch_bounds__(BLOCK) norm_forward_kernel(const ForwardArgs<T, W> a) {
-    constexpr int PACKS = kLaneCols / VEC;
     __shared__ float part[BLOCK / 32][2][1][32];
     wait_for_previous_kernel();
     let_next_kernel_start();
@@ -85,60 +122,54 @@ __global__ void __launch_bounds__(BLOCK) norm_forward_kernel(const ForwardArgs<T
     const int64_t step = static_cast<int64_t>(gridDim.x) * (BLOCK / lanes);
     int64_t row = static_cast<int64_t>(blockIdx.x) * (BLOCK / lanes) + group;
     if (row >= a.rows) return;
+    const bool full = a.cols == lanes * kLaneCols;
     GroupSum<1> sum{part[group], lanes, 1 + group, 0};
-    RowPacks<T, VEC, PACKS> next;
+    RowPacks<T, VEC> next;
     next.load(a.x + row * a.ldx, lane, lanes, a.cols);
-    float gamma[PACKS][VEC], beta[PACKS][VEC];
-    const auto load_weights = [&] {
-#pragma unroll
-        for (int k = 0; k < PACKS; ++k) {
-            const int c = (k * lanes + lane) * VEC;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                gamma[k][i] = 1.f;
-                beta[k][i] = 0.f;
-            }
-            if (a.gamma) load_values<W, VEC>(a.gamma + c, a.cols - c, gamma[k]);
-            if (a.beta) load_values<W, VEC>(a.beta + c, a.cols - c, beta[k]);
-        }
-    };
-    if (KEEP) load_weights();
+    Pair gamma[kPairs], beta[kPairs];
+    if (KEEP) {
+        load_weights<W, VEC>(a.gamma, 1.f, lane, lanes, a.cols, gamma);
+        load_weights<W, VEC>(a.beta, 0.f, lane, lanes, a.cols, beta);
+    }
     const float n = static_cast<float>(a.cols);
     for (; row < a.rows; row += step) {
-        float v[PACKS][VEC];
-        float s[1] = {0.f};
-#pragma unroll
-        for (int k = 0; k < PACKS; ++k) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                v[k][i] = next.p[k].get(i);      // (columns past the row's end are zeros)
-                s[0] += v[k][i];
-            }
-        }
+        Pair v[kPairs];
+        to_pairs(next.p, v);                     // (columns past the row's end are zeros)
         if (row + step < a.rows) next.load(a.x + (row + step) * a.ldx, lane, lanes, a.cols);
+        float s[1] = {sum_of(v)};
         sum(s, lane);
         const float mu = s[0] / n;
-        s[0] = 0.f;
+        const Pair minus(-mu, -mu);
+        Pair square(0.f, 0.f);
 #pragma unroll
-        for (int k = 0; k < PACKS; ++k) {
-            const int left = a.cols - (k * lanes + lane) * VEC;
+        for (int j = 0; j < kPairs; ++j) v[j] = add2(v[j], minus);
+        if (!full) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                v[k][i] -= mu;
-                if (i < left) s[0] += v[k][i] * v[k][i];
+            for (int j = 0; j < kPairs; ++j) {
+                const int k = 2 * j / VEC, c = (k * lanes + lane) * VEC + 2 * j % VEC;
+                const int c1 = VEC == 1 ? c + lanes : c + 1;
+                float lo, hi;
+                v[j].get(lo, hi);
+                v[j] = Pair(c < a.cols ? lo : 0.f, c1 < a.cols ? hi : 0.f);
             }
         }
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) square = fma2(v[j], v[j], square);
+        float lo, hi;
+        square.get(lo, hi);
+        s[0] = lo + hi;
         sum(s, lane);
         const float r = 1.f / sqrtf(s[0] / n + a.eps);
-        if (!KEEP) load_weights();
-#pragma unroll
-        for (int k = 0; k < PACKS; ++k) {
-            const int c = (k * lanes + lane) * VEC;
-            Pack<T, VEC> out;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) out.set(i, v[k][i] * r * gamma[k][i] + beta[k][i]);
-            store_pack<T, VEC>(a.y + row * a.ldy + c, a.cols - c, out);
+        if (!KEEP) {
+            load_weights<W, VEC>(a.gamma, 1.f, lane, lanes, a.cols, gamma);
+            load_weights<W, VEC>(a.beta, 0.f, lane, lanes, a.cols, beta);
         }
+        const Pair r2(r, r);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) v[j] = fma2(mul2(v[j], r2), gamma[j], beta[j]);
+        RowPacks<T, VEC> out;
+        from_pairs(v, out.p);
+        out.store(a.y + row * a.ldy, lane, lanes, a.cols);
         if (lane == 0) {
             if (a.mean) a.mean[row] = mu;
             if (a.rstd) a.rstd[row] = r;
@@ -165,7 +196,6 @@ struct BackwardArgs {
 // threads has no registers left for them); the groups of a block are joined at the end.
 template <typename T, typename W, int VEC, int BLOCK, bool SHARED>
 __global__ void __launch_bounds__(BLOCK) norm_backward_kernel(const BackwardArgs<T, W> a) {
-    constexpr int PACKS = kLaneCols / VEC;
     extern __shared__ float join[];      // [2][lanes * kLaneCols]
     __shared__ float part[BLOCK / 32][2][2][32];
     wait_for_previous_kernel();
@@ -175,25 +205,25 @@ __global__ void __launch_bounds__(BLOCK) norm_backward_kernel(const BackwardArgs
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group;
     GroupSum<2> sum{part[group], lanes, 1 + group, 0};
-    float dg[PACKS][VEC], db[PACKS][VEC], gamma[PACKS][VEC];
-    // sum `which` of the lane's column i of pack k
-    const auto mine = [&](int which, int k, int i) -> float& {
-        return join[(which * kLaneCols + k * VEC + i) * lanes + lane];
+    Pair dg[kPairs], db[kPairs], gamma[kPairs];
+    // sum `which` of the lane's element i of its kLaneCols
+    const auto mine = [&](int which, int i) -> float& { return join[(which * kLaneCols + i) * lanes + lane]; };
+    const auto add_to = [&](int which, int j, Pair v, bool fresh) {
+        float lo, hi;
+        v.get(lo, hi);
+        mine(which, 2 * j) = fresh ? lo : mine(which, 2 * j) + lo;
+        mine(which, 2 * j + 1) = fresh ? hi : mine(which, 2 * j + 1) + hi;
     };
 #pragma unroll
-    for (int k = 0; k < PACKS; ++k) {
-        const int c = (k * lanes + lane) * VEC;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            gamma[k][i] = 1.f;
-            if (SHARED)
-                mine(0, k, i) = mine(1, k, i) = 0.f;
-            else
-                dg[k][i] = db[k][i] = 0.f;
+    for (int j = 0; j < kPairs; ++j) {
+        dg[j] = db[j] = Pair(0.f, 0.f);
+        if (SHARED) {
+            add_to(0, j, dg[j], true);
+            add_to(1, j, db[j], true);
         }
-        if (!SHARED && a.gamma) load_values<W, VEC>(a.gamma + c, a.cols - c, gamma[k]);
     }
-    RowPacks<T, VEC, PACKS> next_x, next_dy;
+    if (!SHARED) load_weights<W, VEC>(a.gamma, 1.f, lane, lanes, a.cols, gamma);
+    RowPacks<T, VEC> next_x, next_dy;
     float next_mean = 0.f, next_rstd = 0.f;
     const auto ask = [&](int64_t r) {
         next_x.load(a.x + r * a.ldx, lane, lanes, a.cols);
@@ -204,60 +234,51 @@ __global__ void __launch_bounds__(BLOCK) norm_backward_kernel(const BackwardArgs
     if (row < a.rows) ask(row);
     const float n = static_cast<float>(a.cols);
     for (; row < a.rows; row += step) {
-        const RowPacks<T, VEC, PACKS> x = next_x, dy = next_dy;
         const float mu = next_mean, r = next_rstd;
+        Pair hat[kPairs], g[kPairs];
+        to_pairs(next_x.p, hat);
+        to_pairs(next_dy.p, g);                  // dy: zero past the row's end, as every sum's term there
         if (row + step < a.rows) ask(row + step);
-        if (SHARED && a.gamma) {
+        if (SHARED) load_weights<W, VEC>(a.gamma, 1.f, lane, lanes, a.cols, gamma);
+        const Pair minus(-mu, -mu), r2(r, r);
+        Pair sum_g(0.f, 0.f), sum_gx(0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < PACKS; ++k) {
-                const int c = (k * lanes + lane) * VEC;
-                load_values<W, VEC>(a.gamma + c, a.cols - c, gamma[k]);
+        for (int j = 0; j < kPairs; ++j) {
+            hat[j] = mul2(add2(hat[j], minus), r2);
+            if (SHARED) {
+                add_to(0, j, mul2(g[j], hat[j]), false);
+                add_to(1, j, g[j], false);
+            } else {
+                dg[j] = fma2(g[j], hat[j], dg[j]);
+                db[j] = add2(db[j], g[j]);
             }
-        }
-        float s[2] = {0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < PACKS; ++k) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                // past the row's end dy, and so every sum's term, is zero
-                const float hat = (x.p[k].get(i) - mu) * r, d = dy.p[k].get(i), g = d * gamma[k][i];
-                s[0] += g;
-                s[1] += g * hat;
-                if (SHARED) {
-                    mine(0, k, i) += d * hat;
-                    mine(1, k, i) += d;
-                } else {
-                    dg[k][i] += d * hat;
-                    db[k][i] += d;
-                }
-            }
+            g[j] = mul2(g[j], gamma[j]);
+            sum_g = add2(sum_g, g[j]);
+            sum_gx = fma2(g[j], hat[j], sum_gx);
         }
         if (!a.dx) continue;
+        float lo, hi, s[2];
+        sum_g.get(lo, hi);
+        s[0] = lo + hi;
+        sum_gx.get(lo, hi);
+        s[1] = lo + hi;
         sum(s, lane);
         const float mean_g = s[0] / n, mean_gx = s[1] / n;
+        const Pair minus_g(-mean_g, -mean_g), minus_gx(-mean_gx, -mean_gx);
 #pragma unroll
-        for (int k = 0; k < PACKS; ++k) {
-            const int c = (k * lanes + lane) * VEC;
-            Pack<T, VEC> out;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float hat = (x.p[k].get(i) - mu) * r, g = dy.p[k].get(i) * gamma[k][i];
-                out.set(i, r * (g - mean_g - hat * mean_gx));
-            }
-            store_pack<T, VEC>(a.dx + row * a.lddx + c, a.cols - c, out);
-        }
+        for (int j = 0; j < kPairs; ++j) g[j] = mul2(r2, fma2(hat[j], minus_gx, add2(g[j], minus_g)));
+        RowPacks<T, VEC> out;
+        from_pairs(g, out.p);
+        out.store(a.dx + row * a.lddx, lane, lanes, a.cols);
     }
     if (!a.weights) return;
     if (!SHARED) {
-        for (int g = 0; g < groups; ++g) {       // the groups in turn
-            if (group == g) {
+        for (int turn = 0; turn < groups; ++turn) {      // the groups in turn
+            if (group == turn) {
 #pragma unroll
-                for (int k = 0; k < PACKS; ++k) {
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        mine(0, k, i) = g == 0 ? dg[k][i] : mine(0, k, i) + dg[k][i];
-                        mine(1, k, i) = g == 0 ? db[k][i] : mine(1, k, i) + db[k][i];
-                    }
+                for (int j = 0; j < kPairs; ++j) {
+                    add_to(0, j, dg[j], turn == 0);
+                    add_to(1, j, db[j], turn == 0);
                 }
             }
             __syncthreads();
