@@ -57,6 +57,7 @@ struct Pack {
         reinterpret_cast<T*>(&raw)[i] = from_f32<T>(v);
     }
     __device__ __forceinline__ void set_raw(int i, T v) { reinterpret_cast<T*>(&raw)[i] = v; }
+    __device__ __forceinline__ void clear() { raw = {}; }
 };
 
 // ---- pairs of fp32 values, which one instruction works on -------------------------
@@ -279,6 +280,86 @@ __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// ---- asynchronous copies into a ring of buffers ------------------------------------
+
+constexpr long long kWaitNs = 2000000000ll;     // the longest wait in a kernel
+constexpr int32_t kErrorIndex = 1;              // bits of a plan's error word
+constexpr int32_t kErrorTimeout = 2;
+
+__device__ __forceinline__ uint32_t shared_address(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// Waits for a phase of the barrier, at most kWaitNs.
+__device__ inline bool wait_phase(uint64_t* barrier, uint32_t parity) {
+    const uint32_t at = shared_address(barrier);
+    long long began = 0;
+    for (uint32_t tries = 0;; ++tries) {
+        uint32_t done;
+        asm volatile(
+            "{\n.reg .pred p;\n"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+            "selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(done) : "r"(at), "r"(parity) : "memory");
+        if (done) return true;
+        long long now;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        if (tries == 0) began = now;
+        if (now - began > kWaitNs) return false;
+    }
+}
+
+// A place in a ring of buffers, and how often it has been passed.
+struct Turn {
+    int at;
+    uint32_t round;
+    __device__ __forceinline__ void next(int by, int size) {
+        for (at += by; at >= size; at -= size) ++round;
+    }
+};
+
+// As wait_phase; when it runs out (or another wait has) it returns at once from then on.
+__device__ __forceinline__ void wait_or_die(uint64_t* barrier, uint32_t parity, int* dead, int32_t* error) {
+    const uint32_t at = shared_address(barrier);
+    long long began = 0;
+    for (uint32_t tries = 0;; ++tries) {
+        uint32_t done;
+        asm volatile(
+            "{\n.reg .pred p;\n"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            "selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(done) : "r"(at), "r"(parity) : "memory");
+        if (done || *static_cast<volatile int*>(dead)) return;
+        long long now;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        if (tries == 0) began = now;
+        if (now - began > kWaitNs) {
+            *static_cast<volatile int*>(dead) = 1;
+            atomicOr(error, kErrorTimeout);
+            return;
+        }
+    }
+}
+
+__device__ __forceinline__ void init_barrier(uint64_t* barrier, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(shared_address(barrier)), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void arrive(uint64_t* barrier) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(shared_address(barrier)) : "memory");
+}
+
+// The barrier's phase ends when these bytes have come (and this was the last arrival);
+// bytes (a multiple of 16) from global to shared memory, both 16-byte aligned.
+__device__ __forceinline__ void expect_bytes(uint64_t* barrier, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
+                 :: "r"(shared_address(barrier)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_bytes(void* to, const void* from, uint32_t bytes, uint64_t* barrier) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(shared_address(to)), "l"(from), "r"(bytes), "r"(shared_address(barrier)) : "memory");
+}
+
 // ---- host ---------------------------------------------------------------------
 
 inline bool valid_elem(gemm_elem_t e) { return e >= GEMM_ELEM_F16 && e <= GEMM_ELEM_F32; }
@@ -319,10 +400,6 @@ inline gemm_status_t allocate(void** p, size_t bytes) {
     *p = nullptr;
     return GEMM_ERR_OOM;
 }
-
-// Bits of an error word.
-constexpr int32_t kErrorIndex = 1;
-constexpr int32_t kErrorTimeout = 2;
 
 // Synchronise, then read and clear an error word.
 inline gemm_status_t check_error_word(int32_t* word, void* stream_ptr) {

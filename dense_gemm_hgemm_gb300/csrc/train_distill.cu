@@ -33,7 +33,6 @@ constexpr int kMaxCluster = 8;                 // blocks that share a row
 constexpr int kPieceBytes = 32 * 1024;         // of a row that a block aims to hold
 constexpr int kMostPieceBytes = 200 * 1024;    // ... and can hold
 constexpr int kMostShared = 224 * 1024;        // dynamic shared memory of any launch
-constexpr long long kWaitNs = 2000000000ll;     // the longest wait in a kernel
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -64,29 +63,6 @@ struct Args {
 
 // ---- asynchronous copies ----------------------------------------------------------
 
-__device__ __forceinline__ uint32_t shared_address(const void* p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-// Waits for a phase of the barrier, at most about two seconds.
-__device__ bool wait_phase(uint64_t* barrier, uint32_t parity) {
-    const uint32_t at = shared_address(barrier);
-    long long began = 0;
-    for (uint32_t tries = 0;; ++tries) {
-        uint32_t done;
-        asm volatile(
-            "{\n.reg .pred p;\n"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-            "selp.u32 %0, 1, 0, p;\n}"
-            : "=r"(done) : "r"(at), "r"(parity) : "memory");
-        if (done) return true;
-        long long now;
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-        if (tries == 0) began = now;
-        if (now - began > kWaitNs) return false;
-    }
-}
-
 // The elements of [src, src + n) into shared memory at dst, which has src's offset
 // from a 16-byte boundary: one thread starts a bulk copy of the whole 16-byte units
 // (counted on the barrier), all threads copy the ragged ends.  Past the ends, up to
@@ -100,13 +76,8 @@ __device__ __forceinline__ void start_copy(T* dst, const T* src, int n, uint64_t
     const int body = (n - head) / VEC * VEC, tail = n - head - body;
     if (threadIdx.x == 0) {
         const uint32_t bytes = static_cast<uint32_t>(body * static_cast<int>(sizeof(T)));
-        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
-                     :: "r"(shared_address(barrier)), "r"(bytes) : "memory");
-        if (bytes > 0)
-            asm volatile(
-                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                :: "r"(shared_address(dst + head)), "l"(src + head), "r"(bytes),
-                   "r"(shared_address(barrier)) : "memory");
+        expect_bytes(barrier, bytes);
+        if (bytes > 0) copy_bytes(dst + head, src + head, bytes, barrier);
     }
     if (threadIdx.x < VEC) {
         const int i = threadIdx.x;
@@ -510,50 +481,6 @@ struct StreamBarriers {
     int dead;                // a wait ran out: nothing waits any more
 };
 
-// A place in a ring of buffers, and how often it has been passed.
-struct Turn {
-    int at;
-    uint32_t round;
-    __device__ __forceinline__ void next(int by, int size) {
-        at += by;
-        if (at >= size) {
-            at -= size;
-            ++round;
-        }
-    }
-};
-
-// As wait_phase; when it runs out (or another wait has) it returns at once from then on.
-__device__ __forceinline__ void wait_or_die(uint64_t* barrier, uint32_t parity, int* dead, int32_t* error) {
-    const uint32_t at = shared_address(barrier);
-    long long began = 0;
-    for (uint32_t tries = 0;; ++tries) {
-        uint32_t done;
-        asm volatile(
-            "{\n.reg .pred p;\n"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-            "selp.u32 %0, 1, 0, p;\n}"
-            : "=r"(done) : "r"(at), "r"(parity) : "memory");
-        if (done || *static_cast<volatile int*>(dead)) return;
-        long long now;
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-        if (tries == 0) began = now;
-        if (now - began > kWaitNs) {
-            *static_cast<volatile int*>(dead) = 1;
-            atomicOr(error, kErrorTimeout);
-            return;
-        }
-    }
-}
-
-__device__ __forceinline__ void init_barrier(uint64_t* barrier, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(shared_address(barrier)), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void arrive(uint64_t* barrier) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(shared_address(barrier)) : "memory");
-}
-
 __device__ __forceinline__ void compute_barrier() {
     asm volatile("bar.sync 1, %0;" :: "n"(kComputeThreads) : "memory");
 }
@@ -634,13 +561,8 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
                 __syncwarp();
                 if (lane == 0 && !*static_cast<volatile int*>(&sh.dead)) {
                     const uint32_t bytes = hi > lo ? static_cast<uint32_t>((hi - lo) * static_cast<int>(sizeof(T))) : 0;
-                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
-                                 :: "r"(shared_address(&sh.full[stage.at])), "r"(bytes) : "memory");
-                    if (bytes > 0)
-                        asm volatile(
-                            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-                            :: "r"(shared_address(to + (lo - at))), "l"(base + lo), "r"(bytes),
-                               "r"(shared_address(&sh.full[stage.at])) : "memory");
+                    expect_bytes(&sh.full[stage.at], bytes);
+                    if (bytes > 0) copy_bytes(to + (lo - at), base + lo, bytes, &sh.full[stage.at]);
                 }
                 stage.next(1, stages);
             }
@@ -745,8 +667,7 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
                 if (a.pieces > 1) {
                     if (worker == 0) {
                         if (lane == 0)
-                            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
-                                         :: "r"(shared_address(&sh.exchanged[turn])), "r"(a.pieces * 16) : "memory");
+                            expect_bytes(&sh.exchanged[turn], static_cast<uint32_t>(a.pieces) * 16);
                         if (lane < a.pieces) {           // this block's numbers, to each block of the row
                             uint32_t slot_at, barrier_at;
                             asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"

@@ -7,6 +7,8 @@ struct gemm_norm_plan {
     int64_t max_rows, cols;
     gemm_elem_t elem, weight_elem;
     int device, num_sms;
+    void* memory;        // one allocation: the error word and `partial`
+    int32_t* error_word;
     float* partial;      // [2][blocks][cols] sums of the weight gradients
 };
 
@@ -16,6 +18,7 @@ namespace {
 constexpr int kThreads = 256;      // of the kernels that loop over a row or a column
 constexpr int kMaxLanes = 1024;
 constexpr int kLaneCols = 16;      // columns a lane keeps in registers
+constexpr int kPairs = kLaneCols / 2;
 
 // ---- rows in registers ----------------------------------------------------------
 //
@@ -25,35 +28,37 @@ constexpr int kLaneCols = 16;      // columns a lane keeps in registers
 // row before it works on the present one.  So a row is read once, and its statistics
 // are exact two-pass ones at no further traffic.
 
-template <typename T, int VEC>
+// WHOLE: the row's length is a multiple of VEC, so a pack is in it or not.
+template <typename T, int VEC, int COLS, bool WHOLE>
 struct RowPacks {
-    static constexpr int PACKS = kLaneCols / VEC;
+    static constexpr int PACKS = COLS / VEC;
     Pack<T, VEC> p[PACKS];
     __device__ __forceinline__ void load(const T* row, int lane, int lanes, int cols) {
 #pragma unroll
         for (int k = 0; k < PACKS; ++k) {
             const int c = (k * lanes + lane) * VEC;
-            p[k] = load_pack<T, VEC>(row + c, cols - c);
+            if (WHOLE && c >= cols) {
+                p[k].clear();
+            } else {
+                p[k] = load_pack<T, VEC>(row + c, WHOLE ? VEC : cols - c);
+            }
         }
     }
     __device__ __forceinline__ void store(T* row, int lane, int lanes, int cols) const {
 #pragma unroll
         for (int k = 0; k < PACKS; ++k) {
             const int c = (k * lanes + lane) * VEC;
-            store_pack<T, VEC>(row + c, cols - c, p[k]);
+            if (!WHOLE || c < cols) store_pack<T, VEC>(row + c, WHOLE ? VEC : cols - c, p[k]);
         }
     }
 };
 
-constexpr int kPairs = kLaneCols / 2;
-
 // A lane's columns of a weight vector (`other` without one, and past the row's end).
-template <typename W, int VEC>
-__device__ __forceinline__ void load_weights(const W* w, float other, int lane, int lanes, int cols, Pair (&v)[kPairs]) {
-    constexpr int PACKS = kLaneCols / VEC;
-    float f[kLaneCols];
+template <typename W, int VEC, int COLS>
+__device__ __forceinline__ void load_weights(const W* w, float other, int lane, int lanes, int cols, Pair (&v)[COLS / 2]) {
+    float f[COLS];
 #pragma unroll
-    for (int k = 0; k < PACKS; ++k) {
+    for (int k = 0; k < COLS / VEC; ++k) {
         const int c = (k * lanes + lane) * VEC;
         float part[VEC];
 #pragma unroll
@@ -63,13 +68,14 @@ __device__ __forceinline__ void load_weights(const W* w, float other, int lane, 
         for (int i = 0; i < VEC; ++i) f[k * VEC + i] = part[i];
     }
 #pragma unroll
-    for (int j = 0; j < kPairs; ++j) v[j] = Pair(f[2 * j], f[2 * j + 1]);
+    for (int j = 0; j < COLS / 2; ++j) v[j] = Pair(f[2 * j], f[2 * j + 1]);
 }
 
-__device__ __forceinline__ float sum_of(const Pair (&v)[kPairs]) {
+template <int N>
+__device__ __forceinline__ float sum_of(const Pair (&v)[N]) {
     Pair s = add2(v[0], v[1]);
 #pragma unroll
-    for (int j = 2; j < kPairs; ++j) s = add2(s, v[j]);
+    for (int j = 2; j < N; ++j) s = add2(s, v[j]);
     float lo, hi;
     s.get(lo, hi);
     return lo + hi;
@@ -98,6 +104,63 @@ struct GroupSum {
     }
 };
 
+// Forward, once a row is in the lanes' pairs: subtracts its mean (columns past the row's
+// end stay zero) and returns it;
+template <int VEC, int N>
+__device__ __forceinline__ float centre(Pair (&v)[N], GroupSum<1>& sum, float inverse_n, bool full, int lane, int lanes,
+                                        int cols) {
+    float s[1] = {sum_of(v)};
+    sum(s, lane);
+    const float mu = s[0] * inverse_n;
+    const Pair minus(-mu, -mu);
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = add2(v[j], minus);
+    if (!full) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int c = (2 * j / VEC * lanes + lane) * VEC + 2 * j % VEC;
+            const int c1 = VEC == 1 ? c + lanes : c + 1;
+            float lo, hi;
+            v[j].get(lo, hi);
+            v[j] = Pair(c < cols ? lo : 0.f, c1 < cols ? hi : 0.f);
+        }
+    }
+    return mu;
+}
+
+// then 1 / sqrt(variance + eps);
+template <int N>
+__device__ __forceinline__ float rstd_of(const Pair (&v)[N], GroupSum<1>& sum, float inverse_n, float eps, int lane) {
+    Pair square = mul2(v[0], v[0]);
+#pragma unroll
+    for (int j = 1; j < N; ++j) square = fma2(v[j], v[j], square);
+    float lo, hi, s[1];
+    square.get(lo, hi);
+    s[0] = lo + hi;
+    sum(s, lane);
+    return rsqrtf(s[0] * inverse_n + eps);
+}
+
+// and the result, with the weights read on the way, a pack at a time (VEC > 1, whole packs).
+template <typename T, typename W, int VEC, int N>
+__device__ __forceinline__ void normalise(const Pair (&v)[N], float r, const W* gamma, const W* beta, T* y, int lane,
+                                          int lanes, int cols) {
+    const Pair r2(r, r);
+#pragma unroll
+    for (int k = 0; k < 2 * N / VEC; ++k) {
+        const int c = (k * lanes + lane) * VEC;
+        if (c >= cols) break;
+        float g[VEC], b[VEC];
+        load_values<W, VEC>(gamma + c, VEC, g);
+        load_values<W, VEC>(beta + c, VEC, b);
+        Pack<T, VEC> out;
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i)
+            set_pair(out, i, fma2(mul2(v[k * (VEC / 2) + i], r2), Pair(g[2 * i], g[2 * i + 1]), Pair(b[2 * i], b[2 * i + 1])));
+        store_pack<T, VEC>(y + c, VEC, out);
+    }
+}
+
 template <typename T, typename W>
 struct ForwardArgs {
     const T* x;
@@ -106,6 +169,7 @@ struct ForwardArgs {
     T* y;
     float* mean;
     float* rstd;
+    int32_t* error;
     int64_t ldx, ldy, rows;
     float eps;
     int cols, lanes;
@@ -124,50 +188,28 @@ __global__ void __launch_bounds__(BLOCK) norm_forward_kernel(const ForwardArgs<T
     if (row >= a.rows) return;
     const bool full = a.cols == lanes * kLaneCols;
     GroupSum<1> sum{part[group], lanes, 1 + group, 0};
-    RowPacks<T, VEC> next;
+    RowPacks<T, VEC, kLaneCols, false> next;
     next.load(a.x + row * a.ldx, lane, lanes, a.cols);
     Pair gamma[kPairs], beta[kPairs];
     if (KEEP) {
-        load_weights<W, VEC>(a.gamma, 1.f, lane, lanes, a.cols, gamma);
-        load_weights<W, VEC>(a.beta, 0.f, lane, lanes, a.cols, beta);
+        load_weights<W, VEC, kLaneCols>(a.gamma, 1.f, lane, lanes, a.cols, gamma);
+        load_weights<W, VEC, kLaneCols>(a.beta, 0.f, lane, lanes, a.cols, beta);
     }
-    const float n = static_cast<float>(a.cols);
+    const float inverse_n = 1.f / static_cast<float>(a.cols);
     for (; row < a.rows; row += step) {
         Pair v[kPairs];
         to_pairs(next.p, v);                     // (columns past the row's end are zeros)
         if (row + step < a.rows) next.load(a.x + (row + step) * a.ldx, lane, lanes, a.cols);
-        float s[1] = {sum_of(v)};
-        sum(s, lane);
-        const float mu = s[0] / n;
-        const Pair minus(-mu, -mu);
-        Pair square(0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < kPairs; ++j) v[j] = add2(v[j], minus);
-        if (!full) {
-#pragma unroll
-            for (int j = 0; j < kPairs; ++j) {
-                const int k = 2 * j / VEC, c = (k * lanes + lane) * VEC + 2 * j % VEC;
-                const int c1 = VEC == 1 ? c + lanes : c + 1;
-                float lo, hi;
-                v[j].get(lo, hi);
-                v[j] = Pair(c < a.cols ? lo : 0.f, c1 < a.cols ? hi : 0.f);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < kPairs; ++j) square = fma2(v[j], v[j], square);
-        float lo, hi;
-        square.get(lo, hi);
-        s[0] = lo + hi;
-        sum(s, lane);
-        const float r = 1.f / sqrtf(s[0] / n + a.eps);
+        const float mu = centre<VEC>(v, sum, inverse_n, full, lane, lanes, a.cols);
+        const float r = rstd_of(v, sum, inverse_n, a.eps, lane);
         if (!KEEP) {
-            load_weights<W, VEC>(a.gamma, 1.f, lane, lanes, a.cols, gamma);
-            load_weights<W, VEC>(a.beta, 0.f, lane, lanes, a.cols, beta);
+            load_weights<W, VEC, kLaneCols>(a.gamma, 1.f, lane, lanes, a.cols, gamma);
+            load_weights<W, VEC, kLaneCols>(a.beta, 0.f, lane, lanes, a.cols, beta);
         }
         const Pair r2(r, r);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) v[j] = fma2(mul2(v[j], r2), gamma[j], beta[j]);
-        RowPacks<T, VEC> out;
+        RowPacks<T, VEC, kLaneCols, false> out;
         from_pairs(v, out.p);
         out.store(a.y + row * a.ldy, lane, lanes, a.cols);
         if (lane == 0) {
@@ -175,6 +217,133 @@ __global__ void __launch_bounds__(BLOCK) norm_forward_kernel(const ForwardArgs<T
             if (a.rstd) a.rstd[row] = r;
         }
     }
+}
+
+// ---- rows through rings ------------------------------------------------------------
+//
+// Many rows: one block an SM, in which each group has a ring of stages in shared memory
+// and brings its next rows there by bulk copies.  The barrier of the group's first sum
+// tells that all lanes have read a stage, so its first lane asks for the next row right
+// behind it; there is no copying warp and no second barrier.  The bytes in flight do not
+// depend on how many registers are left for loads: the register kernels keep 24 KB an SM
+// in flight at 16384 x 4096, the rings over 100 KB.
+
+constexpr int kRingSlots = 64;             // stages of a block, at most
+constexpr int kRingShared = 208 * 1024;    // its dynamic shared memory, at most
+constexpr int kForwardRing = 1024;         // threads of the blocks
+constexpr int kBackwardRing = 512;
+
+// A group's ring; each stage holds a row from each of N sources.
+template <int N>
+struct Ring {
+    uint8_t* memory;
+    uint64_t* full;
+    int* dead;
+    int32_t* error;
+    const uint8_t* src[N];
+    int64_t stride[N], rows, step;         // bytes; the matrix' rows, from one of the group's to its next
+    int row_bytes, stages;
+    Turn turn;
+    int64_t asked;                         // rows asked for, by the lane that asks
+
+    __device__ __forceinline__ void ask(int stage, int64_t row) {
+        if (row >= rows || *static_cast<volatile int*>(dead)) return;
+        expect_bytes(&full[stage], static_cast<uint32_t>(N * row_bytes));
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            copy_bytes(memory + (stage * N + k) * row_bytes, src[k] + row * stride[k], static_cast<uint32_t>(row_bytes),
+                       &full[stage]);
+        ++asked;
+    }
+    // (one lane)
+    __device__ __forceinline__ void begin(int64_t row) {
+        for (int k = 0; k < stages; ++k) ask(k, row + k * step);
+    }
+    // The present stage, once its row has come.
+    __device__ __forceinline__ const uint8_t* wait() const {
+        wait_or_die(&full[turn.at], turn.round & 1, dead, error);
+        return memory + turn.at * N * row_bytes;
+    }
+    // All lanes have read the present stage.
+    __device__ __forceinline__ void release(int lane, int64_t row) {
+        if (lane == 0) ask(turn.at, row + stages * step);
+    }
+    // After a wait that ran out (one lane): what was asked for may still come.
+    __device__ __forceinline__ void end() const {
+        if (!*static_cast<volatile int*>(dead)) return;
+        for (int64_t k = asked > stages ? asked - stages : 0; k < asked; ++k)
+            wait_phase(&full[k % stages], (k / stages) & 1);
+    }
+};
+
+struct RingBarriers {
+    uint64_t full[kRingSlots];
+    int dead;
+};
+
+// (one thread)
+__device__ __forceinline__ void init_ring(RingBarriers& ring, int slots) {
+    for (int k = 0; k < slots; ++k) init_barrier(&ring.full[k], 1);
+    ring.dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+
+// gamma and beta wait in shared memory behind the rings.  COLS columns a lane: with 32 a row
+// takes half the warps of 16, and so half the work that does not depend on its length.
+template <typename T, typename W, int VEC, int COLS>
+__global__ void __launch_bounds__(kForwardRing, 1) norm_forward_ring_kernel(const ForwardArgs<T, W> a, int stages) {
+    extern __shared__ __align__(128) uint8_t memory[];
+    __shared__ RingBarriers barriers;
+    __shared__ float part[kForwardRing / 32][2][1][32];
+    const int lanes = a.lanes, groups = kForwardRing / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+    const int row_bytes = a.cols * static_cast<int>(sizeof(T));
+    W* const gamma = reinterpret_cast<W*>(memory + groups * stages * row_bytes);
+    W* const beta = gamma + lanes * COLS;
+    if (threadIdx.x == 0) init_ring(barriers, groups * stages);
+    __syncthreads();
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    int64_t row = blockIdx.x + static_cast<int64_t>(group) * gridDim.x;
+    Ring<1> ring{memory + group * stages * row_bytes,
+                 barriers.full + group * stages,
+                 &barriers.dead,
+                 a.error,
+                 {reinterpret_cast<const uint8_t*>(a.x)},
+                 {a.ldx * static_cast<int64_t>(sizeof(T))},
+                 a.rows,
+                 static_cast<int64_t>(groups) * gridDim.x,
+                 row_bytes,
+                 stages,
+                 {0, 0},
+                 0};
+    if (lane == 0) ring.begin(row);
+    for (int c = threadIdx.x; c < a.cols; c += kForwardRing) {
+        gamma[c] = a.gamma ? a.gamma[c] : from_f32<W>(1.f);
+        beta[c] = a.beta ? a.beta[c] : from_f32<W>(0.f);
+    }
+    __syncthreads();
+    const bool full = a.cols == lanes * COLS;
+    const float inverse_n = 1.f / static_cast<float>(a.cols);
+    GroupSum<1> sum{part[group], lanes, group, 0};       // (barrier 0 is free from here on)
+    T* y = a.y + row * a.ldy;
+    const int64_t y_step = ring.step * a.ldy;
+    for (; row < a.rows; row += ring.step, y += y_step, ring.turn.next(1, stages)) {
+        Pair v[COLS / 2];
+        {
+            RowPacks<T, VEC, COLS, true> in;
+            in.load(reinterpret_cast<const T*>(ring.wait()), lane, lanes, a.cols);
+            to_pairs(in.p, v);
+        }
+        const float mu = centre<VEC>(v, sum, inverse_n, full, lane, lanes, a.cols);
+        ring.release(lane, row);
+        const float r = rstd_of(v, sum, inverse_n, a.eps, lane);
+        normalise<T, W, VEC>(v, r, gamma, beta, y, lane, lanes, a.cols);
+        if (lane == 0) {
+            if (a.mean) a.mean[row] = mu;
+            if (a.rstd) a.rstd[row] = r;
+        }
+    }
+    if (lane == 0) ring.end();
 }
 
 template <typename T, typename W>
@@ -186,10 +355,64 @@ struct BackwardArgs {
     const T* dy;
     T* dx;
     float* partial;      // [2][gridDim.x][cols]
+    int32_t* error;
     int64_t ldx, lddy, lddx, rows;
     int cols, lanes;
     bool weights;        // dgamma or dbeta is wanted
 };
+
+// Backward, once xh and g are in the lanes' pairs: the group's sums, then dx.
+__device__ __forceinline__ void row_sums(Pair sum_g, Pair sum_gx, GroupSum<2>& sum, int lane, float (&s)[2]) {
+    float lo, hi;
+    sum_g.get(lo, hi);
+    s[0] = lo + hi;
+    sum_gx.get(lo, hi);
+    s[1] = lo + hi;
+    sum(s, lane);
+}
+
+template <typename T, int VEC, bool WHOLE>
+__device__ __forceinline__ void write_dx(const Pair (&hat)[kPairs], Pair (&g)[kPairs], const float (&s)[2], float inverse_n,
+                                         Pair r2, T* dx, int lane, int lanes, int cols) {
+    const float mean_g = s[0] * inverse_n, mean_gx = s[1] * inverse_n;
+    const Pair minus_g(-mean_g, -mean_g), minus_gx(-mean_gx, -mean_gx);
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) g[j] = mul2(r2, fma2(hat[j], minus_gx, add2(g[j], minus_g)));
+    RowPacks<T, VEC, kLaneCols, WHOLE> out;
+    from_pairs(g, out.p);
+    out.store(dx, lane, lanes, cols);
+}
+
+// Sums kept as [2][kLaneCols][lanes] in shared memory, to the block's rows of the partial
+// sums, in the order of the columns.
+template <int VEC, int THREADS>
+__device__ __forceinline__ void copy_partial(int lanes, int cols, const float* join, float* partial) {
+    for (int which = 0; which < 2; ++which) {
+        float* out = partial + (static_cast<int64_t>(which) * gridDim.x + blockIdx.x) * cols;
+        for (int c = threadIdx.x; c < cols; c += THREADS) {
+            const int pack = c / VEC;                    // column c is element c % VEC of this pack
+            out[c] = join[(which * kLaneCols + pack / lanes * VEC + c % VEC) * lanes + pack % lanes];
+        }
+    }
+}
+
+// Joins the groups' sums of a block in shared memory, in the order of the groups, and
+// writes them to the block's place in the partial sums.  `add` is the kernels' add_to.
+template <int VEC, int THREADS, typename A>
+__device__ __forceinline__ void write_partial(const Pair (&dg)[kPairs], const Pair (&db)[kPairs], int group, int groups,
+                                              int lanes, int cols, const float* join, float* partial, A add) {
+    for (int turn = 0; turn < groups; ++turn) {
+        if (group == turn) {
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+                add(0, j, dg[j], turn == 0);
+                add(1, j, db[j], turn == 0);
+            }
+        }
+        __syncthreads();
+    }
+    copy_partial<VEC, THREADS>(lanes, cols, join, partial);
+}
 
 // dx of each row, and the block's sums of dy * xh and dy over its rows: each lane adds
 // up its own columns, in registers (SHARED: in shared memory, where a block of 1024
@@ -222,8 +445,8 @@ __global__ void __launch_bounds__(BLOCK) norm_backward_kernel(const BackwardArgs
             add_to(1, j, db[j], true);
         }
     }
-    if (!SHARED) load_weights<W, VEC>(a.gamma, 1.f, lane, lanes, a.cols, gamma);
-    RowPacks<T, VEC> next_x, next_dy;
+    if (!SHARED) load_weights<W, VEC, kLaneCols>(a.gamma, 1.f, lane, lanes, a.cols, gamma);
+    RowPacks<T, VEC, kLaneCols, false> next_x, next_dy;
     float next_mean = 0.f, next_rstd = 0.f;
     const auto ask = [&](int64_t r) {
         next_x.load(a.x + r * a.ldx, lane, lanes, a.cols);
@@ -232,14 +455,14 @@ __global__ void __launch_bounds__(BLOCK) norm_backward_kernel(const BackwardArgs
         next_rstd = a.rstd[r];
     };
     if (row < a.rows) ask(row);
-    const float n = static_cast<float>(a.cols);
+    const float inverse_n = 1.f / static_cast<float>(a.cols);
     for (; row < a.rows; row += step) {
         const float mu = next_mean, r = next_rstd;
         Pair hat[kPairs], g[kPairs];
         to_pairs(next_x.p, hat);
         to_pairs(next_dy.p, g);                  // dy: zero past the row's end, as every sum's term there
         if (row + step < a.rows) ask(row + step);
-        if (SHARED) load_weights<W, VEC>(a.gamma, 1.f, lane, lanes, a.cols, gamma);
+        if (SHARED) load_weights<W, VEC, kLaneCols>(a.gamma, 1.f, lane, lanes, a.cols, gamma);
         const Pair minus(-mu, -mu), r2(r, r);
         Pair sum_g(0.f, 0.f), sum_gx(0.f, 0.f);
 #pragma unroll
@@ -257,42 +480,100 @@ __global__ void __launch_bounds__(BLOCK) norm_backward_kernel(const BackwardArgs
             sum_gx = fma2(g[j], hat[j], sum_gx);
         }
         if (!a.dx) continue;
-        float lo, hi, s[2];
-        sum_g.get(lo, hi);
-        s[0] = lo + hi;
-        sum_gx.get(lo, hi);
-        s[1] = lo + hi;
-        sum(s, lane);
-        const float mean_g = s[0] / n, mean_gx = s[1] / n;
-        const Pair minus_g(-mean_g, -mean_g), minus_gx(-mean_gx, -mean_gx);
-#pragma unroll
-        for (int j = 0; j < kPairs; ++j) g[j] = mul2(r2, fma2(hat[j], minus_gx, add2(g[j], minus_g)));
-        RowPacks<T, VEC> out;
-        from_pairs(g, out.p);
-        out.store(a.dx + row * a.lddx, lane, lanes, a.cols);
+        float s[2];
+        row_sums(sum_g, sum_gx, sum, lane, s);
+        write_dx<T, VEC, false>(hat, g, s, inverse_n, r2, a.dx + row * a.lddx, lane, lanes, a.cols);
     }
     if (!a.weights) return;
-    if (!SHARED) {
-        for (int turn = 0; turn < groups; ++turn) {      // the groups in turn
-            if (group == turn) {
-#pragma unroll
-                for (int j = 0; j < kPairs; ++j) {
-                    add_to(0, j, dg[j], turn == 0);
-                    add_to(1, j, db[j], turn == 0);
-                }
-            }
-            __syncthreads();
-        }
-    } else {
+    if (SHARED) {
         __syncthreads();
+        copy_partial<VEC, BLOCK>(lanes, a.cols, join, a.partial);
+    } else {
+        write_partial<VEC, BLOCK>(dg, db, group, groups, lanes, a.cols, join, a.partial, add_to);
     }
-    for (int which = 0; which < 2; ++which) {
-        float* out = a.partial + (static_cast<int64_t>(which) * gridDim.x + blockIdx.x) * a.cols;
-        for (int c = threadIdx.x; c < a.cols; c += BLOCK) {
-            const int pack = c / VEC;            // column c is element c % VEC of this pack
-            out[c] = join[(which * kLaneCols + pack / lanes * VEC + c % VEC) * lanes + pack % lanes];
+}
+
+// The same through rings of stages that hold a row of x and one of dy.
+template <typename T, typename W, int VEC>
+__global__ void __launch_bounds__(kBackwardRing, 1) norm_backward_ring_kernel(const BackwardArgs<T, W> a, int stages) {
+    extern __shared__ __align__(128) uint8_t memory[];
+    __shared__ RingBarriers barriers;
+    __shared__ float part[kBackwardRing / 32][2][2][32];
+    const int lanes = a.lanes, groups = kBackwardRing / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+    const int row_bytes = a.cols * static_cast<int>(sizeof(T));
+    if (threadIdx.x == 0) init_ring(barriers, groups * stages);
+    __syncthreads();
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    int64_t row = blockIdx.x + static_cast<int64_t>(group) * gridDim.x;
+    Ring<2> ring{memory + group * stages * 2 * row_bytes,
+                 barriers.full + group * stages,
+                 &barriers.dead,
+                 a.error,
+                 {reinterpret_cast<const uint8_t*>(a.x), reinterpret_cast<const uint8_t*>(a.dy)},
+                 {a.ldx * static_cast<int64_t>(sizeof(T)), a.lddy * static_cast<int64_t>(sizeof(T))},
+                 a.rows,
+                 static_cast<int64_t>(groups) * gridDim.x,
+                 row_bytes,
+                 stages,
+                 {0, 0},
+                 0};
+    if (lane == 0) ring.begin(row);
+    const float inverse_n = 1.f / static_cast<float>(a.cols);
+    GroupSum<2> sum{part[group], lanes, 1 + group, 0};
+    Pair dg[kPairs], db[kPairs], gamma[kPairs];
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) dg[j] = db[j] = Pair(0.f, 0.f);
+    load_weights<W, VEC, kLaneCols>(a.gamma, 1.f, lane, lanes, a.cols, gamma);
+    float next_mean = 0.f, next_rstd = 0.f;
+    const auto ask = [&](int64_t r) {
+        next_mean = a.mean[r];
+        next_rstd = a.rstd[r];
+    };
+    if (row < a.rows) ask(row);
+    T* dx = a.dx ? a.dx + row * a.lddx : nullptr;
+    const int64_t dx_step = a.dx ? ring.step * a.lddx : 0;
+    for (; row < a.rows; row += ring.step, dx += dx_step, ring.turn.next(1, stages)) {
+        const float mu = next_mean, r = next_rstd;
+        if (row + ring.step < a.rows) ask(row + ring.step);
+        Pair hat[kPairs], g[kPairs];
+        {
+            RowPacks<T, VEC, kLaneCols, true> x, dy;
+            const uint8_t* at = ring.wait();
+            x.load(reinterpret_cast<const T*>(at), lane, lanes, a.cols);
+            dy.load(reinterpret_cast<const T*>(at + row_bytes), lane, lanes, a.cols);
+            to_pairs(x.p, hat);
+            to_pairs(dy.p, g);
         }
+        const Pair minus(-mu, -mu), r2(r, r);
+        Pair sum_g(0.f, 0.f), sum_gx(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            hat[j] = mul2(add2(hat[j], minus), r2);
+            dg[j] = fma2(g[j], hat[j], dg[j]);
+            db[j] = add2(db[j], g[j]);
+            g[j] = mul2(g[j], gamma[j]);
+            sum_g = add2(sum_g, g[j]);
+            sum_gx = fma2(g[j], hat[j], sum_gx);
+        }
+        float s[2];
+        row_sums(sum_g, sum_gx, sum, lane, s);
+        ring.release(lane, row);
+        if (a.dx) write_dx<T, VEC, true>(hat, g, s, inverse_n, r2, dx, lane, lanes, a.cols);
     }
+    if (lane == 0) ring.end();
+    if (!a.weights) return;
+    __syncthreads();                                     // the rings have been read: their memory joins the groups
+    float* const join = reinterpret_cast<float*>(memory);
+    const auto add_to = [&](int which, int j, Pair v, bool fresh) {
+        float lo, hi;
+        v.get(lo, hi);
+        float& at = join[(which * kLaneCols + 2 * j) * lanes + lane];
+        float& at1 = join[(which * kLaneCols + 2 * j + 1) * lanes + lane];
+        at = fresh ? lo : at + lo;
+        at1 = fresh ? hi : at1 + hi;
+    };
+    write_partial<VEC, kBackwardRing>(dg, db, group, groups, lanes, a.cols, join, a.partial, add_to);
 }
 
 // The blocks' sums of 32 columns: eight warps take every eighth block, then join.
@@ -431,8 +712,31 @@ gemm_status_t forward_rows(const ForwardArgs<T, W>& a, int sms, void* stream) {
     return launch(kernel, blocks < most ? blocks : most, BLOCK, 0, stream, 1, a);
 }
 
+// Stages of a group's ring whose block also needs `fixed` bytes; 0 where rings do not suit:
+// rows that are no whole 16-byte units, rows too short for a copy each, or too few rows for
+// two to each group of each SM's block.
+int ring_stages(int64_t row_bytes, int sources, int lanes, int threads, int64_t fixed, int64_t rows, int sms) {
+    const int groups = threads / lanes;
+    if (groups == 0 || row_bytes % 16 != 0 || row_bytes < 512 || rows < int64_t{2} * sms * groups) return 0;
+    int64_t stages = (kRingShared - fixed) / (row_bytes * sources * groups);
+    if (stages > kRingSlots / groups) stages = kRingSlots / groups;
+    return stages < 2 ? 0 : static_cast<int>(stages);
+}
+
 template <typename T, typename W, int VEC>
 gemm_status_t forward_vec(const ForwardArgs<T, W>& a, int sms, void* stream) {
+    if constexpr (VEC > 1) {
+        ForwardArgs<T, W> b = a;
+        const bool half = b.lanes > 32;              // 32 columns a lane
+        if (half) b.lanes /= 2;
+        const int64_t row_bytes = static_cast<int64_t>(a.cols) * static_cast<int64_t>(sizeof(T));
+        const int64_t weights = int64_t{2} * a.lanes * kLaneCols * static_cast<int64_t>(sizeof(W));
+        const int stages = ring_stages(row_bytes, 1, b.lanes, kForwardRing, weights, a.rows, sms);
+        const size_t smem = static_cast<size_t>(kForwardRing / b.lanes * stages * row_bytes + weights);
+        if (stages > 0)
+            return half ? launch(norm_forward_ring_kernel<T, W, VEC, 32>, sms, kForwardRing, smem, stream, 1, b, stages)
+                        : launch(norm_forward_ring_kernel<T, W, VEC, 16>, sms, kForwardRing, smem, stream, 1, b, stages);
+    }
     if (a.lanes <= 256) return forward_rows<T, W, VEC, 256, true>(a, sms, stream);
     if (a.lanes == 512) return forward_rows<T, W, VEC, 512, true>(a, sms, stream);
     return forward_rows<T, W, VEC, 1024, false>(a, sms, stream);
@@ -454,7 +758,12 @@ gemm_status_t prepare() {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     lanes * kLaneCols * 2 * static_cast<int>(sizeof(float))) == cudaSuccess;
     };
-    if (allow(norm_backward_kernel<T, W, kVec, 512, false>, 512) && allow(norm_backward_kernel<T, W, 1, 512, false>, 512) &&
+    const auto allow_ring = [](auto kernel) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingShared) == cudaSuccess;
+    };
+    if (allow_ring(norm_forward_ring_kernel<T, W, kVec, 16>) && allow_ring(norm_forward_ring_kernel<T, W, kVec, 32>) &&
+        allow_ring(norm_backward_ring_kernel<T, W, kVec>) &&
+        allow(norm_backward_kernel<T, W, kVec, 512, false>, 512) && allow(norm_backward_kernel<T, W, 1, 512, false>, 512) &&
         allow(norm_backward_kernel<T, W, kVec, 1024, true>, 1024) && allow(norm_backward_kernel<T, W, 1, 1024, true>, 1024))
         return GEMM_OK;
     cudaGetLastError();
@@ -470,7 +779,16 @@ int64_t backward_blocks(int64_t rows, int lanes, int sms) {
 }
 
 template <typename T, typename W, int VEC>
-gemm_status_t backward_vec(const BackwardArgs<T, W>& a, int blocks, void* stream) {
+gemm_status_t backward_vec(const BackwardArgs<T, W>& a, int blocks, int sms, void* stream) {
+    if constexpr (VEC > 1) {
+        const int64_t row_bytes = static_cast<int64_t>(a.cols) * static_cast<int64_t>(sizeof(T));
+        const int stages = ring_stages(row_bytes, 2, a.lanes, kBackwardRing, 0, a.rows, sms);
+        const size_t ring = static_cast<size_t>(2 * (kBackwardRing / (a.lanes > kBackwardRing ? kBackwardRing : a.lanes)) * stages * row_bytes);
+        const size_t join = static_cast<size_t>(a.lanes) * kLaneCols * 2 * sizeof(float);
+        if (stages > 0)
+            return launch(norm_backward_ring_kernel<T, W, VEC>, blocks, kBackwardRing, ring > join ? ring : join, stream, 1,
+                          a, stages);
+    }
     if (a.lanes <= 512) return backward_rows<T, W, VEC, 512, false>(a, blocks, stream);
     return backward_rows<T, W, VEC, 1024, true>(a, blocks, stream);
 }
@@ -500,16 +818,19 @@ gemm_status_t gemm_norm_plan_create(int64_t max_rows, int64_t cols, gemm_elem_t 
     int device = 0, sms = 0;
     const gemm_status_t st = gbt::current_device(&device, &sms);
     if (st != GEMM_OK) return st;
-    void* partial = nullptr;
-    if (max_rows > 0 && gbt::in_registers(cols)) {
-        const int64_t blocks = gbt::backward_blocks(max_rows, gbt::lanes_for(cols), sms);
-        const gemm_status_t room = gbt::allocate(&partial, static_cast<size_t>(blocks * cols) * 2 * sizeof(float));
-        if (room != GEMM_OK) return room;
-    }
+    size_t sums = 0;
+    if (max_rows > 0 && gbt::in_registers(cols))
+        sums = static_cast<size_t>(gbt::backward_blocks(max_rows, gbt::lanes_for(cols), sms) * cols) * 2 * sizeof(float);
+    void* memory = nullptr;
+    gemm_status_t room = gbt::allocate(&memory, 256 + sums);
+    if (room != GEMM_OK) return room;
     gemm_norm_plan* p = new (std::nothrow) gemm_norm_plan();
-    if (!p) {
-        cudaFree(partial);
-        return GEMM_ERR_OOM;
+    if (!p || cudaMemset(memory, 0, 256) != cudaSuccess) {
+        cudaGetLastError();
+        cudaFree(memory);
+        room = p ? GEMM_ERR_CUDA : GEMM_ERR_OOM;
+        delete p;
+        return room;
     }
     p->max_rows = max_rows;
     p->cols = cols;
@@ -517,11 +838,13 @@ gemm_status_t gemm_norm_plan_create(int64_t max_rows, int64_t cols, gemm_elem_t 
     p->weight_elem = weight_elem;
     p->device = device;
     p->num_sms = sms;
-    p->partial = static_cast<float*>(partial);
+    p->memory = memory;
+    p->error_word = static_cast<int32_t*>(memory);
+    p->partial = reinterpret_cast<float*>(static_cast<uint8_t*>(memory) + 256);
     const gemm_status_t ready =
         gbt::with_types(p, [](auto t, auto v) { return gbt::prepare<decltype(t), decltype(v)>(); });
     if (ready != GEMM_OK) {
-        cudaFree(partial);
+        cudaFree(memory);
         delete p;
         return ready;
     }
@@ -545,7 +868,7 @@ gemm_status_t gemm_norm_forward(gemm_norm_plan_t p, int64_t rows, const void* x,
         using W = decltype(v);
         const gbt::ForwardArgs<T, W> a{static_cast<const T*>(x), static_cast<const W*>(gamma),
                                        static_cast<const W*>(beta), static_cast<T*>(y), mean, rstd,
-                                       ldx, ldy, rows, eps, static_cast<int>(p->cols),
+                                       p->error_word, ldx, ldy, rows, eps, static_cast<int>(p->cols),
                                        gbt::lanes_for(p->cols)};
         if (!gbt::in_registers(p->cols))
             return gbt::launch(gbt::norm_forward_wide_kernel<T, W>, rows, gbt::kThreads, 0, stream, 1, a);
@@ -579,7 +902,7 @@ gemm_status_t gemm_norm_backward(gemm_norm_plan_t p, int64_t rows, const void* x
         W* db = static_cast<W*>(dbeta);
         const int lanes = gbt::lanes_for(p->cols);
         gbt::BackwardArgs<T, W> a{static_cast<const T*>(x), static_cast<const W*>(gamma), mean, rstd,
-                                  static_cast<const T*>(dy), static_cast<T*>(dx), p->partial, ldx,
+                                  static_cast<const T*>(dy), static_cast<T*>(dx), p->partial, p->error_word, ldx,
                                   lddy, lddx, rows, static_cast<int>(p->cols), lanes, dg || db};
         const int tiles = static_cast<int>((p->cols + 31) / 32);
         gemm_status_t s = GEMM_OK;
@@ -597,8 +920,8 @@ gemm_status_t gemm_norm_backward(gemm_norm_plan_t p, int64_t rows, const void* x
             const bool vec = gbt::rows_aligned(x, ldx, e) && gbt::rows_aligned(dy, lddy, e) &&
                              (!dx || gbt::rows_aligned(dx, lddx, e)) && gbt::aligned(gamma, 16);
             constexpr int kVec = 16 / static_cast<int>(sizeof(T));
-            s = vec ? gbt::backward_vec<T, W, kVec>(a, blocks, stream)
-                    : gbt::backward_vec<T, W, 1>(a, blocks, stream);
+            s = vec ? gbt::backward_vec<T, W, kVec>(a, blocks, p->num_sms, stream)
+                    : gbt::backward_vec<T, W, 1>(a, blocks, p->num_sms, stream);
         }
         if (s == GEMM_OK && a.weights)
             s = gbt::launch(gbt::norm_weight_join_kernel<W>, 2 * tiles, gbt::kThreads, 0, stream, 1,
@@ -607,9 +930,13 @@ gemm_status_t gemm_norm_backward(gemm_norm_plan_t p, int64_t rows, const void* x
     });
 }
 
+gemm_status_t gemm_norm_plan_check(gemm_norm_plan_t p, void* stream) {
+    return p ? gbt::check_error_word(p->error_word, stream) : GEMM_ERR_INVALID_ARG;
+}
+
 gemm_status_t gemm_norm_plan_destroy(gemm_norm_plan_t p) {
     if (!p) return GEMM_OK;
-    const gemm_status_t st = cudaFree(p->partial) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+    const gemm_status_t st = cudaFree(p->memory) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
     if (st != GEMM_OK) cudaGetLastError();
     delete p;
     return st;

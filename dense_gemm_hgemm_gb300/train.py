@@ -50,6 +50,7 @@ def signatures():
         "gemm_norm_plan_create": ([i64, i64, i32, i32, vpp], i32),
         "gemm_norm_forward": ([vp, i64, vp, i64, vp, vp, f32, vp, i64, vp, vp, vp], i32),
         "gemm_norm_backward": ([vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp], i32),
+        "gemm_norm_plan_check": ([vp, vp], i32),
         "gemm_norm_plan_destroy": ([vp], i32),
         "gemm_embed_plan_create": ([i64, i64, i64, i32, i32, vpp], i32),
         "gemm_embed_forward": ([vp, i64, vp, i32, i64, vp, i64, f32, vp, i64, vp], i32),
@@ -235,6 +236,10 @@ class NormPlan(_Plan):
             pdy, lddy, pdx, lddx, _vector(dgamma, cols, self._weight, "dgamma", True),
             _vector(dbeta, cols, self._weight, "dbeta", True), _stream(stream)),
             "gemm_norm_backward")
+
+    def check(self, stream=None) -> None:
+        """Synchronise `stream`; raise GemmError(GEMM_ERR_DEVICE_TIMEOUT) if a kernel gave up on a wait."""
+        _check(library().gemm_norm_plan_check(self.handle, _stream(stream)), "gemm_norm_plan_check")
 
 
 class EmbedPlan(_Plan):

@@ -89,6 +89,13 @@ gemm_status_t gemm_norm_backward(gemm_norm_plan_t plan, int64_t rows, const void
                                  const void *dy, int64_t lddy, void *dx, int64_t lddx,
                                  void *dgamma, void *dbeta, void *stream);
 
+/*
+ * Synchronise `stream`, then read and clear the plan's error word:
+ * GEMM_ERR_DEVICE_TIMEOUT if a kernel of this plan gave up on a wait, GEMM_ERR_CUDA
+ * if the stream reported an error, else GEMM_OK.
+ */
+gemm_status_t gemm_norm_plan_check(gemm_norm_plan_t plan, void *stream);
+
 /* Free a plan and its device memory.  NULL is a no-op. */
 gemm_status_t gemm_norm_plan_destroy(gemm_norm_plan_t plan);
 
@@ -211,7 +218,10 @@ gemm_status_t gemm_distill_forward_backward(gemm_distill_plan_t plan, int64_t ro
                                             const float *dloss, float *loss, float *lse,
                                             void *dlogits, int64_t ldd, void *stream);
 
-/* As gemm_embed_plan_check, for the teacher's ids. */
+/*
+ * As gemm_embed_plan_check, for the teacher's ids; GEMM_ERR_DEVICE_TIMEOUT if a
+ * kernel of this plan gave up on a wait.
+ */
 gemm_status_t gemm_distill_plan_check(gemm_distill_plan_t plan, void *stream);
 
 /* Free a plan and its device memory.  NULL is a no-op. */

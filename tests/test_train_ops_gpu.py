@@ -54,7 +54,8 @@ def _canary_whole(m):
 
 NORM_SIZES = [(1, 1), (1, 2), (3, 7), (5, 8), (2, 31), (33, 32), (7, 100), (4, 250), (17, 256), (9, 511), (300, 96),
               (5, 1000), (3, 1024), (700, 72), (2, 1031), (6, 2048), (3, 2056), (4, 4096), (310, 1024), (2, 4100),
-              (5, 5000), (3, 8192), (2, 8200), (3, 16384), (2, 16385), (2, 20000), (1, 40001)]
+              (5, 5000), (3, 8192), (2, 8200), (3, 16384), (2, 16385), (2, 20000), (1, 40001),
+              (10000, 256), (5200, 1000), (2500, 1032), (1300, 4096), (700, 8192), (650, 12000), (320, 16384)]
 
 
 def _norm_case(rows, cols, elem, weight, pad, offset, seed=0):
