@@ -141,23 +141,64 @@ __device__ __forceinline__ float rstd_of(const Pair (&v)[N], GroupSum<1>& sum, f
     return rsqrtf(s[0] * inverse_n + eps);
 }
 
-// and the result, with the weights read on the way, a pack at a time (VEC > 1, whole packs).
+// Weights in shared memory.  Packs of eight fp32 values are kept as two halves, each with
+// the others' halves, so that neighbouring lanes' 16-byte reads are neighbours (side by side
+// they would share banks: 61 us instead of 51 at 16384 x 4096 with fp32 weights).
+template <typename W, int VEC>
+struct Staged {
+    static constexpr bool kHalves = VEC * sizeof(W) > 16;
+    static constexpr int kPer = kHalves ? VEC / 2 : VEC;
+    W* at;
+    int half;                // elements of a half: those of the row's packs
+    __device__ __forceinline__ void put(int c, W v) {
+        at[kHalves ? (c % VEC / kPer) * half + c / VEC * kPer + c % kPer : c] = v;
+    }
+    __device__ __forceinline__ void get(int c, float (&v)[VEC]) const {      // the pack at column c
+#pragma unroll
+        for (int h = 0; h < VEC / kPer; ++h) {
+            const Pack<W, kPer> q = load_pack<W, kPer>(at + (kHalves ? h * half + c / VEC * kPer : c), kPer);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) v[h * kPer + i] = q.get(i);
+        }
+    }
+};
+
+// and the result, with the weights read on the way, a pack at a time (whole packs).
 template <typename T, typename W, int VEC, int N>
-__device__ __forceinline__ void normalise(const Pair (&v)[N], float r, const W* gamma, const W* beta, T* y, int lane,
-                                          int lanes, int cols) {
+__device__ __forceinline__ void normalise(const Pair (&v)[N], float r, const Staged<W, VEC>& gamma,
+                                          const Staged<W, VEC>& beta, T* y, int lane, int lanes, int cols) {
     const Pair r2(r, r);
+    if constexpr (VEC == 1) {
 #pragma unroll
-    for (int k = 0; k < 2 * N / VEC; ++k) {
-        const int c = (k * lanes + lane) * VEC;
-        if (c >= cols) break;
-        float g[VEC], b[VEC];
-        load_values<W, VEC>(gamma + c, VEC, g);
-        load_values<W, VEC>(beta + c, VEC, b);
-        Pack<T, VEC> out;
+        for (int j = 0; j < N; ++j) {
+            const int c = 2 * j * lanes + lane, c1 = c + lanes;
+            if (c >= cols) break;
+            float g0[1], g1[1] = {0.f}, b0[1], b1[1] = {0.f}, lo, hi;
+            gamma.get(c, g0);
+            beta.get(c, b0);
+            if (c1 < cols) {
+                gamma.get(c1, g1);
+                beta.get(c1, b1);
+            }
+            fma2(mul2(v[j], r2), Pair(g0[0], g1[0]), Pair(b0[0], b1[0])).get(lo, hi);
+            y[c] = from_f32<T>(lo);
+            if (c1 < cols) y[c1] = from_f32<T>(hi);
+        }
+    } else {
 #pragma unroll
-        for (int i = 0; i < VEC / 2; ++i)
-            set_pair(out, i, fma2(mul2(v[k * (VEC / 2) + i], r2), Pair(g[2 * i], g[2 * i + 1]), Pair(b[2 * i], b[2 * i + 1])));
-        store_pack<T, VEC>(y + c, VEC, out);
+        for (int k = 0; k < 2 * N / VEC; ++k) {
+            const int c = (k * lanes + lane) * VEC;
+            if (c >= cols) break;
+            float g[VEC], b[VEC];
+            gamma.get(c, g);
+            beta.get(c, b);
+            Pack<T, VEC> out;
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i)
+                set_pair(out, i,
+                         fma2(mul2(v[k * (VEC / 2) + i], r2), Pair(g[2 * i], g[2 * i + 1]), Pair(b[2 * i], b[2 * i + 1])));
+            store_pack<T, VEC>(y + c, VEC, out);
+        }
     }
 }
 
@@ -233,8 +274,10 @@ constexpr int kRingShared = 208 * 1024;    // its dynamic shared memory, at most
 constexpr int kForwardRing = 1024;         // threads of the blocks
 constexpr int kBackwardRing = 512;
 
-// A group's ring; each stage holds a row from each of N sources.
-template <int N>
+// A group's ring; each stage holds a row from each of N sources.  Where rows do not begin or
+// end at 16-byte boundaries (ANY), the whole 16-byte units around a row are copied; the first
+// and the last row of the matrix, whose units may reach beyond it, are left to plain loads.
+template <int N, bool ANY>
 struct Ring {
     uint8_t* memory;
     uint64_t* full;
@@ -242,27 +285,45 @@ struct Ring {
     int32_t* error;
     const uint8_t* src[N];
     int64_t stride[N], rows, step;         // bytes; the matrix' rows, from one of the group's to its next
-    int row_bytes, stages;
+    int row_bytes, stage_bytes, stages;    // (stage_bytes: of one source)
     Turn turn;
     int64_t asked;                         // rows asked for, by the lane that asks
 
+    __device__ __forceinline__ bool direct(int64_t row) const { return ANY && (row == 0 || row == rows - 1); }
     __device__ __forceinline__ void ask(int stage, int64_t row) {
         if (row >= rows || *static_cast<volatile int*>(dead)) return;
-        expect_bytes(&full[stage], static_cast<uint32_t>(N * row_bytes));
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-            copy_bytes(memory + (stage * N + k) * row_bytes, src[k] + row * stride[k], static_cast<uint32_t>(row_bytes),
-                       &full[stage]);
         ++asked;
+        if (direct(row)) {
+            expect_bytes(&full[stage], 0);
+            return;
+        }
+        const uint8_t* from[N];
+        uint32_t bytes[N], all = 0;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            from[k] = src[k] + row * stride[k];
+            bytes[k] = static_cast<uint32_t>(row_bytes);
+            if (ANY) {
+                const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(from[k]) & 15u);
+                from[k] -= off;
+                bytes[k] = (off + bytes[k] + 15u) / 16u * 16u;
+            }
+            all += bytes[k];
+        }
+        expect_bytes(&full[stage], all);
+#pragma unroll
+        for (int k = 0; k < N; ++k) copy_bytes(memory + (stage * N + k) * stage_bytes, from[k], bytes[k], &full[stage]);
     }
     // (one lane)
     __device__ __forceinline__ void begin(int64_t row) {
         for (int k = 0; k < stages; ++k) ask(k, row + k * step);
     }
-    // The present stage, once its row has come.
-    __device__ __forceinline__ const uint8_t* wait() const {
-        wait_or_die(&full[turn.at], turn.round & 1, dead, error);
-        return memory + turn.at * N * row_bytes;
+    __device__ __forceinline__ void wait() const { wait_or_die(&full[turn.at], turn.round & 1, dead, error); }
+    // Source k's row, in the present stage (or in the matrix), once waited for.
+    __device__ __forceinline__ const uint8_t* at(int k, int64_t row) const {
+        const uint8_t* from = src[k] + row * stride[k];
+        if (direct(row)) return from;
+        return memory + (turn.at * N + k) * stage_bytes + (ANY ? reinterpret_cast<uintptr_t>(from) & 15u : 0);
     }
     // All lanes have read the present stage.
     __device__ __forceinline__ void release(int lane, int64_t row) {
@@ -275,6 +336,11 @@ struct Ring {
             wait_phase(&full[k % stages], (k / stages) & 1);
     }
 };
+
+// Bytes of a row in a stage.
+__host__ __device__ constexpr int ring_stage_bytes(int row_bytes, bool any) {
+    return any ? (row_bytes + 15) / 16 * 16 + 16 : row_bytes;
+}
 
 struct RingBarriers {
     uint64_t full[kRingSlots];
@@ -296,15 +362,16 @@ __global__ void __launch_bounds__(kForwardRing, 1) norm_forward_ring_kernel(cons
     __shared__ RingBarriers barriers;
     __shared__ float part[kForwardRing / 32][2][1][32];
     const int lanes = a.lanes, groups = kForwardRing / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-    const int row_bytes = a.cols * static_cast<int>(sizeof(T));
-    W* const gamma = reinterpret_cast<W*>(memory + groups * stages * row_bytes);
-    W* const beta = gamma + lanes * COLS;
+    constexpr bool kAny = VEC == 1;
+    const int row_bytes = a.cols * static_cast<int>(sizeof(T)), stage_bytes = ring_stage_bytes(row_bytes, kAny);
+    Staged<W, VEC> gamma{reinterpret_cast<W*>(memory + groups * stages * stage_bytes), lanes * COLS / 2};
+    Staged<W, VEC> beta{gamma.at + lanes * COLS, gamma.half};
     if (threadIdx.x == 0) init_ring(barriers, groups * stages);
     __syncthreads();
     wait_for_previous_kernel();
     let_next_kernel_start();
     int64_t row = blockIdx.x + static_cast<int64_t>(group) * gridDim.x;
-    Ring<1> ring{memory + group * stages * row_bytes,
+    Ring<1, kAny> ring{memory + group * stages * stage_bytes,
                  barriers.full + group * stages,
                  &barriers.dead,
                  a.error,
@@ -313,13 +380,14 @@ __global__ void __launch_bounds__(kForwardRing, 1) norm_forward_ring_kernel(cons
                  a.rows,
                  static_cast<int64_t>(groups) * gridDim.x,
                  row_bytes,
+                 stage_bytes,
                  stages,
                  {0, 0},
                  0};
     if (lane == 0) ring.begin(row);
     for (int c = threadIdx.x; c < a.cols; c += kForwardRing) {
-        gamma[c] = a.gamma ? a.gamma[c] : from_f32<W>(1.f);
-        beta[c] = a.beta ? a.beta[c] : from_f32<W>(0.f);
+        gamma.put(c, a.gamma ? a.gamma[c] : from_f32<W>(1.f));
+        beta.put(c, a.beta ? a.beta[c] : from_f32<W>(0.f));
     }
     __syncthreads();
     const bool full = a.cols == lanes * COLS;
@@ -331,7 +399,8 @@ __global__ void __launch_bounds__(kForwardRing, 1) norm_forward_ring_kernel(cons
         Pair v[COLS / 2];
         {
             RowPacks<T, VEC, COLS, true> in;
-            in.load(reinterpret_cast<const T*>(ring.wait()), lane, lanes, a.cols);
+            ring.wait();
+            in.load(reinterpret_cast<const T*>(ring.at(0, row)), lane, lanes, a.cols);
             to_pairs(in.p, v);
         }
         const float mu = centre<VEC>(v, sum, inverse_n, full, lane, lanes, a.cols);
@@ -500,13 +569,14 @@ __global__ void __launch_bounds__(kBackwardRing, 1) norm_backward_ring_kernel(co
     __shared__ RingBarriers barriers;
     __shared__ float part[kBackwardRing / 32][2][2][32];
     const int lanes = a.lanes, groups = kBackwardRing / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-    const int row_bytes = a.cols * static_cast<int>(sizeof(T));
+    constexpr bool kAny = VEC == 1;
+    const int row_bytes = a.cols * static_cast<int>(sizeof(T)), stage_bytes = ring_stage_bytes(row_bytes, kAny);
     if (threadIdx.x == 0) init_ring(barriers, groups * stages);
     __syncthreads();
     wait_for_previous_kernel();
     let_next_kernel_start();
     int64_t row = blockIdx.x + static_cast<int64_t>(group) * gridDim.x;
-    Ring<2> ring{memory + group * stages * 2 * row_bytes,
+    Ring<2, kAny> ring{memory + group * stages * 2 * stage_bytes,
                  barriers.full + group * stages,
                  &barriers.dead,
                  a.error,
@@ -515,6 +585,7 @@ __global__ void __launch_bounds__(kBackwardRing, 1) norm_backward_ring_kernel(co
                  a.rows,
                  static_cast<int64_t>(groups) * gridDim.x,
                  row_bytes,
+                 stage_bytes,
                  stages,
                  {0, 0},
                  0};
@@ -539,9 +610,9 @@ __global__ void __launch_bounds__(kBackwardRing, 1) norm_backward_ring_kernel(co
         Pair hat[kPairs], g[kPairs];
         {
             RowPacks<T, VEC, kLaneCols, true> x, dy;
-            const uint8_t* at = ring.wait();
-            x.load(reinterpret_cast<const T*>(at), lane, lanes, a.cols);
-            dy.load(reinterpret_cast<const T*>(at + row_bytes), lane, lanes, a.cols);
+            ring.wait();
+            x.load(reinterpret_cast<const T*>(ring.at(0, row)), lane, lanes, a.cols);
+            dy.load(reinterpret_cast<const T*>(ring.at(1, row)), lane, lanes, a.cols);
             to_pairs(x.p, hat);
             to_pairs(dy.p, g);
         }
@@ -713,11 +784,11 @@ gemm_status_t forward_rows(const ForwardArgs<T, W>& a, int sms, void* stream) {
 }
 
 // Stages of a group's ring whose block also needs `fixed` bytes; 0 where rings do not suit:
-// rows that are no whole 16-byte units, rows too short for a copy each, or too few rows for
-// two to each group of each SM's block.
-int ring_stages(int64_t row_bytes, int sources, int lanes, int threads, int64_t fixed, int64_t rows, int sms) {
+// rows of no whole packs, rows too short for a copy each, or too few rows for two to each group of each SM's block.
+int ring_stages(int cols, int vec, int64_t row_bytes, int sources, int lanes, int threads, int64_t fixed, int64_t rows,
+                int sms) {
     const int groups = threads / lanes;
-    if (groups == 0 || row_bytes % 16 != 0 || row_bytes < 512 || rows < int64_t{2} * sms * groups) return 0;
+    if (groups == 0 || row_bytes < 512 || cols % vec != 0 || rows < int64_t{2} * sms * groups) return 0;
     int64_t stages = (kRingShared - fixed) / (row_bytes * sources * groups);
     if (stages > kRingSlots / groups) stages = kRingSlots / groups;
     return stages < 2 ? 0 : static_cast<int>(stages);
@@ -725,17 +796,18 @@ int ring_stages(int64_t row_bytes, int sources, int lanes, int threads, int64_t 
 
 template <typename T, typename W, int VEC>
 gemm_status_t forward_vec(const ForwardArgs<T, W>& a, int sms, void* stream) {
-    if constexpr (VEC > 1) {
-        ForwardArgs<T, W> b = a;
-        const bool half = b.lanes > 32;              // 32 columns a lane
-        if (half) b.lanes /= 2;
-        const int64_t row_bytes = static_cast<int64_t>(a.cols) * static_cast<int64_t>(sizeof(T));
-        const int64_t weights = int64_t{2} * a.lanes * kLaneCols * static_cast<int64_t>(sizeof(W));
-        const int stages = ring_stages(row_bytes, 1, b.lanes, kForwardRing, weights, a.rows, sms);
-        const size_t smem = static_cast<size_t>(kForwardRing / b.lanes * stages * row_bytes + weights);
-        if (stages > 0)
-            return half ? launch(norm_forward_ring_kernel<T, W, VEC, 32>, sms, kForwardRing, smem, stream, 1, b, stages)
-                        : launch(norm_forward_ring_kernel<T, W, VEC, 16>, sms, kForwardRing, smem, stream, 1, b, stages);
+    ForwardArgs<T, W> b = a;
+    const bool half = VEC > 1 && b.lanes > 32;   // 32 columns a lane (single elements take more registers)
+    if (half) b.lanes /= 2;
+    const int64_t stage = ring_stage_bytes(a.cols * static_cast<int>(sizeof(T)), VEC == 1);
+    const int64_t weights = int64_t{2} * a.lanes * kLaneCols * static_cast<int64_t>(sizeof(W));
+    const int stages = ring_stages(a.cols, VEC, stage, 1, b.lanes, kForwardRing, weights, a.rows, sms);
+    if (stages > 0) {
+        const size_t smem = static_cast<size_t>(kForwardRing / b.lanes * stages * stage + weights);
+        if constexpr (VEC > 1) {
+            if (half) return launch(norm_forward_ring_kernel<T, W, VEC, 32>, sms, kForwardRing, smem, stream, 1, b, stages);
+        }
+        return launch(norm_forward_ring_kernel<T, W, VEC, 16>, sms, kForwardRing, smem, stream, 1, b, stages);
     }
     if (a.lanes <= 256) return forward_rows<T, W, VEC, 256, true>(a, sms, stream);
     if (a.lanes == 512) return forward_rows<T, W, VEC, 512, true>(a, sms, stream);
@@ -762,7 +834,8 @@ gemm_status_t prepare() {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingShared) == cudaSuccess;
     };
     if (allow_ring(norm_forward_ring_kernel<T, W, kVec, 16>) && allow_ring(norm_forward_ring_kernel<T, W, kVec, 32>) &&
-        allow_ring(norm_backward_ring_kernel<T, W, kVec>) &&
+        allow_ring(norm_forward_ring_kernel<T, W, 1, 16>) &&
+        allow_ring(norm_backward_ring_kernel<T, W, kVec>) && allow_ring(norm_backward_ring_kernel<T, W, 1>) &&
         allow(norm_backward_kernel<T, W, kVec, 512, false>, 512) && allow(norm_backward_kernel<T, W, 1, 512, false>, 512) &&
         allow(norm_backward_kernel<T, W, kVec, 1024, true>, 1024) && allow(norm_backward_kernel<T, W, 1, 1024, true>, 1024))
         return GEMM_OK;
@@ -780,14 +853,13 @@ int64_t backward_blocks(int64_t rows, int lanes, int sms) {
 
 template <typename T, typename W, int VEC>
 gemm_status_t backward_vec(const BackwardArgs<T, W>& a, int blocks, int sms, void* stream) {
-    if constexpr (VEC > 1) {
-        const int64_t row_bytes = static_cast<int64_t>(a.cols) * static_cast<int64_t>(sizeof(T));
-        const int stages = ring_stages(row_bytes, 2, a.lanes, kBackwardRing, 0, a.rows, sms);
-        const size_t ring = static_cast<size_t>(2 * (kBackwardRing / (a.lanes > kBackwardRing ? kBackwardRing : a.lanes)) * stages * row_bytes);
+    const int64_t stage = ring_stage_bytes(a.cols * static_cast<int>(sizeof(T)), VEC == 1);
+    const int stages = ring_stages(a.cols, VEC, stage, 2, a.lanes, kBackwardRing, 0, a.rows, sms);
+    if (stages > 0) {
+        const size_t ring = static_cast<size_t>(2 * (kBackwardRing / a.lanes) * stages * stage);
         const size_t join = static_cast<size_t>(a.lanes) * kLaneCols * 2 * sizeof(float);
-        if (stages > 0)
-            return launch(norm_backward_ring_kernel<T, W, VEC>, blocks, kBackwardRing, ring > join ? ring : join, stream, 1,
-                          a, stages);
+        return launch(norm_backward_ring_kernel<T, W, VEC>, blocks, kBackwardRing, ring > join ? ring : join, stream, 1,
+                      a, stages);
     }
     if (a.lanes <= 512) return backward_rows<T, W, VEC, 512, false>(a, blocks, stream);
     return backward_rows<T, W, VEC, 1024, true>(a, blocks, stream);
