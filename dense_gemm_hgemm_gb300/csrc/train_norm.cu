@@ -172,16 +172,13 @@ __device__ __forceinline__ void normalise(const Pair (&v)[N], float r, const Sta
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const int c = 2 * j * lanes + lane, c1 = c + lanes;
-            if (c >= cols) break;
-            float g0[1], g1[1] = {0.f}, b0[1], b1[1] = {0.f}, lo, hi;
-            gamma.get(c, g0);
+            float g0[1], g1[1], b0[1], b1[1], lo, hi;
+            gamma.get(c, g0);                            // (there is room for all lanes' columns)
+            gamma.get(c1, g1);
             beta.get(c, b0);
-            if (c1 < cols) {
-                gamma.get(c1, g1);
-                beta.get(c1, b1);
-            }
+            beta.get(c1, b1);
             fma2(mul2(v[j], r2), Pair(g0[0], g1[0]), Pair(b0[0], b1[0])).get(lo, hi);
-            y[c] = from_f32<T>(lo);
+            if (c < cols) y[c] = from_f32<T>(lo);
             if (c1 < cols) y[c1] = from_f32<T>(hi);
         }
     } else {
@@ -269,6 +266,7 @@ __global__ void __launch_bounds__(BLOCK) norm_forward_kernel(const ForwardArgs<T
 // depend on how many registers are left for loads: the register kernels keep 24 KB an SM
 // in flight at 16384 x 4096, the rings over 100 KB.
 
+constexpr int kRingRows = 1 << 30;         // rows are counted in 32 bits there, a step beyond the last
 constexpr int kRingSlots = 64;             // stages of a block, at most
 constexpr int kRingShared = 208 * 1024;    // its dynamic shared memory, at most
 constexpr int kForwardRing = 1024;         // threads of the blocks
@@ -284,14 +282,15 @@ struct Ring {
     int* dead;
     int32_t* error;
     const uint8_t* src[N];
-    int64_t stride[N], rows, step;         // bytes; the matrix' rows, from one of the group's to its next
+    int64_t stride[N];                     // bytes
+    int rows, step;                        // the matrix' rows; from one of the group's to its next
     int row_bytes, stage_bytes, stages;    // (stage_bytes: of one source)
     Turn turn;
-    int64_t asked;                         // rows asked for, by the lane that asks
+    int asked;                             // rows asked for, by the lane that asks
 
-    __device__ __forceinline__ bool direct(int64_t row) const { return ANY && (row == 0 || row == rows - 1); }
-    __device__ __forceinline__ void ask(int stage, int64_t row) {
-        if (row >= rows || *static_cast<volatile int*>(dead)) return;
+    __device__ __forceinline__ bool direct(int row) const { return ANY && (row == 0 || row == rows - 1); }
+    __device__ __forceinline__ void ask(int stage, int row) {
+        if (*static_cast<volatile int*>(dead)) return;
         ++asked;
         if (direct(row)) {
             expect_bytes(&full[stage], 0);
@@ -315,24 +314,24 @@ struct Ring {
         for (int k = 0; k < N; ++k) copy_bytes(memory + (stage * N + k) * stage_bytes, from[k], bytes[k], &full[stage]);
     }
     // (one lane)
-    __device__ __forceinline__ void begin(int64_t row) {
-        for (int k = 0; k < stages; ++k) ask(k, row + k * step);
+    __device__ __forceinline__ void begin(int row) {
+        for (int k = 0; k < stages && row < rows; ++k, row += step) ask(k, row);
     }
     __device__ __forceinline__ void wait() const { wait_or_die(&full[turn.at], turn.round & 1, dead, error); }
     // Source k's row, in the present stage (or in the matrix), once waited for.
-    __device__ __forceinline__ const uint8_t* at(int k, int64_t row) const {
+    __device__ __forceinline__ const uint8_t* at(int k, int row) const {
         const uint8_t* from = src[k] + row * stride[k];
         if (direct(row)) return from;
         return memory + (turn.at * N + k) * stage_bytes + (ANY ? reinterpret_cast<uintptr_t>(from) & 15u : 0);
     }
     // All lanes have read the present stage.
-    __device__ __forceinline__ void release(int lane, int64_t row) {
-        if (lane == 0) ask(turn.at, row + stages * step);
+    __device__ __forceinline__ void release(int lane, int row) {
+        if (lane == 0 && row < rows - stages * step) ask(turn.at, row + stages * step);
     }
     // After a wait that ran out (one lane): what was asked for may still come.
     __device__ __forceinline__ void end() const {
         if (!*static_cast<volatile int*>(dead)) return;
-        for (int64_t k = asked > stages ? asked - stages : 0; k < asked; ++k)
+        for (int k = asked > stages ? asked - stages : 0; k < asked; ++k)
             wait_phase(&full[k % stages], (k / stages) & 1);
     }
 };
@@ -370,21 +369,22 @@ __global__ void __launch_bounds__(kForwardRing, 1) norm_forward_ring_kernel(cons
     __syncthreads();
     wait_for_previous_kernel();
     let_next_kernel_start();
-    int64_t row = blockIdx.x + static_cast<int64_t>(group) * gridDim.x;
+    // (threads behind the last whole group have no rows)
+    int row = group < groups ? static_cast<int>(blockIdx.x + group * gridDim.x) : static_cast<int>(a.rows);
     Ring<1, kAny> ring{memory + group * stages * stage_bytes,
                  barriers.full + group * stages,
                  &barriers.dead,
                  a.error,
                  {reinterpret_cast<const uint8_t*>(a.x)},
                  {a.ldx * static_cast<int64_t>(sizeof(T))},
-                 a.rows,
-                 static_cast<int64_t>(groups) * gridDim.x,
+                 static_cast<int>(a.rows),
+                 static_cast<int>(groups * gridDim.x),
                  row_bytes,
                  stage_bytes,
                  stages,
                  {0, 0},
                  0};
-    if (lane == 0) ring.begin(row);
+    if (lane == 0 && group < groups) ring.begin(row);
     for (int c = threadIdx.x; c < a.cols; c += kForwardRing) {
         gamma.put(c, a.gamma ? a.gamma[c] : from_f32<W>(1.f));
         beta.put(c, a.beta ? a.beta[c] : from_f32<W>(0.f));
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kForwardRing, 1) norm_forward_ring_kernel(cons
     GroupSum<1> sum{part[group], lanes, group, 0};       // (barrier 0 is free from here on)
     T* y = a.y + row * a.ldy;
     const int64_t y_step = ring.step * a.ldy;
-    for (; row < a.rows; row += ring.step, y += y_step, ring.turn.next(1, stages)) {
+    for (; row < ring.rows; row += ring.step, y += y_step, ring.turn.next(1, stages)) {
         Pair v[COLS / 2];
         {
             RowPacks<T, VEC, COLS, true> in;
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kForwardRing, 1) norm_forward_ring_kernel(cons
             if (a.rstd) a.rstd[row] = r;
         }
     }
-    if (lane == 0) ring.end();
+    if (lane == 0 && group < groups) ring.end();
 }
 
 template <typename T, typename W>
@@ -575,21 +575,22 @@ __global__ void __launch_bounds__(kBackwardRing, 1) norm_backward_ring_kernel(co
     __syncthreads();
     wait_for_previous_kernel();
     let_next_kernel_start();
-    int64_t row = blockIdx.x + static_cast<int64_t>(group) * gridDim.x;
+    // (threads behind the last whole group have no rows)
+    int row = group < groups ? static_cast<int>(blockIdx.x + group * gridDim.x) : static_cast<int>(a.rows);
     Ring<2, kAny> ring{memory + group * stages * 2 * stage_bytes,
                  barriers.full + group * stages,
                  &barriers.dead,
                  a.error,
                  {reinterpret_cast<const uint8_t*>(a.x), reinterpret_cast<const uint8_t*>(a.dy)},
                  {a.ldx * static_cast<int64_t>(sizeof(T)), a.lddy * static_cast<int64_t>(sizeof(T))},
-                 a.rows,
-                 static_cast<int64_t>(groups) * gridDim.x,
+                 static_cast<int>(a.rows),
+                 static_cast<int>(groups * gridDim.x),
                  row_bytes,
                  stage_bytes,
                  stages,
                  {0, 0},
                  0};
-    if (lane == 0) ring.begin(row);
+    if (lane == 0 && group < groups) ring.begin(row);
     const float inverse_n = 1.f / static_cast<float>(a.cols);
     GroupSum<2> sum{part[group], lanes, 1 + group, 0};
     Pair dg[kPairs], db[kPairs], gamma[kPairs];
@@ -601,12 +602,12 @@ __global__ void __launch_bounds__(kBackwardRing, 1) norm_backward_ring_kernel(co
         next_mean = a.mean[r];
         next_rstd = a.rstd[r];
     };
-    if (row < a.rows) ask(row);
+    if (row < ring.rows) ask(row);
     T* dx = a.dx ? a.dx + row * a.lddx : nullptr;
     const int64_t dx_step = a.dx ? ring.step * a.lddx : 0;
-    for (; row < a.rows; row += ring.step, dx += dx_step, ring.turn.next(1, stages)) {
+    for (; row < ring.rows; row += ring.step, dx += dx_step, ring.turn.next(1, stages)) {
         const float mu = next_mean, r = next_rstd;
-        if (row + ring.step < a.rows) ask(row + ring.step);
+        if (row < ring.rows - ring.step) ask(row + ring.step);
         Pair hat[kPairs], g[kPairs];
         {
             RowPacks<T, VEC, kLaneCols, true> x, dy;
@@ -632,7 +633,7 @@ __global__ void __launch_bounds__(kBackwardRing, 1) norm_backward_ring_kernel(co
         ring.release(lane, row);
         if (a.dx) write_dx<T, VEC, true>(hat, g, s, inverse_n, r2, dx, lane, lanes, a.cols);
     }
-    if (lane == 0) ring.end();
+    if (lane == 0 && group < groups) ring.end();
     if (!a.weights) return;
     __syncthreads();                                     // the rings have been read: their memory joins the groups
     float* const join = reinterpret_cast<float*>(memory);
@@ -765,7 +766,10 @@ norm_weight_grad_wide_kernel(const BackwardArgs<T, W> a, W* dgamma, W* dbeta) {
 
 // ---- launches ----------------------------------------------------------------------
 
-// Lanes that keep a row of `cols` columns.
+// Lanes of a ring's group: whole warps, `each` columns a lane.
+int ring_lanes(int cols, int each) { return ((cols + each - 1) / each + 31) / 32 * 32; }
+
+// Lanes that keep a row of `cols` columns in the register kernels.
 int lanes_for(int64_t cols) {
     int lanes = 32;
     while (static_cast<int64_t>(lanes) * kLaneCols < cols) lanes *= 2;
@@ -788,7 +792,8 @@ gemm_status_t forward_rows(const ForwardArgs<T, W>& a, int sms, void* stream) {
 int ring_stages(int cols, int vec, int64_t row_bytes, int sources, int lanes, int threads, int64_t fixed, int64_t rows,
                 int sms) {
     const int groups = threads / lanes;
-    if (groups == 0 || row_bytes < 512 || cols % vec != 0 || rows < int64_t{2} * sms * groups) return 0;
+    if (groups == 0 || row_bytes < 512 || cols % vec != 0 || rows < int64_t{2} * sms * groups || rows > kRingRows)
+        return 0;
     int64_t stages = (kRingShared - fixed) / (row_bytes * sources * groups);
     if (stages > kRingSlots / groups) stages = kRingSlots / groups;
     return stages < 2 ? 0 : static_cast<int>(stages);
@@ -797,10 +802,11 @@ int ring_stages(int cols, int vec, int64_t row_bytes, int sources, int lanes, in
 template <typename T, typename W, int VEC>
 gemm_status_t forward_vec(const ForwardArgs<T, W>& a, int sms, void* stream) {
     ForwardArgs<T, W> b = a;
-    const bool half = VEC > 1 && b.lanes > 32;   // 32 columns a lane (single elements take more registers)
-    if (half) b.lanes /= 2;
+    const bool half = VEC > 1 && a.cols > 512;   // 32 columns a lane (single elements take more registers)
+    const int each = half ? 32 : 16;
+    b.lanes = ring_lanes(a.cols, each);
     const int64_t stage = ring_stage_bytes(a.cols * static_cast<int>(sizeof(T)), VEC == 1);
-    const int64_t weights = int64_t{2} * a.lanes * kLaneCols * static_cast<int64_t>(sizeof(W));
+    const int64_t weights = int64_t{2} * b.lanes * each * static_cast<int64_t>(sizeof(W));
     const int stages = ring_stages(a.cols, VEC, stage, 1, b.lanes, kForwardRing, weights, a.rows, sms);
     if (stages > 0) {
         const size_t smem = static_cast<size_t>(kForwardRing / b.lanes * stages * stage + weights);
@@ -853,13 +859,15 @@ int64_t backward_blocks(int64_t rows, int lanes, int sms) {
 
 template <typename T, typename W, int VEC>
 gemm_status_t backward_vec(const BackwardArgs<T, W>& a, int blocks, int sms, void* stream) {
+    BackwardArgs<T, W> b = a;
+    b.lanes = ring_lanes(a.cols, kLaneCols);
     const int64_t stage = ring_stage_bytes(a.cols * static_cast<int>(sizeof(T)), VEC == 1);
-    const int stages = ring_stages(a.cols, VEC, stage, 2, a.lanes, kBackwardRing, 0, a.rows, sms);
+    const int stages = ring_stages(a.cols, VEC, stage, 2, b.lanes, kBackwardRing, 0, a.rows, sms);
     if (stages > 0) {
-        const size_t ring = static_cast<size_t>(2 * (kBackwardRing / a.lanes) * stages * stage);
-        const size_t join = static_cast<size_t>(a.lanes) * kLaneCols * 2 * sizeof(float);
+        const size_t ring = static_cast<size_t>(2 * (kBackwardRing / b.lanes) * stages * stage);
+        const size_t join = static_cast<size_t>(b.lanes) * kLaneCols * 2 * sizeof(float);
         return launch(norm_backward_ring_kernel<T, W, VEC>, blocks, kBackwardRing, ring > join ? ring : join, stream, 1,
-                      a, stages);
+                      b, stages);
     }
     if (a.lanes <= 512) return backward_rows<T, W, VEC, 512, false>(a, blocks, stream);
     return backward_rows<T, W, VEC, 1024, true>(a, blocks, stream);
