@@ -662,9 +662,20 @@ norm_weight_join_kernel(const float* partial, int blocks, int cols, W* dgamma, W
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int64_t c = static_cast<int64_t>(blockIdx.x % tiles) * 32 + lane;
     float s = 0.f;
-    if (c < cols)
-        for (int b = warp; b < blocks; b += kThreads / 32)
-            s += partial[(static_cast<int64_t>(which) * blocks + b) * cols + c];
+    if (c < cols) {
+        constexpr int kAhead = 8;            // loads in flight together: the sums are short chains of them
+        const float* at = partial + static_cast<int64_t>(which) * blocks * cols + c;
+        for (int b = warp; b < blocks; b += kAhead * (kThreads / 32)) {
+            float v[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int row = b + k * (kThreads / 32);
+                v[k] = row < blocks ? at[static_cast<int64_t>(row) * cols] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) s += v[k];
+        }
+    }
     part[warp][lane] = s;
     __syncthreads();
     if (warp != 0 || c >= cols) return;

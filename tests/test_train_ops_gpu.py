@@ -304,6 +304,43 @@ def test_embedding_one_token_many_times(gemm_lib):
             assert torch.equal(dtable, want)
 
 
+@pytest.mark.parametrize("dim,scale_up", [(8, 1), (4096, 1), (8192, 1), (8192, 2), (4095, 1)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embedding_runs_of_every_length(gemm_lib, dim, scale_up, accumulate):
+    """Tokens that come 1 to 70 times each, in several orders of the lengths (so that runs of every length begin and
+    end at every place of the kernels' chunks, whose size depends on tokens and columns), exact in small integers."""
+    lengths = np.concatenate([np.arange(1, 35), np.arange(70, 1, -3), [8, 8, 16, 7, 9, 32, 31, 33, 1, 1, 64, 65, 2]])
+    lengths = np.tile(lengths, scale_up)
+    vocab = len(lengths) + 2
+    rng = np.random.default_rng(dim + scale_up)
+    with gemm_lib.EmbedPlan(vocab, dim, int(lengths.sum()) + 5, "bf16", grad="f32") as plan:
+        for _ in range(3):
+            ids = np.concatenate([np.repeat(np.arange(len(lengths)) + 1, lengths), [-1] * 5])
+            rng.shuffle(ids)
+            rng.shuffle(lengths)
+            ids = torch.as_tensor(ids).cuda()
+            dout = torch.randint(-2, 3, (len(ids), dim), device="cuda").bfloat16()
+            dtable = torch.randint(-2, 3, (vocab, dim), device="cuda").float()
+            want = dtable.clone() if accumulate else torch.zeros_like(dtable)
+            there = ids >= 0
+            want.index_add_(0, ids[there], dout[there].float())
+            plan.backward(ids, dout, dtable, accumulate=accumulate)
+            assert torch.equal(dtable, want)
+
+
+@pytest.mark.parametrize("n", [1000, 4097, 9000, 33000, 70001])
+def test_embedding_sorts_any_number_of_tokens(gemm_lib, n):
+    """From one sorting block to several tiles of a cluster's blocks; 1 to 4 passes over the ids' digits."""
+    for vocab in (300, 70000, 1 << 20):
+        gen = torch.Generator(device="cuda").manual_seed(n)
+        ids = torch.randint(vocab, (n,), generator=gen, device="cuda")
+        dout = torch.randint(-2, 3, (n, 8), generator=gen, device="cuda").float()
+        dtable = torch.full((vocab, 8), 7.0, device="cuda")
+        with gemm_lib.EmbedPlan(vocab, 8, n, "f32") as plan:
+            plan.backward(ids, dout, dtable)
+        assert torch.equal(dtable, torch.zeros_like(dtable).index_add_(0, ids, dout))
+
+
 # ---------------------------------------------------------------- distillation
 
 DISTILL_SIZES = [(1, 1, 1), (1, 8, 3), (3, 7, 7), (5, 100, 1), (2, 1000, 64), (40, 333, 20), (3, 4096, 200), (2, 8200, 33),
