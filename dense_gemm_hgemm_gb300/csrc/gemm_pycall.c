@@ -210,7 +210,7 @@ typedef struct {
     vectorcallfunc vectorcall;
 } TrainCall;
 
-static PyObject *s_dtype, *s_is_cuda, *s_shape, *s_stride;
+static PyObject *s_dtype, *s_is_cuda, *s_shape, *s_stride, *s_is_contiguous;
 
 /* Address of a CUDA tensor of `dims` dimensions with its shape and strides; 0 where
  * it is something else. */
@@ -220,14 +220,21 @@ static int tensor_of(PyObject* t, int dims, void** ptr, int64_t* shape, int64_t*
     Py_XDECREF(r);
     if (!cuda || !address_of(t, s_data_ptr, 1, ptr)) return 0;
     PyObject* a = PyObject_GetAttr(t, s_shape);
-    PyObject* b = a == NULL ? NULL : PyObject_VectorcallMethod(s_stride, &t, 1, NULL);
-    int ok = a != NULL && b != NULL && PyTuple_Check(a) && PyTuple_Check(b) &&
-             PyTuple_GET_SIZE(a) == dims && PyTuple_GET_SIZE(b) == dims;
-    for (int i = 0; ok && i < dims; ++i) {
-        shape[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(a, i));
-        stride[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(b, i));
-    }
+    int ok = a != NULL && PyTuple_Check(a) && PyTuple_GET_SIZE(a) == dims;
+    for (int i = 0; ok && i < dims; ++i) shape[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(a, i));
     Py_XDECREF(a);
+    if (!ok) return 0;
+    /* (the usual answer, for less than the strides) */
+    PyObject* c = PyObject_VectorcallMethod(s_is_contiguous, &t, 1, NULL);
+    Py_XDECREF(c);
+    if (c == Py_True) {
+        stride[dims - 1] = 1;
+        if (dims == 2) stride[0] = shape[1];
+        return !PyErr_Occurred();
+    }
+    PyObject* b = c == NULL ? NULL : PyObject_VectorcallMethod(s_stride, &t, 1, NULL);
+    ok = b != NULL && PyTuple_Check(b) && PyTuple_GET_SIZE(b) == dims;
+    for (int i = 0; ok && i < dims; ++i) stride[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(b, i));
     Py_XDECREF(b);
     return ok && !PyErr_Occurred();
 }
@@ -504,8 +511,9 @@ PyMODINIT_FUNC PyInit__gemm_pycall(void) {
     s_is_cuda = PyUnicode_InternFromString("is_cuda");
     s_shape = PyUnicode_InternFromString("shape");
     s_stride = PyUnicode_InternFromString("stride");
+    s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
     if (s_data_ptr == NULL || s_cuda_stream == NULL || s_dtype == NULL || s_is_cuda == NULL || s_shape == NULL ||
-        s_stride == NULL || PyType_Ready(&RunnerType) < 0 || PyType_Ready(&TrainCallType) < 0)
+        s_stride == NULL || s_is_contiguous == NULL || PyType_Ready(&RunnerType) < 0 || PyType_Ready(&TrainCallType) < 0)
         return NULL;
     PyObject* m = PyModule_Create(&module);
     if (m == NULL) return NULL;

@@ -2,10 +2,15 @@
 // reductions, the launch (programmatic dependent launch on the caller's stream)
 // and the host-side checks.
 #pragma once
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <atomic>
+#include <mutex>
 
 #include "gemm_train.h"
 
@@ -419,34 +424,80 @@ inline bool rows_aligned(const void* p, int64_t ld, int bytes) {
     return aligned(p, 16) && (ld * bytes) % 16 == 0;
 }
 
+// Where a call's kernels go: the caller's stream, on the plan's device.
+struct Queue {
+    void* stream;
+    int device;
+};
+
+// cuLaunchKernelEx, which with a kernel's function handle costs less host time than
+// the runtime's launch of its stub.
+inline PFN_cuLaunchKernelEx_v11060 driver_launch() {
+    static PFN_cuLaunchKernelEx_v11060 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuLaunchKernelEx", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuLaunchKernelEx_v11060>(p);
+    });
+    return fn;
+}
+
+// The kernel's function handle on the device (which is current), looked up once.
+template <auto Kernel>
+CUfunction function_of(int device) {
+    constexpr int kDevices = 16;
+    static std::atomic<CUfunction> known[kDevices];
+    CUfunction fn = device >= 0 && device < kDevices ? known[device].load(std::memory_order_acquire) : nullptr;
+    if (!fn) {
+        cudaFunction_t f = nullptr;
+        if (cudaGetFuncBySymbol(&f, reinterpret_cast<const void*>(Kernel)) != cudaSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        fn = reinterpret_cast<CUfunction>(f);
+        if (device >= 0 && device < kDevices) known[device].store(fn, std::memory_order_release);
+    }
+    return fn;
+}
+
+template <typename T> struct Same { using type = T; };
+
+template <typename... P>
+CUresult fire(void (*)(P...), const CUlaunchConfig& cfg, CUfunction fn, typename Same<P>::type... args) {
+    void* pointers[] = {static_cast<void*>(&args)...};
+    return driver_launch()(&cfg, fn, pointers, nullptr);
+}
+
 // Launch with programmatic dependent launch: the kernel starts its first
 // instructions while the stream's previous kernel ends, and calls
 // wait_for_previous_kernel before it touches memory.
-template <typename... P, typename... A>
-gemm_status_t launch(void (*kernel)(P...), int64_t grid, int block, size_t smem, void* stream,
-                     int cluster, A... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(static_cast<unsigned>(block));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+template <auto Kernel, typename... A>
+gemm_status_t launch(int64_t grid, int block, size_t smem, Queue queue, int cluster, A... args) {
+    const CUfunction fn = function_of<Kernel>(queue.device);
+    if (!fn || !driver_launch()) return GEMM_ERR_LAUNCH;
+    CUlaunchAttribute attr[2];
+    attr[0].id = CU_LAUNCH_ATTRIBUTE_PROGRAMMATIC_STREAM_SERIALIZATION;
+    attr[0].value.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = CU_LAUNCH_ATTRIBUTE_CLUSTER_DIMENSION;
+    attr[1].value.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].value.clusterDim.y = 1;
+    attr[1].value.clusterDim.z = 1;
+    CUlaunchConfig cfg = {};
+    cfg.gridDimX = static_cast<unsigned>(grid);
+    cfg.gridDimY = cfg.gridDimZ = 1;
+    cfg.blockDimX = static_cast<unsigned>(block);
+    cfg.blockDimY = cfg.blockDimZ = 1;
+    cfg.sharedMemBytes = static_cast<unsigned>(smem);
+    cfg.hStream = static_cast<CUstream>(queue.stream);
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cluster > 1) {
-        attr[1].id = cudaLaunchAttributeClusterDimension;
-        attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-        attr[1].val.clusterDim.y = 1;
-        attr[1].val.clusterDim.z = 1;
-        cfg.numAttrs = 2;
-    }
-    if (cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) != cudaSuccess) {
-        cudaGetLastError();
-        return GEMM_ERR_LAUNCH;
-    }
-    return GEMM_OK;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    CUresult r = fire(Kernel, cfg, fn, args...);
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaSetDevice(queue.device) == cudaSuccess)
+        r = fire(Kernel, cfg, fn, args...);              // a thread without a current context
+    return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
 // Calls f with a value of the element type.

@@ -923,23 +923,23 @@ bool is_short(int64_t vocab) {
 }
 
 template <typename T, int MODE>
-gemm_status_t run_short(const Args<T>& a, int64_t rows, void* stream) {
+gemm_status_t run_short(const Args<T>& a, int64_t rows, Queue queue) {
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     const int lanes = (a.vocab + VEC - 1 + VEC - 1) / VEC;        // packs of a row, wherever it begins
     const int64_t blocks = (rows + kWarps - 1) / kWarps;
     const size_t smem = kWarps * kEntryWords * sizeof(float) * ((a.teacher.top + 3) / 4 * 4);
-    if (lanes <= 2 * 32) return launch(distill_short_kernel<T, MODE, 2>, blocks, kThreads, smem, stream, 1, a, rows);
-    if (lanes <= 4 * 32) return launch(distill_short_kernel<T, MODE, 4>, blocks, kThreads, smem, stream, 1, a, rows);
-    if (lanes <= 8 * 32) return launch(distill_short_kernel<T, MODE, 8>, blocks, kThreads, smem, stream, 1, a, rows);
-    return launch(distill_short_kernel<T, MODE, 16>, blocks, kThreads, smem, stream, 1, a, rows);
+    if (lanes <= 2 * 32) return launch<distill_short_kernel<T, MODE, 2>>(blocks, kThreads, smem, queue, 1, a, rows);
+    if (lanes <= 4 * 32) return launch<distill_short_kernel<T, MODE, 4>>(blocks, kThreads, smem, queue, 1, a, rows);
+    if (lanes <= 8 * 32) return launch<distill_short_kernel<T, MODE, 8>>(blocks, kThreads, smem, queue, 1, a, rows);
+    return launch<distill_short_kernel<T, MODE, 16>>(blocks, kThreads, smem, queue, 1, a, rows);
 }
 
 template <typename T, int MODE>
-gemm_status_t run(Args<T> a, int64_t rows, int sms, void* stream) {
-    if (is_short<T>(a.vocab)) return run_short<T, MODE>(a, rows, stream);
+gemm_status_t run(Args<T> a, int64_t rows, int sms, Queue queue) {
+    if (is_short<T>(a.vocab)) return run_short<T, MODE>(a, rows, queue);
     cut_row(a, rows, sms, MODE == kBackward ? INT32_MAX : kMaxCluster);
     const size_t smem = (a.teacher.top * 12 + 15) / 16 * 16 + a.piece * sizeof(T) + 32;
-    return launch(distill_kernel<T, MODE>, rows * a.pieces, kThreads, smem, stream,
+    return launch<distill_kernel<T, MODE>>(rows * a.pieces, kThreads, smem, queue,
                   MODE == kBackward ? 1 : a.pieces, a);
 }
 
@@ -968,11 +968,11 @@ gemm_status_t prepare() {
 }
 
 template <typename T, int MODE>
-gemm_status_t run_stream(Args<T> a, const StreamShape& shape, int64_t rows, void* stream) {
+gemm_status_t run_stream(Args<T> a, const StreamShape& shape, int64_t rows, Queue queue) {
     a.piece = shape.piece;
     a.pieces = shape.pieces;
     const int64_t clusters = rows < shape.clusters ? rows : shape.clusters;
-    return launch(distill_stream_kernel<T, MODE>, clusters * a.pieces, kStreamThreads, shape.smem, stream,
+    return launch<distill_stream_kernel<T, MODE>>(clusters * a.pieces, kStreamThreads, shape.smem, queue,
                   a.pieces, a, rows, shape.stages, shape.slots);
 }
 
@@ -1024,8 +1024,8 @@ StreamShape stream_shape(int64_t vocab, int64_t max_top) {
 }
 
 template <typename T>
-gemm_status_t run_forward_wide(const Args<T>& a, int64_t rows, void* stream) {
-    return launch(distill_forward_wide_kernel<T>, rows, kThreads, a.teacher.top * 12, stream, 1, a);
+gemm_status_t run_forward_wide(const Args<T>& a, int64_t rows, Queue queue) {
+    return launch<distill_forward_wide_kernel<T>>(rows, kThreads, a.teacher.top * 12, queue, 1, a);
 }
 
 // Whether a cluster can hold a row.
@@ -1116,6 +1116,7 @@ gemm_status_t gemm_distill_forward(gemm_distill_plan_t p, int64_t rows, const vo
                                    float* loss, float* lse, void* stream) {
     const gemm_status_t st = gbt::check_call(p, rows, logits, ldl, teacher, temperature);
     if (st != GEMM_OK) return st;
+    const gbt::Queue queue{stream, p->device};
     if (rows > 0 && (!loss || !lse)) return GEMM_ERR_INVALID_ARG;
     if (!gbt::aligned(loss, 4) || !gbt::aligned(lse, 4)) return GEMM_ERR_ALIGNMENT;
     if (rows == 0) return GEMM_OK;
@@ -1125,9 +1126,9 @@ gemm_status_t gemm_distill_forward(gemm_distill_plan_t p, int64_t rows, const vo
         a.loss = loss;
         a.lse = lse;
         if (p->forward.clusters > 0 && rows >= p->forward.clusters)
-            return gbt::run_stream<T, gbt::kForward>(a, p->forward, rows, stream);
-        return gbt::fits(p->vocab, sizeof(T)) ? gbt::run<T, gbt::kForward>(a, rows, p->num_sms, stream)
-                                              : gbt::run_forward_wide(a, rows, stream);
+            return gbt::run_stream<T, gbt::kForward>(a, p->forward, rows, queue);
+        return gbt::fits(p->vocab, sizeof(T)) ? gbt::run<T, gbt::kForward>(a, rows, p->num_sms, queue)
+                                              : gbt::run_forward_wide(a, rows, queue);
     });
 }
 
@@ -1137,6 +1138,7 @@ gemm_status_t gemm_distill_backward(gemm_distill_plan_t p, int64_t rows, const v
                                     int64_t ldd, void* stream) {
     const gemm_status_t st = gbt::check_call(p, rows, logits, ldl, teacher, temperature);
     if (st != GEMM_OK) return st;
+    const gbt::Queue queue{stream, p->device};
     if (rows > 0 && (!lse || !dlogits || ldd < p->vocab)) return GEMM_ERR_INVALID_ARG;
     if (!gbt::aligned(lse, 4) || !gbt::aligned(dloss, 4) ||
         !gbt::aligned(dlogits, gbt::elem_bytes(p->elem)))
@@ -1149,7 +1151,7 @@ gemm_status_t gemm_distill_backward(gemm_distill_plan_t p, int64_t rows, const v
         a.dloss = dloss;
         a.dlogits = static_cast<T*>(dlogits);
         a.ldd = ldd;
-        return gbt::run<T, gbt::kBackward>(a, rows, p->num_sms, stream);
+        return gbt::run<T, gbt::kBackward>(a, rows, p->num_sms, queue);
     });
 }
 
@@ -1160,6 +1162,7 @@ gemm_status_t gemm_distill_forward_backward(gemm_distill_plan_t p, int64_t rows,
                                             void* dlogits, int64_t ldd, void* stream) {
     const gemm_status_t st = gbt::check_call(p, rows, logits, ldl, teacher, temperature);
     if (st != GEMM_OK) return st;
+    const gbt::Queue queue{stream, p->device};
     if (rows > 0 && (!loss || !lse || !dlogits || ldd < p->vocab)) return GEMM_ERR_INVALID_ARG;
     if (!gbt::aligned(loss, 4) || !gbt::aligned(lse, 4) || !gbt::aligned(dloss, 4) ||
         !gbt::aligned(dlogits, gbt::elem_bytes(p->elem)))
@@ -1174,10 +1177,10 @@ gemm_status_t gemm_distill_forward_backward(gemm_distill_plan_t p, int64_t rows,
         a.dlogits = static_cast<T*>(dlogits);
         a.ldd = ldd;
         if (p->both.clusters > 0 && rows >= p->both.clusters)
-            return gbt::run_stream<T, gbt::kBoth>(a, p->both, rows, stream);
-        if (gbt::fits(p->vocab, sizeof(T))) return gbt::run<T, gbt::kBoth>(a, rows, p->num_sms, stream);
-        const gemm_status_t first = gbt::run_forward_wide(a, rows, stream);
-        return first == GEMM_OK ? gbt::run<T, gbt::kBackward>(a, rows, p->num_sms, stream) : first;
+            return gbt::run_stream<T, gbt::kBoth>(a, p->both, rows, queue);
+        if (gbt::fits(p->vocab, sizeof(T))) return gbt::run<T, gbt::kBoth>(a, rows, p->num_sms, queue);
+        const gemm_status_t first = gbt::run_forward_wide(a, rows, queue);
+        return first == GEMM_OK ? gbt::run<T, gbt::kBackward>(a, rows, p->num_sms, queue) : first;
     });
 }
 

@@ -95,7 +95,7 @@ embed_forward_kernel(const LookupParams p, const T* __restrict__ table, T* __res
 }
 
 template <typename T, int VEC>
-gemm_status_t lookup(LookupParams p, int sms, const T* table, T* out, void* stream) {
+gemm_status_t lookup(LookupParams p, int sms, const T* table, T* out, Queue queue) {
     constexpr int PACKS = 2;
     const int64_t packs = (static_cast<int64_t>(p.dim) + VEC - 1) / VEC;
     p.lanes = 8;
@@ -103,9 +103,9 @@ gemm_status_t lookup(LookupParams p, int sms, const T* table, T* out, void* stre
     const int groups = kThreads / p.lanes;
     // four tokens a group where that leaves enough blocks to fill the GPU
     if (p.tokens >= int64_t{4} * 8 * sms * groups)
-        return launch(embed_forward_kernel<T, VEC, PACKS, 4>, (p.tokens + 4 * groups - 1) / (4 * groups), kThreads,
-                      0, stream, 1, p, table, out);
-    return launch(embed_forward_kernel<T, VEC, PACKS, 1>, (p.tokens + groups - 1) / groups, kThreads, 0, stream, 1,
+        return launch<embed_forward_kernel<T, VEC, PACKS, 4>>((p.tokens + 4 * groups - 1) / (4 * groups), kThreads,
+                      0, queue, 1, p, table, out);
+    return launch<embed_forward_kernel<T, VEC, PACKS, 1>>((p.tokens + groups - 1) / groups, kThreads, 0, queue, 1,
                   p, table, out);
 }
 
@@ -617,12 +617,12 @@ int64_t most_chunks(int64_t tokens, int slices, int sms) {
 int slice_columns(int elem, bool aligned) { return aligned ? 32 * 16 / elem : 32 * 4; }
 
 template <typename T, typename G, int VEC, int REP>
-gemm_status_t sum_rows(SumParams s, int sms, const T* dout, G* table, void* stream) {
+gemm_status_t sum_rows(SumParams s, int sms, const T* dout, G* table, Queue queue) {
     const int64_t units = s.chunks * s.slices, warps = kThreads / 32;
     const gemm_status_t st =
-        launch(embed_sum_kernel<T, G, VEC, REP>, (units + warps - 1) / warps, kThreads, 0, stream, 1, s, dout, table);
+        launch<embed_sum_kernel<T, G, VEC, REP>>((units + warps - 1) / warps, kThreads, 0, queue, 1, s, dout, table);
     if (st != GEMM_OK || s.tokens <= s.chunk) return st;     // (no row is longer than a chunk)
-    return launch(embed_join_kernel<G, (VEC > 1)>, 4 * sms, kThreads, 0, stream, 1, s, table);
+    return launch<embed_join_kernel<G, (VEC > 1)>>(4 * sms, kThreads, 0, queue, 1, s, table);
 }
 
 }  // namespace
@@ -703,6 +703,7 @@ gemm_status_t gemm_embed_forward(gemm_embed_plan_t p, int64_t tokens, const void
         return GEMM_ERR_ALIGNMENT;
     const gemm_status_t st = gbt::check_device(p->device);
     if (st != GEMM_OK || tokens == 0) return st;
+    const gbt::Queue queue{stream, p->device};
     const gbt::LookupParams q{ids,  static_cast<int>(id_type), padding, tokens, p->vocab, ldt, ldo, scale,
                               static_cast<int>(p->dim), 0, p->error_word};
     const bool vec = gbt::rows_aligned(table, ldt, e) && gbt::rows_aligned(out, ldo, e);
@@ -711,8 +712,8 @@ gemm_status_t gemm_embed_forward(gemm_embed_plan_t p, int64_t tokens, const void
         constexpr int kVec = 16 / static_cast<int>(sizeof(T));
         const T* from = static_cast<const T*>(table);
         T* to = static_cast<T*>(out);
-        return vec ? gbt::lookup<T, kVec>(q, p->num_sms, from, to, stream)
-                   : gbt::lookup<T, 1>(q, p->num_sms, from, to, stream);
+        return vec ? gbt::lookup<T, kVec>(q, p->num_sms, from, to, queue)
+                   : gbt::lookup<T, 1>(q, p->num_sms, from, to, queue);
     });
 }
 
@@ -730,6 +731,7 @@ gemm_status_t gemm_embed_backward(gemm_embed_plan_t p, int64_t tokens, const voi
         return GEMM_ERR_ALIGNMENT;
     gemm_status_t st = gbt::check_device(p->device);
     if (st != GEMM_OK || (tokens == 0 && accumulate)) return st;
+    const gbt::Queue queue{stream, p->device};
     const int g = gbt::elem_bytes(p->grad_elem);
 
     gbt::SortParams q = {};
@@ -766,7 +768,7 @@ gemm_status_t gemm_embed_backward(gemm_embed_plan_t p, int64_t tokens, const voi
             ++q.fill_shift;
         grid += int64_t{1} << q.fill_shift;
     }
-    st = gbt::launch(gbt::embed_sort_kernel, grid, gbt::kSortThreads, sizeof(gbt::SortShared), stream, ranks, q,
+    st = gbt::launch<gbt::embed_sort_kernel>(grid, gbt::kSortThreads, sizeof(gbt::SortShared), queue, ranks, q,
                      ranks);
     if (st != GEMM_OK || tokens == 0) return st;
 
@@ -796,8 +798,8 @@ gemm_status_t gemm_embed_backward(gemm_embed_plan_t p, int64_t tokens, const voi
             using G = decltype(v);
             const T* d = static_cast<const T*>(dout);
             G* w = static_cast<G*>(dtable);
-            return vec ? gbt::sum_rows<T, G, kVec, 1>(s, p->num_sms, d, w, stream)
-                       : gbt::sum_rows<T, G, 1, 4>(s, p->num_sms, d, w, stream);
+            return vec ? gbt::sum_rows<T, G, kVec, 1>(s, p->num_sms, d, w, queue)
+                       : gbt::sum_rows<T, G, 1, 4>(s, p->num_sms, d, w, queue);
         };
         return p->grad_elem == GEMM_ELEM_F32 ? run(float()) : run(t);
     });

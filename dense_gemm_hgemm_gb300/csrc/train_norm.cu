@@ -790,12 +790,11 @@ int lanes_for(int64_t cols) {
 bool in_registers(int64_t cols) { return cols <= static_cast<int64_t>(kMaxLanes) * kLaneCols; }
 
 template <typename T, typename W, int VEC, int BLOCK, bool KEEP>
-gemm_status_t forward_rows(const ForwardArgs<T, W>& a, int sms, void* stream) {
-    const auto kernel = norm_forward_kernel<T, W, VEC, BLOCK, KEEP>;
+gemm_status_t forward_rows(const ForwardArgs<T, W>& a, int sms, Queue queue) {
     const int groups = BLOCK / a.lanes;
     const int64_t blocks = (a.rows + groups - 1) / groups;
     const int64_t most = static_cast<int64_t>(sms) * (2048 / BLOCK);
-    return launch(kernel, blocks < most ? blocks : most, BLOCK, 0, stream, 1, a);
+    return launch<norm_forward_kernel<T, W, VEC, BLOCK, KEEP>>(blocks < most ? blocks : most, BLOCK, 0, queue, 1, a);
 }
 
 // Stages of a group's ring whose block also needs `fixed` bytes; 0 where rings do not suit:
@@ -811,7 +810,7 @@ int ring_stages(int cols, int vec, int64_t row_bytes, int sources, int lanes, in
 }
 
 template <typename T, typename W, int VEC>
-gemm_status_t forward_vec(const ForwardArgs<T, W>& a, int sms, void* stream) {
+gemm_status_t forward_vec(const ForwardArgs<T, W>& a, int sms, Queue queue) {
     ForwardArgs<T, W> b = a;
     const bool half = VEC > 1 && a.cols > 512;   // 32 columns a lane (single elements take more registers)
     const int each = half ? 32 : 16;
@@ -822,21 +821,20 @@ gemm_status_t forward_vec(const ForwardArgs<T, W>& a, int sms, void* stream) {
     if (stages > 0) {
         const size_t smem = static_cast<size_t>(kForwardRing / b.lanes * stages * stage + weights);
         if constexpr (VEC > 1) {
-            if (half) return launch(norm_forward_ring_kernel<T, W, VEC, 32>, sms, kForwardRing, smem, stream, 1, b, stages);
+            if (half) return launch<norm_forward_ring_kernel<T, W, VEC, 32>>(sms, kForwardRing, smem, queue, 1, b, stages);
         }
-        return launch(norm_forward_ring_kernel<T, W, VEC, 16>, sms, kForwardRing, smem, stream, 1, b, stages);
+        return launch<norm_forward_ring_kernel<T, W, VEC, 16>>(sms, kForwardRing, smem, queue, 1, b, stages);
     }
-    if (a.lanes <= 256) return forward_rows<T, W, VEC, 256, true>(a, sms, stream);
-    if (a.lanes == 512) return forward_rows<T, W, VEC, 512, true>(a, sms, stream);
-    return forward_rows<T, W, VEC, 1024, false>(a, sms, stream);
+    if (a.lanes <= 256) return forward_rows<T, W, VEC, 256, true>(a, sms, queue);
+    if (a.lanes == 512) return forward_rows<T, W, VEC, 512, true>(a, sms, queue);
+    return forward_rows<T, W, VEC, 1024, false>(a, sms, queue);
 }
 
 template <typename T, typename W, int VEC, int BLOCK, bool SHARED>
-gemm_status_t backward_rows(const BackwardArgs<T, W>& a, int blocks, void* stream) {
-    const auto kernel = norm_backward_kernel<T, W, VEC, BLOCK, SHARED>;
+gemm_status_t backward_rows(const BackwardArgs<T, W>& a, int blocks, Queue queue) {
     // (SHARED keeps its sums there whether they are wanted or not)
     const size_t smem = SHARED || a.weights ? static_cast<size_t>(a.lanes) * kLaneCols * 2 * sizeof(float) : 0;
-    return launch(kernel, blocks, BLOCK, smem, stream, 1, a);
+    return launch<norm_backward_kernel<T, W, VEC, BLOCK, SHARED>>(blocks, BLOCK, smem, queue, 1, a);
 }
 
 // Lets the kernels have as much shared memory as their largest launch asks for.
@@ -869,7 +867,7 @@ int64_t backward_blocks(int64_t rows, int lanes, int sms) {
 }
 
 template <typename T, typename W, int VEC>
-gemm_status_t backward_vec(const BackwardArgs<T, W>& a, int blocks, int sms, void* stream) {
+gemm_status_t backward_vec(const BackwardArgs<T, W>& a, int blocks, int sms, Queue queue) {
     BackwardArgs<T, W> b = a;
     b.lanes = ring_lanes(a.cols, kLaneCols);
     const int64_t stage = ring_stage_bytes(a.cols * static_cast<int>(sizeof(T)), VEC == 1);
@@ -877,11 +875,11 @@ gemm_status_t backward_vec(const BackwardArgs<T, W>& a, int blocks, int sms, voi
     if (stages > 0) {
         const size_t ring = static_cast<size_t>(2 * (kBackwardRing / b.lanes) * stages * stage);
         const size_t join = static_cast<size_t>(b.lanes) * kLaneCols * 2 * sizeof(float);
-        return launch(norm_backward_ring_kernel<T, W, VEC>, blocks, kBackwardRing, ring > join ? ring : join, stream, 1,
+        return launch<norm_backward_ring_kernel<T, W, VEC>>(blocks, kBackwardRing, ring > join ? ring : join, queue, 1,
                       b, stages);
     }
-    if (a.lanes <= 512) return backward_rows<T, W, VEC, 512, false>(a, blocks, stream);
-    return backward_rows<T, W, VEC, 1024, true>(a, blocks, stream);
+    if (a.lanes <= 512) return backward_rows<T, W, VEC, 512, false>(a, blocks, queue);
+    return backward_rows<T, W, VEC, 1024, true>(a, blocks, queue);
 }
 
 // Calls f with values of the plan's element and weight types.
@@ -954,6 +952,7 @@ gemm_status_t gemm_norm_forward(gemm_norm_plan_t p, int64_t rows, const void* x,
         return GEMM_ERR_ALIGNMENT;
     const gemm_status_t st = gbt::check_device(p->device);
     if (st != GEMM_OK || rows == 0) return st;
+    const gbt::Queue queue{stream, p->device};
     return gbt::with_types(p, [&](auto t, auto v) {
         using T = decltype(t);
         using W = decltype(v);
@@ -962,12 +961,12 @@ gemm_status_t gemm_norm_forward(gemm_norm_plan_t p, int64_t rows, const void* x,
                                        p->error_word, ldx, ldy, rows, eps, static_cast<int>(p->cols),
                                        gbt::lanes_for(p->cols)};
         if (!gbt::in_registers(p->cols))
-            return gbt::launch(gbt::norm_forward_wide_kernel<T, W>, rows, gbt::kThreads, 0, stream, 1, a);
+            return gbt::launch<gbt::norm_forward_wide_kernel<T, W>>(rows, gbt::kThreads, 0, queue, 1, a);
         const bool vec = gbt::rows_aligned(x, ldx, e) && gbt::rows_aligned(y, ldy, e) &&
                          gbt::aligned(gamma, 16) && gbt::aligned(beta, 16);
         constexpr int kVec = 16 / static_cast<int>(sizeof(T));
-        return vec ? gbt::forward_vec<T, W, kVec>(a, p->num_sms, stream)
-                   : gbt::forward_vec<T, W, 1>(a, p->num_sms, stream);
+        return vec ? gbt::forward_vec<T, W, kVec>(a, p->num_sms, queue)
+                   : gbt::forward_vec<T, W, 1>(a, p->num_sms, queue);
     });
 }
 
@@ -986,6 +985,7 @@ gemm_status_t gemm_norm_backward(gemm_norm_plan_t p, int64_t rows, const void* x
         return GEMM_ERR_ALIGNMENT;
     gemm_status_t st = gbt::check_device(p->device);
     if (st != GEMM_OK) return st;
+    const gbt::Queue queue{stream, p->device};
     return gbt::with_types(p, [&](auto t, auto v) {
         using T = decltype(t);
         using W = decltype(v);
@@ -1000,10 +1000,10 @@ gemm_status_t gemm_norm_backward(gemm_norm_plan_t p, int64_t rows, const void* x
         if (!gbt::in_registers(p->cols)) {
             // (the weight's gradients first: dx may overwrite dy or x)
             if (a.weights)
-                s = gbt::launch(gbt::norm_weight_grad_wide_kernel<T, W>, tiles, gbt::kThreads, 0, stream,
+                s = gbt::launch<gbt::norm_weight_grad_wide_kernel<T, W>>(tiles, gbt::kThreads, 0, queue,
                                 1, a, dg, db);
             if (s == GEMM_OK && dx && rows > 0)
-                s = gbt::launch(gbt::norm_dx_wide_kernel<T, W>, rows, gbt::kThreads, 0, stream, 1, a);
+                s = gbt::launch<gbt::norm_dx_wide_kernel<T, W>>(rows, gbt::kThreads, 0, queue, 1, a);
             return s;
         }
         const int blocks = static_cast<int>(gbt::backward_blocks(rows, lanes, p->num_sms));
@@ -1011,11 +1011,11 @@ gemm_status_t gemm_norm_backward(gemm_norm_plan_t p, int64_t rows, const void* x
             const bool vec = gbt::rows_aligned(x, ldx, e) && gbt::rows_aligned(dy, lddy, e) &&
                              (!dx || gbt::rows_aligned(dx, lddx, e)) && gbt::aligned(gamma, 16);
             constexpr int kVec = 16 / static_cast<int>(sizeof(T));
-            s = vec ? gbt::backward_vec<T, W, kVec>(a, blocks, p->num_sms, stream)
-                    : gbt::backward_vec<T, W, 1>(a, blocks, p->num_sms, stream);
+            s = vec ? gbt::backward_vec<T, W, kVec>(a, blocks, p->num_sms, queue)
+                    : gbt::backward_vec<T, W, 1>(a, blocks, p->num_sms, queue);
         }
         if (s == GEMM_OK && a.weights)
-            s = gbt::launch(gbt::norm_weight_join_kernel<W>, 2 * tiles, gbt::kThreads, 0, stream, 1,
+            s = gbt::launch<gbt::norm_weight_join_kernel<W>>(2 * tiles, gbt::kThreads, 0, queue, 1,
                             p->partial, blocks, static_cast<int>(p->cols), dg, db);
         return s;
     });

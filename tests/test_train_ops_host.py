@@ -91,6 +91,14 @@ class _Tensor:
     def stride(self):
         return self._stride
 
+    def is_contiguous(self):
+        want = 1
+        for n, at in zip(reversed(self.shape), reversed(self._stride)):
+            if at != want:
+                return False
+            want *= n
+        return True
+
 
 def test_entry_points_marshal_what_they_take(gemm_lib):
     """The C entry points hand the C functions the arguments' addresses, sizes and strides, and take nothing
