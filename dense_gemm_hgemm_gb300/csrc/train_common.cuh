@@ -323,7 +323,7 @@ struct Turn {
     }
 };
 
-// As wait_phase; when it runs out (or another wait has) it returns at once from then on.
+// As wait_phase, for whole warps; when it runs out (or another wait has) it returns at once from then on.
 __device__ __forceinline__ void wait_or_die(uint64_t* barrier, uint32_t parity, int* dead, int32_t* error) {
     const uint32_t at = shared_address(barrier);
     long long began = 0;

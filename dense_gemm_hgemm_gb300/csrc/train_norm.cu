@@ -324,9 +324,11 @@ struct Ring {
         if (direct(row)) return from;
         return memory + (turn.at * N + k) * stage_bytes + (ANY ? reinterpret_cast<uintptr_t>(from) & 15u : 0);
     }
-    // All lanes have read the present stage.
+    // All lanes have read the present stage.  (The warp goes on together: without the
+    // __syncwarp its first lane took the rest of the row by itself, twice the instructions.)
     __device__ __forceinline__ void release(int lane, int row) {
         if (lane == 0 && row < rows - stages * step) ask(turn.at, row + stages * step);
+        __syncwarp();
     }
     // After a wait that ran out (one lane): what was asked for may still come.
     __device__ __forceinline__ void end() const {
@@ -465,22 +467,37 @@ __device__ __forceinline__ void copy_partial(int lanes, int cols, const float* j
     }
 }
 
-// Joins the groups' sums of a block in shared memory, in the order of the groups, and
-// writes them to the block's place in the partial sums.  `add` is the kernels' add_to.
-template <int VEC, int THREADS, typename A>
+// The sums of a block's groups, joined in the order of the groups through shared memory
+// (`join`: [groups][2][lanes * kLaneCols], by column), to its rows of the partial sums.
+template <int VEC, int THREADS>
 __device__ __forceinline__ void write_partial(const Pair (&dg)[kPairs], const Pair (&db)[kPairs], int group, int groups,
-                                              int lanes, int cols, const float* join, float* partial, A add) {
-    for (int turn = 0; turn < groups; ++turn) {
-        if (group == turn) {
+                                              int lane, int lanes, int cols, float* join, float* partial) {
+    const int width = lanes * kLaneCols;
+    if (group < groups) {
 #pragma unroll
-            for (int j = 0; j < kPairs; ++j) {
-                add(0, j, dg[j], turn == 0);
-                add(1, j, db[j], turn == 0);
+        for (int which = 0; which < 2; ++which) {
+            float v[kLaneCols];
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) (which == 0 ? dg : db)[j].get(v[2 * j], v[2 * j + 1]);
+            float* to = join + (group * 2 + which) * width;
+#pragma unroll
+            for (int k = 0; k < kLaneCols / VEC; ++k) {
+                float part[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) part[i] = v[k * VEC + i];
+                store_values<float, VEC>(to + (k * lanes + lane) * VEC, VEC, part);
             }
         }
-        __syncthreads();
     }
-    copy_partial<VEC, THREADS>(lanes, cols, join, partial);
+    __syncthreads();
+    for (int which = 0; which < 2; ++which) {
+        float* out = partial + (static_cast<int64_t>(which) * gridDim.x + blockIdx.x) * cols;
+        for (int c = threadIdx.x; c < cols; c += THREADS) {
+            float s = join[which * width + c];
+            for (int g = 1; g < groups; ++g) s += join[(g * 2 + which) * width + c];
+            out[c] = s;
+        }
+    }
 }
 
 // dx of each row, and the block's sums of dy * xh and dy over its rows: each lane adds
@@ -488,7 +505,7 @@ __device__ __forceinline__ void write_partial(const Pair (&dg)[kPairs], const Pa
 // threads has no registers left for them); the groups of a block are joined at the end.
 template <typename T, typename W, int VEC, int BLOCK, bool SHARED>
 __global__ void __launch_bounds__(BLOCK) norm_backward_kernel(const BackwardArgs<T, W> a) {
-    extern __shared__ float join[];      // [2][lanes * kLaneCols]
+    extern __shared__ __align__(16) float join[];
     __shared__ float part[BLOCK / 32][2][2][32];
     wait_for_previous_kernel();
     let_next_kernel_start();
@@ -558,7 +575,7 @@ __global__ void __launch_bounds__(BLOCK) norm_backward_kernel(const BackwardArgs
         __syncthreads();
         copy_partial<VEC, BLOCK>(lanes, a.cols, join, a.partial);
     } else {
-        write_partial<VEC, BLOCK>(dg, db, group, groups, lanes, a.cols, join, a.partial, add_to);
+        write_partial<VEC, BLOCK>(dg, db, group, groups, lane, lanes, a.cols, join, a.partial);
     }
 }
 
@@ -636,16 +653,8 @@ __global__ void __launch_bounds__(kBackwardRing, 1) norm_backward_ring_kernel(co
     if (lane == 0 && group < groups) ring.end();
     if (!a.weights) return;
     __syncthreads();                                     // the rings have been read: their memory joins the groups
-    float* const join = reinterpret_cast<float*>(memory);
-    const auto add_to = [&](int which, int j, Pair v, bool fresh) {
-        float lo, hi;
-        v.get(lo, hi);
-        float& at = join[(which * kLaneCols + 2 * j) * lanes + lane];
-        float& at1 = join[(which * kLaneCols + 2 * j + 1) * lanes + lane];
-        at = fresh ? lo : at + lo;
-        at1 = fresh ? hi : at1 + hi;
-    };
-    write_partial<VEC, kBackwardRing>(dg, db, group, groups, lanes, a.cols, join, a.partial, add_to);
+    write_partial<VEC, kBackwardRing>(dg, db, group, groups, lane, lanes, a.cols, reinterpret_cast<float*>(memory),
+                                      a.partial);
 }
 
 // The blocks' sums of 32 columns: eight warps take every eighth block, then join.
@@ -833,7 +842,7 @@ gemm_status_t forward_vec(const ForwardArgs<T, W>& a, int sms, Queue queue) {
 template <typename T, typename W, int VEC, int BLOCK, bool SHARED>
 gemm_status_t backward_rows(const BackwardArgs<T, W>& a, int blocks, Queue queue) {
     // (SHARED keeps its sums there whether they are wanted or not)
-    const size_t smem = SHARED || a.weights ? static_cast<size_t>(a.lanes) * kLaneCols * 2 * sizeof(float) : 0;
+    const size_t smem = SHARED || a.weights ? static_cast<size_t>(BLOCK) * kLaneCols * 2 * sizeof(float) : 0;
     return launch<norm_backward_kernel<T, W, VEC, BLOCK, SHARED>>(blocks, BLOCK, smem, queue, 1, a);
 }
 
@@ -874,7 +883,7 @@ gemm_status_t backward_vec(const BackwardArgs<T, W>& a, int blocks, int sms, Que
     const int stages = ring_stages(a.cols, VEC, stage, 2, b.lanes, kBackwardRing, 0, a.rows, sms);
     if (stages > 0) {
         const size_t ring = static_cast<size_t>(2 * (kBackwardRing / b.lanes) * stages * stage);
-        const size_t join = static_cast<size_t>(b.lanes) * kLaneCols * 2 * sizeof(float);
+        const size_t join = static_cast<size_t>(kBackwardRing / b.lanes * b.lanes) * kLaneCols * 2 * sizeof(float);
         return launch<norm_backward_ring_kernel<T, W, VEC>>(blocks, kBackwardRing, ring > join ? ring : join, queue, 1,
                       b, stages);
     }
