@@ -81,6 +81,12 @@ __device__ __forceinline__ float sum_of(const Pair (&v)[N]) {
     return lo + hi;
 }
 
+__device__ __forceinline__ float half_sum(float v) {     // over 16 lanes
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
 // Sums over a group, in every lane: shuffles in the warp, then one exchange in shared
 // memory behind the group's own barrier.  Two exchange buffers in turn: a warp that is
 // a sum ahead has passed the barrier that the others reach only after their reads.
@@ -88,18 +94,39 @@ template <int N>
 struct GroupSum {
     float (*part)[N][32];    // [2][N][32] of the group
     int lanes, barrier, turn;
-    __device__ __forceinline__ void operator()(float (&v)[N], int lane) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-        if (lanes == 32) return;
-        const int warps = lanes / 32, l = lane % 32;
-        if (l == 0) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) part[turn][i][lane / 32] = v[i];
-        }
+    __device__ __forceinline__ void meet() {
         asm volatile("bar.sync %0, %1;" :: "r"(barrier), "r"(lanes) : "memory");
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = warp_sum(l < warps ? part[turn][i][l] : 0.f);
+    }
+    __device__ __forceinline__ void operator()(float (&v)[N], int lane) {
+        const int warps = lanes / 32, l = lane % 32;
+        if constexpr (N == 1) {
+            v[0] = warp_sum(v[0]);
+            if (lanes == 32) return;
+            if (l == 0) part[turn][0][lane / 32] = v[0];
+            meet();
+            v[0] = l < warps ? part[turn][0][l] : 0.f;
+            if (warps > 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+            if (warps > 8) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 8);
+            if (warps > 4) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 4);
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], 2);
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+            if (warps <= 16) v[0] = __shfl_sync(0xffffffffu, v[0], 0);
+        } else {
+            // two values share the steps: half the lanes go on with one, half with the other
+            const bool upper = l >= 16;
+            float mine = (upper ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[1], 16);
+            mine = half_sum(mine);
+            if (lanes > 32) {
+                if ((l & 15) == 0) part[turn][upper][lane / 32] = mine;
+                meet();
+                const int w = l & 15;
+                mine = w < warps ? part[turn][upper][w] : 0.f;
+                if (warps > 16) mine += w + 16 < warps ? part[turn][upper][w + 16] : 0.f;
+                mine = half_sum(mine);
+            }
+            v[0] = __shfl_sync(0xffffffffu, mine, 0);
+            v[1] = __shfl_sync(0xffffffffu, mine, 16);
+        }
         turn ^= 1;
     }
 };
