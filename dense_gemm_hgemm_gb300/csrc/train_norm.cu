@@ -22,7 +22,7 @@ constexpr int kPairs = kLaneCols / 2;
 
 // ---- rows in registers ----------------------------------------------------------
 //
-// `lanes` threads (32 to 1024, a power of two) keep one row, kLaneCols columns each:
+// `lanes` threads (4 to 1024, a power of two) keep one row, kLaneCols columns each:
 // PACKS packs of VEC elements, pack k of lane l at column (k * lanes + l) * VEC.  A
 // block has BLOCK / lanes such groups, each with its own rows, and asks for its next
 // row before it works on the present one.  So a row is read once, and its statistics
@@ -92,16 +92,28 @@ __device__ __forceinline__ float half_sum(float v) {     // over 16 lanes
 // a sum ahead has passed the barrier that the others reach only after their reads.
 template <int N>
 struct GroupSum {
-    float (*part)[N][32];    // [2][N][32] of the group
+    float (*part)[N][32];    // [2][N][32] of the group (where it is more than a warp)
     int lanes, barrier, turn;
+    // the lanes of a group within a warp, which other groups share
+    __device__ __forceinline__ float few(float v) const {
+        const unsigned mask = ((1u << lanes) - 1u) << (threadIdx.x % 32 / lanes * lanes);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1)
+            if (o < lanes) v += __shfl_xor_sync(mask, v, o);
+        return v;
+    }
     __device__ __forceinline__ void meet() {
         asm volatile("bar.sync %0, %1;" :: "r"(barrier), "r"(lanes) : "memory");
     }
     __device__ __forceinline__ void operator()(float (&v)[N], int lane) {
         const int warps = lanes / 32, l = lane % 32;
+        if (lanes <= 32) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = lanes == 32 ? warp_sum(v[i]) : few(v[i]);
+            return;
+        }
         if constexpr (N == 1) {
             v[0] = warp_sum(v[0]);
-            if (lanes == 32) return;
             if (l == 0) part[turn][0][lane / 32] = v[0];
             meet();
             v[0] = l < warps ? part[turn][0][l] : 0.f;
@@ -116,14 +128,12 @@ struct GroupSum {
             const bool upper = l >= 16;
             float mine = (upper ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[1], 16);
             mine = half_sum(mine);
-            if (lanes > 32) {
-                if ((l & 15) == 0) part[turn][upper][lane / 32] = mine;
-                meet();
-                const int w = l & 15;
-                mine = w < warps ? part[turn][upper][w] : 0.f;
-                if (warps > 16) mine += w + 16 < warps ? part[turn][upper][w + 16] : 0.f;
-                mine = half_sum(mine);
-            }
+            if ((l & 15) == 0) part[turn][upper][lane / 32] = mine;
+            meet();
+            const int w = l & 15;
+            mine = w < warps ? part[turn][upper][w] : 0.f;
+            if (warps > 16) mine += w + 16 < warps ? part[turn][upper][w + 16] : 0.f;
+            mine = half_sum(mine);
             v[0] = __shfl_sync(0xffffffffu, mine, 0);
             v[1] = __shfl_sync(0xffffffffu, mine, 16);
         }
@@ -252,7 +262,7 @@ __global__ void __launch_bounds__(BLOCK) norm_forward_kernel(const ForwardArgs<T
     int64_t row = static_cast<int64_t>(blockIdx.x) * (BLOCK / lanes) + group;
     if (row >= a.rows) return;
     const bool full = a.cols == lanes * kLaneCols;
-    GroupSum<1> sum{part[group], lanes, 1 + group, 0};
+    GroupSum<1> sum{part[group % (BLOCK / 32)], lanes, 1 + group, 0};
     RowPacks<T, VEC, kLaneCols, false> next;
     next.load(a.x + row * a.ldx, lane, lanes, a.cols);
     Pair gamma[kPairs], beta[kPairs];
@@ -293,7 +303,7 @@ __global__ void __launch_bounds__(BLOCK) norm_forward_kernel(const ForwardArgs<T
 // depend on how many registers are left for loads: the register kernels keep 24 KB an SM
 // in flight at 16384 x 4096, the rings over 100 KB.
 
-constexpr int kRingRows = 1 << 30;         // rows are counted in 32 bits there, a step beyond the last
+constexpr int kRingRows = 1 << 30;         // rows are counted in 32 bits there, some steps beyond the last
 constexpr int kRingSlots = 64;             // stages of a block, at most
 constexpr int kRingShared = 208 * 1024;    // its dynamic shared memory, at most
 constexpr int kForwardRing = 1024;         // threads of the blocks
@@ -351,10 +361,10 @@ struct Ring {
         if (direct(row)) return from;
         return memory + (turn.at * N + k) * stage_bytes + (ANY ? reinterpret_cast<uintptr_t>(from) & 15u : 0);
     }
-    // All lanes have read the present stage.  (The warp goes on together: without the
+    // All lanes have read that stage: the row, `stages` steps on from what it held.  (The warp goes on together: without the
     // __syncwarp its first lane took the rest of the row by itself, twice the instructions.)
-    __device__ __forceinline__ void release(int lane, int row) {
-        if (lane == 0 && row < rows - stages * step) ask(turn.at, row + stages * step);
+    __device__ __forceinline__ void refill(int lane, int stage, int row) {
+        if (lane == 0 && row < rows) ask(stage, row);
         __syncwarp();
     }
     // After a wait that ran out (one lane): what was asked for may still come.
@@ -433,7 +443,7 @@ __global__ void __launch_bounds__(kForwardRing, 1) norm_forward_ring_kernel(cons
             to_pairs(in.p, v);
         }
         const float mu = centre<VEC>(v, sum, inverse_n, full, lane, lanes, a.cols);
-        ring.release(lane, row);
+        ring.refill(lane, ring.turn.at, row + stages * ring.step);
         const float r = rstd_of(v, sum, inverse_n, a.eps, lane);
         normalise<T, W, VEC>(v, r, gamma, beta, y, lane, lanes, a.cols);
         if (lane == 0) {
@@ -540,7 +550,7 @@ __global__ void __launch_bounds__(BLOCK) norm_backward_kernel(const BackwardArgs
     const int groups = BLOCK / lanes;
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group;
-    GroupSum<2> sum{part[group], lanes, 1 + group, 0};
+    GroupSum<2> sum{part[group % (BLOCK / 32)], lanes, 1 + group, 0};
     Pair dg[kPairs], db[kPairs], gamma[kPairs];
     // sum `which` of the lane's element i of its kLaneCols
     const auto mine = [&](int which, int i) -> float& { return join[(which * kLaneCols + i) * lanes + lane]; };
@@ -674,13 +684,118 @@ __global__ void __launch_bounds__(kBackwardRing, 1) norm_backward_ring_kernel(co
         }
         float s[2];
         row_sums(sum_g, sum_gx, sum, lane, s);
-        ring.release(lane, row);
+        ring.refill(lane, ring.turn.at, row + stages * ring.step);
         if (a.dx) write_dx<T, VEC, true>(hat, g, s, inverse_n, r2, dx, lane, lanes, a.cols);
     }
     if (lane == 0 && group < groups) ring.end();
     if (!a.weights) return;
     __syncthreads();                                     // the rings have been read: their memory joins the groups
     write_partial<VEC, kBackwardRing>(dg, db, group, groups, lane, lanes, a.cols, reinterpret_cast<float*>(memory),
+                                      a.partial);
+}
+
+// A lane's columns of a row, in pairs: f(pair, x, dy, gamma).
+template <typename T, typename W, int VEC, typename F>
+__device__ __forceinline__ void each_pair(const T* x, const T* dy, const Staged<W, VEC>& gamma, int lane, int lanes,
+                                          int cols, F f) {
+#pragma unroll
+    for (int k = 0; k < kLaneCols / VEC; ++k) {
+        const int c = (k * lanes + lane) * VEC;
+        if (c >= cols) continue;
+        const Pack<T, VEC> px = load_pack<T, VEC>(x + c, VEC), pd = load_pack<T, VEC>(dy + c, VEC);
+        float g[VEC];
+        gamma.get(c, g);
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j)
+            f(k * (VEC / 2) + j, pair_of(px, j), pair_of(pd, j), Pair(g[2 * j], g[2 * j + 1]));
+    }
+}
+
+// The same for rows of more lanes than such a block has (VEC > 1): a block of 1024 threads
+// has no registers for a row beside the weight gradients' sums, so the row is read twice from
+// its stage, for the sums and for dx, and the stage is refilled when the block has met at the
+// next row's barrier.  4096 x 16384 bf16: 193 us with the sums in shared memory, 119 us so; at
+// 8192 columns, where both fit, 110 us against 77.
+constexpr int kWideRing = 1024;
+
+template <typename T, typename W, int VEC>
+__global__ void __launch_bounds__(kWideRing, 1) norm_backward_wide_ring_kernel(const BackwardArgs<T, W> a, int stages) {
+    extern __shared__ __align__(128) uint8_t memory[];
+    __shared__ RingBarriers barriers;
+    __shared__ float part[kWideRing / 32][2][2][32];
+    constexpr bool kAny = false;
+    const int lanes = a.lanes, groups = 1, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+    const int row_bytes = a.cols * static_cast<int>(sizeof(T)), stage_bytes = ring_stage_bytes(row_bytes, kAny);
+    Staged<W, VEC> gamma{reinterpret_cast<W*>(memory + groups * stages * 2 * stage_bytes), lanes * kLaneCols / 2};
+    if (threadIdx.x == 0) init_ring(barriers, groups * stages);
+    __syncthreads();
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    // (threads behind the last whole group have no rows)
+    int row = group < groups ? static_cast<int>(blockIdx.x + group * gridDim.x) : static_cast<int>(a.rows);
+    Ring<2, kAny> ring{memory + group * stages * 2 * stage_bytes,
+                       barriers.full + group * stages,
+                       &barriers.dead,
+                       a.error,
+                       {reinterpret_cast<const uint8_t*>(a.x), reinterpret_cast<const uint8_t*>(a.dy)},
+                       {a.ldx * static_cast<int64_t>(sizeof(T)), a.lddy * static_cast<int64_t>(sizeof(T))},
+                       static_cast<int>(a.rows),
+                       static_cast<int>(groups * gridDim.x),
+                       row_bytes,
+                       stage_bytes,
+                       stages,
+                       {0, 0},
+                       0};
+    if (lane == 0 && group < groups) ring.begin(row);
+    for (int c = threadIdx.x; c < a.cols; c += kWideRing) gamma.put(c, a.gamma ? a.gamma[c] : from_f32<W>(1.f));
+    __syncthreads();
+    const float inverse_n = 1.f / static_cast<float>(a.cols);
+    GroupSum<2> sum{part[group], lanes, 1 + group, 0};
+    Pair dg[kPairs], db[kPairs];
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) dg[j] = db[j] = Pair(0.f, 0.f);
+    float next_mean = 0.f, next_rstd = 0.f;
+    const auto ask = [&](int r) {
+        next_mean = a.mean[r];
+        next_rstd = a.rstd[r];
+    };
+    if (row < ring.rows) ask(row);
+    int before = -1;                                     // the stage of the group's row before
+    for (; row < ring.rows; row += ring.step, ring.turn.next(1, stages)) {
+        const float mu = next_mean, r = next_rstd;
+        if (row < ring.rows - ring.step) ask(row + ring.step);
+        ring.wait();
+        const T* const x = reinterpret_cast<const T*>(ring.at(0, row));
+        const T* const dy = reinterpret_cast<const T*>(ring.at(1, row));
+        const Pair minus(-mu, -mu), r2(r, r);
+        Pair sum_g(0.f, 0.f), sum_gx(0.f, 0.f);
+        each_pair<T, W, VEC>(x, dy, gamma, lane, lanes, a.cols, [&](int j, Pair v, Pair d, Pair w) {
+            const Pair hat = mul2(add2(v, minus), r2), g = mul2(d, w);
+            dg[j] = fma2(d, hat, dg[j]);
+            db[j] = add2(db[j], d);
+            sum_g = add2(sum_g, g);
+            sum_gx = fma2(g, hat, sum_gx);
+        });
+        float s[2];
+        row_sums(sum_g, sum_gx, sum, lane, s);
+        if (before >= 0) ring.refill(lane, before, row + (stages - 1) * ring.step);
+        before = ring.turn.at;
+        if (!a.dx) continue;
+        // dx = rstd dy gamma - rstd mean(g) - (x - mean) rstd^2 mean(g xh)
+        const float at_x = -r * r * (s[1] * inverse_n), at_1 = -r * (s[0] * inverse_n);
+        const Pair at_x2(at_x, at_x), at_12(at_1, at_1);
+        T* const dx = a.dx + row * a.lddx;
+        Pack<T, VEC> out;
+        each_pair<T, W, VEC>(x, dy, gamma, lane, lanes, a.cols, [&](int j, Pair v, Pair d, Pair w) {
+            const Pair y = fma2(mul2(d, r2), w, fma2(add2(v, minus), at_x2, at_12));
+            set_pair(out, j % (VEC / 2), y);
+            if (j % (VEC / 2) == VEC / 2 - 1) store_pack<T, VEC>(dx + (j / (VEC / 2) * lanes + lane) * VEC, VEC, out);
+        });
+    }
+    if (lane == 0 && group < groups) ring.end();
+    if (!a.weights) return;
+    __syncthreads();                                     // the rings have been read: their memory joins the groups
+    write_partial<VEC, kWideRing>(dg, db, group, groups, lane, lanes, a.cols, reinterpret_cast<float*>(memory),
                                       a.partial);
 }
 
@@ -818,7 +933,7 @@ int ring_lanes(int cols, int each) { return ((cols + each - 1) / each + 31) / 32
 
 // Lanes that keep a row of `cols` columns in the register kernels.
 int lanes_for(int64_t cols) {
-    int lanes = 32;
+    int lanes = 4;
     while (static_cast<int64_t>(lanes) * kLaneCols < cols) lanes *= 2;
     return lanes;
 }
@@ -834,11 +949,12 @@ gemm_status_t forward_rows(const ForwardArgs<T, W>& a, int sms, Queue queue) {
 }
 
 // Stages of a group's ring whose block also needs `fixed` bytes; 0 where rings do not suit:
-// rows of no whole packs, rows too short for a copy each, or too few rows for two to each group of each SM's block.
+// rows of no whole packs, rows too short for a copy each (65536 x 256 bf16: 27 us by rings, 23
+// in registers; single elements take longer to load, and rings pay from half that length), or too few rows for two to each group of each SM's block.
 int ring_stages(int cols, int vec, int64_t row_bytes, int sources, int lanes, int threads, int64_t fixed, int64_t rows,
                 int sms) {
     const int groups = threads / lanes;
-    if (groups == 0 || row_bytes < 512 || cols % vec != 0 || rows < int64_t{2} * sms * groups || rows > kRingRows)
+    if (groups == 0 || row_bytes < (vec == 1 ? 512 : 1024) || cols % vec != 0 || rows < int64_t{2} * sms * groups || rows > kRingRows)
         return 0;
     int64_t stages = (kRingShared - fixed) / (row_bytes * sources * groups);
     if (stages > kRingSlots / groups) stages = kRingSlots / groups;
@@ -847,6 +963,15 @@ int ring_stages(int cols, int vec, int64_t row_bytes, int sources, int lanes, in
 
 template <typename T, typename W, int VEC>
 gemm_status_t forward_vec(const ForwardArgs<T, W>& a, int sms, Queue queue) {
+    if constexpr (VEC > 1) {
+        // rows that end inside a pack: element by element through rings where there are many
+        // (10000 x 5003 bf16, aligned: 72 us; in registers with a partial pack 141 us)
+        const int64_t stage = ring_stage_bytes(a.cols * static_cast<int>(sizeof(T)), true);
+        const int lanes = ring_lanes(a.cols, kLaneCols);
+        const int64_t weights = int64_t{2} * lanes * kLaneCols * static_cast<int64_t>(sizeof(W));
+        if (a.cols % VEC != 0 && ring_stages(a.cols, 1, stage, 1, lanes, kForwardRing, weights, a.rows, sms) > 0)
+            return forward_vec<T, W, 1>(a, sms, queue);
+    }
     ForwardArgs<T, W> b = a;
     const bool half = VEC > 1 && a.cols > 512;   // 32 columns a lane (single elements take more registers)
     const int each = half ? 32 : 16;
@@ -886,7 +1011,8 @@ gemm_status_t prepare() {
     };
     if (allow_ring(norm_forward_ring_kernel<T, W, kVec, 16>) && allow_ring(norm_forward_ring_kernel<T, W, kVec, 32>) &&
         allow_ring(norm_forward_ring_kernel<T, W, 1, 16>) &&
-        allow_ring(norm_backward_ring_kernel<T, W, kVec>) && allow_ring(norm_backward_ring_kernel<T, W, 1>) &&
+        allow_ring(norm_backward_ring_kernel<T, W, kVec>) && allow_ring(norm_backward_wide_ring_kernel<T, W, kVec>) &&
+        allow_ring(norm_backward_ring_kernel<T, W, 1>) &&
         allow(norm_backward_kernel<T, W, kVec, 512, false>, 512) && allow(norm_backward_kernel<T, W, 1, 512, false>, 512) &&
         allow(norm_backward_kernel<T, W, kVec, 1024, true>, 1024) && allow(norm_backward_kernel<T, W, 1, 1024, true>, 1024))
         return GEMM_OK;
@@ -913,6 +1039,15 @@ gemm_status_t backward_vec(const BackwardArgs<T, W>& a, int blocks, int sms, Que
         const size_t join = static_cast<size_t>(kBackwardRing / b.lanes * b.lanes) * kLaneCols * 2 * sizeof(float);
         return launch<norm_backward_ring_kernel<T, W, VEC>>(blocks, kBackwardRing, ring > join ? ring : join, queue, 1,
                       b, stages);
+    }
+    if constexpr (VEC > 1) {
+        const int64_t weights = static_cast<int64_t>(b.lanes) * kLaneCols * static_cast<int64_t>(sizeof(W));
+        const int wide = b.lanes > kBackwardRing ? ring_stages(a.cols, VEC, stage, 2, b.lanes, kWideRing, weights, a.rows, sms) : 0;
+        const size_t ring = static_cast<size_t>(2 * wide * stage + weights);
+        const size_t join = static_cast<size_t>(b.lanes) * kLaneCols * 2 * sizeof(float);
+        if (wide > 0)
+            return launch<norm_backward_wide_ring_kernel<T, W, VEC>>(blocks, kWideRing, ring > join ? ring : join, queue, 1,
+                                                                     b, wide);
     }
     if (a.lanes <= 512) return backward_rows<T, W, VEC, 512, false>(a, blocks, queue);
     return backward_rows<T, W, VEC, 1024, true>(a, blocks, queue);
