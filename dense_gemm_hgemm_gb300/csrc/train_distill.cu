@@ -249,6 +249,24 @@ struct Running {
     }
 };
 
+// A row's softmax: q = inverse * exp2(s c - base).  After a forward pass base is the row's
+// reference and inverse one over its sum, so nothing is rounded between them; from a given
+// log-sum-exp base is that in log2 units, and inverse makes up for its rounding.
+struct Softmax {
+    float base, inverse;
+    __device__ __forceinline__ void of_sum(float k, float sum) {
+        base = finite_base(k);
+        inverse = 1.f / sum;
+    }
+    __device__ __forceinline__ void of_lse(float lse) {
+        constexpr float kLog2eRest = 1.9259629911e-8f;       // log2(e) - kLog2e
+        base = lse * kLog2e;
+        inverse = exp2_fast(-(fmaf(lse, kLog2e, -base) + lse * kLog2eRest));
+    }
+    // the log-sum-exp, from the forward pass' sum
+    __device__ __forceinline__ float lse(float sum) const { return fmaf(base, kLn2, kLn2 * log2f(sum)); }
+};
+
 template <typename T>
 __device__ __forceinline__ Pack<T, 16 / sizeof(T)> all_masked() {
     Pack<T, 16 / static_cast<int>(sizeof(T))> q;
@@ -257,11 +275,11 @@ __device__ __forceinline__ Pack<T, 16 / sizeof(T)> all_masked() {
     return q;
 }
 
-// scale * exp2(s c - log2_all) of each element of a pack.
+// scale * exp2(s c - base) of each element of a pack.
 template <typename T, int VEC>
-__device__ __forceinline__ Pack<T, VEC> gradient(const Pack<T, VEC>& q, float c, float log2_all, float scale) {
+__device__ __forceinline__ Pack<T, VEC> gradient(const Pack<T, VEC>& q, float c, float base, float scale) {
     Pack<T, VEC> g;
-    const Pair c2(c, c), all2(-log2_all, -log2_all), scale2(scale, scale);
+    const Pair c2(c, c), all2(-base, -base), scale2(scale, scale);
 #pragma unroll
     for (int j = 0; j < VEC / 2; ++j) {
         float lo, hi;
@@ -269,6 +287,15 @@ __device__ __forceinline__ Pack<T, VEC> gradient(const Pack<T, VEC>& q, float c,
         set_pair(g, j, mul2(scale2, Pair(exp2_fast(lo), exp2_fast(hi))));
     }
     return g;
+}
+
+// The loss of a row over tau^2 ln 2, from its blocks' parts: the sum over entries of
+// p (log2 p - (s c - k)), each block's from its own k, and p's sum there.
+__device__ __forceinline__ float joined_loss(const float4* parts, int pieces, float base, float mass, float sum) {
+    float total = mass * log2f(sum);
+    for (int r = 0; r < pieces; ++r)
+        total += parts[r].z + (parts[r].w == 0.f ? 0.f : parts[r].w * (base - finite_base(parts[r].x)));
+    return total;
 }
 
 // ---- the kernel ------------------------------------------------------------------------
@@ -320,7 +347,8 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const Args<T> a) {
     T* d = nullptr;
     if (kGrad) d = a.dlogits + row * a.ldd + begin;
 
-    float log2_all = given_lse * kLog2e;                 // log-sum-exp of the whole row, in log2 units
+    Softmax row_q = {0.f, 0.f};
+    if (MODE == kBackward) row_q.of_lse(given_lse);
     bool empty = out;
     const T* src = a.logits + row * a.ldl + begin;
     const int off = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15u) / sizeof(T));
@@ -400,30 +428,26 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const Args<T> a) {
         }
         float high = exchange[0].x, all = exchange[0].y;
         for (int r = 1; r < a.pieces; ++r) merge(high, all, exchange[r].x, exchange[r].y);
-        high = finite_base(high);
+        row_q.of_sum(high, all);
         empty = out || all == 0.f;
-        const float log2_sum = log2f(all);
-        log2_all = high + log2_sum;
         if (rank == 0 && tid == 0) {
-            float total = mass * log2_sum;
-            for (int r = 0; r < a.pieces; ++r)
-                total += exchange[r].z + (exchange[r].w == 0.f ? 0.f : exchange[r].w * (high - finite_base(exchange[r].x)));
+            const float total = joined_loss(exchange, a.pieces, row_q.base, mass, all);
             a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * total;
-            a.lse[row] = empty ? -INFINITY : kLn2 * log2_all;
+            a.lse[row] = empty ? -INFINITY : row_q.lse(all);
         }
     }
     if (!kGrad) return;
 
     const bool same = (reinterpret_cast<uintptr_t>(d) & 15u) == (reinterpret_cast<uintptr_t>(src) & 15u);
     const float scale = a.temperature * (a.dloss ? a.dloss[row] : 1.f);
-    const float q_scale = scale * mass;
+    const float q_scale = scale * (mass * row_q.inverse);
     for (int k = tid; k < packs; k += kThreads) {
         Pack<T, VEC> g;
         if (empty) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) g.set(i, 0.f);
         } else {
-            g = gradient(load_pack<T, VEC>(room + k * VEC, VEC), c, log2_all, q_scale);
+            g = gradient(load_pack<T, VEC>(room + k * VEC, VEC), c, row_q.base, q_scale);
         }
         const int at = k * VEC - off;                    // the pack's first element in the piece
         if (same && at >= 0 && at + VEC <= n) {
@@ -446,7 +470,8 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const Args<T> a) {
                 p += en.p[k];
                 first = first && k >= j;
             }
-            if (first) d[at] = from_f32<T>(scale * (mass * exp2_fast(to_f32(s[at]) * c - log2_all) - p));
+            if (first)
+                d[at] = from_f32<T>(scale * (mass * row_q.inverse * exp2_fast(to_f32(s[at]) * c - row_q.base) - p));
         }
     }
     if (!arrived) wait_phase(&barrier, 0);               // no copy may land in a finished block's memory
@@ -608,7 +633,8 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
             const int packs = (off + n + VEC - 1) / VEC;
             const Turn row_stage = stage;
             bool empty = out;
-            float log2_all = 0.f;                        // the row's log-sum-exp, in log2 units
+            Softmax row_q = {0.f, 0.f};
+            float row_sum = 0.f;
             float terms = 0.f;                           // of the loss: sum p (log2 p - x c)
             if (!out) {
                 Running<T> run;
@@ -692,17 +718,19 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
                 }
                 ++exchanges;
                 empty = sum == 0.f;
-                log2_all = finite_base(k) + log2f(sum);
+                row_q.of_sum(k, sum);
+                row_sum = sum;
             }
             if (rank == 0 && thread == 0) {
-                a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * (terms + mass * log2_all);
-                a.lse[row] = empty ? -INFINITY : kLn2 * log2_all;
+                const float total = fmaf(mass, row_q.base, terms) + mass * log2f(row_sum);
+                a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * total;
+                a.lse[row] = empty ? -INFINITY : row_q.lse(row_sum);
             }
             if (kGrad) {
                 T* const d = a.dlogits + row * a.ldd + begin;
                 const bool same = (reinterpret_cast<uintptr_t>(d) & 15u) == (reinterpret_cast<uintptr_t>(src) & 15u);
                 const float scale = sh.scale[slot];
-                const float q_scale = scale * mass;
+                const float q_scale = scale * (mass * row_q.inverse);
                 stage = row_stage;
                 for (int p0 = 0; p0 < packs; p0 += kStage / VEC) {
                     const T* from = ring + stage.at * kStage;
@@ -712,7 +740,7 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
                         for (int b = 0; b < kBatch; ++b)
                             store_pack<T, VEC>(d + at0 + b * kComputeThreads * VEC, VEC,
                                                gradient(load_pack<T, VEC>(from + (thread + b * kComputeThreads) * VEC, VEC),
-                                                        c, log2_all, q_scale));
+                                                        c, row_q.base, q_scale));
                     } else {
                         for (int b = 0; b < kBatch; ++b) {
                             const int mine = thread + b * kComputeThreads, at = at0 + b * kComputeThreads * VEC;
@@ -722,7 +750,7 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
 #pragma unroll
                                 for (int i = 0; i < VEC; ++i) g.set(i, 0.f);
                             } else {
-                                g = gradient(load_pack<T, VEC>(from + mine * VEC, VEC), c, log2_all, q_scale);
+                                g = gradient(load_pack<T, VEC>(from + mine * VEC, VEC), c, row_q.base, q_scale);
                             }
                             if (same && at >= 0 && at + VEC <= n) {
                                 store_pack<T, VEC>(d + at, VEC, g);
@@ -745,7 +773,7 @@ __global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const
                         const float p = en.own[j];
                         const int at = en.id[j] - begin;
                         if (p >= 0.f && at >= 0 && at < n)
-                            d[at] = from_f32<T>(scale * (mass * exp2_fast(en.x[j] * c - log2_all) - p));
+                            d[at] = from_f32<T>(scale * (mass * row_q.inverse * exp2_fast(en.x[j] * c - row_q.base) - p));
                     }
                 }
             }
@@ -796,7 +824,8 @@ __global__ void __launch_bounds__(kThreads) distill_short_kernel(const Args<T> a
     const float mass = load_entries(en, a.teacher, row, src, c, n, a.error);
     if (kGrad) join_equal_ids(en, top);
     bool empty = mass == 0.f || (MODE == kBackward && given == -INFINITY);
-    float log2_all = given * kLog2e;
+    Softmax row_q = {0.f, 0.f};
+    if (MODE == kBackward) row_q.of_lse(given);
     if (kLoss) {
         Running<T> run;
         run.add(q, c);
@@ -805,20 +834,20 @@ __global__ void __launch_bounds__(kThreads) distill_short_kernel(const Args<T> a
         for (int o = 16; o > 0; o >>= 1)
             merge(k, sum, __shfl_xor_sync(0xffffffffu, k, o), __shfl_xor_sync(0xffffffffu, sum, o));
         empty = empty || sum == 0.f;
-        log2_all = finite_base(k) + log2f(sum);
+        row_q.of_sum(k, sum);
         if (!empty)
             for (int j = lane; j < top; j += 32)
-                if (!(en.p[j] == 0.f)) terms += en.p[j] * (en.log2p[j] - (en.x[j] * c - log2_all));
+                if (!(en.p[j] == 0.f)) terms += en.p[j] * (en.log2p[j] - (en.x[j] * c - row_q.base));
         terms = warp_sum(terms);
         if (lane == 0) {
-            a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * terms;
-            a.lse[row] = empty ? -INFINITY : kLn2 * log2_all;
+            a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * (terms + mass * log2f(sum));
+            a.lse[row] = empty ? -INFINITY : row_q.lse(sum);
         }
     }
     if (!kGrad) return;
     T* const d = a.dlogits + row * a.ldd;
     const bool same = (reinterpret_cast<uintptr_t>(d) & 15u) == (reinterpret_cast<uintptr_t>(src) & 15u);
-    const float q_scale = empty ? 0.f : scale * mass;
+    const float q_scale = empty ? 0.f : scale * (mass * row_q.inverse);
     __syncwarp();                                        // the row has been read: d may be the logits
 #pragma unroll
     for (int b = 0; b < PACKS; ++b) {
@@ -828,7 +857,7 @@ __global__ void __launch_bounds__(kThreads) distill_short_kernel(const Args<T> a
 #pragma unroll
             for (int i = 0; i < VEC; ++i) g.set(i, 0.f);
         } else {
-            g = gradient(q[b], c, log2_all, q_scale);
+            g = gradient(q[b], c, row_q.base, q_scale);
         }
         if (same && at >= 0 && at + VEC <= n) {
             store_pack<T, VEC>(d + at, VEC, g);
@@ -842,7 +871,8 @@ __global__ void __launch_bounds__(kThreads) distill_short_kernel(const Args<T> a
     __syncwarp();                                        // the stores above come first
     for (int j = lane; j < top; j += 32)
         if (en.own[j] >= 0.f)
-            d[en.id[j]] = from_f32<T>(scale * (mass * exp2_fast(en.x[j] * c - log2_all) - en.own[j]));
+            d[en.id[j]] =
+                from_f32<T>(scale * (mass * row_q.inverse * exp2_fast(en.x[j] * c - row_q.base) - en.own[j]));
 }
 
 // ---- rows that no cluster can hold ---------------------------------------------------------
@@ -889,15 +919,16 @@ __global__ void __launch_bounds__(kThreads) distill_forward_wide_kernel(const Ar
     sum = part[1][0];
     for (int w = 1; w < kWarps; ++w) merge(k, sum, part[0][w], part[1][w]);
     const bool empty = mass == 0.f || sum == 0.f;
-    const float log2_all = finite_base(k) + log2f(sum);
+    Softmax row_q;
+    row_q.of_sum(k, sum);
     float total = 0.f;
     if (!empty)
         for (int j = lane; j < top; j += 32)
-            if (!(en.p[j] == 0.f)) total += en.p[j] * (en.log2p[j] - (to_f32(s[en.id[j]]) * c - log2_all));
+            if (!(en.p[j] == 0.f)) total += en.p[j] * (en.log2p[j] - (to_f32(s[en.id[j]]) * c - row_q.base));
     total = warp_sum(total);
     if (lane == 0) {
-        a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * total;
-        a.lse[row] = empty ? -INFINITY : kLn2 * log2_all;
+        a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * (total + mass * log2f(sum));
+        a.lse[row] = empty ? -INFINITY : row_q.lse(sum);
     }
 }
 
