@@ -256,7 +256,7 @@ struct Softmax {
     float base, inverse;
     __device__ __forceinline__ void of_sum(float k, float sum) {
         base = finite_base(k);
-        inverse = 1.f / sum;
+        inverse = __fdividef(1.f, sum);
     }
     __device__ __forceinline__ void of_lse(float lse) {
         constexpr float kLog2eRest = 1.9259629911e-8f;       // log2(e) - kLog2e
@@ -511,7 +511,7 @@ __device__ __forceinline__ void compute_barrier() {
 }
 
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kStreamThreads, 3) distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
+__global__ void __launch_bounds__(kStreamThreads, MODE == kBoth ? 2 : 3) distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     constexpr int kStageBytes = kStageBytesOf<MODE>;
     constexpr int kStage = kStageBytes / static_cast<int>(sizeof(T));     // elements
