@@ -657,11 +657,11 @@ gemm_status_t gemm_embed_plan_create(int64_t vocab, int64_t dim, int64_t max_tok
     *plan = nullptr;
     if (!gbt::valid_elem(elem) || (grad_elem != elem && grad_elem != GEMM_ELEM_F32))
         return GEMM_ERR_UNSUPPORTED;
-    if (vocab < 1 || vocab > INT32_MAX || dim < 1 || dim > INT32_MAX || max_tokens < 0 ||
-        max_tokens > INT32_MAX)
+    if (vocab < 1 || vocab > INT32_MAX || dim < 1 || dim > gbt::kMostColumns ||
+        max_tokens < 0 || max_tokens > INT32_MAX)
         return GEMM_ERR_INVALID_ARG;
     int device = 0, sms = 0;
-    gemm_status_t st = gbt::current_device(&device, &sms);
+    gemm_status_t st = gbt::begin_plan(&device, &sms);
     if (st != GEMM_OK) return st;
     const auto padded = [](size_t bytes) { return (bytes + 255) / 256 * 256; };
     const size_t list = padded(static_cast<size_t>(max_tokens) * 4);

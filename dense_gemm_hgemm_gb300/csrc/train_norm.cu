@@ -26,7 +26,9 @@ constexpr int kPairs = kLaneCols / 2;
 // PACKS packs of VEC elements, pack k of lane l at column (k * lanes + l) * VEC.  A
 // block has BLOCK / lanes such groups, each with its own rows, and asks for its next
 // row before it works on the present one.  So a row is read once, and its statistics
-// are exact two-pass ones at no further traffic.
+// are exact two-pass ones at no further traffic.  These kernels serve few rows (1 x 4096:
+// 2.8 us, the latency of a launch, a load and two sums) and rows too short for a copy each
+// (65536 x 64 bf16: forward 9.3 us, backward 12.5).
 
 // WHOLE: the row's length is a multiple of VEC, so a pack is in it or not.
 template <typename T, int VEC, int COLS, bool WHOLE>
@@ -180,7 +182,7 @@ __device__ __forceinline__ float rstd_of(const Pair (&v)[N], GroupSum<1>& sum, f
 
 // Weights in shared memory.  Packs of eight fp32 values are kept as two halves, each with
 // the others' halves, so that neighbouring lanes' 16-byte reads are neighbours (side by side
-// they would share banks: 61 us instead of 51 at 16384 x 4096 with fp32 weights).
+// they would share banks: 61 us instead of 46 at 16384 x 4096 with fp32 weights).
 template <typename W, int VEC>
 struct Staged {
     static constexpr bool kHalves = VEC * sizeof(W) > 16;
@@ -301,7 +303,12 @@ __global__ void __launch_bounds__(BLOCK) norm_forward_kernel(const ForwardArgs<T
 // tells that all lanes have read a stage, so its first lane asks for the next row right
 // behind it; there is no copying warp and no second barrier.  The bytes in flight do not
 // depend on how many registers are left for loads: the register kernels keep 24 KB an SM
-// in flight at 16384 x 4096, the rings over 100 KB.
+// in flight at 16384 x 4096, the rings over 100 KB.  Forward is bound by bytes: 16384 x 4096
+// bf16 44 us, 0.90 of the copy bandwidth (in registers 64); 65536 x 1000 43 us, 0.91;
+// 4096 x 16384 45 us, 0.88.  Backward does four sums' work an element (two of the row, two of
+// the columns) with 512 threads of 126 registers, and is bound by issuing that and by the
+// one barrier a row that nothing overlaps: 8192 x 8192 77 us, 0.78 (80 where each of the two
+// sums took its own shuffles; 82 in registers).
 
 constexpr int kRingRows = 1 << 30;         // rows are counted in 32 bits there, some steps beyond the last
 constexpr int kRingSlots = 64;             // stages of a block, at most
@@ -361,8 +368,9 @@ struct Ring {
         if (direct(row)) return from;
         return memory + (turn.at * N + k) * stage_bytes + (ANY ? reinterpret_cast<uintptr_t>(from) & 15u : 0);
     }
-    // All lanes have read that stage: the row, `stages` steps on from what it held.  (The warp goes on together: without the
-    // __syncwarp its first lane took the rest of the row by itself, twice the instructions.)
+    // All lanes have read that stage: the row, `stages` steps on from what it held.  (The warp
+    // goes on together: without the __syncwarp its first lane took the rest of the row by
+    // itself, twice the instructions.)
     __device__ __forceinline__ void refill(int lane, int stage, int row) {
         if (lane == 0 && row < rows) ask(stage, row);
         __syncwarp();
@@ -799,7 +807,9 @@ __global__ void __launch_bounds__(kWideRing, 1) norm_backward_wide_ring_kernel(c
                                       a.partial);
 }
 
-// The blocks' sums of 32 columns: eight warps take every eighth block, then join.
+// The blocks' sums of 32 columns: eight warps take every eighth block, then join, in an order
+// that the sizes alone give.  5 us behind a backward call of 8192 x 8192 (10 MB from L2); sums
+// by atomics into dgamma would save it, but their order would change from call to call.
 template <typename W>
 __global__ void __launch_bounds__(kThreads)
 norm_weight_join_kernel(const float* partial, int blocks, int cols, W* dgamma, W* dbeta) {
@@ -835,6 +845,9 @@ norm_weight_join_kernel(const float* partial, int blocks, int cols, W* dgamma, W
 }
 
 // ---- rows too wide for the registers of a block ------------------------------------
+//
+// More than 16384 columns.  Each pass reads the row anew (from L2, for rows of some hundred
+// KB); plain and right, for widths that hardly any model has.
 
 // The sum over the block, in every thread.
 __device__ float block_sum(float v) {
@@ -950,11 +963,13 @@ gemm_status_t forward_rows(const ForwardArgs<T, W>& a, int sms, Queue queue) {
 
 // Stages of a group's ring whose block also needs `fixed` bytes; 0 where rings do not suit:
 // rows of no whole packs, rows too short for a copy each (65536 x 256 bf16: 27 us by rings, 23
-// in registers; single elements take longer to load, and rings pay from half that length), or too few rows for two to each group of each SM's block.
+// in registers; single elements take longer to load, and rings pay from half that length), or
+// too few rows for two to each group of each SM's block.
 int ring_stages(int cols, int vec, int64_t row_bytes, int sources, int lanes, int threads, int64_t fixed, int64_t rows,
                 int sms) {
     const int groups = threads / lanes;
-    if (groups == 0 || row_bytes < (vec == 1 ? 512 : 1024) || cols % vec != 0 || rows < int64_t{2} * sms * groups || rows > kRingRows)
+    if (groups == 0 || row_bytes < (vec == 1 ? 512 : 1024) || cols % vec != 0 ||
+        rows < int64_t{2} * sms * groups || rows > kRingRows)
         return 0;
     int64_t stages = (kRingShared - fixed) / (row_bytes * sources * groups);
     if (stages > kRingSlots / groups) stages = kRingSlots / groups;
@@ -1073,10 +1088,10 @@ gemm_status_t gemm_norm_plan_create(int64_t max_rows, int64_t cols, gemm_elem_t 
     *plan = nullptr;
     if (!gbt::valid_elem(elem) || (weight_elem != elem && weight_elem != GEMM_ELEM_F32))
         return GEMM_ERR_UNSUPPORTED;
-    if (max_rows < 0 || max_rows > INT32_MAX || cols < 1 || cols > INT32_MAX)
+    if (max_rows < 0 || max_rows > INT32_MAX || cols < 1 || cols > gbt::kMostColumns)
         return GEMM_ERR_INVALID_ARG;
     int device = 0, sms = 0;
-    const gemm_status_t st = gbt::current_device(&device, &sms);
+    const gemm_status_t st = gbt::begin_plan(&device, &sms);
     if (st != GEMM_OK) return st;
     size_t sums = 0;
     if (max_rows > 0 && gbt::in_registers(cols))

@@ -58,7 +58,7 @@ typedef enum {
 typedef struct gemm_norm_plan *gemm_norm_plan_t;
 
 /*
- * A plan for up to max_rows rows of `cols` elements (1 <= cols < 2^31,
+ * A plan for up to max_rows rows of `cols` elements (1 <= cols <= 2^30,
  * 0 <= max_rows < 2^31).  elem: type of x, y, dy and dx; weight_elem: type of
  * gamma, beta and their gradients, either elem or GEMM_ELEM_F32 (else
  * GEMM_ERR_UNSUPPORTED).
@@ -105,9 +105,9 @@ typedef struct gemm_embed_plan *gemm_embed_plan_t;
 
 /*
  * A plan for a table of `vocab` rows of `dim` elements and up to max_tokens
- * tokens a call (vocab, dim >= 1, max_tokens >= 0, all < 2^31).  elem: type of
- * the table, of out and of dout; grad_elem: type of the table's gradient, either
- * elem or GEMM_ELEM_F32 (else GEMM_ERR_UNSUPPORTED).
+ * tokens a call (1 <= vocab < 2^31, 1 <= dim <= 2^30, 0 <= max_tokens < 2^31).
+ * elem: type of the table, of out and of dout; grad_elem: type of the table's
+ * gradient, either elem or GEMM_ELEM_F32 (else GEMM_ERR_UNSUPPORTED).
  */
 gemm_status_t gemm_embed_plan_create(int64_t vocab, int64_t dim, int64_t max_tokens,
                                      gemm_elem_t elem, gemm_elem_t grad_elem,
@@ -129,7 +129,8 @@ gemm_status_t gemm_embed_forward(gemm_embed_plan_t plan, int64_t tokens, const v
  * fp32 in an order that depends on the ids alone; padding and out-of-range tokens
  * take no part.  accumulate == 0: every row of dtable is written (rows without a
  * token as zeros); accumulate == 1: the sums are added to dtable (in fp32, then
- * rounded once), and rows without a token are not touched.
+ * rounded once), and rows without a token are not touched.  In fp32 that addition
+ * takes numbers below the smallest normal one as zeros.
  */
 gemm_status_t gemm_embed_backward(gemm_embed_plan_t plan, int64_t tokens, const void *ids,
                                   gemm_index_t id_type, int64_t padding, const void *dout,
@@ -175,7 +176,7 @@ typedef struct {
 
 /*
  * A plan for up to max_rows rows of logits over `vocab` tokens and up to max_top
- * teacher entries a row (1 <= vocab < 2^31, 0 <= max_rows < 2^31,
+ * teacher entries a row (1 <= vocab <= 2^30, 0 <= max_rows < 2^31,
  * 0 <= max_top <= 1024).  elem: type of the logits and of their gradient.
  */
 gemm_status_t gemm_distill_plan_create(int64_t max_rows, int64_t vocab, int64_t max_top,

@@ -25,14 +25,17 @@ def test_every_declared_function_has_a_signature(gemm_lib):
     ("gemm_norm_plan_create", (4, 0, 0, 0), 1),
     ("gemm_norm_plan_create", (-1, 8, 0, 0), 1),
     ("gemm_norm_plan_create", (4, 2 ** 31, 0, 0), 1),
+    ("gemm_norm_plan_create", (4, 2 ** 30 + 1, 0, 0), 1),
     ("gemm_norm_plan_create", (4, 8, 0, 2), None),
     ("gemm_embed_plan_create", (0, 8, 4, 0, 0), 1),
     ("gemm_embed_plan_create", (8, 0, 4, 0, 0), 1),
     ("gemm_embed_plan_create", (8, 8, -4, 0, 0), 1),
     ("gemm_embed_plan_create", (2 ** 31, 8, 4, 0, 0), 1),
+    ("gemm_embed_plan_create", (8, 2 ** 30 + 1, 4, 0, 0), 1),
     ("gemm_embed_plan_create", (8, 8, 4, 1, 0), 2),
     ("gemm_embed_plan_create", (8, 8, 4, 1, 2), None),
     ("gemm_distill_plan_create", (4, 0, 4, 0), 1),
+    ("gemm_distill_plan_create", (4, 2 ** 30 + 1, 4, 0), 1),
     ("gemm_distill_plan_create", (4, 8, 1025, 0), 1),
     ("gemm_distill_plan_create", (4, 8, -1, 0), 1),
     ("gemm_distill_plan_create", (4, 8, 4, 3), 2),
