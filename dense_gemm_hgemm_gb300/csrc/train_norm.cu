@@ -202,10 +202,11 @@ struct Staged {
     }
 };
 
-// and the result, with the weights read on the way, a pack at a time (whole packs).
-template <typename T, typename W, int VEC, int N>
+// and the result, with the weights read on the way, a pack at a time to store(column, pack)
+// (single elements: to y).
+template <typename T, typename W, int VEC, int N, typename F>
 __device__ __forceinline__ void normalise(const Pair (&v)[N], float r, const Staged<W, VEC>& gamma,
-                                          const Staged<W, VEC>& beta, T* y, int lane, int lanes, int cols) {
+                                          const Staged<W, VEC>& beta, T* y, int lane, int lanes, int cols, F store) {
     const Pair r2(r, r);
     if constexpr (VEC == 1) {
 #pragma unroll
@@ -233,7 +234,7 @@ __device__ __forceinline__ void normalise(const Pair (&v)[N], float r, const Sta
             for (int i = 0; i < VEC / 2; ++i)
                 set_pair(out, i,
                          fma2(mul2(v[k * (VEC / 2) + i], r2), Pair(g[2 * i], g[2 * i + 1]), Pair(b[2 * i], b[2 * i + 1])));
-            store_pack<T, VEC>(y + c, VEC, out);
+            store(c, out);
         }
     }
 }
@@ -400,15 +401,79 @@ __device__ __forceinline__ void init_ring(RingBarriers& ring, int slots) {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
+// Rows off the 16-byte boundaries, in packs all the same: a pack is a 16-byte unit of the
+// memory, from the one that the row begins in, so the row's elements stand at the positions
+// off .. end - 1 from there.  A block's rows are multiples of gridDim.x rows apart, which is a
+// multiple of 16 bytes (152 SMs are), so they share `off` and a lane keeps its columns; and
+// what is read and what is written have the same `off` (else single elements move).  Warps
+// with the row's ends take more steps for them.  10000 x 5003 bf16: forward 51 us, backward
+// 110; with single elements 71 and 160; rows of 5008 take 40 and 75.
+template <int VEC>
+struct Span {
+    int off, end;
+    __device__ __forceinline__ bool holds(int p) const { return p >= off && p + VEC <= end; }     // a whole pack
+    __device__ __forceinline__ bool has(int p) const { return p >= off && p < end; }
+    // all packs of a warp's lanes
+    __device__ __forceinline__ bool holds_all(int lane, int lanes, int packs) const {
+        return __all_sync(0xffffffffu, lane * VEC >= off && ((packs - 1) * lanes + lane + 1) * VEC <= end);
+    }
+    // A row's packs; `unguarded`: the units around it may be read.
+    template <typename T, int PACKS>
+    __device__ __forceinline__ void load(Pack<T, VEC> (&q)[PACKS], const T* row, bool unguarded, int lane, int lanes) const {
+#pragma unroll
+        for (int k = 0; k < PACKS; ++k) {
+            const int p = (k * lanes + lane) * VEC;
+            if (p >= end) {
+                q[k].clear();
+            } else if (unguarded || holds(p)) {
+                q[k] = load_pack<T, VEC>(row + (p - off), VEC);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) q[k].set_raw(i, has(p + i) ? row[p - off + i] : from_f32<T>(0.f));
+            }
+        }
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(T* row, int p, const Pack<T, VEC>& q) const {
+        if (holds(p)) {
+            store_pack<T, VEC>(row + (p - off), VEC, q);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (has(p + i)) row[p - off + i] = reinterpret_cast<const T*>(&q.raw)[i];
+        }
+    }
+    // Zeros where the row has no elements.
+    template <int N>
+    __device__ __forceinline__ void clear(Pair (&v)[N], int lane, int lanes) const {
+#pragma unroll
+        for (int k = 0; k < 2 * N / VEC; ++k) {
+            const int p = (k * lanes + lane) * VEC;
+            if (holds(p)) continue;
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i) {
+                float lo, hi;
+                v[k * (VEC / 2) + i].get(lo, hi);
+                v[k * (VEC / 2) + i] = Pair(has(p + 2 * i) ? lo : 0.f, has(p + 2 * i + 1) ? hi : 0.f);
+            }
+        }
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ int off_of_row(const T* base, int64_t ld, int64_t row) {
+    return static_cast<int>((reinterpret_cast<uintptr_t>(base + row * ld) & 15u) / sizeof(T));
+}
+
 // gamma and beta wait in shared memory behind the rings.  COLS columns a lane: with 32 a row
 // takes half the warps of 16, and so half the work that does not depend on its length.
-template <typename T, typename W, int VEC, int COLS>
+template <typename T, typename W, int VEC, int COLS, bool SHIFT>
 __global__ void __launch_bounds__(kForwardRing, 1) norm_forward_ring_kernel(const ForwardArgs<T, W> a, int stages) {
     extern __shared__ __align__(128) uint8_t memory[];
     __shared__ RingBarriers barriers;
     __shared__ float part[kForwardRing / 32][2][1][32];
     const int lanes = a.lanes, groups = kForwardRing / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-    constexpr bool kAny = VEC == 1;
+    constexpr bool kAny = VEC == 1 || SHIFT;
     const int row_bytes = a.cols * static_cast<int>(sizeof(T)), stage_bytes = ring_stage_bytes(row_bytes, kAny);
     Staged<W, VEC> gamma{reinterpret_cast<W*>(memory + groups * stages * stage_bytes), lanes * COLS / 2};
     Staged<W, VEC> beta{gamma.at + lanes * COLS, gamma.half};
@@ -432,11 +497,14 @@ __global__ void __launch_bounds__(kForwardRing, 1) norm_forward_ring_kernel(cons
                  {0, 0},
                  0};
     if (lane == 0 && group < groups) ring.begin(row);
+    const int off = SHIFT ? off_of_row(a.x, a.ldx, blockIdx.x) : 0;
     for (int c = threadIdx.x; c < a.cols; c += kForwardRing) {
-        gamma.put(c, a.gamma ? a.gamma[c] : from_f32<W>(1.f));
-        beta.put(c, a.beta ? a.beta[c] : from_f32<W>(0.f));
+        gamma.put(c + off, a.gamma ? a.gamma[c] : from_f32<W>(1.f));
+        beta.put(c + off, a.beta ? a.beta[c] : from_f32<W>(0.f));
     }
     __syncthreads();
+    const Span<VEC> span{off, off + a.cols};
+    const bool inner = SHIFT && span.holds_all(lane, lanes, COLS / VEC);
     const bool full = a.cols == lanes * COLS;
     const float inverse_n = 1.f / static_cast<float>(a.cols);
     GroupSum<1> sum{part[group], lanes, group, 0};       // (barrier 0 is free from here on)
@@ -447,13 +515,31 @@ __global__ void __launch_bounds__(kForwardRing, 1) norm_forward_ring_kernel(cons
         {
             RowPacks<T, VEC, COLS, true> in;
             ring.wait();
-            in.load(reinterpret_cast<const T*>(ring.at(0, row)), lane, lanes, a.cols);
-            to_pairs(in.p, v);
+            const T* from = reinterpret_cast<const T*>(ring.at(0, row));
+            if constexpr (SHIFT) {
+                if (inner) {
+                    in.load(from - off, lane, lanes, span.end);
+                } else {
+                    span.load(in.p, from, !ring.direct(row), lane, lanes);
+                }
+                to_pairs(in.p, v);
+                if (!inner) span.clear(v, lane, lanes);
+            } else {
+                in.load(from, lane, lanes, a.cols);
+                to_pairs(in.p, v);
+            }
         }
-        const float mu = centre<VEC>(v, sum, inverse_n, full, lane, lanes, a.cols);
+        const float mu = centre<VEC>(v, sum, inverse_n, SHIFT || full, lane, lanes, a.cols);
+        if (SHIFT && !inner) span.clear(v, lane, lanes);
         ring.refill(lane, ring.turn.at, row + stages * ring.step);
         const float r = rstd_of(v, sum, inverse_n, a.eps, lane);
-        normalise<T, W, VEC>(v, r, gamma, beta, y, lane, lanes, a.cols);
+        normalise<T, W, VEC>(v, r, gamma, beta, y, lane, lanes, span.end, [&](int p, const Pack<T, VEC>& q) {
+            if (!SHIFT || inner) {
+                store_pack<T, VEC>(y + (p - off), VEC, q);
+            } else {
+                span.store(y, p, q);
+            }
+        });
         if (lane == 0) {
             if (a.mean) a.mean[row] = mu;
             if (a.rstd) a.rstd[row] = r;
@@ -487,13 +573,18 @@ __device__ __forceinline__ void row_sums(Pair sum_g, Pair sum_gx, GroupSum<2>& s
     sum(s, lane);
 }
 
-template <typename T, int VEC, bool WHOLE>
-__device__ __forceinline__ void write_dx(const Pair (&hat)[kPairs], Pair (&g)[kPairs], const float (&s)[2], float inverse_n,
-                                         Pair r2, T* dx, int lane, int lanes, int cols) {
+__device__ __forceinline__ void dx_of(const Pair (&hat)[kPairs], Pair (&g)[kPairs], const float (&s)[2], float inverse_n,
+                                      Pair r2) {
     const float mean_g = s[0] * inverse_n, mean_gx = s[1] * inverse_n;
     const Pair minus_g(-mean_g, -mean_g), minus_gx(-mean_gx, -mean_gx);
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) g[j] = mul2(r2, fma2(hat[j], minus_gx, add2(g[j], minus_g)));
+}
+
+template <typename T, int VEC, bool WHOLE>
+__device__ __forceinline__ void write_dx(const Pair (&hat)[kPairs], Pair (&g)[kPairs], const float (&s)[2], float inverse_n,
+                                         Pair r2, T* dx, int lane, int lanes, int cols) {
+    dx_of(hat, g, s, inverse_n, r2);
     RowPacks<T, VEC, kLaneCols, WHOLE> out;
     from_pairs(g, out.p);
     out.store(dx, lane, lanes, cols);
@@ -513,10 +604,11 @@ __device__ __forceinline__ void copy_partial(int lanes, int cols, const float* j
 }
 
 // The sums of a block's groups, joined in the order of the groups through shared memory
-// (`join`: [groups][2][lanes * kLaneCols], by column), to its rows of the partial sums.
-template <int VEC, int THREADS>
+// (`join`: [groups][2][lanes * kLaneCols], group g's column c at c + off_of(g)), to its rows of
+// the partial sums.
+template <int VEC, int THREADS, typename F>
 __device__ __forceinline__ void write_partial(const Pair (&dg)[kPairs], const Pair (&db)[kPairs], int group, int groups,
-                                              int lane, int lanes, int cols, float* join, float* partial) {
+                                              int lane, int lanes, int cols, F off_of, float* join, float* partial) {
     const int width = lanes * kLaneCols;
     if (group < groups) {
 #pragma unroll
@@ -538,8 +630,8 @@ __device__ __forceinline__ void write_partial(const Pair (&dg)[kPairs], const Pa
     for (int which = 0; which < 2; ++which) {
         float* out = partial + (static_cast<int64_t>(which) * gridDim.x + blockIdx.x) * cols;
         for (int c = threadIdx.x; c < cols; c += THREADS) {
-            float s = join[which * width + c];
-            for (int g = 1; g < groups; ++g) s += join[(g * 2 + which) * width + c];
+            float s = join[which * width + c + off_of(0)];
+            for (int g = 1; g < groups; ++g) s += join[(g * 2 + which) * width + c + off_of(g)];
             out[c] = s;
         }
     }
@@ -620,18 +712,18 @@ __global__ void __launch_bounds__(BLOCK) norm_backward_kernel(const BackwardArgs
         __syncthreads();
         copy_partial<VEC, BLOCK>(lanes, a.cols, join, a.partial);
     } else {
-        write_partial<VEC, BLOCK>(dg, db, group, groups, lane, lanes, a.cols, join, a.partial);
+        write_partial<VEC, BLOCK>(dg, db, group, groups, lane, lanes, a.cols, [](int) { return 0; }, join, a.partial);
     }
 }
 
 // The same through rings of stages that hold a row of x and one of dy.
-template <typename T, typename W, int VEC>
+template <typename T, typename W, int VEC, bool SHIFT>
 __global__ void __launch_bounds__(kBackwardRing, 1) norm_backward_ring_kernel(const BackwardArgs<T, W> a, int stages) {
     extern __shared__ __align__(128) uint8_t memory[];
     __shared__ RingBarriers barriers;
     __shared__ float part[kBackwardRing / 32][2][2][32];
     const int lanes = a.lanes, groups = kBackwardRing / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-    constexpr bool kAny = VEC == 1;
+    constexpr bool kAny = VEC == 1 || SHIFT;
     const int row_bytes = a.cols * static_cast<int>(sizeof(T)), stage_bytes = ring_stage_bytes(row_bytes, kAny);
     if (threadIdx.x == 0) init_ring(barriers, groups * stages);
     __syncthreads();
@@ -658,7 +750,19 @@ __global__ void __launch_bounds__(kBackwardRing, 1) norm_backward_ring_kernel(co
     Pair dg[kPairs], db[kPairs], gamma[kPairs];
 #pragma unroll
     for (int j = 0; j < kPairs; ++j) dg[j] = db[j] = Pair(0.f, 0.f);
-    load_weights<W, VEC, kLaneCols>(a.gamma, 1.f, lane, lanes, a.cols, gamma);
+    const int off = SHIFT ? off_of_row(a.x, a.ldx, row) : 0;
+    const Span<VEC> span{off, off + a.cols};
+    const bool inner = SHIFT && span.holds_all(lane, lanes, kLaneCols / VEC);
+    if constexpr (SHIFT) {
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            const int p = (2 * j / VEC * lanes + lane) * VEC + 2 * j % VEC;
+            const auto weight = [&](int q) { return !span.has(q) ? 0.f : a.gamma ? to_f32(a.gamma[q - off]) : 1.f; };
+            gamma[j] = Pair(weight(p), weight(p + 1));
+        }
+    } else {
+        load_weights<W, VEC, kLaneCols>(a.gamma, 1.f, lane, lanes, a.cols, gamma);
+    }
     float next_mean = 0.f, next_rstd = 0.f;
     const auto ask = [&](int64_t r) {
         next_mean = a.mean[r];
@@ -674,10 +778,20 @@ __global__ void __launch_bounds__(kBackwardRing, 1) norm_backward_ring_kernel(co
         {
             RowPacks<T, VEC, kLaneCols, true> x, dy;
             ring.wait();
-            x.load(reinterpret_cast<const T*>(ring.at(0, row)), lane, lanes, a.cols);
-            dy.load(reinterpret_cast<const T*>(ring.at(1, row)), lane, lanes, a.cols);
+            const T *from_x = reinterpret_cast<const T*>(ring.at(0, row)), *from_dy = reinterpret_cast<const T*>(ring.at(1, row));
+            if (SHIFT && !inner) {
+                span.load(x.p, from_x, !ring.direct(row), lane, lanes);
+                span.load(dy.p, from_dy, !ring.direct(row), lane, lanes);
+            } else {
+                x.load(from_x - off, lane, lanes, span.end);
+                dy.load(from_dy - off, lane, lanes, span.end);
+            }
             to_pairs(x.p, hat);
             to_pairs(dy.p, g);
+            if (SHIFT && !inner) {
+                span.clear(hat, lane, lanes);
+                span.clear(g, lane, lanes);
+            }
         }
         const Pair minus(-mu, -mu), r2(r, r);
         Pair sum_g(0.f, 0.f), sum_gx(0.f, 0.f);
@@ -693,13 +807,24 @@ __global__ void __launch_bounds__(kBackwardRing, 1) norm_backward_ring_kernel(co
         float s[2];
         row_sums(sum_g, sum_gx, sum, lane, s);
         ring.refill(lane, ring.turn.at, row + stages * ring.step);
-        if (a.dx) write_dx<T, VEC, true>(hat, g, s, inverse_n, r2, dx, lane, lanes, a.cols);
+        if (!a.dx) continue;
+        if (SHIFT && !inner) {
+            RowPacks<T, VEC, kLaneCols, true> out;
+            dx_of(hat, g, s, inverse_n, r2);
+            from_pairs(g, out.p);
+#pragma unroll
+            for (int k = 0; k < kLaneCols / VEC; ++k) span.store(dx, (k * lanes + lane) * VEC, out.p[k]);
+        } else {
+            write_dx<T, VEC, true>(hat, g, s, inverse_n, r2, dx - off, lane, lanes, span.end);
+        }
     }
     if (lane == 0 && group < groups) ring.end();
     if (!a.weights) return;
     __syncthreads();                                     // the rings have been read: their memory joins the groups
-    write_partial<VEC, kBackwardRing>(dg, db, group, groups, lane, lanes, a.cols, reinterpret_cast<float*>(memory),
-                                      a.partial);
+    write_partial<VEC, kBackwardRing>(
+        dg, db, group, groups, lane, lanes, a.cols,
+        [&](int g) { return SHIFT ? off_of_row(a.x, a.ldx, static_cast<int64_t>(blockIdx.x) + g * gridDim.x) : 0; },
+        reinterpret_cast<float*>(memory), a.partial);
 }
 
 // A lane's columns of a row, in pairs: f(pair, x, dy, gamma).
@@ -803,8 +928,8 @@ __global__ void __launch_bounds__(kWideRing, 1) norm_backward_wide_ring_kernel(c
     if (lane == 0 && group < groups) ring.end();
     if (!a.weights) return;
     __syncthreads();                                     // the rings have been read: their memory joins the groups
-    write_partial<VEC, kWideRing>(dg, db, group, groups, lane, lanes, a.cols, reinterpret_cast<float*>(memory),
-                                      a.partial);
+    write_partial<VEC, kWideRing>(dg, db, group, groups, lane, lanes, a.cols, [](int) { return 0; }, reinterpret_cast<float*>(memory),
+                                  a.partial);
 }
 
 // The blocks' sums of 32 columns: eight warps take every eighth block, then join, in an order
@@ -976,11 +1101,41 @@ int ring_stages(int cols, int vec, int64_t row_bytes, int sources, int lanes, in
     return stages < 2 ? 0 : static_cast<int>(stages);
 }
 
+// Whether rows of both matrices can move in packs off the 16-byte boundaries (see Span), in
+// blocks whose rows are multiples of `step` apart.
+template <typename T>
+bool can_shift(const T* a, int64_t lda, const T* b, int64_t ldb, int64_t step) {
+    constexpr int64_t kBytes = sizeof(T);
+    return ((reinterpret_cast<uintptr_t>(a) ^ reinterpret_cast<uintptr_t>(b)) & 15u) == 0 &&
+           (lda - ldb) * kBytes % 16 == 0 && step * lda * kBytes % 16 == 0;
+}
+
+// Rows of any length and alignment in packs, through rings; false where that does not suit.
+// (fp32 elements are wide enough by themselves: 8000 x 4501 backward 118 us so, 125 in packs;
+// and in short rows the warps at the ends are too many: 40000 x 333 fp16 24 and 28 us.)
+template <typename T, typename W>
+bool forward_shifted(const ForwardArgs<T, W>& a, int sms, Queue queue, gemm_status_t* status) {
+    if constexpr (sizeof(T) == 2) {
+        constexpr int kCols = 32;
+        ForwardArgs<T, W> b = a;
+        b.lanes = ring_lanes(a.cols + 7, kCols);
+        const int64_t stage = ring_stage_bytes(a.cols * 2, true);
+        const int64_t weights = int64_t{2} * b.lanes * kCols * static_cast<int64_t>(sizeof(W));
+        const int stages = ring_stages(a.cols, 1, stage, 1, b.lanes, kForwardRing, weights, a.rows, sms);
+        if (a.cols <= 512 || stages == 0 || !can_shift<T>(a.x, a.ldx, a.y, a.ldy, sms)) return false;
+        const size_t smem = static_cast<size_t>(kForwardRing / b.lanes * stages * stage + weights);
+        *status = launch<norm_forward_ring_kernel<T, W, 8, kCols, true>>(sms, kForwardRing, smem, queue, 1, b, stages);
+        return true;
+    }
+    return false;
+}
+
 template <typename T, typename W, int VEC>
 gemm_status_t forward_vec(const ForwardArgs<T, W>& a, int sms, Queue queue) {
     if constexpr (VEC > 1) {
         // rows that end inside a pack: element by element through rings where there are many
-        // (10000 x 5003 bf16, aligned: 72 us; in registers with a partial pack 141 us)
+        // that the packs of Span do not take (10000 x 5003 bf16, aligned: 72 us; in registers with
+        // a partial pack 141 us)
         const int64_t stage = ring_stage_bytes(a.cols * static_cast<int>(sizeof(T)), true);
         const int lanes = ring_lanes(a.cols, kLaneCols);
         const int64_t weights = int64_t{2} * lanes * kLaneCols * static_cast<int64_t>(sizeof(W));
@@ -997,9 +1152,10 @@ gemm_status_t forward_vec(const ForwardArgs<T, W>& a, int sms, Queue queue) {
     if (stages > 0) {
         const size_t smem = static_cast<size_t>(kForwardRing / b.lanes * stages * stage + weights);
         if constexpr (VEC > 1) {
-            if (half) return launch<norm_forward_ring_kernel<T, W, VEC, 32>>(sms, kForwardRing, smem, queue, 1, b, stages);
+            if (half)
+                return launch<norm_forward_ring_kernel<T, W, VEC, 32, false>>(sms, kForwardRing, smem, queue, 1, b, stages);
         }
-        return launch<norm_forward_ring_kernel<T, W, VEC, 16>>(sms, kForwardRing, smem, queue, 1, b, stages);
+        return launch<norm_forward_ring_kernel<T, W, VEC, 16, false>>(sms, kForwardRing, smem, queue, 1, b, stages);
     }
     if (a.lanes <= 256) return forward_rows<T, W, VEC, 256, true>(a, sms, queue);
     if (a.lanes == 512) return forward_rows<T, W, VEC, 512, true>(a, sms, queue);
@@ -1024,10 +1180,18 @@ gemm_status_t prepare() {
     const auto allow_ring = [](auto kernel) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingShared) == cudaSuccess;
     };
-    if (allow_ring(norm_forward_ring_kernel<T, W, kVec, 16>) && allow_ring(norm_forward_ring_kernel<T, W, kVec, 32>) &&
-        allow_ring(norm_forward_ring_kernel<T, W, 1, 16>) &&
-        allow_ring(norm_backward_ring_kernel<T, W, kVec>) && allow_ring(norm_backward_wide_ring_kernel<T, W, kVec>) &&
-        allow_ring(norm_backward_ring_kernel<T, W, 1>) &&
+    if constexpr (sizeof(T) == 2) {
+        if (!allow_ring(norm_forward_ring_kernel<T, W, 8, 32, true>) || !allow_ring(norm_backward_ring_kernel<T, W, 8, true>)) {
+            cudaGetLastError();
+            return GEMM_ERR_LAUNCH;
+        }
+    }
+    if (allow_ring(norm_forward_ring_kernel<T, W, kVec, 16, false>) &&
+        allow_ring(norm_forward_ring_kernel<T, W, kVec, 32, false>) &&
+        allow_ring(norm_forward_ring_kernel<T, W, 1, 16, false>) &&
+        allow_ring(norm_backward_ring_kernel<T, W, kVec, false>) &&
+        allow_ring(norm_backward_ring_kernel<T, W, 1, false>) &&
+        allow_ring(norm_backward_wide_ring_kernel<T, W, kVec>) &&
         allow(norm_backward_kernel<T, W, kVec, 512, false>, 512) && allow(norm_backward_kernel<T, W, 1, 512, false>, 512) &&
         allow(norm_backward_kernel<T, W, kVec, 1024, true>, 1024) && allow(norm_backward_kernel<T, W, 1, 1024, true>, 1024))
         return GEMM_OK;
@@ -1043,6 +1207,26 @@ int64_t backward_blocks(int64_t rows, int lanes, int sms) {
     return blocks < sms ? blocks : sms;
 }
 
+template <typename T, typename W>
+bool backward_shifted(const BackwardArgs<T, W>& a, int blocks, int sms, Queue queue, gemm_status_t* status) {
+    if constexpr (sizeof(T) == 2) {
+        BackwardArgs<T, W> b = a;
+        b.lanes = ring_lanes(a.cols + 7, kLaneCols);
+        const int64_t stage = ring_stage_bytes(a.cols * 2, true);
+        const int stages = ring_stages(a.cols, 1, stage, 2, b.lanes, kBackwardRing, 0, a.rows, sms);
+        if (stages == 0 || !can_shift<T>(a.x, a.ldx, a.dy, a.lddy, blocks) ||
+            (a.dx && !can_shift<T>(a.x, a.ldx, a.dx, a.lddx, blocks)))
+            return false;
+        const int groups = kBackwardRing / b.lanes;
+        const size_t ring = static_cast<size_t>(2 * groups * stages * stage);
+        const size_t join = static_cast<size_t>(groups * b.lanes) * kLaneCols * 2 * sizeof(float);
+        *status = launch<norm_backward_ring_kernel<T, W, 8, true>>(blocks, kBackwardRing, ring > join ? ring : join, queue,
+                         1, b, stages);
+        return true;
+    }
+    return false;
+}
+
 template <typename T, typename W, int VEC>
 gemm_status_t backward_vec(const BackwardArgs<T, W>& a, int blocks, int sms, Queue queue) {
     BackwardArgs<T, W> b = a;
@@ -1052,7 +1236,7 @@ gemm_status_t backward_vec(const BackwardArgs<T, W>& a, int blocks, int sms, Que
     if (stages > 0) {
         const size_t ring = static_cast<size_t>(2 * (kBackwardRing / b.lanes) * stages * stage);
         const size_t join = static_cast<size_t>(kBackwardRing / b.lanes * b.lanes) * kLaneCols * 2 * sizeof(float);
-        return launch<norm_backward_ring_kernel<T, W, VEC>>(blocks, kBackwardRing, ring > join ? ring : join, queue, 1,
+        return launch<norm_backward_ring_kernel<T, W, VEC, false>>(blocks, kBackwardRing, ring > join ? ring : join, queue, 1,
                       b, stages);
     }
     if constexpr (VEC > 1) {
@@ -1151,6 +1335,9 @@ gemm_status_t gemm_norm_forward(gemm_norm_plan_t p, int64_t rows, const void* x,
         const bool vec = gbt::rows_aligned(x, ldx, e) && gbt::rows_aligned(y, ldy, e) &&
                          gbt::aligned(gamma, 16) && gbt::aligned(beta, 16);
         constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+        const bool whole = vec && p->cols % kVec == 0;
+        gemm_status_t status = GEMM_OK;
+        if (!whole && gbt::forward_shifted<T, W>(a, p->num_sms, queue, &status)) return status;
         return vec ? gbt::forward_vec<T, W, kVec>(a, p->num_sms, queue)
                    : gbt::forward_vec<T, W, 1>(a, p->num_sms, queue);
     });
@@ -1197,8 +1384,10 @@ gemm_status_t gemm_norm_backward(gemm_norm_plan_t p, int64_t rows, const void* x
             const bool vec = gbt::rows_aligned(x, ldx, e) && gbt::rows_aligned(dy, lddy, e) &&
                              (!dx || gbt::rows_aligned(dx, lddx, e)) && gbt::aligned(gamma, 16);
             constexpr int kVec = 16 / static_cast<int>(sizeof(T));
-            s = vec ? gbt::backward_vec<T, W, kVec>(a, blocks, p->num_sms, queue)
-                    : gbt::backward_vec<T, W, 1>(a, blocks, p->num_sms, queue);
+            const bool whole = vec && p->cols % kVec == 0;
+            if (whole || !gbt::backward_shifted<T, W>(a, blocks, p->num_sms, queue, &s))
+                s = vec ? gbt::backward_vec<T, W, kVec>(a, blocks, p->num_sms, queue)
+                        : gbt::backward_vec<T, W, 1>(a, blocks, p->num_sms, queue);
         }
         if (s == GEMM_OK && a.weights)
             s = gbt::launch<gbt::norm_weight_join_kernel<W>>(2 * tiles, gbt::kThreads, 0, queue, 1,

@@ -106,6 +106,46 @@ def test_norm(gemm_lib, rows, cols, elem, weight, pad, offset):
         assert all(torch.equal(a, c[k]) for a, k in zip(first, ("y", "dx", "dgamma", "dbeta")))
 
 
+@pytest.mark.parametrize("rows,cols", [(10003, 259), (5003, 1003), (2511, 2049), (1301, 4090), (661, 8185), (331, 16377)])
+@pytest.mark.parametrize("elem,weight", [("bf16", "bf16"), ("f16", "f32"), ("f32", "f32")])
+def test_norm_rows_off_boundaries(gemm_lib, rows, cols, elem, weight):
+    """Contiguous rows of odd lengths, each of which begins inside its neighbour's last 16 bytes."""
+    c = _norm_case(rows, cols, elem, weight, 0, 0, seed=3)
+    with gemm_lib.NormPlan(rows, cols, elem, weight=weight) as plan:
+        def run(x, dy, y, dx):
+            plan.forward(x, c["gamma"], c["beta"], y, c["mean"], c["rstd"])
+            plan.backward(x, c["gamma"], c["mean"], c["rstd"], dy, dx, c["dgamma"], c["dbeta"])
+        run(c["x"], c["dy"], c["y"], c["dx"])
+        torch.cuda.synchronize()
+        _check_norm(c, elem, weight)
+        _canary_whole(c["y"])
+        _canary_whole(c["dx"])
+        y, dx = c["y"].clone(), c["dx"].clone()
+        # in place, the same bits
+        over = c["x"].clone()
+        plan.forward(over, c["gamma"], c["beta"], over)
+        assert torch.equal(over, y)
+        over = c["dy"].clone()
+        plan.backward(c["x"], c["gamma"], c["mean"], c["rstd"], over, over)
+        assert torch.equal(over, dx)
+        # results at other offsets than the inputs': right as well
+        c["y"], c["dx"] = (_rows(np.zeros((rows, cols)), elem, 2, 1) for _ in range(2))
+        run(c["x"], c["dy"], c["y"], c["dx"])
+        torch.cuda.synchronize()
+        _check_norm(c, elem, weight)
+        # a row's bad values at its ends stay out of its neighbours
+        bad = [0, 7, 160, rows - 1]
+        clean = torch.ones(rows, dtype=torch.bool, device="cuda")
+        clean[bad] = False
+        for r, at in zip(bad, (-1, 0, -1, 0)):
+            c["x"][r, at] = math.nan
+        c["dy"][7, -1] = math.inf
+        run(c["x"], c["dy"], y, dx)
+        for name, t in (("y", y), ("dx", dx)):
+            assert bool(torch.isfinite(t[clean]).all()), name
+            assert not bool(torch.isfinite(t[~clean]).any(dim=1).any()), name
+
+
 @pytest.mark.parametrize("rows,cols", [(5, 64), (37, 1000), (3, 4096), (2, 16400)])
 def test_norm_parts(gemm_lib, rows, cols):
     """Without gamma, beta or statistics; each gradient alone; results in place."""
