@@ -1089,12 +1089,15 @@ gemm_status_t forward_rows(const ForwardArgs<T, W>& a, int sms, Queue queue) {
 // Stages of a group's ring whose block also needs `fixed` bytes; 0 where rings do not suit:
 // rows of no whole packs, rows too short for a copy each (65536 x 256 bf16: 27 us by rings, 23
 // in registers; single elements take longer to load, and rings pay from half that length), or
-// too few rows for two to each group of each SM's block.
+// too few rows.  Forward a quarter of the groups with a row each is enough, as all rows are
+// asked for at once (1000 x 4096 bf16 5.3 us, 8.0 in registers; 600 x 4096 4.3 and 5.3; 300 x
+// 4096, below the limit, 3.7 and 3.2); backward, with partial sums a block, every group should
+// have one (300 x 16384 22 us and 29; 600 x 2048 11.1 and 10.9).
 int ring_stages(int cols, int vec, int64_t row_bytes, int sources, int lanes, int threads, int64_t fixed, int64_t rows,
                 int sms) {
     const int groups = threads / lanes;
     if (groups == 0 || row_bytes < (vec == 1 ? 512 : 1024) || cols % vec != 0 ||
-        rows < int64_t{2} * sms * groups || rows > kRingRows)
+        rows < int64_t{sms} * groups / (sources == 1 ? 4 : 1) || rows > kRingRows)
         return 0;
     int64_t stages = (kRingShared - fixed) / (row_bytes * sources * groups);
     if (stages > kRingSlots / groups) stages = kRingSlots / groups;
