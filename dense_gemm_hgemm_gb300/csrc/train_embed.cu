@@ -86,7 +86,7 @@ embed_forward_kernel(const LookupParams p, const T* __restrict__ table, T* __res
         }
 #pragma unroll
         for (int u = 0; u < TOKENS; ++u) {
-            if (first + u >= p.tokens) return;
+            if (first + u >= p.tokens) break;            // (the tokens before go on with further columns)
 #pragma unroll
             for (int k = 0; k < PACKS; ++k) {
                 const int c = c0 + k * p.lanes * VEC;

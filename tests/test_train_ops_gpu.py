@@ -106,7 +106,8 @@ def test_norm(gemm_lib, rows, cols, elem, weight, pad, offset):
         assert all(torch.equal(a, c[k]) for a, k in zip(first, ("y", "dx", "dgamma", "dbeta")))
 
 
-@pytest.mark.parametrize("rows,cols", [(10003, 259), (5003, 1003), (2511, 2049), (1301, 4090), (661, 8185), (331, 16377)])
+@pytest.mark.parametrize("rows,cols", [(10003, 259), (5003, 1003), (2511, 2049), (1301, 4090), (661, 8185), (331, 16377),
+                                       (1300, 1003), (320, 4099), (165, 8190)])
 @pytest.mark.parametrize("elem,weight", [("bf16", "bf16"), ("f16", "f32"), ("f32", "f32")])
 def test_norm_rows_off_boundaries(gemm_lib, rows, cols, elem, weight):
     """Contiguous rows of odd lengths, each of which begins inside its neighbour's last 16 bytes."""
@@ -254,6 +255,21 @@ def _embed_case(n, vocab, dim, elem, grad, index, pad, offset):
             "out": _rows(np.zeros((n, dim)), elem, pad, offset),
             "dout": _rows(rng.normal(size=(n, dim)), elem, pad, offset),
             "dtable": _rows(rng.normal(size=(vocab, dim)), grad, pad, offset)}
+
+
+@pytest.mark.parametrize("elem,n,dim", [("bf16", 4865, 8200), ("f16", 4866, 4104), ("f32", 4867, 4100), ("f32", 9731, 1500),
+                                        ("bf16", 38915, 300), ("bf16", 155651, 128), ("f16", 19459, 97),
+                                        ("bf16", 9730, 2080), ("f32", 77826, 60)])
+def test_lookup_of_many_tokens(gemm_lib, elem, n, dim):
+    """Token counts that leave the last group of tokens incomplete, rows of several steps: every element."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    table = torch.randn(700, dim, generator=gen, device="cuda").to(TYPES[elem])
+    ids = torch.randint(0, 700, (n,), generator=gen, device="cuda")
+    out = torch.full((n + 1, dim), 99.0, dtype=TYPES[elem], device="cuda")
+    with gemm_lib.EmbedPlan(700, dim, n, elem) as plan:
+        plan.forward(ids, table, out[:n], scale=2.0)
+    assert torch.equal(out[:n], 2 * table[ids])
+    assert bool((out[n] == 99).all())
 
 
 @pytest.mark.parametrize("n,vocab,dim", EMBED_SIZES)
