@@ -290,7 +290,18 @@ __device__ __forceinline__ void cluster_barrier() {
 
 // ---- asynchronous copies into a ring of buffers ------------------------------------
 
-constexpr long long kWaitNs = 2000000000ll;     // the longest wait in a kernel
+constexpr uint32_t kWaitNs = 2000000000u;       // the longest wait in a kernel, by default
+
+// A plan's limit of a wait, and its test hook: bytes that the copies of every `every`-th block
+// wait for beyond what they bring.
+struct Waits {
+    uint32_t limit = kWaitNs;            // ns, by the timer's lower word (which wraps after 4.29 s)
+    uint32_t extra = 0, every = 1;
+    __device__ __forceinline__ uint32_t extra_bytes() const {
+        return extra == 0 || blockIdx.x % every != every - 1 ? 0 : extra;
+    }
+};
+
 constexpr int32_t kErrorIndex = 1;              // bits of a plan's error word
 constexpr int32_t kErrorTimeout = 2;
 
@@ -298,10 +309,10 @@ __device__ __forceinline__ uint32_t shared_address(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-// Waits for a phase of the barrier, at most kWaitNs.
-__device__ inline bool wait_phase(uint64_t* barrier, uint32_t parity) {
+// Waits for a phase of the barrier, at most `limit` ns.
+__device__ inline bool wait_phase(uint64_t* barrier, uint32_t parity, uint32_t limit) {
     const uint32_t at = shared_address(barrier);
-    long long began = 0;
+    uint32_t began = 0;
     for (uint32_t tries = 0;; ++tries) {
         uint32_t done;
         asm volatile(
@@ -310,10 +321,10 @@ __device__ inline bool wait_phase(uint64_t* barrier, uint32_t parity) {
             "selp.u32 %0, 1, 0, p;\n}"
             : "=r"(done) : "r"(at), "r"(parity) : "memory");
         if (done) return true;
-        long long now;
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        uint32_t now;
+        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
         if (tries == 0) began = now;
-        if (now - began > kWaitNs) return false;
+        if (now - began > limit) return false;
     }
 }
 
@@ -327,9 +338,10 @@ struct Turn {
 };
 
 // As wait_phase, for whole warps; when it runs out (or another wait has) it returns at once from then on.
-__device__ __forceinline__ void wait_or_die(uint64_t* barrier, uint32_t parity, int* dead, int32_t* error) {
+__device__ __forceinline__ void wait_or_die(uint64_t* barrier, uint32_t parity, int* dead, int32_t* error,
+                                            uint32_t limit) {
     const uint32_t at = shared_address(barrier);
-    long long began = 0;
+    uint32_t began = 0;
     for (uint32_t tries = 0;; ++tries) {
         uint32_t done;
         asm volatile(
@@ -338,10 +350,10 @@ __device__ __forceinline__ void wait_or_die(uint64_t* barrier, uint32_t parity, 
             "selp.u32 %0, 1, 0, p;\n}"
             : "=r"(done) : "r"(at), "r"(parity) : "memory");
         if (done || *static_cast<volatile int*>(dead)) return;
-        long long now;
-        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        uint32_t now;
+        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
         if (tries == 0) began = now;
-        if (now - began > kWaitNs) {
+        if (now - began > limit) {
             *static_cast<volatile int*>(dead) = 1;
             atomicOr(error, kErrorTimeout);
             return;
@@ -369,6 +381,19 @@ __device__ __forceinline__ void copy_bytes(void* to, const void* from, uint32_t 
 }
 
 // ---- host ---------------------------------------------------------------------
+
+inline gemm_status_t set_wait_limit(Waits* w, uint64_t ns) {
+    constexpr uint64_t kMost = 4000000000u;
+    w->limit = ns == 0 ? kWaitNs : static_cast<uint32_t>(ns < kMost ? ns : kMost);
+    return GEMM_OK;
+}
+
+inline gemm_status_t set_wait_test(Waits* w, uint32_t extra_bytes, uint32_t every) {
+    if (extra_bytes > 4096 || extra_bytes % 16 != 0 || every == 0) return GEMM_ERR_INVALID_ARG;
+    w->extra = extra_bytes;
+    w->every = every;
+    return GEMM_OK;
+}
 
 inline bool valid_elem(gemm_elem_t e) { return e >= GEMM_ELEM_F16 && e <= GEMM_ELEM_F32; }
 inline int elem_bytes(gemm_elem_t e) { return e == GEMM_ELEM_F32 ? 4 : 2; }

@@ -20,6 +20,7 @@ struct gemm_distill_plan {
     gemm_elem_t elem;
     int device, num_sms;
     int32_t* error_word;
+    gbt::Waits waits;
     gbt::StreamShape forward, both;
 };
 
@@ -59,6 +60,7 @@ struct Args {
     float temperature;
     int vocab, piece;      // elements; a piece is a multiple of the pack
     int pieces;            // of a row: blocks that share it
+    Waits waits;
 };
 
 // ---- asynchronous copies ----------------------------------------------------------
@@ -66,9 +68,9 @@ struct Args {
 // The elements of [src, src + n) into shared memory at dst, which has src's offset
 // from a 16-byte boundary: one thread starts a bulk copy of the whole 16-byte units
 // (counted on the barrier), all threads copy the ragged ends.  Past the ends, up to
-// the 16-byte boundaries, go -infinities.
+// the 16-byte boundaries, go -infinities.  `extra`: see Waits.
 template <typename T>
-__device__ __forceinline__ void start_copy(T* dst, const T* src, int n, uint64_t* barrier) {
+__device__ __forceinline__ void start_copy(T* dst, const T* src, int n, uint64_t* barrier, uint32_t extra) {
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     const int off = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15u) / sizeof(T));
     int head = (VEC - off) % VEC;                    // elements before the first boundary
@@ -76,7 +78,7 @@ __device__ __forceinline__ void start_copy(T* dst, const T* src, int n, uint64_t
     const int body = (n - head) / VEC * VEC, tail = n - head - body;
     if (threadIdx.x == 0) {
         const uint32_t bytes = static_cast<uint32_t>(body * static_cast<int>(sizeof(T)));
-        expect_bytes(barrier, bytes);
+        expect_bytes(barrier, bytes + extra);
         if (bytes > 0) copy_bytes(dst + head, src + head, bytes, barrier);
     }
     if (threadIdx.x < VEC) {
@@ -361,8 +363,8 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const Args<T> a) {
     const int packs = (off + n + VEC - 1) / VEC;         // from room on
     bool arrived = true;
     if (!out) {
-        start_copy(s, src, n, &barrier);
-        arrived = wait_phase(&barrier, 0);
+        start_copy(s, src, n, &barrier, a.waits.extra_bytes());
+        arrived = wait_phase(&barrier, 0, a.waits.limit);
         if (!arrived) atomicOr(a.error, kErrorTimeout);
         __syncthreads();                                 // the ragged ends
     }
@@ -441,7 +443,10 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const Args<T> a) {
             a.lse[row] = empty ? -INFINITY : row_q.lse(all);
         }
     }
-    if (!kGrad) return;
+    if (!kGrad) {
+        if (!arrived) wait_phase(&barrier, 0, a.waits.limit);   // no copy may land in a finished block's memory
+        return;
+    }
 
     const bool same = (reinterpret_cast<uintptr_t>(d) & 15u) == (reinterpret_cast<uintptr_t>(src) & 15u);
     const float scale = a.temperature * (a.dloss ? a.dloss[row] : 1.f);
@@ -479,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const Args<T> a) {
                 d[at] = from_f32<T>(scale * (mass * row_q.inverse * exp2_fast(to_f32(s[at]) * c - row_q.base) - p));
         }
     }
-    if (!arrived) wait_phase(&barrier, 0);               // no copy may land in a finished block's memory
+    if (!arrived) wait_phase(&barrier, 0, a.waits.limit);       // (as above)
 }
 
 // ---- many rows: a pipeline over rows -----------------------------------------------------
@@ -517,6 +522,7 @@ struct StreamBarriers {
     float part[2][3][kComputeWarps];
     float mass[kMostSlots], scale[kMostSlots];
     int dead;                // a wait ran out: nothing waits any more
+    uint32_t extra;          // bytes that a stage waits for beyond its copies (see Waits)
 };
 
 __device__ __forceinline__ void compute_barrier() {
@@ -559,6 +565,7 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
         }
         for (int k = 0; k < 2; ++k) init_barrier(&sh.exchanged[k], 1);
         sh.dead = 0;
+        sh.extra = a.waits.extra_bytes();
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -570,7 +577,7 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
         Turn stage{0, 0}, turn{0, 0};
         for (int64_t row = first; row < rows; row += step, turn.next(1, slots)) {
             const int slot = turn.at;
-            wait_or_die(&sh.entries_full[slot], turn.round & 1, &sh.dead, a.error);
+            wait_or_die(&sh.entries_full[slot], turn.round & 1, &sh.dead, a.error, a.waits.limit);
             const bool out = sh.mass[slot] == 0.f;
             __syncwarp();
             if (lane == 0) arrive(&sh.entries_empty[slot]);
@@ -587,7 +594,7 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
                 if (tail_begin + lane < end) tail = base[tail_begin + lane];
             }
             for (int at = 0; at < end; at += kStage) {
-                wait_or_die(&sh.empty[stage.at], (stage.round & 1) ^ 1, &sh.dead, a.error);
+                wait_or_die(&sh.empty[stage.at], (stage.round & 1) ^ 1, &sh.dead, a.error, a.waits.limit);
                 T* const to = ring + stage.at * kStage;
                 const int lo = at == 0 ? head_end : at, hi = min(at + kStage, tail_begin);
                 const bool first_pack = at == 0 && off > 0;
@@ -600,7 +607,7 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
                 __syncwarp();
                 if (lane == 0 && !*static_cast<volatile int*>(&sh.dead)) {
                     const uint32_t bytes = hi > lo ? static_cast<uint32_t>((hi - lo) * static_cast<int>(sizeof(T))) : 0;
-                    expect_bytes(&sh.full[stage.at], bytes);
+                    expect_bytes(&sh.full[stage.at], bytes + sh.extra);
                     if (bytes > 0) copy_bytes(to + (lo - at), base + lo, bytes, &sh.full[stage.at]);
                 }
                 stage.next(1, stages);
@@ -610,7 +617,7 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
         if (*static_cast<volatile int*>(&sh.dead)) {
             for (int s = 0; s < stages; ++s) {
                 const uint32_t issued = stage.round + (s < stage.at ? 1 : 0);
-                if (issued > 0) wait_phase(&sh.full[s], (issued - 1) & 1);
+                if (issued > 0) wait_phase(&sh.full[s], (issued - 1) & 1, a.waits.limit);
             }
         }
     } else if (warp <= kEntryWarps) {                    // the teacher's entries
@@ -618,7 +625,7 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
         for (int64_t row = first + (warp - 1) * step; row < rows;
              row += kEntryWarps * step, turn.next(kEntryWarps, slots)) {
             const int slot = turn.at;
-            wait_or_die(&sh.entries_empty[slot], (turn.round & 1) ^ 1, &sh.dead, a.error);
+            wait_or_die(&sh.entries_empty[slot], (turn.round & 1) ^ 1, &sh.dead, a.error, a.waits.limit);
             const Entries en = entries(slot);
             if (row + kEntryWarps * step < rows) prefetch_entries(a.teacher, row + kEntryWarps * step);
             const float dloss = kGrad && a.dloss ? a.dloss[row] : 1.f;
@@ -638,7 +645,7 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
         Turn stage{0, 0}, entry{0, 0};
         for (int64_t row = first; row < rows; row += step, entry.next(1, slots)) {
             const int slot = entry.at;
-            wait_or_die(&sh.entries_full[slot], entry.round & 1, &sh.dead, a.error);
+            wait_or_die(&sh.entries_full[slot], entry.round & 1, &sh.dead, a.error, a.waits.limit);
             const float mass = sh.mass[slot];
             const Entries en = entries(slot);
             const bool out = mass == 0.f;
@@ -653,7 +660,7 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
             if (!out) {
                 Running<T> run;
                 for (int p0 = 0; p0 < packs; p0 += kStage / VEC) {
-                    wait_or_die(&sh.full[stage.at], stage.round & 1, &sh.dead, a.error);
+                    wait_or_die(&sh.full[stage.at], stage.round & 1, &sh.dead, a.error, a.waits.limit);
                     const T* from = ring + stage.at * kStage + thread * VEC;
                     Pack<T, VEC> q[kBatch];
                     if (packs - p0 >= kStage / VEC) {
@@ -721,7 +728,7 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
                         }
                         __syncwarp();
                     }
-                    wait_or_die(&sh.exchanged[turn], (exchanges >> 1) & 1, &sh.dead, a.error);
+                    wait_or_die(&sh.exchanged[turn], (exchanges >> 1) & 1, &sh.dead, a.error, a.waits.limit);
                     k = sh.exchange[turn][0].x;
                     sum = sh.exchange[turn][0].y;
                     terms = sh.exchange[turn][0].z;
@@ -1110,6 +1117,7 @@ Args<T> arguments(const gemm_distill_plan* p, const void* logits, int64_t ldl, c
     a.temperature = temperature;
     a.vocab = static_cast<int>(p->vocab);
     a.error = p->error_word;
+    a.waits = p->waits;
     return a;
 }
 
@@ -1229,6 +1237,14 @@ gemm_status_t gemm_distill_forward_backward(gemm_distill_plan_t p, int64_t rows,
         const gemm_status_t first = gbt::run_forward_wide(a, rows, queue);
         return first == GEMM_OK ? gbt::run<T, gbt::kBackward>(a, rows, p->num_sms, queue) : first;
     });
+}
+
+gemm_status_t gemm_distill_plan_set_timeout(gemm_distill_plan_t p, uint64_t ns) {
+    return p ? gbt::set_wait_limit(&p->waits, ns) : GEMM_ERR_INVALID_ARG;
+}
+
+gemm_status_t gemm_distill_plan_set_wait_test(gemm_distill_plan_t p, uint32_t extra_bytes, uint32_t every) {
+    return p ? gbt::set_wait_test(&p->waits, extra_bytes, every) : GEMM_ERR_INVALID_ARG;
 }
 
 gemm_status_t gemm_distill_plan_check(gemm_distill_plan_t p, void* stream) {

@@ -362,7 +362,7 @@ struct Ring {
     __device__ __forceinline__ void begin(int row) {
         for (int k = 0; k < stages && row < rows; ++k, row += step) ask(k, row);
     }
-    __device__ __forceinline__ void wait() const { wait_or_die(&full[turn.at], turn.round & 1, dead, error); }
+    __device__ __forceinline__ void wait() const { wait_or_die(&full[turn.at], turn.round & 1, dead, error, kWaitNs); }
     // Source k's row, in the present stage (or in the matrix), once waited for.
     __device__ __forceinline__ const uint8_t* at(int k, int row) const {
         const uint8_t* from = src[k] + row * stride[k];
@@ -380,7 +380,7 @@ struct Ring {
     __device__ __forceinline__ void end() const {
         if (!*static_cast<volatile int*>(dead)) return;
         for (int k = asked > stages ? asked - stages : 0; k < asked; ++k)
-            wait_phase(&full[k % stages], (k / stages) & 1);
+            wait_phase(&full[k % stages], (k / stages) & 1, kWaitNs);
     }
 };
 

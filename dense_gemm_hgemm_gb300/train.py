@@ -45,6 +45,7 @@ class gemm_teacher_t(ctypes.Structure):
 def signatures():
     """(argument types, result type) of the C functions of gemm_train.h."""
     i64, i32, vp, f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_float
+    u64, u32 = ctypes.c_uint64, ctypes.c_uint32
     vpp, teacher = ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(gemm_teacher_t)
     return {
         "gemm_norm_plan_create": ([i64, i64, i32, i32, vpp], i32),
@@ -62,6 +63,8 @@ def signatures():
         "gemm_distill_backward": ([vp, i64, vp, i64, teacher, f32, vp, vp, vp, i64, vp], i32),
         "gemm_distill_forward_backward": ([vp, i64, vp, i64, teacher, f32, vp, vp, vp, vp, i64, vp],
                                           i32),
+        "gemm_distill_plan_set_timeout": ([vp, u64], i32),
+        "gemm_distill_plan_set_wait_test": ([vp, u32, u32], i32),
         "gemm_distill_plan_check": ([vp, vp], i32),
         "gemm_distill_plan_destroy": ([vp], i32),
     }
@@ -359,7 +362,17 @@ class DistillPlan(_Plan):
             _vector(loss, rows, GEMM_ELEM_F32, "loss"), _vector(lse, rows, GEMM_ELEM_F32, "lse"),
             pd, ldd, _stream(stream)), "gemm_distill_forward_backward")
 
+    def set_timeout(self, ns: int) -> None:
+        """The limit of a wait in this plan's kernels, in nanoseconds (0: the default, 2e9)."""
+        _check(library().gemm_distill_plan_set_timeout(self.handle, ns), "gemm_distill_plan_set_timeout")
+
+    def set_wait_test(self, extra_bytes: int, every: int = 1) -> None:
+        """Test hook: the copies of every `every`-th block wait for bytes that do not come (0: off)."""
+        _check(library().gemm_distill_plan_set_wait_test(self.handle, extra_bytes, every),
+               "gemm_distill_plan_set_wait_test")
+
     def check(self, stream=None) -> None:
-        """Synchronise `stream`; raise GemmError(GEMM_ERR_INDEX) if a teacher id was too large."""
+        """Synchronise `stream`; raise GemmError(GEMM_ERR_INDEX) if a teacher id was too large,
+        GemmError(GEMM_ERR_DEVICE_TIMEOUT) if a kernel gave up on a wait."""
         _check(library().gemm_distill_plan_check(self.handle, _stream(stream)),
                "gemm_distill_plan_check")

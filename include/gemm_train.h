@@ -220,6 +220,24 @@ gemm_status_t gemm_distill_forward_backward(gemm_distill_plan_t plan, int64_t ro
                                             void *dlogits, int64_t ldd, void *stream);
 
 /*
+ * Set the limit, in nanoseconds, after which a wait in a kernel of this plan
+ * gives up (default 2e9, at most 4e9).  ns == 0 restores the default.  The calls
+ * that follow (graphs captured from then on) have it.
+ */
+gemm_status_t gemm_distill_plan_set_timeout(gemm_distill_plan_t plan, uint64_t ns);
+
+/*
+ * Test hook for failure reporting: in every `every`-th block (1 = all) the copies
+ * of logits wait for `extra_bytes` (a multiple of 16, at most 4096) more than they
+ * bring, so their waits run out, the kernel returns, and the check below reports
+ * GEMM_ERR_DEVICE_TIMEOUT; the results are undefined.  The GPU context stays
+ * usable.  0 restores normal operation.  Rows of up to 16 packs of 16 bytes a
+ * lane of a warp, and rows that no eight blocks can hold, have no such waits.
+ */
+gemm_status_t gemm_distill_plan_set_wait_test(gemm_distill_plan_t plan, uint32_t extra_bytes,
+                                              uint32_t every);
+
+/*
  * As gemm_embed_plan_check, for the teacher's ids; GEMM_ERR_DEVICE_TIMEOUT if a
  * kernel of this plan gave up on a wait.
  */

@@ -1,0 +1,57 @@
+"""Waits that run out in the operators' kernels, without faulting or hanging the GPU.
+
+A plan's wait-test hook makes copies wait for bytes that never come; with a limit of 20 ms the
+bounded waits run out, the kernel lets its own copies land (bounded as well) and returns, and the
+plan's check reports GEMM_ERR_DEVICE_TIMEOUT.  The same plan then computes a right result."""
+import pytest
+
+import test_train_ops_gpu as ops
+
+pytestmark = pytest.mark.gpu
+
+LIMIT = 20_000_000       # ns
+
+
+def _times_out(gemm_lib, plan, call):
+    call()
+    with pytest.raises(gemm_lib.GemmError) as e:
+        plan.check()
+    assert e.value.status == 9
+    plan.check()                         # reported once
+
+
+def _distill_calls(plan, c):
+    return {"forward": lambda: plan.forward(c["logits"], c["ids"], c["values"], c["loss"], c["lse"]),
+            "backward": lambda: plan.backward(c["logits"], c["ids"], c["values"], c["lse"], c["dlogits"], dloss=c["dloss"]),
+            "both": lambda: plan.forward_backward(c["logits"], c["ids"], c["values"], c["loss"], c["lse"], c["dlogits"],
+                                                  dloss=c["dloss"])}
+
+
+@pytest.mark.parametrize("rows,vocab,elem", [(1, 4200, "bf16"), (3, 20011, "f32"), (5, 50000, "bf16"), (40, 9001, "f16")])
+@pytest.mark.parametrize("name", ["forward", "backward", "both"])
+@pytest.mark.parametrize("every", [1, 2])
+def test_distillation_of_few_rows(gemm_lib, rows, vocab, elem, name, every):
+    """Rows by one block per piece (two to eight), which share a row in a cluster: all of the blocks, or every second."""
+    c = ops._distill_case(rows, vocab, 9, elem, "f32", "i64", 0, 0, False, 1.0)
+    with gemm_lib.DistillPlan(rows, vocab, 9, elem) as plan:
+        calls = _distill_calls(plan, c)
+        calls["forward"]()
+        plan.set_timeout(LIMIT)
+        plan.set_wait_test(16, every)
+        _times_out(gemm_lib, plan, calls[name])
+        plan.set_wait_test(0)
+        plan.set_timeout(0)
+        calls["forward"]()
+        calls["backward"]()
+        ops._check_distill(c, elem, 1.0)
+        calls["both"]()
+        ops._check_distill(c, elem, 1.0, what="both: ")
+        plan.check()
+
+
+def test_wait_test_hook_validates(gemm_lib):
+    with gemm_lib.DistillPlan(4, 5000, 3, "f32") as plan:
+        for bad in ((7, 1), (8192, 1), (16, 0)):
+            with pytest.raises(gemm_lib.GemmError) as e:
+                plan.set_wait_test(*bad)
+            assert e.value.status == 1
