@@ -291,6 +291,7 @@ __device__ __forceinline__ void cluster_barrier() {
 // ---- asynchronous copies into a ring of buffers ------------------------------------
 
 constexpr uint32_t kWaitNs = 2000000000u;       // the longest wait in a kernel, by default
+constexpr uint32_t kNoticeNs = 20000;           // ... and the shortest: no limit is looked at before
 
 // A plan's limit of a wait, and its test hook: bytes that the copies of every `every`-th block
 // wait for beyond what they bring.
@@ -309,6 +310,12 @@ __device__ __forceinline__ uint32_t shared_address(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+__device__ __forceinline__ uint32_t timer_ns() {
+    uint32_t now;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+    return now;
+}
+
 // Waits for a phase of the barrier, at most `limit` ns.
 __device__ inline bool wait_phase(uint64_t* barrier, uint32_t parity, uint32_t limit) {
     const uint32_t at = shared_address(barrier);
@@ -321,11 +328,16 @@ __device__ inline bool wait_phase(uint64_t* barrier, uint32_t parity, uint32_t l
             "selp.u32 %0, 1, 0, p;\n}"
             : "=r"(done) : "r"(at), "r"(parity) : "memory");
         if (done) return true;
-        uint32_t now;
-        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+        const uint32_t now = timer_ns();
         if (tries == 0) began = now;
-        if (now - began > limit) return false;
+        if (now - began > kNoticeNs && now - began > limit) return false;
     }
+}
+
+// Waits for a phase of the barrier until `limit` ns after `began`: several waits within one limit.
+__device__ inline void wait_until(uint64_t* barrier, uint32_t parity, uint32_t began, uint32_t limit) {
+    const uint32_t spent = timer_ns() - began;
+    if (spent < limit) wait_phase(barrier, parity, limit - spent);
 }
 
 // A place in a ring of buffers, and how often it has been passed.
@@ -337,9 +349,11 @@ struct Turn {
     }
 };
 
-// As wait_phase, for whole warps; when it runs out (or another wait has) it returns at once from then on.
-__device__ __forceinline__ void wait_or_die(uint64_t* barrier, uint32_t parity, int* dead, int32_t* error,
-                                            uint32_t limit) {
+// As wait_phase, for whole warps, at most *patience ns.  When it runs out, *patience becomes 0;
+// later waits with it last kNoticeNs at most.  (The patience is looked at after that time only:
+// a limit in a register, or one read from shared memory at each try, cost 1% of the time of
+// distillation's pipeline.)
+__device__ __forceinline__ bool wait_or_die(uint64_t* barrier, uint32_t parity, uint32_t* patience, int32_t* error) {
     const uint32_t at = shared_address(barrier);
     uint32_t began = 0;
     for (uint32_t tries = 0;; ++tries) {
@@ -349,16 +363,23 @@ __device__ __forceinline__ void wait_or_die(uint64_t* barrier, uint32_t parity, 
             "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
             "selp.u32 %0, 1, 0, p;\n}"
             : "=r"(done) : "r"(at), "r"(parity) : "memory");
-        if (done || *static_cast<volatile int*>(dead)) return;
-        uint32_t now;
-        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(now));
+        if (done) return true;
+        const uint32_t now = timer_ns();
         if (tries == 0) began = now;
+        if (now - began <= kNoticeNs) continue;
+        const uint32_t limit = *static_cast<volatile uint32_t*>(patience);
+        if (limit == 0) return false;
         if (now - began > limit) {
-            *static_cast<volatile int*>(dead) = 1;
+            *static_cast<volatile uint32_t*>(patience) = 0;
             atomicOr(error, kErrorTimeout);
-            return;
+            return false;
         }
     }
+}
+
+// Whether waits with this patience have been given up.
+__device__ __forceinline__ bool is_dead(const uint32_t* patience) {
+    return *static_cast<const volatile uint32_t*>(patience) == 0;
 }
 
 __device__ __forceinline__ void init_barrier(uint64_t* barrier, uint32_t count) {
@@ -384,7 +405,7 @@ __device__ __forceinline__ void copy_bytes(void* to, const void* from, uint32_t 
 
 inline gemm_status_t set_wait_limit(Waits* w, uint64_t ns) {
     constexpr uint64_t kMost = 4000000000u;
-    w->limit = ns == 0 ? kWaitNs : static_cast<uint32_t>(ns < kMost ? ns : kMost);
+    w->limit = ns == 0 ? kWaitNs : static_cast<uint32_t>(ns < kNoticeNs ? kNoticeNs : ns < kMost ? ns : kMost);
     return GEMM_OK;
 }
 

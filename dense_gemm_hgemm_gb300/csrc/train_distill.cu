@@ -503,6 +503,13 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const Args<T> a) {
 // block's stores go beside the other's sums (three blocks of 32-KB parts 171).  Three warps for
 // the entries, 16-KB stages and logits at the ids taken from the ring were 169 where one warp,
 // 8-KB stages and loads of those logits were 201.
+//
+// When a wait runs out (the block's patience is over, and no later wait lasts), nothing more is
+// copied, prepared or exchanged, and the computing warps go on through their rows with whatever
+// there is (leaving the loop cost 3% of the time).  So how many barriers a row has depends on no
+// data, and what a warp does together on nothing that its lanes may see differently.  Before
+// the block ends, what it asked for and what the other blocks of its cluster sent it lands, by
+// count.
 
 template <int MODE> constexpr int kStageBytesOf = MODE == kBoth ? 16384 : 8192;
 constexpr int kMostStages = 16;
@@ -521,12 +528,24 @@ struct StreamBarriers {
     float4 exchange[2][kMaxCluster];
     float part[2][3][kComputeWarps];
     float mass[kMostSlots], scale[kMostSlots];
-    int dead;                // a wait ran out: nothing waits any more
+    uint32_t sent[kMaxCluster];      // exchanges that each block of the cluster took part in, at its end
+    uint32_t patience;       // ns that a wait may last; 0: one ran out, nothing waits any more
     uint32_t extra;          // bytes that a stage waits for beyond its copies (see Waits)
 };
 
 __device__ __forceinline__ void compute_barrier() {
     asm volatile("bar.sync 1, %0;" :: "n"(kComputeThreads) : "memory");
+}
+
+// The block's warps meet once more, each kind at the end of its part.
+__device__ __forceinline__ void end_of_block() {
+    __syncwarp();
+    asm volatile("bar.sync 0;" ::: "memory");
+}
+
+// Takes bytes that will not come off what the barrier's phase waits for.
+__device__ __forceinline__ void strike_bytes(uint64_t* barrier, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.shared::cta.b64 [%0], %1;" :: "r"(shared_address(barrier)), "r"(bytes) : "memory");
 }
 
 template <typename T, int MODE>
@@ -536,13 +555,15 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
     constexpr int kStageBytes = kStageBytesOf<MODE>;
     constexpr int kStage = kStageBytes / static_cast<int>(sizeof(T));     // elements
     constexpr bool kGrad = MODE == kBoth;
+    constexpr bool kSplit = kGrad;               // a row may be a cluster's (else a.pieces is 1)
     constexpr int kBatch = kStage / VEC / kComputeThreads;                // packs a thread takes of a stage
     extern __shared__ __align__(16) uint8_t memory[];
     __shared__ StreamBarriers sh;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const int rank = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.pieces));
-    const int64_t first = blockIdx.x / static_cast<unsigned>(a.pieces);
-    const int64_t step = gridDim.x / static_cast<unsigned>(a.pieces);
+    const unsigned pieces = kSplit ? static_cast<unsigned>(a.pieces) : 1u;
+    const int rank = static_cast<int>(blockIdx.x % pieces);
+    const int64_t first = blockIdx.x / pieces;
+    const int64_t step = gridDim.x / pieces;
     const int top = a.teacher.top;
     const int padded_top = (top + 3) / 4 * 4;
     T* const ring = reinterpret_cast<T*>(memory);
@@ -564,22 +585,23 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
             init_barrier(&sh.entries_empty[k], kComputeWarps + 1);
         }
         for (int k = 0; k < 2; ++k) init_barrier(&sh.exchanged[k], 1);
-        sh.dead = 0;
+        sh.patience = a.waits.limit;
         sh.extra = a.waits.extra_bytes();
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
-    if (a.pieces > 1) cluster_barrier();                 // the others' barriers exist
+    if (kSplit && a.pieces > 1) cluster_barrier();       // the others' barriers exist
     wait_for_previous_kernel();
     let_next_kernel_start();
 
+    uint32_t sent = 0, received = 0;                     // exchanges that the first computing warp took part in and saw whole
     if (warp == 0) {                                     // copies
         Turn stage{0, 0}, turn{0, 0};
+        uint32_t issued = 0;                             // (lane 0)
         for (int64_t row = first; row < rows; row += step, turn.next(1, slots)) {
             const int slot = turn.at;
-            wait_or_die(&sh.entries_full[slot], turn.round & 1, &sh.dead, a.error, a.waits.limit);
-            const bool out = sh.mass[slot] == 0.f;
-            __syncwarp();
+            wait_or_die(&sh.entries_full[slot], turn.round & 1, &sh.patience, a.error);
+            const bool out = __shfl_sync(0xffffffffu, sh.mass[slot], 0) == 0.f;
             if (lane == 0) arrive(&sh.entries_empty[slot]);
             if (out) continue;
             const T* src = a.logits + row * a.ldl + begin;
@@ -594,7 +616,7 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
                 if (tail_begin + lane < end) tail = base[tail_begin + lane];
             }
             for (int at = 0; at < end; at += kStage) {
-                wait_or_die(&sh.empty[stage.at], (stage.round & 1) ^ 1, &sh.dead, a.error, a.waits.limit);
+                wait_or_die(&sh.empty[stage.at], (stage.round & 1) ^ 1, &sh.patience, a.error);
                 T* const to = ring + stage.at * kStage;
                 const int lo = at == 0 ? head_end : at, hi = min(at + kStage, tail_begin);
                 const bool first_pack = at == 0 && off > 0;
@@ -605,27 +627,31 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 __syncwarp();
-                if (lane == 0 && !*static_cast<volatile int*>(&sh.dead)) {
+                // (a warp that gave up has left its stages unread: they are not filled again)
+                if (lane == 0 && !is_dead(&sh.patience)) {
                     const uint32_t bytes = hi > lo ? static_cast<uint32_t>((hi - lo) * static_cast<int>(sizeof(T))) : 0;
                     expect_bytes(&sh.full[stage.at], bytes + sh.extra);
                     if (bytes > 0) copy_bytes(to + (lo - at), base + lo, bytes, &sh.full[stage.at]);
+                    ++issued;
                 }
                 stage.next(1, stages);
             }
         }
+        end_of_block();
         // A wait that ran out may have left copies behind: let them land (bounded).
-        if (*static_cast<volatile int*>(&sh.dead)) {
-            for (int s = 0; s < stages; ++s) {
-                const uint32_t issued = stage.round + (s < stage.at ? 1 : 0);
-                if (issued > 0) wait_phase(&sh.full[s], (issued - 1) & 1, a.waits.limit);
-            }
+        if (lane == 0 && is_dead(&sh.patience)) {
+            const uint32_t began = timer_ns(), n_stages = static_cast<uint32_t>(stages);
+            for (uint32_t k = issued > n_stages ? issued - n_stages : 0; k < issued; ++k)
+                wait_until(&sh.full[k % n_stages], k / n_stages & 1, began, a.waits.limit);
         }
+        __syncwarp();
     } else if (warp <= kEntryWarps) {                    // the teacher's entries
         Turn turn{warp - 1, 0};
         for (int64_t row = first + (warp - 1) * step; row < rows;
              row += kEntryWarps * step, turn.next(kEntryWarps, slots)) {
             const int slot = turn.at;
-            wait_or_die(&sh.entries_empty[slot], (turn.round & 1) ^ 1, &sh.dead, a.error, a.waits.limit);
+            if (!__all_sync(0xffffffffu, wait_or_die(&sh.entries_empty[slot], (turn.round & 1) ^ 1, &sh.patience, a.error)))
+                break;
             const Entries en = entries(slot);
             if (row + kEntryWarps * step < rows) prefetch_entries(a.teacher, row + kEntryWarps * step);
             const float dloss = kGrad && a.dloss ? a.dloss[row] : 1.f;
@@ -639,14 +665,15 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
             __syncwarp();
             if (lane == 0) arrive(&sh.entries_full[slot]);
         }
+        end_of_block();
     } else {                                             // the arithmetic
         const int thread = tid - kFirstCompute, worker = warp - kFirstCompute / 32;
-        uint32_t exchanges = 0;
         Turn stage{0, 0}, entry{0, 0};
+        uint32_t exchanges = 0;
         for (int64_t row = first; row < rows; row += step, entry.next(1, slots)) {
             const int slot = entry.at;
-            wait_or_die(&sh.entries_full[slot], entry.round & 1, &sh.dead, a.error, a.waits.limit);
-            const float mass = sh.mass[slot];
+            wait_or_die(&sh.entries_full[slot], entry.round & 1, &sh.patience, a.error);
+            const float mass = __shfl_sync(0xffffffffu, sh.mass[slot], 0);
             const Entries en = entries(slot);
             const bool out = mass == 0.f;
             const T* src = a.logits + row * a.ldl + begin;
@@ -657,10 +684,12 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
             Softmax row_q = {0.f, 0.f};
             float row_sum = 0.f;
             float terms = 0.f;                           // of the loss: sum p (log2 p - x c)
-            if (!out) {
+            if (out) {
+                compute_barrier();
+            } else {
                 Running<T> run;
                 for (int p0 = 0; p0 < packs; p0 += kStage / VEC) {
-                    wait_or_die(&sh.full[stage.at], stage.round & 1, &sh.dead, a.error, a.waits.limit);
+                    wait_or_die(&sh.full[stage.at], stage.round & 1, &sh.patience, a.error);
                     const T* from = ring + stage.at * kStage + thread * VEC;
                     Pack<T, VEC> q[kBatch];
                     if (packs - p0 >= kStage / VEC) {
@@ -711,11 +740,12 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
                     merge(k, sum, __shfl_xor_sync(0xffffffffu, k, o), __shfl_xor_sync(0xffffffffu, sum, o));
                     terms += __shfl_xor_sync(0xffffffffu, terms, o);
                 }
-                if (a.pieces > 1) {
-                    if (worker == 0) {
+                if (kSplit && a.pieces > 1) {
+                    // this block's numbers, to each block of the row (none any more once a wait has run out)
+                    if (worker == 0 && __shfl_sync(0xffffffffu, is_dead(&sh.patience), 0) == 0) {
                         if (lane == 0)
                             expect_bytes(&sh.exchanged[turn], static_cast<uint32_t>(a.pieces) * 16);
-                        if (lane < a.pieces) {           // this block's numbers, to each block of the row
+                        if (lane < a.pieces) {
                             uint32_t slot_at, barrier_at;
                             asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
                                          : "=r"(slot_at) : "r"(shared_address(&sh.exchange[turn][rank])), "r"(lane));
@@ -726,9 +756,11 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
                                 "[%5];"
                                 :: "r"(slot_at), "f"(k), "f"(sum), "f"(terms), "f"(0.f), "r"(barrier_at) : "memory");
                         }
+                        ++sent;
                         __syncwarp();
                     }
-                    wait_or_die(&sh.exchanged[turn], (exchanges >> 1) & 1, &sh.dead, a.error, a.waits.limit);
+                    if (wait_or_die(&sh.exchanged[turn], (exchanges >> 1) & 1, &sh.patience, a.error) && sent > exchanges)
+                        received = sent;
                     k = sh.exchange[turn][0].x;
                     sum = sh.exchange[turn][0].y;
                     terms = sh.exchange[turn][0].z;
@@ -788,8 +820,8 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
                         stage.next(1, stages);
                     }
                 }
+                compute_barrier();                       // the stores above come first
                 if (!empty) {
-                    compute_barrier();                   // the stores above come first
                     for (int j = thread; j < top; j += kComputeThreads) {
                         const float p = en.own[j];
                         const int at = en.id[j] - begin;
@@ -801,9 +833,31 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
             __syncwarp();
             if (lane == 0) arrive(&sh.entries_empty[slot]);
         }
+        if (kSplit && a.pieces > 1 && worker == 0 && lane < a.pieces) {
+            uint32_t remote;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                         : "=r"(remote) : "r"(shared_address(&sh.sent[rank])), "r"(lane));
+            asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(remote), "r"(sent) : "memory");
+        }
+        end_of_block();
     }
-    __syncthreads();
-    if (a.pieces > 1) cluster_barrier();                 // no block leaves while others write to it
+    if (!kSplit || a.pieces == 1) return;
+    cluster_barrier();                                   // no block leaves while others write to it
+    if (tid == kFirstCompute) {
+        // ... and none while their numbers are on the way: those that were sent and not waited for.
+        const uint32_t began = timer_ns();
+        for (uint32_t e = received;; ++e) {
+            uint32_t coming = 0;
+            for (int r = 0; r < a.pieces; ++r) coming += sh.sent[r] > e ? 1 : 0;
+            if (e >= sent && coming == 0) break;
+            const uint32_t missing = static_cast<uint32_t>(a.pieces) - coming;
+            if (e >= sent)
+                expect_bytes(&sh.exchanged[e & 1], coming * 16);
+            else if (missing > 0)                        // (all were expected)
+                strike_bytes(&sh.exchanged[e & 1], missing * 16);
+            wait_until(&sh.exchanged[e & 1], (e >> 1) & 1, began, a.waits.limit);
+        }
+    }
 }
 
 // ---- short rows ---------------------------------------------------------------------------

@@ -324,7 +324,7 @@ template <int N, bool ANY>
 struct Ring {
     uint8_t* memory;
     uint64_t* full;
-    int* dead;
+    uint32_t* patience;
     int32_t* error;
     const uint8_t* src[N];
     int64_t stride[N];                     // bytes
@@ -335,7 +335,7 @@ struct Ring {
 
     __device__ __forceinline__ bool direct(int row) const { return ANY && (row == 0 || row == rows - 1); }
     __device__ __forceinline__ void ask(int stage, int row) {
-        if (*static_cast<volatile int*>(dead)) return;
+        if (is_dead(patience)) return;
         ++asked;
         if (direct(row)) {
             expect_bytes(&full[stage], 0);
@@ -362,7 +362,7 @@ struct Ring {
     __device__ __forceinline__ void begin(int row) {
         for (int k = 0; k < stages && row < rows; ++k, row += step) ask(k, row);
     }
-    __device__ __forceinline__ void wait() const { wait_or_die(&full[turn.at], turn.round & 1, dead, error, kWaitNs); }
+    __device__ __forceinline__ void wait() const { wait_or_die(&full[turn.at], turn.round & 1, patience, error); }
     // Source k's row, in the present stage (or in the matrix), once waited for.
     __device__ __forceinline__ const uint8_t* at(int k, int row) const {
         const uint8_t* from = src[k] + row * stride[k];
@@ -378,7 +378,7 @@ struct Ring {
     }
     // After a wait that ran out (one lane): what was asked for may still come.
     __device__ __forceinline__ void end() const {
-        if (!*static_cast<volatile int*>(dead)) return;
+        if (!is_dead(patience)) return;
         for (int k = asked > stages ? asked - stages : 0; k < asked; ++k)
             wait_phase(&full[k % stages], (k / stages) & 1, kWaitNs);
     }
@@ -391,13 +391,13 @@ __host__ __device__ constexpr int ring_stage_bytes(int row_bytes, bool any) {
 
 struct RingBarriers {
     uint64_t full[kRingSlots];
-    int dead;
+    uint32_t patience;           // ns that a wait may last; 0: one ran out, nothing waits any more
 };
 
 // (one thread)
 __device__ __forceinline__ void init_ring(RingBarriers& ring, int slots) {
     for (int k = 0; k < slots; ++k) init_barrier(&ring.full[k], 1);
-    ring.dead = 0;
+    ring.patience = kWaitNs;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kForwardRing, 1) norm_forward_ring_kernel(cons
     int row = group < groups ? static_cast<int>(blockIdx.x + group * gridDim.x) : static_cast<int>(a.rows);
     Ring<1, kAny> ring{memory + group * stages * stage_bytes,
                  barriers.full + group * stages,
-                 &barriers.dead,
+                 &barriers.patience,
                  a.error,
                  {reinterpret_cast<const uint8_t*>(a.x)},
                  {a.ldx * static_cast<int64_t>(sizeof(T))},
@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(kBackwardRing, 1) norm_backward_ring_kernel(co
     int row = group < groups ? static_cast<int>(blockIdx.x + group * gridDim.x) : static_cast<int>(a.rows);
     Ring<2, kAny> ring{memory + group * stages * 2 * stage_bytes,
                  barriers.full + group * stages,
-                 &barriers.dead,
+                 &barriers.patience,
                  a.error,
                  {reinterpret_cast<const uint8_t*>(a.x), reinterpret_cast<const uint8_t*>(a.dy)},
                  {a.ldx * static_cast<int64_t>(sizeof(T)), a.lddy * static_cast<int64_t>(sizeof(T))},
@@ -868,7 +868,7 @@ __global__ void __launch_bounds__(kWideRing, 1) norm_backward_wide_ring_kernel(c
     int row = group < groups ? static_cast<int>(blockIdx.x + group * gridDim.x) : static_cast<int>(a.rows);
     Ring<2, kAny> ring{memory + group * stages * 2 * stage_bytes,
                        barriers.full + group * stages,
-                       &barriers.dead,
+                       &barriers.patience,
                        a.error,
                        {reinterpret_cast<const uint8_t*>(a.x), reinterpret_cast<const uint8_t*>(a.dy)},
                        {a.ldx * static_cast<int64_t>(sizeof(T)), a.lddy * static_cast<int64_t>(sizeof(T))},

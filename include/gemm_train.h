@@ -221,7 +221,7 @@ gemm_status_t gemm_distill_forward_backward(gemm_distill_plan_t plan, int64_t ro
 
 /*
  * Set the limit, in nanoseconds, after which a wait in a kernel of this plan
- * gives up (default 2e9, at most 4e9).  ns == 0 restores the default.  The calls
+ * gives up (default 2e9, 2e4 to 4e9).  ns == 0 restores the default.  The calls
  * that follow (graphs captured from then on) have it.
  */
 gemm_status_t gemm_distill_plan_set_timeout(gemm_distill_plan_t plan, uint64_t ns);

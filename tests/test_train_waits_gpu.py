@@ -3,6 +3,8 @@
 A plan's wait-test hook makes copies wait for bytes that never come; with a limit of 20 ms the
 bounded waits run out, the kernel lets its own copies land (bounded as well) and returns, and the
 plan's check reports GEMM_ERR_DEVICE_TIMEOUT.  The same plan then computes a right result."""
+import time
+
 import pytest
 
 import test_train_ops_gpu as ops
@@ -39,6 +41,35 @@ def test_distillation_of_few_rows(gemm_lib, rows, vocab, elem, name, every):
         plan.set_timeout(LIMIT)
         plan.set_wait_test(16, every)
         _times_out(gemm_lib, plan, calls[name])
+        plan.set_wait_test(0)
+        plan.set_timeout(0)
+        calls["forward"]()
+        calls["backward"]()
+        ops._check_distill(c, elem, 1.0)
+        calls["both"]()
+        ops._check_distill(c, elem, 1.0, what="both: ")
+        plan.check()
+
+
+@pytest.mark.parametrize("rows,vocab,elem", [(700, 9001, "f32"), (480, 20011, "bf16"), (200, 40000, "f16"), (160, 66000, "bf16"),
+                                             (330, 70000, "f32"), (90, 150000, "bf16")])
+@pytest.mark.parametrize("name", ["forward", "both"])
+@pytest.mark.parametrize("every", [1, 2, 5])
+def test_distillation_pipeline(gemm_lib, rows, vocab, elem, name, every):
+    """Many rows, many of them without entries, by one block or by a cluster each: the waits of all blocks, or those of
+    some of a cluster's blocks, run out; then the others wait for their numbers in vain."""
+    c = ops._distill_case(rows, vocab, 9, elem, "f32", "i64", 0, 0, False, 1.0)
+    c["ids"][::3] = -1
+    with gemm_lib.DistillPlan(rows, vocab, 9, elem) as plan:
+        calls = _distill_calls(plan, c)
+        calls[name]()
+        plan.check()
+        plan.set_timeout(LIMIT)
+        plan.set_wait_test(16, every)
+        began = time.perf_counter()
+        _times_out(gemm_lib, plan, calls[name])
+        # a wait or two of each block, one of the next, and what is left behind: each 20 ms at most
+        assert time.perf_counter() - began < 2.0
         plan.set_wait_test(0)
         plan.set_timeout(0)
         calls["forward"]()
