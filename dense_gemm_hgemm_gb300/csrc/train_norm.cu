@@ -10,6 +10,7 @@ struct gemm_norm_plan {
     void* memory;        // one allocation: the error word and `partial`
     int32_t* error_word;
     float* partial;      // [2][blocks][cols] sums of the weight gradients
+    gbt::Waits waits;
 };
 
 namespace gbt {
@@ -251,6 +252,7 @@ struct ForwardArgs {
     int64_t ldx, ldy, rows;
     float eps;
     int cols, lanes;
+    Waits waits;
 };
 
 // KEEP: gamma and beta stay in registers over the rows (else they are read for each
@@ -317,6 +319,12 @@ constexpr int kRingShared = 208 * 1024;    // its dynamic shared memory, at most
 constexpr int kForwardRing = 1024;         // threads of the blocks
 constexpr int kBackwardRing = 512;
 
+// A block's waits: ns that one may last (0: one ran out, nothing waits long any more), and
+// bytes that a stage waits for beyond its copies.
+struct RingWaits {
+    uint32_t patience, limit, extra;
+};
+
 // A group's ring; each stage holds a row from each of N sources.  Where rows do not begin or
 // end at 16-byte boundaries (ANY), the whole 16-byte units around a row are copied; the first
 // and the last row of the matrix, whose units may reach beyond it, are left to plain loads.
@@ -324,7 +332,7 @@ template <int N, bool ANY>
 struct Ring {
     uint8_t* memory;
     uint64_t* full;
-    uint32_t* patience;
+    RingWaits* waits;
     int32_t* error;
     const uint8_t* src[N];
     int64_t stride[N];                     // bytes
@@ -335,10 +343,10 @@ struct Ring {
 
     __device__ __forceinline__ bool direct(int row) const { return ANY && (row == 0 || row == rows - 1); }
     __device__ __forceinline__ void ask(int stage, int row) {
-        if (is_dead(patience)) return;
+        if (is_dead(&waits->patience)) return;
         ++asked;
         if (direct(row)) {
-            expect_bytes(&full[stage], 0);
+            expect_bytes(&full[stage], waits->extra);
             return;
         }
         const uint8_t* from[N];
@@ -354,7 +362,7 @@ struct Ring {
             }
             all += bytes[k];
         }
-        expect_bytes(&full[stage], all);
+        expect_bytes(&full[stage], all + waits->extra);
 #pragma unroll
         for (int k = 0; k < N; ++k) copy_bytes(memory + (stage * N + k) * stage_bytes, from[k], bytes[k], &full[stage]);
     }
@@ -362,7 +370,7 @@ struct Ring {
     __device__ __forceinline__ void begin(int row) {
         for (int k = 0; k < stages && row < rows; ++k, row += step) ask(k, row);
     }
-    __device__ __forceinline__ void wait() const { wait_or_die(&full[turn.at], turn.round & 1, patience, error); }
+    __device__ __forceinline__ void wait() const { wait_or_die(&full[turn.at], turn.round & 1, &waits->patience, error); }
     // Source k's row, in the present stage (or in the matrix), once waited for.
     __device__ __forceinline__ const uint8_t* at(int k, int row) const {
         const uint8_t* from = src[k] + row * stride[k];
@@ -378,9 +386,10 @@ struct Ring {
     }
     // After a wait that ran out (one lane): what was asked for may still come.
     __device__ __forceinline__ void end() const {
-        if (!is_dead(patience)) return;
+        if (!is_dead(&waits->patience)) return;
+        const uint32_t began = timer_ns();
         for (int k = asked > stages ? asked - stages : 0; k < asked; ++k)
-            wait_phase(&full[k % stages], (k / stages) & 1, kWaitNs);
+            wait_until(&full[k % stages], (k / stages) & 1, began, waits->limit);
     }
 };
 
@@ -391,13 +400,13 @@ __host__ __device__ constexpr int ring_stage_bytes(int row_bytes, bool any) {
 
 struct RingBarriers {
     uint64_t full[kRingSlots];
-    uint32_t patience;           // ns that a wait may last; 0: one ran out, nothing waits any more
+    RingWaits waits;
 };
 
 // (one thread)
-__device__ __forceinline__ void init_ring(RingBarriers& ring, int slots) {
+__device__ __forceinline__ void init_ring(RingBarriers& ring, int slots, const Waits& waits) {
     for (int k = 0; k < slots; ++k) init_barrier(&ring.full[k], 1);
-    ring.patience = kWaitNs;
+    ring.waits = {waits.limit, waits.limit, waits.extra_bytes()};
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
@@ -477,7 +486,7 @@ __global__ void __launch_bounds__(kForwardRing, 1) norm_forward_ring_kernel(cons
     const int row_bytes = a.cols * static_cast<int>(sizeof(T)), stage_bytes = ring_stage_bytes(row_bytes, kAny);
     Staged<W, VEC> gamma{reinterpret_cast<W*>(memory + groups * stages * stage_bytes), lanes * COLS / 2};
     Staged<W, VEC> beta{gamma.at + lanes * COLS, gamma.half};
-    if (threadIdx.x == 0) init_ring(barriers, groups * stages);
+    if (threadIdx.x == 0) init_ring(barriers, groups * stages, a.waits);
     __syncthreads();
     wait_for_previous_kernel();
     let_next_kernel_start();
@@ -485,7 +494,7 @@ __global__ void __launch_bounds__(kForwardRing, 1) norm_forward_ring_kernel(cons
     int row = group < groups ? static_cast<int>(blockIdx.x + group * gridDim.x) : static_cast<int>(a.rows);
     Ring<1, kAny> ring{memory + group * stages * stage_bytes,
                  barriers.full + group * stages,
-                 &barriers.patience,
+                 &barriers.waits,
                  a.error,
                  {reinterpret_cast<const uint8_t*>(a.x)},
                  {a.ldx * static_cast<int64_t>(sizeof(T))},
@@ -561,6 +570,7 @@ struct BackwardArgs {
     int64_t ldx, lddy, lddx, rows;
     int cols, lanes;
     bool weights;        // dgamma or dbeta is wanted
+    Waits waits;
 };
 
 // Backward, once xh and g are in the lanes' pairs: the group's sums, then dx.
@@ -725,7 +735,7 @@ __global__ void __launch_bounds__(kBackwardRing, 1) norm_backward_ring_kernel(co
     const int lanes = a.lanes, groups = kBackwardRing / lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
     constexpr bool kAny = VEC == 1 || SHIFT;
     const int row_bytes = a.cols * static_cast<int>(sizeof(T)), stage_bytes = ring_stage_bytes(row_bytes, kAny);
-    if (threadIdx.x == 0) init_ring(barriers, groups * stages);
+    if (threadIdx.x == 0) init_ring(barriers, groups * stages, a.waits);
     __syncthreads();
     wait_for_previous_kernel();
     let_next_kernel_start();
@@ -733,7 +743,7 @@ __global__ void __launch_bounds__(kBackwardRing, 1) norm_backward_ring_kernel(co
     int row = group < groups ? static_cast<int>(blockIdx.x + group * gridDim.x) : static_cast<int>(a.rows);
     Ring<2, kAny> ring{memory + group * stages * 2 * stage_bytes,
                  barriers.full + group * stages,
-                 &barriers.patience,
+                 &barriers.waits,
                  a.error,
                  {reinterpret_cast<const uint8_t*>(a.x), reinterpret_cast<const uint8_t*>(a.dy)},
                  {a.ldx * static_cast<int64_t>(sizeof(T)), a.lddy * static_cast<int64_t>(sizeof(T))},
@@ -860,7 +870,7 @@ __global__ void __launch_bounds__(kWideRing, 1) norm_backward_wide_ring_kernel(c
     const int lanes = a.lanes, groups = 1, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
     const int row_bytes = a.cols * static_cast<int>(sizeof(T)), stage_bytes = ring_stage_bytes(row_bytes, kAny);
     Staged<W, VEC> gamma{reinterpret_cast<W*>(memory + groups * stages * 2 * stage_bytes), lanes * kLaneCols / 2};
-    if (threadIdx.x == 0) init_ring(barriers, groups * stages);
+    if (threadIdx.x == 0) init_ring(barriers, groups * stages, a.waits);
     __syncthreads();
     wait_for_previous_kernel();
     let_next_kernel_start();
@@ -868,7 +878,7 @@ __global__ void __launch_bounds__(kWideRing, 1) norm_backward_wide_ring_kernel(c
     int row = group < groups ? static_cast<int>(blockIdx.x + group * gridDim.x) : static_cast<int>(a.rows);
     Ring<2, kAny> ring{memory + group * stages * 2 * stage_bytes,
                        barriers.full + group * stages,
-                       &barriers.patience,
+                       &barriers.waits,
                        a.error,
                        {reinterpret_cast<const uint8_t*>(a.x), reinterpret_cast<const uint8_t*>(a.dy)},
                        {a.ldx * static_cast<int64_t>(sizeof(T)), a.lddy * static_cast<int64_t>(sizeof(T))},
@@ -1332,7 +1342,7 @@ gemm_status_t gemm_norm_forward(gemm_norm_plan_t p, int64_t rows, const void* x,
         const gbt::ForwardArgs<T, W> a{static_cast<const T*>(x), static_cast<const W*>(gamma),
                                        static_cast<const W*>(beta), static_cast<T*>(y), mean, rstd,
                                        p->error_word, ldx, ldy, rows, eps, static_cast<int>(p->cols),
-                                       gbt::lanes_for(p->cols)};
+                                       gbt::lanes_for(p->cols), p->waits};
         if (!gbt::in_registers(p->cols))
             return gbt::launch<gbt::norm_forward_wide_kernel<T, W>>(rows, gbt::kThreads, 0, queue, 1, a);
         const bool vec = gbt::rows_aligned(x, ldx, e) && gbt::rows_aligned(y, ldy, e) &&
@@ -1370,7 +1380,7 @@ gemm_status_t gemm_norm_backward(gemm_norm_plan_t p, int64_t rows, const void* x
         const int lanes = gbt::lanes_for(p->cols);
         gbt::BackwardArgs<T, W> a{static_cast<const T*>(x), static_cast<const W*>(gamma), mean, rstd,
                                   static_cast<const T*>(dy), static_cast<T*>(dx), p->partial, p->error_word, ldx,
-                                  lddy, lddx, rows, static_cast<int>(p->cols), lanes, dg || db};
+                                  lddy, lddx, rows, static_cast<int>(p->cols), lanes, dg || db, p->waits};
         const int tiles = static_cast<int>((p->cols + 31) / 32);
         gemm_status_t s = GEMM_OK;
         if (!gbt::in_registers(p->cols)) {
@@ -1397,6 +1407,14 @@ gemm_status_t gemm_norm_backward(gemm_norm_plan_t p, int64_t rows, const void* x
                             p->partial, blocks, static_cast<int>(p->cols), dg, db);
         return s;
     });
+}
+
+gemm_status_t gemm_norm_plan_set_timeout(gemm_norm_plan_t p, uint64_t ns) {
+    return p ? gbt::set_wait_limit(&p->waits, ns) : GEMM_ERR_INVALID_ARG;
+}
+
+gemm_status_t gemm_norm_plan_set_wait_test(gemm_norm_plan_t p, uint32_t extra_bytes, uint32_t every) {
+    return p ? gbt::set_wait_test(&p->waits, extra_bytes, every) : GEMM_ERR_INVALID_ARG;
 }
 
 gemm_status_t gemm_norm_plan_check(gemm_norm_plan_t p, void* stream) {

@@ -51,6 +51,8 @@ def signatures():
         "gemm_norm_plan_create": ([i64, i64, i32, i32, vpp], i32),
         "gemm_norm_forward": ([vp, i64, vp, i64, vp, vp, f32, vp, i64, vp, vp, vp], i32),
         "gemm_norm_backward": ([vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp], i32),
+        "gemm_norm_plan_set_timeout": ([vp, u64], i32),
+        "gemm_norm_plan_set_wait_test": ([vp, u32, u32], i32),
         "gemm_norm_plan_check": ([vp, vp], i32),
         "gemm_norm_plan_destroy": ([vp], i32),
         "gemm_embed_plan_create": ([i64, i64, i64, i32, i32, vpp], i32),
@@ -239,6 +241,15 @@ class NormPlan(_Plan):
             pdy, lddy, pdx, lddx, _vector(dgamma, cols, self._weight, "dgamma", True),
             _vector(dbeta, cols, self._weight, "dbeta", True), _stream(stream)),
             "gemm_norm_backward")
+
+    def set_timeout(self, ns: int) -> None:
+        """The limit of a wait in this plan's kernels, in nanoseconds (0: the default, 2e9)."""
+        _check(library().gemm_norm_plan_set_timeout(self.handle, ns), "gemm_norm_plan_set_timeout")
+
+    def set_wait_test(self, extra_bytes: int, every: int = 1) -> None:
+        """Test hook: the copies of every `every`-th block wait for bytes that do not come (0: off)."""
+        _check(library().gemm_norm_plan_set_wait_test(self.handle, extra_bytes, every),
+               "gemm_norm_plan_set_wait_test")
 
     def check(self, stream=None) -> None:
         """Synchronise `stream`; raise GemmError(GEMM_ERR_DEVICE_TIMEOUT) if a kernel gave up on a wait."""

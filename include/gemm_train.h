@@ -90,6 +90,24 @@ gemm_status_t gemm_norm_backward(gemm_norm_plan_t plan, int64_t rows, const void
                                  void *dgamma, void *dbeta, void *stream);
 
 /*
+ * Set the limit, in nanoseconds, after which a wait in a kernel of this plan
+ * gives up (default 2e9, 2e4 to 4e9).  ns == 0 restores the default.  The calls
+ * that follow (graphs captured from then on) have it.
+ */
+gemm_status_t gemm_norm_plan_set_timeout(gemm_norm_plan_t plan, uint64_t ns);
+
+/*
+ * Test hook for failure reporting: in every `every`-th block (1 = all) the copies
+ * of rows wait for `extra_bytes` (a multiple of 16, at most 4096) more than they
+ * bring, so their waits run out, the kernel returns, and the check below reports
+ * GEMM_ERR_DEVICE_TIMEOUT; the results are undefined.  The GPU context stays
+ * usable.  0 restores normal operation.  Few, short and very wide rows, which are
+ * not copied but loaded, have no such waits.
+ */
+gemm_status_t gemm_norm_plan_set_wait_test(gemm_norm_plan_t plan, uint32_t extra_bytes,
+                                           uint32_t every);
+
+/*
  * Synchronise `stream`, then read and clear the plan's error word:
  * GEMM_ERR_DEVICE_TIMEOUT if a kernel of this plan gave up on a wait, GEMM_ERR_CUDA
  * if the stream reported an error, else GEMM_OK.

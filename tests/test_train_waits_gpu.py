@@ -80,8 +80,36 @@ def test_distillation_pipeline(gemm_lib, rows, vocab, elem, name, every):
         plan.check()
 
 
-def test_wait_test_hook_validates(gemm_lib):
-    with gemm_lib.DistillPlan(4, 5000, 3, "f32") as plan:
+@pytest.mark.parametrize("rows,cols,elem,weight", [
+    (1300, 4096, "bf16", "f32"), (5200, 1000, "f16", "f16"), (1301, 4090, "bf16", "bf16"), (3000, 333, "f32", "f32"),
+    (650, 12000, "bf16", "bf16"), (320, 16384, "f16", "f16")])
+@pytest.mark.parametrize("name", ["forward", "backward"])
+@pytest.mark.parametrize("every", [1, 7])
+def test_norm_rings(gemm_lib, rows, cols, elem, weight, name, every):
+    """Rings of whole rows, of rows off the boundaries in packs and in single elements, and of wide rows."""
+    c = ops._norm_case(rows, cols, elem, weight, 0, 0)
+    with gemm_lib.NormPlan(rows, cols, elem, weight=weight) as plan:
+        calls = {"forward": lambda: plan.forward(c["x"], c["gamma"], c["beta"], c["y"], c["mean"], c["rstd"]),
+                 "backward": lambda: plan.backward(c["x"], c["gamma"], c["mean"], c["rstd"], c["dy"], c["dx"], c["dgamma"],
+                                                   c["dbeta"])}
+        calls["forward"]()
+        plan.check()
+        plan.set_timeout(LIMIT)
+        plan.set_wait_test(16, every)
+        began = time.perf_counter()
+        _times_out(gemm_lib, plan, calls[name])
+        assert time.perf_counter() - began < 2.0
+        plan.set_wait_test(0)
+        plan.set_timeout(0)
+        calls["forward"]()
+        calls["backward"]()
+        ops._check_norm(c, elem, weight)
+        plan.check()
+
+
+@pytest.mark.parametrize("make", [lambda g: g.DistillPlan(4, 5000, 3, "f32"), lambda g: g.NormPlan(4, 5000, "f32")])
+def test_wait_test_hook_validates(gemm_lib, make):
+    with make(gemm_lib) as plan:
         for bad in ((7, 1), (8192, 1), (16, 0)):
             with pytest.raises(gemm_lib.GemmError) as e:
                 plan.set_wait_test(*bad)
