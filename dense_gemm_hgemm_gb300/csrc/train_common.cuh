@@ -462,12 +462,28 @@ inline gemm_status_t allocate(void** p, size_t bytes) {
     return GEMM_ERR_OOM;
 }
 
-// Synchronise, then read and clear an error word.
+// Zeros, written before it returns whatever the default stream has queued (a memset there could
+// clear an error word after a kernel on another stream has set it).
+inline gemm_status_t clear_now(void* p, size_t bytes) {
+    cudaStream_t stream;
+    if (cudaStreamCreateWithFlags(&stream, cudaStreamNonBlocking) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_CUDA;
+    }
+    const bool ok = cudaMemsetAsync(p, 0, bytes, stream) == cudaSuccess && cudaStreamSynchronize(stream) == cudaSuccess;
+    if (cudaStreamDestroy(stream) == cudaSuccess && ok) return GEMM_OK;
+    cudaGetLastError();
+    return GEMM_ERR_CUDA;
+}
+
+// Synchronise, then read and clear an error word, all on the stream.
 inline gemm_status_t check_error_word(int32_t* word, void* stream_ptr) {
+    const cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
     int32_t value = 0;
-    if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream_ptr)) != cudaSuccess ||
-        cudaMemcpy(&value, word, sizeof(value), cudaMemcpyDeviceToHost) != cudaSuccess ||
-        (value != 0 && cudaMemset(word, 0, sizeof(value)) != cudaSuccess)) {
+    if (cudaMemcpyAsync(&value, word, sizeof(value), cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+        cudaStreamSynchronize(stream) != cudaSuccess ||
+        (value != 0 && (cudaMemsetAsync(word, 0, sizeof(value), stream) != cudaSuccess ||
+                        cudaStreamSynchronize(stream) != cudaSuccess))) {
         cudaGetLastError();
         return GEMM_ERR_CUDA;
     }

@@ -1197,8 +1197,7 @@ gemm_status_t gemm_distill_plan_create(int64_t max_rows, int64_t vocab, int64_t 
     st = gbt::allocate(&word, 256);
     if (st != GEMM_OK) return st;
     gemm_distill_plan* p = new (std::nothrow) gemm_distill_plan();
-    if (!p || cudaMemset(word, 0, 256) != cudaSuccess) {
-        cudaGetLastError();
+    if (!p || gbt::clear_now(word, 256) != GEMM_OK) {
         cudaFree(word);
         st = p ? GEMM_ERR_CUDA : GEMM_ERR_OOM;
         delete p;

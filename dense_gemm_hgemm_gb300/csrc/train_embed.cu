@@ -683,8 +683,7 @@ gemm_status_t gemm_embed_plan_create(int64_t vocab, int64_t dim, int64_t max_tok
         return GEMM_ERR_LAUNCH;
     }
     gemm_embed_plan* p = new (std::nothrow) gemm_embed_plan();
-    if (!p || cudaMemset(memory, 0, 256) != cudaSuccess) {
-        cudaGetLastError();
+    if (!p || gbt::clear_now(memory, 256) != GEMM_OK) {
         cudaFree(memory);
         st = p ? GEMM_ERR_CUDA : GEMM_ERR_OOM;
         delete p;

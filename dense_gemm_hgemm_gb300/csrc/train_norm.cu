@@ -1297,8 +1297,7 @@ gemm_status_t gemm_norm_plan_create(int64_t max_rows, int64_t cols, gemm_elem_t 
     gemm_status_t room = gbt::allocate(&memory, 256 + sums);
     if (room != GEMM_OK) return room;
     gemm_norm_plan* p = new (std::nothrow) gemm_norm_plan();
-    if (!p || cudaMemset(memory, 0, 256) != cudaSuccess) {
-        cudaGetLastError();
+    if (!p || gbt::clear_now(memory, 256) != GEMM_OK) {
         cudaFree(memory);
         room = p ? GEMM_ERR_CUDA : GEMM_ERR_OOM;
         delete p;
