@@ -20,6 +20,7 @@ struct gemm_distill_plan {
     gemm_elem_t elem;
     int device, num_sms;
     int32_t* error_word;
+    float2* sums;            // of rows that no cluster can hold: maximum and sum, between the directions
     gbt::Waits waits;
     gbt::StreamShape forward, both;
 };
@@ -55,6 +56,7 @@ struct Args {
     float* loss;
     float* lse;
     int32_t* error;
+    float2* sums;          // each row's maximum and sum, where both directions are two kernels
     Teacher teacher;
     int64_t ldl, ldd;
     float temperature;
@@ -204,30 +206,104 @@ __device__ void join_equal_ids(const Entries& en, int top) {
 
 // ---- running maximum and sum ----------------------------------------------------------
 //
-// One pass over the row gives both.  Of a set of logits s: k = max s c, in log2 units, and sum exp2(s c - k).  The reference
-// k is rounded once and subtracted exactly from then on, so it costs no accuracy.  A
-// reference below kMasked is that of masked logits only (-infinity, or a type's lowest
-// value, whose scaled value may leave fp32): their sum counts from zero and is zero.
+// One pass over the row gives both.  Of a set of logits s: m = max s and sum exp2((s - m) c), c
+// being log2(e) / temperature.  Where |m c| is below kNear, that is exp2(s c - k) with k = m c
+// rounded, one instruction for two logits, times exp2 of that rounding, which is exact and
+// applied once.  Further out it would be exp2 of hundreds: there the maximum is subtracted
+// from the logits first.  (Without that, rows at masks of -1e10 gave infinities or nothing.)
+// A maximum below the limit of masks (-infinity, or a type's lowest value) is that of masked
+// logits only: their sum counts from zero and is zero.
 
-constexpr float kMasked = -1e30f;
+constexpr float kMasked = -1e30f;             // m c
+constexpr float kNear = 268435456.f;          // 2^28: m c is rounded by 16 at most
+constexpr float kNearGiven = 4194304.f;       // 2^22: a given log-sum-exp, by a fifth
 
-__device__ __forceinline__ float finite_base(float k) { return k < kMasked ? 0.f : k; }
+__device__ __forceinline__ float finite_base(float m, float c) { return m * c < kMasked ? 0.f : m; }
 
-__device__ __forceinline__ void merge(float& k, float& s, float k2, float s2) {
-    const float high = fmaxf(k, k2), base = finite_base(high);
-    s = s * exp2_fast(k - base) + s2 * exp2_fast(k2 - base);
-    k = high;
+// Of a set of logits and teacher entries: m, the sum, the entries' part of the loss, p (log2 p -
+// (x - m) c), x being the logit at the entry, and their mass.
+struct alignas(16) Part {
+    float m, sum, terms, here;
+    // The same, counted from a maximum that is no lower.
+    __device__ __forceinline__ void count_from(float high, float c) {
+        const float d = (m - finite_base(high, c)) * c;
+        sum *= exp2_fast(d);
+        if (here != 0.f) terms -= here * d;
+        m = high;
+    }
+    __device__ __forceinline__ void add_entry(float p, float log2p, float x, float c) {
+        if (x > m) count_from(x, c);
+        terms += p * (log2p - (x - finite_base(m, c)) * c);
+        here += p;
+    }
+};
+
+// The parts of LANES neighbouring lanes joined, in each of them (ENTRIES: with terms and mass).
+template <int LANES, bool ENTRIES>
+__device__ __forceinline__ void join_lanes(Part& p, float c) {
+    float high = p.m;
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
+    p.count_from(high, c);
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) {
+        p.sum += __shfl_xor_sync(0xffffffffu, p.sum, o);
+        if (ENTRIES) {
+            p.terms += __shfl_xor_sync(0xffffffffu, p.terms, o);
+            p.here += __shfl_xor_sync(0xffffffffu, p.here, o);
+        }
+    }
+}
+
+// The parts of a row's blocks joined, by a whole warp.
+__device__ __forceinline__ Part join_blocks(const Part* parts, int blocks, float c) {
+    if (blocks == 2) {
+        Part all = parts[0], other = parts[1];
+        const float high = fmaxf(all.m, other.m);
+        all.count_from(high, c);
+        other.count_from(high, c);
+        all.sum += other.sum;
+        all.terms += other.terms;
+        all.here += other.here;
+        return all;
+    }
+    const int r = threadIdx.x % kMaxCluster;
+    Part all = r < blocks ? parts[r] : Part{-INFINITY, 0.f, 0.f, 0.f};
+    join_lanes<kMaxCluster, true>(all, c);
+    return all;
+}
+
+// The sum over a thread's packs of a row (first, first + step, ... of those from the 16-byte
+// boundary off elements before src on) counted from their maximum m.  It is rare; the pipeline
+// over fp32 rows takes 9% longer with it inside, short rows 4% longer with a call.
+template <typename T>
+__device__ __forceinline__ float far_sum(const T* src, int off, int n, int first, int step, float m, float c) {
+    constexpr int VEC = 16 / static_cast<int>(sizeof(T));
+    const float base = finite_base(m, c);
+    float sum = 0.f;
+#pragma unroll 1
+    for (int at = first * VEC - off; at < n; at += step * VEC)
+#pragma unroll 1
+        for (int i = 0; i < VEC; ++i)
+            if (at + i >= 0 && at + i < n) sum += exp2_fast((to_f32(src[at + i]) - base) * c);
+    return sum;
+}
+template <typename T>
+__device__ __noinline__ float call_far_sum(const T* src, int off, int n, int first, int step, float m, float c) {
+    return far_sum(src, off, n, first, step, m, c);
 }
 
 template <typename T>
 struct Running {
     static constexpr int VEC = 16 / static_cast<int>(sizeof(T));
-    float k = -INFINITY;
+    float m = -INFINITY, k = -INFINITY;       // the maximum, and that times c
     Pair sum = Pair(0.f, 0.f), sum_b = Pair(0.f, 0.f);
 
+    // (below -kNear the sum counts from zero and is zero)
     template <int N>
     __device__ __forceinline__ void add(const Pack<T, VEC> (&q)[N], float c) {
-        const float high = fmaxf(k, pack_max(q) * c), base = finite_base(high);
+        m = fmaxf(m, pack_max(q));
+        const float high = m * c, base = high < -kNear ? 0.f : high;
         const float shrink = exp2_fast(k - base);
         k = high;
         sum = mul2(sum, Pair(shrink, shrink));
@@ -244,30 +320,83 @@ struct Running {
             }
         }
     }
-    __device__ __forceinline__ float total() const {
+    // The logits' part; far from zero they are read once more (see far_sum).
+    __device__ __forceinline__ Part total(float c, const T* src, int off, int n, int first, int step) const {
         float lo, hi;
         add2(sum, sum_b).get(lo, hi);
-        return lo + hi;
+        lo += hi;
+        if (fabsf(k) < kNear) return Part{m, lo * exp2_fast(-fmaf(m, c, -k)), 0.f, 0.f};
+        if (k < kMasked) return Part{m, lo, 0.f, 0.f};
+        return Part{m, call_far_sum(src, off, n, first, step, m, c), 0.f, 0.f};
     }
 };
 
-// A row's softmax: q = inverse * exp2(s c - base).  After a forward pass base is the row's
-// reference and inverse one over its sum, so nothing is rounded between them; from a given
-// log-sum-exp base is that in log2 units, and inverse makes up for its rounding.
+// The smaller of the number and zero; NaN stays.
+__device__ __forceinline__ float at_most_zero(float v) {
+    asm("min.NaN.f32 %0, %0, 0f00000000;" : "+f"(v));
+    return v;
+}
+
+// A row's softmax, from a forward pass' maximum and sum, between which nothing is rounded, or
+// from a given log-sum-exp.  Near: q = inverse * exp2(s c - k), inverse making up for the
+// rounding of k.  Far: q = inverse * exp2((s - base) c + rest), at most inverse (a given
+// log-sum-exp has the rounding of its own size, which is large there).
 struct Softmax {
-    float base, inverse;
-    __device__ __forceinline__ void of_sum(float k, float sum) {
-        base = finite_base(k);
-        inverse = __fdividef(1.f, sum);
+    float base, k, rest, inverse;
+    bool far;
+    __device__ __forceinline__ void of_sum(const Part& row, float c) {
+        base = finite_base(row.m, c);
+        k = base * c;
+        far = !(fabsf(k) < kNear);
+        rest = 0.f;
+        inverse = __fdividef(far ? 1.f : exp2_fast(-fmaf(base, c, -k)), row.sum);
     }
-    __device__ __forceinline__ void of_lse(float lse) {
-        constexpr float kLog2eRest = 1.9259629911e-8f;       // log2(e) - kLog2e
-        base = lse * kLog2e;
-        inverse = exp2_fast(-(fmaf(lse, kLog2e, -base) + lse * kLog2eRest));
+    // (far, whatever the size)
+    __device__ __forceinline__ void of_sum_over(const Part& row, float c) {
+        *this = Softmax{finite_base(row.m, c), 0.f, 0.f, __fdividef(1.f, row.sum), true};
+    }
+    __device__ __forceinline__ void of_lse(float lse, float temperature, float c) {
+        base = lse * temperature;
+        k = base * c;
+        far = !(fabsf(k) < kNearGiven);
+        rest = fmaf(-lse, temperature, base) * c;
+        inverse = far ? 1.f : exp2_fast(rest - fmaf(base, c, -k));
+    }
+    // q over inverse, at a logit
+    __device__ __forceinline__ float at(float s, float c) const {
+        return exp2_fast(far ? at_most_zero(fmaf(s - base, c, rest)) : fmaf(s, c, -k));
     }
     // the log-sum-exp, from the forward pass' sum
-    __device__ __forceinline__ float lse(float sum) const { return fmaf(base, kLn2, kLn2 * log2f(sum)); }
+    __device__ __forceinline__ float lse(float sum, float temperature) const {
+        return fmaf(base, 1.f / temperature, kLn2 * log2f(sum));
+    }
 };
+
+// exp2((s - base) c) of two logits: what short rows take whatever their size (a second path for
+// far rows cost 4% of their time, this one instruction nothing).
+__device__ __forceinline__ Pair exp2_over(Pair s, Pair minus_base, Pair c) {
+    float lo, hi;
+    mul2(add2(s, minus_base), c).get(lo, hi);
+    return Pair(exp2_fast(lo), exp2_fast(hi));
+}
+
+// The sum of that over some packs.
+template <typename T, int VEC, int N>
+__device__ __forceinline__ float sum_over(const Pack<T, VEC> (&q)[N], float base, float c) {
+    const Pair c2(c, c), base2(-base, -base);
+    Pair sum(0.f, 0.f), sum_b(0.f, 0.f);
+#pragma unroll
+    for (int b = 0; b < N; ++b) {
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) {
+            Pair& to = j & 1 ? sum_b : sum;
+            to = add2(to, exp2_over(pair_of(q[b], j), base2, c2));
+        }
+    }
+    float lo, hi;
+    add2(sum, sum_b).get(lo, hi);
+    return lo + hi;
+}
 
 template <typename T>
 __device__ __forceinline__ Pack<T, 16 / sizeof(T)> all_masked() {
@@ -277,11 +406,11 @@ __device__ __forceinline__ Pack<T, 16 / sizeof(T)> all_masked() {
     return q;
 }
 
-// scale * exp2(s c - base) of each element of a pack.
+// scale * exp2(s c - k) of each element of a pack.
 template <typename T, int VEC>
-__device__ __forceinline__ Pack<T, VEC> gradient(const Pack<T, VEC>& q, float c, float base, float scale) {
+__device__ __forceinline__ Pack<T, VEC> gradient(const Pack<T, VEC>& q, float c, float k, float scale) {
     Pack<T, VEC> g;
-    const Pair c2(c, c), all2(-base, -base), scale2(scale, scale);
+    const Pair c2(c, c), all2(-k, -k), scale2(scale, scale);
 #pragma unroll
     for (int j = 0; j < VEC / 2; ++j) {
         float lo, hi;
@@ -291,13 +420,14 @@ __device__ __forceinline__ Pack<T, VEC> gradient(const Pack<T, VEC>& q, float c,
     return g;
 }
 
-// The loss of a row over tau^2 ln 2, from its blocks' parts: the sum over entries of
-// p (log2 p - (s c - k)), each block's from its own k, and p's sum there.
-__device__ __forceinline__ float joined_loss(const float4* parts, int pieces, float base, float mass, float sum) {
-    float total = mass * log2f(sum);
-    for (int r = 0; r < pieces; ++r)
-        total += parts[r].z + (parts[r].w == 0.f ? 0.f : parts[r].w * (base - finite_base(parts[r].x)));
-    return total;
+// The same by exp2_over.
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> gradient_over(const Pack<T, VEC>& q, float c, float base, float scale) {
+    Pack<T, VEC> g;
+#pragma unroll
+    for (int j = 0; j < VEC / 2; ++j)
+        set_pair(g, j, mul2(Pair(scale, scale), exp2_over(pair_of(q, j), Pair(-base, -base), Pair(c, c))));
+    return g;
 }
 
 // ---- the kernel ------------------------------------------------------------------------
@@ -312,13 +442,13 @@ __device__ __forceinline__ float joined_loss(const float4* parts, int pieces, fl
 // six or more an SM hide one another's waits (2048 x 50021 fp16: 61 us, 0.97 of the copy
 // bandwidth).
 template <typename T, int MODE>
-__global__ void __launch_bounds__(kThreads, 4) distill_kernel(const Args<T> a) {
+__global__ void __launch_bounds__(kThreads, MODE != kBackward ? 4 : sizeof(T) == 2 ? 8 : 6) distill_kernel(const Args<T> a) {
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     constexpr bool kLoss = (MODE & kForward) != 0, kGrad = (MODE & kBackward) != 0;
     extern __shared__ __align__(16) uint8_t memory[];
     __shared__ uint64_t barrier;
-    __shared__ float4 exchange[kMaxCluster];     // a block's m, sum, loss part, mass part
-    __shared__ float part[2][kWarps];
+    __shared__ Part exchange[kMaxCluster];
+    __shared__ Part part[kWarps];
     __shared__ float row_mass;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int64_t row = blockIdx.x / static_cast<unsigned>(a.pieces);
@@ -354,8 +484,15 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const Args<T> a) {
     T* d = nullptr;
     if (kGrad) d = a.dlogits + row * a.ldd + begin;
 
-    Softmax row_q = {0.f, 0.f};
-    if (MODE == kBackward) row_q.of_lse(given_lse);
+    Softmax row_q = {0.f, 0.f, 0.f, 0.f, false};
+    if (MODE == kBackward && !out) {
+        if (a.sums) {
+            const float2 row_sum = a.sums[row];
+            row_q.of_sum({row_sum.x, row_sum.y, 0.f, 0.f}, c);
+        } else {
+            row_q.of_lse(given_lse, a.temperature, c);
+        }
+    }
     bool empty = out;
     const T* src = a.logits + row * a.ldl + begin;
     const int off = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15u) / sizeof(T));
@@ -381,34 +518,26 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const Args<T> a) {
                 run.add(q, c);
             }
         }
-        float k = run.k, sum = run.total();
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            merge(k, sum, __shfl_xor_sync(0xffffffffu, k, o), __shfl_xor_sync(0xffffffffu, sum, o));
-        if (lane == 0) {
-            part[0][warp] = k;
-            part[1][warp] = sum;
-        }
+        Part mine = run.total(c, s, off, n, tid, kThreads);
+        join_lanes<32, false>(mine, c);
+        if (lane == 0) part[warp] = mine;
         __syncthreads();
-        k = part[0][0];
-        sum = part[1][0];
-        for (int w = 1; w < kWarps; ++w) merge(k, sum, part[0][w], part[1][w]);
-        // the entries in the piece: p (log2 p - (s c - k)), and their mass
+        // the piece's, and the entries in it
         if (warp == 0) {
-            float terms = 0.f, here = 0.f;
+            mine = part[lane % kWarps];
+            join_lanes<kWarps, false>(mine, c);
             if (!out) {
-                const float base = finite_base(k);
+                const float base = finite_base(mine.m, c);
                 for (int j = lane; j < top; j += 32) {
                     const int at = en.id[j] - begin;
                     if (en.id[j] >= 0 && at >= 0 && at < n && !(en.p[j] == 0.f)) {
-                        terms += en.p[j] * (en.log2p[j] - (to_f32(s[at]) * c - base));
-                        here += en.p[j];
+                        mine.terms += en.p[j] * (en.log2p[j] - (to_f32(s[at]) - base) * c);
+                        mine.here += en.p[j];
                     }
                 }
-                terms = warp_sum(terms);
-                here = warp_sum(here);
+                mine.terms = warp_sum(mine.terms);
+                mine.here = warp_sum(mine.here);
             }
-            const float4 mine = make_float4(k, sum, terms, here);
             if (shared_row) {
                 __syncwarp();
                 // every block has started: put this block's numbers into each one's memory
@@ -418,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const Args<T> a) {
                     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
                                  : "=r"(remote) : "r"(shared_address(&exchange[rank])), "r"(lane));
                     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};"
-                                 :: "r"(remote), "f"(mine.x), "f"(mine.y), "f"(mine.z), "f"(mine.w)
+                                 :: "r"(remote), "f"(mine.m), "f"(mine.sum), "f"(mine.terms), "f"(mine.here)
                                  : "memory");
                 }
             } else if (lane == 0) {
@@ -433,14 +562,13 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const Args<T> a) {
         } else {
             __syncthreads();
         }
-        float high = exchange[0].x, all = exchange[0].y;
-        for (int r = 1; r < a.pieces; ++r) merge(high, all, exchange[r].x, exchange[r].y);
-        row_q.of_sum(high, all);
-        empty = out || all == 0.f;
+        const Part all = join_blocks(exchange, a.pieces, c);
+        row_q.of_sum(all, c);
+        empty = out || all.sum == 0.f;
         if (rank == 0 && tid == 0) {
-            const float total = joined_loss(exchange, a.pieces, row_q.base, mass, all);
+            const float total = all.terms + mass * log2f(all.sum);
             a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * total;
-            a.lse[row] = empty ? -INFINITY : row_q.lse(all);
+            a.lse[row] = empty ? -INFINITY : row_q.lse(all.sum, a.temperature);
         }
     }
     if (!kGrad) {
@@ -451,13 +579,16 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const Args<T> a) {
     const bool same = (reinterpret_cast<uintptr_t>(d) & 15u) == (reinterpret_cast<uintptr_t>(src) & 15u);
     const float scale = a.temperature * (a.dloss ? a.dloss[row] : 1.f);
     const float q_scale = scale * (mass * row_q.inverse);
-    for (int k = tid; k < packs; k += kThreads) {
+    if (!empty && row_q.far) {
+#pragma unroll 1
+        for (int i = tid; i < n; i += kThreads) d[i] = from_f32<T>(q_scale * row_q.at(to_f32(s[i]), c));
+    } else for (int k = tid; k < packs; k += kThreads) {
         Pack<T, VEC> g;
         if (empty) {
 #pragma unroll
             for (int i = 0; i < VEC; ++i) g.set(i, 0.f);
         } else {
-            g = gradient(load_pack<T, VEC>(room + k * VEC, VEC), c, row_q.base, q_scale);
+            g = gradient(load_pack<T, VEC>(room + k * VEC, VEC), c, row_q.k, q_scale);
         }
         const int at = k * VEC - off;                    // the pack's first element in the piece
         if (same && at >= 0 && at + VEC <= n) {
@@ -481,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 4) distill_kernel(const Args<T> a) {
                 first = first && k >= j;
             }
             if (first)
-                d[at] = from_f32<T>(scale * (mass * row_q.inverse * exp2_fast(to_f32(s[at]) * c - row_q.base) - p));
+                d[at] = from_f32<T>(scale * (mass * row_q.inverse * row_q.at(to_f32(s[at]), c) - p));
         }
     }
     if (!arrived) wait_phase(&barrier, 0, a.waits.limit);       // (as above)
@@ -525,8 +656,8 @@ struct StreamBarriers {
     uint64_t full[kMostStages], empty[kMostStages];
     uint64_t entries_full[kMostSlots], entries_empty[kMostSlots];
     uint64_t exchanged[2];
-    float4 exchange[2][kMaxCluster];
-    float part[2][3][kComputeWarps];
+    Part exchange[2][kMaxCluster];
+    Part part[2][kComputeWarps];
     float mass[kMostSlots], scale[kMostSlots];
     uint32_t sent[kMaxCluster];      // exchanges that each block of the cluster took part in, at its end
     uint32_t patience;       // ns that a wait may last; 0: one ran out, nothing waits any more
@@ -681,9 +812,8 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
             const int packs = (off + n + VEC - 1) / VEC;
             const Turn row_stage = stage;
             bool empty = out;
-            Softmax row_q = {0.f, 0.f};
-            float row_sum = 0.f;
-            float terms = 0.f;                           // of the loss: sum p (log2 p - x c)
+            Softmax row_q = {0.f, 0.f, 0.f, 0.f, false};
+            Part all = {0.f, 0.f, 0.f, 0.f};
             if (out) {
                 compute_barrier();
             } else {
@@ -709,37 +839,24 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
                     run.add(q, c);
                     stage.next(1, stages);
                 }
-                // the entries of this part (forward: of the row, by the row's first block)
+                // and the entries of this part
+                all = run.total(c, src, off, n, thread, kComputeThreads);        // (the stages may have gone)
                 for (int j = thread; j < top; j += kComputeThreads) {
                     const int at = en.id[j] - begin;
-                    if (en.id[j] < 0 || (kGrad ? at < 0 || at >= n : rank != 0)) continue;
+                    if (en.id[j] < 0 || at < 0 || at >= n) continue;
                     if (kGrad) {                         // the row's stages still hold its logits
                         int s = row_stage.at + (off + at) / kStage;
                         if (s >= stages) s -= stages;
                         en.x[j] = to_f32(ring[s * kStage + (off + at) % kStage]);
                     }
-                    if (!(en.p[j] == 0.f)) terms += en.p[j] * (en.log2p[j] - en.x[j] * c);
+                    if (!(en.p[j] == 0.f)) all.add_entry(en.p[j], en.log2p[j], en.x[j], c);
                 }
-                float k = run.k, sum = run.total();
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
-                    merge(k, sum, __shfl_xor_sync(0xffffffffu, k, o), __shfl_xor_sync(0xffffffffu, sum, o));
-                terms = warp_sum(terms);
+                join_lanes<32, true>(all, c);
                 const int turn = exchanges & 1;
-                if (lane == 0) {
-                    sh.part[turn][0][worker] = k;
-                    sh.part[turn][1][worker] = sum;
-                    sh.part[turn][2][worker] = terms;
-                }
+                if (lane == 0) sh.part[turn][worker] = all;
                 compute_barrier();
-                k = sh.part[turn][0][lane % kComputeWarps];
-                sum = sh.part[turn][1][lane % kComputeWarps];
-                terms = sh.part[turn][2][lane % kComputeWarps];
-#pragma unroll
-                for (int o = kComputeWarps / 2; o > 0; o >>= 1) {
-                    merge(k, sum, __shfl_xor_sync(0xffffffffu, k, o), __shfl_xor_sync(0xffffffffu, sum, o));
-                    terms += __shfl_xor_sync(0xffffffffu, terms, o);
-                }
+                all = sh.part[turn][lane % kComputeWarps];
+                join_lanes<kComputeWarps, true>(all, c);
                 if (kSplit && a.pieces > 1) {
                     // this block's numbers, to each block of the row (none any more once a wait has run out)
                     if (worker == 0 && __shfl_sync(0xffffffffu, is_dead(&sh.patience), 0) == 0) {
@@ -754,30 +871,23 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
                             asm volatile(
                                 "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, "
                                 "[%5];"
-                                :: "r"(slot_at), "f"(k), "f"(sum), "f"(terms), "f"(0.f), "r"(barrier_at) : "memory");
+                                :: "r"(slot_at), "f"(all.m), "f"(all.sum), "f"(all.terms), "f"(all.here), "r"(barrier_at) : "memory");
                         }
                         ++sent;
                         __syncwarp();
                     }
                     if (wait_or_die(&sh.exchanged[turn], (exchanges >> 1) & 1, &sh.patience, a.error) && sent > exchanges)
                         received = sent;
-                    k = sh.exchange[turn][0].x;
-                    sum = sh.exchange[turn][0].y;
-                    terms = sh.exchange[turn][0].z;
-                    for (int r = 1; r < a.pieces; ++r) {
-                        merge(k, sum, sh.exchange[turn][r].x, sh.exchange[turn][r].y);
-                        terms += sh.exchange[turn][r].z;
-                    }
+                    all = join_blocks(sh.exchange[turn], a.pieces, c);
                 }
                 ++exchanges;
-                empty = sum == 0.f;
-                row_q.of_sum(k, sum);
-                row_sum = sum;
+                empty = all.sum == 0.f;
+                row_q.of_sum(all, c);
             }
             if (rank == 0 && thread == 0) {
-                const float total = fmaf(mass, row_q.base, terms) + mass * log2f(row_sum);
+                const float total = all.terms + mass * log2f(all.sum);
                 a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * total;
-                a.lse[row] = empty ? -INFINITY : row_q.lse(row_sum);
+                a.lse[row] = empty ? -INFINITY : row_q.lse(all.sum, a.temperature);
             }
             if (kGrad) {
                 T* const d = a.dlogits + row * a.ldd + begin;
@@ -785,7 +895,19 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
                 const float scale = sh.scale[slot];
                 const float q_scale = scale * (mass * row_q.inverse);
                 stage = row_stage;
-                for (int p0 = 0; p0 < packs; p0 += kStage / VEC) {
+                if (!empty && row_q.far) {
+#pragma unroll 1
+                    for (int i = thread; i < n; i += kComputeThreads) {
+                        int s = row_stage.at + (off + i) / kStage;
+                        if (s >= stages) s -= stages;
+                        d[i] = from_f32<T>(q_scale * row_q.at(to_f32(ring[s * kStage + (off + i) % kStage]), c));
+                    }
+                    __syncwarp();
+                    for (int p0 = 0; p0 < packs; p0 += kStage / VEC) {
+                        if (lane == 0) arrive(&sh.empty[stage.at]);
+                        stage.next(1, stages);
+                    }
+                } else for (int p0 = 0; p0 < packs; p0 += kStage / VEC) {
                     const T* from = ring + stage.at * kStage;
                     const int at0 = (p0 + thread) * VEC - off;       // of the first pack, in the piece
                     if (!empty && same && p0 * VEC >= off && p0 * VEC - off + kStage <= n) {
@@ -793,7 +915,7 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
                         for (int b = 0; b < kBatch; ++b)
                             store_pack<T, VEC>(d + at0 + b * kComputeThreads * VEC, VEC,
                                                gradient(load_pack<T, VEC>(from + (thread + b * kComputeThreads) * VEC, VEC),
-                                                        c, row_q.base, q_scale));
+                                                        c, row_q.k, q_scale));
                     } else {
                         for (int b = 0; b < kBatch; ++b) {
                             const int mine = thread + b * kComputeThreads, at = at0 + b * kComputeThreads * VEC;
@@ -803,7 +925,7 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
 #pragma unroll
                                 for (int i = 0; i < VEC; ++i) g.set(i, 0.f);
                             } else {
-                                g = gradient(load_pack<T, VEC>(from + mine * VEC, VEC), c, row_q.base, q_scale);
+                                g = gradient(load_pack<T, VEC>(from + mine * VEC, VEC), c, row_q.k, q_scale);
                             }
                             if (same && at >= 0 && at + VEC <= n) {
                                 store_pack<T, VEC>(d + at, VEC, g);
@@ -826,7 +948,7 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
                         const float p = en.own[j];
                         const int at = en.id[j] - begin;
                         if (p >= 0.f && at >= 0 && at < n)
-                            d[at] = from_f32<T>(scale * (mass * row_q.inverse * exp2_fast(en.x[j] * c - row_q.base) - p));
+                            d[at] = from_f32<T>(scale * (mass * row_q.inverse * row_q.at(en.x[j], c) - p));
                     }
                 }
             }
@@ -867,8 +989,15 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
 // blocks' and barriers' time of the other kernels is several times that of the memory (16384
 // x 1000 bf16, both directions: 27 us).  Bound by the entries' chain of loads and sums, which is
 // most of the work of such a row (16384 x 250: 18 us).
+// Blocks an SM that are worth holding the registers down for (without a spill): 16384 x 1000 bf16
+// both directions 24.5 us, 29 with a block less.
 template <typename T, int MODE, int PACKS>
-__global__ void __launch_bounds__(kThreads) distill_short_kernel(const Args<T> a, int64_t rows) {
+constexpr int kShortBlocks = sizeof(T) == 4 ? (PACKS == 2 ? 5 : PACKS == 4 ? 4 : PACKS == 8 ? 3 : 2)
+                             : MODE == kForward ? (PACKS <= 4 ? 5 : PACKS == 8 ? 4 : 2)
+                             : PACKS == 2 ? 5 : PACKS == 4 ? 4 : MODE == kBackward ? (PACKS == 8 ? 3 : 2) : PACKS == 8 ? 2 : 1;
+
+template <typename T, int MODE, int PACKS>
+__global__ void __launch_bounds__(kThreads, kShortBlocks<T, MODE, PACKS>) distill_short_kernel(const Args<T> a, int64_t rows) {
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
     constexpr bool kLoss = (MODE & kForward) != 0, kGrad = (MODE & kBackward) != 0;
     extern __shared__ __align__(16) uint8_t memory[];
@@ -901,24 +1030,20 @@ __global__ void __launch_bounds__(kThreads) distill_short_kernel(const Args<T> a
     const float mass = load_entries(en, a.teacher, row, src, c, n, a.error);
     if (kGrad) join_equal_ids(en, top);
     bool empty = mass == 0.f || (MODE == kBackward && given == -INFINITY);
-    Softmax row_q = {0.f, 0.f};
-    if (MODE == kBackward) row_q.of_lse(given);
+    Softmax row_q = {0.f, 0.f, 0.f, 0.f, false};
+    if (MODE == kBackward) row_q.of_lse(given, a.temperature, c);
     if (kLoss) {
-        Running<T> run;
-        run.add(q, c);
-        float k = run.k, sum = run.total(), terms = 0.f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            merge(k, sum, __shfl_xor_sync(0xffffffffu, k, o), __shfl_xor_sync(0xffffffffu, sum, o));
-        empty = empty || sum == 0.f;
-        row_q.of_sum(k, sum);
+        Part all = {warp_max(pack_max(q)), 0.f, 0.f, 0.f};
+        all.sum = warp_sum(sum_over(q, finite_base(all.m, c), c));
+        empty = empty || all.sum == 0.f;
+        row_q.of_sum_over(all, c);
         if (!empty)
             for (int j = lane; j < top; j += 32)
-                if (!(en.p[j] == 0.f)) terms += en.p[j] * (en.log2p[j] - (en.x[j] * c - row_q.base));
-        terms = warp_sum(terms);
+                if (!(en.p[j] == 0.f)) all.terms += en.p[j] * (en.log2p[j] - (en.x[j] - row_q.base) * c);
+        all.terms = warp_sum(all.terms);
         if (lane == 0) {
-            a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * (terms + mass * log2f(sum));
-            a.lse[row] = empty ? -INFINITY : row_q.lse(sum);
+            a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * (all.terms + mass * log2f(all.sum));
+            a.lse[row] = empty ? -INFINITY : row_q.lse(all.sum, a.temperature);
         }
     }
     if (!kGrad) return;
@@ -926,6 +1051,10 @@ __global__ void __launch_bounds__(kThreads) distill_short_kernel(const Args<T> a
     const bool same = (reinterpret_cast<uintptr_t>(d) & 15u) == (reinterpret_cast<uintptr_t>(src) & 15u);
     const float q_scale = empty ? 0.f : scale * (mass * row_q.inverse);
     __syncwarp();                                        // the row has been read: d may be the logits
+    if (MODE == kBackward && !empty && row_q.far) {
+#pragma unroll 1
+        for (int i = lane; i < n; i += 32) d[i] = from_f32<T>(q_scale * row_q.at(to_f32(src[i]), c));
+    } else
 #pragma unroll
     for (int b = 0; b < PACKS; ++b) {
         const int at = (b * 32 + lane) * VEC - off;
@@ -934,7 +1063,7 @@ __global__ void __launch_bounds__(kThreads) distill_short_kernel(const Args<T> a
 #pragma unroll
             for (int i = 0; i < VEC; ++i) g.set(i, 0.f);
         } else {
-            g = gradient(q[b], c, row_q.base, q_scale);
+            g = kLoss ? gradient_over(q[b], c, row_q.base, q_scale) : gradient(q[b], c, row_q.k, q_scale);
         }
         if (same && at >= 0 && at + VEC <= n) {
             store_pack<T, VEC>(d + at, VEC, g);
@@ -949,7 +1078,7 @@ __global__ void __launch_bounds__(kThreads) distill_short_kernel(const Args<T> a
     for (int j = lane; j < top; j += 32)
         if (en.own[j] >= 0.f)
             d[en.id[j]] =
-                from_f32<T>(scale * (mass * row_q.inverse * exp2_fast(en.x[j] * c - row_q.base) - en.own[j]));
+                from_f32<T>(scale * (mass * row_q.inverse * row_q.at(en.x[j], c) - en.own[j]));
 }
 
 // ---- rows that no cluster can hold ---------------------------------------------------------
@@ -959,7 +1088,7 @@ __global__ void __launch_bounds__(kThreads) distill_short_kernel(const Args<T> a
 template <typename T>
 __global__ void __launch_bounds__(kThreads) distill_forward_wide_kernel(const Args<T> a) {
     extern __shared__ __align__(16) uint8_t memory[];
-    __shared__ float part[2][kWarps];
+    __shared__ Part part[kWarps];
     __shared__ float row_mass;
     const int top = a.teacher.top, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     Entries en;
@@ -977,35 +1106,29 @@ __global__ void __launch_bounds__(kThreads) distill_forward_wide_kernel(const Ar
     }
     __syncthreads();
     const float mass = row_mass;
-    float k = -INFINITY, sum = 0.f;
+    Part all = {-INFINITY, 0.f, 0.f, 0.f};
     if (mass != 0.f) {
-        for (int i = threadIdx.x; i < a.vocab; i += kThreads) k = fmaxf(k, to_f32(s[i]) * c);
-        const float base = finite_base(k);
-        for (int i = threadIdx.x; i < a.vocab; i += kThreads) sum += exp2_fast(to_f32(s[i]) * c - base);
+        for (int i = threadIdx.x; i < a.vocab; i += kThreads) all.m = fmaxf(all.m, to_f32(s[i]));
+        const float base = finite_base(all.m, c);
+        for (int i = threadIdx.x; i < a.vocab; i += kThreads) all.sum += exp2_fast((to_f32(s[i]) - base) * c);
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        merge(k, sum, __shfl_xor_sync(0xffffffffu, k, o), __shfl_xor_sync(0xffffffffu, sum, o));
-    if (lane == 0) {
-        part[0][warp] = k;
-        part[1][warp] = sum;
-    }
+    join_lanes<32, false>(all, c);
+    if (lane == 0) part[warp] = all;
     __syncthreads();
     if (warp != 0) return;
-    k = part[0][0];
-    sum = part[1][0];
-    for (int w = 1; w < kWarps; ++w) merge(k, sum, part[0][w], part[1][w]);
-    const bool empty = mass == 0.f || sum == 0.f;
+    all = part[lane % kWarps];
+    join_lanes<kWarps, false>(all, c);
+    const bool empty = mass == 0.f || all.sum == 0.f;
     Softmax row_q;
-    row_q.of_sum(k, sum);
-    float total = 0.f;
+    row_q.of_sum(all, c);
+    if (a.sums && lane == 0) a.sums[row] = make_float2(all.m, all.sum);
     if (!empty)
         for (int j = lane; j < top; j += 32)
-            if (!(en.p[j] == 0.f)) total += en.p[j] * (en.log2p[j] - (to_f32(s[en.id[j]]) * c - row_q.base));
-    total = warp_sum(total);
+            if (!(en.p[j] == 0.f)) all.terms += en.p[j] * (en.log2p[j] - (to_f32(s[en.id[j]]) - row_q.base) * c);
+    all.terms = warp_sum(all.terms);
     if (lane == 0) {
-        a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * (total + mass * log2f(sum));
-        a.lse[row] = empty ? -INFINITY : row_q.lse(sum);
+        a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * (all.terms + mass * log2f(all.sum));
+        a.lse[row] = empty ? -INFINITY : row_q.lse(all.sum, a.temperature);
     }
 }
 
@@ -1194,7 +1317,8 @@ gemm_status_t gemm_distill_plan_create(int64_t max_rows, int64_t vocab, int64_t 
     st = gbt::with_elem(elem, [](auto v) { return gbt::prepare<decltype(v)>(); });
     if (st != GEMM_OK) return st;
     void* word = nullptr;
-    st = gbt::allocate(&word, 256);
+    const size_t sums = gbt::fits(vocab, gbt::elem_bytes(elem)) ? 0 : static_cast<size_t>(max_rows) * sizeof(float2);
+    st = gbt::allocate(&word, 256 + sums);
     if (st != GEMM_OK) return st;
     gemm_distill_plan* p = new (std::nothrow) gemm_distill_plan();
     if (!p || gbt::clear_now(word, 256) != GEMM_OK) {
@@ -1210,6 +1334,7 @@ gemm_status_t gemm_distill_plan_create(int64_t max_rows, int64_t vocab, int64_t 
     p->device = device;
     p->num_sms = sms;
     p->error_word = static_cast<int32_t*>(word);
+    p->sums = reinterpret_cast<float2*>(static_cast<uint8_t*>(word) + 256);
     gbt::with_elem(elem, [&](auto v) {
         p->forward = gbt::stream_shape<decltype(v), gbt::kForward>(vocab, max_top);
         p->both = gbt::stream_shape<decltype(v), gbt::kBoth>(vocab, max_top);
@@ -1287,6 +1412,7 @@ gemm_status_t gemm_distill_forward_backward(gemm_distill_plan_t p, int64_t rows,
         if (p->both.clusters > 0 && rows >= p->both.clusters)
             return gbt::run_stream<T, gbt::kBoth>(a, p->both, rows, queue);
         if (gbt::fits(p->vocab, sizeof(T))) return gbt::run<T, gbt::kBoth>(a, rows, p->num_sms, queue);
+        a.sums = p->sums;
         const gemm_status_t first = gbt::run_forward_wide(a, rows, queue);
         return first == GEMM_OK ? gbt::run<T, gbt::kBackward>(a, rows, p->num_sms, queue) : first;
     });

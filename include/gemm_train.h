@@ -217,9 +217,10 @@ gemm_status_t gemm_distill_forward(gemm_distill_plan_t plan, int64_t rows, const
 
 /*
  * dlogits_i = dloss * tau * (P * q_i - sum of p_j over j with ids_j == i),
- * P = sum_j p_j, from the forward call's lse.  dloss: the upstream gradient of
- * each row's loss (`rows` fp32 values), or NULL for ones.  dlogits may be logits
- * (same stride).
+ * P = sum_j p_j, from the forward call's lse.  That is a number in fp32: each q_i is
+ * as far off, relatively, as lse is absolutely (2^-24 of its size; from 2^22 on no q_i
+ * is above one).  dloss: the upstream gradient of each row's loss (`rows` fp32
+ * values), or NULL for ones.  dlogits may be logits (same stride).
  */
 gemm_status_t gemm_distill_backward(gemm_distill_plan_t plan, int64_t rows, const void *logits,
                                     int64_t ldl, const gemm_teacher_t *teacher, float temperature,
@@ -229,7 +230,7 @@ gemm_status_t gemm_distill_backward(gemm_distill_plan_t plan, int64_t rows, cons
 /*
  * Both in one call, for a training step whose upstream gradient is known before
  * the loss: each row's logits are read from memory once where they fit on the
- * chip.
+ * chip, and the gradient does not go through the rounded lse.
  */
 gemm_status_t gemm_distill_forward_backward(gemm_distill_plan_t plan, int64_t rows,
                                             const void *logits, int64_t ldl,

@@ -1,0 +1,77 @@
+"""Distillation and layer norm at values far from one, where a formula's steps can leave fp32
+although its result does not."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import test_train_ops_gpu as ops
+import train_oracle as to
+
+pytestmark = pytest.mark.gpu
+
+
+# few and many short rows; rows in pieces, a cluster's each; the pipeline, by one block and by clusters; wide rows
+SIZES = [(3, 40), (700, 40), (3, 9000), (700, 9000), (160, 66000), (1, 850000)]
+
+
+@pytest.mark.parametrize("rows,vocab", SIZES)
+@pytest.mark.parametrize("tau", [1.0, 0.7])
+def test_distillation_of_shifted_rows(gemm_lib, rows, vocab, tau):
+    """A number added to all of a row's logits changes its log-sum-exp alone.  The logits are multiples of 1/8, so they
+    and the shift add exactly; the bounds are those of the rows before the shift."""
+    tau = float(np.float32(tau))
+    c = ops._distill_case(rows, vocab, 9, "f32", "f32", "i64", 0, 0, False, tau)
+    near = torch.round(c["logits"] * 8) / 8
+    c["logits"] = near
+    args = (ops._f64(near), c["ids"].cpu().numpy(), ops._f64(c["values"]), tau)
+    want = to.distill(*args, dloss=ops._f64(c["dloss"]))
+    bound = to.distill_bounds(*args, "f32", dloss=ops._f64(c["dloss"]))
+    with gemm_lib.DistillPlan(rows, vocab, 9, "f32") as plan:
+        for shift in (0.0, 2.0 ** 20, -2.0 ** 20):
+            far = near + shift
+            far[near == -math.inf] = -math.inf
+            for both in (False, True):
+                c["loss"].fill_(7.0)
+                if both:
+                    plan.forward_backward(far, c["ids"], c["values"], c["loss"], c["lse"], c["dlogits"], dloss=c["dloss"],
+                                          temperature=tau)
+                    ops._within(c["dlogits"], want[2], bound[2], "dlogits of rows moved by %g" % shift)
+                else:
+                    plan.forward(far, c["ids"], c["values"], c["loss"], c["lse"], temperature=tau)
+                ops._within(c["loss"], want[0], bound[0], "loss of rows moved by %g" % shift)
+                ops._within(c["lse"], want[1] + shift / tau, bound[1] + 4 * to.U * abs(shift / tau),
+                            "lse of rows moved by %g" % shift)
+
+
+@pytest.mark.parametrize("rows,vocab", SIZES)
+@pytest.mark.parametrize("elem", ["f32", "bf16"])
+@pytest.mark.parametrize("tau", [1.0, 0.5, 0.7, 30.0])
+@pytest.mark.parametrize("level", [-1e9, -3e9, -1e10, -1e20, 1e15])
+def test_distillation_of_level_rows(gemm_lib, rows, vocab, elem, tau, level):
+    """Rows whose logits are all one large number (a mask that leaves nothing and is no infinity): uniform."""
+    tau = float(np.float32(tau))
+    ids, values = torch.tensor([[1, 5]], device="cuda").repeat(rows, 1), torch.zeros(rows, 2, device="cuda")
+    loss, lse = torch.full((rows,), 7.0, device="cuda"), torch.empty(rows, device="cuda")
+    logits = torch.full((rows, vocab), level, device="cuda").to(ops.TYPES[elem])
+    level = float(logits[0, 0])
+    grad = torch.full((rows, vocab), 7.0, device="cuda").to(ops.TYPES[elem])
+    # p = 1/2 twice, q = 1 / vocab: some roundings of numbers up to the logarithms; the sum of vocab ones
+    few = 64 * to.U + to.lanes(vocab)
+    want = tau * tau * math.log(vocab / 2)
+    q = torch.full((vocab,), 1.0 / vocab, device="cuda", dtype=torch.float64)
+    q[[1, 5]] -= 0.5
+    with gemm_lib.DistillPlan(rows, vocab, 2, elem) as plan:
+        for both in (False, True):
+            if both:
+                plan.forward_backward(logits, ids, values, loss, lse, grad, temperature=tau)
+                off = (grad.double() - tau * q).abs()
+                assert bool((off <= tau * few * (1.0 / vocab + 0.5 * (q < 0)) + to.ROUND[elem] * tau * q.abs()).all())
+            else:
+                plan.forward(logits, ids, values, loss, lse, temperature=tau)
+            assert bool(((loss - want).abs() <= few * tau * tau * (math.log(vocab) + 1)).all())
+            assert bool(((lse - level / tau).abs() <= 4 * to.U * abs(level / tau) + math.log(vocab)).all())
+        # log(vocab) is below the unit of such a log-sum-exp: what the gradient makes of it is finite
+        plan.backward(logits, ids, values, lse, grad, temperature=tau)
+        assert bool((grad.abs() <= tau).all())
