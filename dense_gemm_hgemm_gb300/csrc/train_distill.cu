@@ -214,7 +214,7 @@ __device__ void join_equal_ids(const Entries& en, int top) {
 // A maximum below the limit of masks (-infinity, or a type's lowest value) is that of masked
 // logits only: their sum counts from zero and is zero.
 
-constexpr float kMasked = -1e30f;             // m c
+constexpr float kMasked = -1e30f * kLog2e;    // m c, of a logit of -1e30 times the temperature
 constexpr float kNear = 268435456.f;          // 2^28: m c is rounded by 16 at most
 constexpr float kNearGiven = 4194304.f;       // 2^22: a given log-sum-exp, by a fifth
 

@@ -75,3 +75,36 @@ def test_distillation_of_level_rows(gemm_lib, rows, vocab, elem, tau, level):
         # log(vocab) is below the unit of such a log-sum-exp: what the gradient makes of it is finite
         plan.backward(logits, ids, values, lse, grad, temperature=tau)
         assert bool((grad.abs() <= tau).all())
+
+
+@pytest.mark.parametrize("rows,vocab", [(3, 40), (3, 9000), (700, 9000), (700, 40)])
+def test_distillation_limit_of_masks(gemm_lib, rows, vocab):
+    """A logit below -1e30 times the temperature is a mask, one above it is a logit: a row that has only such
+    ones is uniform.  (At this temperature the scale of the exponents is exactly one.)"""
+    tau = float(np.float32(1.4426950408889634))
+    kept, masked = -1.2e30, -1.5e30
+    ids, values = torch.tensor([[1, 5]], device="cuda").repeat(rows, 1), torch.zeros(rows, 2, device="cuda")
+    loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    grad = torch.empty(rows, vocab, device="cuda")
+    with gemm_lib.DistillPlan(rows, vocab, 2, "f32") as plan:
+        for level in (kept, masked):
+            logits = torch.full((rows, vocab), level, device="cuda")
+            for both in (False, True):
+                loss.fill_(7.0)
+                grad.fill_(7.0)
+                if both:
+                    plan.forward_backward(logits, ids, values, loss, lse, grad, temperature=tau)
+                else:
+                    plan.forward(logits, ids, values, loss, lse, temperature=tau)
+                if level == masked:
+                    assert not bool(loss.any()) and bool((lse == -math.inf).all())
+                    assert not both or not bool(grad.any())
+                    continue
+                # p = 1/2 twice, q = 1 / vocab: a few roundings of numbers up to log(vocab)
+                want = tau * tau * math.log(vocab / 2)
+                assert bool(((loss - want).abs() <= 64 * to.U * want).all())
+                assert bool(((lse - kept / tau).abs() <= 4 * to.U * -kept).all())
+                if both:
+                    q = torch.full((vocab,), 1.0 / vocab, device="cuda", dtype=torch.float64)
+                    q[[1, 5]] -= 0.5
+                    assert bool(((grad.double() - tau * q).abs() <= 64 * to.U * (1.0 / vocab + 0.5 * (q < 0))).all())
