@@ -105,7 +105,7 @@ struct Entries {
     float* own;    // sum of p over an id's equals at its first entry, -1 at the others
 };
 
-// One warp: a row's entries; returns the mass.  Logits are scaled to log2 values by
+// One warp: a row's entries; returns the mass.  Values are scaled to log2 units by
 // c = log2(e) / temperature.  `logits`: the row's, whose values at the ids go to en.x, or
 // null.  The loads of kBatch * 32 entries are in flight together.
 template <typename T>
@@ -140,23 +140,24 @@ __device__ float load_entries(const Entries& en, const Teacher& t, int64_t row, 
         for (int u = 0; u < kBatch; ++u) {
             const int j = j0 + u * 32;
             if (j >= t.top) break;
-            const float l = id[u] < 0 ? -INFINITY : v[u] * c;
+            const float own = id[u] < 0 ? -INFINITY : v[u];
             en.id[j] = id[u] < 0 ? -1 : static_cast<int32_t>(id[u]);
-            en.log2p[j] = l;
+            en.log2p[j] = own;
             if (logits) en.x[j] = x[u];
-            high = fmaxf(high, l);
+            high = fmaxf(high, own);
         }
     }
-    float norm = given;
+    // log2 p = (v - base) c - rest: the largest value is taken off before the values are scaled
+    float base = 0.f, rest = given;
     if (!t.lse) {
         high = warp_max(high);
-        for (int j = lane; j < t.top; j += 32)
-            sum += en.log2p[j] == -INFINITY ? 0.f : exp2_fast(en.log2p[j] - high);
-        norm = high + log2f(warp_sum(sum));
+        base = high == -INFINITY ? 0.f : high;
+        for (int j = lane; j < t.top; j += 32) sum += exp2_fast((en.log2p[j] - base) * c);
+        rest = log2f(warp_sum(sum));
     }
     sum = 0.f;
     for (int j = lane; j < t.top; j += 32) {
-        const float l = en.log2p[j] == -INFINITY ? -INFINITY : en.log2p[j] - norm;
+        const float l = en.log2p[j] == -INFINITY ? -INFINITY : fmaf(en.log2p[j] - base, c, -rest);
         en.log2p[j] = l;
         en.p[j] = exp2_fast(l);
         sum += en.p[j];

@@ -108,3 +108,43 @@ def test_distillation_limit_of_masks(gemm_lib, rows, vocab):
                     q = torch.full((vocab,), 1.0 / vocab, device="cuda", dtype=torch.float64)
                     q[[1, 5]] -= 0.5
                     assert bool(((grad.double() - tau * q).abs() <= 64 * to.U * (1.0 / vocab + 0.5 * (q < 0))).all())
+
+
+@pytest.mark.parametrize("rows,vocab", SIZES)
+@pytest.mark.parametrize("tau", [1.0, 0.7])
+def test_distillation_of_shifted_teachers(gemm_lib, rows, vocab, tau):
+    """A number added to all of a row's teacher values changes nothing where they add exactly (multiples of 1/8)."""
+    tau = float(np.float32(tau))
+    c = ops._distill_case(rows, vocab, 9, "f32", "f32", "i64", 0, 0, False, tau)
+    near = torch.round(c["values"] * 8) / 8
+    args = (ops._f64(c["logits"]), c["ids"].cpu().numpy(), ops._f64(near), tau)
+    want = to.distill(*args, dloss=ops._f64(c["dloss"]))
+    bound = to.distill_bounds(*args, "f32", dloss=ops._f64(c["dloss"]))
+    with gemm_lib.DistillPlan(rows, vocab, 9, "f32") as plan:
+        for shift in (0.0, 2.0 ** 20, -2.0 ** 20):
+            more = {"temperature": tau}
+            plan.forward(c["logits"], c["ids"], near + shift, c["loss"], c["lse"], **more)
+            ops._within(c["loss"], want[0], bound[0], "loss of a teacher moved by %g" % shift)
+            plan.backward(c["logits"], c["ids"], near + shift, c["lse"], c["dlogits"], dloss=c["dloss"], **more)
+            ops._within(c["dlogits"], want[2], bound[2], "dlogits of a teacher moved by %g" % shift)
+            plan.forward_backward(c["logits"], c["ids"], near + shift, c["loss"], c["lse"], c["dlogits"], dloss=c["dloss"], **more)
+            ops._within(c["loss"], want[0], bound[0], "both: loss of a teacher moved by %g" % shift)
+            ops._within(c["dlogits"], want[2], bound[2], "both: dlogits of a teacher moved by %g" % shift)
+
+
+@pytest.mark.parametrize("rows,vocab", SIZES)
+@pytest.mark.parametrize("value,level", [("f32", -3.4028234663852886e38), ("f32", -1e10), ("bf16", -3e38), ("f16", -65504.0)])
+@pytest.mark.parametrize("tau", [1.0, 0.7, 4.0])
+def test_distillation_of_level_teachers(gemm_lib, rows, vocab, value, level, tau):
+    """Only infinities have no mass: four entries of any one value, the type's lowest too, are 1/4 each."""
+    tau = float(np.float32(tau))
+    c = ops._distill_case(rows, vocab, 4, "f32", value, "i64", 0, 0, False, tau, mask=False)
+    args = (ops._f64(c["logits"]), c["ids"].cpu().numpy(), np.zeros((rows, 4)), tau)
+    want = to.distill(*args, dloss=ops._f64(c["dloss"]))
+    bound = to.distill_bounds(*args, "f32", dloss=ops._f64(c["dloss"]))
+    c["values"].fill_(level)
+    with gemm_lib.DistillPlan(rows, vocab, 4, "f32") as plan:
+        plan.forward_backward(c["logits"], c["ids"], c["values"], c["loss"], c["lse"], c["dlogits"], dloss=c["dloss"],
+                              temperature=tau)
+        ops._within(c["loss"], want[0], bound[0], "loss")
+        ops._within(c["dlogits"], want[2], bound[2], "dlogits")
