@@ -924,13 +924,13 @@ __global__ void __launch_bounds__(kWideRing, 1) norm_backward_wide_ring_kernel(c
         if (before >= 0) ring.refill(lane, before, row + (stages - 1) * ring.step);
         before = ring.turn.at;
         if (!a.dx) continue;
-        // dx = rstd dy gamma - rstd mean(g) - (x - mean) rstd^2 mean(g xh)
-        const float at_x = -r * r * (s[1] * inverse_n), at_1 = -r * (s[0] * inverse_n);
-        const Pair at_x2(at_x, at_x), at_12(at_1, at_1);
+        // (rstd^2 is not formed: it would leave fp32 before the result does)
+        const float mean_g = s[0] * inverse_n, mean_gx = s[1] * inverse_n;
+        const Pair minus_g(-mean_g, -mean_g), minus_gx(-mean_gx, -mean_gx);
         T* const dx = a.dx + row * a.lddx;
         Pack<T, VEC> out;
         each_pair<T, W, VEC>(x, dy, gamma, lane, lanes, a.cols, [&](int j, Pair v, Pair d, Pair w) {
-            const Pair y = fma2(mul2(d, r2), w, fma2(add2(v, minus), at_x2, at_12));
+            const Pair y = mul2(r2, fma2(d, w, fma2(mul2(add2(v, minus), r2), minus_gx, minus_g)));
             set_pair(out, j % (VEC / 2), y);
             if (j % (VEC / 2) == VEC / 2 - 1) store_pack<T, VEC>(dx + (j / (VEC / 2) * lanes + lane) * VEC, VEC, out);
         });

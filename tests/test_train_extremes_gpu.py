@@ -148,3 +148,27 @@ def test_distillation_of_level_teachers(gemm_lib, rows, vocab, value, level, tau
                               temperature=tau)
         ops._within(c["loss"], want[0], bound[0], "loss")
         ops._within(c["dlogits"], want[2], bound[2], "dlogits")
+
+
+@pytest.mark.parametrize("rows,cols", [(5, 200), (3000, 333), (1300, 1024), (400, 8192), (320, 8200), (320, 12000), (320, 12003), (3, 17000)])
+@pytest.mark.parametrize("elem", ["f32", "bf16"])
+@pytest.mark.parametrize("exponent", [-76, 70])
+def test_norm_of_small_and_large_rows(gemm_lib, rows, cols, elem, exponent):
+    """Rows times a power of two, without eps: rstd is divided by it, and dx times rstd's change.  The square of either
+    leaves fp32; neither result does.  The bounds are those of the scaled rows."""
+    c = ops._norm_case(rows, cols, elem, "f32", 0, 0, seed=9)
+    scale = 2.0 ** exponent
+    c["x"][1] = torch.randn(cols, device="cuda").to(ops.TYPES[elem])     # (a row without variance has no norm without eps)
+    c["x"].mul_(scale)
+    c["dy"].mul_(2.0 ** -20)
+    with gemm_lib.NormPlan(rows, cols, elem, weight="f32") as plan:
+        x = c["x"].double()
+        mean = x.mean(1)
+        c["mean"].copy_(mean)
+        c["rstd"].copy_(1 / (x - mean[:, None]).square().mean(1).sqrt())
+        plan.backward(c["x"], c["gamma"], c["mean"], c["rstd"], c["dy"], c["dx"], c["dgamma"], c["dbeta"])
+        args = (ops._f64(c["x"]), ops._f64(c["gamma"]), ops._f64(c["mean"]), ops._f64(c["rstd"]), ops._f64(c["dy"]))
+        want, bound = to.norm_backward(*args), to.norm_backward_bounds(*args, elem, "f32")
+        for k, name in enumerate(("dx", "dgamma", "dbeta")):
+            ops._within(c[name], want[k], bound[k], name)
+        plan.check()
