@@ -1220,20 +1220,31 @@ int64_t backward_blocks(int64_t rows, int lanes, int sms) {
     return blocks < sms ? blocks : sms;
 }
 
+// Blocks of a ring's backward launch, where the register kernels would have `blocks`: those, or
+// as many as give each of the rings' groups two rows (2500 x 125 fp32 13.8 us with the 40 blocks
+// of the register kernels' shorter groups).  A block on every SM is not better: a call of 2500 x
+// 256 fp32 takes 6.5 us with 79 blocks, beside which the next launch starts, and 9.8 with 152.
+int ring_blocks(int64_t rows, int lanes, int blocks, int sms) {
+    const int64_t pairs = int64_t{2} * (kBackwardRing / lanes), enough = (rows + pairs - 1) / pairs;
+    return enough <= blocks ? blocks : enough < sms ? static_cast<int>(enough) : sms;
+}
+
 template <typename T, typename W>
-bool backward_shifted(const BackwardArgs<T, W>& a, int blocks, int sms, Queue queue, gemm_status_t* status) {
+bool backward_shifted(const BackwardArgs<T, W>& a, int* blocks, int sms, Queue queue, gemm_status_t* status) {
     if constexpr (sizeof(T) == 2) {
         BackwardArgs<T, W> b = a;
         b.lanes = ring_lanes(a.cols + 7, kLaneCols);
         const int64_t stage = ring_stage_bytes(a.cols * 2, true);
         const int stages = ring_stages(a.cols, 1, stage, 2, b.lanes, kBackwardRing, 0, a.rows, sms);
-        if (stages == 0 || !can_shift<T>(a.x, a.ldx, a.dy, a.lddy, blocks) ||
-            (a.dx && !can_shift<T>(a.x, a.ldx, a.dx, a.lddx, blocks)))
+        if (stages == 0) return false;
+        const int grid = ring_blocks(a.rows, b.lanes, *blocks, sms);
+        if (!can_shift<T>(a.x, a.ldx, a.dy, a.lddy, grid) || (a.dx && !can_shift<T>(a.x, a.ldx, a.dx, a.lddx, grid)))
             return false;
+        *blocks = grid;
         const int groups = kBackwardRing / b.lanes;
         const size_t ring = static_cast<size_t>(2 * groups * stages * stage);
         const size_t join = static_cast<size_t>(groups * b.lanes) * kLaneCols * 2 * sizeof(float);
-        *status = launch<norm_backward_ring_kernel<T, W, 8, true>>(blocks, kBackwardRing, ring > join ? ring : join, queue,
+        *status = launch<norm_backward_ring_kernel<T, W, 8, true>>(grid, kBackwardRing, ring > join ? ring : join, queue,
                          1, b, stages);
         return true;
     }
@@ -1241,7 +1252,7 @@ bool backward_shifted(const BackwardArgs<T, W>& a, int blocks, int sms, Queue qu
 }
 
 template <typename T, typename W, int VEC>
-gemm_status_t backward_vec(const BackwardArgs<T, W>& a, int blocks, int sms, Queue queue) {
+gemm_status_t backward_vec(const BackwardArgs<T, W>& a, int* blocks, int sms, Queue queue) {
     BackwardArgs<T, W> b = a;
     b.lanes = ring_lanes(a.cols, kLaneCols);
     const int64_t stage = ring_stage_bytes(a.cols * static_cast<int>(sizeof(T)), VEC == 1);
@@ -1249,7 +1260,8 @@ gemm_status_t backward_vec(const BackwardArgs<T, W>& a, int blocks, int sms, Que
     if (stages > 0) {
         const size_t ring = static_cast<size_t>(2 * (kBackwardRing / b.lanes) * stages * stage);
         const size_t join = static_cast<size_t>(kBackwardRing / b.lanes * b.lanes) * kLaneCols * 2 * sizeof(float);
-        return launch<norm_backward_ring_kernel<T, W, VEC, false>>(blocks, kBackwardRing, ring > join ? ring : join, queue, 1,
+        *blocks = ring_blocks(a.rows, b.lanes, *blocks, sms);
+        return launch<norm_backward_ring_kernel<T, W, VEC, false>>(*blocks, kBackwardRing, ring > join ? ring : join, queue, 1,
                       b, stages);
     }
     if constexpr (VEC > 1) {
@@ -1258,11 +1270,11 @@ gemm_status_t backward_vec(const BackwardArgs<T, W>& a, int blocks, int sms, Que
         const size_t ring = static_cast<size_t>(2 * wide * stage + weights);
         const size_t join = static_cast<size_t>(b.lanes) * kLaneCols * 2 * sizeof(float);
         if (wide > 0)
-            return launch<norm_backward_wide_ring_kernel<T, W, VEC>>(blocks, kWideRing, ring > join ? ring : join, queue, 1,
+            return launch<norm_backward_wide_ring_kernel<T, W, VEC>>(*blocks, kWideRing, ring > join ? ring : join, queue, 1,
                                                                      b, wide);
     }
-    if (a.lanes <= 512) return backward_rows<T, W, VEC, 512, false>(a, blocks, queue);
-    return backward_rows<T, W, VEC, 1024, true>(a, blocks, queue);
+    if (a.lanes <= 512) return backward_rows<T, W, VEC, 512, false>(a, *blocks, queue);
+    return backward_rows<T, W, VEC, 1024, true>(a, *blocks, queue);
 }
 
 // Calls f with values of the plan's element and weight types.
@@ -1291,8 +1303,11 @@ gemm_status_t gemm_norm_plan_create(int64_t max_rows, int64_t cols, gemm_elem_t 
     const gemm_status_t st = gbt::begin_plan(&device, &sms);
     if (st != GEMM_OK) return st;
     size_t sums = 0;
-    if (max_rows > 0 && gbt::in_registers(cols))
-        sums = static_cast<size_t>(gbt::backward_blocks(max_rows, gbt::lanes_for(cols), sms) * cols) * 2 * sizeof(float);
+    if (max_rows > 0 && gbt::in_registers(cols)) {
+        // (rings take no fewer rows than SMs, and have no more blocks)
+        const int64_t blocks = max_rows >= sms ? sms : gbt::backward_blocks(max_rows, gbt::lanes_for(cols), sms);
+        sums = static_cast<size_t>(blocks * cols) * 2 * sizeof(float);
+    }
     void* memory = nullptr;
     gemm_status_t room = gbt::allocate(&memory, 256 + sums);
     if (room != GEMM_OK) return room;
@@ -1391,15 +1406,15 @@ gemm_status_t gemm_norm_backward(gemm_norm_plan_t p, int64_t rows, const void* x
                 s = gbt::launch<gbt::norm_dx_wide_kernel<T, W>>(rows, gbt::kThreads, 0, queue, 1, a);
             return s;
         }
-        const int blocks = static_cast<int>(gbt::backward_blocks(rows, lanes, p->num_sms));
+        int blocks = static_cast<int>(gbt::backward_blocks(rows, lanes, p->num_sms));
         if (blocks > 0) {
             const bool vec = gbt::rows_aligned(x, ldx, e) && gbt::rows_aligned(dy, lddy, e) &&
                              (!dx || gbt::rows_aligned(dx, lddx, e)) && gbt::aligned(gamma, 16);
             constexpr int kVec = 16 / static_cast<int>(sizeof(T));
             const bool whole = vec && p->cols % kVec == 0;
-            if (whole || !gbt::backward_shifted<T, W>(a, blocks, p->num_sms, queue, &s))
-                s = vec ? gbt::backward_vec<T, W, kVec>(a, blocks, p->num_sms, queue)
-                        : gbt::backward_vec<T, W, 1>(a, blocks, p->num_sms, queue);
+            if (whole || !gbt::backward_shifted<T, W>(a, &blocks, p->num_sms, queue, &s))
+                s = vec ? gbt::backward_vec<T, W, kVec>(a, &blocks, p->num_sms, queue)
+                        : gbt::backward_vec<T, W, 1>(a, &blocks, p->num_sms, queue);
         }
         if (s == GEMM_OK && a.weights)
             s = gbt::launch<gbt::norm_weight_join_kernel<W>>(2 * tiles, gbt::kThreads, 0, queue, 1,
