@@ -13,8 +13,9 @@
  *       directly; every other call, a box[0] that is None (plan closed) and a
  *       non-zero status go to general(*args, **kwargs), the binding's own path,
  *       which handles the other argument forms and raises the error.
- *   TrainCall(kind, function, plan, elem, weight, types, cols, rows, device, raw_stream)
- *       -> a callable for one call of one plan of gemm_train.h.  It takes the
+ *   TrainCall(kind, function, plan, elem, weight, types, cols, rows, device, raw_stream, only=-1)
+ *       -> a callable for one call of one plan of gemm_train.h (only: the index of
+ *       the device that tensors have to be on, -1 = not looked at).  It takes the
  *       call's arguments by position (tensors, numbers, the stream last: an int,
  *       None for the current one, or an object with cuda_stream), checks them as
  *       the binding's general path does and returns the C function's status, or
@@ -207,18 +208,28 @@ typedef struct {
     int64_t cols, rows;      /* of the matrices (rows: of an embedding table) */
     PyObject* device;
     PyObject* raw_stream;    /* callable: device -> the current stream's handle */
+    long only;               /* the device that tensors have to be on; -1: there is one, not asked */
     vectorcallfunc vectorcall;
 } TrainCall;
 
-static PyObject *s_dtype, *s_is_cuda, *s_shape, *s_stride, *s_is_contiguous;
+static PyObject *s_dtype, *s_is_cuda, *s_get_device, *s_shape, *s_stride, *s_is_contiguous;
+
+/* Whether the tensor is on the plan's device (asked where there are several). */
+static int on_device(const TrainCall* call, PyObject* t) {
+    if (call->only < 0) return 1;
+    PyObject* r = PyObject_CallMethodNoArgs(t, s_get_device);
+    const long device = r == NULL ? -1 : PyLong_AsLong(r);
+    Py_XDECREF(r);
+    return device == call->only;
+}
 
 /* Address of a CUDA tensor of `dims` dimensions with its shape and strides; 0 where
  * it is something else. */
-static int tensor_of(PyObject* t, int dims, void** ptr, int64_t* shape, int64_t* stride) {
+static int tensor_of(const TrainCall* call, PyObject* t, int dims, void** ptr, int64_t* shape, int64_t* stride) {
     PyObject* r = PyObject_GetAttr(t, s_is_cuda);
     const int cuda = r == Py_True;
     Py_XDECREF(r);
-    if (!cuda || !address_of(t, s_data_ptr, 1, ptr)) return 0;
+    if (!cuda || !address_of(t, s_data_ptr, 1, ptr) || !on_device(call, t)) return 0;
     PyObject* a = PyObject_GetAttr(t, s_shape);
     int ok = a != NULL && PyTuple_Check(a) && PyTuple_GET_SIZE(a) == dims;
     for (int i = 0; ok && i < dims; ++i) shape[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(a, i));
@@ -255,9 +266,9 @@ static int type_among(PyObject* t, PyObject* types, int from, int to) {
 }
 
 /* A rows x cols matrix with contiguous rows (*rows < 0: any number, which is set). */
-static int matrix(PyObject* t, int64_t* rows, int64_t cols, void** ptr, int64_t* ld) {
+static int matrix(const TrainCall* call, PyObject* t, int64_t* rows, int64_t cols, void** ptr, int64_t* ld) {
     int64_t shape[2], stride[2];
-    if (!tensor_of(t, 2, ptr, shape, stride)) return 0;
+    if (!tensor_of(call, t, 2, ptr, shape, stride)) return 0;
     if (*rows < 0) *rows = shape[0];
     if (shape[0] != *rows || shape[1] != cols || (cols > 1 && stride[1] != 1)) return 0;
     *ld = *rows > 1 ? stride[0] : cols;
@@ -265,13 +276,13 @@ static int matrix(PyObject* t, int64_t* rows, int64_t cols, void** ptr, int64_t*
 }
 
 /* A contiguous vector of n values of the type, or None where that is allowed. */
-static int vector(PyObject* t, PyObject* dtype, int64_t n, int none, void** ptr) {
+static int vector(const TrainCall* call, PyObject* t, PyObject* dtype, int64_t n, int none, void** ptr) {
     int64_t shape, stride;
     if (t == Py_None) {
         *ptr = NULL;
         return none;
     }
-    return (dtype == NULL || has_type(t, dtype)) && tensor_of(t, 1, ptr, &shape, &stride) &&
+    return (dtype == NULL || has_type(t, dtype)) && tensor_of(call, t, 1, ptr, &shape, &stride) &&
            shape == n && (n < 2 || stride == 1);
 }
 
@@ -300,12 +311,12 @@ static int teacher_of(const TrainCall* c, PyObject* ids, PyObject* values, PyObj
     int64_t shape[2], stride[2], n = rows;
     void *pi, *pv, *pl;
     const int id_type = type_among(ids, c->types, 3, 5), elem = type_among(values, c->types, 0, 3);
-    if (id_type < 0 || elem < 0 || !tensor_of(ids, 2, &pi, shape, stride)) return 0;
+    if (id_type < 0 || elem < 0 || !tensor_of(c, ids, 2, &pi, shape, stride)) return 0;
     const int64_t top = shape[1];
     if (shape[0] != rows || (top > 1 && stride[1] != 1)) return 0;
     t->ld_ids = rows > 1 ? stride[0] : top;
-    if (!matrix(values, &n, top, &pv, &t->ld_values) ||
-        !vector(lse, PyTuple_GET_ITEM(c->types, 2), rows, 1, &pl))
+    if (!matrix(c, values, &n, top, &pv, &t->ld_values) ||
+        !vector(c, lse, PyTuple_GET_ITEM(c->types, 2), rows, 1, &pl))
         return 0;
     t->ids = pi;
     t->values = pv;
@@ -324,10 +335,10 @@ static int train_call(const TrainCall* c, PyObject* const* v, Py_ssize_t n) {
     double x;
     switch (c->kind) {
         case NORM_FORWARD:
-            if (n != 8 || !has_type(v[0], c->elem) || !matrix(v[0], &rows, c->cols, &p[0], &ld[0]) ||
-                !vector(v[1], c->weight, c->cols, 1, &p[1]) || !vector(v[2], c->weight, c->cols, 1, &p[2]) ||
-                !has_type(v[3], c->elem) || !matrix(v[3], &rows, c->cols, &p[3], &ld[1]) ||
-                !vector(v[4], f32, rows, 1, &p[4]) || !vector(v[5], f32, rows, 1, &p[5]) ||
+            if (n != 8 || !has_type(v[0], c->elem) || !matrix(c, v[0], &rows, c->cols, &p[0], &ld[0]) ||
+                !vector(c, v[1], c->weight, c->cols, 1, &p[1]) || !vector(c, v[2], c->weight, c->cols, 1, &p[2]) ||
+                !has_type(v[3], c->elem) || !matrix(c, v[3], &rows, c->cols, &p[3], &ld[1]) ||
+                !vector(c, v[4], f32, rows, 1, &p[4]) || !vector(c, v[5], f32, rows, 1, &p[5]) ||
                 !number(v[6], &x) || !stream_of(c, v[7], &stream))
                 return -1;
             return ((int (*)(void*, int64_t, const void*, int64_t, const void*, const void*, float, void*,
@@ -336,12 +347,12 @@ static int train_call(const TrainCall* c, PyObject* const* v, Py_ssize_t n) {
         case NORM_BACKWARD:
             p[5] = NULL;
             ld[2] = 0;
-            if (n != 9 || !has_type(v[0], c->elem) || !matrix(v[0], &rows, c->cols, &p[0], &ld[0]) ||
-                !vector(v[1], c->weight, c->cols, 1, &p[1]) || !vector(v[2], f32, rows, 0, &p[2]) ||
-                !vector(v[3], f32, rows, 0, &p[3]) || !has_type(v[4], c->elem) ||
-                !matrix(v[4], &rows, c->cols, &p[4], &ld[1]) ||
-                (v[5] != Py_None && (!has_type(v[5], c->elem) || !matrix(v[5], &rows, c->cols, &p[5], &ld[2]))) ||
-                !vector(v[6], c->weight, c->cols, 1, &p[6]) || !vector(v[7], c->weight, c->cols, 1, &p[7]) ||
+            if (n != 9 || !has_type(v[0], c->elem) || !matrix(c, v[0], &rows, c->cols, &p[0], &ld[0]) ||
+                !vector(c, v[1], c->weight, c->cols, 1, &p[1]) || !vector(c, v[2], f32, rows, 0, &p[2]) ||
+                !vector(c, v[3], f32, rows, 0, &p[3]) || !has_type(v[4], c->elem) ||
+                !matrix(c, v[4], &rows, c->cols, &p[4], &ld[1]) ||
+                (v[5] != Py_None && (!has_type(v[5], c->elem) || !matrix(c, v[5], &rows, c->cols, &p[5], &ld[2]))) ||
+                !vector(c, v[6], c->weight, c->cols, 1, &p[6]) || !vector(c, v[7], c->weight, c->cols, 1, &p[7]) ||
                 !stream_of(c, v[8], &stream))
                 return -1;
             return ((int (*)(void*, int64_t, const void*, int64_t, const void*, const void*, const void*,
@@ -352,12 +363,12 @@ static int train_call(const TrainCall* c, PyObject* const* v, Py_ssize_t n) {
             const int back = c->kind == EMBED_BACKWARD;
             int64_t shape, stride, vocab = c->rows;
             const int id_type = n == 6 + back ? type_among(v[0], c->types, 3, 5) : -1;
-            if (id_type < 0 || !tensor_of(v[0], 1, &p[0], &shape, &stride) || (shape > 1 && stride != 1)) return -1;
+            if (id_type < 0 || !tensor_of(c, v[0], 1, &p[0], &shape, &stride) || (shape > 1 && stride != 1)) return -1;
             rows = shape;
             PyObject* const by_token = v[back ? 1 : 2];
             PyObject* const table = v[back ? 2 : 1];
-            if (!has_type(by_token, c->elem) || !matrix(by_token, &rows, c->cols, &p[1], &ld[0]) ||
-                !has_type(table, back ? c->weight : c->elem) || !matrix(table, &vocab, c->cols, &p[2], &ld[1]) ||
+            if (!has_type(by_token, c->elem) || !matrix(c, by_token, &rows, c->cols, &p[1], &ld[0]) ||
+                !has_type(table, back ? c->weight : c->elem) || !matrix(c, table, &vocab, c->cols, &p[2], &ld[1]) ||
                 !number(v[3], &x))
                 return -1;
             const int64_t padding = PyLong_AsLongLong(v[4]);
@@ -378,14 +389,14 @@ static int train_call(const TrainCall* c, PyObject* const* v, Py_ssize_t n) {
             Teacher t;
             int k = 3;
             if (n != 7 + forward + 2 * backward || !has_type(v[0], c->elem) ||
-                !matrix(v[0], &rows, c->cols, &p[0], &ld[0]))
+                !matrix(c, v[0], &rows, c->cols, &p[0], &ld[0]))
                 return -1;
             p[1] = p[3] = p[4] = NULL;
-            if (forward && !vector(v[k++], f32, rows, 0, &p[1])) return -1;
-            if (!vector(v[k++], f32, rows, 0, &p[2])) return -1;
+            if (forward && !vector(c, v[k++], f32, rows, 0, &p[1])) return -1;
+            if (!vector(c, v[k++], f32, rows, 0, &p[2])) return -1;
             if (backward) {
-                if (!has_type(v[k], c->elem) || !matrix(v[k], &rows, c->cols, &p[3], &ld[1])) return -1;
-                if (!vector(v[k + 1], f32, rows, 1, &p[4])) return -1;
+                if (!has_type(v[k], c->elem) || !matrix(c, v[k], &rows, c->cols, &p[3], &ld[1])) return -1;
+                if (!vector(c, v[k + 1], f32, rows, 1, &p[4])) return -1;
                 k += 2;
             }
             if (!number(v[k], &x) || !teacher_of(c, v[1], v[2], v[k + 1], rows, &t) || !stream_of(c, v[k + 2], &stream))
@@ -417,13 +428,14 @@ static PyObject* train_call_vector(PyObject* self, PyObject* const* args, size_t
 static PyObject* train_call_new(PyTypeObject* type, PyObject* args, PyObject* kwds) {
     int kind;
     long long cols, rows;
+    long only = -1;
     PyObject *fn, *plan, *elem, *weight, *types, *device, *raw_stream;
     if (kwds != NULL && PyDict_GET_SIZE(kwds) != 0) {
         PyErr_SetString(PyExc_TypeError, "TrainCall takes its arguments by position");
         return NULL;
     }
-    if (!PyArg_ParseTuple(args, "iOOOOO!LLOO:TrainCall", &kind, &fn, &plan, &elem, &weight, &PyTuple_Type,
-                          &types, &cols, &rows, &device, &raw_stream))
+    if (!PyArg_ParseTuple(args, "iOOOOO!LLOO|l:TrainCall", &kind, &fn, &plan, &elem, &weight, &PyTuple_Type,
+                          &types, &cols, &rows, &device, &raw_stream, &only))
         return NULL;
     void* f = PyLong_AsVoidPtr(fn);
     void* h = PyErr_Occurred() ? NULL : PyLong_AsVoidPtr(plan);
@@ -445,6 +457,7 @@ static PyObject* train_call_new(PyTypeObject* type, PyObject* args, PyObject* kw
     self->rows = rows;
     self->device = Py_NewRef(device);
     self->raw_stream = Py_NewRef(raw_stream);
+    self->only = only;
     self->vectorcall = train_call_vector;
     return (PyObject*)self;
 }
@@ -509,11 +522,12 @@ PyMODINIT_FUNC PyInit__gemm_pycall(void) {
     s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
     s_dtype = PyUnicode_InternFromString("dtype");
     s_is_cuda = PyUnicode_InternFromString("is_cuda");
+    s_get_device = PyUnicode_InternFromString("get_device");
     s_shape = PyUnicode_InternFromString("shape");
     s_stride = PyUnicode_InternFromString("stride");
     s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
-    if (s_data_ptr == NULL || s_cuda_stream == NULL || s_dtype == NULL || s_is_cuda == NULL || s_shape == NULL ||
-        s_stride == NULL || s_is_contiguous == NULL || PyType_Ready(&RunnerType) < 0 || PyType_Ready(&TrainCallType) < 0)
+    if (s_data_ptr == NULL || s_cuda_stream == NULL || s_dtype == NULL || s_is_cuda == NULL ||
+        s_get_device == NULL || s_shape == NULL ||        s_stride == NULL || s_is_contiguous == NULL || PyType_Ready(&RunnerType) < 0 || PyType_Ready(&TrainCallType) < 0)
         return NULL;
     PyObject* m = PyModule_Create(&module);
     if (m == NULL) return NULL;

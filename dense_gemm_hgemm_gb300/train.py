@@ -107,11 +107,17 @@ def _index_of(t, what):
     return i
 
 
+def _on_device(t) -> bool:
+    """Whether a tensor is on the current device (the library refuses a plan of another one)."""
+    import torch
+    return t.is_cuda and t.get_device() == torch.cuda.current_device()
+
+
 def _matrix(t, rows, cols, elem, what):
     """(address, row stride) of a rows x cols device matrix with contiguous rows
     (`elem` None: any type)."""
-    if not t.is_cuda or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise GemmError(_INVALID_ARG, "%s: a %d x %d matrix on the device is needed"
+    if not _on_device(t) or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise GemmError(_INVALID_ARG, "%s: a %d x %d matrix on the current device is needed"
                         % (what, rows, cols))
     if elem is not None and _torch_elems.get(t.dtype) != elem:
         raise GemmError(_UNSUPPORTED, "%s: %s" % (what, t.dtype))
@@ -128,8 +134,8 @@ def _vector(t, n, elem, what, may_be_none=False):
         if may_be_none:
             return None
         raise GemmError(_INVALID_ARG, "%s: a tensor is needed" % what)
-    if not t.is_cuda or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        raise GemmError(_INVALID_ARG, "%s: a contiguous vector of %d values on the device is needed"
+    if not _on_device(t) or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise GemmError(_INVALID_ARG, "%s: a contiguous vector of %d values on the current device is needed"
                         % (what, n))
     if elem is not None and _torch_elems.get(t.dtype) != elem:
         raise GemmError(_UNSUPPORTED, "%s: %s" % (what, t.dtype))
@@ -164,7 +170,8 @@ class _Plan:
             raw = lambda device: torch.cuda.current_stream(device).cuda_stream  # noqa: E731
         kinds = (torch.float16, torch.bfloat16, torch.float32)
         return call(kind, ctypes.cast(getattr(library(), name), ctypes.c_void_p).value, self.handle, kinds[elem],
-                    kinds[weight], (*kinds, torch.int32, torch.int64), cols, rows, torch.cuda.current_device(), raw)
+                    kinds[weight], (*kinds, torch.int32, torch.int64), cols, rows, torch.cuda.current_device(), raw,
+                    torch.cuda.current_device() if torch.cuda.device_count() > 1 else -1)
 
     @staticmethod
     def _taken(entry, name, args) -> bool:
