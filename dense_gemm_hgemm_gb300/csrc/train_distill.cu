@@ -1,5 +1,6 @@
 // train_distill.cu -- the distillation loss of gemm_train.h against a teacher's top
 // logits, forward and backward.
+#include <float.h>
 #include <math.h>
 
 #include <new>
@@ -1267,7 +1268,8 @@ gemm_status_t check_call(const gemm_distill_plan* p, int64_t rows, const void* l
                          const gemm_teacher_t* t, float temperature) {
     if (!p || rows < 0 || rows > p->max_rows || !t) return GEMM_ERR_INVALID_ARG;
     if (!valid_index(t->id_type) || !valid_elem(t->value_elem)) return GEMM_ERR_UNSUPPORTED;
-    if (!(temperature > 0.f) || t->top < 0 || t->top > p->max_top) return GEMM_ERR_INVALID_ARG;
+    // (a normal number: of others the scale, or the product with a masked logit, is none)
+    if (!(temperature >= FLT_MIN && temperature <= FLT_MAX) || t->top < 0 || t->top > p->max_top) return GEMM_ERR_INVALID_ARG;
     if (rows > 0 && (!logits || ldl < p->vocab)) return GEMM_ERR_INVALID_ARG;
     if (rows > 0 && t->top > 0 &&
         (!t->ids || !t->values || t->ld_ids < t->top || t->ld_values < t->top))

@@ -208,7 +208,7 @@ gemm_status_t gemm_distill_plan_create(int64_t max_rows, int64_t vocab, int64_t 
  * only) or where no logit is above -infinity: loss 0, lse -infinity, gradient 0.
  * Logits of -infinity (masked tokens) have q = 0, and a logit below -1e30 * tau
  * counts as one (masks of a type's lowest value); NaN logits give NaN.
- * temperature > 0.  An id >= vocab is reported by gemm_distill_plan_check and
+ * temperature: a normal positive number.  An id >= vocab is reported by gemm_distill_plan_check and
  * taken as no entry.
  */
 gemm_status_t gemm_distill_forward(gemm_distill_plan_t plan, int64_t rows, const void *logits,

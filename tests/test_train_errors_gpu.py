@@ -36,3 +36,17 @@ def test_errors_of_a_plan_made_while_the_default_stream_is_busy(gemm_lib, kind):
                 late.check(side)
             assert e.value.status == 12
             late.check(side)                         # reported once
+
+
+@pytest.mark.parametrize("temperature", [float("inf"), float("nan"), 0.0, -1.0, 1e-40])
+@pytest.mark.parametrize("call", ["forward", "backward", "forward_backward"])
+def test_temperatures_that_are_no_normal_numbers_are_refused(gemm_lib, temperature, call):
+    x, w = torch.zeros(4, 64, device="cuda"), torch.zeros(4, device="cuda")
+    ids, values = torch.zeros(4, 3, dtype=torch.int64, device="cuda"), torch.zeros(4, 3, device="cuda")
+    args = {"forward": (x, ids, values, w, w), "backward": (x, ids, values, w, x), "forward_backward": (x, ids, values, w, w, x)}
+    with gemm_lib.DistillPlan(4, 64, 3, "f32") as plan:
+        with pytest.raises(gemm_lib.GemmError) as e:
+            getattr(plan, call)(*args[call], temperature=temperature)
+        assert e.value.status == 1
+    torch.cuda.synchronize()
+    assert not bool(x.any()) and not bool(w.any())
