@@ -69,7 +69,7 @@ class Student:
 
     def check(self):
         """Raises what the kernels have to report."""
-        for plan in (self.embed, self.distill, self.product, self.to_input, self.to_weight):
+        for plan in (self.embed, self.norm, self.distill, self.product, self.to_input, self.to_weight):
             plan.check()
 
     def close(self):
