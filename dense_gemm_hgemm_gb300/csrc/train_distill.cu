@@ -435,14 +435,14 @@ __device__ __forceinline__ Pack<T, VEC> gradient_over(const Pack<T, VEC>& q, flo
 // ---- the kernel ------------------------------------------------------------------------
 //
 // A block holds one piece of a row's logits in shared memory.  Forward: the blocks of a
-// row form a cluster; each finds its piece's k and sum in one pass, and they exchange
-// those and their parts of the loss.  Backward: the gradient of the piece, from the
+// row form a cluster; each finds its piece's maximum and sum in one pass, and they
+// exchange those and their parts of the loss.  Backward: the gradient of the piece, from the
 // piece.  Both: the piece is read from memory once.
 //
 // Serves calls of few rows, whose pieces fill the GPU (33 x 32000 fp32, forward: 4.5 us, the
-// chain of load, sum and exchange), and every backward call: there blocks are independent and
-// six or more an SM hide one another's waits (2048 x 50021 fp16: 61 us, 0.97 of the copy
-// bandwidth).
+// chain of load, sum and exchange), and every backward call but those of short rows: there
+// blocks are independent and six or more an SM hide one another's waits (2048 x 50021 fp16: 62
+// us, 0.96 of the copy bandwidth; 67 with six blocks an SM for 16-bit logits instead of eight).
 template <typename T, int MODE>
 __global__ void __launch_bounds__(kThreads, MODE != kBackward ? 4 : sizeof(T) == 2 ? 8 : 6) distill_kernel(const Args<T> a) {
     constexpr int VEC = 16 / static_cast<int>(sizeof(T));
@@ -630,12 +630,15 @@ __global__ void __launch_bounds__(kThreads, MODE != kBackward ? 4 : sizeof(T) ==
 // gradient is written, and copy the next row into those that are free.  So memory is busy
 // while a row is reduced, and no block starts or ends per row.
 //
-// Bound by bytes.  Forward, 4096 x 128000 bf16, top 64: 152 us, 0.97 of the copy bandwidth
+// Bound by bytes.  Forward, 4096 x 128000 bf16, top 64: 154 us, 0.96 of the copy bandwidth
 // (with unpaired arithmetic 209, and 384 then by a block per piece of a row).  Both directions,
-// 4096 x 64000 bf16: 166 us, 0.92; parts of at most 64 KB and two blocks an SM, so that one
+// 4096 x 64000 bf16: 167 us, 0.91; parts of at most 64 KB and two blocks an SM, so that one
 // block's stores go beside the other's sums (three blocks of 32-KB parts 171).  Three warps for
 // the entries, 16-KB stages and logits at the ids taken from the ring were 169 where one warp,
-// 8-KB stages and loads of those logits were 201.
+// 8-KB stages and loads of those logits were 201.  With 200 entries a row, 387 us: the search
+// for equal ids, 200 x 200 a row by one warp, is what takes them.  Forward pays from few rows
+// on: 455 rows of 128000, the last count before this kernel, take 42 us by the one above,
+// 456 take 22; both directions 151 and 152 rows of 64000, 15 us each.
 //
 // When a wait runs out (the block's patience is over, and no later wait lasts), nothing more is
 // copied, prepared or exchanged, and the computing warps go on through their rows with whatever
@@ -991,8 +994,9 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
 // blocks' and barriers' time of the other kernels is several times that of the memory (16384
 // x 1000 bf16, both directions: 27 us).  Bound by the entries' chain of loads and sums, which is
 // most of the work of such a row (16384 x 250: 18 us).
-// Blocks an SM that are worth holding the registers down for (without a spill): 16384 x 1000 bf16
-// both directions 24.5 us, 29 with a block less.
+// Blocks an SM that are worth holding the registers down for (none spills but the
+// 16-bit forward kernels of 8 packs, 32 bytes): 16384 x 1000 bf16 both directions 24.5 us, 29 with
+// a block less.
 template <typename T, int MODE, int PACKS>
 constexpr int kShortBlocks = sizeof(T) == 4 ? (PACKS == 2 ? 5 : PACKS == 4 ? 4 : PACKS == 8 ? 3 : 2)
                              : MODE == kForward ? (PACKS <= 4 ? 5 : PACKS == 8 ? 4 : 2)

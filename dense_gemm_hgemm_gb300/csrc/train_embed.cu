@@ -205,10 +205,12 @@ __device__ __forceinline__ uint32_t key_of(const SortParams& p, int64_t t, bool 
     return p.vocab;
 }
 
-// One cluster, as its blocks must meet between passes: up to 8192 tokens have their pairs in
+// One cluster, as its blocks must meet between passes: up to 16384 tokens have their pairs in
 // its shared memory throughout (with the passes through global memory, and partial sums for
 // every row that crosses a chunk, the 4099 tokens above took 28 us).  Digits of up to 9 bits,
-// one thread each: two passes serve 2^18 rows.
+// one thread each: two passes serve up to 2^18 - 1 rows (the number of rows is a key itself).
+// More tokens go through global memory, each ranked twice a pass: 32768 into 64000 x 1024 bf16
+// written whole take 82 us against 29 for the bytes, 131072 take 234 against 59.
 //
 // One stable pass of a radix sort over the cluster: each block ranks a contiguous span of
 // the input, tile by tile; a warp ranks 32 keys at a time by matching their digits, so no

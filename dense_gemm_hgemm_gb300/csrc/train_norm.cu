@@ -307,11 +307,11 @@ __global__ void __launch_bounds__(BLOCK) norm_forward_kernel(const ForwardArgs<T
 // behind it; there is no copying warp and no second barrier.  The bytes in flight do not
 // depend on how many registers are left for loads: the register kernels keep 24 KB an SM
 // in flight at 16384 x 4096, the rings over 100 KB.  Forward is bound by bytes: 16384 x 4096
-// bf16 44 us, 0.90 of the copy bandwidth (in registers 64); 65536 x 1000 43 us, 0.91;
-// 4096 x 16384 45 us, 0.88.  Backward does four sums' work an element (two of the row, two of
-// the columns) with 512 threads of 126 registers, and is bound by issuing that and by the
+// bf16 44.5 us, 0.90 of the copy bandwidth (in registers 64), fp32 87 us, 0.92; 65536 x 1000
+// 44 us, 0.89; 4096 x 16384 45 us, 0.88.  Backward does four sums' work an element (two of the row, two of
+// the columns) with 512 threads of 125 registers, and is bound by issuing that and by the
 // one barrier a row that nothing overlaps: 8192 x 8192 77 us, 0.78 (80 where each of the two
-// sums took its own shuffles; 82 in registers).
+// sums took its own shuffles; 82 in registers); fp32 138 us, 0.87.
 
 constexpr int kRingRows = 1 << 30;         // rows are counted in 32 bits there, some steps beyond the last
 constexpr int kRingSlots = 64;             // stages of a block, at most
@@ -412,8 +412,8 @@ __device__ __forceinline__ void init_ring(RingBarriers& ring, int slots, const W
 
 // Rows off the 16-byte boundaries, in packs all the same: a pack is a 16-byte unit of the
 // memory, from the one that the row begins in, so the row's elements stand at the positions
-// off .. end - 1 from there.  A block's rows are multiples of gridDim.x rows apart, which is a
-// multiple of 16 bytes (152 SMs are), so they share `off` and a lane keeps its columns; and
+// off .. end - 1 from there.  A block's rows are multiples of gridDim.x rows apart, which has to
+// be a multiple of 16 bytes (152 rows are), so they share `off` and a lane keeps its columns; and
 // what is read and what is written have the same `off` (else single elements move).  Warps
 // with the row's ends take more steps for them.  10000 x 5003 bf16: forward 51 us, backward
 // 110; with single elements 71 and 160; rows of 5008 take 40 and 75.
@@ -857,8 +857,8 @@ __device__ __forceinline__ void each_pair(const T* x, const T* dy, const Staged<
 // The same for rows of more lanes than such a block has (VEC > 1): a block of 1024 threads
 // has no registers for a row beside the weight gradients' sums, so the row is read twice from
 // its stage, for the sums and for dx, and the stage is refilled when the block has met at the
-// next row's barrier.  4096 x 16384 bf16: 193 us with the sums in shared memory, 119 us so; at
-// 8192 columns, where both fit, 110 us against 77.
+// next row's barrier.  4096 x 16384 bf16: 193 us with the sums in shared memory, 115 us so (its
+// 64 registers a thread spill 28 to 100 bytes); at 8192 columns, where both fit, 110 us against 77.
 constexpr int kWideRing = 1024;
 
 template <typename T, typename W, int VEC>
@@ -982,7 +982,8 @@ norm_weight_join_kernel(const float* partial, int blocks, int cols, W* dgamma, W
 // ---- rows too wide for the registers of a block ------------------------------------
 //
 // More than 16384 columns.  Each pass reads the row anew (from L2, for rows of some hundred
-// KB); plain and right, for widths that hardly any model has.
+// KB); plain and right, for widths that hardly any model has (4096 x 20000 bf16: forward 179
+// us, 0.27 of the copy bandwidth, backward 430, 0.17).
 
 // The sum over the block, in every thread.
 __device__ float block_sum(float v) {

@@ -11,7 +11,9 @@
  * They take and leave matrices as the products of gemm.h do: row-major, rows of
  * `cols` contiguous elements whose starts are `ld` elements apart (ld >= cols),
  * so the logits of a product whose N was padded to a multiple of 8 are used in
- * place.  Elements between cols and ld are neither read nor written.
+ * place.  Elements between cols and ld are never written, and take no part in a
+ * result; the norm may read those within 16 bytes of a row that is not the matrix'
+ * first or last.
  *
  * Types: fp16, bf16 or fp32 elements (gemm_elem_t).  All sums, softmax and norm
  * statistics are fp32; a result is rounded once (to nearest even) to its type.
