@@ -60,7 +60,7 @@ struct Args {
     float2* sums;          // each row's maximum and sum, where both directions are two kernels
     Teacher teacher;
     int64_t ldl, ldd;
-    float temperature;
+    float temperature, inverse, c;      // ... one over it, log2(e) over it
     int vocab, piece;      // elements; a piece is a multiple of the pack
     int pieces;            // of a row: blocks that share it
     Waits waits;
@@ -369,8 +369,8 @@ struct Softmax {
         return exp2_fast(far ? at_most_zero(fmaf(s - base, c, rest)) : fmaf(s, c, -k));
     }
     // the log-sum-exp, from the forward pass' sum
-    __device__ __forceinline__ float lse(float sum, float temperature) const {
-        return fmaf(base, 1.f / temperature, kLn2 * log2f(sum));
+    __device__ __forceinline__ float lse(float sum, float inverse_temperature) const {
+        return fmaf(base, inverse_temperature, kLn2 * log2f(sum));
     }
 };
 
@@ -439,7 +439,7 @@ __device__ __forceinline__ Pack<T, VEC> gradient_over(const Pack<T, VEC>& q, flo
 // exchange those and their parts of the loss.  Backward: the gradient of the piece, from the
 // piece.  Both: the piece is read from memory once.
 //
-// Serves calls of few rows, whose pieces fill the GPU (33 x 32000 fp32, forward: 4.5 us, the
+// Serves calls of few rows, whose pieces fill the GPU (33 x 32000 fp32, forward: 4.4 us, the
 // chain of load, sum and exchange), and every backward call but those of short rows: there
 // blocks are independent and six or more an SM hide one another's waits (2048 x 50021 fp16: 62
 // us, 0.96 of the copy bandwidth; 67 with six blocks an SM for 16-bit logits instead of eight).
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, MODE != kBackward ? 4 : sizeof(T) ==
     wait_for_previous_kernel();
     let_next_kernel_start();
 
-    const float c = kLog2e / a.temperature;
+    const float c = a.c;
     if (warp == 0) {
         const float mass = load_entries<T>(en, a.teacher, row, nullptr, c, a.vocab, a.error);
         if (lane == 0) row_mass = mass;
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, MODE != kBackward ? 4 : sizeof(T) ==
         if (rank == 0 && tid == 0) {
             const float total = all.terms + mass * log2f(all.sum);
             a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * total;
-            a.lse[row] = empty ? -INFINITY : row_q.lse(all.sum, a.temperature);
+            a.lse[row] = empty ? -INFINITY : row_q.lse(all.sum, a.inverse);
         }
     }
     if (!kGrad) {
@@ -710,6 +710,8 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
     };
     const int begin = rank * a.piece;
     const int n = min(a.piece, a.vocab - begin);
+    // (divided here and below, not on the host as for the other kernels: 900 x 128000 fp32 both
+    // directions took 165 us with that, 149 so, in whatever way it changes the order of things)
     const float c = kLog2e / a.temperature;
     if (tid == 0) {
         for (int k = 0; k < stages; ++k) {
@@ -892,7 +894,7 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
             if (rank == 0 && thread == 0) {
                 const float total = all.terms + mass * log2f(all.sum);
                 a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * total;
-                a.lse[row] = empty ? -INFINITY : row_q.lse(all.sum, a.temperature);
+                a.lse[row] = empty ? -INFINITY : row_q.lse(all.sum, 1.f / a.temperature);
             }
             if (kGrad) {
                 T* const d = a.dlogits + row * a.ldd + begin;
@@ -992,10 +994,11 @@ distill_stream_kernel(const Args<T> a, int64_t rows, int stages, int slots) {
 // A warp keeps a whole row in registers, PACKS packs a lane, and asks for it before it
 // prepares the teacher's entries.  No block-wide step: for rows of some hundred logits the
 // blocks' and barriers' time of the other kernels is several times that of the memory (16384
-// x 1000 bf16, both directions: 27 us).  Bound by the entries' chain of loads and sums, which is
-// most of the work of such a row (16384 x 250: 18 us).
+// x 1000 bf16, both directions, 16 entries a row: 24 us, 64 entries 36).  Bound by the entries' chain of loads and sums, which is
+// most of the work of such a row (16384 x 250, 16 entries:
+// 18 us).
 // Blocks an SM that are worth holding the registers down for (none spills but the
-// 16-bit forward kernels of 8 packs, 32 bytes): 16384 x 1000 bf16 both directions 24.5 us, 29 with
+// 16-bit forward kernels of 8 packs, 32 bytes): 16384 x 1000 bf16 both directions 24 us, 29 with
 // a block less.
 template <typename T, int MODE, int PACKS>
 constexpr int kShortBlocks = sizeof(T) == 4 ? (PACKS == 2 ? 5 : PACKS == 4 ? 4 : PACKS == 8 ? 3 : 2)
@@ -1032,7 +1035,7 @@ __global__ void __launch_bounds__(kThreads, kShortBlocks<T, MODE, PACKS>) distil
     }
     const float given = MODE == kBackward ? a.lse[row] : 0.f;
     const float scale = kGrad ? a.temperature * (a.dloss ? a.dloss[row] : 1.f) : 0.f;
-    const float c = kLog2e / a.temperature;
+    const float c = a.c;
     const float mass = load_entries(en, a.teacher, row, src, c, n, a.error);
     if (kGrad) join_equal_ids(en, top);
     bool empty = mass == 0.f || (MODE == kBackward && given == -INFINITY);
@@ -1049,7 +1052,7 @@ __global__ void __launch_bounds__(kThreads, kShortBlocks<T, MODE, PACKS>) distil
         all.terms = warp_sum(all.terms);
         if (lane == 0) {
             a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * (all.terms + mass * log2f(all.sum));
-            a.lse[row] = empty ? -INFINITY : row_q.lse(all.sum, a.temperature);
+            a.lse[row] = empty ? -INFINITY : row_q.lse(all.sum, a.inverse);
         }
     }
     if (!kGrad) return;
@@ -1105,7 +1108,7 @@ __global__ void __launch_bounds__(kThreads) distill_forward_wide_kernel(const Ar
     let_next_kernel_start();
     const int64_t row = blockIdx.x;
     const T* s = a.logits + row * a.ldl;
-    const float c = kLog2e / a.temperature;
+    const float c = a.c;
     if (warp == 0) {
         const float mass = load_entries<T>(en, a.teacher, row, nullptr, c, a.vocab, a.error);
         if (lane == 0) row_mass = mass;
@@ -1134,7 +1137,7 @@ __global__ void __launch_bounds__(kThreads) distill_forward_wide_kernel(const Ar
     all.terms = warp_sum(all.terms);
     if (lane == 0) {
         a.loss[row] = empty ? 0.f : a.temperature * a.temperature * kLn2 * (all.terms + mass * log2f(all.sum));
-        a.lse[row] = empty ? -INFINITY : row_q.lse(all.sum, a.temperature);
+        a.lse[row] = empty ? -INFINITY : row_q.lse(all.sum, a.inverse);
     }
 }
 
@@ -1299,6 +1302,8 @@ Args<T> arguments(const gemm_distill_plan* p, const void* logits, int64_t ldl, c
                         static_cast<int>(t->id_type),
                         static_cast<int>(t->value_elem)};
     a.temperature = temperature;
+    a.inverse = 1.f / temperature;
+    a.c = kLog2e / temperature;
     a.vocab = static_cast<int>(p->vocab);
     a.error = p->error_word;
     a.waits = p->waits;
