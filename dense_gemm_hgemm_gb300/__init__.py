@@ -28,6 +28,7 @@ __all__ = [
     "gemm_abi_version", "gemm_launch_empty", "gemm_run_splitk_noalloc", "gemm_noalloc_check",
     "gemm_noalloc_set_wait_test", "gemm_probe_mma_rate", "library", "DTYPES",
     "ELEMS", "NormPlan", "EmbedPlan", "DistillPlan",
+    "RmsNormPlan", "fp8_quantize",
 ]
 
 GEMM_F16, GEMM_BF16, GEMM_I8_I32 = 0, 1, 2
@@ -113,6 +114,7 @@ def library() -> ctypes.CDLL:
                 "tma_intensity_run": ([i32, i32, ctypes.c_float, ctypes.c_float, vp, vp, i64, i32,
                                        vp, vp], i32),
                 **train.signatures(),
+                **ffn.signatures(),
             }
             for name, (args, res) in sig.items():
                 fn = getattr(lib, name)
@@ -396,5 +398,6 @@ class Plan:
             pass
 
 
-from . import train   # noqa: E402  (needs the names above)
+from . import ffn, train   # noqa: E402  (they need the names above)
+from .ffn import RmsNormPlan, fp8_quantize   # noqa: E402
 from .train import ELEMS, DistillPlan, EmbedPlan, NormPlan   # noqa: E402

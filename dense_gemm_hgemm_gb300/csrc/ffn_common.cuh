@@ -1,0 +1,81 @@
+// ffn_common.cuh -- what the kernels of gemm_ffn.h share: groups of eight columns of any
+// type and alignment, and e4m3 numbers with their scales.
+#pragma once
+#include "gemm_ffn.h"
+#include "train_common.cuh"
+
+namespace gbt {
+
+constexpr int kGroup = 128;                    // elements that share a scale
+constexpr float kE4m3Top = 448.f;              // the largest e4m3 number
+constexpr float kLeastScale = 1.17549435e-38f; // 2^-126: one over it is a normal number
+
+inline int64_t groups_of(int64_t cols) { return (cols + kGroup - 1) / kGroup; }
+
+// The first n of eight elements at p as fp32 (the rest zeros).  whole: p is aligned to 16 bytes.
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int n, bool whole, float (&v)[8]) {
+    if (whole && n >= 8) {
+        load_values<T, 8>(p, 8, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, int n, bool whole, const float (&v)[8]) {
+    if (whole && n >= 8) {
+        store_values<T, 8>(p, 8, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = from_f32<T>(v[i]);
+    }
+}
+
+// Two numbers as e4m3 (to nearest even, at most 448 in size): lo in the lower byte.
+__device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint2 e4m3_eight(const float (&v)[8], float inverse) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = e4m3_pair(v[2 * i] * inverse, v[2 * i + 1] * inverse);
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+
+// The first n of eight bytes.  whole: p is aligned to 8 bytes.
+__device__ __forceinline__ void store_bytes(uint8_t* p, int n, bool whole, uint2 v) {
+    if (whole && n >= 8) {
+        *reinterpret_cast<uint2*>(p) = v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = static_cast<uint8_t>((i < 4 ? v.x : v.y) >> (i % 4 * 8));
+    }
+}
+
+// The largest size among eight numbers (NaN aside, which fmaxf passes over).
+__device__ __forceinline__ float largest(const float (&v)[8]) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+    return m;
+}
+// ... among 16 lanes, which hold 128 columns, in each of them.
+__device__ __forceinline__ float largest_of_group(float m) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return m;
+}
+
+__device__ __forceinline__ float scale_of(float largest) { return fmaxf(largest * (1.f / kE4m3Top), kLeastScale); }
+
+// Whether rows of eight-element packs can move whole.
+inline bool packs_aligned(const void* p, int64_t ld, int bytes) { return !p || rows_aligned(p, ld, bytes); }
+inline bool bytes_aligned(const void* p, int64_t ld) { return aligned(p, 8) && ld % 8 == 0; }
+
+}  // namespace gbt

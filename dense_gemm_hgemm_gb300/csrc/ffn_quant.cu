@@ -1,0 +1,143 @@
+// ffn_quant.cu -- conversion of a matrix to e4m3 with scales (gemm_ffn.h).
+#include "ffn_common.cuh"
+
+namespace gbt {
+namespace {
+
+constexpr int kQuantThreads = 256;
+constexpr int kSide = 128;                   // a block's tile: 128 x 128 elements
+constexpr int kPacks = 8;                    // packs of eight columns that a thread holds
+
+struct QuantArgs {
+    const void* x;
+    uint8_t* q;
+    float* scales;
+    int64_t ldx, ldq, lds;
+    int rows, cols, tiles_across;
+    bool whole_x, whole_q;
+};
+
+// A block converts one tile of 128 x 128 elements, which its threads keep in registers between
+// the largest value and the conversion: x is read once and q written once, 32 KB of bf16 in
+// flight a block.  Thread t holds columns 8 (t % 16) .. + 7 of eight rows: a row's 128 columns
+// are 16 lanes of a warp.  The rows are t / 16 + 16 k, or, transposed, 8 (t / 16) + k: then eight
+// values of a column are eight bytes of a result's row, which goes through shared memory with
+// its 8-byte units exchanged so that no two lanes of a store or a load meet in a bank.
+template <typename T, bool SQUARE, bool TRANSPOSE>
+__global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs a) {
+    __shared__ uint32_t high[kSide];                             // sizes, as bits (their order is the numbers')
+    __shared__ alignas(16) uint2 turned[TRANSPOSE ? kSide * kSide / 8 : 1];
+    const int tid = static_cast<int>(threadIdx.x), at = tid % 16, row = tid / 16;
+    const int row0 = static_cast<int>(blockIdx.x / a.tiles_across) * kSide;
+    const int col0 = static_cast<int>(blockIdx.x % a.tiles_across) * kSide;
+    const int c = col0 + at * 8, left = a.cols - c;
+    if (tid < kSide) high[tid] = 0;
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    float v[kPacks][8];
+#pragma unroll
+    for (int k = 0; k < kPacks; ++k) {
+        const int r = row0 + (TRANSPOSE ? row * 8 + k : row + 16 * k);
+        load8(static_cast<const T*>(a.x) + r * a.ldx + c, r < a.rows ? left : 0, a.whole_x, v[k]);
+    }
+    if constexpr (SQUARE || TRANSPOSE) __syncthreads();
+    if constexpr (SQUARE) {
+        float m = 0.f;
+#pragma unroll
+        for (int k = 0; k < kPacks; ++k) m = fmaxf(m, largest(v[k]));
+        m = warp_max(m);
+        if (tid % 32 == 0) atomicMax(&high[0], __float_as_uint(m));
+        __syncthreads();
+    } else if constexpr (TRANSPOSE) {
+        // the largest of each column: over a thread's rows, the warp's two, and the warps
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float m = 0.f;
+#pragma unroll
+            for (int k = 0; k < kPacks; ++k) m = fmaxf(m, fabsf(v[k][i]));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+            if (tid % 32 < 16) atomicMax(&high[at * 8 + i], __float_as_uint(m));
+        }
+        __syncthreads();
+    }
+    if constexpr (!TRANSPOSE) {
+        float square = 0.f, inverse = 0.f;
+        if constexpr (SQUARE) {
+            square = scale_of(__uint_as_float(high[0]));
+            inverse = 1.f / square;
+            if (tid == 0) a.scales[row0 / kSide * a.lds + col0 / kSide] = square;
+        }
+#pragma unroll
+        for (int k = 0; k < kPacks; ++k) {
+            const int r = row0 + row + 16 * k;
+            if constexpr (!SQUARE) {
+                const float s = scale_of(largest_of_group(largest(v[k])));
+                inverse = 1.f / s;
+                if (at == 0 && r < a.rows) a.scales[r * a.lds + col0 / kSide] = s;
+            }
+            store_bytes(a.q + r * a.ldq + c, r < a.rows ? left : 0, a.whole_q, e4m3_eight(v[k], inverse));
+        }
+    } else {
+        // q's row is x's column: its scale index runs along x's rows
+        if constexpr (SQUARE) {
+            if (tid == 0) a.scales[col0 / kSide * a.lds + row0 / kSide] = scale_of(__uint_as_float(high[0]));
+        } else {
+            if (tid < kSide && col0 + tid < a.cols)
+                a.scales[(col0 + tid) * a.lds + row0 / kSide] = scale_of(__uint_as_float(high[tid]));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float inverse = 1.f / scale_of(__uint_as_float(high[SQUARE ? 0 : at * 8 + i]));
+            float down[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) down[k] = v[k][i];
+            turned[(at * 8 + i) * 16 + (row ^ at)] = e4m3_eight(down, inverse);
+        }
+        __syncthreads();
+        // 128 rows of 128 bytes, eight a thread and step
+#pragma unroll
+        for (int k = 0; k < kSide / 16; ++k) {
+            const int r = row + 16 * k;
+            const uint2 w = turned[r * 16 + (at ^ (r / 8))];
+            store_bytes(a.q + (col0 + r) * a.ldq + row0 + at * 8, col0 + r < a.cols ? a.rows - row0 - at * 8 : 0,
+                        a.whole_q, w);
+        }
+    }
+}
+
+}  // namespace
+}  // namespace gbt
+
+extern "C" gemm_status_t gemm_fp8_quantize(int64_t rows, int64_t cols, gemm_elem_t elem, const void* x,
+                                           int64_t ldx, gemm_scale_t kind, int32_t transpose, void* q,
+                                           int64_t ldq, float* scales, int64_t lds, void* stream) {
+    using namespace gbt;
+    if (!valid_elem(elem) || (kind != GEMM_SCALE_ROW && kind != GEMM_SCALE_SQUARE)) return GEMM_ERR_UNSUPPORTED;
+    if (rows < 0 || cols < 0 || rows > INT32_MAX - kSide || cols > INT32_MAX - kSide || (transpose != 0 && transpose != 1))
+        return GEMM_ERR_INVALID_ARG;
+    const int64_t down = groups_of(rows), across = groups_of(cols);
+    if (down * across > (int64_t{1} << 30)) return GEMM_ERR_INVALID_ARG;
+    const int64_t out_cols = transpose ? rows : cols;
+    if (rows > 0 && cols > 0 && (!x || !q || !scales || ldx < cols || ldq < out_cols || lds < groups_of(out_cols)))
+        return GEMM_ERR_INVALID_ARG;
+    const int e = elem_bytes(elem);
+    if (!aligned(x, e) || !aligned(scales, 4)) return GEMM_ERR_ALIGNMENT;
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_NO_DEVICE;
+    }
+    if (rows == 0 || cols == 0) return GEMM_OK;
+    const QuantArgs a{x, static_cast<uint8_t*>(q), scales, ldx, ldq, lds, static_cast<int>(rows), static_cast<int>(cols),
+                      static_cast<int>(across), rows_aligned(x, ldx, e), bytes_aligned(q, ldq)};
+    const Queue queue{stream, device};
+    return with_elem(elem, [&](auto t) {
+        using T = decltype(t);
+        const int64_t tiles = down * across;
+        if (kind == GEMM_SCALE_ROW)
+            return transpose ? launch<quantize_kernel<T, false, true>>(tiles, kQuantThreads, 0, queue, 1, a)
+                             : launch<quantize_kernel<T, false, false>>(tiles, kQuantThreads, 0, queue, 1, a);
+        return transpose ? launch<quantize_kernel<T, true, true>>(tiles, kQuantThreads, 0, queue, 1, a)
+                         : launch<quantize_kernel<T, true, false>>(tiles, kQuantThreads, 0, queue, 1, a);
+    });
+}

@@ -1,0 +1,552 @@
+// ffn_rms.cu -- root-mean-square norm with the residual's addition (gemm_ffn.h).
+#include <new>
+
+#include "ffn_common.cuh"
+
+struct gemm_rms_plan {
+    int64_t max_rows, cols;
+    gemm_elem_t elem, weight_elem;
+    int device, num_sms;
+    float* partial;      // [blocks][cols] sums of the weight's gradient
+};
+
+namespace gbt {
+namespace {
+
+constexpr int kRowPacks = 2;                  // packs of eight columns that a lane holds
+constexpr int kLaneColumns = 8 * kRowPacks;
+constexpr int kMostRowLanes = 1024;
+constexpr int kRowColumns = kMostRowLanes * kLaneColumns;   // the longest row that a block holds
+
+// Lanes that hold a row: a power of two, so that a group divides a block; 16 at least, which
+// are the 128 columns of a scale.
+int row_lanes(int64_t cols) {
+    int lanes = 16;
+    while (lanes < kMostRowLanes && lanes * kLaneColumns < cols) lanes *= 2;
+    return lanes;
+}
+
+// The sum over a row's lanes, in each of them.  part: one float per warp of the block (all of
+// its threads meet here where a row has more than a warp).
+template <int BLOCK>
+__device__ __forceinline__ float row_sum(float v, int lanes, float* part) {
+    if (lanes == 16) {
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    }
+    v = warp_sum(v);
+    if (lanes == 32) return v;
+    const int warp = static_cast<int>(threadIdx.x) / 32, warps = lanes / 32;
+    if (threadIdx.x % 32 == 0) part[warp] = v;
+    __syncthreads();
+    const int l = static_cast<int>(threadIdx.x) % 32;
+    v = part[warp / warps * warps + l % warps];      // every warp's sum, 32 / warps times
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        if (o < warps) v += __shfl_xor_sync(0xffffffffu, v, o);
+    }
+    return v;
+}
+
+template <typename T, typename W>
+struct RmsForwardArgs {
+    const T* x;
+    const T* residual;
+    const W* gamma;
+    T* total;
+    T* y;
+    uint8_t* q;
+    float* scales;
+    float* rstd;
+    int64_t ldx, ldr, ldt, ldy, ldq, lds, rows;
+    float eps;
+    int cols, lanes;
+    bool whole;                 // rows and gamma move in packs
+};
+
+// x + residual as it is kept: an fp32 sum (one rounding), rounded to T.
+template <typename T>
+__device__ __forceinline__ void sum8(const T* x, const T* residual, int n, bool whole, float (&v)[8]) {
+    load8(x, n, whole, v);
+    if (residual) {
+        float r[8];
+        load8(residual, n, whole, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = to_f32(from_f32<T>(v[i] + r[i]));
+    }
+}
+
+// y of a pack from t, and its conversion where Q8 (all lanes of a warp come here).
+template <typename T, typename W, bool Q8>
+__device__ __forceinline__ void finish_pack(const RmsForwardArgs<T, W>& a, int64_t row, int c, int n, float rstd,
+                                            float (&t)[8]) {
+    float w[8];
+    if (a.gamma) load8(a.gamma + c, n, a.whole, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = a.gamma ? t[i] * rstd * w[i] : t[i] * rstd;
+    if constexpr (Q8) {
+        const float s = scale_of(largest_of_group(largest(t)));
+        if (n > 0) {
+            if (c % kGroup == 0) a.scales[row * a.lds + c / kGroup] = s;
+            store_bytes(a.q + row * a.ldq + c, n, a.whole, e4m3_eight(t, 1.f / s));
+        }
+    } else if (n > 0) {
+        store8(a.y + row * a.ldy + c, n, a.whole, t);
+    }
+}
+
+// A row is held by `lanes` threads, 16 columns each: it is read once, and its sum of squares
+// and results come from registers.  Bound by memory; the loads in flight are those of the
+// blocks that share an SM, so a block does not look beyond its rows.
+template <typename T, typename W, int BLOCK, bool Q8>
+__global__ void __launch_bounds__(BLOCK) rms_forward_kernel(const RmsForwardArgs<T, W> a) {
+    __shared__ float part[BLOCK / 32];
+    const int lane = static_cast<int>(threadIdx.x) & (a.lanes - 1);
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (BLOCK / a.lanes) + threadIdx.x / a.lanes;
+    const bool there = row < a.rows;
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    float t[kRowPacks][8];
+#pragma unroll
+    for (int k = 0; k < kRowPacks; ++k) {
+        const int c = (k * a.lanes + lane) * 8;
+        sum8(a.x + row * a.ldx + c, a.residual ? a.residual + row * a.ldr + c : nullptr, there ? a.cols - c : 0, a.whole,
+             t[k]);
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kRowPacks; ++k) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(t[k][i], t[k][i], sum);
+    }
+    if (a.total && there) {
+#pragma unroll
+        for (int k = 0; k < kRowPacks; ++k) {
+            const int c = (k * a.lanes + lane) * 8;
+            store8(a.total + row * a.ldt + c, a.cols - c, a.whole, t[k]);
+        }
+    }
+    sum = row_sum<BLOCK>(sum, a.lanes, part);
+    const float rstd = 1.f / sqrtf(sum / static_cast<float>(a.cols) + a.eps);
+    if (a.rstd && there && lane == 0) a.rstd[row] = rstd;
+#pragma unroll
+    for (int k = 0; k < kRowPacks; ++k) {
+        const int c = (k * a.lanes + lane) * 8;
+        finish_pack<T, W, Q8>(a, row, c, there ? a.cols - c : 0, rstd, t[k]);
+    }
+}
+
+// Longer rows: a block goes over its row twice.
+template <typename T, typename W, bool Q8>
+__global__ void __launch_bounds__(kMostRowLanes) rms_forward_wide_kernel(const RmsForwardArgs<T, W> a) {
+    __shared__ float part[kMostRowLanes / 32];
+    const int64_t row = blockIdx.x;
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    const T* x = a.x + row * a.ldx;
+    const T* residual = a.residual ? a.residual + row * a.ldr : nullptr;
+    T* total = a.total ? a.total + row * a.ldt : nullptr;
+    float sum = 0.f;
+    for (int c = static_cast<int>(threadIdx.x) * 8; c < a.cols; c += kMostRowLanes * 8) {
+        float t[8];
+        sum8(x + c, residual ? residual + c : nullptr, a.cols - c, a.whole, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(t[i], t[i], sum);
+        if (total) store8(total + c, a.cols - c, a.whole, t);
+    }
+    sum = row_sum<kMostRowLanes>(sum, kMostRowLanes, part);
+    const float rstd = 1.f / sqrtf(sum / static_cast<float>(a.cols) + a.eps);
+    if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+    // (a thread reads back only what it wrote: total may be x or the residual.  All lanes of a
+    // warp go through every step: the largest value of a group is taken among them.)
+    for (int c0 = 0; c0 < a.cols; c0 += kMostRowLanes * 8) {
+        const int c = c0 + static_cast<int>(threadIdx.x) * 8, n = a.cols - c;
+        float t[8];
+        if (total) {
+            load8(static_cast<const T*>(total) + c, n, a.whole, t);
+        } else {
+            sum8(x + c, residual ? residual + c : nullptr, n, a.whole, t);
+        }
+        finish_pack<T, W, Q8>(a, row, c, n, rstd, t);
+    }
+}
+
+// ---------------------------------------------------------------- backward
+
+template <typename T, typename W>
+struct RmsBackwardArgs {
+    const T* total;
+    const W* gamma;
+    const float* rstd;
+    const T* dy;
+    const T* dtotal;
+    T* dx;
+    float* partial;             // [grid][cols], or NULL: no gradient of gamma wanted
+    int64_t ldt, lddy, lddt, lddx, rows;
+    int cols, lanes;
+    bool whole;
+};
+
+template <typename W>
+__device__ __forceinline__ void weight8(const W* gamma, int c, int n, bool whole, float (&w)[8]) {
+    if (gamma) {
+        load8(gamma + c, n, whole, w);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    }
+}
+
+// Blocks of a backward kernel that share an SM (its registers: 128 a thread).
+constexpr int backward_blocks_an_sm(int block) { return block < 512 ? 512 / block : 1; }
+
+// A block goes over rows blockIdx.x, + gridDim.x, ... (BLOCK / lanes at a time) and keeps its
+// share of the weight's gradient in registers, 16 columns a lane.
+template <typename T, typename W, int BLOCK>
+__global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backward_kernel(const RmsBackwardArgs<T, W> a) {
+    extern __shared__ float shared[];            // (where a block has several groups: their sums)
+    __shared__ float part[2][BLOCK / 32];
+    const int lane = static_cast<int>(threadIdx.x) & (a.lanes - 1);
+    const int groups = BLOCK / a.lanes, group = static_cast<int>(threadIdx.x) / a.lanes;
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    float dgamma[kRowPacks][8] = {};
+    int turn = 0;
+    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups; row0 < a.rows; row0 += static_cast<int64_t>(gridDim.x) * groups) {
+        const int64_t row = row0 + group;
+        const bool there = row < a.rows;
+        const float rstd = there ? a.rstd[row] : 0.f;
+        float hat[kRowPacks][8], g[kRowPacks][8], more[kRowPacks][8];
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < kRowPacks; ++k) {
+            const int c = (k * a.lanes + lane) * 8, n = there ? a.cols - c : 0;
+            load8(a.total + row * a.ldt + c, n, a.whole, hat[k]);
+            load8(a.dy + row * a.lddy + c, n, a.whole, g[k]);
+            if (a.dtotal) load8(a.dtotal + row * a.lddt + c, n, a.whole, more[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kRowPacks; ++k) {
+            const int c = (k * a.lanes + lane) * 8;
+            float w[8];
+            weight8(a.gamma, c, a.cols - c, a.whole, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                hat[k][i] *= rstd;
+                dgamma[k][i] = fmaf(g[k][i], hat[k][i], dgamma[k][i]);
+                g[k][i] *= w[i];
+                sum = fmaf(g[k][i], hat[k][i], sum);
+            }
+        }
+        if (!a.dx) continue;                     // (all of the block)
+        sum = row_sum<BLOCK>(sum, a.lanes, part[turn]);
+        turn ^= 1;
+        const float mean = sum / static_cast<float>(a.cols);
+#pragma unroll
+        for (int k = 0; k < kRowPacks; ++k) {
+            const int c = (k * a.lanes + lane) * 8, n = there ? a.cols - c : 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                g[k][i] = rstd * (g[k][i] - hat[k][i] * mean);
+                if (a.dtotal) g[k][i] += more[k][i];
+            }
+            if (n > 0) store8(a.dx + row * a.lddx + c, n, a.whole, g[k]);
+        }
+    }
+    if (!a.partial) return;
+    float* to = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols;
+    if (groups > 1) {
+#pragma unroll
+        for (int k = 0; k < kRowPacks; ++k) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) shared[threadIdx.x * kLaneColumns + k * 8 + i] = dgamma[k][i];
+        }
+        __syncthreads();
+        if (group != 0) return;
+        for (int other = 1; other < groups; ++other) {
+#pragma unroll
+            for (int k = 0; k < kRowPacks; ++k) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    dgamma[k][i] += shared[(other * a.lanes + lane) * kLaneColumns + k * 8 + i];
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kRowPacks; ++k) {
+        const int c = (k * a.lanes + lane) * 8;
+        store8(to + c, a.cols - c, a.cols % 4 == 0, dgamma[k]);
+    }
+}
+
+// Longer rows: dx, a row a block, twice over it.
+template <typename T, typename W>
+__global__ void __launch_bounds__(kMostRowLanes) rms_dx_wide_kernel(const RmsBackwardArgs<T, W> a) {
+    __shared__ float part[kMostRowLanes / 32];
+    const int64_t row = blockIdx.x;
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    const T* total = a.total + row * a.ldt;
+    const T* dy = a.dy + row * a.lddy;
+    const float rstd = a.rstd[row];
+    float sum = 0.f;
+    for (int c = static_cast<int>(threadIdx.x) * 8; c < a.cols; c += kMostRowLanes * 8) {
+        float t[8], g[8], w[8];
+        load8(total + c, a.cols - c, a.whole, t);
+        load8(dy + c, a.cols - c, a.whole, g);
+        weight8(a.gamma, c, a.cols - c, a.whole, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(g[i] * w[i], t[i] * rstd, sum);
+    }
+    const float mean = row_sum<kMostRowLanes>(sum, kMostRowLanes, part) / static_cast<float>(a.cols);
+    for (int c = static_cast<int>(threadIdx.x) * 8; c < a.cols; c += kMostRowLanes * 8) {
+        float t[8], g[8], w[8], more[8];
+        load8(total + c, a.cols - c, a.whole, t);
+        load8(dy + c, a.cols - c, a.whole, g);
+        weight8(a.gamma, c, a.cols - c, a.whole, w);
+        if (a.dtotal) load8(a.dtotal + row * a.lddt + c, a.cols - c, a.whole, more);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            g[i] = rstd * (g[i] * w[i] - t[i] * rstd * mean);
+            if (a.dtotal) g[i] += more[i];
+        }
+        store8(a.dx + row * a.lddx + c, a.cols - c, a.whole, g);
+    }
+}
+
+constexpr int kJoinThreads = 256;
+
+// ... and gamma's gradient, 32 columns a block, its eight warps over the rows.
+template <typename T, typename W>
+__global__ void __launch_bounds__(kJoinThreads) rms_dgamma_wide_kernel(const RmsBackwardArgs<T, W> a, W* dgamma) {
+    __shared__ float part[kJoinThreads / 32][32];
+    const int lane = static_cast<int>(threadIdx.x) % 32, warp = static_cast<int>(threadIdx.x) / 32;
+    const int c = static_cast<int>(blockIdx.x) * 32 + lane;
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    float sum = 0.f;
+    if (c < a.cols) {
+#pragma unroll 8
+        for (int64_t row = warp; row < a.rows; row += kJoinThreads / 32)
+            sum = fmaf(to_f32(a.dy[row * a.lddy + c]), to_f32(a.total[row * a.ldt + c]) * a.rstd[row], sum);
+    }
+    part[warp][lane] = sum;
+    __syncthreads();
+    if (warp != 0 || c >= a.cols) return;
+#pragma unroll
+    for (int w = 1; w < kJoinThreads / 32; ++w) sum += part[w][lane];
+    dgamma[c] = from_f32<W>(sum);
+}
+
+// The blocks' sums of a column, in their order.
+template <typename W>
+__global__ void __launch_bounds__(kJoinThreads) rms_dgamma_join_kernel(const float* partial, int blocks, int cols, W* dgamma) {
+    __shared__ float part[kJoinThreads / 32][32];
+    const int lane = static_cast<int>(threadIdx.x) % 32, warp = static_cast<int>(threadIdx.x) / 32;
+    const int c = static_cast<int>(blockIdx.x) * 32 + lane;
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    float sum = 0.f;
+    if (c < cols) {
+#pragma unroll 8
+        for (int b = warp; b < blocks; b += kJoinThreads / 32) sum += partial[static_cast<int64_t>(b) * cols + c];
+    }
+    part[warp][lane] = sum;
+    __syncthreads();
+    if (warp != 0 || c >= cols) return;
+#pragma unroll
+    for (int w = 1; w < kJoinThreads / 32; ++w) sum += part[w][lane];
+    dgamma[c] = from_f32<W>(sum);
+}
+
+// ---------------------------------------------------------------- launches
+
+constexpr int row_block(int lanes) { return lanes < 128 ? 128 : lanes; }
+
+template <typename T, typename W, bool Q8>
+gemm_status_t forward(const RmsForwardArgs<T, W>& a, Queue queue) {
+    if (a.cols > kRowColumns)
+        return launch<rms_forward_wide_kernel<T, W, Q8>>(a.rows, kMostRowLanes, 0, queue, 1, a);
+    const int block = row_block(a.lanes);
+    const int64_t grid = (a.rows + block / a.lanes - 1) / (block / a.lanes);
+    switch (block) {
+        case 128: return launch<rms_forward_kernel<T, W, 128, Q8>>(grid, 128, 0, queue, 1, a);
+        case 256: return launch<rms_forward_kernel<T, W, 256, Q8>>(grid, 256, 0, queue, 1, a);
+        case 512: return launch<rms_forward_kernel<T, W, 512, Q8>>(grid, 512, 0, queue, 1, a);
+        default: return launch<rms_forward_kernel<T, W, 1024, Q8>>(grid, 1024, 0, queue, 1, a);
+    }
+}
+
+// Blocks of a backward launch: enough for every row, at most what the SMs hold at once.
+int64_t backward_grid(int64_t rows, int lanes, int sms) {
+    const int block = row_block(lanes), groups = block / lanes;
+    const int64_t blocks = (rows + groups - 1) / groups, most = static_cast<int64_t>(sms) * backward_blocks_an_sm(block);
+    return blocks < most ? blocks : most;
+}
+
+template <typename T, typename W>
+gemm_status_t backward(const RmsBackwardArgs<T, W>& a, int64_t grid, Queue queue) {
+    const int block = row_block(a.lanes);
+    const size_t smem = block > a.lanes ? static_cast<size_t>(block) * kLaneColumns * sizeof(float) : 0;
+    switch (block) {
+        case 128: return launch<rms_backward_kernel<T, W, 128>>(grid, 128, smem, queue, 1, a);
+        case 256: return launch<rms_backward_kernel<T, W, 256>>(grid, 256, smem, queue, 1, a);
+        case 512: return launch<rms_backward_kernel<T, W, 512>>(grid, 512, smem, queue, 1, a);
+        default: return launch<rms_backward_kernel<T, W, 1024>>(grid, 1024, smem, queue, 1, a);
+    }
+}
+
+template <typename F>
+gemm_status_t with_types(const gemm_rms_plan* p, F f) {
+    return with_elem(p->elem, [&](auto t) {
+        if (p->weight_elem == GEMM_ELEM_F32) return f(t, float());
+        return f(t, t);
+    });
+}
+
+gemm_status_t check_forward(const gemm_rms_plan* p, int64_t rows, const void* x, int64_t ldx, const void* residual,
+                            int64_t ldr, const void* gamma, float eps, const void* total, int64_t ldt, const void* out,
+                            int64_t ldo, const float* rstd) {
+    if (!p || rows < 0 || rows > p->max_rows || !(eps >= 0.f)) return GEMM_ERR_INVALID_ARG;
+    if (rows > 0 && (!x || !out || ldx < p->cols || ldo < p->cols || (residual && ldr < p->cols) ||
+                     (total && (ldt < p->cols || total == out))))
+        return GEMM_ERR_INVALID_ARG;
+    const int e = elem_bytes(p->elem);
+    if (!aligned(x, e) || !aligned(residual, e) || !aligned(total, e) || !aligned(gamma, elem_bytes(p->weight_elem)) ||
+        !aligned(rstd, 4))
+        return GEMM_ERR_ALIGNMENT;
+    return check_device(p->device);
+}
+
+}  // namespace
+}  // namespace gbt
+
+extern "C" {
+
+gemm_status_t gemm_rms_plan_create(int64_t max_rows, int64_t cols, gemm_elem_t elem, gemm_elem_t weight_elem,
+                                   gemm_rms_plan_t* plan) {
+    if (!plan) return GEMM_ERR_INVALID_ARG;
+    *plan = nullptr;
+    if (!gbt::valid_elem(elem) || (weight_elem != elem && weight_elem != GEMM_ELEM_F32)) return GEMM_ERR_UNSUPPORTED;
+    if (max_rows < 0 || max_rows > INT32_MAX || cols < 1 || cols > gbt::kMostColumns) return GEMM_ERR_INVALID_ARG;
+    int device = 0, sms = 0;
+    const gemm_status_t st = gbt::begin_plan(&device, &sms);
+    if (st != GEMM_OK) return st;
+    size_t sums = 0;
+    if (cols <= gbt::kRowColumns)
+        sums = static_cast<size_t>(gbt::backward_grid(max_rows, gbt::row_lanes(cols), sms) * cols) * sizeof(float);
+    void* memory = nullptr;
+    const gemm_status_t room = sums > 0 ? gbt::allocate(&memory, sums) : GEMM_OK;
+    if (room != GEMM_OK) return room;
+    gemm_rms_plan* p = new (std::nothrow) gemm_rms_plan();
+    if (!p) {
+        cudaFree(memory);
+        return GEMM_ERR_OOM;
+    }
+    p->max_rows = max_rows;
+    p->cols = cols;
+    p->elem = elem;
+    p->weight_elem = weight_elem;
+    p->device = device;
+    p->num_sms = sms;
+    p->partial = static_cast<float*>(memory);
+    *plan = p;
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_rms_forward(gemm_rms_plan_t p, int64_t rows, const void* x, int64_t ldx, const void* residual,
+                               int64_t ldr, const void* gamma, float eps, void* total, int64_t ldt, void* y,
+                               int64_t ldy, float* rstd, void* stream) {
+    const gemm_status_t st = gbt::check_forward(p, rows, x, ldx, residual, ldr, gamma, eps, total, ldt, y, ldy, rstd);
+    if (st != GEMM_OK) return st;
+    const int e = gbt::elem_bytes(p->elem);
+    if (!gbt::aligned(y, e)) return GEMM_ERR_ALIGNMENT;
+    if (rows == 0) return GEMM_OK;
+    const bool whole = gbt::rows_aligned(x, ldx, e) && gbt::packs_aligned(residual, ldr, e) &&
+                       gbt::packs_aligned(total, ldt, e) && gbt::rows_aligned(y, ldy, e) && gbt::aligned(gamma, 16);
+    return gbt::with_types(p, [&](auto t, auto v) {
+        using T = decltype(t);
+        using W = decltype(v);
+        const gbt::RmsForwardArgs<T, W> a{static_cast<const T*>(x), static_cast<const T*>(residual),
+                                          static_cast<const W*>(gamma), static_cast<T*>(total), static_cast<T*>(y), nullptr,
+                                          nullptr, rstd, ldx, ldr, ldt, ldy, 0, 0, rows, eps, static_cast<int>(p->cols),
+                                          gbt::row_lanes(p->cols), whole};
+        return gbt::forward<T, W, false>(a, gbt::Queue{stream, p->device});
+    });
+}
+
+gemm_status_t gemm_rms_forward_fp8(gemm_rms_plan_t p, int64_t rows, const void* x, int64_t ldx, const void* residual,
+                                   int64_t ldr, const void* gamma, float eps, void* total, int64_t ldt, void* q,
+                                   int64_t ldq, float* scales, int64_t lds, float* rstd, void* stream) {
+    const gemm_status_t st = gbt::check_forward(p, rows, x, ldx, residual, ldr, gamma, eps, total, ldt, q, ldq, rstd);
+    if (st != GEMM_OK) return st;
+    if (rows > 0 && (!scales || lds < gbt::groups_of(p->cols))) return GEMM_ERR_INVALID_ARG;
+    if (!gbt::aligned(scales, 4)) return GEMM_ERR_ALIGNMENT;
+    if (rows == 0) return GEMM_OK;
+    const int e = gbt::elem_bytes(p->elem);
+    const bool whole = gbt::rows_aligned(x, ldx, e) && gbt::packs_aligned(residual, ldr, e) &&
+                       gbt::packs_aligned(total, ldt, e) && gbt::bytes_aligned(q, ldq) && gbt::aligned(gamma, 16);
+    return gbt::with_types(p, [&](auto t, auto v) {
+        using T = decltype(t);
+        using W = decltype(v);
+        const gbt::RmsForwardArgs<T, W> a{static_cast<const T*>(x), static_cast<const T*>(residual),
+                                          static_cast<const W*>(gamma), static_cast<T*>(total), nullptr,
+                                          static_cast<uint8_t*>(q), scales, rstd, ldx, ldr, ldt, 0, ldq, lds, rows, eps,
+                                          static_cast<int>(p->cols), gbt::row_lanes(p->cols), whole};
+        return gbt::forward<T, W, true>(a, gbt::Queue{stream, p->device});
+    });
+}
+
+gemm_status_t gemm_rms_backward(gemm_rms_plan_t p, int64_t rows, const void* total, int64_t ldt, const void* gamma,
+                                const float* rstd, const void* dy, int64_t lddy, const void* dtotal, int64_t lddt,
+                                void* dx, int64_t lddx, void* dgamma, void* stream) {
+    if (!p || rows < 0 || rows > p->max_rows) return GEMM_ERR_INVALID_ARG;
+    if (rows > 0 && (!total || !rstd || !dy || ldt < p->cols || lddy < p->cols || (dtotal && lddt < p->cols) ||
+                     (dx && lddx < p->cols)))
+        return GEMM_ERR_INVALID_ARG;
+    const int e = gbt::elem_bytes(p->elem), w = gbt::elem_bytes(p->weight_elem);
+    if (!gbt::aligned(total, e) || !gbt::aligned(dy, e) || !gbt::aligned(dtotal, e) || !gbt::aligned(dx, e) ||
+        !gbt::aligned(gamma, w) || !gbt::aligned(dgamma, w) || !gbt::aligned(rstd, 4))
+        return GEMM_ERR_ALIGNMENT;
+    const gemm_status_t st = gbt::check_device(p->device);
+    if (st != GEMM_OK || (!dx && !dgamma)) return st;
+    const bool whole = gbt::rows_aligned(total, ldt, e) && gbt::rows_aligned(dy, lddy, e) &&
+                       gbt::packs_aligned(dtotal, lddt, e) && gbt::packs_aligned(dx, lddx, e) && gbt::aligned(gamma, 16);
+    const gbt::Queue queue{stream, p->device};
+    return gbt::with_types(p, [&](auto t, auto v) {
+        using T = decltype(t);
+        using W = decltype(v);
+        const int cols = static_cast<int>(p->cols), lanes = gbt::row_lanes(cols);
+        const unsigned tiles = static_cast<unsigned>((p->cols + 31) / 32);
+        const gbt::RmsBackwardArgs<T, W> a{static_cast<const T*>(total), static_cast<const W*>(gamma), rstd,
+                                           static_cast<const T*>(dy), static_cast<const T*>(dtotal), static_cast<T*>(dx),
+                                           dgamma ? p->partial : nullptr, ldt, lddy, lddt, lddx, rows, cols, lanes, whole};
+        gemm_status_t s = GEMM_OK;
+        if (cols > gbt::kRowColumns) {
+            // (the weight's gradient first: dx may overwrite dy or total)
+            if (dgamma)
+                s = gbt::launch<gbt::rms_dgamma_wide_kernel<T, W>>(tiles, gbt::kJoinThreads, 0, queue, 1, a,
+                                                                    static_cast<W*>(dgamma));
+            if (s == GEMM_OK && dx && rows > 0)
+                s = gbt::launch<gbt::rms_dx_wide_kernel<T, W>>(rows, gbt::kMostRowLanes, 0, queue, 1, a);
+            return s;
+        }
+        const int64_t grid = gbt::backward_grid(rows, lanes, p->num_sms);
+        if (grid > 0) s = gbt::backward<T, W>(a, grid, queue);
+        if (s == GEMM_OK && dgamma)
+            s = gbt::launch<gbt::rms_dgamma_join_kernel<W>>(tiles, gbt::kJoinThreads, 0, queue, 1, p->partial,
+                                                            static_cast<int>(grid), cols, static_cast<W*>(dgamma));
+        return s;
+    });
+}
+
+gemm_status_t gemm_rms_plan_destroy(gemm_rms_plan_t p) {
+    if (!p) return GEMM_OK;
+    const gemm_status_t st = cudaFree(p->partial) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+    if (st != GEMM_OK) cudaGetLastError();
+    delete p;
+    return st;
+}
+
+}  // extern "C"

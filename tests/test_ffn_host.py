@@ -1,0 +1,105 @@
+"""Host side of the feed-forward block's operators (no GPU needed): exports, refusals of the C functions
+before they touch a device, plan creation without one, and the oracle of their tests."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import ffn_oracle as ref
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HAS_GPU = torch.cuda.is_available()
+
+
+def test_every_declared_function_has_a_signature(gemm_lib):
+    text = open(os.path.join(ROOT, "include", "gemm_ffn.h"), encoding="utf-8").read()
+    names = set(re.findall(r"\b(gemm_[a-z_0-9]+)\s*\(", re.sub(r"/\*.*?\*/", "", text, flags=re.S)))
+    assert names == set(gemm_lib.ffn.signatures())
+    for n in names:
+        assert getattr(gemm_lib.library(), n).argtypes is not None
+
+
+@pytest.mark.parametrize("name,args,expect", [
+    ("gemm_rms_plan_create", (4, 8, 7, 2), 2),              # unknown type
+    ("gemm_rms_plan_create", (4, 8, 0, 1), 2),              # bf16 weights of an fp16 norm
+    ("gemm_rms_plan_create", (4, 0, 0, 0), 1),
+    ("gemm_rms_plan_create", (-1, 8, 0, 0), 1),
+    ("gemm_rms_plan_create", (2 ** 31, 8, 0, 0), 1),
+    ("gemm_rms_plan_create", (4, 2 ** 30 + 1, 0, 0), 1),
+    ("gemm_rms_plan_create", (4, 8, 0, 2), None),
+])
+def test_plan_creation_validates_first(gemm_lib, name, args, expect):
+    h = ctypes.c_void_p()
+    lib = gemm_lib.library()
+    st = getattr(lib, name)(*args, ctypes.byref(h))
+    assert st == (expect if expect is not None else 0 if HAS_GPU else 4)
+    if st == 0:
+        assert getattr(lib, name.replace("create", "destroy"))(h.value) == 0
+    else:
+        assert not h.value
+    assert getattr(lib, name)(*args, None) == 1
+
+
+def test_null_handles(gemm_lib):
+    lib = gemm_lib.library()
+    assert lib.gemm_rms_forward(None, 0, None, 0, None, 0, None, 0.0, None, 0, None, 0, None, None) == 1
+    assert lib.gemm_rms_forward_fp8(None, 0, None, 0, None, 0, None, 0.0, None, 0, None, 0, None, 0, None, None) == 1
+    assert lib.gemm_rms_backward(None, 0, None, 0, None, None, None, 0, None, 0, None, 0, None, None) == 1
+    assert lib.gemm_rms_plan_destroy(None) == 0
+
+
+@pytest.mark.parametrize("args,expect", [
+    ((4, 8, 9, 4096, 8, 0, 0, 4096, 8, 4096, 1), 2),         # type
+    ((4, 8, 0, 4096, 8, 2, 0, 4096, 8, 4096, 1), 2),         # kind of scales
+    ((4, 8, 0, 4096, 8, 0, 2, 4096, 8, 4096, 1), 1),         # transpose
+    ((-4, 8, 0, 4096, 8, 0, 0, 4096, 8, 4096, 1), 1),
+    ((4, 2 ** 31, 0, 4096, 2 ** 31, 0, 0, 4096, 2 ** 31, 4096, 2 ** 24), 1),
+    ((4, 8, 0, 4096, 7, 0, 0, 4096, 8, 4096, 1), 1),         # strides
+    ((4, 8, 0, 4096, 8, 0, 0, 4096, 7, 4096, 1), 1),
+    ((4, 8, 0, 4096, 8, 0, 1, 4096, 3, 4096, 1), 1),
+    ((4, 200, 0, 4096, 200, 0, 0, 4096, 200, 4096, 1), 1),
+    ((4, 8, 0, None, 8, 0, 0, 4096, 8, 4096, 1), 1),
+    ((4, 8, 0, 4096, 8, 0, 0, 4096, 8, None, 1), 1),
+    ((4, 8, 0, 4097, 8, 0, 0, 4096, 8, 4096, 1), 3),
+    ((4, 8, 0, 4096, 8, 0, 0, 4096, 8, 4098, 1), 3),
+])
+def test_conversion_validates_first(gemm_lib, args, expect):
+    assert gemm_lib.library().gemm_fp8_quantize(*args, None) == expect
+
+
+@pytest.mark.skipif(HAS_GPU, reason="checks the no-device path")
+def test_plans_without_a_gpu_raise(gemm_lib):
+    for make, status in ((lambda: gemm_lib.RmsNormPlan(4, 8), 4), (lambda: gemm_lib.RmsNormPlan(4, 8, "i8"), 2),
+                         (lambda: gemm_lib.fp8_quantize(*[torch.zeros(4, 8)] * 3), 1)):
+        with pytest.raises(gemm_lib.GemmError) as e:
+            make()
+        assert e.value.status == status
+
+
+def test_oracle_gradients_agree_with_differences():
+    g = torch.Generator().manual_seed(0)
+    r = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+    t, gamma, dy, dt, step = r(4, 9), r(9), r(4, 9), r(4, 9), 1e-5
+    value = lambda t, gamma: ((ref.rms_forward(t, gamma, 1e-5)[0] * dy).sum() + (t * dt).sum())  # noqa: E731
+    rstd = ref.rms_forward(t, gamma, 1e-5)[1]
+    dx, dgamma = ref.rms_backward(t, gamma, rstd, dy, dt)
+    for at in ((0, 0), (2, 5), (3, 8)):
+        d = torch.zeros_like(t)
+        d[at] = step
+        assert abs((value(t + d, gamma) - value(t - d, gamma)) / (2 * step) - dx[at]) < 1e-7
+        e = torch.zeros_like(gamma)
+        e[at[1]] = step
+        assert abs((value(t, gamma + e) - value(t, gamma - e)) / (2 * step) - dgamma[at[1]]) < 1e-7
+    x = r(50)
+    for kind in ("silu", "gelu", "relu", "none"):
+        slope = (ref.act(x + step, kind)[0] - ref.act(x - step, kind)[0]) / (2 * step)
+        assert (slope - ref.act(x, kind)[1]).abs().max() < 1e-7
+
+
+def test_oracle_conversion():
+    x = torch.tensor([[448.0, 1.0, -3.3, 2.0 ** -10]])
+    q, s = ref.quantize(x, False)
+    assert s.item() == 1.0 and q.float().tolist() == [[448.0, 1.0, -3.25, 0.0]]     # 2^-10 is half the smallest: even
+    assert (ref.stands_for(q, s, False) - x.double()).abs().le(ref.conversion_bound(x.double(), s, False)).all()
