@@ -28,7 +28,7 @@ __all__ = [
     "gemm_abi_version", "gemm_launch_empty", "gemm_run_splitk_noalloc", "gemm_noalloc_check",
     "gemm_noalloc_set_wait_test", "gemm_probe_mma_rate", "library", "DTYPES",
     "ELEMS", "NormPlan", "EmbedPlan", "DistillPlan",
-    "RmsNormPlan", "fp8_quantize",
+    "RmsNormPlan", "fp8_quantize", "Fp8Plan", "GatedPlan",
 ]
 
 GEMM_F16, GEMM_BF16, GEMM_I8_I32 = 0, 1, 2
@@ -399,5 +399,5 @@ class Plan:
 
 
 from . import ffn, train   # noqa: E402  (they need the names above)
-from .ffn import RmsNormPlan, fp8_quantize   # noqa: E402
+from .ffn import Fp8Plan, GatedPlan, RmsNormPlan, fp8_quantize   # noqa: E402
 from .train import ELEMS, DistillPlan, EmbedPlan, NormPlan   # noqa: E402

@@ -1,0 +1,440 @@
+// ffn_fp8.cu -- the product of e4m3 matrices with a scale for each 128 elements (gemm_ffn.h).
+#include <new>
+#include <type_traits>
+
+#include "ffn_mma.cuh"
+#include "gemm_launch.h"
+
+struct gemm_fp8_plan {
+    int64_t M, N, K;
+    gemm_elem_t out;
+    gemm_scale_t b_scales;
+    gbf::PlanBase base;
+};
+
+namespace gbf {
+namespace {
+
+constexpr int kSumWarps = 8;                      // of a CTA
+constexpr int kPairThreads = 64 + 32 * kSumWarps;
+
+// BYROW: B's scales go by rows.
+template <bool BYROW>
+struct Fp8Layout {
+    static constexpr int kStages = BYROW ? 5 : 6;
+    static constexpr int kStageBytes = 2 * kTileSlot;                  // A and this CTA's half of B
+    static constexpr int kRing = kStages * kStageBytes;
+    static constexpr int kStoreBuf = 32 * kRowBytes;
+    static constexpr int kStaging = kSumWarps * kStoreBuf;
+    static constexpr int kScales = BYROW ? 2 * 256 * 4 : 0;
+    static constexpr int kTotal = 1024 + kRing + kStaging + 256 + kScales;
+    static_assert(kTotal <= 232448, "exceeds the 227 KiB a CTA may use");
+};
+
+struct Fp8Params {
+    int32_t M, N;
+    int32_t num_kb, m_blocks, num_units;
+    uint32_t idesc, tx_extra;
+    bool whole_a, whole_b;                        // the scales' rows move in fours
+    const float* a_scales;
+    const float* b_scales;
+    int32_t* error_word;
+    uint64_t timeout_ns;
+    RasterDiv rd;
+};
+
+// Whether `ok` holds in all of the four warps that meet at this barrier; what they wrote to shared
+// memory before is there after it.
+__device__ __forceinline__ bool all_of_half(int barrier, bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t"
+        ".reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.red.and.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t"
+        "}"
+        : "=r"(all)
+        : "r"(ok ? 1u : 0u), "r"(barrier)
+        : "memory");
+    return all != 0;
+}
+
+// Many rows: a pair of SMs computes 256 x 256 of C, as the plain product's pair does
+// (gemm_kernel_2cta.cuh).  The tensor cores know no scales, so the sum over each 128 elements of
+// K has an accumulator of its own (two of 256 columns in turn, all of TMEM), which eight warps a CTA
+// multiply by the scales of its row and column and add to fp32 sums in registers, 128 columns a
+// thread.  One such step is 512 cycles of the tensor cores; a thread's share is 128 accumulators
+// from TMEM and 64 fused multiply-adds of two.
+template <int OUT, bool BYROW>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                    const __grid_constant__ CUtensorMap tmap_c, const Fp8Params p) {
+    using L = Fp8Layout<BYROW>;
+    constexpr int kStages = L::kStages;
+    constexpr int kBN = 256, kHalf = 128;
+    constexpr uint32_t kPairTx = 2 * L::kStageBytes;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    const uint32_t ring = smem_addr(smem), ring_b = ring + kStages * kTileSlot;
+    const uint32_t staging = ring + L::kRing;
+    SharedCtl<kStages>* ctl = reinterpret_cast<SharedCtl<kStages>*>(smem + L::kRing + L::kStaging);
+    float* col_scales = reinterpret_cast<float*>(smem + L::kRing + L::kStaging + 256);   // [2][256]
+
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / 32, 0);
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int32_t pair = static_cast<int32_t>(blockIdx.x >> 1), npairs = static_cast<int32_t>(gridDim.x >> 1);
+
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&tmap_a);
+        prefetch_tmap(&tmap_b);
+        prefetch_tmap(&tmap_c);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_addr(&ctl->full[s]), 1);
+            mbar_init(smem_addr(&ctl->empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_addr(&ctl->tmem_full[b]), 1);
+            mbar_init(smem_addr(&ctl->tmem_empty[b]), 2 * kSumWarps);
+        }
+        mbar_init(smem_addr(&ctl->drain), 1);
+        ctl->abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_addr(&ctl->tmem_base), 2 * kBN);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = ctl->tmem_base;
+    const Watch watch{&ctl->abort, p.error_word, p.timeout_ns};
+    if (!leader && threadIdx.x == 0) {
+        // the leader's MMAs address the peer's TMEM with the leader's address
+        if (ld_dsmem_u32(map_to_rank(smem_addr(&ctl->tmem_base), 0)) != tmem_base) {
+            atomicCAS(p.error_word, 0, kSitePairTmem);
+            ctl->abort = 1;
+        }
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    if (warp == 0) {
+        if (elect_one_sync()) {
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int32_t u = pair; ok && u < p.num_units; u += npairs) {
+                int32_t m_blk, n_blk;
+                raster_tile_fast(p.m_blocks, p.rd, u, &m_blk, &n_blk);
+                const int32_t a_row = (2 * m_blk + static_cast<int32_t>(rank)) * kBM;
+                const int32_t b_row = (2 * n_blk + static_cast<int32_t>(rank)) * kHalf;
+                for (int32_t kb = 0; kb < p.num_kb; ++kb) {
+                    if (issued >= kStages &&
+                        !wait_phase(smem_addr(&ctl->empty[stage]), phase ^ 1u, watch, kSiteProducerEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = smem_addr(&ctl->full[stage]);
+                    if (leader) mbar_arrive_expect_tx(full, kPairTx + p.tx_extra);
+                    const uint32_t full_lead = map_to_rank(full, 0);
+                    tma_load_2d_pair(ring + stage * kTileSlot, &tmap_a, full_lead, kb * kRowBytes, a_row);
+                    tma_load_2d_pair(ring_b + stage * kTileSlot, &tmap_b, full_lead, kb * kRowBytes, b_row);
+                    issued = issued < kStages ? issued + 1 : kStages;
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // both CTAs' copies count on the leader's barriers: they land before the pair can leave
+            for (int i = 0; i < issued; ++i) {
+                if (--stage < 0) {
+                    stage = kStages - 1;
+                    phase ^= 1u;
+                }
+                if (leader) wait_phase_unwind(smem_addr(&ctl->full[stage]), phase, 100000000ull);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (leader && elect_one_sync()) {
+            int stage = 0;
+            uint32_t phase = 0, turn = 0;
+            bool ok = true;
+            for (int32_t u = pair; ok && u < p.num_units; u += npairs) {
+                for (int32_t kb = 0; kb < p.num_kb; ++kb, ++turn) {
+                    const uint32_t buf = turn & 1u;
+                    if ((turn >= 2 && !wait_phase_cluster(smem_addr(&ctl->tmem_empty[buf]), ((turn >> 1) & 1u) ^ 1u, watch,
+                                                          kSiteMmaTmemEmpty)) ||
+                        !wait_phase(smem_addr(&ctl->full[stage]), phase, watch, kSiteMmaFull)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t a_desc = sw128_kmajor_desc(ring + stage * kTileSlot);
+                    const uint64_t b_desc = sw128_kmajor_desc(ring_b + stage * kTileSlot);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_f8_pair(tmem_base + buf * kBN, a_desc + 2 * k, b_desc + 2 * k, p.idesc, k > 0 ? 1u : 0u);
+                    umma_commit_pair(smem_addr(&ctl->tmem_full[buf]), 3);
+                    umma_commit_pair(smem_addr(&ctl->empty[stage]), 3);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            umma_commit_pair(smem_addr(&ctl->drain), 1);
+            wait_phase_unwind(smem_addr(&ctl->drain), 0, 100000000ull);
+        }
+        __syncwarp();
+    } else {
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        const int column = half * kHalf + ((static_cast<int>(threadIdx.x) - 64) & (kHalf - 1));   // of the tile, BYROW
+        const uint32_t acc_at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(half * kHalf);
+        const uint32_t buf_at = staging + static_cast<uint32_t>((warp - 2) * L::kStoreBuf);
+        uint32_t turn = 0;
+        bool ok = true;
+        for (int32_t u = pair; ok && u < p.num_units; u += npairs) {
+            int32_t m_blk, n_blk;
+            raster_tile_fast(p.m_blocks, p.rd, u, &m_blk, &n_blk);
+            const int32_t y = (2 * m_blk + static_cast<int32_t>(rank)) * kBM + quad * 32, row = y + lane;
+            const int32_t x = n_blk * kBN + half * kHalf;
+            float acc[kHalf];
+#pragma unroll
+            for (int c = 0; c < kHalf; ++c) acc[c] = 0.f;
+            ScaleRow sa, sb;
+            sa.begin(row < p.M ? p.a_scales + static_cast<int64_t>(row) * p.num_kb : nullptr, 0, p.num_kb, p.whole_a);
+            if constexpr (BYROW) {
+                const int32_t col = n_blk * kBN + column;
+                sb.begin(col < p.N ? p.b_scales + static_cast<int64_t>(col) * p.num_kb : nullptr, 0, p.num_kb, p.whole_b);
+            } else {
+                sb.begin(x < p.N ? p.b_scales + static_cast<int64_t>(x / kHalf) * p.num_kb : nullptr, 0, p.num_kb, p.whole_b);
+            }
+            for (int32_t kb = 0; kb < p.num_kb; ++kb, ++turn) {
+                const uint32_t buf = turn & 1u;
+                float s = sa.get(kb, 0, p.num_kb, p.whole_a);
+                const float b = sb.get(kb, 0, p.num_kb, p.whole_b);
+                if constexpr (BYROW) {
+                    // (the reads of this buffer, two steps back, ended before the last step's barrier)
+                    col_scales[buf * 256 + column] = b;
+                } else {
+                    s *= b;
+                }
+                ok = wait_phase(smem_addr(&ctl->tmem_full[buf]), (turn >> 1) & 1u, watch, kSiteEpiTmemFull);
+                if constexpr (BYROW) ok = all_of_half(1 + half, ok);   // (and its warps leave together)
+                if (!ok) break;
+                tc_fence_after();
+                const gbt::Pair s2(s, s);
+                uint32_t v[2][16];
+                tmem_ld_32x32b_x16(acc_at + buf * kBN, v[0]);
+#pragma unroll
+                for (int c = 0; c < kHalf / 16; ++c) {
+                    tmem_ld_wait16(v[c & 1]);
+                    if (c + 1 < kHalf / 16) {
+                        tmem_ld_32x32b_x16(acc_at + buf * kBN + (c + 1) * 16, v[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(map_to_rank(smem_addr(&ctl->tmem_empty[buf]), 0));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int at = c * 16 + 2 * j;
+                        gbt::Pair t(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1]));
+                        if constexpr (BYROW) {
+                            const float2 w = *reinterpret_cast<const float2*>(col_scales + buf * 256 + half * kHalf + at);
+                            t = gbt::mul2(t, gbt::Pair(w.x, w.y));
+                        }
+                        gbt::fma2(t, s2, gbt::Pair(acc[at], acc[at + 1])).get(acc[at], acc[at + 1]);
+                    }
+                }
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int c = 0; c < kHalf; c += 64) {
+                if (y >= p.M || x + c >= p.N) continue;      // (the whole warp)
+                uint32_t w[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) w[i] = pack2<OUT>(acc[c + 2 * i], acc[c + 2 * i + 1]);
+                if (lane == 0) bulk_wait_group_read<0>();
+                __syncwarp();
+                stage_store_row(buf_at, lane, 0, w, 8);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(&tmap_c, buf_at, x + c, y);
+                    bulk_commit_group();
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    cluster_sync_all();                              // the pair's MMAs, TMEM reads and copies are all finished
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 2 * kBN);
+    } else if (warp >= 2) {
+        if (lane == 0) bulk_wait_group_read<0>();    // the stores have read their buffers
+        __syncwarp();
+    }
+}
+
+// ---------------------------------------------------------------- launches
+
+template <int OUT>
+bool prepare() {
+    return allow_shared<fp8_pair_kernel<OUT, false>>(Fp8Layout<false>::kTotal) &&
+           allow_shared<fp8_pair_kernel<OUT, true>>(Fp8Layout<true>::kTotal) &&
+           allow_shared<few_rows_kernel<true, OUT, 32>>(FewLayout<32>::kTotal) &&
+           allow_shared<few_rows_kernel<true, OUT, 128>>(FewLayout<128>::kTotal);
+}
+
+template <int OUT>
+gemm_status_t run(const gemm_fp8_plan* p, const void* A, const float* a_scales, const void* B, const float* b_scales, void* C,
+                  gbt::Queue queue) {
+    const int64_t M = p->M, N = p->N, K = p->K;
+    const bool few = M <= kTileSide && p->b_scales == GEMM_SCALE_SQUARE;
+    const int box = few && M <= 32 ? 32 : kTileSide;
+    CUtensorMap a, b, c;
+    if (!encode_map(&a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, A, M, K, K, box) ||
+        !encode_map(&b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, B, N, K, K, kTileSide))
+        return GEMM_ERR_TENSORMAP;
+    const int32_t num_kb = static_cast<int32_t>(gbt::groups_of(K));
+    const bool whole_a = num_kb % 4 == 0 && gbt::aligned(a_scales, 16), whole_b = num_kb % 4 == 0 && gbt::aligned(b_scales, 16);
+    if (few) {
+        FewParams f{};
+        f.M = static_cast<int32_t>(M);
+        f.N = static_cast<int32_t>(N);
+        f.num_kb = num_kb;
+        f.m_blocks = 1;
+        const int64_t tiles = (N + kTileSide - 1) / kTileSide;
+        f.slices = few_slices(tiles, num_kb, p->base.num_sms);
+        f.kb_per_slice = (num_kb + f.slices - 1) / f.slices;
+        f.idesc = descriptor(0, kTileSide, kTileSide);
+        f.tx_extra = p->base.tx_extra;
+        f.whole_a = whole_a;
+        f.whole_b = whole_b;
+        f.a_scales = a_scales;
+        f.b_scales = b_scales;
+        f.out = C;
+        f.error_word = p->base.error_word;
+        f.timeout_ns = p->base.timeout_ns;
+        if (box == 32)
+            return gbt::launch<few_rows_kernel<true, OUT, 32>>(tiles * f.slices, kThreads, FewLayout<32>::kTotal, queue, f.slices, a,
+                                                               b, b, f);
+        return gbt::launch<few_rows_kernel<true, OUT, 128>>(tiles * f.slices, kThreads, FewLayout<128>::kTotal, queue, f.slices, a, b,
+                                                            b, f);
+    }
+    if (!encode_map(&c, OUT == kOutF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, C, M, N, N, 32))
+        return GEMM_ERR_TENSORMAP;
+    Fp8Params f{};
+    f.M = static_cast<int32_t>(M);
+    f.N = static_cast<int32_t>(N);
+    f.num_kb = num_kb;
+    f.m_blocks = static_cast<int32_t>((M + 255) / 256);
+    const int32_t n_blocks = static_cast<int32_t>((N + 255) / 256);
+    f.num_units = f.m_blocks * n_blocks;
+    f.idesc = descriptor(0, 256, 256);
+    f.tx_extra = p->base.tx_extra;
+    f.whole_a = whole_a;
+    f.whole_b = whole_b;
+    f.a_scales = a_scales;
+    f.b_scales = b_scales;
+    f.error_word = p->base.error_word;
+    f.timeout_ns = p->base.timeout_ns;
+    // bands of eight row blocks: the 76 pairs cover about 8 x 9 tiles at a time
+    f.rd = make_raster_div(f.m_blocks, n_blocks, f.m_blocks < 8 ? f.m_blocks : 8);
+    const int pairs = p->base.num_sms / 2, grid = 2 * (f.num_units < pairs ? f.num_units : pairs);
+    if (p->b_scales == GEMM_SCALE_ROW)
+        return gbt::launch<fp8_pair_kernel<OUT, true>>(grid, kPairThreads, Fp8Layout<true>::kTotal, queue, 2, a, b, c, f);
+    return gbt::launch<fp8_pair_kernel<OUT, false>>(grid, kPairThreads, Fp8Layout<false>::kTotal, queue, 2, a, b, c, f);
+}
+
+}  // namespace
+}  // namespace gbf
+
+extern "C" {
+
+gemm_status_t gemm_fp8_plan_create(int64_t M, int64_t N, int64_t K, gemm_elem_t out, gemm_scale_t b_scales,
+                                   gemm_fp8_plan_t* plan) {
+    using namespace gbf;
+    if (!plan) return GEMM_ERR_INVALID_ARG;
+    *plan = nullptr;
+    if ((out != GEMM_ELEM_F16 && out != GEMM_ELEM_BF16) || (b_scales != GEMM_SCALE_ROW && b_scales != GEMM_SCALE_SQUARE))
+        return GEMM_ERR_UNSUPPORTED;
+    if (M < 0 || N < 0 || K < 0 || M > INT32_MAX - 256 || N > INT32_MAX - 256 || K > INT32_MAX - 128) return GEMM_ERR_INVALID_ARG;
+    if (N % 8 != 0 || K % 16 != 0) return GEMM_ERR_ALIGNMENT;
+    if ((M / 128 + 1) * (N / 128 + 1) > (int64_t{1} << 27)) return GEMM_ERR_INVALID_ARG;   // tiles in 32 bits
+    gemm_fp8_plan* p = new (std::nothrow) gemm_fp8_plan();
+    if (!p) return GEMM_ERR_OOM;
+    p->M = M;
+    p->N = N;
+    p->K = K;
+    p->out = out;
+    p->b_scales = b_scales;
+    gemm_status_t st = open_plan(&p->base);
+    if (st == GEMM_OK && !(out == GEMM_ELEM_F16 ? prepare<kOutF16>() : prepare<kOutBF16>())) {
+        close_plan(&p->base);
+        st = GEMM_ERR_LAUNCH;
+    }
+    if (st != GEMM_OK) {
+        delete p;
+        return st;
+    }
+    *plan = p;
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_fp8_run(gemm_fp8_plan_t p, const void* A, const float* a_scales, const void* B, const float* b_scales,
+                           void* C, void* stream) {
+    using namespace gbf;
+    if (!p) return GEMM_ERR_INVALID_ARG;
+    const gemm_status_t st = gbt::check_device(p->base.device);
+    if (st != GEMM_OK) return st;
+    if (p->M == 0 || p->N == 0) return GEMM_OK;
+    if (!C || (p->K > 0 && (!A || !B || !a_scales || !b_scales))) return GEMM_ERR_INVALID_ARG;
+    if (!gbt::aligned(A, 16) || !gbt::aligned(B, 16) || !gbt::aligned(C, 16) || !gbt::aligned(a_scales, 4) ||
+        !gbt::aligned(b_scales, 4))
+        return GEMM_ERR_ALIGNMENT;
+    if (p->K == 0) {
+        if (launch_zero_fill(C, p->M * p->N * 2, p->base.num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess)
+            return GEMM_OK;
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    const gbt::Queue queue{stream, p->base.device};
+    return p->out == GEMM_ELEM_F16 ? run<kOutF16>(p, A, a_scales, B, b_scales, C, queue)
+                                   : run<kOutBF16>(p, A, a_scales, B, b_scales, C, queue);
+}
+
+gemm_status_t gemm_fp8_plan_set_timeout(gemm_fp8_plan_t p, uint64_t ns) {
+    if (!p) return GEMM_ERR_INVALID_ARG;
+    p->base.timeout_ns = ns ? ns : gbf::kWaitLimitNs;
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_fp8_plan_set_wait_test(gemm_fp8_plan_t p, uint32_t extra_bytes) {
+    if (!p || extra_bytes > 4096 || (extra_bytes & 15u)) return GEMM_ERR_INVALID_ARG;
+    p->base.tx_extra = extra_bytes;
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_fp8_plan_check(gemm_fp8_plan_t p, void* stream) {
+    return p ? gbf::check_plan(&p->base, stream) : GEMM_ERR_INVALID_ARG;
+}
+
+gemm_status_t gemm_fp8_plan_destroy(gemm_fp8_plan_t p) {
+    if (!p) return GEMM_OK;
+    const gemm_status_t st = gbf::close_plan(&p->base);
+    delete p;
+    return st;
+}
+
+}  // extern "C"

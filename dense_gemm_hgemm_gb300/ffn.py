@@ -13,15 +13,21 @@ shape, type or device than the call's raises ``GemmError`` before anything is qu
         norm.backward(t, gamma, rstd, dy, dx, dgamma, dtotal=dt)
         norm.forward_fp8(x, gamma, q, scales, residual=r, total=t)
     fp8_quantize(w, wq, w_scales, block="square")
+    with Fp8Plan(M, N, K, "bf16") as product:
+        product.run(q, scales, wq, w_scales, c)
+    with GatedPlan(M, F, K, "bf16", act="silu") as gated:           # w: 2F x K, the gate's rows first
+        gated.forward(y, w, h, gate_up=gu)
+        gated.backward(y, w, gu, dh, dgu, dy, dw)
 """
 from __future__ import annotations
 
 import ctypes
 
-from . import GemmError, _check, _stream, library
-from .train import _INVALID_ARG, _UNSUPPORTED, GEMM_ELEM_F32, _elem, _elem_of, _matrix, _on_device, _Plan, _torch_types, _vector
+from . import ACTIVATIONS, GemmError, _check, _stream, library
+from .train import (_INVALID_ARG, _UNSUPPORTED, GEMM_ELEM_F32, _elem, _elem_of, _matrix, _on_device, _Plan, _torch_types,
+                    _vector)
 
-__all__ = ["GEMM_SCALE_ROW", "GEMM_SCALE_SQUARE", "SCALES", "RmsNormPlan", "fp8_quantize"]
+__all__ = ["GEMM_SCALE_ROW", "GEMM_SCALE_SQUARE", "SCALES", "RmsNormPlan", "fp8_quantize", "Fp8Plan", "GatedPlan"]
 
 GEMM_SCALE_ROW, GEMM_SCALE_SQUARE = 0, 1
 SCALES = {"row": GEMM_SCALE_ROW, "square": GEMM_SCALE_SQUARE}
@@ -39,6 +45,14 @@ def signatures():
         "gemm_rms_backward": ([vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp], i32),
         "gemm_rms_plan_destroy": ([vp], i32),
         "gemm_fp8_quantize": ([i64, i64, i32, vp, i64, i32, i32, vp, i64, vp, i64, vp], i32),
+        "gemm_fp8_plan_create": ([i64, i64, i64, i32, i32, vpp], i32),
+        "gemm_fp8_run": ([vp, vp, vp, vp, vp, vp, vp], i32),
+        "gemm_gated_plan_create": ([i64, i64, i64, i32, i32, vpp], i32),
+        "gemm_gated_forward": ([vp, vp, vp, vp, vp, vp], i32),
+        "gemm_gated_backward": ([vp, vp, vp, vp, vp, vp, vp, vp, vp], i32),
+        **{"gemm_%s_plan_%s" % (kind, call): ([vp, *more], i32) for kind in ("fp8", "gated")
+           for call, more in (("set_timeout", [ctypes.c_uint64]), ("set_wait_test", [ctypes.c_uint32]), ("check", [vp]),
+                              ("destroy", []))},
     }
 
 
@@ -64,6 +78,36 @@ def _bytes_matrix(t, rows, cols, what):
 
 def _optional(t, rows, cols, elem, what):
     return (None, 0) if t is None else _matrix(t, rows, cols, elem, what)
+
+
+def _whole(t, rows, cols, elem, what):
+    """Address of a contiguous rows x cols matrix."""
+    address, ld = _matrix(t, rows, cols, elem, what)
+    if ld != cols and rows * cols > 0:
+        raise GemmError(_INVALID_ARG, "%s: a contiguous matrix is needed" % what)
+    return address
+
+
+class _ProductPlan(_Plan):
+    """A plan of a product: its waits' limit, their test hook and their check (`_kind`: of its C functions)."""
+
+    _kind = ""
+
+    def _call(self, name, *args):
+        name = "gemm_%s_plan_%s" % (self._kind, name)
+        _check(getattr(library(), name)(self.handle, *args), name)
+
+    def set_timeout(self, ns: int) -> None:
+        """The limit of a wait in this plan's kernels, in nanoseconds (0: the default, 2e9)."""
+        self._call("set_timeout", ns)
+
+    def set_wait_test(self, extra_bytes: int) -> None:
+        """Test hook: the ring's slots wait for bytes that do not come (0: off)."""
+        self._call("set_wait_test", extra_bytes)
+
+    def check(self, stream=None) -> None:
+        """Synchronise `stream`; raise GemmError(GEMM_ERR_DEVICE_TIMEOUT) if a kernel gave up on a wait."""
+        self._call("check", _stream(stream))
 
 
 class RmsNormPlan(_Plan):
@@ -128,3 +172,62 @@ def fp8_quantize(x, q, scales, block="row", transpose: bool = False, stream=None
                       "scales")
     _check(library().gemm_fp8_quantize(rows, cols, _elem_of(x, "x"), px, ldx, kind, 1 if transpose else 0, pq, ldq, ps, lds,
                                        _stream(stream)), "gemm_fp8_quantize")
+
+
+class Fp8Plan(_ProductPlan):
+    """C = A B^T of e4m3 matrices (A M x K, B N x K) with scales, C of `dtype` ("f16" or "bf16").  A's scales go
+    by rows, B's by squares (`b_scales` "square") or by rows ("row")."""
+
+    _destroy, _kind = "gemm_fp8_plan_destroy", "fp8"
+
+    def __init__(self, M: int, N: int, K: int, dtype="bf16", b_scales="square"):
+        self.M, self.N, self.K = M, N, K
+        self._elem, self._scales = _elem(dtype), _scale_kind(b_scales)
+        self._create("gemm_fp8_plan_create", M, N, K, self._elem, self._scales)
+
+    def run(self, A, a_scales, B, b_scales, C, stream=None) -> None:
+        """C = A B^T.  All matrices contiguous."""
+        M, N, K = self.M, self.N, self.K
+        _bytes_matrix(A, M, K, "A")
+        _bytes_matrix(B, N, K, "B")
+        n = _groups(K)
+        _check(library().gemm_fp8_run(
+            self.handle, _whole(A, M, K, None, "A"), _whole(a_scales, M, n, GEMM_ELEM_F32, "a_scales"),
+            _whole(B, N, K, None, "B"),
+            _whole(b_scales, _groups(N) if self._scales == GEMM_SCALE_SQUARE else N, n, GEMM_ELEM_F32, "b_scales"),
+            _whole(C, M, N, self._elem, "C"), _stream(stream)), "gemm_fp8_run")
+
+
+class GatedPlan(_ProductPlan):
+    """H = act(X Wg^T) * (X Wu^T) with X M x K, W = [Wg; Wu] 2F x K and H M x F, all of `dtype` ("f16" or "bf16");
+    act: "silu", "gelu", "relu" or "none"."""
+
+    _destroy, _kind = "gemm_gated_plan_destroy", "gated"
+
+    def __init__(self, M: int, F: int, K: int, dtype="bf16", act="silu"):
+        self.M, self.F, self.K = M, F, K
+        self._elem = _elem(dtype)
+        if isinstance(act, str) and act not in ACTIVATIONS:
+            raise GemmError(_UNSUPPORTED, "activation %r" % act)
+        self._create("gemm_gated_plan_create", M, F, K, self._elem, ACTIVATIONS[act] if isinstance(act, str) else int(act))
+
+    def _matrix(self, t, rows, cols, what, may_be_none=False):
+        if t is None and may_be_none:
+            return None
+        if t is None:
+            raise GemmError(_INVALID_ARG, "%s: a tensor is needed" % what)
+        return _whole(t, rows, cols, self._elem, what)
+
+    def forward(self, X, W, H, gate_up=None, stream=None) -> None:
+        """H; and both products side by side (M x 2F), for backward, where `gate_up` is given."""
+        M, F, K, m = self.M, self.F, self.K, self._matrix
+        _check(library().gemm_gated_forward(self.handle, m(X, M, K, "X"), m(W, 2 * F, K, "W"), m(H, M, F, "H"),
+                                            m(gate_up, M, 2 * F, "gate_up", True), _stream(stream)), "gemm_gated_forward")
+
+    def backward(self, X, W, gate_up, dH, dgate_up, dX=None, dW=None, stream=None) -> None:
+        """dgate_up (which may be gate_up) from dH, and from it dX and dW, each optional (W and X may be None with them)."""
+        M, F, K, m = self.M, self.F, self.K, self._matrix
+        _check(library().gemm_gated_backward(
+            self.handle, m(X, M, K, "X", dW is None), m(W, 2 * F, K, "W", dX is None), m(gate_up, M, 2 * F, "gate_up"),
+            m(dH, M, F, "dH"), m(dgate_up, M, 2 * F, "dgate_up"), m(dX, M, K, "dX", True), m(dW, 2 * F, K, "dW", True),
+            _stream(stream)), "gemm_gated_backward")

@@ -6,6 +6,8 @@
  *                 rows' type or in 8 bits with scales, and its gradients
  *   8 bits        a matrix as e4m3 numbers with a scale for each 128 elements of a
  *                 row, or for each 128 x 128 elements; as it stands or transposed
+ *   8-bit product C = A * B^T of such matrices
+ *   gated product H = act(X * Wg^T) * (X * Wu^T), and its gradients
  *
  * Types, ownership, threading and errors as in gemm.h and gemm_train.h: matrices
  * are row-major; calls are asynchronous on the caller's stream, allocate nothing,
@@ -110,6 +112,76 @@ gemm_status_t gemm_rms_plan_destroy(gemm_rms_plan_t plan);
 gemm_status_t gemm_fp8_quantize(int64_t rows, int64_t cols, gemm_elem_t elem, const void *x,
                                 int64_t ldx, gemm_scale_t kind, int32_t transpose, void *q,
                                 int64_t ldq, float *scales, int64_t lds, void *stream);
+
+/* ------------------------------------------------------------------ 8-bit product */
+
+typedef struct gemm_fp8_plan *gemm_fp8_plan_t;
+
+/*
+ * A plan for C[i][j] = sum over groups g of a_scales[i][g] * sb(j, g) * sum over k in g of
+ * A[i][k] * B[j][k], with A M x K and B N x K (e4m3, K-contiguous) and C M x N of `out`
+ * (GEMM_ELEM_F16 or GEMM_ELEM_BF16).  A's scales go by rows, B's by b_scales: squares
+ * (weights) or rows (where both are activations).  K has to be a multiple of 16 and N of
+ * 8 (GEMM_ERR_ALIGNMENT).
+ */
+gemm_status_t gemm_fp8_plan_create(int64_t M, int64_t N, int64_t K, gemm_elem_t out,
+                                   gemm_scale_t b_scales, gemm_fp8_plan_t *plan);
+
+/*
+ * Queue the product.  A, B and C contiguous and 16-byte aligned; scales contiguous
+ * (M x ceil(K/128), and N or ceil(N/128) x ceil(K/128)), 4-byte aligned (16-byte aligned
+ * ones are faster).  K == 0 writes zeros.  C overlaps no operand.
+ */
+gemm_status_t gemm_fp8_run(gemm_fp8_plan_t plan, const void *A, const float *a_scales, const void *B,
+                           const float *b_scales, void *C, void *stream);
+
+/*
+ * As gemm_plan_set_timeout, gemm_plan_set_wait_test, gemm_plan_check and
+ * gemm_plan_destroy of gemm.h.
+ */
+gemm_status_t gemm_fp8_plan_set_timeout(gemm_fp8_plan_t plan, uint64_t ns);
+gemm_status_t gemm_fp8_plan_set_wait_test(gemm_fp8_plan_t plan, uint32_t extra_bytes);
+gemm_status_t gemm_fp8_plan_check(gemm_fp8_plan_t plan, void *stream);
+gemm_status_t gemm_fp8_plan_destroy(gemm_fp8_plan_t plan);
+
+/* ------------------------------------------------------------------ gated product */
+
+typedef struct gemm_gated_plan *gemm_gated_plan_t;
+
+/*
+ * A plan for H = act(X * Wg^T) * (X * Wu^T): X is M x K, W = [Wg; Wu] is 2F x K (rows
+ * 0 .. F-1 the gate's weights, F .. 2F-1 the other's) and H is M x F, all of `elem`
+ * (GEMM_ELEM_F16 or GEMM_ELEM_BF16) and contiguous.  F and K have to be multiples of 8
+ * (GEMM_ERR_ALIGNMENT).  act: GEMM_ACT_NONE, _RELU, _GELU or _SILU.
+ */
+gemm_status_t gemm_gated_plan_create(int64_t M, int64_t F, int64_t K, gemm_elem_t elem,
+                                     gemm_activation_t act, gemm_gated_plan_t *plan);
+
+/*
+ * Queue H.  gate_up (M x 2F) receives both products side by side, rounded to the type:
+ * what the backward call takes; NULL: not kept.  H itself is of the unrounded products.
+ * K == 0 gives zeros.  Pointers 16-byte aligned; outputs overlap no operand.
+ */
+gemm_status_t gemm_gated_forward(gemm_gated_plan_t plan, const void *X, const void *W, void *H,
+                                 void *gate_up, void *stream);
+
+/*
+ * Gradients, with g and u the halves of gate_up's rows:
+ *     dgate_up = [dH * u * act'(g), dH * act(g)]      (M x 2F, rounded to the type)
+ *     dX = dgate_up * W                               (M x K)
+ *     dW = dgate_up^T * X                             (2F x K)
+ * dX and dW may each be NULL (not computed; W and X are then not read).  dgate_up may
+ * be gate_up.  dX and dW are products of gemm.h over dgate_up.  act'(0) of ReLU is 0.
+ */
+gemm_status_t gemm_gated_backward(gemm_gated_plan_t plan, const void *X, const void *W,
+                                  const void *gate_up, const void *dH, void *dgate_up, void *dX,
+                                  void *dW, void *stream);
+
+/* As for gemm_fp8_plan_t (the backward products' waits included). */
+gemm_status_t gemm_gated_plan_set_timeout(gemm_gated_plan_t plan, uint64_t ns);
+gemm_status_t gemm_gated_plan_set_wait_test(gemm_gated_plan_t plan, uint32_t extra_bytes);
+gemm_status_t gemm_gated_plan_check(gemm_gated_plan_t plan, void *stream);
+gemm_status_t gemm_gated_plan_destroy(gemm_gated_plan_t plan);
 
 #ifdef __cplusplus
 }

@@ -112,3 +112,48 @@ def act(g, kind):
     if kind == "relu":
         return g.clamp_min(0), (g > 0).double()
     return g, torch.ones_like(g)
+
+
+def mma_error(k, step):
+    """The error of a sum of k products by tensor cores, over the sum of the magnitudes: each instruction adds `step`
+    products and the sum so far, and loses at worst a whole unit (2 U) at each of its additions; the products are exact.
+    An instruction aligns its terms and adds them at once, so the running sum is cut once an instruction."""
+    return (k / step + step) * 2 * U
+
+
+def fp8_product(a, a_scales, b, b_scales, square):
+    """(C, bound before rounding) of an 8-bit product: per group of 128 an exact-product sum, then the scales' product
+    (U), a fused multiply-add (U) and a sum over the groups."""
+    x, w = stands_for(a, a_scales, False), stands_for(b, b_scales, square)
+    size = x.abs() @ w.abs().t()
+    return x @ w.t(), (mma_error(GROUP, 32) + (groups(a.shape[1]) + 4) * U) * size
+
+
+LIPSCHITZ = 1.13      # of the activations
+ACT_ERROR = 2.0 ** -18    # relative, of the fp32 activation with its fast exponential and quotient, for sizes up to 90
+# In the lower tails exp and erfc fall below the smallest normal fp32 number (at g = -30 erfc is 1e-197), which no
+# fp32 value can stand for: what is below 2^-126 may be taken as zero, and g (up to 2^7) multiplies it.
+ACT_TINY = 2.0 ** -119
+
+
+def gated_forward(x, w, kind):
+    """(H, bound, gate_up, bound) before rounding."""
+    x, w = x.double(), w.double()
+    gu, size = x @ w.t(), x.abs() @ w.abs().t()
+    off = mma_error(x.shape[1], 16) * size
+    f = w.shape[0] // 2
+    g, u, dg, du = gu[:, :f], gu[:, f:], off[:, :f], off[:, f:]
+    a = act(g, kind)[0]
+    bound = LIPSCHITZ * dg * (u.abs() + du) + a.abs() * du + ACT_ERROR * (a * u).abs() + ACT_TINY * u.abs()
+    return a * u, bound, gu, off
+
+
+def gate_gradient(gate_up, dh, kind):
+    """(dgate_up, bound before rounding)"""
+    f = dh.shape[1]
+    g, u, dh = gate_up.double()[:, :f], gate_up.double()[:, f:], dh.double()
+    a, slope = act(g, kind)
+    want = torch.cat([dh * u * slope, dh * a], 1)
+    # act' is a sum of two terms, each of at most 1.2 in size
+    bound = torch.cat([(dh * u).abs() * (2.5 * ACT_ERROR + ACT_TINY), (dh * a).abs() * ACT_ERROR + dh.abs() * ACT_TINY], 1)
+    return want, bound

@@ -29,6 +29,22 @@ def test_every_declared_function_has_a_signature(gemm_lib):
     ("gemm_rms_plan_create", (2 ** 31, 8, 0, 0), 1),
     ("gemm_rms_plan_create", (4, 2 ** 30 + 1, 0, 0), 1),
     ("gemm_rms_plan_create", (4, 8, 0, 2), None),
+    ("gemm_fp8_plan_create", (4, 8, 16, 2, 0), 2),          # fp32 results
+    ("gemm_fp8_plan_create", (4, 8, 16, 0, 2), 2),          # kind of scales
+    ("gemm_fp8_plan_create", (-4, 8, 16, 0, 0), 1),
+    ("gemm_fp8_plan_create", (4, 8, 2 ** 31 - 16, 0, 0), 1),
+    ("gemm_fp8_plan_create", (4, 12, 16, 0, 0), 3),
+    ("gemm_fp8_plan_create", (4, 8, 24, 0, 0), 3),
+    ("gemm_fp8_plan_create", (2 ** 30, 2 ** 30, 16, 0, 0), 1),
+    ("gemm_fp8_plan_create", (4, 8, 16, 1, 1), None),
+    ("gemm_gated_plan_create", (4, 8, 8, 2, 3), 2),         # fp32 elements
+    ("gemm_gated_plan_create", (4, 8, 8, 0, 4), 2),         # unknown activation
+    ("gemm_gated_plan_create", (4, -8, 8, 0, 3), 1),
+    ("gemm_gated_plan_create", (4, 2 ** 30, 8, 0, 3), 1),
+    ("gemm_gated_plan_create", (2 ** 28, 2 ** 20, 8, 0, 3), 1),
+    ("gemm_gated_plan_create", (4, 12, 8, 0, 3), 3),
+    ("gemm_gated_plan_create", (4, 8, 12, 0, 3), 3),
+    ("gemm_gated_plan_create", (4, 8, 8, 1, 3), None),
 ])
 def test_plan_creation_validates_first(gemm_lib, name, args, expect):
     h = ctypes.c_void_p()
@@ -48,6 +64,14 @@ def test_null_handles(gemm_lib):
     assert lib.gemm_rms_forward_fp8(None, 0, None, 0, None, 0, None, 0.0, None, 0, None, 0, None, 0, None, None) == 1
     assert lib.gemm_rms_backward(None, 0, None, 0, None, None, None, 0, None, 0, None, 0, None, None) == 1
     assert lib.gemm_rms_plan_destroy(None) == 0
+    assert lib.gemm_fp8_run(None, None, None, None, None, None, None) == 1
+    assert lib.gemm_gated_forward(None, None, None, None, None, None) == 1
+    assert lib.gemm_gated_backward(None, None, None, None, None, None, None, None, None) == 1
+    for kind in ("fp8", "gated"):
+        assert getattr(lib, "gemm_%s_plan_set_timeout" % kind)(None, 1) == 1
+        assert getattr(lib, "gemm_%s_plan_set_wait_test" % kind)(None, 16) == 1
+        assert getattr(lib, "gemm_%s_plan_check" % kind)(None, None) == 1
+        assert getattr(lib, "gemm_%s_plan_destroy" % kind)(None) == 0
 
 
 @pytest.mark.parametrize("args,expect", [
@@ -72,6 +96,8 @@ def test_conversion_validates_first(gemm_lib, args, expect):
 @pytest.mark.skipif(HAS_GPU, reason="checks the no-device path")
 def test_plans_without_a_gpu_raise(gemm_lib):
     for make, status in ((lambda: gemm_lib.RmsNormPlan(4, 8), 4), (lambda: gemm_lib.RmsNormPlan(4, 8, "i8"), 2),
+                         (lambda: gemm_lib.Fp8Plan(4, 8, 16), 4), (lambda: gemm_lib.Fp8Plan(4, 8, 16, b_scales="column"), 2),
+                         (lambda: gemm_lib.GatedPlan(4, 8, 8), 4), (lambda: gemm_lib.GatedPlan(4, 8, 8, act="tanh"), 2),
                          (lambda: gemm_lib.fp8_quantize(*[torch.zeros(4, 8)] * 3), 1)):
         with pytest.raises(gemm_lib.GemmError) as e:
             make()
