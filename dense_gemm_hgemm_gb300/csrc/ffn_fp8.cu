@@ -16,7 +16,11 @@ namespace gbf {
 namespace {
 
 constexpr int kSumWarps = 8;                      // of a CTA
-constexpr int kPairThreads = 64 + 32 * kSumWarps;
+constexpr int kFirstSumWarp = 4;                  // after the copies', the MMAs' and the column scales' two
+constexpr int kPairThreads = 32 * (kFirstSumWarp + kSumWarps);
+// Registers of a thread: 168 at the launch; the first warpgroup's go to the other two.
+constexpr int kLaunchRegisters = 168, kFewRegisters = 88, kSumRegisters = 208;
+static_assert(128 * kFewRegisters + 256 * kSumRegisters <= kPairThreads * kLaunchRegisters, "registers of the block");
 
 // BYROW: B's scales go by rows.
 template <bool BYROW>
@@ -26,7 +30,7 @@ struct Fp8Layout {
     static constexpr int kRing = kStages * kStageBytes;
     static constexpr int kStoreBuf = 32 * kRowBytes;
     static constexpr int kStaging = kSumWarps * kStoreBuf;
-    static constexpr int kScales = BYROW ? 2 * 256 * 4 : 0;
+    static constexpr int kScales = BYROW ? 4 * 256 * 4 : 0;
     static constexpr int kTotal = 1024 + kRing + kStaging + 256 + kScales;
     static_assert(kTotal <= 232448, "exceeds the 227 KiB a CTA may use");
 };
@@ -35,7 +39,6 @@ struct Fp8Params {
     int32_t M, N;
     int32_t num_kb, m_blocks, num_units;
     uint32_t idesc, tx_extra;
-    bool whole_a, whole_b;                        // the scales' rows move in fours
     const float* a_scales;
     const float* b_scales;
     int32_t* error_word;
@@ -43,22 +46,24 @@ struct Fp8Params {
     RasterDiv rd;
 };
 
-// Whether `ok` holds in all of the four warps that meet at this barrier; what they wrote to shared
-// memory before is there after it.
-__device__ __forceinline__ bool all_of_half(int barrier, bool ok) {
-    uint32_t all;
-    asm volatile(
-        "{\n\t"
-        ".reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.red.and.pred q, %2, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t"
-        "}"
-        : "=r"(all)
-        : "r"(ok ? 1u : 0u), "r"(barrier)
-        : "memory");
-    return all != 0;
+// One scale on its way to shared memory; and this thread's arrival on a barrier once all that it
+// has asked for so far is there.
+__device__ __forceinline__ void fetch_scale(uint32_t to, const float* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
+__device__ __forceinline__ void arrive_when_fetched(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+template <int STAGES>
+struct Fp8Ctl {
+    uint64_t full[STAGES], empty[STAGES];
+    uint64_t tmem_full[2][2], tmem_empty[2][2];      // [turn][half of the columns]
+    uint64_t scales_full[4], scales_empty[4];        // BYROW
+    uint64_t drain;
+    uint32_t tmem_base;
+    int32_t abort;
+};
 
 // Many rows: a pair of SMs computes 256 x 256 of C, as the plain product's pair does
 // (gemm_kernel_2cta.cuh).  The tensor cores know no scales, so the sum over each 128 elements of
@@ -66,21 +71,25 @@ __device__ __forceinline__ bool all_of_half(int barrier, bool ok) {
 // multiply by the scales of its row and column and add to fp32 sums in registers, 128 columns a
 // thread.  One such step is 512 cycles of the tensor cores; a thread's share is 128 accumulators
 // from TMEM and 64 fused multiply-adds of two.
+// The two halves of the columns are MMAs and barriers of their own: from the end of a half's
+// MMAs to the next ones into its accumulators the tensor cores have three other halves to do,
+// which hides the way to the warps and back.  So that a half is 128 neighbouring columns
+// (one square of scales), each CTA brings 64 rows of B for each of them.
 template <int OUT, bool BYROW>
 __global__ void __launch_bounds__(kPairThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                     const __grid_constant__ CUtensorMap tmap_c, const Fp8Params p) {
     using L = Fp8Layout<BYROW>;
     constexpr int kStages = L::kStages;
-    constexpr int kBN = 256, kHalf = 128;
+    constexpr int kBN = 256, kHalf = 128, kStep = BYROW ? 16 : 16;
     constexpr uint32_t kPairTx = 2 * L::kStageBytes;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     const uint32_t ring = smem_addr(smem), ring_b = ring + kStages * kTileSlot;
     const uint32_t staging = ring + L::kRing;
-    SharedCtl<kStages>* ctl = reinterpret_cast<SharedCtl<kStages>*>(smem + L::kRing + L::kStaging);
-    float* col_scales = reinterpret_cast<float*>(smem + L::kRing + L::kStaging + 256);   // [2][256]
+    Fp8Ctl<kStages>* ctl = reinterpret_cast<Fp8Ctl<kStages>*>(smem + L::kRing + L::kStaging);
+    const uint32_t col_scales = staging + L::kStaging + 256;      // BYROW: [4][256] fp32, of four steps in turn
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / 32, 0);
     const int lane = static_cast<int>(threadIdx.x) & 31;
@@ -96,9 +105,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_init(smem_addr(&ctl->full[s]), 1);
             mbar_init(smem_addr(&ctl->empty[s]), 1);
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(smem_addr(&ctl->tmem_full[b]), 1);
-            mbar_init(smem_addr(&ctl->tmem_empty[b]), 2 * kSumWarps);
+        for (int b = 0; b < 4; ++b) {
+            mbar_init(smem_addr(&ctl->tmem_full[b >> 1][b & 1]), 1);
+            mbar_init(smem_addr(&ctl->tmem_empty[b >> 1][b & 1]), kSumWarps);   // four of each CTA
+        }
+        for (int b = 0; b < 4; ++b) {
+            mbar_init(smem_addr(&ctl->scales_full[b]), 64);
+            mbar_init(smem_addr(&ctl->scales_empty[b]), kSumWarps);
         }
         mbar_init(smem_addr(&ctl->drain), 1);
         ctl->abort = 0;
@@ -123,81 +136,118 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     grid_dependency_wait();
     grid_launch_dependents();
 
-    if (warp == 0) {
-        if (elect_one_sync()) {
-            int stage = 0, issued = 0;
-            uint32_t phase = 0;
+    // (each warpgroup as one: the four warps of a group change their registers together)
+    if (warp < kFirstSumWarp) {
+        fewer_registers<kFewRegisters>();
+        if (warp == 0) {
+            if (elect_one_sync()) {
+                int stage = 0, issued = 0;
+                uint32_t phase = 0;
+                bool ok = true;
+                for (int32_t u = pair; ok && u < p.num_units; u += npairs) {
+                    int32_t m_blk, n_blk;
+                    raster_tile_fast(p.m_blocks, p.rd, u, &m_blk, &n_blk);
+                    const int32_t a_row = (2 * m_blk + static_cast<int32_t>(rank)) * kBM;
+                    const int32_t b_row = n_blk * kBN + static_cast<int32_t>(rank) * (kHalf / 2);
+                    for (int32_t kb = 0; kb < p.num_kb; ++kb) {
+                        if (issued >= kStages &&
+                            !wait_phase(smem_addr(&ctl->empty[stage]), phase ^ 1u, watch, kSiteProducerEmpty)) {
+                            ok = false;
+                            break;
+                        }
+                        const uint32_t full = smem_addr(&ctl->full[stage]);
+                        if (leader) mbar_arrive_expect_tx(full, kPairTx + p.tx_extra);
+                        const uint32_t full_lead = map_to_rank(full, 0);
+                        tma_load_2d_pair(ring + stage * kTileSlot, &tmap_a, full_lead, kb * kRowBytes, a_row);
+                        tma_load_2d_pair(ring_b + stage * kTileSlot, &tmap_b, full_lead, kb * kRowBytes, b_row);
+                        tma_load_2d_pair(ring_b + stage * kTileSlot + kTileSlot / 2, &tmap_b, full_lead, kb * kRowBytes,
+                                         b_row + kHalf);
+                        issued = issued < kStages ? issued + 1 : kStages;
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+                // both CTAs' copies count on the leader's barriers: they land before the pair can leave
+                for (int i = 0; i < issued; ++i) {
+                    if (--stage < 0) {
+                        stage = kStages - 1;
+                        phase ^= 1u;
+                    }
+                    if (leader) wait_phase_unwind(smem_addr(&ctl->full[stage]), phase, 100000000ull);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            if (leader && elect_one_sync()) {
+                int stage = 0;
+                uint32_t phase = 0, turn = 0;
+                bool ok = true;
+                for (int32_t u = pair; ok && u < p.num_units; u += npairs) {
+                    for (int32_t kb = 0; ok && kb < p.num_kb; ++kb, ++turn) {
+                        const uint32_t buf = turn & 1u;
+                        ok = wait_phase(smem_addr(&ctl->full[stage]), phase, watch, kSiteMmaFull);
+                        const uint64_t a_desc = sw128_kmajor_desc(ring + stage * kTileSlot);
+                        const uint64_t b_desc = sw128_kmajor_desc(ring_b + stage * kTileSlot);
+#pragma unroll
+                        for (uint32_t half = 0; half < 2; ++half) {
+                            if (ok && turn >= 2)
+                                ok = wait_phase_cluster(smem_addr(&ctl->tmem_empty[buf][half]), ((turn >> 1) & 1u) ^ 1u, watch,
+                                                        kSiteMmaTmemEmpty);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                umma_f8_pair(tmem_base + buf * kBN + half * kHalf, a_desc + 2 * k,
+                                             b_desc + half * (kTileSlot / 2 >> 4) + 2 * k, p.idesc, k > 0 ? 1u : 0u);
+                            umma_commit_pair(smem_addr(&ctl->tmem_full[buf][half]), 3);
+                        }
+                        if (!ok) break;
+                        umma_commit_pair(smem_addr(&ctl->empty[stage]), 3);
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+                umma_commit_pair(smem_addr(&ctl->drain), 1);
+                wait_phase_unwind(smem_addr(&ctl->drain), 0, 100000000ull);
+            }
+            __syncwarp();
+        } else if constexpr (BYROW) {
+            // the scales of the tile's columns, four a thread, up to four steps ahead
+            const int first = static_cast<int>(threadIdx.x) - 64;
+            uint32_t turn = 0;
             bool ok = true;
             for (int32_t u = pair; ok && u < p.num_units; u += npairs) {
                 int32_t m_blk, n_blk;
                 raster_tile_fast(p.m_blocks, p.rd, u, &m_blk, &n_blk);
-                const int32_t a_row = (2 * m_blk + static_cast<int32_t>(rank)) * kBM;
-                const int32_t b_row = (2 * n_blk + static_cast<int32_t>(rank)) * kHalf;
-                for (int32_t kb = 0; kb < p.num_kb; ++kb) {
-                    if (issued >= kStages &&
-                        !wait_phase(smem_addr(&ctl->empty[stage]), phase ^ 1u, watch, kSiteProducerEmpty)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t full = smem_addr(&ctl->full[stage]);
-                    if (leader) mbar_arrive_expect_tx(full, kPairTx + p.tx_extra);
-                    const uint32_t full_lead = map_to_rank(full, 0);
-                    tma_load_2d_pair(ring + stage * kTileSlot, &tmap_a, full_lead, kb * kRowBytes, a_row);
-                    tma_load_2d_pair(ring_b + stage * kTileSlot, &tmap_b, full_lead, kb * kRowBytes, b_row);
-                    issued = issued < kStages ? issued + 1 : kStages;
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-            }
-            // both CTAs' copies count on the leader's barriers: they land before the pair can leave
-            for (int i = 0; i < issued; ++i) {
-                if (--stage < 0) {
-                    stage = kStages - 1;
-                    phase ^= 1u;
-                }
-                if (leader) wait_phase_unwind(smem_addr(&ctl->full[stage]), phase, 100000000ull);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (leader && elect_one_sync()) {
-            int stage = 0;
-            uint32_t phase = 0, turn = 0;
-            bool ok = true;
-            for (int32_t u = pair; ok && u < p.num_units; u += npairs) {
-                for (int32_t kb = 0; kb < p.num_kb; ++kb, ++turn) {
-                    const uint32_t buf = turn & 1u;
-                    if ((turn >= 2 && !wait_phase_cluster(smem_addr(&ctl->tmem_empty[buf]), ((turn >> 1) & 1u) ^ 1u, watch,
-                                                          kSiteMmaTmemEmpty)) ||
-                        !wait_phase(smem_addr(&ctl->full[stage]), phase, watch, kSiteMmaFull)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t a_desc = sw128_kmajor_desc(ring + stage * kTileSlot);
-                    const uint64_t b_desc = sw128_kmajor_desc(ring_b + stage * kTileSlot);
+                const float* from[4];                    // (columns outside C take the last one's)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_f8_pair(tmem_base + buf * kBN, a_desc + 2 * k, b_desc + 2 * k, p.idesc, k > 0 ? 1u : 0u);
-                    umma_commit_pair(smem_addr(&ctl->tmem_full[buf]), 3);
-                    umma_commit_pair(smem_addr(&ctl->empty[stage]), 3);
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
+                for (int i = 0; i < 4; ++i)
+                    from[i] = p.b_scales + static_cast<int64_t>(min(n_blk * kBN + first + 64 * i, p.N - 1)) * p.num_kb;
+                for (int32_t kb = 0; kb < p.num_kb; ++kb, ++turn) {
+                    const uint32_t slot = turn & 3u;
+                    if (turn >= 4 && !wait_phase(smem_addr(&ctl->scales_empty[slot]), ((turn >> 2) & 1u) ^ 1u, watch,
+                                                 kSiteProducerEmpty)) {
+                        ok = false;
+                        break;
                     }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        fetch_scale(col_scales + (slot * kBN + static_cast<uint32_t>(first + 64 * i)) * 4, from[i] + kb);
+                    arrive_when_fetched(smem_addr(&ctl->scales_full[slot]));
                 }
             }
-            umma_commit_pair(smem_addr(&ctl->drain), 1);
-            wait_phase_unwind(smem_addr(&ctl->drain), 0, 100000000ull);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
         }
-        __syncwarp();
     } else {
-        const int quad = warp & 3, half = (warp - 2) >> 2;
-        const int column = half * kHalf + ((static_cast<int>(threadIdx.x) - 64) & (kHalf - 1));   // of the tile, BYROW
+        more_registers<kSumRegisters>();
+        const int quad = warp & 3, half = (warp - kFirstSumWarp) >> 2;
         const uint32_t acc_at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(half * kHalf);
-        const uint32_t buf_at = staging + static_cast<uint32_t>((warp - 2) * L::kStoreBuf);
+        const uint32_t buf_at = staging + static_cast<uint32_t>((warp - kFirstSumWarp) * L::kStoreBuf);
         uint32_t turn = 0;
         bool ok = true;
         for (int32_t u = pair; ok && u < p.num_units; u += npairs) {
@@ -208,51 +258,71 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             float acc[kHalf];
 #pragma unroll
             for (int c = 0; c < kHalf; ++c) acc[c] = 0.f;
+            // (rows and columns outside C take the last one's scales, and are not stored)
             ScaleRow sa, sb;
-            sa.begin(row < p.M ? p.a_scales + static_cast<int64_t>(row) * p.num_kb : nullptr, 0, p.num_kb, p.whole_a);
-            if constexpr (BYROW) {
-                const int32_t col = n_blk * kBN + column;
-                sb.begin(col < p.N ? p.b_scales + static_cast<int64_t>(col) * p.num_kb : nullptr, 0, p.num_kb, p.whole_b);
-            } else {
-                sb.begin(x < p.N ? p.b_scales + static_cast<int64_t>(x / kHalf) * p.num_kb : nullptr, 0, p.num_kb, p.whole_b);
-            }
+            sa.begin(p.a_scales + static_cast<int64_t>(min(row, p.M - 1)) * p.num_kb, 0);
+            if constexpr (!BYROW) sb.begin(p.b_scales + static_cast<int64_t>(min(x, p.N - 1) / kHalf) * p.num_kb, 0);
             for (int32_t kb = 0; kb < p.num_kb; ++kb, ++turn) {
                 const uint32_t buf = turn & 1u;
-                float s = sa.get(kb, 0, p.num_kb, p.whole_a);
-                const float b = sb.get(kb, 0, p.num_kb, p.whole_b);
+                float s = sa.get(kb + 1 < p.num_kb);
                 if constexpr (BYROW) {
-                    // (the reads of this buffer, two steps back, ended before the last step's barrier)
-                    col_scales[buf * 256 + column] = b;
+                    ok = wait_phase(smem_addr(&ctl->scales_full[turn & 3u]), (turn >> 2) & 1u, watch, kSiteEpiTmemFull);
                 } else {
-                    s *= b;
+                    s *= sb.get(kb + 1 < p.num_kb);
                 }
-                ok = wait_phase(smem_addr(&ctl->tmem_full[buf]), (turn >> 1) & 1u, watch, kSiteEpiTmemFull);
-                if constexpr (BYROW) ok = all_of_half(1 + half, ok);   // (and its warps leave together)
+                const gbt::Pair s2(s, s);
+                // BYROW: the products of both scales for a step's columns, made while the sums before them arrive
+                gbt::Pair w[2][kStep / 2];
+                const uint32_t scales_at = col_scales + ((turn & 3u) * kBN + static_cast<uint32_t>(half * kHalf)) * 4;
+                float4 f[kStep / 4];
+                const auto read_scales = [&](int c) {
+#pragma unroll
+                    for (int j = 0; j < kStep / 4; ++j)
+                        f[j] = ld_shared_f4(scales_at + static_cast<uint32_t>((c * kStep + 4 * j) * 4));
+                };
+                const auto join_scales = [&](int c) {
+#pragma unroll
+                    for (int j = 0; j < kStep / 4; ++j) {
+                        w[c & 1][2 * j] = gbt::mul2(gbt::Pair(f[j].x, f[j].y), s2);
+                        w[c & 1][2 * j + 1] = gbt::mul2(gbt::Pair(f[j].z, f[j].w), s2);
+                    }
+                };
+                if constexpr (BYROW) {
+                    if (ok) {
+                        read_scales(0);
+                        join_scales(0);
+                        read_scales(1);
+                    }
+                }
+                ok = ok && wait_phase(smem_addr(&ctl->tmem_full[buf][half]), (turn >> 1) & 1u, watch, kSiteEpiTmemFull);
                 if (!ok) break;
                 tc_fence_after();
-                const gbt::Pair s2(s, s);
-                uint32_t v[2][16];
-                tmem_ld_32x32b_x16(acc_at + buf * kBN, v[0]);
+                uint32_t v[2][kStep];
+                tmem_read(acc_at + buf * kBN, v[0]);
 #pragma unroll
-                for (int c = 0; c < kHalf / 16; ++c) {
-                    tmem_ld_wait16(v[c & 1]);
-                    if (c + 1 < kHalf / 16) {
-                        tmem_ld_32x32b_x16(acc_at + buf * kBN + (c + 1) * 16, v[(c + 1) & 1]);
+                for (int c = 0; c < kHalf / kStep; ++c) {
+                    tmem_arrived(v[c & 1]);
+                    if (c + 1 < kHalf / kStep) {
+                        tmem_read(acc_at + buf * kBN + (c + 1) * kStep, v[(c + 1) & 1]);
                     } else {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_remote(map_to_rank(smem_addr(&ctl->tmem_empty[buf]), 0));
+                        if (lane == 0) arrive_leader(smem_addr(&ctl->tmem_empty[buf][half]));
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int at = c * 16 + 2 * j;
-                        gbt::Pair t(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1]));
-                        if constexpr (BYROW) {
-                            const float2 w = *reinterpret_cast<const float2*>(col_scales + buf * 256 + half * kHalf + at);
-                            t = gbt::mul2(t, gbt::Pair(w.x, w.y));
-                        }
-                        gbt::fma2(t, s2, gbt::Pair(acc[at], acc[at + 1])).get(acc[at], acc[at + 1]);
+                    for (int j = 0; j < kStep; j += 2) {
+                        const int at = c * kStep + j;
+                        const gbt::Pair t(__uint_as_float(v[c & 1][j]), __uint_as_float(v[c & 1][j + 1]));
+                        gbt::fma2(t, BYROW ? w[c & 1][j / 2] : s2, gbt::Pair(acc[at], acc[at + 1])).get(acc[at], acc[at + 1]);
                     }
+                    if constexpr (BYROW) {
+                        if (c + 1 < kHalf / kStep) join_scales(c + 1);
+                        if (c + 2 < kHalf / kStep) read_scales(c + 2);
+                    }
+                }
+                if constexpr (BYROW) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&ctl->scales_empty[turn & 3u]));
                 }
             }
             if (!ok) break;
@@ -280,7 +350,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, 2 * kBN);
-    } else if (warp >= 2) {
+    } else if (warp >= kFirstSumWarp) {
         if (lane == 0) bulk_wait_group_read<0>();    // the stores have read their buffers
         __syncwarp();
     }
@@ -304,10 +374,9 @@ gemm_status_t run(const gemm_fp8_plan* p, const void* A, const float* a_scales, 
     const int box = few && M <= 32 ? 32 : kTileSide;
     CUtensorMap a, b, c;
     if (!encode_map(&a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, A, M, K, K, box) ||
-        !encode_map(&b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, B, N, K, K, kTileSide))
+        !encode_map(&b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, B, N, K, K, few ? kTileSide : kTileSide / 2))
         return GEMM_ERR_TENSORMAP;
     const int32_t num_kb = static_cast<int32_t>(gbt::groups_of(K));
-    const bool whole_a = num_kb % 4 == 0 && gbt::aligned(a_scales, 16), whole_b = num_kb % 4 == 0 && gbt::aligned(b_scales, 16);
     if (few) {
         FewParams f{};
         f.M = static_cast<int32_t>(M);
@@ -319,8 +388,6 @@ gemm_status_t run(const gemm_fp8_plan* p, const void* A, const float* a_scales, 
         f.kb_per_slice = (num_kb + f.slices - 1) / f.slices;
         f.idesc = descriptor(0, kTileSide, kTileSide);
         f.tx_extra = p->base.tx_extra;
-        f.whole_a = whole_a;
-        f.whole_b = whole_b;
         f.a_scales = a_scales;
         f.b_scales = b_scales;
         f.out = C;
@@ -341,10 +408,8 @@ gemm_status_t run(const gemm_fp8_plan* p, const void* A, const float* a_scales, 
     f.m_blocks = static_cast<int32_t>((M + 255) / 256);
     const int32_t n_blocks = static_cast<int32_t>((N + 255) / 256);
     f.num_units = f.m_blocks * n_blocks;
-    f.idesc = descriptor(0, 256, 256);
+    f.idesc = descriptor(0, 256, 128);
     f.tx_extra = p->base.tx_extra;
-    f.whole_a = whole_a;
-    f.whole_b = whole_b;
     f.a_scales = a_scales;
     f.b_scales = b_scales;
     f.error_word = p->base.error_word;

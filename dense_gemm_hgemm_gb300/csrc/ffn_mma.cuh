@@ -18,14 +18,14 @@ constexpr int kTileSlot = kTileSide * kRowBytes;     // 16 KiB
 
 // The accumulators that a tcgen05.ld brought are there (tied to the registers, so that no use of
 // them can be moved before the wait).
-__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                  :: "memory");
 }
-// 32 lanes x 16 consecutive 32-bit TMEM columns -> 16 registers per thread.
-__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+// 32 lanes x 16 or 8 consecutive 32-bit TMEM columns -> as many registers per thread.
+__device__ __forceinline__ void tmem_read(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -33,6 +33,26 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :: "memory");
+}
+__device__ __forceinline__ void tmem_read(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+// The registers of a warpgroup (all of its warps): fewer, or more out of what others gave up.
+template <int N> __device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // One K = 32 step over e4m3 operands.
@@ -84,34 +104,31 @@ __device__ __forceinline__ void with_act(int act, F f) {
 
 // ---- scales along K -------------------------------------------------------------------
 
-// One row of scales, read four groups at a time and four ahead of their use.
+// One row of scales, each read a step before its use.  (A thread's reads of 32 groups are one
+// line; four at a time took registers that the sums need.  The read is volatile to stay
+// before the wait that hides it: left to the compiler it moved to its use.)
 struct ScaleRow {
-    const float* at;      // NULL: zeros (a row outside the matrix)
-    float4 now, next;
-    __device__ __forceinline__ float4 four(int kb, int num_kb, bool whole) const {
-        if (!at || kb >= num_kb) return make_float4(0.f, 0.f, 0.f, 0.f);
-        if (whole) return __ldg(reinterpret_cast<const float4*>(at + kb));
-        float4 v;
-        v.x = __ldg(at + kb);
-        v.y = kb + 1 < num_kb ? __ldg(at + kb + 1) : 0.f;
-        v.z = kb + 2 < num_kb ? __ldg(at + kb + 2) : 0.f;
-        v.w = kb + 3 < num_kb ? __ldg(at + kb + 3) : 0.f;
-        return v;
+    const float* at;
+    float next;
+    __device__ __forceinline__ void read() { asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(next) : "l"(at)); }
+    __device__ __forceinline__ void begin(const float* row, int kb) {
+        at = row + kb;
+        read();
     }
-    // Before group kb, the first of a run that starts at a multiple of four.
-    __device__ __forceinline__ void begin(const float* row, int kb, int num_kb, bool whole) {
-        at = row;
-        next = four(kb & ~3, num_kb, whole);
-    }
-    __device__ __forceinline__ float get(int kb, int kb_first, int num_kb, bool whole) {
-        if ((kb & 3) == 0 || kb == kb_first) {
-            now = next;
-            next = four((kb & ~3) + 4, num_kb, whole);
-        }
-        const float lo = (kb & 1) ? now.y : now.x, hi = (kb & 1) ? now.w : now.z;
-        return (kb & 2) ? hi : lo;
+    __device__ __forceinline__ float get(bool more) {
+        const float now = next;
+        ++at;
+        if (more) read();
+        return now;
     }
 };
+
+// Arrive on the pair leader's barrier at this offset.  (What it orders are reads of TMEM, which
+// are complete: a release at cluster scope would wait for every load in flight besides, and
+// took two thirds of the 8-bit product's time.)
+__device__ __forceinline__ void arrive_leader(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(map_to_rank(bar, 0)) : "memory");
+}
 
 // ---- few rows: one tile of up to 128 rows by 128 weight rows a cluster, K in slices -----------
 //
@@ -131,7 +148,6 @@ struct FewParams {
     int32_t num_kb, m_blocks, slices, kb_per_slice;
     uint32_t idesc, tx_extra;
     int32_t act;                 // gated
-    bool whole_a, whole_b;       // 8 bit: the scales' rows move in fours
     const float* a_scales;
     const float* b_scales;
     void* out;                   // M x N
@@ -285,33 +301,34 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int c = 0; c < kTileSide; ++c) acc[c] = 0.f;
             ScaleRow sa, sb;
-            sa.begin(row0 + row < p.M ? p.a_scales + static_cast<int64_t>(row0 + row) * p.num_kb : nullptr, kb0, p.num_kb,
-                     p.whole_a);
-            sb.begin(p.b_scales + static_cast<int64_t>(n_blk) * p.num_kb, kb0, p.num_kb, p.whole_b);
+            if (ok) {                                    // (rows behind the last take its scales, and are not stored)
+                sa.begin(p.a_scales + static_cast<int64_t>(min(row0 + row, p.M - 1)) * p.num_kb, kb0);
+                sb.begin(p.b_scales + static_cast<int64_t>(n_blk) * p.num_kb, kb0);
+            }
             for (int kb = kb0; kb < kb1; ++kb) {
                 const uint32_t i = static_cast<uint32_t>(kb - kb0), buf = i & 1u;
-                const float s = sa.get(kb, kb0, p.num_kb, p.whole_a) * sb.get(kb, kb0, p.num_kb, p.whole_b);
+                const float s = sa.get(kb + 1 < kb1) * sb.get(kb + 1 < kb1);
                 if (!wait_phase(smem_addr(&ctl->tmem_full[buf]), (i >> 1) & 1u, watch, kSiteEpiTmemFull)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const gbt::Pair s2(s, s);
-                uint32_t v[2][16];
-                tmem_ld_32x32b_x16(lanes_at + buf * kTileSide, v[0]);
+                uint32_t v[2][8];
+                tmem_read(lanes_at + buf * kTileSide, v[0]);
 #pragma unroll
-                for (int c = 0; c < kTileSide / 16; ++c) {
-                    tmem_ld_wait16(v[c & 1]);
-                    if (c + 1 < kTileSide / 16) {
-                        tmem_ld_32x32b_x16(lanes_at + buf * kTileSide + (c + 1) * 16, v[(c + 1) & 1]);
+                for (int c = 0; c < kTileSide / 8; ++c) {
+                    tmem_arrived(v[c & 1]);
+                    if (c + 1 < kTileSide / 8) {
+                        tmem_read(lanes_at + buf * kTileSide + (c + 1) * 8, v[(c + 1) & 1]);
                     } else {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_addr(&ctl->tmem_empty[buf]));
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int at = c * 16 + 2 * j;
+                    for (int j = 0; j < 4; ++j) {
+                        const int at = c * 8 + 2 * j;
                         const gbt::Pair t(__uint_as_float(v[c & 1][2 * j]), __uint_as_float(v[c & 1][2 * j + 1]));
                         gbt::fma2(t, s2, gbt::Pair(acc[at], acc[at + 1])).get(acc[at], acc[at + 1]);
                     }

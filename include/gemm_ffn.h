@@ -129,8 +129,7 @@ gemm_status_t gemm_fp8_plan_create(int64_t M, int64_t N, int64_t K, gemm_elem_t 
 
 /*
  * Queue the product.  A, B and C contiguous and 16-byte aligned; scales contiguous
- * (M x ceil(K/128), and N or ceil(N/128) x ceil(K/128)), 4-byte aligned (16-byte aligned
- * ones are faster).  K == 0 writes zeros.  C overlaps no operand.
+ * (M x ceil(K/128), and N or ceil(N/128) x ceil(K/128)), 4-byte aligned.  K == 0 writes zeros.  C overlaps no operand.
  */
 gemm_status_t gemm_fp8_run(gemm_fp8_plan_t plan, const void *A, const float *a_scales, const void *B,
                            const float *b_scales, void *C, void *stream);
