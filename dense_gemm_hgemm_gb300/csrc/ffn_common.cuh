@@ -12,27 +12,49 @@ constexpr float kLeastScale = 1.17549435e-38f; // 2^-126: one over it is a norma
 
 inline int64_t groups_of(int64_t cols) { return (cols + kGroup - 1) / kGroup; }
 
-// The first n of eight elements at p as fp32 (the rest zeros).  whole: p is aligned to 16 bytes.
+// Eight neighbouring columns of a row as they are in memory.  WHOLE: rows start at 16-byte
+// boundaries and have a multiple of eight columns, so the eight move together or not at all
+// (no branch: all loads of a thread are in flight at once); else element by element.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int n, bool whole, float (&v)[8]) {
-    if (whole && n >= 8) {
-        load_values<T, 8>(p, 8, v);
-    } else {
+struct Eight {
+    static constexpr int kPer = 16 / static_cast<int>(sizeof(T)), kParts = 8 / kPer;
+    Pack<T, kPer> part[kParts];
+    template <bool WHOLE>
+    __device__ __forceinline__ void load(const T* p, int n) {
+        if constexpr (WHOLE) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
-    }
-}
-
-template <typename T>
-__device__ __forceinline__ void store8(T* p, int n, bool whole, const float (&v)[8]) {
-    if (whole && n >= 8) {
-        store_values<T, 8>(p, 8, v);
-    } else {
+            for (int k = 0; k < kParts; ++k) {
+                part[k].clear();
+                if (n > 0) part[k].raw = *reinterpret_cast<const uint4*>(p + k * kPer);
+            }
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = from_f32<T>(v[i]);
+            for (int i = 0; i < 8; ++i) part[i / kPer].set_raw(i % kPer, i < n ? p[i] : from_f32<T>(0.f));
+        }
     }
-}
+    template <bool WHOLE>
+    __device__ __forceinline__ void store(T* p, int n) const {
+        if constexpr (WHOLE) {
+#pragma unroll
+            for (int k = 0; k < kParts; ++k)
+                if (n > 0) *reinterpret_cast<uint4*>(p + k * kPer) = part[k].raw;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < n) p[i] = reinterpret_cast<const T*>(&part[i / kPer].raw)[i % kPer];
+        }
+    }
+    __device__ __forceinline__ float get(int i) const { return part[i / kPer].get(i % kPer); }
+    __device__ __forceinline__ void set(int i, float v) { part[i / kPer].set(i % kPer, v); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = get(i);
+    }
+    __device__ __forceinline__ void set(const float (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) set(i, v[i]);
+    }
+};
 
 // Two numbers as e4m3 (to nearest even, at most 448 in size): lo in the lower byte.
 __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
@@ -47,10 +69,11 @@ __device__ __forceinline__ uint2 e4m3_eight(const float (&v)[8], float inverse) 
     return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
-// The first n of eight bytes.  whole: p is aligned to 8 bytes.
-__device__ __forceinline__ void store_bytes(uint8_t* p, int n, bool whole, uint2 v) {
-    if (whole && n >= 8) {
-        *reinterpret_cast<uint2*>(p) = v;
+// The first n of eight bytes (WHOLE: all or none, p aligned to 8 bytes).
+template <bool WHOLE>
+__device__ __forceinline__ void store_bytes(uint8_t* p, int n, uint2 v) {
+    if constexpr (WHOLE) {
+        if (n > 0) *reinterpret_cast<uint2*>(p) = v;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)

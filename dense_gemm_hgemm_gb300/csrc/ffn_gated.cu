@@ -266,18 +266,18 @@ __global__ void __launch_bounds__(kGradThreads) gate_grad_kernel(const T* gate_u
     gbt::wait_for_previous_kernel();
     gbt::let_next_kernel_start();
     if (c >= F) return;
-    float g[8], u[8], d[8];
-    gbt::load8(gate_up + row * 2 * F + c, 8, true, g);
-    gbt::load8(gate_up + row * 2 * F + F + c, 8, true, u);
-    gbt::load8(dh + row * F + c, 8, true, d);
+    gbt::Eight<T> g, u, d;
+    g.template load<true>(gate_up + row * 2 * F + c, 8);
+    u.template load<true>(gate_up + row * 2 * F + F + c, 8);
+    d.template load<true>(dh + row * F + c, 8);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float2 a = gate_and_slope<ACT>(g[i]);
-        g[i] = d[i] * u[i] * a.y;
-        u[i] = d[i] * a.x;
+        const float2 a = gate_and_slope<ACT>(g.get(i));
+        g.set(i, d.get(i) * u.get(i) * a.y);
+        u.set(i, d.get(i) * a.x);
     }
-    gbt::store8(dgate_up + row * 2 * F + c, 8, true, g);
-    gbt::store8(dgate_up + row * 2 * F + F + c, 8, true, u);
+    g.template store<true>(dgate_up + row * 2 * F + c, 8);
+    u.template store<true>(dgate_up + row * 2 * F + F + c, 8);
 }
 
 template <typename T>

@@ -1,4 +1,6 @@
 // ffn_quant.cu -- conversion of a matrix to e4m3 with scales (gemm_ffn.h).
+#include <type_traits>
+
 #include "ffn_common.cuh"
 
 namespace gbt {
@@ -14,7 +16,6 @@ struct QuantArgs {
     float* scales;
     int64_t ldx, ldq, lds;
     int rows, cols, tiles_across;
-    bool whole_x, whole_q;
 };
 
 // A block converts one tile of 128 x 128 elements, which its threads keep in registers between
@@ -23,7 +24,8 @@ struct QuantArgs {
 // are 16 lanes of a warp.  The rows are t / 16 + 16 k, or, transposed, 8 (t / 16) + k: then eight
 // values of a column are eight bytes of a result's row, which goes through shared memory with
 // its 8-byte units exchanged so that no two lanes of a store or a load meet in a bank.
-template <typename T, bool SQUARE, bool TRANSPOSE>
+// WHOLE: of x and of q (see Eight).
+template <typename T, bool SQUARE, bool TRANSPOSE, bool WHOLE>
 __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs a) {
     __shared__ uint32_t high[kSide];                             // sizes, as bits (their order is the numbers')
     __shared__ alignas(16) uint2 turned[TRANSPOSE ? kSide * kSide / 8 : 1];
@@ -34,12 +36,15 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs
     if (tid < kSide) high[tid] = 0;
     wait_for_previous_kernel();
     let_next_kernel_start();
-    float v[kPacks][8];
+    Eight<T> held[kPacks];
 #pragma unroll
     for (int k = 0; k < kPacks; ++k) {
         const int r = row0 + (TRANSPOSE ? row * 8 + k : row + 16 * k);
-        load8(static_cast<const T*>(a.x) + r * a.ldx + c, r < a.rows ? left : 0, a.whole_x, v[k]);
+        held[k].template load<WHOLE>(static_cast<const T*>(a.x) + r * a.ldx + c, r < a.rows ? left : 0);
     }
+    float v[kPacks][8];
+#pragma unroll
+    for (int k = 0; k < kPacks; ++k) held[k].get(v[k]);
     if constexpr (SQUARE || TRANSPOSE) __syncthreads();
     if constexpr (SQUARE) {
         float m = 0.f;
@@ -75,7 +80,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs
                 inverse = 1.f / s;
                 if (at == 0 && r < a.rows) a.scales[r * a.lds + col0 / kSide] = s;
             }
-            store_bytes(a.q + r * a.ldq + c, r < a.rows ? left : 0, a.whole_q, e4m3_eight(v[k], inverse));
+            store_bytes<WHOLE>(a.q + r * a.ldq + c, r < a.rows ? left : 0, e4m3_eight(v[k], inverse));
         }
     } else {
         // q's row is x's column: its scale index runs along x's rows
@@ -99,8 +104,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs
         for (int k = 0; k < kSide / 16; ++k) {
             const int r = row + 16 * k;
             const uint2 w = turned[r * 16 + (at ^ (r / 8))];
-            store_bytes(a.q + (col0 + r) * a.ldq + row0 + at * 8, col0 + r < a.cols ? a.rows - row0 - at * 8 : 0,
-                        a.whole_q, w);
+            store_bytes<WHOLE>(a.q + (col0 + r) * a.ldq + row0 + at * 8, col0 + r < a.cols ? a.rows - row0 - at * 8 : 0, w);
         }
     }
 }
@@ -129,15 +133,20 @@ extern "C" gemm_status_t gemm_fp8_quantize(int64_t rows, int64_t cols, gemm_elem
     }
     if (rows == 0 || cols == 0) return GEMM_OK;
     const QuantArgs a{x, static_cast<uint8_t*>(q), scales, ldx, ldq, lds, static_cast<int>(rows), static_cast<int>(cols),
-                      static_cast<int>(across), rows_aligned(x, ldx, e), bytes_aligned(q, ldq)};
+                      static_cast<int>(across)};
+    const bool whole = cols % 8 == 0 && out_cols % 8 == 0 && rows_aligned(x, ldx, e) && bytes_aligned(q, ldq);
     const Queue queue{stream, device};
+    const int64_t tiles = down * across;
     return with_elem(elem, [&](auto t) {
         using T = decltype(t);
-        const int64_t tiles = down * across;
-        if (kind == GEMM_SCALE_ROW)
-            return transpose ? launch<quantize_kernel<T, false, true>>(tiles, kQuantThreads, 0, queue, 1, a)
-                             : launch<quantize_kernel<T, false, false>>(tiles, kQuantThreads, 0, queue, 1, a);
-        return transpose ? launch<quantize_kernel<T, true, true>>(tiles, kQuantThreads, 0, queue, 1, a)
-                         : launch<quantize_kernel<T, true, false>>(tiles, kQuantThreads, 0, queue, 1, a);
+        const auto go = [&](auto square, auto turned) {
+            constexpr bool kSquare = decltype(square)::value, kTurned = decltype(turned)::value;
+            return whole ? launch<quantize_kernel<T, kSquare, kTurned, true>>(tiles, kQuantThreads, 0, queue, 1, a)
+                         : launch<quantize_kernel<T, kSquare, kTurned, false>>(tiles, kQuantThreads, 0, queue, 1, a);
+        };
+        using Yes = std::true_type;
+        using No = std::false_type;
+        if (kind == GEMM_SCALE_ROW) return transpose ? go(No(), Yes()) : go(No(), No());
+        return transpose ? go(Yes(), Yes()) : go(Yes(), No());
     });
 }

@@ -62,44 +62,37 @@ struct RmsForwardArgs {
     int64_t ldx, ldr, ldt, ldy, ldq, lds, rows;
     float eps;
     int cols, lanes;
-    bool whole;                 // rows and gamma move in packs
 };
 
 // x + residual as it is kept: an fp32 sum (one rounding), rounded to T.
 template <typename T>
-__device__ __forceinline__ void sum8(const T* x, const T* residual, int n, bool whole, float (&v)[8]) {
-    load8(x, n, whole, v);
-    if (residual) {
-        float r[8];
-        load8(residual, n, whole, r);
+__device__ __forceinline__ void add_eight(Eight<T>& x, const Eight<T>& residual) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_f32(from_f32<T>(v[i] + r[i]));
-    }
+    for (int i = 0; i < 8; ++i) x.set(i, x.get(i) + residual.get(i));
 }
 
-// y of a pack from t, and its conversion where Q8 (all lanes of a warp come here).
-template <typename T, typename W, bool Q8>
-__device__ __forceinline__ void finish_pack(const RmsForwardArgs<T, W>& a, int64_t row, int c, int n, float rstd,
-                                            float (&t)[8]) {
-    float w[8];
-    if (a.gamma) load8(a.gamma + c, n, a.whole, w);
+// y of eight columns from t, and its conversion where Q8 (all lanes of a warp come here).
+template <typename T, typename W, bool Q8, bool WHOLE>
+__device__ __forceinline__ void finish_eight(const RmsForwardArgs<T, W>& a, int64_t row, int c, int n, float rstd,
+                                             const Eight<T>& t, const Eight<W>& gamma) {
+    float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = a.gamma ? t[i] * rstd * w[i] : t[i] * rstd;
+    for (int i = 0; i < 8; ++i) y[i] = a.gamma ? t.get(i) * rstd * gamma.get(i) : t.get(i) * rstd;
     if constexpr (Q8) {
-        const float s = scale_of(largest_of_group(largest(t)));
-        if (n > 0) {
-            if (c % kGroup == 0) a.scales[row * a.lds + c / kGroup] = s;
-            store_bytes(a.q + row * a.ldq + c, n, a.whole, e4m3_eight(t, 1.f / s));
-        }
-    } else if (n > 0) {
-        store8(a.y + row * a.ldy + c, n, a.whole, t);
+        const float s = scale_of(largest_of_group(largest(y)));
+        if (n > 0 && c % kGroup == 0) a.scales[row * a.lds + c / kGroup] = s;
+        store_bytes<WHOLE>(a.q + row * a.ldq + c, n, e4m3_eight(y, 1.f / s));
+    } else {
+        Eight<T> out;
+        out.set(y);
+        out.template store<WHOLE>(a.y + row * a.ldy + c, n);
     }
 }
 
 // A row is held by `lanes` threads, 16 columns each: it is read once, and its sum of squares
 // and results come from registers.  Bound by memory; the loads in flight are those of the
 // blocks that share an SM, so a block does not look beyond its rows.
-template <typename T, typename W, int BLOCK, bool Q8>
+template <typename T, typename W, int BLOCK, bool Q8, bool WHOLE>
 __global__ void __launch_bounds__(BLOCK) rms_forward_kernel(const RmsForwardArgs<T, W> a) {
     __shared__ float part[BLOCK / 32];
     const int lane = static_cast<int>(threadIdx.x) & (a.lanes - 1);
@@ -107,24 +100,31 @@ __global__ void __launch_bounds__(BLOCK) rms_forward_kernel(const RmsForwardArgs
     const bool there = row < a.rows;
     wait_for_previous_kernel();
     let_next_kernel_start();
-    float t[kRowPacks][8];
+    Eight<T> t[kRowPacks], r[kRowPacks];
+    Eight<W> gamma[kRowPacks];
 #pragma unroll
     for (int k = 0; k < kRowPacks; ++k) {
         const int c = (k * a.lanes + lane) * 8;
-        sum8(a.x + row * a.ldx + c, a.residual ? a.residual + row * a.ldr + c : nullptr, there ? a.cols - c : 0, a.whole,
-             t[k]);
+        t[k].template load<WHOLE>(a.x + row * a.ldx + c, there ? a.cols - c : 0);
+        r[k].template load<WHOLE>(a.residual + row * a.ldr + c, there && a.residual ? a.cols - c : 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kRowPacks; ++k) {
+        const int c = (k * a.lanes + lane) * 8;
+        gamma[k].template load<WHOLE>(a.gamma + c, a.gamma ? a.cols - c : 0);
     }
     float sum = 0.f;
 #pragma unroll
     for (int k = 0; k < kRowPacks; ++k) {
+        if (a.residual) add_eight(t[k], r[k]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(t[k][i], t[k][i], sum);
+        for (int i = 0; i < 8; ++i) sum = fmaf(t[k].get(i), t[k].get(i), sum);
     }
-    if (a.total && there) {
+    if (a.total) {
 #pragma unroll
         for (int k = 0; k < kRowPacks; ++k) {
             const int c = (k * a.lanes + lane) * 8;
-            store8(a.total + row * a.ldt + c, a.cols - c, a.whole, t[k]);
+            t[k].template store<WHOLE>(a.total + row * a.ldt + c, there ? a.cols - c : 0);
         }
     }
     sum = row_sum<BLOCK>(sum, a.lanes, part);
@@ -133,12 +133,12 @@ __global__ void __launch_bounds__(BLOCK) rms_forward_kernel(const RmsForwardArgs
 #pragma unroll
     for (int k = 0; k < kRowPacks; ++k) {
         const int c = (k * a.lanes + lane) * 8;
-        finish_pack<T, W, Q8>(a, row, c, there ? a.cols - c : 0, rstd, t[k]);
+        finish_eight<T, W, Q8, WHOLE>(a, row, c, there ? a.cols - c : 0, rstd, t[k], gamma[k]);
     }
 }
 
 // Longer rows: a block goes over its row twice.
-template <typename T, typename W, bool Q8>
+template <typename T, typename W, bool Q8, bool WHOLE>
 __global__ void __launch_bounds__(kMostRowLanes) rms_forward_wide_kernel(const RmsForwardArgs<T, W> a) {
     __shared__ float part[kMostRowLanes / 32];
     const int64_t row = blockIdx.x;
@@ -147,13 +147,19 @@ __global__ void __launch_bounds__(kMostRowLanes) rms_forward_wide_kernel(const R
     const T* x = a.x + row * a.ldx;
     const T* residual = a.residual ? a.residual + row * a.ldr : nullptr;
     T* total = a.total ? a.total + row * a.ldt : nullptr;
+    const auto sum_at = [&](int c, int n, Eight<T>& t) {
+        Eight<T> r;
+        t.template load<WHOLE>(x + c, n);
+        r.template load<WHOLE>(residual + c, residual ? n : 0);
+        if (residual) add_eight(t, r);
+    };
     float sum = 0.f;
     for (int c = static_cast<int>(threadIdx.x) * 8; c < a.cols; c += kMostRowLanes * 8) {
-        float t[8];
-        sum8(x + c, residual ? residual + c : nullptr, a.cols - c, a.whole, t);
+        Eight<T> t;
+        sum_at(c, a.cols - c, t);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(t[i], t[i], sum);
-        if (total) store8(total + c, a.cols - c, a.whole, t);
+        for (int i = 0; i < 8; ++i) sum = fmaf(t.get(i), t.get(i), sum);
+        if (total) t.template store<WHOLE>(total + c, a.cols - c);
     }
     sum = row_sum<kMostRowLanes>(sum, kMostRowLanes, part);
     const float rstd = 1.f / sqrtf(sum / static_cast<float>(a.cols) + a.eps);
@@ -162,13 +168,15 @@ __global__ void __launch_bounds__(kMostRowLanes) rms_forward_wide_kernel(const R
     // warp go through every step: the largest value of a group is taken among them.)
     for (int c0 = 0; c0 < a.cols; c0 += kMostRowLanes * 8) {
         const int c = c0 + static_cast<int>(threadIdx.x) * 8, n = a.cols - c;
-        float t[8];
+        Eight<T> t;
+        Eight<W> gamma;
+        gamma.template load<WHOLE>(a.gamma + c, a.gamma ? n : 0);
         if (total) {
-            load8(static_cast<const T*>(total) + c, n, a.whole, t);
+            t.template load<WHOLE>(total + c, n);
         } else {
-            sum8(x + c, residual ? residual + c : nullptr, n, a.whole, t);
+            sum_at(c, n, t);
         }
-        finish_pack<T, W, Q8>(a, row, c, n, rstd, t);
+        finish_eight<T, W, Q8, WHOLE>(a, row, c, n, rstd, t, gamma);
     }
 }
 
@@ -185,58 +193,67 @@ struct RmsBackwardArgs {
     float* partial;             // [grid][cols], or NULL: no gradient of gamma wanted
     int64_t ldt, lddy, lddt, lddx, rows;
     int cols, lanes;
-    bool whole;
 };
 
-template <typename W>
-__device__ __forceinline__ void weight8(const W* gamma, int c, int n, bool whole, float (&w)[8]) {
-    if (gamma) {
-        load8(gamma + c, n, whole, w);
-    } else {
+// What a lane needs of a row, as it is in memory.
+template <typename T, bool WHOLE>
+struct RmsRow {
+    Eight<T> t[kRowPacks], dy[kRowPacks], more[kRowPacks];
+    float rstd;
+    template <typename W>
+    __device__ __forceinline__ void load(const RmsBackwardArgs<T, W>& a, int64_t row, int lane) {
+        const bool there = row < a.rows;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = 1.f;
+        for (int k = 0; k < kRowPacks; ++k) {
+            const int c = (k * a.lanes + lane) * 8, n = there ? a.cols - c : 0;
+            t[k].template load<WHOLE>(a.total + row * a.ldt + c, n);
+            dy[k].template load<WHOLE>(a.dy + row * a.lddy + c, n);
+            more[k].template load<WHOLE>(a.dtotal + row * a.lddt + c, a.dtotal ? n : 0);
+        }
+        rstd = there ? a.rstd[row] : 0.f;
     }
-}
+};
 
 // Blocks of a backward kernel that share an SM (its registers: 128 a thread).
 constexpr int backward_blocks_an_sm(int block) { return block < 512 ? 512 / block : 1; }
 
 // A block goes over rows blockIdx.x, + gridDim.x, ... (BLOCK / lanes at a time) and keeps its
-// share of the weight's gradient in registers, 16 columns a lane.
-template <typename T, typename W, int BLOCK>
+// share of the weight's gradient in registers, 16 columns a lane.  The next row's loads are in
+// flight during the present one's sum (not with 1024 threads, whose registers do not hold two rows).
+template <typename T, typename W, int BLOCK, bool WHOLE>
 __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backward_kernel(const RmsBackwardArgs<T, W> a) {
+    constexpr bool kAhead = BLOCK <= 512;
     extern __shared__ float shared[];            // (where a block has several groups: their sums)
     __shared__ float part[2][BLOCK / 32];
     const int lane = static_cast<int>(threadIdx.x) & (a.lanes - 1);
     const int groups = BLOCK / a.lanes, group = static_cast<int>(threadIdx.x) / a.lanes;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     wait_for_previous_kernel();
     let_next_kernel_start();
     float dgamma[kRowPacks][8] = {};
     int turn = 0;
-    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups; row0 < a.rows; row0 += static_cast<int64_t>(gridDim.x) * groups) {
+    RmsRow<T, WHOLE> next;
+    if (kAhead) next.load(a, static_cast<int64_t>(blockIdx.x) * groups + group, lane);
+    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups; row0 < a.rows; row0 += step) {
         const int64_t row = row0 + group;
-        const bool there = row < a.rows;
-        const float rstd = there ? a.rstd[row] : 0.f;
-        float hat[kRowPacks][8], g[kRowPacks][8], more[kRowPacks][8];
+        RmsRow<T, WHOLE> now;
+        if constexpr (kAhead) {
+            now = next;
+            next.load(a, row + step, lane);
+        } else {
+            now.load(a, row, lane);
+        }
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < kRowPacks; ++k) {
-            const int c = (k * a.lanes + lane) * 8, n = there ? a.cols - c : 0;
-            load8(a.total + row * a.ldt + c, n, a.whole, hat[k]);
-            load8(a.dy + row * a.lddy + c, n, a.whole, g[k]);
-            if (a.dtotal) load8(a.dtotal + row * a.lddt + c, n, a.whole, more[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < kRowPacks; ++k) {
             const int c = (k * a.lanes + lane) * 8;
-            float w[8];
-            weight8(a.gamma, c, a.cols - c, a.whole, w);
+            Eight<W> w;
+            w.template load<WHOLE>(a.gamma + c, a.gamma ? a.cols - c : 0);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                hat[k][i] *= rstd;
-                dgamma[k][i] = fmaf(g[k][i], hat[k][i], dgamma[k][i]);
-                g[k][i] *= w[i];
-                sum = fmaf(g[k][i], hat[k][i], sum);
+                const float hat = now.t[k].get(i) * now.rstd, d = now.dy[k].get(i);
+                dgamma[k][i] = fmaf(d, hat, dgamma[k][i]);
+                sum = fmaf(a.gamma ? d * w.get(i) : d, hat, sum);
             }
         }
         if (!a.dx) continue;                     // (all of the block)
@@ -245,13 +262,17 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
         const float mean = sum / static_cast<float>(a.cols);
 #pragma unroll
         for (int k = 0; k < kRowPacks; ++k) {
-            const int c = (k * a.lanes + lane) * 8, n = there ? a.cols - c : 0;
+            const int c = (k * a.lanes + lane) * 8, n = row < a.rows ? a.cols - c : 0;
+            Eight<W> w;
+            w.template load<WHOLE>(a.gamma + c, a.gamma ? a.cols - c : 0);
+            Eight<T> out;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                g[k][i] = rstd * (g[k][i] - hat[k][i] * mean);
-                if (a.dtotal) g[k][i] += more[k][i];
+                const float d = now.dy[k].get(i), g = a.gamma ? d * w.get(i) : d;
+                const float dx = now.rstd * (g - now.t[k].get(i) * now.rstd * mean);
+                out.set(i, a.dtotal ? dx + now.more[k].get(i) : dx);
             }
-            if (n > 0) store8(a.dx + row * a.lddx + c, n, a.whole, g[k]);
+            out.template store<WHOLE>(a.dx + row * a.lddx + c, n);
         }
     }
     if (!a.partial) return;
@@ -276,12 +297,14 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
 #pragma unroll
     for (int k = 0; k < kRowPacks; ++k) {
         const int c = (k * a.lanes + lane) * 8;
-        store8(to + c, a.cols - c, a.cols % 4 == 0, dgamma[k]);
+        Eight<float> out;
+        out.set(dgamma[k]);
+        out.template store<WHOLE>(to + c, a.cols - c);
     }
 }
 
 // Longer rows: dx, a row a block, twice over it.
-template <typename T, typename W>
+template <typename T, typename W, bool WHOLE>
 __global__ void __launch_bounds__(kMostRowLanes) rms_dx_wide_kernel(const RmsBackwardArgs<T, W> a) {
     __shared__ float part[kMostRowLanes / 32];
     const int64_t row = blockIdx.x;
@@ -292,26 +315,28 @@ __global__ void __launch_bounds__(kMostRowLanes) rms_dx_wide_kernel(const RmsBac
     const float rstd = a.rstd[row];
     float sum = 0.f;
     for (int c = static_cast<int>(threadIdx.x) * 8; c < a.cols; c += kMostRowLanes * 8) {
-        float t[8], g[8], w[8];
-        load8(total + c, a.cols - c, a.whole, t);
-        load8(dy + c, a.cols - c, a.whole, g);
-        weight8(a.gamma, c, a.cols - c, a.whole, w);
+        Eight<T> t, g;
+        Eight<W> w;
+        t.template load<WHOLE>(total + c, a.cols - c);
+        g.template load<WHOLE>(dy + c, a.cols - c);
+        w.template load<WHOLE>(a.gamma + c, a.gamma ? a.cols - c : 0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(g[i] * w[i], t[i] * rstd, sum);
+        for (int i = 0; i < 8; ++i) sum = fmaf(a.gamma ? g.get(i) * w.get(i) : g.get(i), t.get(i) * rstd, sum);
     }
     const float mean = row_sum<kMostRowLanes>(sum, kMostRowLanes, part) / static_cast<float>(a.cols);
     for (int c = static_cast<int>(threadIdx.x) * 8; c < a.cols; c += kMostRowLanes * 8) {
-        float t[8], g[8], w[8], more[8];
-        load8(total + c, a.cols - c, a.whole, t);
-        load8(dy + c, a.cols - c, a.whole, g);
-        weight8(a.gamma, c, a.cols - c, a.whole, w);
-        if (a.dtotal) load8(a.dtotal + row * a.lddt + c, a.cols - c, a.whole, more);
+        Eight<T> t, g, more;
+        Eight<W> w;
+        t.template load<WHOLE>(total + c, a.cols - c);
+        g.template load<WHOLE>(dy + c, a.cols - c);
+        w.template load<WHOLE>(a.gamma + c, a.gamma ? a.cols - c : 0);
+        more.template load<WHOLE>(a.dtotal + row * a.lddt + c, a.dtotal ? a.cols - c : 0);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            g[i] = rstd * (g[i] * w[i] - t[i] * rstd * mean);
-            if (a.dtotal) g[i] += more[i];
+            const float dx = rstd * ((a.gamma ? g.get(i) * w.get(i) : g.get(i)) - t.get(i) * rstd * mean);
+            g.set(i, a.dtotal ? dx + more.get(i) : dx);
         }
-        store8(a.dx + row * a.lddx + c, a.cols - c, a.whole, g);
+        g.template store<WHOLE>(a.dx + row * a.lddx + c, a.cols - c);
     }
 }
 
@@ -364,17 +389,17 @@ __global__ void __launch_bounds__(kJoinThreads) rms_dgamma_join_kernel(const flo
 
 constexpr int row_block(int lanes) { return lanes < 128 ? 128 : lanes; }
 
-template <typename T, typename W, bool Q8>
+template <typename T, typename W, bool Q8, bool WHOLE>
 gemm_status_t forward(const RmsForwardArgs<T, W>& a, Queue queue) {
     if (a.cols > kRowColumns)
-        return launch<rms_forward_wide_kernel<T, W, Q8>>(a.rows, kMostRowLanes, 0, queue, 1, a);
+        return launch<rms_forward_wide_kernel<T, W, Q8, WHOLE>>(a.rows, kMostRowLanes, 0, queue, 1, a);
     const int block = row_block(a.lanes);
     const int64_t grid = (a.rows + block / a.lanes - 1) / (block / a.lanes);
     switch (block) {
-        case 128: return launch<rms_forward_kernel<T, W, 128, Q8>>(grid, 128, 0, queue, 1, a);
-        case 256: return launch<rms_forward_kernel<T, W, 256, Q8>>(grid, 256, 0, queue, 1, a);
-        case 512: return launch<rms_forward_kernel<T, W, 512, Q8>>(grid, 512, 0, queue, 1, a);
-        default: return launch<rms_forward_kernel<T, W, 1024, Q8>>(grid, 1024, 0, queue, 1, a);
+        case 128: return launch<rms_forward_kernel<T, W, 128, Q8, WHOLE>>(grid, 128, 0, queue, 1, a);
+        case 256: return launch<rms_forward_kernel<T, W, 256, Q8, WHOLE>>(grid, 256, 0, queue, 1, a);
+        case 512: return launch<rms_forward_kernel<T, W, 512, Q8, WHOLE>>(grid, 512, 0, queue, 1, a);
+        default: return launch<rms_forward_kernel<T, W, 1024, Q8, WHOLE>>(grid, 1024, 0, queue, 1, a);
     }
 }
 
@@ -385,15 +410,15 @@ int64_t backward_grid(int64_t rows, int lanes, int sms) {
     return blocks < most ? blocks : most;
 }
 
-template <typename T, typename W>
+template <typename T, typename W, bool WHOLE>
 gemm_status_t backward(const RmsBackwardArgs<T, W>& a, int64_t grid, Queue queue) {
     const int block = row_block(a.lanes);
     const size_t smem = block > a.lanes ? static_cast<size_t>(block) * kLaneColumns * sizeof(float) : 0;
     switch (block) {
-        case 128: return launch<rms_backward_kernel<T, W, 128>>(grid, 128, smem, queue, 1, a);
-        case 256: return launch<rms_backward_kernel<T, W, 256>>(grid, 256, smem, queue, 1, a);
-        case 512: return launch<rms_backward_kernel<T, W, 512>>(grid, 512, smem, queue, 1, a);
-        default: return launch<rms_backward_kernel<T, W, 1024>>(grid, 1024, smem, queue, 1, a);
+        case 128: return launch<rms_backward_kernel<T, W, 128, WHOLE>>(grid, 128, smem, queue, 1, a);
+        case 256: return launch<rms_backward_kernel<T, W, 256, WHOLE>>(grid, 256, smem, queue, 1, a);
+        case 512: return launch<rms_backward_kernel<T, W, 512, WHOLE>>(grid, 512, smem, queue, 1, a);
+        default: return launch<rms_backward_kernel<T, W, 1024, WHOLE>>(grid, 1024, smem, queue, 1, a);
     }
 }
 
@@ -463,7 +488,7 @@ gemm_status_t gemm_rms_forward(gemm_rms_plan_t p, int64_t rows, const void* x, i
     const int e = gbt::elem_bytes(p->elem);
     if (!gbt::aligned(y, e)) return GEMM_ERR_ALIGNMENT;
     if (rows == 0) return GEMM_OK;
-    const bool whole = gbt::rows_aligned(x, ldx, e) && gbt::packs_aligned(residual, ldr, e) &&
+    const bool whole = p->cols % 8 == 0 && gbt::rows_aligned(x, ldx, e) && gbt::packs_aligned(residual, ldr, e) &&
                        gbt::packs_aligned(total, ldt, e) && gbt::rows_aligned(y, ldy, e) && gbt::aligned(gamma, 16);
     return gbt::with_types(p, [&](auto t, auto v) {
         using T = decltype(t);
@@ -471,8 +496,9 @@ gemm_status_t gemm_rms_forward(gemm_rms_plan_t p, int64_t rows, const void* x, i
         const gbt::RmsForwardArgs<T, W> a{static_cast<const T*>(x), static_cast<const T*>(residual),
                                           static_cast<const W*>(gamma), static_cast<T*>(total), static_cast<T*>(y), nullptr,
                                           nullptr, rstd, ldx, ldr, ldt, ldy, 0, 0, rows, eps, static_cast<int>(p->cols),
-                                          gbt::row_lanes(p->cols), whole};
-        return gbt::forward<T, W, false>(a, gbt::Queue{stream, p->device});
+                                          gbt::row_lanes(p->cols)};
+        const gbt::Queue queue{stream, p->device};
+        return whole ? gbt::forward<T, W, false, true>(a, queue) : gbt::forward<T, W, false, false>(a, queue);
     });
 }
 
@@ -485,7 +511,7 @@ gemm_status_t gemm_rms_forward_fp8(gemm_rms_plan_t p, int64_t rows, const void* 
     if (!gbt::aligned(scales, 4)) return GEMM_ERR_ALIGNMENT;
     if (rows == 0) return GEMM_OK;
     const int e = gbt::elem_bytes(p->elem);
-    const bool whole = gbt::rows_aligned(x, ldx, e) && gbt::packs_aligned(residual, ldr, e) &&
+    const bool whole = p->cols % 8 == 0 && gbt::rows_aligned(x, ldx, e) && gbt::packs_aligned(residual, ldr, e) &&
                        gbt::packs_aligned(total, ldt, e) && gbt::bytes_aligned(q, ldq) && gbt::aligned(gamma, 16);
     return gbt::with_types(p, [&](auto t, auto v) {
         using T = decltype(t);
@@ -493,8 +519,9 @@ gemm_status_t gemm_rms_forward_fp8(gemm_rms_plan_t p, int64_t rows, const void* 
         const gbt::RmsForwardArgs<T, W> a{static_cast<const T*>(x), static_cast<const T*>(residual),
                                           static_cast<const W*>(gamma), static_cast<T*>(total), nullptr,
                                           static_cast<uint8_t*>(q), scales, rstd, ldx, ldr, ldt, 0, ldq, lds, rows, eps,
-                                          static_cast<int>(p->cols), gbt::row_lanes(p->cols), whole};
-        return gbt::forward<T, W, true>(a, gbt::Queue{stream, p->device});
+                                          static_cast<int>(p->cols), gbt::row_lanes(p->cols)};
+        const gbt::Queue queue{stream, p->device};
+        return whole ? gbt::forward<T, W, true, true>(a, queue) : gbt::forward<T, W, true, false>(a, queue);
     });
 }
 
@@ -511,7 +538,7 @@ gemm_status_t gemm_rms_backward(gemm_rms_plan_t p, int64_t rows, const void* tot
         return GEMM_ERR_ALIGNMENT;
     const gemm_status_t st = gbt::check_device(p->device);
     if (st != GEMM_OK || (!dx && !dgamma)) return st;
-    const bool whole = gbt::rows_aligned(total, ldt, e) && gbt::rows_aligned(dy, lddy, e) &&
+    const bool whole = p->cols % 8 == 0 && gbt::rows_aligned(total, ldt, e) && gbt::rows_aligned(dy, lddy, e) &&
                        gbt::packs_aligned(dtotal, lddt, e) && gbt::packs_aligned(dx, lddx, e) && gbt::aligned(gamma, 16);
     const gbt::Queue queue{stream, p->device};
     return gbt::with_types(p, [&](auto t, auto v) {
@@ -521,7 +548,7 @@ gemm_status_t gemm_rms_backward(gemm_rms_plan_t p, int64_t rows, const void* tot
         const unsigned tiles = static_cast<unsigned>((p->cols + 31) / 32);
         const gbt::RmsBackwardArgs<T, W> a{static_cast<const T*>(total), static_cast<const W*>(gamma), rstd,
                                            static_cast<const T*>(dy), static_cast<const T*>(dtotal), static_cast<T*>(dx),
-                                           dgamma ? p->partial : nullptr, ldt, lddy, lddt, lddx, rows, cols, lanes, whole};
+                                           dgamma ? p->partial : nullptr, ldt, lddy, lddt, lddx, rows, cols, lanes};
         gemm_status_t s = GEMM_OK;
         if (cols > gbt::kRowColumns) {
             // (the weight's gradient first: dx may overwrite dy or total)
@@ -529,11 +556,12 @@ gemm_status_t gemm_rms_backward(gemm_rms_plan_t p, int64_t rows, const void* tot
                 s = gbt::launch<gbt::rms_dgamma_wide_kernel<T, W>>(tiles, gbt::kJoinThreads, 0, queue, 1, a,
                                                                     static_cast<W*>(dgamma));
             if (s == GEMM_OK && dx && rows > 0)
-                s = gbt::launch<gbt::rms_dx_wide_kernel<T, W>>(rows, gbt::kMostRowLanes, 0, queue, 1, a);
+                s = whole ? gbt::launch<gbt::rms_dx_wide_kernel<T, W, true>>(rows, gbt::kMostRowLanes, 0, queue, 1, a)
+                          : gbt::launch<gbt::rms_dx_wide_kernel<T, W, false>>(rows, gbt::kMostRowLanes, 0, queue, 1, a);
             return s;
         }
         const int64_t grid = gbt::backward_grid(rows, lanes, p->num_sms);
-        if (grid > 0) s = gbt::backward<T, W>(a, grid, queue);
+        if (grid > 0) s = whole ? gbt::backward<T, W, true>(a, grid, queue) : gbt::backward<T, W, false>(a, grid, queue);
         if (s == GEMM_OK && dgamma)
             s = gbt::launch<gbt::rms_dgamma_join_kernel<W>>(tiles, gbt::kJoinThreads, 0, queue, 1, p->partial,
                                                             static_cast<int>(grid), cols, static_cast<W*>(dgamma));
