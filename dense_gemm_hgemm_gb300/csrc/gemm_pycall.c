@@ -1,5 +1,5 @@
 /* gemm_pycall.c -- CPython entry points for the per-call functions of the C ABI:
- * gemm_run, gemm_launch_empty and the calls of gemm_train.h: one vectorcall with plain integer
+ * gemm_run, gemm_launch_empty and the calls of gemm_train.h and gemm_ffn.h: one vectorcall with plain integer
  * arguments instead of a ctypes call that converts each argument.  Argument
  * marshalling only: the functions are called through the addresses the Python
  * binding hands over once, after it has loaded libgemm_gb300.so.
@@ -13,9 +13,12 @@
  *       directly; every other call, a box[0] that is None (plan closed) and a
  *       non-zero status go to general(*args, **kwargs), the binding's own path,
  *       which handles the other argument forms and raises the error.
- *   TrainCall(kind, function, plan, elem, weight, types, cols, rows, device, raw_stream, only=-1)
- *       -> a callable for one call of one plan of gemm_train.h (only: the index of
- *       the device that tensors have to be on, -1 = not looked at).  It takes the
+ *   TrainCall(kind, function, plan, elem, weight, types, cols, rows, device, raw_stream, only=-1,
+ *             depth=0, square=0)
+ *       -> a callable for one call of one plan of gemm_train.h or gemm_ffn.h (only: the index of
+ *       the device that tensors have to be on, -1 = not looked at; types: the five dtypes of
+ *       gemm_train.h and, for calls with 8-bit matrices, theirs; depth: a product's K; square: its
+ *       second operand's scales go by squares; plan 0 for a call without one).  It takes the
  *       call's arguments by position (tensors, numbers, the stream last: an int,
  *       None for the current one, or an object with cuda_stream), checks them as
  *       the binding's general path does and returns the C function's status, or
@@ -195,7 +198,8 @@ typedef struct {      /* gemm_teacher_t */
 } Teacher;
 
 enum { NORM_FORWARD, NORM_BACKWARD, EMBED_FORWARD, EMBED_BACKWARD, DISTILL_FORWARD,
-       DISTILL_BACKWARD, DISTILL_BOTH, TRAIN_KINDS };
+       DISTILL_BACKWARD, DISTILL_BOTH, RMS_FORWARD, RMS_FORWARD_FP8, RMS_BACKWARD, FP8_RUN,
+       GATED_FORWARD, GATED_BACKWARD, QUANTIZE, TRAIN_KINDS };
 
 typedef struct {
     PyObject_HEAD
@@ -204,8 +208,10 @@ typedef struct {
     void* plan;
     PyObject* elem;          /* torch dtypes: the plan's elements, */
     PyObject* weight;        /* its weights or table gradients, */
-    PyObject* types;         /* and (float16, bfloat16, float32, int32, int64) */
-    int64_t cols, rows;      /* of the matrices (rows: of an embedding table) */
+    PyObject* types;         /* and (float16, bfloat16, float32, int32, int64[, float8_e4m3fn]) */
+    int64_t cols, rows;      /* of the matrices (rows: of an embedding table, or a product's result) */
+    int64_t depth;           /* a product's K */
+    int square;              /* its second operand's scales */
     PyObject* device;
     PyObject* raw_stream;    /* callable: device -> the current stream's handle */
     long only;               /* the device that tensors have to be on; -1: there is one, not asked */
@@ -275,6 +281,25 @@ static int matrix(const TrainCall* call, PyObject* t, int64_t* rows, int64_t col
     return 1;
 }
 
+/* A rows x cols matrix of the type with contiguous rows; None, a NULL pointer, where that is allowed. */
+static int typed(const TrainCall* call, PyObject* t, PyObject* dtype, int64_t* rows, int64_t cols, int none, void** ptr,
+                 int64_t* ld) {
+    if (t == Py_None) {
+        *ptr = NULL;
+        *ld = 0;
+        return none;
+    }
+    return has_type(t, dtype) && matrix(call, t, rows, cols, ptr, ld);
+}
+
+/* ... all of it contiguous. */
+static int whole(const TrainCall* call, PyObject* t, PyObject* dtype, int64_t rows, int64_t cols, int none, void** ptr) {
+    int64_t ld;
+    return typed(call, t, dtype, &rows, cols, none, ptr, &ld) && (*ptr == NULL || ld == cols || rows * cols == 0);
+}
+
+static int64_t groups_of(int64_t n) { return (n + 127) / 128; }
+
 /* A contiguous vector of n values of the type, or None where that is allowed. */
 static int vector(const TrainCall* call, PyObject* t, PyObject* dtype, int64_t n, int none, void** ptr) {
     int64_t shape, stride;
@@ -325,6 +350,95 @@ static int teacher_of(const TrainCall* c, PyObject* ids, PyObject* values, PyObj
     t->id_type = id_type;
     t->value_elem = elem;
     return 1;
+}
+
+/* The calls of gemm_ffn.h. */
+static int ffn_call(const TrainCall* c, PyObject* const* v, Py_ssize_t n) {
+    PyObject* const f32 = PyTuple_GET_ITEM(c->types, 2);
+    PyObject* const e4m3 = PyTuple_GET_ITEM(c->types, 5);
+    void *p[7], *stream;
+    int64_t ld[5], rows = -1;
+    double x;
+    switch (c->kind) {
+        case RMS_FORWARD:            /* x, gamma, y, rstd, residual, total, eps, stream */
+        case RMS_FORWARD_FP8: {      /* x, gamma, q, scales, rstd, residual, total, eps, stream */
+            const int fp8 = c->kind == RMS_FORWARD_FP8;
+            PyObject* const* m = v + fp8;
+            if (n != 8 + fp8 || !typed(c, v[0], c->elem, &rows, c->cols, 0, &p[0], &ld[0]) ||
+                !vector(c, v[1], c->weight, c->cols, 1, &p[1]) ||
+                !typed(c, v[2], fp8 ? e4m3 : c->elem, &rows, c->cols, 0, &p[2], &ld[2]) ||
+                (fp8 && !typed(c, v[3], f32, &rows, groups_of(c->cols), 0, &p[6], &ld[1])) ||
+                !vector(c, m[3], f32, rows, 1, &p[3]) || !typed(c, m[4], c->elem, &rows, c->cols, 1, &p[4], &ld[3]) ||
+                !typed(c, m[5], c->elem, &rows, c->cols, 1, &p[5], &ld[4]) || !number(m[6], &x) ||
+                !stream_of(c, m[7], &stream))
+                return -1;
+            if (fp8)
+                return ((int (*)(void*, int64_t, const void*, int64_t, const void*, int64_t, const void*, float, void*,
+                                 int64_t, void*, int64_t, void*, int64_t, void*, void*))c->fn)(
+                    c->plan, rows, p[0], ld[0], p[4], ld[3], p[1], (float)x, p[5], ld[4], p[2], ld[2], p[6], ld[1], p[3],
+                    stream);
+            return ((int (*)(void*, int64_t, const void*, int64_t, const void*, int64_t, const void*, float, void*,
+                             int64_t, void*, int64_t, void*, void*))c->fn)(
+                c->plan, rows, p[0], ld[0], p[4], ld[3], p[1], (float)x, p[5], ld[4], p[2], ld[2], p[3], stream);
+        }
+        case RMS_BACKWARD:           /* total, gamma, rstd, dy, dx, dgamma, dtotal, stream */
+            if (n != 8 || !typed(c, v[0], c->elem, &rows, c->cols, 0, &p[0], &ld[0]) ||
+                !vector(c, v[1], c->weight, c->cols, 1, &p[1]) || !vector(c, v[2], f32, rows, 0, &p[2]) ||
+                !typed(c, v[3], c->elem, &rows, c->cols, 0, &p[3], &ld[1]) ||
+                !typed(c, v[4], c->elem, &rows, c->cols, 1, &p[4], &ld[2]) ||
+                !vector(c, v[5], c->weight, c->cols, 1, &p[5]) ||
+                !typed(c, v[6], c->elem, &rows, c->cols, 1, &p[6], &ld[3]) || !stream_of(c, v[7], &stream))
+                return -1;
+            return ((int (*)(void*, int64_t, const void*, int64_t, const void*, const void*, const void*, int64_t,
+                             const void*, int64_t, void*, int64_t, void*, void*))c->fn)(
+                c->plan, rows, p[0], ld[0], p[1], p[2], p[3], ld[1], p[6], ld[3], p[4], ld[2], p[5], stream);
+        case FP8_RUN: {              /* A, a_scales, B, b_scales, C, stream */
+            const int64_t M = c->rows, N = c->cols, K = c->depth;
+            if (n != 6 || !whole(c, v[0], e4m3, M, K, 0, &p[0]) || !whole(c, v[1], f32, M, groups_of(K), 0, &p[1]) ||
+                !whole(c, v[2], e4m3, N, K, 0, &p[2]) ||
+                !whole(c, v[3], f32, c->square ? groups_of(N) : N, groups_of(K), 0, &p[3]) ||
+                !whole(c, v[4], c->elem, M, N, 0, &p[4]) || !stream_of(c, v[5], &stream))
+                return -1;
+            return ((int (*)(void*, const void*, const void*, const void*, const void*, void*, void*))c->fn)(
+                c->plan, p[0], p[1], p[2], p[3], p[4], stream);
+        }
+        case GATED_FORWARD: {        /* X, W, H, gate_up, stream */
+            const int64_t M = c->rows, F = c->cols, K = c->depth;
+            if (n != 5 || !whole(c, v[0], c->elem, M, K, 0, &p[0]) || !whole(c, v[1], c->elem, 2 * F, K, 0, &p[1]) ||
+                !whole(c, v[2], c->elem, M, F, 0, &p[2]) || !whole(c, v[3], c->elem, M, 2 * F, 1, &p[3]) ||
+                !stream_of(c, v[4], &stream))
+                return -1;
+            return ((int (*)(void*, const void*, const void*, void*, void*, void*))c->fn)(c->plan, p[0], p[1], p[2], p[3],
+                                                                                         stream);
+        }
+        case GATED_BACKWARD: {       /* X, W, gate_up, dH, dgate_up, dX, dW, stream */
+            const int64_t M = c->rows, F = c->cols, K = c->depth;
+            if (n != 8 || !whole(c, v[0], c->elem, M, K, v[6] == Py_None, &p[0]) ||
+                !whole(c, v[1], c->elem, 2 * F, K, v[5] == Py_None, &p[1]) ||
+                !whole(c, v[2], c->elem, M, 2 * F, 0, &p[2]) || !whole(c, v[3], c->elem, M, F, 0, &p[3]) ||
+                !whole(c, v[4], c->elem, M, 2 * F, 0, &p[4]) || !whole(c, v[5], c->elem, M, K, 1, &p[5]) ||
+                !whole(c, v[6], c->elem, 2 * F, K, 1, &p[6]) || !stream_of(c, v[7], &stream))
+                return -1;
+            return ((int (*)(void*, const void*, const void*, const void*, const void*, void*, void*, void*, void*))c->fn)(
+                c->plan, p[0], p[1], p[2], p[3], p[4], p[5], p[6], stream);
+        }
+        default: {                   /* QUANTIZE: x, q, scales, kind of scales, transpose, stream */
+            int64_t shape[2], stride[2];
+            const int elem = n == 6 ? type_among(v[0], c->types, 0, 3) : -1;
+            if (elem < 0 || !tensor_of(c, v[0], 2, &p[0], shape, stride) || (shape[1] > 1 && stride[1] != 1)) return -1;
+            const int kind = (int)PyLong_AsLong(v[3]), turned = PyObject_IsTrue(v[4]);
+            if (turned < 0 || PyErr_Occurred()) return -1;
+            int64_t out = shape[turned ? 1 : 0], down = kind == 1 ? groups_of(out) : out;
+            const int64_t across = shape[turned ? 0 : 1];
+            if (!typed(c, v[1], e4m3, &out, across, 0, &p[1], &ld[1]) ||
+                !typed(c, v[2], f32, &down, groups_of(across), 0, &p[2], &ld[2]) || !stream_of(c, v[5], &stream))
+                return -1;
+            ld[0] = shape[0] > 1 ? stride[0] : shape[1];
+            return ((int (*)(int64_t, int64_t, int, const void*, int64_t, int, int, void*, int64_t, void*, int64_t,
+                             void*))c->fn)(shape[0], shape[1], elem, p[0], ld[0], kind, turned, p[1], ld[1], p[2], ld[2],
+                                           stream);
+        }
+    }
 }
 
 /* The status of the call, or -1 where an argument does not fit. */
@@ -420,29 +534,32 @@ static PyObject* train_call_vector(PyObject* self, PyObject* const* args, size_t
         PyErr_SetString(PyExc_TypeError, "TrainCall takes its arguments by position");
         return NULL;
     }
-    const int st = train_call((const TrainCall*)self, args, PyVectorcall_NARGS(nargsf));
+    const TrainCall* const call = (const TrainCall*)self;
+    const int st = (call->kind < RMS_FORWARD ? train_call : ffn_call)(call, args, PyVectorcall_NARGS(nargsf));
     if (st < 0) PyErr_Clear();
     return PyLong_FromLong(st);
 }
 
 static PyObject* train_call_new(PyTypeObject* type, PyObject* args, PyObject* kwds) {
     int kind;
-    long long cols, rows;
+    long long cols, rows, depth = 0;
     long only = -1;
+    int square = 0;
     PyObject *fn, *plan, *elem, *weight, *types, *device, *raw_stream;
     if (kwds != NULL && PyDict_GET_SIZE(kwds) != 0) {
         PyErr_SetString(PyExc_TypeError, "TrainCall takes its arguments by position");
         return NULL;
     }
-    if (!PyArg_ParseTuple(args, "iOOOOO!LLOO|l:TrainCall", &kind, &fn, &plan, &elem, &weight, &PyTuple_Type,
-                          &types, &cols, &rows, &device, &raw_stream, &only))
+    if (!PyArg_ParseTuple(args, "iOOOOO!LLOO|lLp:TrainCall", &kind, &fn, &plan, &elem, &weight, &PyTuple_Type,
+                          &types, &cols, &rows, &device, &raw_stream, &only, &depth, &square))
         return NULL;
     void* f = PyLong_AsVoidPtr(fn);
     void* h = PyErr_Occurred() ? NULL : PyLong_AsVoidPtr(plan);
     if (PyErr_Occurred()) return NULL;
-    if (kind < 0 || kind >= TRAIN_KINDS || f == NULL || h == NULL || PyTuple_GET_SIZE(types) != 5 ||
-        !PyCallable_Check(raw_stream)) {
-        PyErr_SetString(PyExc_ValueError, "TrainCall: unknown kind, null address, five dtypes and a callable needed");
+    const Py_ssize_t dtypes = PyTuple_GET_SIZE(types);
+    if (kind < 0 || kind >= TRAIN_KINDS || f == NULL || (h == NULL && kind != QUANTIZE) ||
+        dtypes != (kind < RMS_FORWARD ? 5 : 6) || !PyCallable_Check(raw_stream)) {
+        PyErr_SetString(PyExc_ValueError, "TrainCall: unknown kind, null address, five dtypes (six for gemm_ffn.h) and a callable needed");
         return NULL;
     }
     TrainCall* self = (TrainCall*)type->tp_alloc(type, 0);
@@ -455,6 +572,8 @@ static PyObject* train_call_new(PyTypeObject* type, PyObject* args, PyObject* kw
     self->types = Py_NewRef(types);
     self->cols = cols;
     self->rows = rows;
+    self->depth = depth;
+    self->square = square;
     self->device = Py_NewRef(device);
     self->raw_stream = Py_NewRef(raw_stream);
     self->only = only;
@@ -493,7 +612,7 @@ static PyTypeObject TrainCallType = {
     .tp_name = "_gemm_pycall.TrainCall",
     .tp_basicsize = sizeof(TrainCall),
     .tp_flags = Py_TPFLAGS_DEFAULT | Py_TPFLAGS_HAVE_GC | Py_TPFLAGS_HAVE_VECTORCALL,
-    .tp_doc = "One call of one plan of gemm_train.h: its status, or -1 where an argument does not fit",
+    .tp_doc = "One call of one plan of gemm_train.h or gemm_ffn.h: its status, or -1 where an argument does not fit",
     .tp_new = train_call_new,
     .tp_dealloc = train_call_dealloc,
     .tp_traverse = train_call_traverse,
@@ -514,7 +633,7 @@ static PyMethodDef methods[] = {
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gemm_pycall",
                                     "Vectorcall entry points for gemm_run and gemm_launch_empty, "
-                                    "a per-plan runner, and the calls of gemm_train.h.",
+                                    "a per-plan runner, and the calls of gemm_train.h and gemm_ffn.h.",
                                     -1, methods, NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit__gemm_pycall(void) {

@@ -56,6 +56,22 @@ def signatures():
     }
 
 
+# calls that the C entry points know, by their numbers there
+_RMS_FORWARD, _RMS_FORWARD_FP8, _RMS_BACKWARD, _FP8_RUN, _GATED_FORWARD, _GATED_BACKWARD, _QUANTIZE = range(7, 14)
+
+
+class _FfnPlan(_Plan):
+    """A plan whose calls have C entry points (``_enter``), of which ``_drop`` forgets all."""
+
+    def _enter(self, kind, name, elem, weight, cols, rows=0, *more):
+        import torch
+        return self._entry(kind, name, elem, weight, cols, rows, *more, extra_types=(torch.float8_e4m3fn,))
+
+    def _drop(self):
+        for name in [n for n in vars(self) if n.startswith("_enter_")]:
+            setattr(self, name, None)
+
+
 def _groups(n: int) -> int:
     return -(-n // GROUP)
 
@@ -88,7 +104,7 @@ def _whole(t, rows, cols, elem, what):
     return address
 
 
-class _ProductPlan(_Plan):
+class _ProductPlan(_FfnPlan):
     """A plan of a product: its waits' limit, their test hook and their check (`_kind`: of its C functions)."""
 
     _kind = ""
@@ -110,7 +126,7 @@ class _ProductPlan(_Plan):
         self._call("check", _stream(stream))
 
 
-class RmsNormPlan(_Plan):
+class RmsNormPlan(_FfnPlan):
     """Root-mean-square norm over rows of `cols` elements, for up to `max_rows` rows a call."""
 
     _destroy = "gemm_rms_plan_destroy"
@@ -120,6 +136,10 @@ class RmsNormPlan(_Plan):
         self._elem = _elem(dtype)
         self._weight = self._elem if weight is None else _elem(weight)
         self._create("gemm_rms_plan_create", max_rows, cols, self._elem, self._weight)
+        self._enter_forward, self._enter_fp8, self._enter_backward = (
+            self._enter(kind, name, self._elem, self._weight, cols)
+            for kind, name in ((_RMS_FORWARD, "gemm_rms_forward"), (_RMS_FORWARD_FP8, "gemm_rms_forward_fp8"),
+                               (_RMS_BACKWARD, "gemm_rms_backward")))
 
     def _inputs(self, x, gamma, residual, total, eps):
         rows, cols = x.shape[0], self.cols
@@ -129,6 +149,8 @@ class RmsNormPlan(_Plan):
 
     def forward(self, x, gamma, y, rstd=None, residual=None, total=None, eps: float = 1e-5, stream=None) -> None:
         """y = t * rstd * gamma of t = x + residual; total and rstd (fp32) are kept for backward."""
+        if self._taken(self._enter_forward, "gemm_rms_forward", (x, gamma, y, rstd, residual, total, eps, stream)):
+            return
         args = self._inputs(x, gamma, residual, total, eps)
         rows = args[0]
         _check(library().gemm_rms_forward(
@@ -138,6 +160,9 @@ class RmsNormPlan(_Plan):
     def forward_fp8(self, x, gamma, q, scales, rstd=None, residual=None, total=None, eps: float = 1e-5,
                     stream=None) -> None:
         """As forward, with y as e4m3 numbers and their scales by rows."""
+        if self._taken(self._enter_fp8, "gemm_rms_forward_fp8",
+                       (x, gamma, q, scales, rstd, residual, total, eps, stream)):
+            return
         args = self._inputs(x, gamma, residual, total, eps)
         rows = args[0]
         _check(library().gemm_rms_forward_fp8(
@@ -148,6 +173,8 @@ class RmsNormPlan(_Plan):
     def backward(self, total, gamma, rstd, dy, dx=None, dgamma=None, dtotal=None, stream=None) -> None:
         """Gradients of x (and of the residual) and of gamma, each optional, from dy and from dtotal,
         the gradient that reaches the sum on its other way."""
+        if self._taken(self._enter_backward, "gemm_rms_backward", (total, gamma, rstd, dy, dx, dgamma, dtotal, stream)):
+            return
         rows, cols = total.shape[0], self.cols
         _check(library().gemm_rms_backward(
             self.handle, rows, *_matrix(total, rows, cols, self._elem, "total"),
@@ -157,11 +184,29 @@ class RmsNormPlan(_Plan):
             _stream(stream)), "gemm_rms_backward")
 
 
+_quantize = None            # the C entry point of fp8_quantize, where there is one device
+
+
+def _quantize_entry():
+    global _quantize
+    if _quantize is None:
+        import torch
+        library()
+        if not torch.cuda.is_available() or torch.cuda.device_count() != 1:
+            return None
+        call = _FfnPlan()
+        call.handle = 0
+        _quantize = call._enter(_QUANTIZE, "gemm_fp8_quantize", 0, 0, 0)
+    return _quantize
+
+
 def fp8_quantize(x, q, scales, block="row", transpose: bool = False, stream=None) -> None:
     """x as e4m3 numbers `q` with fp32 `scales` for each 128 elements of a row ("row") or each
     128 x 128 elements ("square"); of its transpose where `transpose`."""
-    _torch_types()
     kind = _scale_kind(block)
+    if _Plan._taken(_quantize_entry(), "gemm_fp8_quantize", (x, q, scales, kind, transpose, stream)):
+        return
+    _torch_types()
     if not _on_device(x) or x.dim() != 2:
         raise GemmError(_INVALID_ARG, "x: a matrix on the current device is needed")
     rows, cols = x.shape
@@ -184,9 +229,13 @@ class Fp8Plan(_ProductPlan):
         self.M, self.N, self.K = M, N, K
         self._elem, self._scales = _elem(dtype), _scale_kind(b_scales)
         self._create("gemm_fp8_plan_create", M, N, K, self._elem, self._scales)
+        self._enter_run = self._enter(_FP8_RUN, "gemm_fp8_run", self._elem, self._elem, N, M, K,
+                                      self._scales == GEMM_SCALE_SQUARE)
 
     def run(self, A, a_scales, B, b_scales, C, stream=None) -> None:
         """C = A B^T.  All matrices contiguous."""
+        if self._taken(self._enter_run, "gemm_fp8_run", (A, a_scales, B, b_scales, C, stream)):
+            return
         M, N, K = self.M, self.N, self.K
         _bytes_matrix(A, M, K, "A")
         _bytes_matrix(B, N, K, "B")
@@ -210,6 +259,9 @@ class GatedPlan(_ProductPlan):
         if isinstance(act, str) and act not in ACTIVATIONS:
             raise GemmError(_UNSUPPORTED, "activation %r" % act)
         self._create("gemm_gated_plan_create", M, F, K, self._elem, ACTIVATIONS[act] if isinstance(act, str) else int(act))
+        self._enter_forward, self._enter_backward = (
+            self._enter(kind, name, self._elem, self._elem, F, M, K)
+            for kind, name in ((_GATED_FORWARD, "gemm_gated_forward"), (_GATED_BACKWARD, "gemm_gated_backward")))
 
     def _matrix(self, t, rows, cols, what, may_be_none=False):
         if t is None and may_be_none:
@@ -220,12 +272,16 @@ class GatedPlan(_ProductPlan):
 
     def forward(self, X, W, H, gate_up=None, stream=None) -> None:
         """H; and both products side by side (M x 2F), for backward, where `gate_up` is given."""
+        if self._taken(self._enter_forward, "gemm_gated_forward", (X, W, H, gate_up, stream)):
+            return
         M, F, K, m = self.M, self.F, self.K, self._matrix
         _check(library().gemm_gated_forward(self.handle, m(X, M, K, "X"), m(W, 2 * F, K, "W"), m(H, M, F, "H"),
                                             m(gate_up, M, 2 * F, "gate_up", True), _stream(stream)), "gemm_gated_forward")
 
     def backward(self, X, W, gate_up, dH, dgate_up, dX=None, dW=None, stream=None) -> None:
         """dgate_up (which may be gate_up) from dH, and from it dX and dW, each optional (W and X may be None with them)."""
+        if self._taken(self._enter_backward, "gemm_gated_backward", (X, W, gate_up, dH, dgate_up, dX, dW, stream)):
+            return
         M, F, K, m = self.M, self.F, self.K, self._matrix
         _check(library().gemm_gated_backward(
             self.handle, m(X, M, K, "X", dW is None), m(W, 2 * F, K, "W", dX is None), m(gate_up, M, 2 * F, "gate_up"),

@@ -157,7 +157,7 @@ class _Plan:
         _check(getattr(library(), name)(*args, ctypes.byref(h)), name)
         self.handle = h.value
 
-    def _entry(self, kind, name, elem, weight, cols, rows=0):
+    def _entry(self, kind, name, elem, weight, cols, rows=0, *more, extra_types=()):
         """The C entry point of one call of this plan, which checks the arguments and
         marshals them (the general path below each method does the same in Python and
         says what is wrong); None where the C module could not be built."""
@@ -170,8 +170,9 @@ class _Plan:
             raw = lambda device: torch.cuda.current_stream(device).cuda_stream  # noqa: E731
         kinds = (torch.float16, torch.bfloat16, torch.float32)
         return call(kind, ctypes.cast(getattr(library(), name), ctypes.c_void_p).value, self.handle, kinds[elem],
-                    kinds[weight], (*kinds, torch.int32, torch.int64), cols, rows, torch.cuda.current_device(), raw,
-                    torch.cuda.current_device() if torch.cuda.device_count() > 1 else -1)
+                    kinds[weight], (*kinds, torch.int32, torch.int64, *extra_types), cols, rows,
+                    torch.cuda.current_device(), raw,
+                    torch.cuda.current_device() if torch.cuda.device_count() > 1 else -1, *more)
 
     @staticmethod
     def _taken(entry, name, args) -> bool:

@@ -129,3 +129,101 @@ def test_oracle_conversion():
     q, s = ref.quantize(x, False)
     assert s.item() == 1.0 and q.float().tolist() == [[448.0, 1.0, -3.25, 0.0]]     # 2^-10 is half the smallest: even
     assert (ref.stands_for(q, s, False) - x.double()).abs().le(ref.conversion_bound(x.double(), s, False)).all()
+
+
+class _Tensor:
+    """A stand-in for a device tensor."""
+    is_cuda = True
+
+    def __init__(self, address, shape, ld, dtype):
+        self.address, self.shape, self.dtype = address, tuple(shape), dtype
+        self._stride = (ld, 1) if len(self.shape) == 2 else (1,)
+
+    def data_ptr(self):
+        return self.address
+
+    def stride(self):
+        return self._stride
+
+    def is_contiguous(self):
+        return len(self.shape) == 1 or self._stride[0] == self.shape[1]
+
+
+def test_entry_points_marshal_what_they_take(gemm_lib):
+    """The C entry points hand the C functions the arguments' addresses, sizes and strides, and take nothing
+    that does not fit; a fake function stands in for the library's."""
+    gemm_lib.library()
+    pc = gemm_lib._pycall
+    if pc is None or not hasattr(pc, "TrainCall"):
+        pytest.skip("CPython entry points not built")
+    seen = []
+    bf, f32, f8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+    kinds = (torch.float16, bf, f32, torch.int32, torch.int64, f8)
+
+    def fake(kind, name, *sizes, plan=4096):
+        args, res = gemm_lib.ffn.signatures()[name]
+        fn = ctypes.CFUNCTYPE(res, *args)(lambda *a: seen.append(a) or 0)
+        cols, rows, *more = sizes
+        return pc.TrainCall(kind, ctypes.cast(fn, ctypes.c_void_p).value, plan, bf, f32, kinds, cols, rows, 0,
+                            lambda device: 77 + device, -1, *more), fn
+    m = lambda at, rows=6, cols=200, ld=None, dtype=bf: _Tensor(at, (rows, cols), cols if ld is None else ld, dtype)  # noqa: E731
+    v = lambda at, n, dtype=f32: _Tensor(at, (n,), 1, dtype)  # noqa: E731
+
+    call, keep = fake(7, "gemm_rms_forward", 200, 0)
+    assert call(m(0x100, ld=208), v(0x200, 200), m(0x300), v(0x400, 6), None, m(0x600, ld=224), 0.5, None) == 0
+    assert seen[-1] == (4096, 6, 0x100, 208, None, 0, 0x200, 0.5, 0x600, 224, 0x300, 200, 0x400, 77)
+    n = len(seen)
+    for i, bad in ((0, m(0x100, dtype=f32)), (0, None), (1, v(0x200, 199)), (2, m(0x300, rows=5)), (2, m(0x300, dtype=f8)),
+                   (3, v(0x400, 5)), (4, m(0x500, cols=100)), (5, m(0x600, dtype=f32)), (6, "eps")):
+        args = [m(0x100), v(0x200, 200), m(0x300), None, None, None, 0.5, None]
+        args[i] = bad
+        assert call(*args) == -1
+    assert len(seen) == n
+    call, keep = fake(8, "gemm_rms_forward_fp8", 200, 0)
+    assert call(m(0x100), None, m(0x300, dtype=f8, ld=256), m(0x700, cols=2, ld=4, dtype=f32), None, m(0x500, ld=201), None, 0.5, 9) == 0
+    assert seen[-1] == (4096, 6, 0x100, 200, 0x500, 201, None, 0.5, None, 0, 0x300, 256, 0x700, 4, None, 9)
+    assert call(m(0x100), None, m(0x300), m(0x700, cols=2, dtype=f32), None, None, None, 0.5, 9) == -1
+    assert call(m(0x100), None, m(0x300, dtype=f8), m(0x700, cols=1, dtype=f32), None, None, None, 0.5, 9) == -1
+    assert call(m(0x100), None, m(0x300, dtype=f8), None, None, None, None, 0.5, 9) == -1
+    call, keep = fake(9, "gemm_rms_backward", 200, 0)
+    assert call(m(0x100, ld=201), v(0x200, 200), v(0x300, 6), m(0x400, ld=202), m(0x500, ld=203), v(0x600, 200), m(0x700, ld=204), 9) == 0
+    assert seen[-1] == (4096, 6, 0x100, 201, 0x200, 0x300, 0x400, 202, 0x700, 204, 0x500, 203, 0x600, 9)
+    assert call(m(0x100), None, v(0x300, 6), m(0x400), None, None, None, 9) == 0
+    assert seen[-1] == (4096, 6, 0x100, 200, None, 0x300, 0x400, 200, None, 0, None, 0, None, 9)
+    assert call(m(0x100), None, None, m(0x400), None, None, None, 9) == -1
+
+    q = lambda at, rows, cols, ld=None: m(at, rows, cols, ld, f8)  # noqa: E731
+    s = lambda at, rows, cols, ld=None: m(at, rows, cols, ld, f32)  # noqa: E731
+    for square, down in ((True, 3), (False, 264)):
+        call, keep = fake(10, "gemm_fp8_run", 264, 6, 144, square)
+        args = [q(0x100, 6, 144), s(0x200, 6, 2), q(0x300, 264, 144), s(0x400, down, 2), m(0x500, 6, 264), None]
+        assert call(*args) == 0
+        assert seen[-1] == (4096, 0x100, 0x200, 0x300, 0x400, 0x500, 77)
+        for i, bad in ((0, q(0x100, 6, 144, 160)), (0, m(0x100, 6, 144)), (1, s(0x200, 6, 1)), (2, q(0x300, 6, 144)),
+                       (3, s(0x400, 2, 2)), (4, m(0x500, 6, 264, dtype=f32)), (4, None)):
+            assert call(*args[:i], bad, *args[i + 1:]) == -1
+    call, keep = fake(11, "gemm_gated_forward", 40, 6, 200)
+    assert call(m(0x100), m(0x200, 80), m(0x300, 6, 40), None, 9) == 0
+    assert seen[-1] == (4096, 0x100, 0x200, 0x300, None, 9)
+    assert call(m(0x100), m(0x200, 80), m(0x300, 6, 40), m(0x400, 6, 80), 9) == 0 and seen[-1][4] == 0x400
+    assert call(m(0x100), m(0x200, 40), m(0x300, 6, 40), None, 9) == -1
+    assert call(m(0x100, ld=208), m(0x200, 80), m(0x300, 6, 40), None, 9) == -1
+    call, keep = fake(12, "gemm_gated_backward", 40, 6, 200)
+    assert call(m(0x100), m(0x200, 80), m(0x300, 6, 80), m(0x400, 6, 40), m(0x500, 6, 80), m(0x600), m(0x700, 80), 9) == 0
+    assert seen[-1] == (4096, 0x100, 0x200, 0x300, 0x400, 0x500, 0x600, 0x700, 9)
+    assert call(None, None, m(0x300, 6, 80), m(0x400, 6, 40), m(0x500, 6, 80), None, None, 9) == 0
+    assert call(None, m(0x200, 80), m(0x300, 6, 80), m(0x400, 6, 40), m(0x500, 6, 80), None, m(0x700, 80), 9) == -1
+    assert call(m(0x100), None, m(0x300, 6, 80), m(0x400, 6, 40), m(0x500, 6, 80), m(0x600), None, 9) == -1
+
+    call, keep = fake(13, "gemm_fp8_quantize", 0, 0, plan=0)
+    assert call(m(0x100, ld=208), q(0x200, 6, 200, 256), s(0x300, 6, 2, 5), 0, False, 9) == 0
+    assert seen[-1] == (6, 200, 1, 0x100, 208, 0, 0, 0x200, 256, 0x300, 5, 9)
+    assert call(m(0x100), q(0x200, 200, 6), s(0x300, 200, 1), 0, True, 9) == 0
+    assert seen[-1] == (6, 200, 1, 0x100, 200, 0, 1, 0x200, 6, 0x300, 1, 9)
+    assert call(m(0x100), q(0x200, 200, 6), s(0x300, 2, 1), 1, True, 9) == 0
+    assert call(m(0x100), q(0x200, 6, 200), s(0x300, 6, 2), 1, False, 9) == -1
+    assert call(m(0x100), q(0x200, 6, 200), s(0x300, 6, 2), 0, True, 9) == -1
+    assert call(m(0x100, dtype=f8), q(0x200, 6, 200), s(0x300, 6, 2), 0, False, 9) == -1
+    for kind, plan, types in ((14, 1, kinds), (7, 0, kinds), (7, 1, kinds[:5]), (6, 1, kinds)):
+        with pytest.raises(ValueError):
+            pc.TrainCall(kind, 1, plan, bf, bf, types, 1, 1, 0, len)
