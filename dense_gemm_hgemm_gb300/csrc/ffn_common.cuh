@@ -12,9 +12,16 @@ constexpr float kLeastScale = 1.17549435e-38f; // 2^-126: one over it is a norma
 
 inline int64_t groups_of(int64_t cols) { return (cols + kGroup - 1) / kGroup; }
 
-// Eight neighbouring columns of a row as they are in memory.  WHOLE: rows start at 16-byte
-// boundaries and have a multiple of eight columns, so the eight move together or not at all
-// (no branch: all loads of a thread are in flight at once); else element by element.
+// Eight columns of a row as they are in memory, of the 128 that 16 threads hold together.
+// WHOLE: rows start at 16-byte boundaries and have a multiple of eight columns; a thread has
+// eight neighbours, which move together or not at all (no branch: all loads of a thread are in
+// flight at once).  Else it has every 16th, element by element: the 16 threads' accesses are
+// neighbours (neighbours of a thread made each access 32 sectors of a warp).
+constexpr int kApart = 16;
+template <bool WHOLE>
+__device__ __forceinline__ int first_column(int thread) {
+    return WHOLE ? thread * 8 : (thread & ~15) * 8 + (thread & 15);
+}
 template <typename T>
 struct Eight {
     static constexpr int kPer = 16 / static_cast<int>(sizeof(T)), kParts = 8 / kPer;
@@ -29,7 +36,7 @@ struct Eight {
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) part[i / kPer].set_raw(i % kPer, i < n ? p[i] : from_f32<T>(0.f));
+            for (int i = 0; i < 8; ++i) part[i / kPer].set_raw(i % kPer, i * kApart < n ? p[i * kApart] : from_f32<T>(0.f));
         }
     }
     template <bool WHOLE>
@@ -41,7 +48,7 @@ struct Eight {
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (i < n) p[i] = reinterpret_cast<const T*>(&part[i / kPer].raw)[i % kPer];
+                if (i * kApart < n) p[i * kApart] = reinterpret_cast<const T*>(&part[i / kPer].raw)[i % kPer];
         }
     }
     __device__ __forceinline__ float get(int i) const { return part[i / kPer].get(i % kPer); }
@@ -69,7 +76,7 @@ __device__ __forceinline__ uint2 e4m3_eight(const float (&v)[8], float inverse) 
     return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
-// The first n of eight bytes (WHOLE: all or none, p aligned to 8 bytes).
+// Eight bytes, placed as the columns of an Eight (WHOLE: p aligned to 8 bytes).
 template <bool WHOLE>
 __device__ __forceinline__ void store_bytes(uint8_t* p, int n, uint2 v) {
     if constexpr (WHOLE) {
@@ -77,7 +84,7 @@ __device__ __forceinline__ void store_bytes(uint8_t* p, int n, uint2 v) {
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = static_cast<uint8_t>((i < 4 ? v.x : v.y) >> (i % 4 * 8));
+            if (i * kApart < n) p[i * kApart] = static_cast<uint8_t>((i < 4 ? v.x : v.y) >> (i % 4 * 8));
     }
 }
 

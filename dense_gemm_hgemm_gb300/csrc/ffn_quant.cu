@@ -20,10 +20,10 @@ struct QuantArgs {
 
 // A block converts one tile of 128 x 128 elements, which its threads keep in registers between
 // the largest value and the conversion: x is read once and q written once, 32 KB of bf16 in
-// flight a block.  Thread t holds columns 8 (t % 16) .. + 7 of eight rows: a row's 128 columns
-// are 16 lanes of a warp.  The rows are t / 16 + 16 k, or, transposed, 8 (t / 16) + k: then eight
-// values of a column are eight bytes of a result's row, which goes through shared memory with
-// its 8-byte units exchanged so that no two lanes of a store or a load meet in a bank.
+// flight a block.  16 threads hold a row's 128 columns (as Eight has them), each of eight rows:
+// t / 16 + 16 k, or, transposed, 8 (t / 16) + k, so that a column's eight values are eight
+// bytes of a result's row.  That goes through shared memory, its 8-byte units exchanged
+// within a row by `turn` so that no two lanes of a store or a load meet in a bank.
 // WHOLE: of x and of q (see Eight).
 template <typename T, bool SQUARE, bool TRANSPOSE, bool WHOLE>
 __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs a) {
@@ -32,7 +32,9 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs
     const int tid = static_cast<int>(threadIdx.x), at = tid % 16, row = tid / 16;
     const int row0 = static_cast<int>(blockIdx.x / a.tiles_across) * kSide;
     const int col0 = static_cast<int>(blockIdx.x % a.tiles_across) * kSide;
-    const int c = col0 + at * 8, left = a.cols - c;
+    const int c = col0 + first_column<WHOLE>(at), left = a.cols - c;
+    const auto column = [&](int i) { return WHOLE ? at * 8 + i : at + kApart * i; };    // of the tile
+    const auto turn = [](int col) { return WHOLE ? col / 8 : col % 16; };
     if (tid < kSide) high[tid] = 0;
     wait_for_previous_kernel();
     let_next_kernel_start();
@@ -61,7 +63,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs
 #pragma unroll
             for (int k = 0; k < kPacks; ++k) m = fmaxf(m, fabsf(v[k][i]));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-            if (tid % 32 < 16) atomicMax(&high[at * 8 + i], __float_as_uint(m));
+            if (tid % 32 < 16) atomicMax(&high[column(i)], __float_as_uint(m));
         }
         __syncthreads();
     }
@@ -92,19 +94,28 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantArgs
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float inverse = 1.f / scale_of(__uint_as_float(high[SQUARE ? 0 : at * 8 + i]));
+            const float inverse = 1.f / scale_of(__uint_as_float(high[SQUARE ? 0 : column(i)]));
             float down[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) down[k] = v[k][i];
-            turned[(at * 8 + i) * 16 + (row ^ at)] = e4m3_eight(down, inverse);
+            turned[column(i) * 16 + (row ^ turn(column(i)))] = e4m3_eight(down, inverse);
         }
         __syncthreads();
         // 128 rows of 128 bytes, eight a thread and step
 #pragma unroll
         for (int k = 0; k < kSide / 16; ++k) {
-            const int r = row + 16 * k;
-            const uint2 w = turned[r * 16 + (at ^ (r / 8))];
-            store_bytes<WHOLE>(a.q + (col0 + r) * a.ldq + row0 + at * 8, col0 + r < a.cols ? a.rows - row0 - at * 8 : 0, w);
+            const int r = row + 16 * k, n = col0 + r < a.cols ? a.rows - row0 - column(0) : 0;
+            uint8_t* to = a.q + (col0 + r) * a.ldq + row0 + column(0);
+            if constexpr (WHOLE) {
+                store_bytes<true>(to, n, turned[r * 16 + (at ^ turn(r))]);
+            } else {
+                const uint8_t* bytes = reinterpret_cast<const uint8_t*>(turned + r * 16);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int b = column(i);
+                    if (kApart * i < n) to[kApart * i] = bytes[((b / 8) ^ turn(r)) * 8 + b % 8];
+                }
+            }
         }
     }
 }

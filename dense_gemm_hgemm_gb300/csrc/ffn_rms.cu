@@ -104,13 +104,13 @@ __global__ void __launch_bounds__(BLOCK) rms_forward_kernel(const RmsForwardArgs
     Eight<W> gamma[kRowPacks];
 #pragma unroll
     for (int k = 0; k < kRowPacks; ++k) {
-        const int c = (k * a.lanes + lane) * 8;
+        const int c = first_column<WHOLE>(k * a.lanes + lane);
         t[k].template load<WHOLE>(a.x + row * a.ldx + c, there ? a.cols - c : 0);
         r[k].template load<WHOLE>(a.residual + row * a.ldr + c, there && a.residual ? a.cols - c : 0);
     }
 #pragma unroll
     for (int k = 0; k < kRowPacks; ++k) {
-        const int c = (k * a.lanes + lane) * 8;
+        const int c = first_column<WHOLE>(k * a.lanes + lane);
         gamma[k].template load<WHOLE>(a.gamma + c, a.gamma ? a.cols - c : 0);
     }
     float sum = 0.f;
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(BLOCK) rms_forward_kernel(const RmsForwardArgs
     if (a.total) {
 #pragma unroll
         for (int k = 0; k < kRowPacks; ++k) {
-            const int c = (k * a.lanes + lane) * 8;
+            const int c = first_column<WHOLE>(k * a.lanes + lane);
             t[k].template store<WHOLE>(a.total + row * a.ldt + c, there ? a.cols - c : 0);
         }
     }
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(BLOCK) rms_forward_kernel(const RmsForwardArgs
     if (a.rstd && there && lane == 0) a.rstd[row] = rstd;
 #pragma unroll
     for (int k = 0; k < kRowPacks; ++k) {
-        const int c = (k * a.lanes + lane) * 8;
+        const int c = first_column<WHOLE>(k * a.lanes + lane);
         finish_eight<T, W, Q8, WHOLE>(a, row, c, there ? a.cols - c : 0, rstd, t[k], gamma[k]);
     }
 }
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kMostRowLanes) rms_forward_wide_kernel(const R
         if (residual) add_eight(t, r);
     };
     float sum = 0.f;
-    for (int c = static_cast<int>(threadIdx.x) * 8; c < a.cols; c += kMostRowLanes * 8) {
+    for (int c = first_column<WHOLE>(static_cast<int>(threadIdx.x)); c < a.cols; c += kMostRowLanes * 8) {
         Eight<T> t;
         sum_at(c, a.cols - c, t);
 #pragma unroll
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kMostRowLanes) rms_forward_wide_kernel(const R
     // (a thread reads back only what it wrote: total may be x or the residual.  All lanes of a
     // warp go through every step: the largest value of a group is taken among them.)
     for (int c0 = 0; c0 < a.cols; c0 += kMostRowLanes * 8) {
-        const int c = c0 + static_cast<int>(threadIdx.x) * 8, n = a.cols - c;
+        const int c = c0 + first_column<WHOLE>(static_cast<int>(threadIdx.x)), n = a.cols - c;
         Eight<T> t;
         Eight<W> gamma;
         gamma.template load<WHOLE>(a.gamma + c, a.gamma ? n : 0);
@@ -205,7 +205,7 @@ struct RmsRow {
         const bool there = row < a.rows;
 #pragma unroll
         for (int k = 0; k < kRowPacks; ++k) {
-            const int c = (k * a.lanes + lane) * 8, n = there ? a.cols - c : 0;
+            const int c = first_column<WHOLE>(k * a.lanes + lane), n = there ? a.cols - c : 0;
             t[k].template load<WHOLE>(a.total + row * a.ldt + c, n);
             dy[k].template load<WHOLE>(a.dy + row * a.lddy + c, n);
             more[k].template load<WHOLE>(a.dtotal + row * a.lddt + c, a.dtotal ? n : 0);
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < kRowPacks; ++k) {
-            const int c = (k * a.lanes + lane) * 8;
+            const int c = first_column<WHOLE>(k * a.lanes + lane);
             Eight<W> w;
             w.template load<WHOLE>(a.gamma + c, a.gamma ? a.cols - c : 0);
 #pragma unroll
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
         const float mean = sum / static_cast<float>(a.cols);
 #pragma unroll
         for (int k = 0; k < kRowPacks; ++k) {
-            const int c = (k * a.lanes + lane) * 8, n = row < a.rows ? a.cols - c : 0;
+            const int c = first_column<WHOLE>(k * a.lanes + lane), n = row < a.rows ? a.cols - c : 0;
             Eight<W> w;
             w.template load<WHOLE>(a.gamma + c, a.gamma ? a.cols - c : 0);
             Eight<T> out;
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
     }
 #pragma unroll
     for (int k = 0; k < kRowPacks; ++k) {
-        const int c = (k * a.lanes + lane) * 8;
+        const int c = first_column<WHOLE>(k * a.lanes + lane);
         Eight<float> out;
         out.set(dgamma[k]);
         out.template store<WHOLE>(to + c, a.cols - c);
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kMostRowLanes) rms_dx_wide_kernel(const RmsBac
     const T* dy = a.dy + row * a.lddy;
     const float rstd = a.rstd[row];
     float sum = 0.f;
-    for (int c = static_cast<int>(threadIdx.x) * 8; c < a.cols; c += kMostRowLanes * 8) {
+    for (int c = first_column<WHOLE>(static_cast<int>(threadIdx.x)); c < a.cols; c += kMostRowLanes * 8) {
         Eight<T> t, g;
         Eight<W> w;
         t.template load<WHOLE>(total + c, a.cols - c);
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kMostRowLanes) rms_dx_wide_kernel(const RmsBac
         for (int i = 0; i < 8; ++i) sum = fmaf(a.gamma ? g.get(i) * w.get(i) : g.get(i), t.get(i) * rstd, sum);
     }
     const float mean = row_sum<kMostRowLanes>(sum, kMostRowLanes, part) / static_cast<float>(a.cols);
-    for (int c = static_cast<int>(threadIdx.x) * 8; c < a.cols; c += kMostRowLanes * 8) {
+    for (int c = first_column<WHOLE>(static_cast<int>(threadIdx.x)); c < a.cols; c += kMostRowLanes * 8) {
         Eight<T> t, g, more;
         Eight<W> w;
         t.template load<WHOLE>(total + c, a.cols - c);
