@@ -52,15 +52,9 @@ struct Eight {
         }
     }
     __device__ __forceinline__ float get(int i) const { return part[i / kPer].get(i % kPer); }
-    __device__ __forceinline__ void set(int i, float v) { part[i / kPer].set(i % kPer, v); }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = get(i);
-    }
-    __device__ __forceinline__ void set(const float (&v)[8]) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) set(i, v[i]);
-    }
+    // ... and all of them in pairs, as fp32 instructions take them
+    __device__ __forceinline__ void get(Pair (&v)[4]) const { to_pairs(part, v); }
+    __device__ __forceinline__ void set(const Pair (&v)[4]) { from_pairs(v, part); }
 };
 
 // Two numbers as e4m3 (to nearest even, at most 448 in size): lo in the lower byte.
@@ -69,10 +63,15 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint2 e4m3_eight(const float (&v)[8], float inverse) {
+__device__ __forceinline__ uint2 e4m3_eight(const Pair (&v)[4], float inverse) {
+    const Pair by(inverse, inverse);
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = e4m3_pair(v[2 * i] * inverse, v[2 * i + 1] * inverse);
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        mul2(v[i], by).get(lo, hi);
+        w[i] = e4m3_pair(lo, hi);
+    }
     return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
@@ -89,10 +88,14 @@ __device__ __forceinline__ void store_bytes(uint8_t* p, int n, uint2 v) {
 }
 
 // The largest size among eight numbers (NaN aside, which fmaxf passes over).
-__device__ __forceinline__ float largest(const float (&v)[8]) {
+__device__ __forceinline__ float largest(const Pair (&v)[4]) {
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        v[i].get(lo, hi);
+        m = fmaxf(fmaxf(m, fabsf(lo)), fabsf(hi));
+    }
     return m;
 }
 // ... among 16 lanes, which hold 128 columns, in each of them.

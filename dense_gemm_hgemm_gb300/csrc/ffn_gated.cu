@@ -270,12 +270,20 @@ __global__ void __launch_bounds__(kGradThreads) gate_grad_kernel(const T* gate_u
     g.template load<true>(gate_up + row * 2 * F + c, 8);
     u.template load<true>(gate_up + row * 2 * F + F + c, 8);
     d.template load<true>(dh + row * F + c, 8);
+    gbt::Pair gate[4], up[4], grad[4];
+    g.get(gate);
+    u.get(up);
+    d.get(grad);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float2 a = gate_and_slope<ACT>(g.get(i));
-        g.set(i, d.get(i) * u.get(i) * a.y);
-        u.set(i, d.get(i) * a.x);
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        gate[i].get(lo, hi);
+        const float2 a = gate_and_slope<ACT>(lo), b = gate_and_slope<ACT>(hi);
+        gate[i] = gbt::mul2(gbt::mul2(grad[i], up[i]), gbt::Pair(a.y, b.y));
+        up[i] = gbt::mul2(grad[i], gbt::Pair(a.x, b.x));
     }
+    g.set(gate);
+    u.set(up);
     g.template store<true>(dgate_up + row * 2 * F + c, 8);
     u.template store<true>(dgate_up + row * 2 * F + F + c, 8);
 }

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kQuantThreads, (sizeof(T) == 2 ? 3 : 2) + (kHe
         float m = 0.f;
 #pragma unroll
         for (int k = 0; k < kPacks; ++k) {
-            float v[8];
+            Pair v[4];
             held[k].get(v);
             m = fmaxf(m, largest(v));
         }
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kQuantThreads, (sizeof(T) == 2 ? 3 : 2) + (kHe
 #pragma unroll
         for (int k = 0; k < kPacks; ++k) {
             const int r = row0 + row + 16 * k;
-            float v[8];
+            Pair v[4];
             held[k].get(v);
             if constexpr (!SQUARE) {
                 const float s = scale_of(largest_of_group(largest(v)));
@@ -103,9 +103,9 @@ __global__ void __launch_bounds__(kQuantThreads, (sizeof(T) == 2 ? 3 : 2) + (kHe
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float inverse = 1.f / scale_of(__uint_as_float(high[SQUARE ? 0 : column(i)]));
-            float down[8];
+            Pair down[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) down[k] = held[k].get(i);
+            for (int k = 0; k < 4; ++k) down[k] = Pair(held[2 * k].get(i), held[2 * k + 1].get(i));
             turned[column(i) * 16 + (row ^ turn(column(i)))] = e4m3_eight(down, inverse);
         }
         __syncthreads();

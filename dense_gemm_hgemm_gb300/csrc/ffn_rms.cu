@@ -67,17 +67,43 @@ struct RmsForwardArgs {
 // x + residual as it is kept: an fp32 sum (one rounding), rounded to T.
 template <typename T>
 __device__ __forceinline__ void add_eight(Eight<T>& x, const Eight<T>& residual) {
+    Pair v[4], r[4];
+    x.get(v);
+    residual.get(r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x.set(i, x.get(i) + residual.get(i));
+    for (int i = 0; i < 4; ++i) v[i] = add2(v[i], r[i]);
+    x.set(v);
+}
+
+// sum + the squares of eight columns
+template <typename T>
+__device__ __forceinline__ Pair add_squares(const Eight<T>& t, Pair sum) {
+    Pair v[4];
+    t.get(v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum = fma2(v[i], v[i], sum);
+    return sum;
+}
+
+__device__ __forceinline__ float both(Pair v) {
+    float lo, hi;
+    v.get(lo, hi);
+    return lo + hi;
 }
 
 // y of eight columns from t, and its conversion where Q8 (all lanes of a warp come here).
 template <typename T, typename W, bool Q8, bool WHOLE>
 __device__ __forceinline__ void finish_eight(const RmsForwardArgs<T, W>& a, int64_t row, int c, int n, float rstd,
                                              const Eight<T>& t, const Eight<W>& gamma) {
-    float y[8];
+    Pair y[4], w[4];
+    t.get(y);
+    gamma.get(w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = a.gamma ? t.get(i) * rstd * gamma.get(i) : t.get(i) * rstd;
+    for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], Pair(rstd, rstd));
+    if (a.gamma) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], w[i]);
+    }
     if constexpr (Q8) {
         const float s = scale_of(largest_of_group(largest(y)));
         if (n > 0 && c % kGroup == 0) a.scales[row * a.lds + c / kGroup] = s;
@@ -89,51 +115,79 @@ __device__ __forceinline__ void finish_eight(const RmsForwardArgs<T, W>& a, int6
     }
 }
 
+// What a lane needs of a row, as it is in memory.
+template <typename T, bool WHOLE>
+struct RmsInput {
+    Eight<T> x[kRowPacks], r[kRowPacks];
+    template <typename W>
+    __device__ __forceinline__ void load(const RmsForwardArgs<T, W>& a, int64_t row, int lane) {
+        const bool there = row < a.rows;
+#pragma unroll
+        for (int k = 0; k < kRowPacks; ++k) {
+            const int c = first_column<WHOLE>(k * a.lanes + lane);
+            x[k].template load<WHOLE>(a.x + row * a.ldx + c, there ? a.cols - c : 0);
+            r[k].template load<WHOLE>(a.residual + row * a.ldr + c, there && a.residual ? a.cols - c : 0);
+        }
+    }
+};
+
+// Blocks of a forward kernel that share an SM (its registers: 80 a thread, 64 with 1024).
+constexpr int forward_blocks_an_sm(int block) { return block < 1024 ? 768 / block > 0 ? 768 / block : 1 : 1; }
+
 // A row is held by `lanes` threads, 16 columns each: it is read once, and its sum of squares
-// and results come from registers.  Bound by memory; the loads in flight are those of the
-// blocks that share an SM, so a block does not look beyond its rows.
+// and results come from registers.  A block goes over rows blockIdx.x, + gridDim.x, ... (BLOCK /
+// lanes at a time); the next row's loads are in flight during the present one's sum (not with
+// 1024 threads, whose registers do not hold two rows).
 template <typename T, typename W, int BLOCK, bool Q8, bool WHOLE>
-__global__ void __launch_bounds__(BLOCK) rms_forward_kernel(const RmsForwardArgs<T, W> a) {
-    __shared__ float part[BLOCK / 32];
+__global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK)) rms_forward_kernel(const RmsForwardArgs<T, W> a) {
+    constexpr bool kAhead = BLOCK <= 512;
+    __shared__ float part[2][BLOCK / 32];
     const int lane = static_cast<int>(threadIdx.x) & (a.lanes - 1);
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (BLOCK / a.lanes) + threadIdx.x / a.lanes;
-    const bool there = row < a.rows;
+    const int groups = BLOCK / a.lanes, group = static_cast<int>(threadIdx.x) / a.lanes;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     wait_for_previous_kernel();
     let_next_kernel_start();
-    Eight<T> t[kRowPacks], r[kRowPacks];
+    int turn = 0;
+    RmsInput<T, WHOLE> next;
+    if (kAhead) next.load(a, static_cast<int64_t>(blockIdx.x) * groups + group, lane);
     Eight<W> gamma[kRowPacks];
-#pragma unroll
-    for (int k = 0; k < kRowPacks; ++k) {
-        const int c = first_column<WHOLE>(k * a.lanes + lane);
-        t[k].template load<WHOLE>(a.x + row * a.ldx + c, there ? a.cols - c : 0);
-        r[k].template load<WHOLE>(a.residual + row * a.ldr + c, there && a.residual ? a.cols - c : 0);
-    }
 #pragma unroll
     for (int k = 0; k < kRowPacks; ++k) {
         const int c = first_column<WHOLE>(k * a.lanes + lane);
         gamma[k].template load<WHOLE>(a.gamma + c, a.gamma ? a.cols - c : 0);
     }
-    float sum = 0.f;
+    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups; row0 < a.rows; row0 += step) {
+        const int64_t row = row0 + group;
+        const bool there = row < a.rows;
+        RmsInput<T, WHOLE> now;
+        if constexpr (kAhead) {
+            now = next;
+            next.load(a, row + step, lane);
+        } else {
+            now.load(a, row, lane);
+        }
+        Pair squares(0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < kRowPacks; ++k) {
-        if (a.residual) add_eight(t[k], r[k]);
+        for (int k = 0; k < kRowPacks; ++k) {
+            if (a.residual) add_eight(now.x[k], now.r[k]);
+            squares = add_squares(now.x[k], squares);
+        }
+        if (a.total) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(t[k].get(i), t[k].get(i), sum);
-    }
-    if (a.total) {
+            for (int k = 0; k < kRowPacks; ++k) {
+                const int c = first_column<WHOLE>(k * a.lanes + lane);
+                now.x[k].template store<WHOLE>(a.total + row * a.ldt + c, there ? a.cols - c : 0);
+            }
+        }
+        const float sum = row_sum<BLOCK>(both(squares), a.lanes, part[turn]);
+        turn ^= 1;
+        const float rstd = 1.f / sqrtf(sum / static_cast<float>(a.cols) + a.eps);
+        if (a.rstd && there && lane == 0) a.rstd[row] = rstd;
 #pragma unroll
         for (int k = 0; k < kRowPacks; ++k) {
             const int c = first_column<WHOLE>(k * a.lanes + lane);
-            t[k].template store<WHOLE>(a.total + row * a.ldt + c, there ? a.cols - c : 0);
+            finish_eight<T, W, Q8, WHOLE>(a, row, c, there ? a.cols - c : 0, rstd, now.x[k], gamma[k]);
         }
-    }
-    sum = row_sum<BLOCK>(sum, a.lanes, part);
-    const float rstd = 1.f / sqrtf(sum / static_cast<float>(a.cols) + a.eps);
-    if (a.rstd && there && lane == 0) a.rstd[row] = rstd;
-#pragma unroll
-    for (int k = 0; k < kRowPacks; ++k) {
-        const int c = first_column<WHOLE>(k * a.lanes + lane);
-        finish_eight<T, W, Q8, WHOLE>(a, row, c, there ? a.cols - c : 0, rstd, t[k], gamma[k]);
     }
 }
 
@@ -153,15 +207,14 @@ __global__ void __launch_bounds__(kMostRowLanes) rms_forward_wide_kernel(const R
         r.template load<WHOLE>(residual + c, residual ? n : 0);
         if (residual) add_eight(t, r);
     };
-    float sum = 0.f;
+    Pair squares(0.f, 0.f);
     for (int c = first_column<WHOLE>(static_cast<int>(threadIdx.x)); c < a.cols; c += kMostRowLanes * 8) {
         Eight<T> t;
         sum_at(c, a.cols - c, t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(t.get(i), t.get(i), sum);
+        squares = add_squares(t, squares);
         if (total) t.template store<WHOLE>(total + c, a.cols - c);
     }
-    sum = row_sum<kMostRowLanes>(sum, kMostRowLanes, part);
+    const float sum = row_sum<kMostRowLanes>(both(squares), kMostRowLanes, part);
     const float rstd = 1.f / sqrtf(sum / static_cast<float>(a.cols) + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
     // (a thread reads back only what it wrote: total may be x or the residual.  All lanes of a
@@ -223,14 +276,19 @@ constexpr int backward_blocks_an_sm(int block) { return block < 512 ? 512 / bloc
 template <typename T, typename W, int BLOCK, bool WHOLE>
 __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backward_kernel(const RmsBackwardArgs<T, W> a) {
     constexpr bool kAhead = BLOCK <= 512;
-    extern __shared__ float shared[];            // (where a block has several groups: their sums)
+    extern __shared__ Pair shared[];             // (where a block has several groups: their sums)
     __shared__ float part[2][BLOCK / 32];
     const int lane = static_cast<int>(threadIdx.x) & (a.lanes - 1);
     const int groups = BLOCK / a.lanes, group = static_cast<int>(threadIdx.x) / a.lanes;
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     wait_for_previous_kernel();
     let_next_kernel_start();
-    float dgamma[kRowPacks][8] = {};
+    Pair dgamma[kRowPacks][4];
+#pragma unroll
+    for (int k = 0; k < kRowPacks; ++k) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dgamma[k][i] = Pair(0.f, 0.f);
+    }
     int turn = 0;
     RmsRow<T, WHOLE> next;
     if (kAhead) next.load(a, static_cast<int64_t>(blockIdx.x) * groups + group, lane);
@@ -243,35 +301,47 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
         } else {
             now.load(a, row, lane);
         }
-        float sum = 0.f;
+        // (hat and g are made twice: kept over the sum, they would take the next row's registers)
+        const auto hat_and_g = [&](int k, Pair (&hat)[4], Pair (&d)[4], Pair (&g)[4]) {
+            const int c = first_column<WHOLE>(k * a.lanes + lane);
+            Eight<W> gamma;
+            gamma.template load<WHOLE>(a.gamma + c, a.gamma ? a.cols - c : 0);
+            now.t[k].get(hat);
+            now.dy[k].get(d);
+            gamma.get(g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                hat[i] = mul2(hat[i], Pair(now.rstd, now.rstd));
+                g[i] = a.gamma ? mul2(d[i], g[i]) : d[i];
+            }
+        };
+        Pair products(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < kRowPacks; ++k) {
-            const int c = first_column<WHOLE>(k * a.lanes + lane);
-            Eight<W> w;
-            w.template load<WHOLE>(a.gamma + c, a.gamma ? a.cols - c : 0);
+            Pair hat[4], d[4], g[4];
+            hat_and_g(k, hat, d, g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float hat = now.t[k].get(i) * now.rstd, d = now.dy[k].get(i);
-                dgamma[k][i] = fmaf(d, hat, dgamma[k][i]);
-                sum = fmaf(a.gamma ? d * w.get(i) : d, hat, sum);
+            for (int i = 0; i < 4; ++i) {
+                dgamma[k][i] = fma2(d[i], hat[i], dgamma[k][i]);
+                products = fma2(g[i], hat[i], products);
             }
         }
         if (!a.dx) continue;                     // (all of the block)
-        sum = row_sum<BLOCK>(sum, a.lanes, part[turn]);
+        const float mean = row_sum<BLOCK>(both(products), a.lanes, part[turn]) / static_cast<float>(a.cols);
         turn ^= 1;
-        const float mean = sum / static_cast<float>(a.cols);
 #pragma unroll
         for (int k = 0; k < kRowPacks; ++k) {
             const int c = first_column<WHOLE>(k * a.lanes + lane), n = row < a.rows ? a.cols - c : 0;
-            Eight<W> w;
-            w.template load<WHOLE>(a.gamma + c, a.gamma ? a.cols - c : 0);
-            Eight<T> out;
+            Pair hat[4], d[4], g[4];
+            hat_and_g(k, hat, d, g);
+            now.more[k].get(d);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float d = now.dy[k].get(i), g = a.gamma ? d * w.get(i) : d;
-                const float dx = now.rstd * (g - now.t[k].get(i) * now.rstd * mean);
-                out.set(i, a.dtotal ? dx + now.more[k].get(i) : dx);
+            for (int i = 0; i < 4; ++i) {
+                g[i] = mul2(fma2(hat[i], Pair(-mean, -mean), g[i]), Pair(now.rstd, now.rstd));
+                if (a.dtotal) g[i] = add2(g[i], d[i]);
             }
+            Eight<T> out;
+            out.set(g);
             out.template store<WHOLE>(a.dx + row * a.lddx + c, n);
         }
     }
@@ -281,7 +351,7 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
 #pragma unroll
         for (int k = 0; k < kRowPacks; ++k) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) shared[threadIdx.x * kLaneColumns + k * 8 + i] = dgamma[k][i];
+            for (int i = 0; i < 4; ++i) shared[(k * 4 + i) * BLOCK + threadIdx.x] = dgamma[k][i];
         }
         __syncthreads();
         if (group != 0) return;
@@ -289,8 +359,8 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
 #pragma unroll
             for (int k = 0; k < kRowPacks; ++k) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    dgamma[k][i] += shared[(other * a.lanes + lane) * kLaneColumns + k * 8 + i];
+                for (int i = 0; i < 4; ++i)
+                    dgamma[k][i] = add2(dgamma[k][i], shared[(k * 4 + i) * BLOCK + other * a.lanes + lane]);
             }
         }
     }
@@ -331,11 +401,19 @@ __global__ void __launch_bounds__(kMostRowLanes) rms_dx_wide_kernel(const RmsBac
         g.template load<WHOLE>(dy + c, a.cols - c);
         w.template load<WHOLE>(a.gamma + c, a.gamma ? a.cols - c : 0);
         more.template load<WHOLE>(a.dtotal + row * a.lddt + c, a.dtotal ? a.cols - c : 0);
+        Pair hat[4], v[4], by[4], d[4];
+        t.get(hat);
+        g.get(v);
+        w.get(by);
+        more.get(d);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float dx = rstd * ((a.gamma ? g.get(i) * w.get(i) : g.get(i)) - t.get(i) * rstd * mean);
-            g.set(i, a.dtotal ? dx + more.get(i) : dx);
+        for (int i = 0; i < 4; ++i) {
+            hat[i] = mul2(hat[i], Pair(rstd, rstd));
+            if (a.gamma) v[i] = mul2(v[i], by[i]);
+            v[i] = mul2(fma2(hat[i], Pair(-mean, -mean), v[i]), Pair(rstd, rstd));
+            if (a.dtotal) v[i] = add2(v[i], d[i]);
         }
+        g.set(v);
         g.template store<WHOLE>(a.dx + row * a.lddx + c, a.cols - c);
     }
 }
@@ -390,11 +468,12 @@ __global__ void __launch_bounds__(kJoinThreads) rms_dgamma_join_kernel(const flo
 constexpr int row_block(int lanes) { return lanes < 128 ? 128 : lanes; }
 
 template <typename T, typename W, bool Q8, bool WHOLE>
-gemm_status_t forward(const RmsForwardArgs<T, W>& a, Queue queue) {
+gemm_status_t forward(const RmsForwardArgs<T, W>& a, int sms, Queue queue) {
     if (a.cols > kRowColumns)
         return launch<rms_forward_wide_kernel<T, W, Q8, WHOLE>>(a.rows, kMostRowLanes, 0, queue, 1, a);
     const int block = row_block(a.lanes);
-    const int64_t grid = (a.rows + block / a.lanes - 1) / (block / a.lanes);
+    const int64_t blocks = (a.rows + block / a.lanes - 1) / (block / a.lanes);
+    const int64_t most = static_cast<int64_t>(sms) * forward_blocks_an_sm(block), grid = blocks < most ? blocks : most;
     switch (block) {
         case 128: return launch<rms_forward_kernel<T, W, 128, Q8, WHOLE>>(grid, 128, 0, queue, 1, a);
         case 256: return launch<rms_forward_kernel<T, W, 256, Q8, WHOLE>>(grid, 256, 0, queue, 1, a);
@@ -498,7 +577,7 @@ gemm_status_t gemm_rms_forward(gemm_rms_plan_t p, int64_t rows, const void* x, i
                                           nullptr, rstd, ldx, ldr, ldt, ldy, 0, 0, rows, eps, static_cast<int>(p->cols),
                                           gbt::row_lanes(p->cols)};
         const gbt::Queue queue{stream, p->device};
-        return whole ? gbt::forward<T, W, false, true>(a, queue) : gbt::forward<T, W, false, false>(a, queue);
+        return whole ? gbt::forward<T, W, false, true>(a, p->num_sms, queue) : gbt::forward<T, W, false, false>(a, p->num_sms, queue);
     });
 }
 
@@ -521,7 +600,7 @@ gemm_status_t gemm_rms_forward_fp8(gemm_rms_plan_t p, int64_t rows, const void* 
                                           static_cast<uint8_t*>(q), scales, rstd, ldx, ldr, ldt, 0, ldq, lds, rows, eps,
                                           static_cast<int>(p->cols), gbt::row_lanes(p->cols)};
         const gbt::Queue queue{stream, p->device};
-        return whole ? gbt::forward<T, W, true, true>(a, queue) : gbt::forward<T, W, true, false>(a, queue);
+        return whole ? gbt::forward<T, W, true, true>(a, p->num_sms, queue) : gbt::forward<T, W, true, false>(a, p->num_sms, queue);
     });
 }
 
