@@ -248,8 +248,8 @@ struct RmsBackwardArgs {
     int cols, lanes;
 };
 
-// What a lane needs of a row, as it is in memory.
-template <typename T, bool WHOLE>
+// What a lane needs of a row, as it is in memory (MORE: dtotal too).
+template <typename T, bool WHOLE, bool MORE>
 struct RmsRow {
     Eight<T> t[kRowPacks], dy[kRowPacks], more[kRowPacks];
     float rstd;
@@ -261,7 +261,7 @@ struct RmsRow {
             const int c = first_column<WHOLE>(k * a.lanes + lane), n = there ? a.cols - c : 0;
             t[k].template load<WHOLE>(a.total + row * a.ldt + c, n);
             dy[k].template load<WHOLE>(a.dy + row * a.lddy + c, n);
-            more[k].template load<WHOLE>(a.dtotal + row * a.lddt + c, a.dtotal ? n : 0);
+            if (MORE) more[k].template load<WHOLE>(a.dtotal + row * a.lddt + c, a.dtotal ? n : 0);
         }
         rstd = there ? a.rstd[row] : 0.f;
     }
@@ -272,29 +272,41 @@ constexpr int backward_blocks_an_sm(int block) { return block < 512 ? 512 / bloc
 
 // A block goes over rows blockIdx.x, + gridDim.x, ... (BLOCK / lanes at a time) and keeps its
 // share of the weight's gradient in registers, 16 columns a lane.  The next row's loads are in
-// flight during the present one's sum (not with 1024 threads, whose registers do not hold two rows).
+// flight during the present one's sum (not with 1024 threads, whose registers do not hold two rows:
+// there gamma and dtotal are loaded where they are used, too, and the weight's gradient is in shared
+// memory).
 template <typename T, typename W, int BLOCK, bool WHOLE>
 __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backward_kernel(const RmsBackwardArgs<T, W> a) {
     constexpr bool kAhead = BLOCK <= 512;
-    extern __shared__ Pair shared[];             // (where a block has several groups: their sums)
+    extern __shared__ Pair shared[];             // the weight's gradient: of 1024 threads, or of several groups
     __shared__ float part[2][BLOCK / 32];
     const int lane = static_cast<int>(threadIdx.x) & (a.lanes - 1);
     const int groups = BLOCK / a.lanes, group = static_cast<int>(threadIdx.x) / a.lanes;
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     wait_for_previous_kernel();
     let_next_kernel_start();
+    const auto kept = [&](int k, int i) -> Pair& { return shared[(k * 4 + i) * BLOCK + threadIdx.x]; };
     Pair dgamma[kRowPacks][4];
 #pragma unroll
     for (int k = 0; k < kRowPacks; ++k) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dgamma[k][i] = Pair(0.f, 0.f);
+        for (int i = 0; i < 4; ++i) (kAhead ? dgamma[k][i] : kept(k, i)) = Pair(0.f, 0.f);
     }
     int turn = 0;
-    RmsRow<T, WHOLE> next;
+    Eight<W> gamma[kRowPacks];
+    const auto load_gamma = [&](int k) {
+        const int c = first_column<WHOLE>(k * a.lanes + lane);
+        gamma[k].template load<WHOLE>(a.gamma + c, a.gamma ? a.cols - c : 0);
+    };
+    if constexpr (kAhead) {
+#pragma unroll
+        for (int k = 0; k < kRowPacks; ++k) load_gamma(k);
+    }
+    RmsRow<T, WHOLE, kAhead> next;
     if (kAhead) next.load(a, static_cast<int64_t>(blockIdx.x) * groups + group, lane);
     for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups; row0 < a.rows; row0 += step) {
         const int64_t row = row0 + group;
-        RmsRow<T, WHOLE> now;
+        RmsRow<T, WHOLE, kAhead> now;
         if constexpr (kAhead) {
             now = next;
             next.load(a, row + step, lane);
@@ -303,12 +315,10 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
         }
         // (hat and g are made twice: kept over the sum, they would take the next row's registers)
         const auto hat_and_g = [&](int k, Pair (&hat)[4], Pair (&d)[4], Pair (&g)[4]) {
-            const int c = first_column<WHOLE>(k * a.lanes + lane);
-            Eight<W> gamma;
-            gamma.template load<WHOLE>(a.gamma + c, a.gamma ? a.cols - c : 0);
+            if constexpr (!kAhead) load_gamma(k);
             now.t[k].get(hat);
             now.dy[k].get(d);
-            gamma.get(g);
+            gamma[k].get(g);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 hat[i] = mul2(hat[i], Pair(now.rstd, now.rstd));
@@ -322,7 +332,8 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
             hat_and_g(k, hat, d, g);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                dgamma[k][i] = fma2(d[i], hat[i], dgamma[k][i]);
+                Pair& to = kAhead ? dgamma[k][i] : kept(k, i);
+                to = fma2(d[i], hat[i], to);
                 products = fma2(g[i], hat[i], products);
             }
         }
@@ -334,6 +345,7 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
             const int c = first_column<WHOLE>(k * a.lanes + lane), n = row < a.rows ? a.cols - c : 0;
             Pair hat[4], d[4], g[4];
             hat_and_g(k, hat, d, g);
+            if constexpr (!kAhead) now.more[k].template load<WHOLE>(a.dtotal + row * a.lddt + c, a.dtotal ? n : 0);
             now.more[k].get(d);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -346,12 +358,19 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
         }
     }
     if (!a.partial) return;
+    if constexpr (!kAhead) {
+#pragma unroll
+        for (int k = 0; k < kRowPacks; ++k) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dgamma[k][i] = kept(k, i);
+        }
+    }
     float* to = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols;
     if (groups > 1) {
 #pragma unroll
         for (int k = 0; k < kRowPacks; ++k) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) shared[(k * 4 + i) * BLOCK + threadIdx.x] = dgamma[k][i];
+            for (int i = 0; i < 4; ++i) kept(k, i) = dgamma[k][i];
         }
         __syncthreads();
         if (group != 0) return;
@@ -492,7 +511,7 @@ int64_t backward_grid(int64_t rows, int lanes, int sms) {
 template <typename T, typename W, bool WHOLE>
 gemm_status_t backward(const RmsBackwardArgs<T, W>& a, int64_t grid, Queue queue) {
     const int block = row_block(a.lanes);
-    const size_t smem = block > a.lanes ? static_cast<size_t>(block) * kLaneColumns * sizeof(float) : 0;
+    const size_t smem = block > a.lanes || block == kMostRowLanes ? static_cast<size_t>(block) * kLaneColumns * sizeof(float) : 0;
     switch (block) {
         case 128: return launch<rms_backward_kernel<T, W, 128, WHOLE>>(grid, 128, smem, queue, 1, a);
         case 256: return launch<rms_backward_kernel<T, W, 256, WHOLE>>(grid, 256, smem, queue, 1, a);
@@ -507,6 +526,18 @@ gemm_status_t with_types(const gemm_rms_plan* p, F f) {
         if (p->weight_elem == GEMM_ELEM_F32) return f(t, float());
         return f(t, t);
     });
+}
+
+// Lets the kernels of long rows have the shared memory that they ask for.
+template <typename T, typename W>
+gemm_status_t prepare() {
+    constexpr int kBytes = kMostRowLanes * kLaneColumns * static_cast<int>(sizeof(float));
+    constexpr auto kAttribute = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    if (cudaFuncSetAttribute(rms_backward_kernel<T, W, kMostRowLanes, true>, kAttribute, kBytes) == cudaSuccess &&
+        cudaFuncSetAttribute(rms_backward_kernel<T, W, kMostRowLanes, false>, kAttribute, kBytes) == cudaSuccess)
+        return GEMM_OK;
+    cudaGetLastError();
+    return GEMM_ERR_LAUNCH;
 }
 
 gemm_status_t check_forward(const gemm_rms_plan* p, int64_t rows, const void* x, int64_t ldx, const void* residual,
@@ -555,6 +586,11 @@ gemm_status_t gemm_rms_plan_create(int64_t max_rows, int64_t cols, gemm_elem_t e
     p->device = device;
     p->num_sms = sms;
     p->partial = static_cast<float*>(memory);
+    const gemm_status_t ready = gbt::with_types(p, [](auto t, auto v) { return gbt::prepare<decltype(t), decltype(v)>(); });
+    if (ready != GEMM_OK) {
+        gemm_rms_plan_destroy(p);
+        return ready;
+    }
     *plan = p;
     return GEMM_OK;
 }
