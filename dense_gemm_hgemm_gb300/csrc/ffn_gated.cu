@@ -18,7 +18,10 @@ namespace {
 
 constexpr int kPairStages = 6;
 constexpr int kTileF = 128;                       // columns of H in a tile
+constexpr int kPairEpilogue = 8;                  // epilogue warps: two to each quarter of the TMEM lanes
+constexpr int kPairThreads = 64 + 32 * kPairEpilogue;
 using PairLayout = SmemLayout2<2 * kTileF, kPairStages, 1>;
+static_assert(kPairEpilogue * PairLayout::kStoreBufBytes <= PairLayout::kStagingBytes, "a store buffer a warp");
 
 struct GatedParams {
     int32_t M, F;
@@ -34,9 +37,10 @@ struct GatedParams {
 // tcgen05.mma of 256 x 256.  In such a pair each CTA brings half of the B operand, so the
 // leader brings the gate's rows and its peer the other half's: both products of one column of
 // H end in the same TMEM lane, columns c and 128 + c, and the epilogue has them side by side.
-// The main loop is the plain product's (gemm_kernel_2cta.cuh), bound by the tensor cores.
+// The main loop is the plain product's (gemm_kernel_2cta.cuh), bound by the tensor cores; eight
+// epilogue warps of 64 columns keep the activation behind it.
 template <int OUT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     gated_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_gate,
                       const __grid_constant__ CUtensorMap tmap_up, const __grid_constant__ CUtensorMap tmap_h,
                       const __grid_constant__ CUtensorMap tmap_keep_gate, const __grid_constant__ CUtensorMap tmap_keep_up,
@@ -70,7 +74,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_addr(&ctl->tmem_full[b]), 1);
-            mbar_init(smem_addr(&ctl->tmem_empty[b]), 2 * kEpiWarps);
+            mbar_init(smem_addr(&ctl->tmem_empty[b]), 2 * kPairEpilogue);
         }
         mbar_init(smem_addr(&ctl->drain), 1);
         ctl->abort = 0;
@@ -169,60 +173,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        const int quad = warp & 3;
-        const uint32_t lanes_at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
-        const uint32_t store_buf = staging + static_cast<uint32_t>((warp - 2) * 2 * L::kStoreBufBytes);
-        uint32_t sel = 0, turn = 0;
-        // 64 columns of 32 rows, through one of the warp's two buffers
-        const auto store = [&](const CUtensorMap* map, const uint32_t (&v)[64], int32_t x, int32_t y) {
-            const uint32_t buf = store_buf + sel * L::kStoreBufBytes;
-            if (lane == 0) bulk_wait_group_read<1>();
+        const int quad = warp & 3, c = ((warp - 2) >> 2) * 64;
+        const uint32_t lanes_at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(c);
+        const uint32_t store_buf = staging + static_cast<uint32_t>((warp - 2) * L::kStoreBufBytes);
+        uint32_t turn = 0;
+        // 64 columns of 32 rows through the warp's buffer, 32 columns of them at a time
+        const auto store = [&](const CUtensorMap* map, int32_t x, int32_t y, auto columns) {
+            if (lane == 0) bulk_wait_group_read<0>();
             __syncwarp();
-            uint32_t w[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = pack2<OUT>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-            stage_store_row(buf, lane, 0, w, 8);
+            for (int h = 0; h < 2; ++h) {
+                uint32_t v[32], w[16];
+                columns(h * 32, v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = pack2<OUT>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                stage_store_row(store_buf, lane, h * 4, w, 4);
+            }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                tma_store_2d(map, buf, x, y);
+                tma_store_2d(map, store_buf, x, y);
                 bulk_commit_group();
             }
-            sel ^= 1u;
         };
         for (int32_t u = pair; u < p.num_units; u += npairs, ++turn) {
             int32_t m_blk, f_blk;
             raster_tile_fast(p.m_blocks, p.rd, u, &m_blk, &f_blk);
-            const int32_t y = (2 * m_blk + static_cast<int32_t>(rank)) * kBM + quad * 32;
-            const uint32_t buf = turn & 1u;
+            const int32_t y = (2 * m_blk + static_cast<int32_t>(rank)) * kBM + quad * 32, x = f_blk * kTileF + c;
+            const uint32_t buf = turn & 1u, gate_at = lanes_at + buf * kBN, up_at = gate_at + kTileF;
             if (!wait_phase(smem_addr(&ctl->tmem_full[buf]), (turn >> 1) & 1u, watch, kSiteEpiTmemFull)) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < kTileF; c += 64) {
-                const int32_t x = f_blk * kTileF + c;
-                if (y >= p.M || x >= p.F) continue;      // (the whole warp)
-                uint32_t g[64], v[64];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    tmem_ld_32x32b_x32(lanes_at + buf * kBN + c + h * 32, reinterpret_cast<uint32_t(&)[32]>(g[h * 32]));
-                    tmem_ld_32x32b_x32(lanes_at + buf * kBN + kTileF + c + h * 32,
-                                       reinterpret_cast<uint32_t(&)[32]>(v[h * 32]));
-                }
-                tmem_ld_wait();
+            if (y < p.M && x < p.F) {                    // (the whole warp)
+                const auto products = [&](uint32_t at) {
+                    return [=](int col, uint32_t (&v)[32]) {
+                        tmem_ld_32x32b_x32(at + static_cast<uint32_t>(col), v);
+                        tmem_ld_wait();
+                    };
+                };
                 if (p.keep) {
-                    store(&tmap_keep_gate, g, x, y);
-                    store(&tmap_keep_up, v, x, y);
+                    store(&tmap_keep_gate, x, y, products(gate_at));
+                    store(&tmap_keep_up, x, y, products(up_at));
                 }
                 with_act(p.act, [&](auto act) {
+                    store(&tmap_h, x, y, [&](int col, uint32_t (&v)[32]) {
+                        uint32_t g[32];
+                        tmem_ld_32x32b_x32(gate_at + static_cast<uint32_t>(col), g);
+                        tmem_ld_32x32b_x32(up_at + static_cast<uint32_t>(col), v);
+                        tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        v[i] = __float_as_uint(gate_fn<decltype(act)::value>(__uint_as_float(g[i])) * __uint_as_float(v[i]));
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = __float_as_uint(gate_fn<decltype(act)::value>(__uint_as_float(g[i])) * __uint_as_float(v[i]));
+                    });
                 });
-                store(&tmap_h, v, x, y);
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(map_to_rank(smem_addr(&ctl->tmem_empty[buf]), 0));
+            if (lane == 0) arrive_leader(smem_addr(&ctl->tmem_empty[buf]));
         }
     }
 
@@ -246,9 +252,8 @@ template <int ACT>
 __device__ __forceinline__ float2 gate_and_slope(float g) {
     if constexpr (ACT == GEMM_ACT_RELU) return make_float2(gate_fn<ACT>(g), g > 0.f ? 1.f : 0.f);
     if constexpr (ACT == GEMM_ACT_GELU) {
-        const float phi = 0.5f * erfcf(g * -0.70710678118654752f);
-        const float density = 0.39894228040143268f * __expf(-0.5f * g * g);
-        return make_float2(g * phi, density == 0.f ? phi : fmaf(g, density, phi));   // (inf * 0)
+        const float e = bell(g), phi = normal_cdf(g, e);
+        return make_float2(g * phi, e == 0.f ? phi : fmaf(g, 0.39894228f * e, phi));   // (inf * 0)
     }
     if constexpr (ACT == GEMM_ACT_SILU) {
         const float s = sigmoid(g), rest = sigmoid(-g);
@@ -372,7 +377,7 @@ gemm_status_t forward_many(const gemm_gated_plan* p, const void* X, const void* 
     // bands of eight row blocks: the 76 pairs cover about 8 x 9 tiles at a time
     g.rd = make_raster_div(g.m_blocks, f_blocks, g.m_blocks < 8 ? g.m_blocks : 8);
     const int pairs = p->base.num_sms / 2;
-    return gbt::launch<gated_pair_kernel<OUT>>(2 * (g.num_units < pairs ? g.num_units : pairs), kThreads, PairLayout::kTotal,
+    return gbt::launch<gated_pair_kernel<OUT>>(2 * (g.num_units < pairs ? g.num_units : pairs), kPairThreads, PairLayout::kTotal,
                                                queue, 2, x, gate, up, h, keep_gate, keep_up, g);
 }
 

@@ -83,11 +83,34 @@ __device__ __forceinline__ float sigmoid(float g) {
     const float s = __fdividef(1.f, 1.f + e);
     return g < 0.f ? e * s : s;
 }
-// act(g) of gemm_activation_t, with the lower tails to relative accuracy (erfc, not 1 + erf).
+// exp(-g^2 / 2)
+__device__ __forceinline__ float bell(float g) {
+    const float w = g * 0.84932180f;                  // sqrt(log2(e) / 2)
+    return gbt::exp2_fast(-(w * w));
+}
+// The normal distribution's Phi(g), both tails to relative accuracy, with e = bell(g).  For z =
+// |g| / sqrt 2 the upper tail is erfc(z) / 2 = exp(-z^2) t Q(t) / 2 with t = 1 / (1 + 0.45 z): a smooth
+// function of t in (0, 1], here a polynomial of degree 7 fitted to erfc(z) exp(z^2) / t for z up to 10
+// (weighted least squares, the weights moved to the largest relative errors; 3.1e-7 at most).
+// With the exponential's rounding 1e-6 for |g| up to 4 and 1.2e-5 at 12.  erfcf took 6 us more of
+// 1024 x 4096 x 2048 (23 us with SiLU).
+__device__ __forceinline__ float normal_cdf(float g, float e) {
+    const float t = __fdividef(1.f, fmaf(0.45f * 0.70710678f, fabsf(g), 1.f));
+    float q = fmaf(6.684802473e-02f, t, -2.401618809e-01f);
+    q = fmaf(q, t, 2.086041719e-01f);
+    q = fmaf(q, t, 4.054885730e-02f);
+    q = fmaf(q, t, 1.884976625e-01f);
+    q = fmaf(q, t, 2.281251252e-01f);
+    q = fmaf(q, t, 2.536289692e-01f);
+    q = fmaf(q, t, 2.539093792e-01f);
+    q *= 0.5f * t * e;
+    return g < 0.f ? q : 1.f - q;
+}
+// act(g) of gemm_activation_t, with the lower tails to relative accuracy.
 template <int ACT>
 __device__ __forceinline__ float gate_fn(float g) {
     if constexpr (ACT == GEMM_ACT_RELU) return fmaxf(g, 0.f) + (g != g ? g : 0.f);
-    if constexpr (ACT == GEMM_ACT_GELU) return 0.5f * g * erfcf(g * -0.70710678118654752f);
+    if constexpr (ACT == GEMM_ACT_GELU) return g * normal_cdf(g, bell(g));
     if constexpr (ACT == GEMM_ACT_SILU) return g * sigmoid(g);
     return g;
 }
