@@ -19,18 +19,18 @@ constexpr int kSumWarps = 8;                      // of a CTA
 constexpr int kFirstSumWarp = 4;                  // after the copies', the MMAs' and the column scales' two
 constexpr int kPairThreads = 32 * (kFirstSumWarp + kSumWarps);
 // Registers of a thread: 168 at the launch; the first warpgroup's go to the other two.
-constexpr int kLaunchRegisters = 168, kFewRegisters = 88, kSumRegisters = 208;
+constexpr int kLaunchRegisters = 168, kFewRegisters = 72, kSumRegisters = 216;
 static_assert(128 * kFewRegisters + 256 * kSumRegisters <= kPairThreads * kLaunchRegisters, "registers of the block");
 
 // BYROW: B's scales go by rows.
 template <bool BYROW>
 struct Fp8Layout {
-    static constexpr int kStages = BYROW ? 5 : 6;
+    static constexpr int kStages = BYROW ? 4 : 6;
     static constexpr int kStageBytes = 2 * kTileSlot;                  // A and this CTA's half of B
     static constexpr int kRing = kStages * kStageBytes;
     static constexpr int kStoreBuf = 32 * kRowBytes;
     static constexpr int kStaging = kSumWarps * kStoreBuf;
-    static constexpr int kScales = BYROW ? 4 * 256 * 4 : 0;
+    static constexpr int kScales = BYROW ? 4 * (256 + kTileSide) * 16 : 0;
     static constexpr int kTotal = 1024 + kRing + kStaging + 256 + kScales;
     static_assert(kTotal <= 232448, "exceeds the 227 KiB a CTA may use");
 };
@@ -39,6 +39,7 @@ struct Fp8Params {
     int32_t M, N;
     int32_t num_kb, m_blocks, num_units;
     uint32_t idesc, tx_extra;
+    bool whole_scales;                            // by rows: their rows move in fours
     const float* a_scales;
     const float* b_scales;
     int32_t* error_word;
@@ -51,8 +52,28 @@ struct Fp8Params {
 __device__ __forceinline__ void fetch_scale(uint32_t to, const float* from) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
+__device__ __forceinline__ void fetch_scales(uint32_t to, const float* from) {      // four, 16-byte aligned
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
 __device__ __forceinline__ void arrive_when_fetched(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ gbt::Pair ld_shared_twice(uint32_t saddr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(saddr) : "memory");
+    gbt::Pair p;
+    asm volatile("mov.b64 %0, {%1, %1};" : "=l"(p.bits) : "f"(v));
+    return p;
+}
+// Values 16 bytes apart.
+__device__ __forceinline__ gbt::Pair ld_shared_pair(uint32_t saddr) {
+    float lo, hi;
+    asm volatile("ld.shared.f32 %0, [%2];\n\tld.shared.f32 %1, [%2 + 16];" : "=f"(lo), "=f"(hi) : "r"(saddr) : "memory");
+    return gbt::Pair(lo, hi);
+}
+__device__ __forceinline__ void st_shared_u1(uint32_t saddr, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(saddr), "r"(v) : "memory");
 }
 
 template <int STAGES>
@@ -81,7 +102,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     const __grid_constant__ CUtensorMap tmap_c, const Fp8Params p) {
     using L = Fp8Layout<BYROW>;
     constexpr int kStages = L::kStages;
-    constexpr int kBN = 256, kHalf = 128, kStep = BYROW ? 16 : 16;
+    constexpr int kBN = 256, kHalf = 128, kStep = 16;
     constexpr uint32_t kPairTx = 2 * L::kStageBytes;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -89,7 +110,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t ring = smem_addr(smem), ring_b = ring + kStages * kTileSlot;
     const uint32_t staging = ring + L::kRing;
     Fp8Ctl<kStages>* ctl = reinterpret_cast<Fp8Ctl<kStages>*>(smem + L::kRing + L::kStaging);
-    const uint32_t col_scales = staging + L::kStaging + 256;      // BYROW: [4][256] fp32, of four steps in turn
+    // BYROW: the scales of the tile's 256 columns and of this CTA's 128 rows, for four steps; four such slots
+    constexpr uint32_t kSlot = (kBN + kBM) * 16;
+    const uint32_t scales = staging + L::kStaging + 256;
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / 32, 0);
     const int lane = static_cast<int>(threadIdx.x) & 31;
@@ -216,27 +239,37 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
             __syncwarp();
         } else if constexpr (BYROW) {
-            // the scales of the tile's columns, four a thread, up to four steps ahead
+            // the scales of the tile's columns and rows, of six of them a thread, four steps at a time
             const int first = static_cast<int>(threadIdx.x) - 64;
             uint32_t turn = 0;
             bool ok = true;
             for (int32_t u = pair; ok && u < p.num_units; u += npairs) {
                 int32_t m_blk, n_blk;
                 raster_tile_fast(p.m_blocks, p.rd, u, &m_blk, &n_blk);
-                const float* from[4];                    // (columns outside C take the last one's)
+                const int32_t row = (2 * m_blk + static_cast<int32_t>(rank)) * kBM;
+                const float* from[6];                    // (rows and columns outside C take the last one's)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    from[i] = p.b_scales + static_cast<int64_t>(min(n_blk * kBN + first + 64 * i, p.N - 1)) * p.num_kb;
-                for (int32_t kb = 0; kb < p.num_kb; ++kb, ++turn) {
+                for (int i = 0; i < 6; ++i) {
+                    const int at = first + 64 * i;
+                    from[i] = i < 4 ? p.b_scales + static_cast<int64_t>(min(n_blk * kBN + at, p.N - 1)) * p.num_kb
+                                    : p.a_scales + static_cast<int64_t>(min(row + at - kBN, p.M - 1)) * p.num_kb;
+                }
+                for (int32_t kb = 0; kb < p.num_kb; kb += 4, ++turn) {
                     const uint32_t slot = turn & 3u;
                     if (turn >= 4 && !wait_phase(smem_addr(&ctl->scales_empty[slot]), ((turn >> 2) & 1u) ^ 1u, watch,
                                                  kSiteProducerEmpty)) {
                         ok = false;
                         break;
                     }
+                    const uint32_t to = scales + slot * kSlot + static_cast<uint32_t>(first) * 16;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        fetch_scale(col_scales + (slot * kBN + static_cast<uint32_t>(first + 64 * i)) * 4, from[i] + kb);
+                    for (int i = 0; i < 6; ++i) {
+                        if (p.whole_scales) {
+                            fetch_scales(to + 64 * 16 * i, from[i] + kb);
+                        } else {
+                            for (int k = 0; k < 4 && kb + k < p.num_kb; ++k) fetch_scale(to + 64 * 16 * i + 4 * k, from[i] + kb + k);
+                        }
+                    }
                     arrive_when_fetched(smem_addr(&ctl->scales_full[slot]));
                 }
             }
@@ -248,98 +281,144 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const int quad = warp & 3, half = (warp - kFirstSumWarp) >> 2;
         const uint32_t acc_at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(half * kHalf);
         const uint32_t buf_at = staging + static_cast<uint32_t>((warp - kFirstSumWarp) * L::kStoreBuf);
-        uint32_t turn = 0;
+        uint32_t turn = 0, four = 0;                         // steps; BYROW: runs of four
         bool ok = true;
         for (int32_t u = pair; ok && u < p.num_units; u += npairs) {
             int32_t m_blk, n_blk;
             raster_tile_fast(p.m_blocks, p.rd, u, &m_blk, &n_blk);
-            const int32_t y = (2 * m_blk + static_cast<int32_t>(rank)) * kBM + quad * 32, row = y + lane;
+            const int32_t y = (2 * m_blk + static_cast<int32_t>(rank)) * kBM + quad * 32;
             const int32_t x = n_blk * kBN + half * kHalf;
-            float acc[kHalf];
-#pragma unroll
-            for (int c = 0; c < kHalf; ++c) acc[c] = 0.f;
-            // (rows and columns outside C take the last one's scales, and are not stored)
-            ScaleRow sa, sb;
-            sa.begin(p.a_scales + static_cast<int64_t>(min(row, p.M - 1)) * p.num_kb, 0);
-            if constexpr (!BYROW) sb.begin(p.b_scales + static_cast<int64_t>(min(x, p.N - 1) / kHalf) * p.num_kb, 0);
-            for (int32_t kb = 0; kb < p.num_kb; ++kb, ++turn) {
-                const uint32_t buf = turn & 1u;
-                float s = sa.get(kb + 1 < p.num_kb);
-                if constexpr (BYROW) {
-                    ok = wait_phase(smem_addr(&ctl->scales_full[turn & 3u]), (turn >> 2) & 1u, watch, kSiteEpiTmemFull);
-                } else {
-                    s *= sb.get(kb + 1 < p.num_kb);
-                }
-                const gbt::Pair s2(s, s);
-                // BYROW: the products of both scales for a step's columns, made while the sums before them arrive
-                gbt::Pair w[2][kStep / 2];
-                const uint32_t scales_at = col_scales + ((turn & 3u) * kBN + static_cast<uint32_t>(half * kHalf)) * 4;
-                float4 f[kStep / 4];
-                const auto read_scales = [&](int c) {
-#pragma unroll
-                    for (int j = 0; j < kStep / 4; ++j)
-                        f[j] = ld_shared_f4(scales_at + static_cast<uint32_t>((c * kStep + 4 * j) * 4));
-                };
-                const auto join_scales = [&](int c) {
-#pragma unroll
-                    for (int j = 0; j < kStep / 4; ++j) {
-                        w[c & 1][2 * j] = gbt::mul2(gbt::Pair(f[j].x, f[j].y), s2);
-                        w[c & 1][2 * j + 1] = gbt::mul2(gbt::Pair(f[j].z, f[j].w), s2);
-                    }
-                };
-                if constexpr (BYROW) {
-                    if (ok) {
-                        read_scales(0);
-                        join_scales(0);
-                        read_scales(1);
-                    }
-                }
-                ok = ok && wait_phase(smem_addr(&ctl->tmem_full[buf][half]), (turn >> 1) & 1u, watch, kSiteEpiTmemFull);
-                if (!ok) break;
-                tc_fence_after();
-                uint32_t v[2][kStep];
-                tmem_read(acc_at + buf * kBN, v[0]);
-#pragma unroll
-                for (int c = 0; c < kHalf / kStep; ++c) {
-                    tmem_arrived(v[c & 1]);
-                    if (c + 1 < kHalf / kStep) {
-                        tmem_read(acc_at + buf * kBN + (c + 1) * kStep, v[(c + 1) & 1]);
-                    } else {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) arrive_leader(smem_addr(&ctl->tmem_empty[buf][half]));
-                    }
-#pragma unroll
-                    for (int j = 0; j < kStep; j += 2) {
-                        const int at = c * kStep + j;
-                        const gbt::Pair t(__uint_as_float(v[c & 1][j]), __uint_as_float(v[c & 1][j + 1]));
-                        gbt::fma2(t, BYROW ? w[c & 1][j / 2] : s2, gbt::Pair(acc[at], acc[at + 1])).get(acc[at], acc[at + 1]);
-                    }
-                    if constexpr (BYROW) {
-                        if (c + 1 < kHalf / kStep) join_scales(c + 1);
-                        if (c + 2 < kHalf / kStep) read_scales(c + 2);
-                    }
-                }
-                if constexpr (BYROW) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_addr(&ctl->scales_empty[turn & 3u]));
-                }
-            }
-            if (!ok) break;
-#pragma unroll
-            for (int c = 0; c < kHalf; c += 64) {
-                if (y >= p.M || x + c >= p.N) continue;      // (the whole warp)
-                uint32_t w[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) w[i] = pack2<OUT>(acc[c + 2 * i], acc[c + 2 * i + 1]);
+            const bool inside = y < p.M;                     // (of the whole warp; columns are looked at below)
+            // 64 columns of the warp's rows, which `place` writes to its buffer
+            const auto store = [&](int c, auto place) {
+                if (!inside || x + c >= p.N) return;
                 if (lane == 0) bulk_wait_group_read<0>();
                 __syncwarp();
-                stage_store_row(buf_at, lane, 0, w, 8);
+                place();
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
                     tma_store_2d(&tmap_c, buf_at, x + c, y);
                     bulk_commit_group();
+                }
+            };
+            float acc[kHalf];
+#pragma unroll
+            for (int c = 0; c < kHalf; ++c) acc[c] = 0.f;
+            if constexpr (!BYROW) {
+                // a thread has a row: one factor for its 128 columns
+                ScaleRow sa, sb;
+                // (rows and columns outside C take the last one's scales, and are not stored)
+                sa.begin(p.a_scales + static_cast<int64_t>(min(y + lane, p.M - 1)) * p.num_kb, 0);
+                sb.begin(p.b_scales + static_cast<int64_t>(min(x, p.N - 1) / kHalf) * p.num_kb, 0);
+                for (int32_t kb = 0; kb < p.num_kb; ++kb, ++turn) {
+                    const uint32_t buf = turn & 1u;
+                    const float s = sa.get(kb + 1 < p.num_kb) * sb.get(kb + 1 < p.num_kb);
+                    ok = wait_phase(smem_addr(&ctl->tmem_full[buf][half]), (turn >> 1) & 1u, watch, kSiteEpiTmemFull);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const gbt::Pair s2(s, s);
+                    uint32_t v[2][kStep];
+                    tmem_read(acc_at + buf * kBN, v[0]);
+#pragma unroll
+                    for (int c = 0; c < kHalf / kStep; ++c) {
+                        tmem_arrived(v[c & 1]);
+                        if (c + 1 < kHalf / kStep) {
+                            tmem_read(acc_at + buf * kBN + (c + 1) * kStep, v[(c + 1) & 1]);
+                        } else {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive_leader(smem_addr(&ctl->tmem_empty[buf][half]));
+                        }
+#pragma unroll
+                        for (int j = 0; j < kStep; j += 2) {
+                            const int at = c * kStep + j;
+                            const gbt::Pair t(__uint_as_float(v[c & 1][j]), __uint_as_float(v[c & 1][j + 1]));
+                            gbt::fma2(t, s2, gbt::Pair(acc[at], acc[at + 1])).get(acc[at], acc[at + 1]);
+                        }
+                    }
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < kHalf; c += 64) {
+                    store(c, [&] {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) w[i] = pack2<OUT>(acc[c + 2 * i], acc[c + 2 * i + 1]);
+                        stage_store_row(buf_at, lane, 0, w, 8);
+                    });
+                }
+            } else {
+                // A factor for each row and column: a thread has two columns in eight of rows lane / 4 + 8 h.
+                // (With a row a thread, each of them read the scales of all 128 columns: 64 KB a step
+                // through the SM's 128 bytes a cycle, 0.92 us a step against XX.)
+                const int group = lane / 4, two = lane % 4;
+                for (int32_t kb = 0; kb < p.num_kb; ++kb, ++turn) {
+                    const uint32_t buf = turn & 1u, place = four & 3u;
+                    const uint32_t slot = scales + place * kSlot + static_cast<uint32_t>(kb & 3) * 4;
+                    if ((kb & 3) == 0)
+                        ok = wait_phase(smem_addr(&ctl->scales_full[place]), (four >> 2) & 1u, watch, kSiteEpiTmemFull);
+                    gbt::Pair s[4];
+                    if (ok) {
+#pragma unroll
+                        for (int h = 0; h < 4; ++h)
+                            s[h] = ld_shared_twice(slot + static_cast<uint32_t>(kBN + quad * 32 + 8 * h + group) * 16);
+                        ok = wait_phase(smem_addr(&ctl->tmem_full[buf][half]), (turn >> 1) & 1u, watch, kSiteEpiTmemFull);
+                    }
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t cols_at = slot + static_cast<uint32_t>(half * kHalf + 2 * two) * 16;
+                    uint32_t v[2][kStep];
+                    tmem_read_by_fours(acc_at + buf * kBN, v[0]);
+                    gbt::Pair w[4];
+                    // step c: columns 32 (c / 2) .. + 31 of the upper or lower 16 rows
+#pragma unroll
+                    for (int c = 0; c < kHalf / kStep; ++c) {
+                        if (c % 2 == 0) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) w[i] = ld_shared_pair(cols_at + static_cast<uint32_t>(16 * c + 8 * i) * 16);
+                        }
+                        tmem_arrived(v[c & 1]);
+                        if (c + 1 < kHalf / kStep) {
+                            tmem_read_by_fours(acc_at + buf * kBN + ((c + 1) / 2) * 32 + (static_cast<uint32_t>((c + 1) % 2 * 16) << 16),
+                                               v[(c + 1) & 1]);
+                        } else {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive_leader(smem_addr(&ctl->tmem_empty[buf][half]));
+                        }
+#pragma unroll
+                        for (int j = 0; j < kStep; j += 2) {
+                            const int at = c * kStep + j;
+                            const gbt::Pair t(__uint_as_float(v[c & 1][j]), __uint_as_float(v[c & 1][j + 1]));
+                            gbt::fma2(gbt::mul2(t, w[j / 4]), s[c % 2 * 2 + j / 2 % 2], gbt::Pair(acc[at], acc[at + 1]))
+                                .get(acc[at], acc[at + 1]);
+                        }
+                    }
+                    if ((kb & 3) == 3 || kb + 1 == p.num_kb) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_addr(&ctl->scales_empty[place]));
+                        ++four;
+                    }
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < kHalf; c += 64) {
+                    store(c, [&] {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {        // 32 columns, 16 rows
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const int at = (c / kStep + k) * kStep + 4 * i + 2 * h;
+                                    const int r = k % 2 * 16 + h * 8 + group, unit = k / 2 * 4 + i;
+                                    st_shared_u1(buf_at + static_cast<uint32_t>(r * kRowBytes + ((unit ^ (r & 7)) * 16) + two * 4),
+                                                 pack2<OUT>(acc[at], acc[at + 1]));
+                                }
+                            }
+                        }
+                    });
                 }
             }
         }
@@ -410,6 +489,7 @@ gemm_status_t run(const gemm_fp8_plan* p, const void* A, const float* a_scales, 
     f.num_units = f.m_blocks * n_blocks;
     f.idesc = descriptor(0, 256, 128);
     f.tx_extra = p->base.tx_extra;
+    f.whole_scales = num_kb % 4 == 0 && gbt::aligned(a_scales, 16) && gbt::aligned(b_scales, 16);
     f.a_scales = a_scales;
     f.b_scales = b_scales;
     f.error_word = p->base.error_word;

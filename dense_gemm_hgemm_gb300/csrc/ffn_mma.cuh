@@ -47,6 +47,18 @@ __device__ __forceinline__ void tmem_read(uint32_t taddr, uint32_t (&r)[8]) {
                  : "memory");
 }
 
+// 16 lanes x 32 consecutive TMEM columns -> 16 registers per thread: for i < 4, registers 4i, 4i + 1 are
+// columns 8i + 2 (t % 4), + 1 of lane t / 4, and 4i + 2, 4i + 3 those of lane t / 4 + 8.
+__device__ __forceinline__ void tmem_read_by_fours(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
 // The registers of a warpgroup (all of its warps): fewer, or more out of what others gave up.
 template <int N> __device__ __forceinline__ void fewer_registers() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
