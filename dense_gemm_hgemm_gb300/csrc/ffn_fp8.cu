@@ -22,16 +22,18 @@ constexpr int kPairThreads = 32 * (kFirstSumWarp + kSumWarps);
 constexpr int kLaunchRegisters = 168, kFewRegisters = 72, kSumRegisters = 216;
 static_assert(128 * kFewRegisters + 256 * kSumRegisters <= kPairThreads * kLaunchRegisters, "registers of the block");
 
-// BYROW: B's scales go by rows.
+// The tiles of a kind of scales (BYROW: B's go by rows): `kParts` parts of 128 columns.
 template <bool BYROW>
 struct Fp8Layout {
-    static constexpr int kStages = BYROW ? 4 : 6;
-    static constexpr int kStageBytes = 2 * kTileSlot;                  // A and this CTA's half of B
-    static constexpr int kRing = kStages * kStageBytes;
+    static constexpr int kParts = BYROW ? 1 : 2;
+    static constexpr int kBN = kTileSide * kParts;
+    static constexpr int kStages = BYROW ? 5 : 6;
+    static constexpr int kBSlot = kTileSlot / 2 * kParts;              // this CTA's 64 rows of each part of B
+    static constexpr int kRing = kStages * (kTileSlot + kBSlot);
     static constexpr int kStoreBuf = 32 * kRowBytes;
     static constexpr int kStaging = kSumWarps * kStoreBuf;
-    static constexpr int kScales = BYROW ? 4 * (256 + kTileSide) * 16 : 0;
-    static constexpr int kTotal = 1024 + kRing + kStaging + 256 + kScales;
+    static constexpr int kScaleSlot = 2 * kTileSide * 16;              // BYROW: of 128 columns and 128 rows, four steps
+    static constexpr int kTotal = 1024 + kRing + kStaging + 256 + (BYROW ? 4 * kScaleSlot : 0);
     static_assert(kTotal <= 232448, "exceeds the 227 KiB a CTA may use");
 };
 
@@ -62,9 +64,7 @@ __device__ __forceinline__ void arrive_when_fetched(uint32_t bar) {
 __device__ __forceinline__ gbt::Pair ld_shared_twice(uint32_t saddr) {
     float v;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(saddr) : "memory");
-    gbt::Pair p;
-    asm volatile("mov.b64 %0, {%1, %1};" : "=l"(p.bits) : "f"(v));
-    return p;
+    return gbt::Pair(v, v);
 }
 // Values 16 bytes apart.
 __device__ __forceinline__ gbt::Pair ld_shared_pair(uint32_t saddr) {
@@ -79,40 +79,44 @@ __device__ __forceinline__ void st_shared_u1(uint32_t saddr, uint32_t v) {
 template <int STAGES>
 struct Fp8Ctl {
     uint64_t full[STAGES], empty[STAGES];
-    uint64_t tmem_full[2][2], tmem_empty[2][2];      // [turn][half of the columns]
+    uint64_t sums_full[4], sums_empty[4];            // of the accumulators, four times 128 columns
     uint64_t scales_full[4], scales_empty[4];        // BYROW
     uint64_t drain;
     uint32_t tmem_base;
     int32_t abort;
 };
+static_assert(sizeof(Fp8Ctl<6>) <= 256, "control block");
 
-// Many rows: a pair of SMs computes 256 x 256 of C, as the plain product's pair does
+// Many rows: a pair of SMs computes 256 rows of C, as the plain product's pair does
 // (gemm_kernel_2cta.cuh).  The tensor cores know no scales, so the sum over each 128 elements of
-// K has an accumulator of its own (two of 256 columns in turn, all of TMEM), which eight warps a CTA
-// multiply by the scales of its row and column and add to fp32 sums in registers, 128 columns a
-// thread.  One such step is 512 cycles of the tensor cores; a thread's share is 128 accumulators
-// from TMEM and 64 fused multiply-adds of two.
-// The two halves of the columns are MMAs and barriers of their own: from the end of a half's
-// MMAs to the next ones into its accumulators the tensor cores have three other halves to do,
-// which hides the way to the warps and back.  So that a half is 128 neighbouring columns
-// (one square of scales), each CTA brings 64 rows of B for each of them.
+// K and 128 columns has an accumulator of its own, four of them in turn (all of TMEM), which eight
+// warps a CTA multiply by the scales of its rows and columns and add to fp32 sums in registers.
+// From the end of an accumulator's MMAs to the next ones into it the tensor cores have three
+// others to do, which hides the way to the warps and back.
+//   squares: tiles of 256 columns.  Four warps take a part of 128 (one square of scales, for which
+//            each CTA brings 64 rows of B); a thread has a row, with one factor for its 128 columns.
+//            A step is 512 cycles of the tensor cores and 128 reads and 64 double multiply-adds of
+//            a thread: 0.43 us, 2.8 PFLOP/s.
+//   by rows: tiles of 128 columns, as there are twice the multiplications.  The eight warps take 64
+//            columns each; a thread has two columns in eight of four rows (with a row a thread, each
+//            of them read the scales of all columns), whose scales two warps bring four steps at a
+//            time (read a step at a time they were 256 lines a step, more than the first-level
+//            cache holds).  2048 x 2304 x 16384: XX us, 93 with 256 columns a tile.
 template <int OUT, bool BYROW>
 __global__ void __launch_bounds__(kPairThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                     const __grid_constant__ CUtensorMap tmap_c, const Fp8Params p) {
     using L = Fp8Layout<BYROW>;
-    constexpr int kStages = L::kStages;
-    constexpr int kBN = 256, kHalf = 128, kStep = 16;
-    constexpr uint32_t kPairTx = 2 * L::kStageBytes;
+    constexpr int kStages = L::kStages, kParts = L::kParts, kBN = L::kBN;
+    constexpr int kPart = kTileSide, kStep = 16;
+    constexpr int kCols = BYROW ? kPart / 2 : kPart;  // of a warp
+    constexpr uint32_t kPairTx = 2 * (kTileSlot + L::kBSlot);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     const uint32_t ring = smem_addr(smem), ring_b = ring + kStages * kTileSlot;
-    const uint32_t staging = ring + L::kRing;
+    const uint32_t staging = ring + L::kRing, scales = staging + L::kStaging + 256;
     Fp8Ctl<kStages>* ctl = reinterpret_cast<Fp8Ctl<kStages>*>(smem + L::kRing + L::kStaging);
-    // BYROW: the scales of the tile's 256 columns and of this CTA's 128 rows, for four steps; four such slots
-    constexpr uint32_t kSlot = (kBN + kBM) * 16;
-    const uint32_t scales = staging + L::kStaging + 256;
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x) / 32, 0);
     const int lane = static_cast<int>(threadIdx.x) & 31;
@@ -129,10 +133,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_init(smem_addr(&ctl->empty[s]), 1);
         }
         for (int b = 0; b < 4; ++b) {
-            mbar_init(smem_addr(&ctl->tmem_full[b >> 1][b & 1]), 1);
-            mbar_init(smem_addr(&ctl->tmem_empty[b >> 1][b & 1]), kSumWarps);   // four of each CTA
-        }
-        for (int b = 0; b < 4; ++b) {
+            mbar_init(smem_addr(&ctl->sums_full[b]), 1);
+            mbar_init(smem_addr(&ctl->sums_empty[b]), 2 * kSumWarps / kParts);   // the part's warps, of both CTAs
             mbar_init(smem_addr(&ctl->scales_full[b]), 64);
             mbar_init(smem_addr(&ctl->scales_empty[b]), kSumWarps);
         }
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         fence_barrier_init();
     }
     if (warp == 1) {
-        tmem_alloc_pair(smem_addr(&ctl->tmem_base), 2 * kBN);
+        tmem_alloc_pair(smem_addr(&ctl->tmem_base), 4 * kPart);
         tmem_relinquish_pair();
     }
     tc_fence_before();
@@ -163,6 +165,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (warp < kFirstSumWarp) {
         fewer_registers<kFewRegisters>();
         if (warp == 0) {
+            // ------------------------------------------------ copies (both CTAs)
             if (elect_one_sync()) {
                 int stage = 0, issued = 0;
                 uint32_t phase = 0;
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     int32_t m_blk, n_blk;
                     raster_tile_fast(p.m_blocks, p.rd, u, &m_blk, &n_blk);
                     const int32_t a_row = (2 * m_blk + static_cast<int32_t>(rank)) * kBM;
-                    const int32_t b_row = n_blk * kBN + static_cast<int32_t>(rank) * (kHalf / 2);
+                    const int32_t b_row = n_blk * kBN + static_cast<int32_t>(rank) * (kPart / 2);
                     for (int32_t kb = 0; kb < p.num_kb; ++kb) {
                         if (issued >= kStages &&
                             !wait_phase(smem_addr(&ctl->empty[stage]), phase ^ 1u, watch, kSiteProducerEmpty)) {
@@ -182,9 +185,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         if (leader) mbar_arrive_expect_tx(full, kPairTx + p.tx_extra);
                         const uint32_t full_lead = map_to_rank(full, 0);
                         tma_load_2d_pair(ring + stage * kTileSlot, &tmap_a, full_lead, kb * kRowBytes, a_row);
-                        tma_load_2d_pair(ring_b + stage * kTileSlot, &tmap_b, full_lead, kb * kRowBytes, b_row);
-                        tma_load_2d_pair(ring_b + stage * kTileSlot + kTileSlot / 2, &tmap_b, full_lead, kb * kRowBytes,
-                                         b_row + kHalf);
+#pragma unroll
+                        for (int part = 0; part < kParts; ++part)
+                            tma_load_2d_pair(ring_b + stage * L::kBSlot + part * (kTileSlot / 2), &tmap_b, full_lead,
+                                             kb * kRowBytes, b_row + part * kPart);
                         issued = issued < kStages ? issued + 1 : kStages;
                         if (++stage == kStages) {
                             stage = 0;
@@ -203,28 +207,29 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
             __syncwarp();
         } else if (warp == 1) {
+            // ------------------------------------------------ MMAs (leader)
             if (leader && elect_one_sync()) {
                 int stage = 0;
-                uint32_t phase = 0, turn = 0;
+                uint32_t phase = 0, turn = 0;            // turn: accumulators used so far
                 bool ok = true;
                 for (int32_t u = pair; ok && u < p.num_units; u += npairs) {
-                    for (int32_t kb = 0; ok && kb < p.num_kb; ++kb, ++turn) {
-                        const uint32_t buf = turn & 1u;
+                    for (int32_t kb = 0; ok && kb < p.num_kb; ++kb) {
                         ok = wait_phase(smem_addr(&ctl->full[stage]), phase, watch, kSiteMmaFull);
                         const uint64_t a_desc = sw128_kmajor_desc(ring + stage * kTileSlot);
-                        const uint64_t b_desc = sw128_kmajor_desc(ring_b + stage * kTileSlot);
+                        const uint64_t b_desc = sw128_kmajor_desc(ring_b + stage * L::kBSlot);
 #pragma unroll
-                        for (uint32_t half = 0; half < 2; ++half) {
-                            if (ok && turn >= 2)
-                                ok = wait_phase_cluster(smem_addr(&ctl->tmem_empty[buf][half]), ((turn >> 1) & 1u) ^ 1u, watch,
+                        for (uint32_t part = 0; part < kParts; ++part, ++turn) {
+                            const uint32_t slot = turn & 3u;
+                            if (ok && turn >= 4)
+                                ok = wait_phase_cluster(smem_addr(&ctl->sums_empty[slot]), ((turn >> 2) & 1u) ^ 1u, watch,
                                                         kSiteMmaTmemEmpty);
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                umma_f8_pair(tmem_base + buf * kBN + half * kHalf, a_desc + 2 * k,
-                                             b_desc + half * (kTileSlot / 2 >> 4) + 2 * k, p.idesc, k > 0 ? 1u : 0u);
-                            umma_commit_pair(smem_addr(&ctl->tmem_full[buf][half]), 3);
+                                umma_f8_pair(tmem_base + slot * kPart, a_desc + 2 * k, b_desc + part * (kTileSlot / 2 >> 4) + 2 * k,
+                                             p.idesc, k > 0 ? 1u : 0u);
+                            umma_commit_pair(smem_addr(&ctl->sums_full[slot]), 3);
                         }
                         if (!ok) break;
                         umma_commit_pair(smem_addr(&ctl->empty[stage]), 3);
@@ -239,31 +244,29 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
             __syncwarp();
         } else if constexpr (BYROW) {
-            // the scales of the tile's columns and rows, of six of them a thread, four steps at a time
+            // ------------------------------------------------ the tile's scales, of two columns and two rows a thread
             const int first = static_cast<int>(threadIdx.x) - 64;
-            uint32_t turn = 0;
+            uint32_t four = 0;                           // runs of four steps
             bool ok = true;
             for (int32_t u = pair; ok && u < p.num_units; u += npairs) {
                 int32_t m_blk, n_blk;
                 raster_tile_fast(p.m_blocks, p.rd, u, &m_blk, &n_blk);
-                const int32_t row = (2 * m_blk + static_cast<int32_t>(rank)) * kBM;
-                const float* from[6];                    // (rows and columns outside C take the last one's)
+                const int32_t row = (2 * m_blk + static_cast<int32_t>(rank)) * kBM + first, col = n_blk * kBN + first;
+                const float* from[4];                    // (rows and columns outside C take the last one's)
 #pragma unroll
-                for (int i = 0; i < 6; ++i) {
-                    const int at = first + 64 * i;
-                    from[i] = i < 4 ? p.b_scales + static_cast<int64_t>(min(n_blk * kBN + at, p.N - 1)) * p.num_kb
-                                    : p.a_scales + static_cast<int64_t>(min(row + at - kBN, p.M - 1)) * p.num_kb;
-                }
-                for (int32_t kb = 0; kb < p.num_kb; kb += 4, ++turn) {
-                    const uint32_t slot = turn & 3u;
-                    if (turn >= 4 && !wait_phase(smem_addr(&ctl->scales_empty[slot]), ((turn >> 2) & 1u) ^ 1u, watch,
+                for (int i = 0; i < 4; ++i)
+                    from[i] = i < 2 ? p.b_scales + static_cast<int64_t>(min(col + 64 * i, p.N - 1)) * p.num_kb
+                                    : p.a_scales + static_cast<int64_t>(min(row + 64 * (i - 2), p.M - 1)) * p.num_kb;
+                for (int32_t kb = 0; kb < p.num_kb; kb += 4, ++four) {
+                    const uint32_t slot = four & 3u;
+                    if (four >= 4 && !wait_phase(smem_addr(&ctl->scales_empty[slot]), ((four >> 2) & 1u) ^ 1u, watch,
                                                  kSiteProducerEmpty)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t to = scales + slot * kSlot + static_cast<uint32_t>(first) * 16;
+                    const uint32_t to = scales + slot * L::kScaleSlot + static_cast<uint32_t>(first) * 16;
 #pragma unroll
-                    for (int i = 0; i < 6; ++i) {
+                    for (int i = 0; i < 4; ++i) {
                         if (p.whole_scales) {
                             fetch_scales(to + 64 * 16 * i, from[i] + kb);
                         } else {
@@ -277,9 +280,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             __syncwarp();
         }
     } else {
+        // ---------------------------------------------------- sums (both CTAs)
         more_registers<kSumRegisters>();
-        const int quad = warp & 3, half = (warp - kFirstSumWarp) >> 2;
-        const uint32_t acc_at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(half * kHalf);
+        const int quad = warp & 3, which = (warp - kFirstSumWarp) >> 2;   // which part, or which half of the only one
+        const uint32_t part = BYROW ? 0 : which;
+        const uint32_t lanes_at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(BYROW ? which * kCols : 0);
         const uint32_t buf_at = staging + static_cast<uint32_t>((warp - kFirstSumWarp) * L::kStoreBuf);
         uint32_t turn = 0, four = 0;                         // steps; BYROW: runs of four
         bool ok = true;
@@ -287,11 +292,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             int32_t m_blk, n_blk;
             raster_tile_fast(p.m_blocks, p.rd, u, &m_blk, &n_blk);
             const int32_t y = (2 * m_blk + static_cast<int32_t>(rank)) * kBM + quad * 32;
-            const int32_t x = n_blk * kBN + half * kHalf;
-            const bool inside = y < p.M;                     // (of the whole warp; columns are looked at below)
+            const int32_t x = n_blk * kBN + which * kCols;
             // 64 columns of the warp's rows, which `place` writes to its buffer
             const auto store = [&](int c, auto place) {
-                if (!inside || x + c >= p.N) return;
+                if (y >= p.M || x + c >= p.N) return;        // (the whole warp)
                 if (lane == 0) bulk_wait_group_read<0>();
                 __syncwarp();
                 place();
@@ -302,45 +306,47 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     bulk_commit_group();
                 }
             };
-            float acc[kHalf];
+            const auto release = [&](uint32_t slot) {        // (the accumulators are in registers)
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_leader(smem_addr(&ctl->sums_empty[slot]));
+            };
+            float acc[kCols];
 #pragma unroll
-            for (int c = 0; c < kHalf; ++c) acc[c] = 0.f;
+            for (int c = 0; c < kCols; ++c) acc[c] = 0.f;
             if constexpr (!BYROW) {
-                // a thread has a row: one factor for its 128 columns
                 ScaleRow sa, sb;
                 // (rows and columns outside C take the last one's scales, and are not stored)
                 sa.begin(p.a_scales + static_cast<int64_t>(min(y + lane, p.M - 1)) * p.num_kb, 0);
-                sb.begin(p.b_scales + static_cast<int64_t>(min(x, p.N - 1) / kHalf) * p.num_kb, 0);
+                sb.begin(p.b_scales + static_cast<int64_t>(min(x, p.N - 1) / kPart) * p.num_kb, 0);
                 for (int32_t kb = 0; kb < p.num_kb; ++kb, ++turn) {
-                    const uint32_t buf = turn & 1u;
+                    const uint32_t slot = (turn & 1u) * 2 + part, at = lanes_at + slot * kPart;
                     const float s = sa.get(kb + 1 < p.num_kb) * sb.get(kb + 1 < p.num_kb);
-                    ok = wait_phase(smem_addr(&ctl->tmem_full[buf][half]), (turn >> 1) & 1u, watch, kSiteEpiTmemFull);
+                    ok = wait_phase(smem_addr(&ctl->sums_full[slot]), (turn >> 1) & 1u, watch, kSiteEpiTmemFull);
                     if (!ok) break;
                     tc_fence_after();
                     const gbt::Pair s2(s, s);
                     uint32_t v[2][kStep];
-                    tmem_read(acc_at + buf * kBN, v[0]);
+                    tmem_read(at, v[0]);
 #pragma unroll
-                    for (int c = 0; c < kHalf / kStep; ++c) {
+                    for (int c = 0; c < kCols / kStep; ++c) {
                         tmem_arrived(v[c & 1]);
-                        if (c + 1 < kHalf / kStep) {
-                            tmem_read(acc_at + buf * kBN + (c + 1) * kStep, v[(c + 1) & 1]);
+                        if (c + 1 < kCols / kStep) {
+                            tmem_read(at + (c + 1) * kStep, v[(c + 1) & 1]);
                         } else {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) arrive_leader(smem_addr(&ctl->tmem_empty[buf][half]));
+                            release(slot);
                         }
 #pragma unroll
                         for (int j = 0; j < kStep; j += 2) {
-                            const int at = c * kStep + j;
+                            const int to = c * kStep + j;
                             const gbt::Pair t(__uint_as_float(v[c & 1][j]), __uint_as_float(v[c & 1][j + 1]));
-                            gbt::fma2(t, s2, gbt::Pair(acc[at], acc[at + 1])).get(acc[at], acc[at + 1]);
+                            gbt::fma2(t, s2, gbt::Pair(acc[to], acc[to + 1])).get(acc[to], acc[to + 1]);
                         }
                     }
                 }
                 if (!ok) break;
 #pragma unroll
-                for (int c = 0; c < kHalf; c += 64) {
+                for (int c = 0; c < kCols; c += 64) {
                     store(c, [&] {
                         uint32_t w[32];
 #pragma unroll
@@ -349,50 +355,44 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     });
                 }
             } else {
-                // A factor for each row and column: a thread has two columns in eight of rows lane / 4 + 8 h.
-                // (With a row a thread, each of them read the scales of all 128 columns: 64 KB a step
-                // through the SM's 128 bytes a cycle, 0.92 us a step against XX.)
-                const int group = lane / 4, two = lane % 4;
+                const int group = lane / 4, two = lane % 4;  // rows group + 8 h, columns 8 i + 2 two, + 1
                 for (int32_t kb = 0; kb < p.num_kb; ++kb, ++turn) {
-                    const uint32_t buf = turn & 1u, place = four & 3u;
-                    const uint32_t slot = scales + place * kSlot + static_cast<uint32_t>(kb & 3) * 4;
+                    const uint32_t slot = turn & 3u, at = lanes_at + slot * kPart, place = four & 3u;
+                    const uint32_t scales_at = scales + place * L::kScaleSlot + static_cast<uint32_t>(kb & 3) * 4;
                     if ((kb & 3) == 0)
                         ok = wait_phase(smem_addr(&ctl->scales_full[place]), (four >> 2) & 1u, watch, kSiteEpiTmemFull);
                     gbt::Pair s[4];
                     if (ok) {
 #pragma unroll
                         for (int h = 0; h < 4; ++h)
-                            s[h] = ld_shared_twice(slot + static_cast<uint32_t>(kBN + quad * 32 + 8 * h + group) * 16);
-                        ok = wait_phase(smem_addr(&ctl->tmem_full[buf][half]), (turn >> 1) & 1u, watch, kSiteEpiTmemFull);
+                            s[h] = ld_shared_twice(scales_at + static_cast<uint32_t>(kPart + quad * 32 + 8 * h + group) * 16);
+                        ok = wait_phase(smem_addr(&ctl->sums_full[slot]), (turn >> 2) & 1u, watch, kSiteEpiTmemFull);
                     }
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t cols_at = slot + static_cast<uint32_t>(half * kHalf + 2 * two) * 16;
+                    const uint32_t cols_at = scales_at + static_cast<uint32_t>(which * kCols + 2 * two) * 16;
                     uint32_t v[2][kStep];
-                    tmem_read_by_fours(acc_at + buf * kBN, v[0]);
+                    tmem_read_by_fours(at, v[0]);
                     gbt::Pair w[4];
                     // step c: columns 32 (c / 2) .. + 31 of the upper or lower 16 rows
 #pragma unroll
-                    for (int c = 0; c < kHalf / kStep; ++c) {
+                    for (int c = 0; c < kCols / kStep; ++c) {
                         if (c % 2 == 0) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i) w[i] = ld_shared_pair(cols_at + static_cast<uint32_t>(16 * c + 8 * i) * 16);
                         }
                         tmem_arrived(v[c & 1]);
-                        if (c + 1 < kHalf / kStep) {
-                            tmem_read_by_fours(acc_at + buf * kBN + ((c + 1) / 2) * 32 + (static_cast<uint32_t>((c + 1) % 2 * 16) << 16),
-                                               v[(c + 1) & 1]);
+                        if (c + 1 < kCols / kStep) {
+                            tmem_read_by_fours(at + ((c + 1) / 2) * 32 + (static_cast<uint32_t>((c + 1) % 2 * 16) << 16), v[(c + 1) & 1]);
                         } else {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) arrive_leader(smem_addr(&ctl->tmem_empty[buf][half]));
+                            release(slot);
                         }
 #pragma unroll
                         for (int j = 0; j < kStep; j += 2) {
-                            const int at = c * kStep + j;
+                            const int to = c * kStep + j;
                             const gbt::Pair t(__uint_as_float(v[c & 1][j]), __uint_as_float(v[c & 1][j + 1]));
-                            gbt::fma2(gbt::mul2(t, w[j / 4]), s[c % 2 * 2 + j / 2 % 2], gbt::Pair(acc[at], acc[at + 1]))
-                                .get(acc[at], acc[at + 1]);
+                            gbt::fma2(gbt::mul2(t, w[j / 4]), s[c % 2 * 2 + j / 2 % 2], gbt::Pair(acc[to], acc[to + 1]))
+                                .get(acc[to], acc[to + 1]);
                         }
                     }
                     if ((kb & 3) == 3 || kb + 1 == p.num_kb) {
@@ -402,24 +402,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     }
                 }
                 if (!ok) break;
+                store(0, [&] {
 #pragma unroll
-                for (int c = 0; c < kHalf; c += 64) {
-                    store(c, [&] {
+                    for (int c = 0; c < kCols / kStep; ++c) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {        // 32 columns, 16 rows
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    const int at = (c / kStep + k) * kStep + 4 * i + 2 * h;
-                                    const int r = k % 2 * 16 + h * 8 + group, unit = k / 2 * 4 + i;
-                                    st_shared_u1(buf_at + static_cast<uint32_t>(r * kRowBytes + ((unit ^ (r & 7)) * 16) + two * 4),
-                                                 pack2<OUT>(acc[at], acc[at + 1]));
-                                }
-                            }
+                        for (int j = 0; j < kStep; j += 2) {
+                            const int r = c % 2 * 16 + j / 2 % 2 * 8 + group, unit = c / 2 * 4 + j / 4;
+                            st_shared_u1(buf_at + static_cast<uint32_t>(r * kRowBytes + ((unit ^ (r & 7)) * 16) + two * 4),
+                                         pack2<OUT>(acc[c * kStep + j], acc[c * kStep + j + 1]));
                         }
-                    });
-                }
+                    }
+                });
             }
         }
     }
@@ -428,7 +421,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     cluster_sync_all();                              // the pair's MMAs, TMEM reads and copies are all finished
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem_base, 2 * kBN);
+        tmem_dealloc_pair(tmem_base, 4 * kPart);
     } else if (warp >= kFirstSumWarp) {
         if (lane == 0) bulk_wait_group_read<0>();    // the stores have read their buffers
         __syncwarp();
@@ -485,7 +478,8 @@ gemm_status_t run(const gemm_fp8_plan* p, const void* A, const float* a_scales, 
     f.N = static_cast<int32_t>(N);
     f.num_kb = num_kb;
     f.m_blocks = static_cast<int32_t>((M + 255) / 256);
-    const int32_t n_blocks = static_cast<int32_t>((N + 255) / 256);
+    const int64_t tile_n = p->b_scales == GEMM_SCALE_ROW ? Fp8Layout<true>::kBN : Fp8Layout<false>::kBN;
+    const int32_t n_blocks = static_cast<int32_t>((N + tile_n - 1) / tile_n);
     f.num_units = f.m_blocks * n_blocks;
     f.idesc = descriptor(0, 256, 128);
     f.tx_extra = p->base.tx_extra;

@@ -208,6 +208,57 @@ __device__ __forceinline__ uint32_t sums_at(int row, int c4) {
     return static_cast<uint32_t>(row * kTileSide * 4 + ((c4 ^ (row & 31)) * 16));
 }
 
+// The end of a tile whose S slices' sums stand in their CTAs' shared memory: each CTA finishes every
+// S-th run of groups of four columns.  All slices' loads are under way before the first is
+// used: one way to the other SMs, not S (M = 128, S = 8 of 1024 x 8192: XX us, YY before).
+template <bool F8, int OUT, int RM, int S>
+__device__ __forceinline__ void few_rows_finish(const FewParams& p, uint32_t sums, int row0, int n_blk, int slice) {
+    constexpr int kAcross = F8 ? kTileSide / 4 : kTileSide / 8;
+    const int rows = min(RM, p.M - row0), groups = rows * kAcross;
+    const int col0 = n_blk * (F8 ? kTileSide : kTileSide / 2);
+    uint32_t base[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) base[s] = map_to_rank(sums, static_cast<uint32_t>(s));
+    for (int i = slice * kThreads + static_cast<int>(threadIdx.x); i < groups; i += S * kThreads) {
+        const int row = i / kAcross, c4 = i % kAcross, col = col0 + c4 * 4;
+        if (col >= p.N) continue;                        // (N % 8 == 0)
+        const uint32_t at = sums_at(row, c4), at_u = sums_at(row, (c4 + kAcross) % (kTileSide / 4));
+        uint4 v[S], w[S];
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            v[s] = ld_dsmem_u4(base[s] + at);
+            if constexpr (!F8) w[s] = ld_dsmem_u4(base[s] + at_u);
+        }
+        float g[4] = {}, u[4] = {};
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            g[0] += __uint_as_float(v[s].x);
+            g[1] += __uint_as_float(v[s].y);
+            g[2] += __uint_as_float(v[s].z);
+            g[3] += __uint_as_float(v[s].w);
+            if constexpr (!F8) {
+                u[0] += __uint_as_float(w[s].x);
+                u[1] += __uint_as_float(w[s].y);
+                u[2] += __uint_as_float(w[s].z);
+                u[3] += __uint_as_float(w[s].w);
+            }
+        }
+        if constexpr (!F8) {
+            if (p.gate_up) {
+                uint16_t* to = static_cast<uint16_t*>(p.gate_up) + static_cast<int64_t>(row0 + row) * 2 * p.N + col;
+                *reinterpret_cast<uint2*>(to) = make_uint2(pack2<OUT>(g[0], g[1]), pack2<OUT>(g[2], g[3]));
+                *reinterpret_cast<uint2*>(to + p.N) = make_uint2(pack2<OUT>(u[0], u[1]), pack2<OUT>(u[2], u[3]));
+            }
+            with_act(p.act, [&](auto act) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) g[k] = gate_fn<decltype(act)::value>(g[k]) * u[k];
+            });
+        }
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(row0 + row) * p.N + col) =
+            make_uint2(pack2<OUT>(g[0], g[1]), pack2<OUT>(g[2], g[3]));
+    }
+}
+
 template <bool F8, int OUT, int RM>
 __global__ void __launch_bounds__(kThreads, 2)
     few_rows_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
@@ -405,42 +456,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
 
-    // Each CTA finishes every slices-th group of four columns of every row.
-    constexpr int kAcross = F8 ? kTileSide / 4 : kTileSide / 8;
-    const int rows = min(RM, p.M - row0), groups = rows * kAcross;
-    const int col0 = n_blk * (F8 ? kTileSide : kTileSide / 2);
-    for (int i = slice * kThreads + static_cast<int>(threadIdx.x); i < groups; i += p.slices * kThreads) {
-        const int row = i / kAcross, c4 = i % kAcross, col = col0 + c4 * 4;
-        if (col >= p.N) continue;                        // (N % 8 == 0)
-        float g[4] = {}, u[4] = {};
-        const uint32_t at = ring_a + sums_at(row, c4), at_u = ring_a + sums_at(row, (c4 + kAcross) % (kTileSide / 4));
-        for (int s = 0; s < p.slices; ++s) {
-            const uint4 v = ld_dsmem_u4(map_to_rank(at, static_cast<uint32_t>(s)));
-            g[0] += __uint_as_float(v.x);
-            g[1] += __uint_as_float(v.y);
-            g[2] += __uint_as_float(v.z);
-            g[3] += __uint_as_float(v.w);
-            if constexpr (!F8) {
-                const uint4 w = ld_dsmem_u4(map_to_rank(at_u, static_cast<uint32_t>(s)));
-                u[0] += __uint_as_float(w.x);
-                u[1] += __uint_as_float(w.y);
-                u[2] += __uint_as_float(w.z);
-                u[3] += __uint_as_float(w.w);
-            }
-        }
-        if constexpr (!F8) {
-            if (p.gate_up) {
-                uint16_t* to = static_cast<uint16_t*>(p.gate_up) + static_cast<int64_t>(row0 + row) * 2 * p.N + col;
-                *reinterpret_cast<uint2*>(to) = make_uint2(pack2<OUT>(g[0], g[1]), pack2<OUT>(g[2], g[3]));
-                *reinterpret_cast<uint2*>(to + p.N) = make_uint2(pack2<OUT>(u[0], u[1]), pack2<OUT>(u[2], u[3]));
-            }
-            with_act(p.act, [&](auto act) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) g[k] = gate_fn<decltype(act)::value>(g[k]) * u[k];
-            });
-        }
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(row0 + row) * p.N + col) =
-            make_uint2(pack2<OUT>(g[0], g[1]), pack2<OUT>(g[2], g[3]));
+    switch (p.slices) {
+        case 1: few_rows_finish<F8, OUT, RM, 1>(p, ring_a, row0, n_blk, slice); break;
+        case 2: few_rows_finish<F8, OUT, RM, 2>(p, ring_a, row0, n_blk, slice); break;
+        case 4: few_rows_finish<F8, OUT, RM, 4>(p, ring_a, row0, n_blk, slice); break;
+        default: few_rows_finish<F8, OUT, RM, 8>(p, ring_a, row0, n_blk, slice); break;
     }
     cluster_sync_all();                                  // (nobody reads this CTA's sums any more)
 }
