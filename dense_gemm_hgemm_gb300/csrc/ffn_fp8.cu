@@ -442,22 +442,26 @@ template <int OUT>
 gemm_status_t run(const gemm_fp8_plan* p, const void* A, const float* a_scales, const void* B, const float* b_scales, void* C,
                   gbt::Queue queue) {
     const int64_t M = p->M, N = p->N, K = p->K;
-    const bool few = M <= kTileSide && p->b_scales == GEMM_SCALE_SQUARE;
+    const int32_t num_kb = static_cast<int32_t>(gbt::groups_of(K));
+    constexpr FewRates kRates{0.29, 0.33, 1.6, 0.38, 0.5};
+    const int64_t few_tiles = gbt::groups_of(M) * gbt::groups_of(N), pair_tiles = ((M + 255) / 256) * ((N + 255) / 256);
+    FewChoice choice{0, 0};
+    if (p->b_scales == GEMM_SCALE_SQUARE)
+        choice = choose_kernel(M, few_tiles, pair_tiles, num_kb, static_cast<double>(N) * K, p->base.num_sms, kRates);
+    const bool few = choice.slices > 0;
     const int box = few && M <= 32 ? 32 : kTileSide;
     CUtensorMap a, b, c;
     if (!encode_map(&a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, A, M, K, K, box) ||
         !encode_map(&b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, B, N, K, K, few ? kTileSide : kTileSide / 2))
         return GEMM_ERR_TENSORMAP;
-    const int32_t num_kb = static_cast<int32_t>(gbt::groups_of(K));
     if (few) {
         FewParams f{};
         f.M = static_cast<int32_t>(M);
         f.N = static_cast<int32_t>(N);
         f.num_kb = num_kb;
-        f.m_blocks = 1;
-        const int64_t tiles = (N + kTileSide - 1) / kTileSide;
-        f.slices = few_slices(tiles, num_kb, p->base.num_sms);
-        f.kb_per_slice = (num_kb + f.slices - 1) / f.slices;
+        f.m_blocks = static_cast<int32_t>(gbt::groups_of(M));
+        f.slices = choice.slices;
+        f.kb_per_slice = choice.kb_per_slice;
         f.idesc = descriptor(0, kTileSide, kTileSide);
         f.tx_extra = p->base.tx_extra;
         f.a_scales = a_scales;
@@ -466,9 +470,9 @@ gemm_status_t run(const gemm_fp8_plan* p, const void* A, const float* a_scales, 
         f.error_word = p->base.error_word;
         f.timeout_ns = p->base.timeout_ns;
         if (box == 32)
-            return gbt::launch<few_rows_kernel<true, OUT, 32>>(tiles * f.slices, kThreads, FewLayout<32>::kTotal, queue, f.slices, a,
+            return gbt::launch<few_rows_kernel<true, OUT, 32>>(few_tiles * f.slices, kThreads, FewLayout<32>::kTotal, queue, f.slices, a,
                                                                b, b, f);
-        return gbt::launch<few_rows_kernel<true, OUT, 128>>(tiles * f.slices, kThreads, FewLayout<128>::kTotal, queue, f.slices, a, b,
+        return gbt::launch<few_rows_kernel<true, OUT, 128>>(few_tiles * f.slices, kThreads, FewLayout<128>::kTotal, queue, f.slices, a, b,
                                                             b, f);
     }
     if (!encode_map(&c, OUT == kOutF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, C, M, N, N, 32))

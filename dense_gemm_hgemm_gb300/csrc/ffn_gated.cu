@@ -319,7 +319,7 @@ bool prepare() {
 }
 
 template <int OUT>
-gemm_status_t forward_few(const gemm_gated_plan* p, const void* X, const void* W, void* H, void* gate_up, gbt::Queue queue) {
+gemm_status_t forward_few(const gemm_gated_plan* p, const FewChoice& choice, const void* X, const void* W, void* H, void* gate_up, gbt::Queue queue) {
     const auto type = OUT == kOutF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const int box = p->M <= 32 ? 32 : kTileSide;
     CUtensorMap x, gate, up;
@@ -333,8 +333,8 @@ gemm_status_t forward_few(const gemm_gated_plan* p, const void* X, const void* W
     f.num_kb = static_cast<int32_t>((p->K + kBK - 1) / kBK);
     f.m_blocks = static_cast<int32_t>((p->M + kTileSide - 1) / kTileSide);
     const int64_t tiles = f.m_blocks * ((p->F + kTileSide / 2 - 1) / (kTileSide / 2));
-    f.slices = few_slices(tiles, f.num_kb, p->base.num_sms);
-    f.kb_per_slice = (f.num_kb + f.slices - 1) / f.slices;
+    f.slices = choice.slices;
+    f.kb_per_slice = choice.kb_per_slice;
     f.idesc = descriptor(OUT == kOutF16 ? 0 : 1, kTileSide, kTileSide);
     f.tx_extra = p->base.tx_extra;
     f.act = p->act;
@@ -383,7 +383,13 @@ gemm_status_t forward_many(const gemm_gated_plan* p, const void* X, const void* 
 
 template <int OUT>
 gemm_status_t forward(const gemm_gated_plan* p, const void* X, const void* W, void* H, void* gate_up, gbt::Queue queue) {
-    return p->M <= kTileSide ? forward_few<OUT>(p, X, W, H, gate_up, queue) : forward_many<OUT>(p, X, W, H, gate_up, queue);
+    constexpr FewRates kRates{0.22, 0.35, 1.35, 0.29, 1.0};
+    const int64_t few = ((p->M + kTileSide - 1) / kTileSide) * ((p->F + kTileSide / 2 - 1) / (kTileSide / 2));
+    const int64_t pair = ((p->M + 2 * kBM - 1) / (2 * kBM)) * ((p->F + kTileF - 1) / kTileF);
+    const FewChoice choice = choose_kernel(p->M, few, pair, static_cast<int>((p->K + kBK - 1) / kBK), 4.0 * p->F * p->K,
+                                           p->base.num_sms, kRates);
+    return choice.slices > 0 ? forward_few<OUT>(p, choice, X, W, H, gate_up, queue)
+                             : forward_many<OUT>(p, X, W, H, gate_up, queue);
 }
 
 bool overlaps_16(const void* a, const void* b, const void* c, const void* d) {

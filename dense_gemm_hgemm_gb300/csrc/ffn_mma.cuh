@@ -210,7 +210,7 @@ __device__ __forceinline__ uint32_t sums_at(int row, int c4) {
 
 // The end of a tile whose S slices' sums stand in their CTAs' shared memory: each CTA finishes every
 // S-th run of groups of four columns.  All slices' loads are under way before the first is
-// used: one way to the other SMs, not S (M = 128, S = 8 of 1024 x 8192: XX us, YY before).
+// used: one way to the other SMs, not S.
 template <bool F8, int OUT, int RM, int S>
 __device__ __forceinline__ void few_rows_finish(const FewParams& p, uint32_t sums, int row0, int n_blk, int slice) {
     constexpr int kAcross = F8 ? kTileSide / 4 : kTileSide / 8;
@@ -544,17 +544,45 @@ inline gemm_status_t check_plan(PlanBase* b, void* stream) {
     return st == GEMM_ERR_INDEX ? GEMM_ERR_DEVICE_TIMEOUT : st;   // (any site code is a wait's)
 }
 
-// The slices of K of a product of few rows over `tiles` tiles: the number of CTAs that brings
-// the tiles' k-blocks to an end first, two CTAs an SM; a slice has four k-blocks at least.
-inline int few_slices(int64_t tiles, int num_kb, int num_sms) {
-    int best = 1;
+// ---- which kernel: estimates in microseconds, from measurements between 1 and 1024 rows of weights from
+// 1024 x 512 to 16384 x 8192 (within a quarter of the measured time where the choice is close)
+
+struct FewRates {
+    double kb_32, kb_128;       // a k-block of a CTA whose SM it has alone, for boxes of 32 and of 128 rows
+    double shared;              // ... times this where two share the SM
+    double pair_kb, pair_wave;  // a k-block, and a tile's end, of the kernel of many rows
+};
+struct FewChoice {
+    int slices;                 // of K, of the kernel of few rows; 0: the kernel of many rows is faster
+    int kb_per_slice;
+};
+
+// few_tiles, pair_tiles: tiles of the two kernels; weight_bytes: what has to come from memory in any
+// case.  Up to 128 rows the kernel of few rows takes all: both are bound by memory there, and the
+// other one streams worse (1 x 8192 x 4096 gated 40 against 24 us, 128 rows 27 against 27).
+inline FewChoice choose_kernel(int64_t rows, int64_t few_tiles, int64_t pair_tiles, int num_kb, double weight_bytes, int num_sms,
+                               const FewRates& r) {
+    const double memory = 3 + weight_bytes / 6.2e6;
+    FewChoice best{0, 0};
     double least = 0;
-    for (int s = 1; s <= 8; s *= 2) {
-        if (s > 1 && num_kb < 4 * s) break;
-        const int64_t waves = (tiles * s + 2 * num_sms - 1) / (2 * num_sms);
-        const double time = static_cast<double>(waves) * ((num_kb + s - 1) / s);
-        if (s == 1 || time < least) {
-            best = s;
+    const bool few_only = rows <= kTileSide;
+    if (!few_only) {
+        const int64_t waves = (pair_tiles + num_sms / 2 - 1) / (num_sms / 2);
+        least = 3 + static_cast<double>(waves) * (num_kb * r.pair_kb + r.pair_wave);
+        if (least < memory) least = memory;
+    }
+    // CTAs of a cluster of s that are resident at once, two an SM: clusters of eight do not fill the
+    // GPU's groups of SMs (15 clusters of 152 SMs with one CTA each, 36 of four)
+    const double resident[] = {2.0, 2.0, 1.89, 1.57};
+    for (int s = 1, k = 0; s <= 8 && s <= num_kb; s *= 2, ++k) {
+        const int per = (num_kb + s - 1) / s;
+        const int64_t ctas = few_tiles * s, slots = static_cast<int64_t>(resident[k] * num_sms);
+        const int64_t waves = (ctas + slots - 1) / slots;
+        const double kb = (rows <= 32 ? r.kb_32 : r.kb_128) * (ctas > num_sms ? r.shared : 1.0);
+        double time = 2 + 0.7 * k + static_cast<double>(waves) * (per * kb + (s > 1 ? 1.0 : 0.5));
+        if (time < memory) time = memory;
+        if ((best.slices == 0 && few_only) || time < least) {
+            best = FewChoice{s, per};
             least = time;
         }
     }
