@@ -22,13 +22,13 @@ constexpr int kPairThreads = 32 * (kFirstSumWarp + kSumWarps);
 constexpr int kLaunchRegisters = 168, kFewRegisters = 72, kSumRegisters = 216;
 static_assert(128 * kFewRegisters + 256 * kSumRegisters <= kPairThreads * kLaunchRegisters, "registers of the block");
 
-// The tiles of a kind of scales (BYROW: B's go by rows): `kParts` parts of 128 columns.
+// The tiles of a kind of scales (BYROW: B's go by rows).
 template <bool BYROW>
 struct Fp8Layout {
-    static constexpr int kParts = BYROW ? 1 : 2;
-    static constexpr int kBN = kTileSide * kParts;
+    static constexpr int kBN = BYROW ? 128 : 256;
+    static constexpr int kTurns = 512 / kBN;                           // accumulators: all of TMEM
     static constexpr int kStages = BYROW ? 5 : 6;
-    static constexpr int kBSlot = kTileSlot / 2 * kParts;              // this CTA's 64 rows of each part of B
+    static constexpr int kBSlot = kBN / 2 * kRowBytes;                 // this CTA's half of B's rows
     static constexpr int kRing = kStages * (kTileSlot + kBSlot);
     static constexpr int kStoreBuf = 32 * kRowBytes;
     static constexpr int kStaging = kSumWarps * kStoreBuf;
@@ -79,7 +79,7 @@ __device__ __forceinline__ void st_shared_u1(uint32_t saddr, uint32_t v) {
 template <int STAGES>
 struct Fp8Ctl {
     uint64_t full[STAGES], empty[STAGES];
-    uint64_t sums_full[4], sums_empty[4];            // of the accumulators, four times 128 columns
+    uint64_t sums_full[4], sums_empty[4];            // of the accumulators
     uint64_t scales_full[4], scales_empty[4];        // BYROW
     uint64_t drain;
     uint32_t tmem_base;
@@ -89,27 +89,28 @@ static_assert(sizeof(Fp8Ctl<6>) <= 256, "control block");
 
 // Many rows: a pair of SMs computes 256 rows of C, as the plain product's pair does
 // (gemm_kernel_2cta.cuh).  The tensor cores know no scales, so the sum over each 128 elements of
-// K and 128 columns has an accumulator of its own, four of them in turn (all of TMEM), which eight
-// warps a CTA multiply by the scales of its rows and columns and add to fp32 sums in registers.
-// From the end of an accumulator's MMAs to the next ones into it the tensor cores have three
-// others to do, which hides the way to the warps and back.
-//   squares: tiles of 256 columns.  Four warps take a part of 128 (one square of scales, for which
-//            each CTA brings 64 rows of B); a thread has a row, with one factor for its 128 columns.
-//            A step is 512 cycles of the tensor cores and 128 reads and 64 double multiply-adds of
-//            a thread: 0.43 us, 2.8 PFLOP/s.
-//   by rows: tiles of 128 columns, as there are twice the multiplications.  The eight warps take 64
-//            columns each; a thread has two columns in eight of four rows (with a row a thread, each
-//            of them read the scales of all columns), whose scales two warps bring four steps at a
-//            time (read a step at a time they were 256 lines a step, more than the first-level
-//            cache holds).  2048 x 2304 x 16384: XX us, 93 with 256 columns a tile.
+// K has an accumulator of its own, two or four of them in turn (all of TMEM), which eight warps a CTA
+// multiply by the scales of its rows and columns and add to fp32 sums in registers.
+//   squares: tiles of 256 columns, two accumulators.  Four warps take 128 columns (one square of
+//            scales); a thread has a row, with one factor for its 128 columns.  A step is 512 cycles
+//            of the tensor cores and 128 reads of TMEM and 64 double multiply-adds of a thread:
+//            0.42 us, 2.8 PFLOP/s over one wave (0.34 where the MMAs do not wait for the warps).
+//            Accumulators of 128 columns, 32 instead of 16 columns a read and single instead of
+//            double multiply-adds all gave the same.  Nothing may spill: what is stored to local memory
+//            right after its load makes the thread wait for it (0.7 to 1.2 us a step).
+//   by rows: tiles of 128 columns, four accumulators.  The eight warps take 64 columns each; a thread
+//            has two columns in eight of four rows, whose scales two warps bring four steps at a time
+//            (read a step at a time they were 384 lines a step, more than the first-level cache
+//            holds).  A step is 0.37 us; in tiles of 256 columns it was 0.73, with fewer tiles to fill the
+//            SMs (1000 x 2056 x 4112: 16 us, 30 in those tiles).
 template <int OUT, bool BYROW>
 __global__ void __launch_bounds__(kPairThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                     const __grid_constant__ CUtensorMap tmap_c, const Fp8Params p) {
     using L = Fp8Layout<BYROW>;
-    constexpr int kStages = L::kStages, kParts = L::kParts, kBN = L::kBN;
-    constexpr int kPart = kTileSide, kStep = 16;
-    constexpr int kCols = BYROW ? kPart / 2 : kPart;  // of a warp
+    constexpr int kStages = L::kStages, kTurns = L::kTurns, kBN = L::kBN, kStep = 16;
+    constexpr int kTurnBits = BYROW ? 2 : 1;
+    constexpr int kCols = kBN / 2;                   // of a warp
     constexpr uint32_t kPairTx = 2 * (kTileSlot + L::kBSlot);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         for (int b = 0; b < 4; ++b) {
             mbar_init(smem_addr(&ctl->sums_full[b]), 1);
-            mbar_init(smem_addr(&ctl->sums_empty[b]), 2 * kSumWarps / kParts);   // the part's warps, of both CTAs
+            mbar_init(smem_addr(&ctl->sums_empty[b]), 2 * kSumWarps);   // of both CTAs
             mbar_init(smem_addr(&ctl->scales_full[b]), 64);
             mbar_init(smem_addr(&ctl->scales_empty[b]), kSumWarps);
         }
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         fence_barrier_init();
     }
     if (warp == 1) {
-        tmem_alloc_pair(smem_addr(&ctl->tmem_base), 4 * kPart);
+        tmem_alloc_pair(smem_addr(&ctl->tmem_base), kTurns * kBN);
         tmem_relinquish_pair();
     }
     tc_fence_before();
@@ -174,10 +175,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     int32_t m_blk, n_blk;
                     raster_tile_fast(p.m_blocks, p.rd, u, &m_blk, &n_blk);
                     const int32_t a_row = (2 * m_blk + static_cast<int32_t>(rank)) * kBM;
-                    const int32_t b_row = n_blk * kBN + static_cast<int32_t>(rank) * (kPart / 2);
+                    const int32_t b_row = n_blk * kBN + static_cast<int32_t>(rank) * (kBN / 2);
                     for (int32_t kb = 0; kb < p.num_kb; ++kb) {
                         if (issued >= kStages &&
-                            !wait_phase(smem_addr(&ctl->empty[stage]), phase ^ 1u, watch, kSiteProducerEmpty)) {
+                            !await(smem_addr(&ctl->empty[stage]), phase ^ 1u, watch, kSiteProducerEmpty)) {
                             ok = false;
                             break;
                         }
@@ -185,10 +186,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         if (leader) mbar_arrive_expect_tx(full, kPairTx + p.tx_extra);
                         const uint32_t full_lead = map_to_rank(full, 0);
                         tma_load_2d_pair(ring + stage * kTileSlot, &tmap_a, full_lead, kb * kRowBytes, a_row);
-#pragma unroll
-                        for (int part = 0; part < kParts; ++part)
-                            tma_load_2d_pair(ring_b + stage * L::kBSlot + part * (kTileSlot / 2), &tmap_b, full_lead,
-                                             kb * kRowBytes, b_row + part * kPart);
+                        tma_load_2d_pair(ring_b + stage * L::kBSlot, &tmap_b, full_lead, kb * kRowBytes, b_row);
                         issued = issued < kStages ? issued + 1 : kStages;
                         if (++stage == kStages) {
                             stage = 0;
@@ -210,28 +208,24 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             // ------------------------------------------------ MMAs (leader)
             if (leader && elect_one_sync()) {
                 int stage = 0;
-                uint32_t phase = 0, turn = 0;            // turn: accumulators used so far
+                uint32_t phase = 0, turn = 0;            // turn: steps so far
                 bool ok = true;
                 for (int32_t u = pair; ok && u < p.num_units; u += npairs) {
-                    for (int32_t kb = 0; ok && kb < p.num_kb; ++kb) {
-                        ok = wait_phase(smem_addr(&ctl->full[stage]), phase, watch, kSiteMmaFull);
+                    for (int32_t kb = 0; kb < p.num_kb; ++kb, ++turn) {
+                        const uint32_t slot = turn % kTurns;
+                        if (!await(smem_addr(&ctl->full[stage]), phase, watch, kSiteMmaFull) ||
+                            (turn >= kTurns && !await(smem_addr(&ctl->sums_empty[slot]), ((turn >> kTurnBits) & 1u) ^ 1u, watch,
+                                                           kSiteMmaTmemEmpty))) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
                         const uint64_t a_desc = sw128_kmajor_desc(ring + stage * kTileSlot);
                         const uint64_t b_desc = sw128_kmajor_desc(ring_b + stage * L::kBSlot);
 #pragma unroll
-                        for (uint32_t part = 0; part < kParts; ++part, ++turn) {
-                            const uint32_t slot = turn & 3u;
-                            if (ok && turn >= 4)
-                                ok = wait_phase_cluster(smem_addr(&ctl->sums_empty[slot]), ((turn >> 2) & 1u) ^ 1u, watch,
-                                                        kSiteMmaTmemEmpty);
-                            if (!ok) break;
-                            tc_fence_after();
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                umma_f8_pair(tmem_base + slot * kPart, a_desc + 2 * k, b_desc + part * (kTileSlot / 2 >> 4) + 2 * k,
-                                             p.idesc, k > 0 ? 1u : 0u);
-                            umma_commit_pair(smem_addr(&ctl->sums_full[slot]), 3);
-                        }
-                        if (!ok) break;
+                        for (int k = 0; k < 4; ++k)
+                            umma_f8_pair(tmem_base + slot * kBN, a_desc + 2 * k, b_desc + 2 * k, p.idesc, k > 0 ? 1u : 0u);
+                        umma_commit_pair(smem_addr(&ctl->sums_full[slot]), 3);
                         umma_commit_pair(smem_addr(&ctl->empty[stage]), 3);
                         if (++stage == kStages) {
                             stage = 0;
@@ -259,7 +253,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                                     : p.a_scales + static_cast<int64_t>(min(row + 64 * (i - 2), p.M - 1)) * p.num_kb;
                 for (int32_t kb = 0; kb < p.num_kb; kb += 4, ++four) {
                     const uint32_t slot = four & 3u;
-                    if (four >= 4 && !wait_phase(smem_addr(&ctl->scales_empty[slot]), ((four >> 2) & 1u) ^ 1u, watch,
+                    if (four >= 4 && !await(smem_addr(&ctl->scales_empty[slot]), ((four >> 2) & 1u) ^ 1u, watch,
                                                  kSiteProducerEmpty)) {
                         ok = false;
                         break;
@@ -282,9 +276,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     } else {
         // ---------------------------------------------------- sums (both CTAs)
         more_registers<kSumRegisters>();
-        const int quad = warp & 3, which = (warp - kFirstSumWarp) >> 2;   // which part, or which half of the only one
-        const uint32_t part = BYROW ? 0 : which;
-        const uint32_t lanes_at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(BYROW ? which * kCols : 0);
+        const int quad = warp & 3, which = (warp - kFirstSumWarp) >> 2;   // which half of the columns
+        const uint32_t lanes_at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(which * kCols);
         const uint32_t buf_at = staging + static_cast<uint32_t>((warp - kFirstSumWarp) * L::kStoreBuf);
         uint32_t turn = 0, four = 0;                         // steps; BYROW: runs of four
         bool ok = true;
@@ -318,11 +311,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 ScaleRow sa, sb;
                 // (rows and columns outside C take the last one's scales, and are not stored)
                 sa.begin(p.a_scales + static_cast<int64_t>(min(y + lane, p.M - 1)) * p.num_kb, 0);
-                sb.begin(p.b_scales + static_cast<int64_t>(min(x, p.N - 1) / kPart) * p.num_kb, 0);
+                sb.begin(p.b_scales + static_cast<int64_t>(min(x, p.N - 1) / kTileSide) * p.num_kb, 0);
                 for (int32_t kb = 0; kb < p.num_kb; ++kb, ++turn) {
-                    const uint32_t slot = (turn & 1u) * 2 + part, at = lanes_at + slot * kPart;
+                    const uint32_t slot = turn % kTurns, at = lanes_at + slot * kBN;
                     const float s = sa.get(kb + 1 < p.num_kb) * sb.get(kb + 1 < p.num_kb);
-                    ok = wait_phase(smem_addr(&ctl->sums_full[slot]), (turn >> 1) & 1u, watch, kSiteEpiTmemFull);
+                    ok = await(smem_addr(&ctl->sums_full[slot]), (turn >> kTurnBits) & 1u, watch, kSiteEpiTmemFull);
                     if (!ok) break;
                     tc_fence_after();
                     const gbt::Pair s2(s, s);
@@ -357,16 +350,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             } else {
                 const int group = lane / 4, two = lane % 4;  // rows group + 8 h, columns 8 i + 2 two, + 1
                 for (int32_t kb = 0; kb < p.num_kb; ++kb, ++turn) {
-                    const uint32_t slot = turn & 3u, at = lanes_at + slot * kPart, place = four & 3u;
+                    const uint32_t slot = turn % kTurns, at = lanes_at + slot * kBN, place = four & 3u;
                     const uint32_t scales_at = scales + place * L::kScaleSlot + static_cast<uint32_t>(kb & 3) * 4;
                     if ((kb & 3) == 0)
-                        ok = wait_phase(smem_addr(&ctl->scales_full[place]), (four >> 2) & 1u, watch, kSiteEpiTmemFull);
+                        ok = await(smem_addr(&ctl->scales_full[place]), (four >> 2) & 1u, watch, kSiteEpiTmemFull);
                     gbt::Pair s[4];
                     if (ok) {
 #pragma unroll
                         for (int h = 0; h < 4; ++h)
-                            s[h] = ld_shared_twice(scales_at + static_cast<uint32_t>(kPart + quad * 32 + 8 * h + group) * 16);
-                        ok = wait_phase(smem_addr(&ctl->sums_full[slot]), (turn >> 2) & 1u, watch, kSiteEpiTmemFull);
+                            s[h] = ld_shared_twice(scales_at + static_cast<uint32_t>(kBN + quad * 32 + 8 * h + group) * 16);
+                        ok = await(smem_addr(&ctl->sums_full[slot]), (turn >> kTurnBits) & 1u, watch, kSiteEpiTmemFull);
                     }
                     if (!ok) break;
                     tc_fence_after();
@@ -421,7 +414,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     cluster_sync_all();                              // the pair's MMAs, TMEM reads and copies are all finished
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem_base, 4 * kPart);
+        tmem_dealloc_pair(tmem_base, kTurns * kBN);
     } else if (warp >= kFirstSumWarp) {
         if (lane == 0) bulk_wait_group_read<0>();    // the stores have read their buffers
         __syncwarp();
@@ -452,7 +445,7 @@ gemm_status_t run(const gemm_fp8_plan* p, const void* A, const float* a_scales, 
     const int box = few && M <= 32 ? 32 : kTileSide;
     CUtensorMap a, b, c;
     if (!encode_map(&a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, A, M, K, K, box) ||
-        !encode_map(&b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, B, N, K, K, few ? kTileSide : kTileSide / 2))
+        !encode_map(&b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, B, N, K, K, few || p->b_scales == GEMM_SCALE_SQUARE ? kTileSide : kTileSide / 2))
         return GEMM_ERR_TENSORMAP;
     if (few) {
         FewParams f{};
@@ -485,7 +478,7 @@ gemm_status_t run(const gemm_fp8_plan* p, const void* A, const float* a_scales, 
     const int64_t tile_n = p->b_scales == GEMM_SCALE_ROW ? Fp8Layout<true>::kBN : Fp8Layout<false>::kBN;
     const int32_t n_blocks = static_cast<int32_t>((N + tile_n - 1) / tile_n);
     f.num_units = f.m_blocks * n_blocks;
-    f.idesc = descriptor(0, 256, 128);
+    f.idesc = descriptor(0, 256, static_cast<int>(tile_n));
     f.tx_extra = p->base.tx_extra;
     f.whole_scales = num_kb % 4 == 0 && gbt::aligned(a_scales, 16) && gbt::aligned(b_scales, 16);
     f.a_scales = a_scales;

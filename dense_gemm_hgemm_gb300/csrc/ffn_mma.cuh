@@ -89,6 +89,14 @@ __device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t a_desc, u
         : "memory");
 }
 
+// As wait_phase, which reads the global timer once the first look has failed; here only after many.
+__device__ __forceinline__ bool await(uint32_t bar, uint32_t parity, const Watch& w, int32_t site) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return wait_phase(bar, parity, w, site);
+}
+
 // sigmoid(g), to fp32 accuracy in relative terms on both sides of zero.
 __device__ __forceinline__ float sigmoid(float g) {
     const float e = __expf(-fabsf(g));
