@@ -153,7 +153,7 @@ __device__ __forceinline__ void with_act(int act, F f) {
 struct ScaleRow {
     const float* at;
     float next;
-    __device__ __forceinline__ void read() { asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(next) : "l"(at)); }
+    __device__ __forceinline__ void read() { asm volatile("ld.global.f32 %0, [%1];" : "=f"(next) : "l"(at)); }
     __device__ __forceinline__ void begin(const float* row, int kb) {
         at = row + kb;
         read();

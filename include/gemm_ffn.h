@@ -18,8 +18,8 @@
  *   GEMM_ERR_UNSUPPORTED  an unknown type, activation or kind of scales
  *   GEMM_ERR_ALIGNMENT    a pointer (or a size of a product's operand) that is not
  *                         aligned as the call needs it
- * A plan is used with the device current on which it was made, by one thread at a
- * time.  All sums and statistics are fp32; a result is rounded once, to nearest even.
+ * A plan is used with the device current on which it was made, by one thread and on
+ * one stream at a time (graphs captured from one plan are replayed one after another).  All sums and statistics are fp32; a result is rounded once, to nearest even.
  * Results do not depend on the schedule: the same inputs give the same bits.
  */
 #ifndef GB300_GEMM_FFN_H
@@ -67,7 +67,9 @@ gemm_status_t gemm_rms_plan_create(int64_t max_rows, int64_t cols, gemm_elem_t e
  * For each of `rows` rows: t = x + residual, rounded to the rows' type (residual NULL:
  * t = x), rstd = 1 / sqrt(mean t^2 + eps), y = t * rstd * gamma (gamma NULL = ones).
  * total (NULL: not kept) receives t, rstd (NULL: not kept) one fp32 value a row: what
- * the backward call takes.  eps >= 0.  total and y may each be x or residual (same
+ * the backward call takes.  eps >= 0.  The sum of squares is fp32: it has to stay within
+ * that type (elements of up to about 1e18; a row beyond has rstd 0), and with eps == 0 a
+ * row's mean square may not underflow.  total and y may each be x or residual (same
  * stride), but not the same matrix; matrices overlap in no other way.
  */
 gemm_status_t gemm_rms_forward(gemm_rms_plan_t plan, int64_t rows, const void *x, int64_t ldx,
