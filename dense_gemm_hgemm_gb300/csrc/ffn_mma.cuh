@@ -5,6 +5,8 @@
 // fills a ring by TMA, one thread issues tcgen05.mma into TMEM, epilogue warps take the sums
 // from there; every wait is bounded and leads to the common exit when it runs out.
 #pragma once
+#include <cmath>
+
 #include "ffn_common.cuh"
 #include "gemm_kernel_2cta.cuh"
 
@@ -316,6 +318,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     const uint32_t tmem_base = ctl->tmem_base;
     const Watch watch{&ctl->abort, p.error_word, p.timeout_ns};
+    if (warp == 0 && elect_one_sync()) {
+        // the first weights on their way to the second-level cache while the previous kernel ends
+        for (int kb = kb0; kb < kb1 && kb < kb0 + kStages; ++kb) {
+            if constexpr (F8) {
+                tma_prefetch_l2_2d(&tmap_b, kb * kElems, n_blk * kTileSide);
+            } else {
+                tma_prefetch_l2_2d(&tmap_b, kb * kElems, n_blk * (kTileSide / 2));
+                tma_prefetch_l2_2d(&tmap_b2, kb * kElems, n_blk * (kTileSide / 2));
+            }
+        }
+    }
+    __syncwarp();
     grid_dependency_wait();
     grid_launch_dependents();
 
@@ -570,14 +584,15 @@ struct FewChoice {
 // other one streams worse (1 x 8192 x 4096 gated 40 against 24 us, 128 rows 27 against 27).
 inline FewChoice choose_kernel(int64_t rows, int64_t few_tiles, int64_t pair_tiles, int num_kb, double weight_bytes, int num_sms,
                                const FewRates& r) {
-    const double memory = 3 + weight_bytes / 6.2e6;
+    // (the weights' way from memory and the rest overlap, less the nearer they are to each other)
+    const double memory = 2.2 + weight_bytes / 6.6e6;
+    const auto with_memory = [&](double time) { return std::sqrt(std::sqrt(std::pow(time, 4) + std::pow(memory, 4))); };
     FewChoice best{0, 0};
     double least = 0;
     const bool few_only = rows <= kTileSide;
     if (!few_only) {
         const int64_t waves = (pair_tiles + num_sms / 2 - 1) / (num_sms / 2);
-        least = 3 + static_cast<double>(waves) * (num_kb * r.pair_kb + r.pair_wave);
-        if (least < memory) least = memory;
+        least = with_memory(3 + static_cast<double>(waves) * (num_kb * r.pair_kb + r.pair_wave));
     }
     // CTAs of a cluster of s that are resident at once, two an SM: clusters of eight do not fill the
     // GPU's groups of SMs (15 clusters of 152 SMs with one CTA each, 36 of four)
@@ -587,8 +602,7 @@ inline FewChoice choose_kernel(int64_t rows, int64_t few_tiles, int64_t pair_til
         const int64_t ctas = few_tiles * s, slots = static_cast<int64_t>(resident[k] * num_sms);
         const int64_t waves = (ctas + slots - 1) / slots;
         const double kb = (rows <= 32 ? r.kb_32 : r.kb_128) * (ctas > num_sms ? r.shared : 1.0);
-        double time = 2 + 0.7 * k + static_cast<double>(waves) * (per * kb + (s > 1 ? 1.0 : 0.5));
-        if (time < memory) time = memory;
+        const double time = with_memory(2 + 0.7 * k + static_cast<double>(waves) * (per * kb + (s > 1 ? 1.0 : 0.5)));
         if ((best.slices == 0 && few_only) || time < least) {
             best = FewChoice{s, per};
             least = time;
