@@ -269,6 +269,13 @@ __device__ __forceinline__ void few_rows_finish(const FewParams& p, uint32_t sum
     }
 }
 
+// All threads of the cluster have come here; orders no memory (a release would wait for the results'
+// stores to be performed).
+__device__ __forceinline__ void leave_together() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 template <bool F8, int OUT, int RM>
 __global__ void __launch_bounds__(kThreads, 2)
     few_rows_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
@@ -474,7 +481,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     }
     tc_fence_before();
-    cluster_sync_all();                                  // the slices' sums are there
+    if (p.slices > 1) {
+        cluster_sync_all();                              // the slices' sums are there
+    } else {
+        __syncthreads();
+    }
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
 
@@ -484,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         case 4: few_rows_finish<F8, OUT, RM, 4>(p, ring_a, row0, n_blk, slice); break;
         default: few_rows_finish<F8, OUT, RM, 8>(p, ring_a, row0, n_blk, slice); break;
     }
-    cluster_sync_all();                                  // (nobody reads this CTA's sums any more)
+    if (p.slices > 1) leave_together();                  // (nobody reads this CTA's sums any more)
 }
 
 // ---- host -----------------------------------------------------------------------------
