@@ -10,6 +10,7 @@ struct gemm_fp8_plan {
     gemm_elem_t out;
     gemm_scale_t b_scales;
     gbf::PlanBase base;
+    gbf::FewChoice choice;       // of the kernel (by squares)
 };
 
 namespace gbf {
@@ -431,16 +432,20 @@ bool prepare() {
            allow_shared<few_rows_kernel<true, OUT, 128>>(FewLayout<128>::kTotal);
 }
 
+FewChoice choose(const gemm_fp8_plan* p) {
+    constexpr FewRates kRates{0.29, 0.33, 1.6, 0.38, 0.5};
+    if (p->b_scales != GEMM_SCALE_SQUARE) return FewChoice{0, 0};
+    return choose_kernel(p->M, gbt::groups_of(p->M) * gbt::groups_of(p->N), ((p->M + 255) / 256) * ((p->N + 255) / 256),
+                         static_cast<int>(gbt::groups_of(p->K)), static_cast<double>(p->N) * p->K, p->base.num_sms, kRates);
+}
+
 template <int OUT>
 gemm_status_t run(const gemm_fp8_plan* p, const void* A, const float* a_scales, const void* B, const float* b_scales, void* C,
                   gbt::Queue queue) {
     const int64_t M = p->M, N = p->N, K = p->K;
     const int32_t num_kb = static_cast<int32_t>(gbt::groups_of(K));
-    constexpr FewRates kRates{0.29, 0.33, 1.6, 0.38, 0.5};
-    const int64_t few_tiles = gbt::groups_of(M) * gbt::groups_of(N), pair_tiles = ((M + 255) / 256) * ((N + 255) / 256);
-    FewChoice choice{0, 0};
-    if (p->b_scales == GEMM_SCALE_SQUARE)
-        choice = choose_kernel(M, few_tiles, pair_tiles, num_kb, static_cast<double>(N) * K, p->base.num_sms, kRates);
+    const int64_t few_tiles = gbt::groups_of(M) * gbt::groups_of(N);
+    const FewChoice& choice = p->choice;
     const bool few = choice.slices > 0;
     const int box = few && M <= 32 ? 32 : kTileSide;
     CUtensorMap a, b, c;
@@ -524,6 +529,7 @@ gemm_status_t gemm_fp8_plan_create(int64_t M, int64_t N, int64_t K, gemm_elem_t 
         delete p;
         return st;
     }
+    p->choice = choose(p);
     *plan = p;
     return GEMM_OK;
 }

@@ -10,6 +10,7 @@ struct gemm_gated_plan {
     gemm_elem_t elem;
     gemm_activation_t act;
     gbf::PlanBase base;
+    gbf::FewChoice choice;       // of the forward kernel
     gemm_plan_t dx, dw;          // the gradients' products
 };
 
@@ -319,7 +320,7 @@ bool prepare() {
 }
 
 template <int OUT>
-gemm_status_t forward_few(const gemm_gated_plan* p, const FewChoice& choice, const void* X, const void* W, void* H, void* gate_up, gbt::Queue queue) {
+gemm_status_t forward_few(const gemm_gated_plan* p, const void* X, const void* W, void* H, void* gate_up, gbt::Queue queue) {
     const auto type = OUT == kOutF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const int box = p->M <= 32 ? 32 : kTileSide;
     CUtensorMap x, gate, up;
@@ -333,8 +334,8 @@ gemm_status_t forward_few(const gemm_gated_plan* p, const FewChoice& choice, con
     f.num_kb = static_cast<int32_t>((p->K + kBK - 1) / kBK);
     f.m_blocks = static_cast<int32_t>((p->M + kTileSide - 1) / kTileSide);
     const int64_t tiles = f.m_blocks * ((p->F + kTileSide / 2 - 1) / (kTileSide / 2));
-    f.slices = choice.slices;
-    f.kb_per_slice = choice.kb_per_slice;
+    f.slices = p->choice.slices;
+    f.kb_per_slice = p->choice.kb_per_slice;
     f.idesc = descriptor(OUT == kOutF16 ? 0 : 1, kTileSide, kTileSide);
     f.tx_extra = p->base.tx_extra;
     f.act = p->act;
@@ -383,16 +384,18 @@ gemm_status_t forward_many(const gemm_gated_plan* p, const void* X, const void* 
 
 template <int OUT>
 gemm_status_t forward(const gemm_gated_plan* p, const void* X, const void* W, void* H, void* gate_up, gbt::Queue queue) {
-    constexpr FewRates kRates{0.22, 0.35, 1.35, 0.29, 1.0};
-    const int64_t few = ((p->M + kTileSide - 1) / kTileSide) * ((p->F + kTileSide / 2 - 1) / (kTileSide / 2));
-    const int64_t pair = ((p->M + 2 * kBM - 1) / (2 * kBM)) * ((p->F + kTileF - 1) / kTileF);
-    const FewChoice choice = choose_kernel(p->M, few, pair, static_cast<int>((p->K + kBK - 1) / kBK), 4.0 * p->F * p->K,
-                                           p->base.num_sms, kRates);
-    return choice.slices > 0 ? forward_few<OUT>(p, choice, X, W, H, gate_up, queue)
-                             : forward_many<OUT>(p, X, W, H, gate_up, queue);
+    return p->choice.slices > 0 ? forward_few<OUT>(p, X, W, H, gate_up, queue)
+                                : forward_many<OUT>(p, X, W, H, gate_up, queue);
 }
 
-bool overlaps_16(const void* a, const void* b, const void* c, const void* d) {
+FewChoice choose(int64_t M, int64_t F, int64_t K, int num_sms) {
+    constexpr FewRates kRates{0.22, 0.35, 1.35, 0.29, 1.0};
+    const int64_t few = ((M + kTileSide - 1) / kTileSide) * ((F + kTileSide / 2 - 1) / (kTileSide / 2));
+    const int64_t pair = ((M + 2 * kBM - 1) / (2 * kBM)) * ((F + kTileF - 1) / kTileF);
+    return choose_kernel(M, few, pair, static_cast<int>((K + kBK - 1) / kBK), 4.0 * F * K, num_sms, kRates);
+}
+
+bool misaligned(const void* a, const void* b, const void* c, const void* d) {
     return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(c) |
              reinterpret_cast<uintptr_t>(d)) & 15u) != 0;
 }
@@ -426,6 +429,7 @@ gemm_status_t gemm_gated_plan_create(int64_t M, int64_t F, int64_t K, gemm_elem_
         delete p;
         return st;
     }
+    p->choice = choose(M, F, K, p->base.num_sms);
     const gemm_dtype_t type = elem == GEMM_ELEM_F16 ? GEMM_F16 : GEMM_BF16;
     if (!(elem == GEMM_ELEM_F16 ? prepare<kOutF16>() : prepare<kOutBF16>())) st = GEMM_ERR_LAUNCH;
     if (st == GEMM_OK) st = gemm_plan_create(M, K, 2 * F, type, GEMM_LAYOUT_NN, &p->dx);
@@ -445,7 +449,7 @@ gemm_status_t gemm_gated_forward(gemm_gated_plan_t p, const void* X, const void*
     if (st != GEMM_OK) return st;
     if (p->M == 0 || p->F == 0) return GEMM_OK;
     if (!H || (p->K > 0 && (!X || !W))) return GEMM_ERR_INVALID_ARG;
-    if (overlaps_16(X, W, H, gate_up)) return GEMM_ERR_ALIGNMENT;
+    if (misaligned(X, W, H, gate_up)) return GEMM_ERR_ALIGNMENT;
     if (p->K == 0) {
         if (launch_zero_fill(H, p->M * p->F * 2, p->base.num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
             (gate_up && launch_zero_fill(gate_up, p->M * p->F * 4, p->base.num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)) {
@@ -468,7 +472,7 @@ gemm_status_t gemm_gated_backward(gemm_gated_plan_t p, const void* X, const void
     const bool some = p->M > 0 && p->F > 0;
     if (some && (!gate_up || !dH || !dgate_up)) return GEMM_ERR_INVALID_ARG;
     if ((dX && some && p->K > 0 && !W) || (dW && some && p->K > 0 && !X)) return GEMM_ERR_INVALID_ARG;
-    if (overlaps_16(X, W, gate_up, dH) || overlaps_16(dgate_up, dX, dW, nullptr)) return GEMM_ERR_ALIGNMENT;
+    if (misaligned(X, W, gate_up, dH) || misaligned(dgate_up, dX, dW, nullptr)) return GEMM_ERR_ALIGNMENT;
     const gbt::Queue queue{stream, p->base.device};
     if (some)
         st = p->elem == GEMM_ELEM_F16 ? gate_grad<__half>(p, gate_up, dH, dgate_up, queue)

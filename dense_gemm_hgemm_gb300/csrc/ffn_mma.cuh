@@ -597,7 +597,7 @@ inline FewChoice choose_kernel(int64_t rows, int64_t few_tiles, int64_t pair_til
                                const FewRates& r) {
     // (the weights' way from memory and the rest overlap, less the nearer they are to each other)
     const double memory = 2.2 + weight_bytes / 6.6e6;
-    const auto with_memory = [&](double time) { return std::sqrt(std::sqrt(std::pow(time, 4) + std::pow(memory, 4))); };
+    const auto with_memory = [&](double time) { return std::sqrt(std::sqrt(time * time * time * time + memory * memory * memory * memory)); };
     FewChoice best{0, 0};
     double least = 0;
     const bool few_only = rows <= kTileSide;

@@ -139,7 +139,7 @@ extern "C" gemm_status_t gemm_fp8_quantize(int64_t rows, int64_t cols, gemm_elem
     if (rows < 0 || cols < 0 || rows > INT32_MAX - kSide || cols > INT32_MAX - kSide || (transpose != 0 && transpose != 1))
         return GEMM_ERR_INVALID_ARG;
     const int64_t down = groups_of(rows), across = groups_of(cols);
-    if (down * across > (int64_t{1} << 30)) return GEMM_ERR_INVALID_ARG;
+    if (down * across > (int64_t{1} << 29)) return GEMM_ERR_INVALID_ARG;
     const int64_t out_cols = transpose ? rows : cols;
     if (rows > 0 && cols > 0 && (!x || !q || !scales || ldx < cols || ldq < out_cols || lds < groups_of(out_cols)))
         return GEMM_ERR_INVALID_ARG;

@@ -108,7 +108,7 @@ gemm_status_t gemm_rms_plan_destroy(gemm_rms_plan_t plan);
 /*
  * x (rows x cols of `elem`) to 8 bits: q and scales of x, or of its transpose where
  * `transpose` is 1 (q is then cols x rows).  ldq, lds: row strides of q (in bytes) and
- * of the scales.  rows, cols: 0 to 2^31 - 1, at most 2^30 squares of 128 x 128.  No plan is
+ * of the scales.  rows, cols: 0 to 2^31 - 1, at most 2^29 squares of 128 x 128.  No plan is
  * needed; the call goes to the current device.
  */
 gemm_status_t gemm_fp8_quantize(int64_t rows, int64_t cols, gemm_elem_t elem, const void *x,
@@ -172,7 +172,8 @@ gemm_status_t gemm_gated_forward(gemm_gated_plan_t plan, const void *X, const vo
  *     dX = dgate_up * W                               (M x K)
  *     dW = dgate_up^T * X                             (2F x K)
  * dX and dW may each be NULL (not computed; W and X are then not read).  dgate_up may
- * be gate_up.  dX and dW are products of gemm.h over dgate_up.  act'(0) of ReLU is 0.
+ * be gate_up; outputs overlap no other operand.  dX and dW are products of gemm.h over
+ * dgate_up.  act'(0) of ReLU is 0.
  */
 gemm_status_t gemm_gated_backward(gemm_gated_plan_t plan, const void *X, const void *W,
                                   const void *gate_up, const void *dH, void *dgate_up, void *dX,
