@@ -131,15 +131,19 @@ struct RmsInput {
     }
 };
 
-// Blocks of a forward kernel that share an SM (its registers: 80 a thread, 64 with 1024).
-constexpr int forward_blocks_an_sm(int block) { return block < 1024 ? 768 / block > 0 ? 768 / block : 1 : 1; }
+// Blocks of a forward kernel that share an SM (its registers: 80 a thread, 128 for fp32 rows, 64 with
+// 1024 threads).
+constexpr int forward_blocks_an_sm(int block, int bytes) {
+    const int threads = bytes == 4 ? 512 : 768;
+    return block < threads ? threads / block : 1;
+}
 
 // A row is held by `lanes` threads, 16 columns each: it is read once, and its sum of squares
 // and results come from registers.  A block goes over rows blockIdx.x, + gridDim.x, ... (BLOCK /
 // lanes at a time); the next row's loads are in flight during the present one's sum (not with
 // 1024 threads, whose registers do not hold two rows).
 template <typename T, typename W, int BLOCK, bool Q8, bool WHOLE>
-__global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK)) rms_forward_kernel(const RmsForwardArgs<T, W> a) {
+__global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK, sizeof(T))) rms_forward_kernel(const RmsForwardArgs<T, W> a) {
     constexpr bool kAhead = BLOCK <= 512;
     __shared__ float part[2][BLOCK / 32];
     const int lane = static_cast<int>(threadIdx.x) & (a.lanes - 1);
@@ -273,12 +277,12 @@ constexpr int backward_blocks_an_sm(int block) { return block < 512 ? 512 / bloc
 // A block goes over rows blockIdx.x, + gridDim.x, ... (BLOCK / lanes at a time) and keeps its
 // share of the weight's gradient in registers, 16 columns a lane.  The next row's loads are in
 // flight during the present one's sum (not with 1024 threads, whose registers do not hold two rows:
-// there gamma and dtotal are loaded where they are used, too, and the weight's gradient is in shared
-// memory).
+// there dtotal is loaded where it is used, too).  So are gamma, and the weight's gradient is in shared
+// memory, with 1024 threads and with fp32 rows, which take twice the registers.
 template <typename T, typename W, int BLOCK, bool WHOLE>
 __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backward_kernel(const RmsBackwardArgs<T, W> a) {
-    constexpr bool kAhead = BLOCK <= 512;
-    extern __shared__ Pair shared[];             // the weight's gradient: of 1024 threads, or of several groups
+    constexpr bool kAhead = BLOCK <= 512, kRoom = kAhead && sizeof(T) == 2;
+    extern __shared__ Pair shared[];             // the weight's gradient: of each thread, or of several groups
     __shared__ float part[2][BLOCK / 32];
     const int lane = static_cast<int>(threadIdx.x) & (a.lanes - 1);
     const int groups = BLOCK / a.lanes, group = static_cast<int>(threadIdx.x) / a.lanes;
@@ -290,7 +294,7 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
 #pragma unroll
     for (int k = 0; k < kRowPacks; ++k) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) (kAhead ? dgamma[k][i] : kept(k, i)) = Pair(0.f, 0.f);
+        for (int i = 0; i < 4; ++i) (kRoom ? dgamma[k][i] : kept(k, i)) = Pair(0.f, 0.f);
     }
     int turn = 0;
     Eight<W> gamma[kRowPacks];
@@ -298,7 +302,7 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
         const int c = first_column<WHOLE>(k * a.lanes + lane);
         gamma[k].template load<WHOLE>(a.gamma + c, a.gamma ? a.cols - c : 0);
     };
-    if constexpr (kAhead) {
+    if constexpr (kRoom) {
 #pragma unroll
         for (int k = 0; k < kRowPacks; ++k) load_gamma(k);
     }
@@ -315,7 +319,7 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
         }
         // (hat and g are made twice: kept over the sum, they would take the next row's registers)
         const auto hat_and_g = [&](int k, Pair (&hat)[4], Pair (&d)[4], Pair (&g)[4]) {
-            if constexpr (!kAhead) load_gamma(k);
+            if constexpr (!kRoom) load_gamma(k);
             now.t[k].get(hat);
             now.dy[k].get(d);
             gamma[k].get(g);
@@ -332,7 +336,7 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
             hat_and_g(k, hat, d, g);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                Pair& to = kAhead ? dgamma[k][i] : kept(k, i);
+                Pair& to = kRoom ? dgamma[k][i] : kept(k, i);
                 to = fma2(d[i], hat[i], to);
                 products = fma2(g[i], hat[i], products);
             }
@@ -358,7 +362,7 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
         }
     }
     if (!a.partial) return;
-    if constexpr (!kAhead) {
+    if constexpr (!kRoom) {
 #pragma unroll
         for (int k = 0; k < kRowPacks; ++k) {
 #pragma unroll
@@ -492,7 +496,7 @@ gemm_status_t forward(const RmsForwardArgs<T, W>& a, int sms, Queue queue) {
         return launch<rms_forward_wide_kernel<T, W, Q8, WHOLE>>(a.rows, kMostRowLanes, 0, queue, 1, a);
     const int block = row_block(a.lanes);
     const int64_t blocks = (a.rows + block / a.lanes - 1) / (block / a.lanes);
-    const int64_t most = static_cast<int64_t>(sms) * forward_blocks_an_sm(block), grid = blocks < most ? blocks : most;
+    const int64_t most = static_cast<int64_t>(sms) * forward_blocks_an_sm(block, sizeof(T)), grid = blocks < most ? blocks : most;
     switch (block) {
         case 128: return launch<rms_forward_kernel<T, W, 128, Q8, WHOLE>>(grid, 128, 0, queue, 1, a);
         case 256: return launch<rms_forward_kernel<T, W, 256, Q8, WHOLE>>(grid, 256, 0, queue, 1, a);
@@ -511,7 +515,8 @@ int64_t backward_grid(int64_t rows, int lanes, int sms) {
 template <typename T, typename W, bool WHOLE>
 gemm_status_t backward(const RmsBackwardArgs<T, W>& a, int64_t grid, Queue queue) {
     const int block = row_block(a.lanes);
-    const size_t smem = block > a.lanes || block == kMostRowLanes ? static_cast<size_t>(block) * kLaneColumns * sizeof(float) : 0;
+    const bool shared = block > a.lanes || block == kMostRowLanes || sizeof(T) == 4;
+    const size_t smem = shared ? static_cast<size_t>(block) * kLaneColumns * sizeof(float) : 0;
     switch (block) {
         case 128: return launch<rms_backward_kernel<T, W, 128, WHOLE>>(grid, 128, smem, queue, 1, a);
         case 256: return launch<rms_backward_kernel<T, W, 256, WHOLE>>(grid, 256, smem, queue, 1, a);
