@@ -435,7 +435,8 @@ bool prepare() {
 FewChoice choose(const gemm_fp8_plan* p) {
     constexpr FewRates kRates{0.29, 0.33, 1.6, 0.38, 0.5};
     if (p->b_scales != GEMM_SCALE_SQUARE) return FewChoice{0, 0};
-    return choose_kernel(p->M, gbt::groups_of(p->M) * gbt::groups_of(p->N), ((p->M + 255) / 256) * ((p->N + 255) / 256),
+    const int64_t tiles = ((p->M + 255) / 256) * ((p->N + 255) / 256), pairs = p->base.num_sms / 2;
+    return choose_kernel(p->M, gbt::groups_of(p->M) * gbt::groups_of(p->N), static_cast<double>((tiles + pairs - 1) / pairs),
                          static_cast<int>(gbt::groups_of(p->K)), static_cast<double>(p->N) * p->K, p->base.num_sms, kRates);
 }
 

@@ -11,6 +11,7 @@ struct gemm_gated_plan {
     gemm_activation_t act;
     gbf::PlanBase base;
     gbf::FewChoice choice;       // of the forward kernel
+    int width;                   // of the tiles of the kernel of many rows
     gemm_plan_t dx, dw;          // the gradients' products
 };
 
@@ -18,7 +19,7 @@ namespace gbf {
 namespace {
 
 constexpr int kPairStages = 6;
-constexpr int kTileF = 128;                       // columns of H in a tile
+constexpr int kTileF = 128;                       // columns of H in a tile, at most
 constexpr int kPairEpilogue = 8;                  // epilogue warps: two to each quarter of the TMEM lanes
 constexpr int kPairThreads = 64 + 32 * kPairEpilogue;
 using PairLayout = SmemLayout2<2 * kTileF, kPairStages, 1>;
@@ -26,9 +27,12 @@ static_assert(kPairEpilogue * PairLayout::kStoreBufBytes <= PairLayout::kStaging
 
 struct GatedParams {
     int32_t M, F;
+    int32_t width;               // columns of H in a tile: 64 to 128, a multiple of 16
     int32_t num_kb, m_blocks, num_units;
     uint32_t idesc, tx_extra;
-    int32_t act, keep;
+    int32_t act;
+    void* H;
+    void* gate_up;               // NULL: not kept
     int32_t* error_word;
     uint64_t timeout_ns;
     RasterDiv rd;
@@ -39,7 +43,9 @@ struct GatedParams {
 // leader brings the gate's rows and its peer the other half's: both products of one column of
 // H end in the same TMEM lane, columns c and 128 + c, and the epilogue has them side by side.
 // The main loop is the plain product's (gemm_kernel_2cta.cuh), bound by the tensor cores; eight
-// epilogue warps of 64 columns keep the activation behind it.
+// epilogue warps of 64 columns keep the activation behind it.  Narrower tiles (a smaller N) take the place
+// of a last wave that would be nearly empty; their last columns, less than 64, are stored by
+// each thread from its row.
 template <int OUT>
 __global__ void __launch_bounds__(kPairThreads, 1)
     gated_pair_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_gate,
@@ -50,7 +56,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     constexpr int kStages = kPairStages;
     constexpr int kBN = 2 * kTileF;
     constexpr uint32_t kTmemCols = 2 * kBN;
-    constexpr uint32_t kPairTx = 2 * L::kStageBytes;
+    const uint32_t pair_tx = 2 * (L::kASlotBytes + static_cast<uint32_t>(p.width) * kRowBytes);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -109,7 +115,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             for (int32_t u = pair; ok && u < p.num_units; u += npairs) {
                 int32_t m_blk, f_blk;
                 raster_tile_fast(p.m_blocks, p.rd, u, &m_blk, &f_blk);
-                const int32_t x_row = (2 * m_blk + static_cast<int32_t>(rank)) * kBM, w_row = f_blk * kTileF;
+                const int32_t x_row = (2 * m_blk + static_cast<int32_t>(rank)) * kBM, w_row = f_blk * p.width;
                 for (int32_t kb = 0; kb < p.num_kb; ++kb) {
                     if (issued >= kStages &&
                         !wait_phase(smem_addr(&ctl->empty[stage]), phase ^ 1u, watch, kSiteProducerEmpty)) {
@@ -117,7 +123,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         break;
                     }
                     const uint32_t full = smem_addr(&ctl->full[stage]);
-                    if (leader) mbar_arrive_expect_tx(full, kPairTx + p.tx_extra);
+                    if (leader) mbar_arrive_expect_tx(full, pair_tx + p.tx_extra);
                     const uint32_t full_lead = map_to_rank(full, 0);
                     tma_load_2d_pair(ring + stage * L::kASlotBytes, &tmap_x, full_lead, kb * kBK, x_row);
                     tma_load_2d_pair(ring_b + stage * L::kBTileBytes, tmap_w, full_lead, kb * kBK, w_row);
@@ -178,18 +184,33 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const uint32_t lanes_at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(c);
         const uint32_t store_buf = staging + static_cast<uint32_t>((warp - 2) * L::kStoreBufBytes);
         uint32_t turn = 0;
-        // 64 columns of 32 rows through the warp's buffer, 32 columns of them at a time
-        const auto store = [&](const CUtensorMap* map, int32_t x, int32_t y, auto columns) {
-            if (lane == 0) bulk_wait_group_read<0>();
-            __syncwarp();
+        const int cols = min(64, p.width - c);           // of the warp
+        // its columns of 32 rows, 32 at a time: 64 through the warp's buffer, fewer from the registers
+        // to row y + lane of a matrix whose rows are ld apart
+        const auto store = [&](const CUtensorMap* map, void* to, int64_t ld, int32_t x, int32_t y, auto columns) {
+            const bool whole = cols == 64;
+            if (whole) {
+                if (lane == 0) bulk_wait_group_read<0>();
+                __syncwarp();
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                if (h * 32 >= cols) break;
                 uint32_t v[32], w[16];
                 columns(h * 32, v);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) w[i] = pack2<OUT>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                stage_store_row(store_buf, lane, h * 4, w, 4);
+                if (whole) {
+                    stage_store_row(store_buf, lane, h * 4, w, 4);
+                } else if (y + lane < p.M) {
+                    uint16_t* row = static_cast<uint16_t*>(to) + static_cast<int64_t>(y + lane) * ld + x + h * 32;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)              // (F % 8 == 0)
+                        if (h * 32 + g * 8 < cols && x + h * 32 + g * 8 < p.F)
+                            *reinterpret_cast<uint4*>(row + g * 8) = make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
+                }
             }
+            if (!whole) return;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -200,23 +221,24 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int32_t u = pair; u < p.num_units; u += npairs, ++turn) {
             int32_t m_blk, f_blk;
             raster_tile_fast(p.m_blocks, p.rd, u, &m_blk, &f_blk);
-            const int32_t y = (2 * m_blk + static_cast<int32_t>(rank)) * kBM + quad * 32, x = f_blk * kTileF + c;
-            const uint32_t buf = turn & 1u, gate_at = lanes_at + buf * kBN, up_at = gate_at + kTileF;
+            const int32_t y = (2 * m_blk + static_cast<int32_t>(rank)) * kBM + quad * 32, x = f_blk * p.width + c;
+            const uint32_t buf = turn & 1u, gate_at = lanes_at + buf * kBN, up_at = gate_at + static_cast<uint32_t>(p.width);
             if (!wait_phase(smem_addr(&ctl->tmem_full[buf]), (turn >> 1) & 1u, watch, kSiteEpiTmemFull)) break;
             tc_fence_after();
-            if (y < p.M && x < p.F) {                    // (the whole warp)
+            if (y < p.M && x < p.F && cols > 0) {        // (the whole warp)
                 const auto products = [&](uint32_t at) {
                     return [=](int col, uint32_t (&v)[32]) {
                         tmem_ld_32x32b_x32(at + static_cast<uint32_t>(col), v);
                         tmem_ld_wait();
                     };
                 };
-                if (p.keep) {
-                    store(&tmap_keep_gate, x, y, products(gate_at));
-                    store(&tmap_keep_up, x, y, products(up_at));
+                if (p.gate_up) {
+                    store(&tmap_keep_gate, p.gate_up, 2 * static_cast<int64_t>(p.F), x, y, products(gate_at));
+                    store(&tmap_keep_up, static_cast<uint16_t*>(p.gate_up) + p.F, 2 * static_cast<int64_t>(p.F), x, y,
+                          products(up_at));
                 }
                 with_act(p.act, [&](auto act) {
-                    store(&tmap_h, x, y, [&](int col, uint32_t (&v)[32]) {
+                    store(&tmap_h, p.H, p.F, x, y, [&](int col, uint32_t (&v)[32]) {
                         uint32_t g[32];
                         tmem_ld_32x32b_x32(gate_at + static_cast<uint32_t>(col), g);
                         tmem_ld_32x32b_x32(up_at + static_cast<uint32_t>(col), v);
@@ -357,22 +379,24 @@ gemm_status_t forward_many(const gemm_gated_plan* p, const void* X, const void* 
     CUtensorMap x, gate, up, h, keep_gate, keep_up;
     uint16_t* keep = static_cast<uint16_t*>(gate_up ? gate_up : H);
     const int64_t stride = gate_up ? 2 * F : F, second = gate_up ? F : 0;
-    if (!encode_map(&x, type, 2, X, M, K, K, kTileSide) || !encode_map(&gate, type, 2, W, F, K, K, kTileF) ||
-        !encode_map(&up, type, 2, static_cast<const uint16_t*>(W) + F * K, F, K, K, kTileF) ||
+    if (!encode_map(&x, type, 2, X, M, K, K, kTileSide) || !encode_map(&gate, type, 2, W, F, K, K, p->width) ||
+        !encode_map(&up, type, 2, static_cast<const uint16_t*>(W) + F * K, F, K, K, p->width) ||
         !encode_map(&h, type, 2, H, M, F, F, 32) || !encode_map(&keep_gate, type, 2, keep, M, F, stride, 32) ||
         !encode_map(&keep_up, type, 2, keep + second, M, F, stride, 32))
         return GEMM_ERR_TENSORMAP;
     GatedParams g{};
     g.M = static_cast<int32_t>(M);
     g.F = static_cast<int32_t>(F);
+    g.width = p->width;
     g.num_kb = static_cast<int32_t>((K + kBK - 1) / kBK);
     g.m_blocks = static_cast<int32_t>((M + 2 * kBM - 1) / (2 * kBM));
-    const int32_t f_blocks = static_cast<int32_t>((F + kTileF - 1) / kTileF);
+    const int32_t f_blocks = static_cast<int32_t>((F + p->width - 1) / p->width);
     g.num_units = g.m_blocks * f_blocks;
-    g.idesc = descriptor(OUT == kOutF16 ? 0 : 1, 2 * kBM, 2 * kTileF);
+    g.idesc = descriptor(OUT == kOutF16 ? 0 : 1, 2 * kBM, 2 * p->width);
     g.tx_extra = p->base.tx_extra;
     g.act = p->act;
-    g.keep = gate_up ? 1 : 0;
+    g.H = H;
+    g.gate_up = gate_up;
     g.error_word = p->base.error_word;
     g.timeout_ns = p->base.timeout_ns;
     // bands of eight row blocks: the 76 pairs cover about 8 x 9 tiles at a time
@@ -388,11 +412,28 @@ gemm_status_t forward(const gemm_gated_plan* p, const void* X, const void* W, vo
                                 : forward_many<OUT>(p, X, W, H, gate_up, queue);
 }
 
-FewChoice choose(int64_t M, int64_t F, int64_t K, int num_sms) {
+// The width of the tiles of the kernel of many rows, 64 to 128 columns of H: the one whose waves over the SM
+// pairs take the least, where a tile of width w takes 0.35 + 0.65 w / 128 of a full one (1000 x 3000 x 1000 17.8 us
+// with 128, 15.0 with 80; 1024 x 4096 x 2048 22.7 with 128, 21.1 with 112; from some waves on 128 is best:
+// 4096 x 8192 x 4096 277 against 286).  *waves: what they take, in waves of full tiles.
+int tile_width(int64_t M, int64_t F, int num_sms, double* waves) {
+    const int64_t pairs = num_sms / 2, rows = (M + 2 * kBM - 1) / (2 * kBM);
+    int best = kTileF;
+    for (int w = kTileF; w >= 64; w -= 16) {
+        const int64_t tiles = rows * ((F + w - 1) / w);
+        const double time = static_cast<double>((tiles + pairs - 1) / pairs) * (0.35 + 0.65 * w / kTileF);
+        if (w == kTileF || time < 0.97 * *waves) {
+            best = w;
+            *waves = time;
+        }
+    }
+    return best;
+}
+
+FewChoice choose(int64_t M, int64_t F, int64_t K, double pair_waves, int num_sms) {
     constexpr FewRates kRates{0.22, 0.35, 1.35, 0.29, 1.0};
     const int64_t few = ((M + kTileSide - 1) / kTileSide) * ((F + kTileSide / 2 - 1) / (kTileSide / 2));
-    const int64_t pair = ((M + 2 * kBM - 1) / (2 * kBM)) * ((F + kTileF - 1) / kTileF);
-    return choose_kernel(M, few, pair, static_cast<int>((K + kBK - 1) / kBK), 4.0 * F * K, num_sms, kRates);
+    return choose_kernel(M, few, pair_waves, static_cast<int>((K + kBK - 1) / kBK), 4.0 * F * K, num_sms, kRates);
 }
 
 bool misaligned(const void* a, const void* b, const void* c, const void* d) {
@@ -429,7 +470,9 @@ gemm_status_t gemm_gated_plan_create(int64_t M, int64_t F, int64_t K, gemm_elem_
         delete p;
         return st;
     }
-    p->choice = choose(M, F, K, p->base.num_sms);
+    double waves = 0;
+    p->width = tile_width(M, F, p->base.num_sms, &waves);
+    p->choice = choose(M, F, K, waves, p->base.num_sms);
     const gemm_dtype_t type = elem == GEMM_ELEM_F16 ? GEMM_F16 : GEMM_BF16;
     if (!(elem == GEMM_ELEM_F16 ? prepare<kOutF16>() : prepare<kOutBF16>())) st = GEMM_ERR_LAUNCH;
     if (st == GEMM_OK) st = gemm_plan_create(M, K, 2 * F, type, GEMM_LAYOUT_NN, &p->dx);

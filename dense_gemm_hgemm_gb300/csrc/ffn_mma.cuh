@@ -590,10 +590,10 @@ struct FewChoice {
     int kb_per_slice;
 };
 
-// few_tiles, pair_tiles: tiles of the two kernels; weight_bytes: what has to come from memory in any
-// case.  Up to 128 rows the kernel of few rows takes all: both are bound by memory there, and the
+// few_tiles: tiles of the kernel of few rows; pair_waves: waves of the other one's over the pairs of SMs;
+// weight_bytes: what has to come from memory in any case.  Up to 128 rows the kernel of few rows takes all: both are bound by memory there, and the
 // other one streams worse (1 x 8192 x 4096 gated 40 against 24 us, 128 rows 27 against 27).
-inline FewChoice choose_kernel(int64_t rows, int64_t few_tiles, int64_t pair_tiles, int num_kb, double weight_bytes, int num_sms,
+inline FewChoice choose_kernel(int64_t rows, int64_t few_tiles, double pair_waves, int num_kb, double weight_bytes, int num_sms,
                                const FewRates& r) {
     // (the weights' way from memory and the rest overlap, less the nearer they are to each other)
     const double memory = 2.2 + weight_bytes / 6.6e6;
@@ -601,10 +601,7 @@ inline FewChoice choose_kernel(int64_t rows, int64_t few_tiles, int64_t pair_til
     FewChoice best{0, 0};
     double least = 0;
     const bool few_only = rows <= kTileSide;
-    if (!few_only) {
-        const int64_t waves = (pair_tiles + num_sms / 2 - 1) / (num_sms / 2);
-        least = with_memory(3 + static_cast<double>(waves) * (num_kb * r.pair_kb + r.pair_wave));
-    }
+    if (!few_only) least = with_memory(3 + pair_waves * (num_kb * r.pair_kb + r.pair_wave));
     // CTAs of a cluster of s that are resident at once, two an SM: clusters of eight do not fill the
     // GPU's groups of SMs (15 clusters of 152 SMs with one CTA each, 36 of four)
     const double resident[] = {2.0, 2.0, 1.89, 1.57};

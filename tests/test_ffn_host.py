@@ -227,3 +227,22 @@ def test_entry_points_marshal_what_they_take(gemm_lib):
     for kind, plan, types in ((14, 1, kinds), (7, 0, kinds), (7, 1, kinds[:5]), (6, 1, kinds)):
         with pytest.raises(ValueError):
             pc.TrainCall(kind, 1, plan, bf, bf, types, 1, 1, 0, len)
+
+
+def test_entry_points_take_the_plans_device_only(gemm_lib):
+    gemm_lib.library()
+    pc = gemm_lib._pycall
+    if pc is None or not hasattr(pc, "TrainCall"):
+        pytest.skip("CPython entry points not built")
+    args, res = gemm_lib.ffn.signatures()["gemm_gated_forward"]
+    fn = ctypes.CFUNCTYPE(res, *args)(lambda *a: 0)
+    kinds = (torch.float16, torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.float8_e4m3fn)
+    call = pc.TrainCall(11, ctypes.cast(fn, ctypes.c_void_p).value, 4096, torch.bfloat16, torch.bfloat16, kinds, 40, 6, 1,
+                        lambda device: 0, 1, 200)
+
+    def at(device, rows, cols):
+        t = _Tensor(4096, (rows, cols), cols, torch.bfloat16)
+        t.get_device = lambda: device
+        return t
+    for x, w, h, want in ((1, 1, 1, 0), (0, 1, 1, -1), (1, 0, 1, -1), (1, 1, 0, -1)):
+        assert call(at(x, 6, 200), at(w, 80, 200), at(h, 6, 40), None, 9) == want

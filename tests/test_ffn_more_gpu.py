@@ -244,3 +244,23 @@ def test_norm_of_extreme_rows(gemm_lib, cols):
         far = (ref.stands_for(q.cpu(), s.cpu(), False) - want).abs()
         assert (far <= ref.conversion_bound(want, s.cpu(), False) * (1 + 1e-6) + 2 * (e + 6 * ref.U) * want.abs() + 2.0 ** -126).all()
         assert (s[0] == 2.0 ** -126).all() and (q[0].view(torch.uint8) & 0x7f).eq(0).all()
+
+
+@pytest.mark.parametrize("F", [3000, 4096, 4872, 5992, 6008, 7200, 7208, 8400, 8416, 9728])
+@pytest.mark.parametrize("elem,act", [("bf16", "silu"), ("f16", "none")])
+def test_gated_tiles_of_each_width(gemm_lib, F, elem, act):
+    """250 rows are one row of tiles: from 75 tiles of 64 columns to 76 of 128, whole and ragged at the end."""
+    M, K = 250, 1032
+    X, W = _randn(M, K, seed=F, dtype=T[elem]), _randn(2 * F, K, seed=F + 1, dtype=T[elem], scale=2 * K ** -0.5)
+    want, bound, gate_up, off = ref.gated_forward(X, W, act)
+    whole, kept_whole = (torch.full((M + 1, n), 7.0, dtype=T[elem], device="cuda") for n in (F, 2 * F))
+    with gemm_lib.GatedPlan(M, F, K, elem, act=act) as plan:
+        plan.forward(X, W, whole[:M], gate_up=kept_whole[:M])
+        plan.check()
+        alone = torch.empty(M, F, dtype=T[elem], device="cuda")
+        plan.forward(X, W, alone)
+        plan.check()
+    H, kept = whole[:M], kept_whole[:M]
+    assert torch.equal(alone, H) and (whole[M:] == 7).all() and (kept_whole[M:] == 7).all()
+    assert ((H.double() - want).abs() <= bound + ref.rounded(want, elem) * 1.01).all()
+    assert ((kept.double() - gate_up).abs() <= off + ref.rounded(gate_up, elem) * 1.01).all()
