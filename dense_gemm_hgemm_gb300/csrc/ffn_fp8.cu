@@ -11,6 +11,7 @@ struct gemm_fp8_plan {
     gemm_scale_t b_scales;
     gbf::PlanBase base;
     gbf::FewChoice choice;       // of the kernel (by squares)
+    int width;                   // of the tiles of the kernel of many rows
 };
 
 namespace gbf {
@@ -23,12 +24,12 @@ constexpr int kPairThreads = 32 * (kFirstSumWarp + kSumWarps);
 constexpr int kLaunchRegisters = 168, kFewRegisters = 72, kSumRegisters = 216;
 static_assert(128 * kFewRegisters + 256 * kSumRegisters <= kPairThreads * kLaunchRegisters, "registers of the block");
 
-// The tiles of a kind of scales (BYROW: B's go by rows).
-template <bool BYROW>
+// Tiles of 256 rows by BN columns (BYROW: B's scales go by rows).
+template <bool BYROW, int BN>
 struct Fp8Layout {
-    static constexpr int kBN = BYROW ? 128 : 256;
+    static constexpr int kBN = BN;
     static constexpr int kTurns = 512 / kBN;                           // accumulators: all of TMEM
-    static constexpr int kStages = BYROW ? 5 : 6;
+    static constexpr int kStages = BYROW ? 5 : BN == 128 ? 7 : 6;
     static constexpr int kBSlot = kBN / 2 * kRowBytes;                 // this CTA's half of B's rows
     static constexpr int kRing = kStages * (kTileSlot + kBSlot);
     static constexpr int kStoreBuf = 32 * kRowBytes;
@@ -86,14 +87,15 @@ struct Fp8Ctl {
     uint32_t tmem_base;
     int32_t abort;
 };
-static_assert(sizeof(Fp8Ctl<6>) <= 256, "control block");
+static_assert(sizeof(Fp8Ctl<7>) <= 256, "control block");
 
 // Many rows: a pair of SMs computes 256 rows of C, as the plain product's pair does
 // (gemm_kernel_2cta.cuh).  The tensor cores know no scales, so the sum over each 128 elements of
 // K has an accumulator of its own, two or four of them in turn (all of TMEM), which eight warps a CTA
 // multiply by the scales of its rows and columns and add to fp32 sums in registers.
-//   squares: tiles of 256 columns, two accumulators.  Four warps take 128 columns (one square of
-//            scales); a thread has a row, with one factor for its 128 columns.  A step is 512 cycles
+//   squares: tiles of 256 columns, two accumulators, or of 128, four.  Four warps take half of the
+//            columns (of one square of scales); a thread has a row, with one factor for them.  A step
+//            of 128 columns is 0.25 us, of 256 it is 512 cycles
 //            of the tensor cores and 128 reads of TMEM and 64 double multiply-adds of a thread:
 //            0.42 us, 2.8 PFLOP/s over one wave (0.34 where the MMAs do not wait for the warps).
 //            Accumulators of 128 columns, 32 instead of 16 columns a read and single instead of
@@ -104,13 +106,14 @@ static_assert(sizeof(Fp8Ctl<6>) <= 256, "control block");
 //            (read a step at a time they were 384 lines a step, more than the first-level cache
 //            holds).  A step is 0.37 us; in tiles of 256 columns it was 0.73, with fewer tiles to fill the
 //            SMs (1000 x 2056 x 4112: 16 us, 30 in those tiles).
-template <int OUT, bool BYROW>
+template <int OUT, bool BYROW, int BN>
 __global__ void __launch_bounds__(kPairThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                     const __grid_constant__ CUtensorMap tmap_c, const Fp8Params p) {
-    using L = Fp8Layout<BYROW>;
+    using L = Fp8Layout<BYROW, BN>;
+    static_assert(!BYROW || BN == 128, "tiles by rows");
     constexpr int kStages = L::kStages, kTurns = L::kTurns, kBN = L::kBN, kStep = 16;
-    constexpr int kTurnBits = BYROW ? 2 : 1;
+    constexpr int kTurnBits = kTurns == 4 ? 2 : 1;
     constexpr int kCols = kBN / 2;                   // of a warp
     constexpr uint32_t kPairTx = 2 * (kTileSlot + L::kBSlot);
     extern __shared__ uint8_t smem_raw[];
@@ -426,18 +429,27 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
 template <int OUT>
 bool prepare() {
-    return allow_shared<fp8_pair_kernel<OUT, false>>(Fp8Layout<false>::kTotal) &&
-           allow_shared<fp8_pair_kernel<OUT, true>>(Fp8Layout<true>::kTotal) &&
+    return allow_shared<fp8_pair_kernel<OUT, false, 256>>(Fp8Layout<false, 256>::kTotal) &&
+           allow_shared<fp8_pair_kernel<OUT, false, 128>>(Fp8Layout<false, 128>::kTotal) &&
+           allow_shared<fp8_pair_kernel<OUT, true, 128>>(Fp8Layout<true, 128>::kTotal) &&
            allow_shared<few_rows_kernel<true, OUT, 32>>(FewLayout<32>::kTotal) &&
            allow_shared<few_rows_kernel<true, OUT, 128>>(FewLayout<128>::kTotal);
 }
 
-FewChoice choose(const gemm_fp8_plan* p) {
+// The kernel and, by squares, its tiles' columns: a step of 128 takes 0.6 of one of 256, so they are taken
+// where they make less than 1.6 times the waves (512 x 4096 x 4096: 64 tiles or 32 for 76 pairs, 11.0 and
+// 15.3 us; 1024 x 4096 x 4096: 128 or 64, 18.3 and 16.2; 8192 x 8192 x 8192: 461 and 358).
+void choose(gemm_fp8_plan* p) {
     constexpr FewRates kRates{0.29, 0.33, 1.6, 0.38, 0.5};
-    if (p->b_scales != GEMM_SCALE_SQUARE) return FewChoice{0, 0};
-    const int64_t tiles = ((p->M + 255) / 256) * ((p->N + 255) / 256), pairs = p->base.num_sms / 2;
-    return choose_kernel(p->M, gbt::groups_of(p->M) * gbt::groups_of(p->N), static_cast<double>((tiles + pairs - 1) / pairs),
-                         static_cast<int>(gbt::groups_of(p->K)), static_cast<double>(p->N) * p->K, p->base.num_sms, kRates);
+    p->choice = FewChoice{0, 0};
+    p->width = 128;
+    if (p->b_scales != GEMM_SCALE_SQUARE) return;
+    const int64_t pairs = p->base.num_sms / 2, m_blocks = (p->M + 255) / 256;
+    const auto waves = [&](int64_t width) { return (m_blocks * ((p->N + width - 1) / width) + pairs - 1) / pairs; };
+    const double wide = static_cast<double>(waves(256)), narrow = 0.6 * static_cast<double>(waves(128));
+    if (narrow >= wide) p->width = 256;
+    p->choice = choose_kernel(p->M, gbt::groups_of(p->M) * gbt::groups_of(p->N), p->width == 256 ? wide : narrow,
+                              static_cast<int>(gbt::groups_of(p->K)), static_cast<double>(p->N) * p->K, p->base.num_sms, kRates);
 }
 
 template <int OUT>
@@ -451,7 +463,7 @@ gemm_status_t run(const gemm_fp8_plan* p, const void* A, const float* a_scales, 
     const int box = few && M <= 32 ? 32 : kTileSide;
     CUtensorMap a, b, c;
     if (!encode_map(&a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, A, M, K, K, box) ||
-        !encode_map(&b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, B, N, K, K, few || p->b_scales == GEMM_SCALE_SQUARE ? kTileSide : kTileSide / 2))
+        !encode_map(&b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, B, N, K, K, few ? kTileSide : p->width / 2))
         return GEMM_ERR_TENSORMAP;
     if (few) {
         FewParams f{};
@@ -481,10 +493,9 @@ gemm_status_t run(const gemm_fp8_plan* p, const void* A, const float* a_scales, 
     f.N = static_cast<int32_t>(N);
     f.num_kb = num_kb;
     f.m_blocks = static_cast<int32_t>((M + 255) / 256);
-    const int64_t tile_n = p->b_scales == GEMM_SCALE_ROW ? Fp8Layout<true>::kBN : Fp8Layout<false>::kBN;
-    const int32_t n_blocks = static_cast<int32_t>((N + tile_n - 1) / tile_n);
+    const int32_t n_blocks = static_cast<int32_t>((N + p->width - 1) / p->width);
     f.num_units = f.m_blocks * n_blocks;
-    f.idesc = descriptor(0, 256, static_cast<int>(tile_n));
+    f.idesc = descriptor(0, 256, p->width);
     f.tx_extra = p->base.tx_extra;
     f.whole_scales = num_kb % 4 == 0 && gbt::aligned(a_scales, 16) && gbt::aligned(b_scales, 16);
     f.a_scales = a_scales;
@@ -494,9 +505,15 @@ gemm_status_t run(const gemm_fp8_plan* p, const void* A, const float* a_scales, 
     // bands of eight row blocks: the 76 pairs cover about 8 x 9 tiles at a time
     f.rd = make_raster_div(f.m_blocks, n_blocks, f.m_blocks < 8 ? f.m_blocks : 8);
     const int pairs = p->base.num_sms / 2, grid = 2 * (f.num_units < pairs ? f.num_units : pairs);
-    if (p->b_scales == GEMM_SCALE_ROW)
-        return gbt::launch<fp8_pair_kernel<OUT, true>>(grid, kPairThreads, Fp8Layout<true>::kTotal, queue, 2, a, b, c, f);
-    return gbt::launch<fp8_pair_kernel<OUT, false>>(grid, kPairThreads, Fp8Layout<false>::kTotal, queue, 2, a, b, c, f);
+    const auto go = [&](auto byrow, auto width) {
+        constexpr bool kByRow = decltype(byrow)::value;
+        constexpr int kWidth = decltype(width)::value;
+        return gbt::launch<fp8_pair_kernel<OUT, kByRow, kWidth>>(grid, kPairThreads, Fp8Layout<kByRow, kWidth>::kTotal, queue, 2, a, b,
+                                                                 c, f);
+    };
+    if (p->b_scales == GEMM_SCALE_ROW) return go(std::true_type(), std::integral_constant<int, 128>());
+    return p->width == 128 ? go(std::false_type(), std::integral_constant<int, 128>())
+                           : go(std::false_type(), std::integral_constant<int, 256>());
 }
 
 }  // namespace
@@ -530,7 +547,7 @@ gemm_status_t gemm_fp8_plan_create(int64_t M, int64_t N, int64_t K, gemm_elem_t 
         delete p;
         return st;
     }
-    p->choice = choose(p);
+    choose(p);
     *plan = p;
     return GEMM_OK;
 }

@@ -246,6 +246,21 @@ def test_norm_of_extreme_rows(gemm_lib, cols):
         assert (s[0] == 2.0 ** -126).all() and (q[0].view(torch.uint8) & 0x7f).eq(0).all()
 
 
+@pytest.mark.parametrize("M,N,K", [(400, 4096, 1040), (400, 4104, 512), (300, 9728, 144), (512, 9736, 640), (768, 8192, 272)])
+@pytest.mark.parametrize("out", ["bf16", "f16"])
+def test_8_bit_tiles_of_each_width(gemm_lib, M, N, K, out):
+    """Two and three rows of tiles by squares, of 128 columns where all run at once, else of 256."""
+    a, b = (torch.randn(r, K, generator=torch.Generator().manual_seed(r + K)).to(FP8) for r in (M, N))
+    sa, sb = (torch.rand(r, ref.groups(K), generator=torch.Generator().manual_seed(r)) + 0.5 for r in (M, ref.groups(N)))
+    whole = torch.full((M + 1, N), 7.0, dtype=T[out], device="cuda")
+    with gemm_lib.Fp8Plan(M, N, K, out) as plan:
+        plan.run(a.cuda(), sa.cuda(), b.cuda(), sb.cuda(), whole[:M])
+        plan.check()
+    want, bound = ref.fp8_product(a.cuda(), sa.cuda(), b.cuda(), sb.cuda(), True)
+    assert (whole[M:] == 7).all()
+    assert ((whole[:M].double() - want).abs() <= bound + ref.rounded(want, out) * 1.01).all()
+
+
 @pytest.mark.parametrize("F", [3000, 4096, 4872, 5992, 6008, 7200, 7208, 8400, 8416, 9728])
 @pytest.mark.parametrize("elem,act", [("bf16", "silu"), ("f16", "none")])
 def test_gated_tiles_of_each_width(gemm_lib, F, elem, act):
