@@ -591,8 +591,9 @@ struct FewChoice {
 };
 
 // few_tiles: tiles of the kernel of few rows; pair_waves: waves of the other one's over the pairs of SMs;
-// weight_bytes: what has to come from memory in any case.  Up to 128 rows the kernel of few rows takes all: both are bound by memory there, and the
-// other one streams worse (1 x 8192 x 4096 gated 40 against 24 us, 128 rows 27 against 27).
+// weight_bytes: what has to come from memory in any case.  Up to 128 rows the kernel of few rows takes
+// all: both are bound by memory there, and the other one streams worse (1 x 8192 x 4096 gated 40 against
+// 24 us, 128 rows 27 against 27).
 inline FewChoice choose_kernel(int64_t rows, int64_t few_tiles, double pair_waves, int num_kb, double weight_bytes, int num_sms,
                                const FewRates& r) {
     // (the weights' way from memory and the rest overlap, less the nearer they are to each other)

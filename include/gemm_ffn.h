@@ -19,7 +19,8 @@
  *   GEMM_ERR_ALIGNMENT    a pointer (or a size of a product's operand) that is not
  *                         aligned as the call needs it
  * A plan is used with the device current on which it was made, by one thread and on
- * one stream at a time (graphs captured from one plan are replayed one after another).  All sums and statistics are fp32; a result is rounded once, to nearest even.
+ * one stream at a time (graphs captured from one plan are replayed one after another).
+ * All sums and statistics are fp32; a result is rounded once, to nearest even.
  * Results do not depend on the schedule: the same inputs give the same bits.
  */
 #ifndef GB300_GEMM_FFN_H
@@ -124,14 +125,16 @@ typedef struct gemm_fp8_plan *gemm_fp8_plan_t;
  * A[i][k] * B[j][k], with A M x K and B N x K (e4m3, K-contiguous) and C M x N of `out`
  * (GEMM_ELEM_F16 or GEMM_ELEM_BF16).  A's scales go by rows, B's by b_scales: squares
  * (weights) or rows (where both are activations).  K has to be a multiple of 16 and N of
- * 8 (GEMM_ERR_ALIGNMENT).
+ * 8 (GEMM_ERR_ALIGNMENT); M, N <= 2^31 - 257, K <= 2^31 - 129, and at most 2^27 tiles of
+ * 128 x 128 of C.
  */
 gemm_status_t gemm_fp8_plan_create(int64_t M, int64_t N, int64_t K, gemm_elem_t out,
                                    gemm_scale_t b_scales, gemm_fp8_plan_t *plan);
 
 /*
  * Queue the product.  A, B and C contiguous and 16-byte aligned; scales contiguous
- * (M x ceil(K/128), and N or ceil(N/128) x ceil(K/128)), 4-byte aligned.  K == 0 writes zeros.  C overlaps no operand.
+ * (M x ceil(K/128), and N or ceil(N/128) x ceil(K/128)), 4-byte aligned.  K == 0 writes
+ * zeros.  C overlaps no operand.
  */
 gemm_status_t gemm_fp8_run(gemm_fp8_plan_t plan, const void *A, const float *a_scales, const void *B,
                            const float *b_scales, void *C, void *stream);
@@ -153,7 +156,8 @@ typedef struct gemm_gated_plan *gemm_gated_plan_t;
  * A plan for H = act(X * Wg^T) * (X * Wu^T): X is M x K, W = [Wg; Wu] is 2F x K (rows
  * 0 .. F-1 the gate's weights, F .. 2F-1 the other's) and H is M x F, all of `elem`
  * (GEMM_ELEM_F16 or GEMM_ELEM_BF16) and contiguous.  F and K have to be multiples of 8
- * (GEMM_ERR_ALIGNMENT).  act: GEMM_ACT_NONE, _RELU, _GELU or _SILU.
+ * (GEMM_ERR_ALIGNMENT); M, K < 2^31, F < 2^30, and at most 2^27 tiles of 128 x 64 of H.
+ * act: GEMM_ACT_NONE, _RELU, _GELU or _SILU.
  */
 gemm_status_t gemm_gated_plan_create(int64_t M, int64_t F, int64_t K, gemm_elem_t elem,
                                      gemm_activation_t act, gemm_gated_plan_t *plan);
