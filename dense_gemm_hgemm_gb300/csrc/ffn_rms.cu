@@ -62,6 +62,7 @@ struct RmsForwardArgs {
     int64_t ldx, ldr, ldt, ldy, ldq, lds, rows;
     float eps;
     int cols, lanes;
+    bool total_along, y_along;   // (shifted kernels: at x's distance from the 16-byte boundaries)
 };
 
 // x + residual as it is kept: an fp32 sum (one rounding), rounded to T.
@@ -195,6 +196,141 @@ __global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK, sizeof(T)))
     }
 }
 
+// ---- rows off the 16-byte boundaries, all inputs' by the same distance (the type's rows of one length
+// and padding).  A lane holds Eights that start at the boundaries: row `shift` elements behind one has
+// column 8 e - shift + i in element i of Eight e, and the first and the last Eight reach beyond the row
+// (16 bytes move where one of them is the row's; the others' values are dropped, and not written).  What
+// belongs to a column (weights, their gradients) is in shared memory, with a column's place at
+// (column % 8) * stride + column / 8 + 1: lanes are neighbours there whatever the shift.  Element by element,
+// as rms_forward_kernel moves such rows, 10000 x 5003 bf16 takes 149 us (here 99) and its gradient 198 (here
+// 121).  It keeps the rows whose Eights, one more than their columns need, would take twice the lanes (16384
+// x 4096 130 us, here 165), fp32 results (8192 x 4099 92 us, here 102; the gradient 234, here 124) and
+// results of 8 bits, whose scales' columns no longer are a lane's (through shared memory, 165 us to 146 at
+// 10000 x 5003, but 93 to 119 at 8192 x 4099 fp32).
+
+struct Columns {
+    int stride;
+    __device__ __forceinline__ explicit Columns(int lanes) : stride(2 * lanes + 2) {}
+    __device__ __forceinline__ int size() const { return 8 * stride; }
+    __device__ __forceinline__ int at(int column) const { return (column & 7) * stride + (column >> 3) + 1; }   // from -8
+};
+constexpr size_t columns_bytes(int lanes) { return 8 * (2 * static_cast<size_t>(lanes) + 2) * sizeof(float); }
+
+template <typename T>
+__device__ __forceinline__ int shift_of(const T* row) {
+    return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+}
+
+// An Eight at a boundary, of which elements first .. end - 1 are the row's.
+template <typename T>
+__device__ __forceinline__ void load_part(Eight<T>& v, const T* p, int end) {
+#pragma unroll
+    for (int k = 0; k < Eight<T>::kParts; ++k) {
+        v.part[k].clear();
+        if (end > k * Eight<T>::kPer) v.part[k].raw = *reinterpret_cast<const uint4*>(p + k * Eight<T>::kPer);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void keep_part(Eight<T>& v, int first, int end) {
+    if (first <= 0 && end >= 8) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < first || i >= end) v.part[i / Eight<T>::kPer].set_raw(i % Eight<T>::kPer, from_f32<T>(0.f));
+}
+// (along: p is at a boundary)
+template <typename T>
+__device__ __forceinline__ void store_part(const Eight<T>& v, T* p, int first, int end, bool along) {
+    if (along && first <= 0 && end >= 8) {
+        v.template store<true>(p, 8);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i >= first && i < end) p[i] = reinterpret_cast<const T*>(&v.part[i / Eight<T>::kPer].raw)[i % Eight<T>::kPer];
+}
+
+// The weights (ones where there are none) at their columns' places, zeros at the others.
+template <typename W>
+__device__ __forceinline__ void place_weights(float* room, const Columns& places, const W* gamma, int cols, int lanes) {
+    for (int c = static_cast<int>(threadIdx.x) - 8; c < lanes * kLaneColumns; c += static_cast<int>(blockDim.x))
+        room[places.at(c)] = c < 0 || c >= cols ? 0.f : gamma ? to_f32(gamma[c]) : 1.f;
+}
+
+template <typename T>
+struct ShiftedInput {
+    Eight<T> x[kRowPacks], r[kRowPacks];
+    template <typename W>
+    __device__ __forceinline__ void load(const RmsForwardArgs<T, W>& a, int64_t row, int lane) {
+        const T* from = a.x + row * a.ldx;
+        const int shift = shift_of(from);
+#pragma unroll
+        for (int k = 0; k < kRowPacks; ++k) {
+            const int c = 8 * (k * a.lanes + lane) - shift, end = row < a.rows ? a.cols - c : 0;
+            load_part(x[k], from + c, end);
+            load_part(r[k], a.residual + row * a.ldr + c, a.residual ? end : 0);
+        }
+    }
+};
+
+// As rms_forward_kernel, for results of T.
+template <typename T, typename W, int BLOCK>
+__global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK, sizeof(T))) rms_forward_shifted_kernel(const RmsForwardArgs<T, W> a) {
+    constexpr bool kAhead = BLOCK <= 512;
+    extern __shared__ float room[];              // the weights
+    __shared__ float part[2][BLOCK / 32];
+    const Columns places(a.lanes);
+    const int lane = static_cast<int>(threadIdx.x) & (a.lanes - 1);
+    const int groups = BLOCK / a.lanes, group = static_cast<int>(threadIdx.x) / a.lanes;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    ShiftedInput<T> next;
+    if (kAhead) next.load(a, static_cast<int64_t>(blockIdx.x) * groups + group, lane);
+    place_weights(room, places, a.gamma, a.cols, a.lanes);
+    __syncthreads();
+    const float* const weights = room + lane;
+    int turn = 0;
+    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups; row0 < a.rows; row0 += step) {
+        const int64_t row = row0 + group;
+        const bool there = row < a.rows;
+        ShiftedInput<T> now;
+        if constexpr (kAhead) {
+            now = next;
+            next.load(a, row + step, lane);
+        } else {
+            now.load(a, row, lane);
+        }
+        const int shift = shift_of(a.x + row * a.ldx);
+        Pair squares(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kRowPacks; ++k) {
+            const int c = 8 * (k * a.lanes + lane) - shift, end = there ? a.cols - c : 0;
+            if (a.residual) add_eight(now.x[k], now.r[k]);
+            keep_part(now.x[k], -c, end);
+            squares = add_squares(now.x[k], squares);
+            if (a.total) store_part(now.x[k], a.total + row * a.ldt + c, -c, end, a.total_along);
+        }
+        const float sum = row_sum<BLOCK>(both(squares), a.lanes, part[turn]);
+        turn ^= 1;
+        const float rstd = 1.f / sqrtf(sum / static_cast<float>(a.cols) + a.eps);
+        if (a.rstd && there && lane == 0) a.rstd[row] = rstd;
+#pragma unroll
+        for (int k = 0; k < kRowPacks; ++k) {
+            const int c = 8 * (k * a.lanes + lane) - shift;
+            Pair y[4];
+            now.x[k].get(y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const Pair w(weights[places.at(2 * i - shift) + k * a.lanes], weights[places.at(2 * i + 1 - shift) + k * a.lanes]);
+                y[i] = mul2(mul2(y[i], Pair(rstd, rstd)), w);
+            }
+            Eight<T> out;
+            out.set(y);
+            store_part(out, a.y + row * a.ldy + c, -c, there ? a.cols - c : 0, a.y_along);
+        }
+    }
+}
+
 // Longer rows: a block goes over its row twice.
 template <typename T, typename W, bool Q8, bool WHOLE>
 __global__ void __launch_bounds__(kMostRowLanes) rms_forward_wide_kernel(const RmsForwardArgs<T, W> a) {
@@ -250,6 +386,7 @@ struct RmsBackwardArgs {
     float* partial;             // [grid][cols], or NULL: no gradient of gamma wanted
     int64_t ldt, lddy, lddt, lddx, rows;
     int cols, lanes;
+    bool dx_along;               // (shifted kernels: at total's distance from the 16-byte boundaries)
 };
 
 // What a lane needs of a row, as it is in memory (MORE: dtotal too).
@@ -396,6 +533,118 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
     }
 }
 
+template <typename T, bool MORE>
+struct ShiftedRow {
+    Eight<T> t[kRowPacks], dy[kRowPacks], more[kRowPacks];
+    float rstd;
+    template <typename W>
+    __device__ __forceinline__ void load(const RmsBackwardArgs<T, W>& a, int64_t row, int lane) {
+        const T* from = a.total + row * a.ldt;
+        const int shift = shift_of(from);
+#pragma unroll
+        for (int k = 0; k < kRowPacks; ++k) {
+            const int c = 8 * (k * a.lanes + lane) - shift, end = row < a.rows ? a.cols - c : 0;
+            load_part(t[k], from + c, end);
+            load_part(dy[k], a.dy + row * a.lddy + c, end);
+            if (MORE) load_part(more[k], a.dtotal + row * a.lddt + c, a.dtotal ? end : 0);
+        }
+        rstd = row < a.rows ? a.rstd[row] : 0.f;
+    }
+};
+
+// As rms_backward_kernel, with rows off the boundaries (see rms_forward_shifted_kernel): a column's sum
+// has its place in shared memory, where one lane or its neighbour adds to it.
+template <typename T, typename W, int BLOCK>
+__global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backward_shifted_kernel(const RmsBackwardArgs<T, W> a) {
+    constexpr bool kAhead = BLOCK <= 512;
+    extern __shared__ float room[];              // the weights; their gradients, of each group
+    __shared__ float part[2][BLOCK / 32];
+    const Columns places(a.lanes);
+    const int lane = static_cast<int>(threadIdx.x) & (a.lanes - 1);
+    const int groups = BLOCK / a.lanes, group = static_cast<int>(threadIdx.x) / a.lanes;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+    float* const dgamma = room + places.size();
+    wait_for_previous_kernel();
+    let_next_kernel_start();
+    ShiftedRow<T, kAhead> next;
+    if (kAhead) next.load(a, static_cast<int64_t>(blockIdx.x) * groups + group, lane);
+    place_weights(room, places, a.gamma, a.cols, a.lanes);
+    for (int i = static_cast<int>(threadIdx.x); i < groups * places.size(); i += BLOCK) dgamma[i] = 0.f;
+    __syncthreads();
+    const float* const weights = room + lane;
+    float* const sums = dgamma + group * places.size() + lane;
+    int turn = 0;
+    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups; row0 < a.rows; row0 += step) {
+        const int64_t row = row0 + group;
+        ShiftedRow<T, kAhead> now;
+        if constexpr (kAhead) {
+            now = next;
+            next.load(a, row + step, lane);
+        } else {
+            now.load(a, row, lane);
+        }
+        const int shift = shift_of(a.total + row * a.ldt);
+        const auto hat_and_g = [&](int k, Pair (&hat)[4], Pair (&d)[4], Pair (&g)[4]) {
+            now.t[k].get(hat);
+            now.dy[k].get(d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                hat[i] = mul2(hat[i], Pair(now.rstd, now.rstd));
+                g[i] = mul2(d[i], Pair(weights[places.at(2 * i - shift) + k * a.lanes], weights[places.at(2 * i + 1 - shift) + k * a.lanes]));
+            }
+        };
+        Pair products(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kRowPacks; ++k) {
+            const int c = 8 * (k * a.lanes + lane) - shift, end = row < a.rows ? a.cols - c : 0;
+            keep_part(now.t[k], -c, end);
+            keep_part(now.dy[k], -c, end);
+            Pair hat[4], d[4], g[4];
+            hat_and_g(k, hat, d, g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                products = fma2(g[i], hat[i], products);
+                float& lo = sums[places.at(2 * i - shift) + k * a.lanes];
+                float& hi = sums[places.at(2 * i + 1 - shift) + k * a.lanes];
+                fma2(d[i], hat[i], Pair(lo, hi)).get(lo, hi);
+            }
+        }
+        // (all meet here: the next row's lanes add where this one's neighbours did)
+        if (a.lanes <= 32) {
+            __syncwarp();
+        } else if (!a.dx) {
+            __syncthreads();
+        }
+        if (!a.dx) continue;
+        const float mean = row_sum<BLOCK>(both(products), a.lanes, part[turn]) / static_cast<float>(a.cols);
+        turn ^= 1;
+#pragma unroll
+        for (int k = 0; k < kRowPacks; ++k) {
+            const int c = 8 * (k * a.lanes + lane) - shift, end = row < a.rows ? a.cols - c : 0;
+            Pair hat[4], d[4], g[4];
+            hat_and_g(k, hat, d, g);
+            if constexpr (!kAhead) load_part(now.more[k], a.dtotal + row * a.lddt + c, a.dtotal ? end : 0);
+            now.more[k].get(d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                g[i] = mul2(fma2(hat[i], Pair(-mean, -mean), g[i]), Pair(now.rstd, now.rstd));
+                if (a.dtotal) g[i] = add2(g[i], d[i]);
+            }
+            Eight<T> out;
+            out.set(g);
+            store_part(out, a.dx + row * a.lddx + c, -c, end, a.dx_along);
+        }
+    }
+    if (!a.partial) return;
+    __syncthreads();
+    float* to = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols;
+    for (int c = static_cast<int>(threadIdx.x); c < a.cols; c += BLOCK) {
+        float sum = 0.f;
+        for (int g = 0; g < groups; ++g) sum += dgamma[g * places.size() + places.at(c)];
+        to[c] = sum;
+    }
+}
+
 // Longer rows: dx, a row a block, twice over it.
 template <typename T, typename W, bool WHOLE>
 __global__ void __launch_bounds__(kMostRowLanes) rms_dx_wide_kernel(const RmsBackwardArgs<T, W> a) {
@@ -490,6 +739,30 @@ __global__ void __launch_bounds__(kJoinThreads) rms_dgamma_join_kernel(const flo
 
 constexpr int row_block(int lanes) { return lanes < 128 ? 128 : lanes; }
 
+// Whether rows of q lie as far from the 16-byte boundaries as p's (NULL: none there).
+bool along(const void* p, int64_t ldp, const void* q, int64_t ldq, int bytes) {
+    return !q || (((reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(q)) & 15u) == 0 && (ldp - ldq) * bytes % 16 == 0);
+}
+// Whether a row's lanes hold it wherever in an Eight it starts.
+bool shiftable(int64_t cols) { return cols + 7 <= kRowColumns && row_lanes(cols + 7) == row_lanes(cols); }
+
+template <typename T, typename W>
+gemm_status_t forward_shifted(const RmsForwardArgs<T, W>& a, int sms, Queue queue) {
+    const int block = row_block(a.lanes);
+    const size_t smem = columns_bytes(a.lanes);
+    const int64_t blocks = (a.rows + block / a.lanes - 1) / (block / a.lanes);
+    const int64_t most = static_cast<int64_t>(sms) * forward_blocks_an_sm(block, sizeof(T)), grid = blocks < most ? blocks : most;
+    switch (block) {
+        case 128: return launch<rms_forward_shifted_kernel<T, W, 128>>(grid, 128, smem, queue, 1, a);
+        case 256: return launch<rms_forward_shifted_kernel<T, W, 256>>(grid, 256, smem, queue, 1, a);
+        case 512: return launch<rms_forward_shifted_kernel<T, W, 512>>(grid, 512, smem, queue, 1, a);
+        default: return launch<rms_forward_shifted_kernel<T, W, 1024>>(grid, 1024, smem, queue, 1, a);
+    }
+}
+
+// Shared memory of a gradient's shifted kernel.
+constexpr size_t backward_room(int lanes) { return columns_bytes(lanes) * (1 + row_block(lanes) / lanes); }
+
 template <typename T, typename W, bool Q8, bool WHOLE>
 gemm_status_t forward(const RmsForwardArgs<T, W>& a, int sms, Queue queue) {
     if (a.cols > kRowColumns)
@@ -525,6 +798,18 @@ gemm_status_t backward(const RmsBackwardArgs<T, W>& a, int64_t grid, Queue queue
     }
 }
 
+template <typename T, typename W>
+gemm_status_t backward_shifted(const RmsBackwardArgs<T, W>& a, int64_t grid, Queue queue) {
+    const int block = row_block(a.lanes);
+    const size_t smem = backward_room(a.lanes);
+    switch (block) {
+        case 128: return launch<rms_backward_shifted_kernel<T, W, 128>>(grid, 128, smem, queue, 1, a);
+        case 256: return launch<rms_backward_shifted_kernel<T, W, 256>>(grid, 256, smem, queue, 1, a);
+        case 512: return launch<rms_backward_shifted_kernel<T, W, 512>>(grid, 512, smem, queue, 1, a);
+        default: return launch<rms_backward_shifted_kernel<T, W, 1024>>(grid, 1024, smem, queue, 1, a);
+    }
+}
+
 template <typename F>
 gemm_status_t with_types(const gemm_rms_plan* p, F f) {
     return with_elem(p->elem, [&](auto t) {
@@ -534,13 +819,22 @@ gemm_status_t with_types(const gemm_rms_plan* p, F f) {
 }
 
 // Lets the kernels of long rows have the shared memory that they ask for.
+template <auto KERNEL>
+bool allow(size_t bytes) {
+    return cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) == cudaSuccess;
+}
 template <typename T, typename W>
 gemm_status_t prepare() {
-    constexpr int kBytes = kMostRowLanes * kLaneColumns * static_cast<int>(sizeof(float));
-    constexpr auto kAttribute = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    if (cudaFuncSetAttribute(rms_backward_kernel<T, W, kMostRowLanes, true>, kAttribute, kBytes) == cudaSuccess &&
-        cudaFuncSetAttribute(rms_backward_kernel<T, W, kMostRowLanes, false>, kAttribute, kBytes) == cudaSuccess)
-        return GEMM_OK;
+    constexpr size_t kBytes = kMostRowLanes * kLaneColumns * sizeof(float);
+    if (allow<rms_backward_kernel<T, W, kMostRowLanes, true>>(kBytes) && allow<rms_backward_kernel<T, W, kMostRowLanes, false>>(kBytes) &&
+        allow<rms_backward_shifted_kernel<T, W, 512>>(backward_room(512)) &&
+        allow<rms_backward_shifted_kernel<T, W, 1024>>(backward_room(1024))) {
+        if constexpr (sizeof(T) == 4) {
+            return GEMM_OK;
+        } else if (allow<rms_forward_shifted_kernel<T, W, 1024>>(columns_bytes(1024))) {
+            return GEMM_OK;
+        }
+    }
     cudaGetLastError();
     return GEMM_ERR_LAUNCH;
 }
@@ -610,14 +904,19 @@ gemm_status_t gemm_rms_forward(gemm_rms_plan_t p, int64_t rows, const void* x, i
     if (rows == 0) return GEMM_OK;
     const bool whole = p->cols % 8 == 0 && gbt::rows_aligned(x, ldx, e) && gbt::packs_aligned(residual, ldr, e) &&
                        gbt::packs_aligned(total, ldt, e) && gbt::rows_aligned(y, ldy, e) && gbt::aligned(gamma, 16);
+    const bool shifted = !whole && gbt::shiftable(p->cols) && gbt::along(x, ldx, residual, ldr, e);
     return gbt::with_types(p, [&](auto t, auto v) {
         using T = decltype(t);
         using W = decltype(v);
         const gbt::RmsForwardArgs<T, W> a{static_cast<const T*>(x), static_cast<const T*>(residual),
                                           static_cast<const W*>(gamma), static_cast<T*>(total), static_cast<T*>(y), nullptr,
                                           nullptr, rstd, ldx, ldr, ldt, ldy, 0, 0, rows, eps, static_cast<int>(p->cols),
-                                          gbt::row_lanes(p->cols)};
+                                          gbt::row_lanes(p->cols), gbt::along(x, ldx, total, ldt, e),
+                                          gbt::along(x, ldx, y, ldy, e)};
         const gbt::Queue queue{stream, p->device};
+        if constexpr (sizeof(T) == 2) {
+            if (shifted) return gbt::forward_shifted<T, W>(a, p->num_sms, queue);
+        }
         return whole ? gbt::forward<T, W, false, true>(a, p->num_sms, queue) : gbt::forward<T, W, false, false>(a, p->num_sms, queue);
     });
 }
@@ -639,7 +938,7 @@ gemm_status_t gemm_rms_forward_fp8(gemm_rms_plan_t p, int64_t rows, const void* 
         const gbt::RmsForwardArgs<T, W> a{static_cast<const T*>(x), static_cast<const T*>(residual),
                                           static_cast<const W*>(gamma), static_cast<T*>(total), nullptr,
                                           static_cast<uint8_t*>(q), scales, rstd, ldx, ldr, ldt, 0, ldq, lds, rows, eps,
-                                          static_cast<int>(p->cols), gbt::row_lanes(p->cols)};
+                                          static_cast<int>(p->cols), gbt::row_lanes(p->cols), false, false};
         const gbt::Queue queue{stream, p->device};
         return whole ? gbt::forward<T, W, true, true>(a, p->num_sms, queue) : gbt::forward<T, W, true, false>(a, p->num_sms, queue);
     });
@@ -660,6 +959,9 @@ gemm_status_t gemm_rms_backward(gemm_rms_plan_t p, int64_t rows, const void* tot
     if (st != GEMM_OK || (!dx && !dgamma)) return st;
     const bool whole = p->cols % 8 == 0 && gbt::rows_aligned(total, ldt, e) && gbt::rows_aligned(dy, lddy, e) &&
                        gbt::packs_aligned(dtotal, lddt, e) && gbt::packs_aligned(dx, lddx, e) && gbt::aligned(gamma, 16);
+    // (a result's place decides nothing but its stores: the same numbers wherever it goes)
+    const bool shifted = !whole && gbt::shiftable(p->cols) && gbt::along(total, ldt, dy, lddy, e) &&
+                         gbt::along(total, ldt, dtotal, lddt, e);
     const gbt::Queue queue{stream, p->device};
     return gbt::with_types(p, [&](auto t, auto v) {
         using T = decltype(t);
@@ -668,7 +970,8 @@ gemm_status_t gemm_rms_backward(gemm_rms_plan_t p, int64_t rows, const void* tot
         const unsigned tiles = static_cast<unsigned>((p->cols + 31) / 32);
         const gbt::RmsBackwardArgs<T, W> a{static_cast<const T*>(total), static_cast<const W*>(gamma), rstd,
                                            static_cast<const T*>(dy), static_cast<const T*>(dtotal), static_cast<T*>(dx),
-                                           dgamma ? p->partial : nullptr, ldt, lddy, lddt, lddx, rows, cols, lanes};
+                                           dgamma ? p->partial : nullptr, ldt, lddy, lddt, lddx, rows, cols, lanes,
+                                           gbt::along(total, ldt, dx, lddx, e)};
         gemm_status_t s = GEMM_OK;
         if (cols > gbt::kRowColumns) {
             // (the weight's gradient first: dx may overwrite dy or total)
@@ -681,7 +984,10 @@ gemm_status_t gemm_rms_backward(gemm_rms_plan_t p, int64_t rows, const void* tot
             return s;
         }
         const int64_t grid = gbt::backward_grid(rows, lanes, p->num_sms);
-        if (grid > 0) s = whole ? gbt::backward<T, W, true>(a, grid, queue) : gbt::backward<T, W, false>(a, grid, queue);
+        if (grid > 0)
+            s = shifted ? gbt::backward_shifted<T, W>(a, grid, queue)
+                : whole ? gbt::backward<T, W, true>(a, grid, queue)
+                        : gbt::backward<T, W, false>(a, grid, queue);
         if (s == GEMM_OK && dgamma)
             s = gbt::launch<gbt::rms_dgamma_join_kernel<W>>(tiles, gbt::kJoinThreads, 0, queue, 1, p->partial,
                                                             static_cast<int>(grid), cols, static_cast<W*>(dgamma));

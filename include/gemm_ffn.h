@@ -71,7 +71,9 @@ gemm_status_t gemm_rms_plan_create(int64_t max_rows, int64_t cols, gemm_elem_t e
  * the backward call takes.  eps >= 0.  The sum of squares is fp32: it has to stay within
  * that type (elements of up to about 1e18; a row beyond has rstd 0), and with eps == 0 a
  * row's mean square may not underflow.  total and y may each be x or residual (same
- * stride), but not the same matrix; matrices overlap in no other way.
+ * stride), but not the same matrix; matrices overlap in no other way.  Rows are read in
+ * 16 aligned bytes, of which at least one is the row's; only a row's own elements are used
+ * and written.
  */
 gemm_status_t gemm_rms_forward(gemm_rms_plan_t plan, int64_t rows, const void *x, int64_t ldx,
                                const void *residual, int64_t ldr, const void *gamma, float eps,

@@ -246,6 +246,72 @@ def test_norm_of_extreme_rows(gemm_lib, cols):
         assert (s[0] == 2.0 ** -126).all() and (q[0].view(torch.uint8) & 0x7f).eq(0).all()
 
 
+def _off(values, first, pad):
+    """A device matrix of `values` whose first element lies `first` elements behind a boundary and whose rows stand
+    `pad` elements apart, and the whole of its buffer, filled with 7 elsewhere."""
+    rows, cols = values.shape
+    whole = torch.full((first + rows * (cols + pad) + 8,), 7.0, dtype=values.dtype, device="cuda")
+    m = whole.as_strided((rows, cols), (cols + pad, 1), first)
+    m.copy_(values)
+    return m, whole
+
+
+def _only_in(m, whole):
+    m.fill_(7.0)
+    return bool((whole == 7).all())
+
+
+@pytest.mark.parametrize("cols", [1, 2, 7, 9, 121, 249, 250, 255, 505, 506, 1001, 1024, 2041, 2048, 4089, 4090, 8185, 8186, 8192,
+                                  16377, 16378])
+@pytest.mark.parametrize("elem,weight", [("bf16", "f32"), ("f16", "f16"), ("f32", "f32")])
+def test_norm_of_rows_off_the_boundaries(gemm_lib, cols, elem, weight):
+    """Inputs at one distance from the boundaries or at several, results at the same or at another: the same numbers
+    wherever the results go, and nothing written beside them."""
+    rows = 37 if cols < 4000 else 5
+    x, r, dy, dt = (_randn(rows, cols, seed=s + cols, dtype=T[elem]) for s in range(4))
+    gamma = (1 + 0.2 * _randn(cols, seed=9)).to(T[weight])
+    total = ref.rms_total(x, r)
+    want, want_rstd = ref.rms_forward(total, gamma, 1e-5)
+    e = ref.rms_error(cols)
+    zeros = torch.zeros_like(x)
+    with gemm_lib.RmsNormPlan(rows, cols, elem, weight=weight) as plan:
+        for first, pad, other in ((1, 0, 1), (3, 5, 3), (7, 8, 7), (0, 1, 0), (2, 3, 5)):
+            (a, _), (b, _), (d, _), (m, _) = (_off(v, at, pad) for v, at in ((x, first), (r, other), (dy, first), (dt, other)))
+            (y, y_all), (t, t_all), (far, far_all), (t2, _) = (
+                _off(zeros, *at) for at in ((first, pad), (first, pad), (first + 1, pad + 2), (0, 0)))
+            rstd = torch.empty(rows, device="cuda")
+            plan.forward(a, gamma, y, rstd, residual=b, total=t)
+            plan.forward(a, gamma, far, residual=b, total=t2)
+            assert torch.equal(y, far) and torch.equal(t, t2) and torch.equal(t, total)
+            assert ((rstd.double() - want_rstd).abs() <= e * want_rstd).all()
+            assert ((y.double() - want).abs() <= 1.01 * (e + 3 * ref.U) * want.abs() + ref.rounded(want, elem)).all()
+            assert all(_only_in(*v) for v in ((y, y_all), (t, t_all), (far, far_all)))
+            (q, q_all), (s, s_all) = _off(torch.zeros(rows, cols, device="cuda").to(torch.uint8), first, 1), _off(
+                torch.zeros(rows, ref.groups(cols), device="cuda"), 0, 1)
+            plan.forward_fp8(a, gamma, q.view(FP8), s, residual=b)
+            off = (ref.stands_for(q.view(FP8), s, False) - want).abs()
+            assert (off <= ref.conversion_bound(want, s, False) * (1 + 1e-6) + 2 * (e + 6 * ref.U) * want.abs() + 2.0 ** -126).all()
+            largest = ref.quantize(want.float().cpu(), False)[1].double().cuda()
+            assert ((s.double() - largest).abs() <= (e + 6 * ref.U) * largest).all()
+            assert _only_in(q, q_all) and _only_in(s, s_all)
+            rstd = want_rstd.float()
+            (dx, dx_all), (far, far_all) = _off(zeros, first, pad), _off(zeros, first + 1, pad + 2)
+            t.copy_(total)
+            dgamma, again = torch.empty_like(gamma), torch.empty_like(gamma)
+            plan.backward(t, gamma, rstd, d, dx, dgamma, dtotal=m)
+            plan.backward(t, gamma, rstd, d, far, dtotal=m)
+            plan.backward(t, gamma, rstd, d, None, again)
+            grad, grad_gamma = ref.rms_backward(total, gamma, rstd, dy, dt)
+            bound, bound_gamma = ref.rms_backward_bounds(total, gamma, rstd, dy, dt, elem, weight)
+            assert torch.equal(dx, far)
+            for got in (dgamma, again):
+                assert ((got.double() - grad_gamma).abs() <= bound_gamma).all()
+            assert ((dx.double() - grad).abs() <= bound).all()
+            plan.backward(t, gamma, rstd, d, d, dtotal=m)
+            assert torch.equal(d, dx)
+            assert _only_in(dx, dx_all) and _only_in(far, far_all)
+
+
 @pytest.mark.parametrize("M,N,K", [(400, 4096, 1040), (400, 4104, 512), (300, 9728, 144), (512, 9736, 640), (768, 8192, 272)])
 @pytest.mark.parametrize("out", ["bf16", "f16"])
 def test_8_bit_tiles_of_each_width(gemm_lib, M, N, K, out):
