@@ -29,11 +29,12 @@ template <bool BYROW, int BN>
 struct Fp8Layout {
     static constexpr int kBN = BN;
     static constexpr int kTurns = 512 / kBN;                           // accumulators: all of TMEM
-    static constexpr int kStages = BYROW ? 5 : BN == 128 ? 7 : 6;
+    static constexpr int kStages = BN == 128 && !BYROW ? 7 : 5;
     static constexpr int kBSlot = kBN / 2 * kRowBytes;                 // this CTA's half of B's rows
     static constexpr int kRing = kStages * (kTileSlot + kBSlot);
     static constexpr int kStoreBuf = 32 * kRowBytes;
-    static constexpr int kStaging = kSumWarps * kStoreBuf;
+    static constexpr int kStoreBufs = BN / 128;                        // of a warp: one for 64 columns
+    static constexpr int kStaging = kSumWarps * kStoreBufs * kStoreBuf;
     static constexpr int kScaleSlot = 2 * kTileSide * 16;              // BYROW: of 128 columns and 128 rows, four steps
     static constexpr int kTotal = 1024 + kRing + kStaging + 256 + (BYROW ? 4 * kScaleSlot : 0);
     static_assert(kTotal <= 232448, "exceeds the 227 KiB a CTA may use");
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         more_registers<kSumRegisters>();
         const int quad = warp & 3, which = (warp - kFirstSumWarp) >> 2;   // which half of the columns
         const uint32_t lanes_at = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(which * kCols);
-        const uint32_t buf_at = staging + static_cast<uint32_t>((warp - kFirstSumWarp) * L::kStoreBuf);
+        const uint32_t buf_at = staging + static_cast<uint32_t>((warp - kFirstSumWarp) * L::kStoreBufs * L::kStoreBuf);
         uint32_t turn = 0, four = 0;                         // steps; BYROW: runs of four
         bool ok = true;
         for (int32_t u = pair; ok && u < p.num_units; u += npairs) {
@@ -290,16 +291,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             raster_tile_fast(p.m_blocks, p.rd, u, &m_blk, &n_blk);
             const int32_t y = (2 * m_blk + static_cast<int32_t>(rank)) * kBM + quad * 32;
             const int32_t x = n_blk * kBN + which * kCols;
-            // 64 columns of the warp's rows, which `place` writes to its buffer
+            // 64 columns of the warp's rows, which `place` writes to a buffer of the warp
             const auto store = [&](int c, auto place) {
                 if (y >= p.M || x + c >= p.N) return;        // (the whole warp)
-                if (lane == 0) bulk_wait_group_read<0>();
+                const uint32_t buf = buf_at + static_cast<uint32_t>(c / 64 * L::kStoreBuf);
+                if (lane == 0) bulk_wait_group_read<L::kStoreBufs - 1>();
                 __syncwarp();
-                place();
+                place(buf);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    tma_store_2d(&tmap_c, buf_at, x + c, y);
+                    tma_store_2d(&tmap_c, buf, x + c, y);
                     bulk_commit_group();
                 }
             };
@@ -344,11 +346,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (!ok) break;
 #pragma unroll
                 for (int c = 0; c < kCols; c += 64) {
-                    store(c, [&] {
+                    store(c, [&](uint32_t buf) {
                         uint32_t w[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) w[i] = pack2<OUT>(acc[c + 2 * i], acc[c + 2 * i + 1]);
-                        stage_store_row(buf_at, lane, 0, w, 8);
+                        stage_store_row(buf, lane, 0, w, 8);
                     });
                 }
             } else {
@@ -399,13 +401,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     }
                 }
                 if (!ok) break;
-                store(0, [&] {
+                store(0, [&](uint32_t buf) {
 #pragma unroll
                     for (int c = 0; c < kCols / kStep; ++c) {
 #pragma unroll
                         for (int j = 0; j < kStep; j += 2) {
                             const int r = c % 2 * 16 + j / 2 % 2 * 8 + group, unit = c / 2 * 4 + j / 4;
-                            st_shared_u1(buf_at + static_cast<uint32_t>(r * kRowBytes + ((unit ^ (r & 7)) * 16) + two * 4),
+                            st_shared_u1(buf + static_cast<uint32_t>(r * kRowBytes + ((unit ^ (r & 7)) * 16) + two * 4),
                                          pack2<OUT>(acc[c * kStep + j], acc[c * kStep + j + 1]));
                         }
                     }
