@@ -1,5 +1,7 @@
 // ffn_rms.cu -- root-mean-square norm with the residual's addition (gemm_ffn.h).
+#include <algorithm>
 #include <new>
+#include <type_traits>
 
 #include "ffn_common.cuh"
 
@@ -18,13 +20,39 @@ constexpr int kLaneColumns = 8 * kRowPacks;
 constexpr int kMostRowLanes = 1024;
 constexpr int kRowColumns = kMostRowLanes * kLaneColumns;   // the longest row that a block holds
 
-// Lanes that hold a row: a power of two, so that a group divides a block; 16 at least, which
-// are the 128 columns of a scale.
+// Lanes that hold a row: up to 128 a power of two, so that a group divides a block of 128; 16 at least, which
+// are the 128 columns of a scale.  More are a block of their own, whole warps (in powers of two, 8192 x 5120
+// bf16 took 65 us instead of 52, to 8 bits 75 instead of 49, its gradient 77 instead of 66).
+constexpr int kSharedBlock = 128;
 int row_lanes(int64_t cols) {
     int lanes = 16;
-    while (lanes < kMostRowLanes && lanes * kLaneColumns < cols) lanes *= 2;
-    return lanes;
+    while (lanes < kSharedBlock && lanes * kLaneColumns < cols) lanes *= 2;
+    if (lanes * kLaneColumns >= cols) return lanes;
+    return static_cast<int>(std::min<int64_t>((cols + 32 * kLaneColumns - 1) / (32 * kLaneColumns) * 32, kMostRowLanes));
 }
+constexpr int row_block(int lanes) { return lanes < kSharedBlock ? kSharedBlock : lanes; }
+// The block sizes that kernels are made for, each for lanes up to it.
+template <typename F>
+gemm_status_t with_block(int lanes, F f) {
+    if (lanes <= kSharedBlock) return f(std::integral_constant<int, kSharedBlock>());
+    if (lanes <= 256) return f(std::integral_constant<int, 256>());
+    if (lanes <= 384) return f(std::integral_constant<int, 384>());
+    if (lanes <= 512) return f(std::integral_constant<int, 512>());
+    if (lanes <= 768) return f(std::integral_constant<int, 768>());
+    return f(std::integral_constant<int, kMostRowLanes>());
+}
+// A thread's place in such a block.
+template <int BLOCK>
+struct RowPlace {
+    int lane, group, groups, threads;
+    __device__ __forceinline__ explicit RowPlace(int lanes) {
+        const int tid = static_cast<int>(threadIdx.x);
+        lane = BLOCK == kSharedBlock ? tid & (lanes - 1) : tid;
+        group = BLOCK == kSharedBlock ? tid / lanes : 0;
+        groups = BLOCK == kSharedBlock ? BLOCK / lanes : 1;
+        threads = BLOCK == kSharedBlock ? BLOCK : lanes;
+    }
+};
 
 // The sum over a row's lanes, in each of them.  part: one float per warp of the block (all of
 // its threads meet here where a row has more than a warp).
@@ -40,13 +68,8 @@ __device__ __forceinline__ float row_sum(float v, int lanes, float* part) {
     const int warp = static_cast<int>(threadIdx.x) / 32, warps = lanes / 32;
     if (threadIdx.x % 32 == 0) part[warp] = v;
     __syncthreads();
-    const int l = static_cast<int>(threadIdx.x) % 32;
-    v = part[warp / warps * warps + l % warps];      // every warp's sum, 32 / warps times
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        if (o < warps) v += __shfl_xor_sync(0xffffffffu, v, o);
-    }
-    return v;
+    const int l = static_cast<int>(threadIdx.x) % 32, first = lanes > kSharedBlock ? 0 : warp & -warps;
+    return warp_sum(l < warps ? part[first + l] : 0.f);
 }
 
 template <typename T, typename W>
@@ -138,6 +161,9 @@ constexpr int forward_blocks_an_sm(int block, int bytes) {
     const int threads = bytes == 4 ? 512 : 768;
     return block < threads ? threads / block : 1;
 }
+// Whether a lane's registers hold the next row, too.
+template <int BLOCK, typename T>
+constexpr bool kForwardAhead = BLOCK <= (sizeof(T) == 4 ? 512 : 768);
 
 // A row is held by `lanes` threads, 16 columns each: it is read once, and its sum of squares
 // and results come from registers.  A block goes over rows blockIdx.x, + gridDim.x, ... (BLOCK /
@@ -145,10 +171,10 @@ constexpr int forward_blocks_an_sm(int block, int bytes) {
 // 1024 threads, whose registers do not hold two rows).
 template <typename T, typename W, int BLOCK, bool Q8, bool WHOLE>
 __global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK, sizeof(T))) rms_forward_kernel(const RmsForwardArgs<T, W> a) {
-    constexpr bool kAhead = BLOCK <= 512;
+    constexpr bool kAhead = kForwardAhead<BLOCK, T>;
     __shared__ float part[2][BLOCK / 32];
-    const int lane = static_cast<int>(threadIdx.x) & (a.lanes - 1);
-    const int groups = BLOCK / a.lanes, group = static_cast<int>(threadIdx.x) / a.lanes;
+    const RowPlace<BLOCK> at(a.lanes);
+    const int lane = at.lane, group = at.group, groups = at.groups;
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     wait_for_previous_kernel();
     let_next_kernel_start();
@@ -202,11 +228,11 @@ __global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK, sizeof(T)))
 // (16 bytes move where one of them is the row's; the others' values are dropped, and not written).  What
 // belongs to a column (weights, their gradients) is in shared memory, with a column's place at
 // (column % 8) * stride + column / 8 + 1: lanes are neighbours there whatever the shift.  Element by element,
-// as rms_forward_kernel moves such rows, 10000 x 5003 bf16 takes 149 us (here 99) and its gradient 198 (here
-// 121).  It keeps the rows whose Eights, one more than their columns need, would take twice the lanes (16384
-// x 4096 130 us, here 165), fp32 results (8192 x 4099 92 us, here 102; the gradient 234, here 124) and
-// results of 8 bits, whose scales' columns no longer are a lane's (through shared memory, 165 us to 146 at
-// 10000 x 5003, but 93 to 119 at 8192 x 4099 fp32).
+// as rms_forward_kernel moves such rows, 10000 x 5003 bf16 took 149 us (here 99, 70 in blocks of whole
+// warps) and its gradient 198 (here 121, 88).  It keeps the rows whose Eights, one more than their columns
+// need, would take twice the lanes (32768 x 1024 bf16, rows of 1027: 65 us, here 79; the gradient 88, here 96),
+// fp32 results (16384 x 4096, rows of 4099: 164 us, here 186) and results of 8 bits, whose scales' columns no
+// longer are a lane's (through shared memory, 165 us to 146 at 10000 x 5003, but 93 to 119 at 8192 x 4099 fp32).
 
 struct Columns {
     int stride;
@@ -275,12 +301,12 @@ struct ShiftedInput {
 // As rms_forward_kernel, for results of T.
 template <typename T, typename W, int BLOCK>
 __global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK, sizeof(T))) rms_forward_shifted_kernel(const RmsForwardArgs<T, W> a) {
-    constexpr bool kAhead = BLOCK <= 512;
+    constexpr bool kAhead = kForwardAhead<BLOCK, T>;
     extern __shared__ float room[];              // the weights
     __shared__ float part[2][BLOCK / 32];
     const Columns places(a.lanes);
-    const int lane = static_cast<int>(threadIdx.x) & (a.lanes - 1);
-    const int groups = BLOCK / a.lanes, group = static_cast<int>(threadIdx.x) / a.lanes;
+    const RowPlace<BLOCK> at(a.lanes);
+    const int lane = at.lane, group = at.group, groups = at.groups;
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     wait_for_previous_kernel();
     let_next_kernel_start();
@@ -410,19 +436,27 @@ struct RmsRow {
 
 // Blocks of a backward kernel that share an SM (its registers: 128 a thread).
 constexpr int backward_blocks_an_sm(int block) { return block < 512 ? 512 / block : 1; }
+// Whether a lane's registers hold the next row, too ...
+template <int BLOCK, typename T>
+constexpr bool kBackwardAhead = BLOCK <= (sizeof(T) == 4 ? 512 : 768);
+// ... and of that dtotal, too; and the weights and their gradient.
+template <int BLOCK>
+constexpr bool kBackwardMore = BLOCK <= 512;
+template <int BLOCK, typename T>
+constexpr bool kBackwardRoom = BLOCK <= 512 && sizeof(T) == 2;
 
 // A block goes over rows blockIdx.x, + gridDim.x, ... (BLOCK / lanes at a time) and keeps its
 // share of the weight's gradient in registers, 16 columns a lane.  The next row's loads are in
-// flight during the present one's sum (not with 1024 threads, whose registers do not hold two rows:
-// there dtotal is loaded where it is used, too).  So are gamma, and the weight's gradient is in shared
-// memory, with 1024 threads and with fp32 rows, which take twice the registers.
+// flight during the present one's sum (not with 1024 threads, whose registers do not hold two rows;
+// above 512 dtotal is loaded where it is used).  So are gamma, and the weight's gradient is in shared
+// memory, above 512 threads and with fp32 rows, which take twice the registers.
 template <typename T, typename W, int BLOCK, bool WHOLE>
 __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backward_kernel(const RmsBackwardArgs<T, W> a) {
-    constexpr bool kAhead = BLOCK <= 512, kRoom = kAhead && sizeof(T) == 2;
+    constexpr bool kAhead = kBackwardAhead<BLOCK, T>, kMore = kBackwardMore<BLOCK>, kRoom = kBackwardRoom<BLOCK, T>;
     extern __shared__ Pair shared[];             // the weight's gradient: of each thread, or of several groups
     __shared__ float part[2][BLOCK / 32];
-    const int lane = static_cast<int>(threadIdx.x) & (a.lanes - 1);
-    const int groups = BLOCK / a.lanes, group = static_cast<int>(threadIdx.x) / a.lanes;
+    const RowPlace<BLOCK> at(a.lanes);
+    const int lane = at.lane, group = at.group, groups = at.groups;
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     wait_for_previous_kernel();
     let_next_kernel_start();
@@ -443,11 +477,11 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
 #pragma unroll
         for (int k = 0; k < kRowPacks; ++k) load_gamma(k);
     }
-    RmsRow<T, WHOLE, kAhead> next;
+    RmsRow<T, WHOLE, kMore> next;
     if (kAhead) next.load(a, static_cast<int64_t>(blockIdx.x) * groups + group, lane);
     for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups; row0 < a.rows; row0 += step) {
         const int64_t row = row0 + group;
-        RmsRow<T, WHOLE, kAhead> now;
+        RmsRow<T, WHOLE, kMore> now;
         if constexpr (kAhead) {
             now = next;
             next.load(a, row + step, lane);
@@ -486,7 +520,7 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
             const int c = first_column<WHOLE>(k * a.lanes + lane), n = row < a.rows ? a.cols - c : 0;
             Pair hat[4], d[4], g[4];
             hat_and_g(k, hat, d, g);
-            if constexpr (!kAhead) now.more[k].template load<WHOLE>(a.dtotal + row * a.lddt + c, a.dtotal ? n : 0);
+            if constexpr (!kMore) now.more[k].template load<WHOLE>(a.dtotal + row * a.lddt + c, a.dtotal ? n : 0);
             now.more[k].get(d);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -556,27 +590,27 @@ struct ShiftedRow {
 // has its place in shared memory, where one lane or its neighbour adds to it.
 template <typename T, typename W, int BLOCK>
 __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backward_shifted_kernel(const RmsBackwardArgs<T, W> a) {
-    constexpr bool kAhead = BLOCK <= 512;
+    constexpr bool kAhead = kBackwardAhead<BLOCK, T>, kMore = kBackwardMore<BLOCK>;
     extern __shared__ float room[];              // the weights; their gradients, of each group
     __shared__ float part[2][BLOCK / 32];
     const Columns places(a.lanes);
-    const int lane = static_cast<int>(threadIdx.x) & (a.lanes - 1);
-    const int groups = BLOCK / a.lanes, group = static_cast<int>(threadIdx.x) / a.lanes;
+    const RowPlace<BLOCK> at(a.lanes);
+    const int lane = at.lane, group = at.group, groups = at.groups;
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     float* const dgamma = room + places.size();
     wait_for_previous_kernel();
     let_next_kernel_start();
-    ShiftedRow<T, kAhead> next;
+    ShiftedRow<T, kMore> next;
     if (kAhead) next.load(a, static_cast<int64_t>(blockIdx.x) * groups + group, lane);
     place_weights(room, places, a.gamma, a.cols, a.lanes);
-    for (int i = static_cast<int>(threadIdx.x); i < groups * places.size(); i += BLOCK) dgamma[i] = 0.f;
+    for (int i = static_cast<int>(threadIdx.x); i < groups * places.size(); i += at.threads) dgamma[i] = 0.f;
     __syncthreads();
     const float* const weights = room + lane;
     float* const sums = dgamma + group * places.size() + lane;
     int turn = 0;
     for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups; row0 < a.rows; row0 += step) {
         const int64_t row = row0 + group;
-        ShiftedRow<T, kAhead> now;
+        ShiftedRow<T, kMore> now;
         if constexpr (kAhead) {
             now = next;
             next.load(a, row + step, lane);
@@ -623,7 +657,7 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
             const int c = 8 * (k * a.lanes + lane) - shift, end = row < a.rows ? a.cols - c : 0;
             Pair hat[4], d[4], g[4];
             hat_and_g(k, hat, d, g);
-            if constexpr (!kAhead) load_part(now.more[k], a.dtotal + row * a.lddt + c, a.dtotal ? end : 0);
+            if constexpr (!kMore) load_part(now.more[k], a.dtotal + row * a.lddt + c, a.dtotal ? end : 0);
             now.more[k].get(d);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -638,7 +672,7 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
     if (!a.partial) return;
     __syncthreads();
     float* to = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols;
-    for (int c = static_cast<int>(threadIdx.x); c < a.cols; c += BLOCK) {
+    for (int c = static_cast<int>(threadIdx.x); c < a.cols; c += at.threads) {
         float sum = 0.f;
         for (int g = 0; g < groups; ++g) sum += dgamma[g * places.size() + places.at(c)];
         to[c] = sum;
@@ -737,27 +771,24 @@ __global__ void __launch_bounds__(kJoinThreads) rms_dgamma_join_kernel(const flo
 
 // ---------------------------------------------------------------- launches
 
-constexpr int row_block(int lanes) { return lanes < 128 ? 128 : lanes; }
-
 // Whether rows of q lie as far from the 16-byte boundaries as p's (NULL: none there).
 bool along(const void* p, int64_t ldp, const void* q, int64_t ldq, int bytes) {
     return !q || (((reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(q)) & 15u) == 0 && (ldp - ldq) * bytes % 16 == 0);
 }
-// Whether a row's lanes hold it wherever in an Eight it starts.
-bool shiftable(int64_t cols) { return cols + 7 <= kRowColumns && row_lanes(cols + 7) == row_lanes(cols); }
+// Whether a row of few more lanes (a quarter at most) holds it wherever in an Eight it starts.
+bool shiftable(int64_t cols) { return cols + 7 <= kRowColumns && row_lanes(cols + 7) * 4 <= row_lanes(cols) * 5; }
+
+int64_t forward_grid(int64_t rows, int lanes, int bytes, int sms) {
+    const int block = row_block(lanes), groups = block / lanes;
+    return std::min((rows + groups - 1) / groups, static_cast<int64_t>(sms) * forward_blocks_an_sm(block, bytes));
+}
 
 template <typename T, typename W>
 gemm_status_t forward_shifted(const RmsForwardArgs<T, W>& a, int sms, Queue queue) {
-    const int block = row_block(a.lanes);
-    const size_t smem = columns_bytes(a.lanes);
-    const int64_t blocks = (a.rows + block / a.lanes - 1) / (block / a.lanes);
-    const int64_t most = static_cast<int64_t>(sms) * forward_blocks_an_sm(block, sizeof(T)), grid = blocks < most ? blocks : most;
-    switch (block) {
-        case 128: return launch<rms_forward_shifted_kernel<T, W, 128>>(grid, 128, smem, queue, 1, a);
-        case 256: return launch<rms_forward_shifted_kernel<T, W, 256>>(grid, 256, smem, queue, 1, a);
-        case 512: return launch<rms_forward_shifted_kernel<T, W, 512>>(grid, 512, smem, queue, 1, a);
-        default: return launch<rms_forward_shifted_kernel<T, W, 1024>>(grid, 1024, smem, queue, 1, a);
-    }
+    return with_block(a.lanes, [&](auto block) {
+        return launch<rms_forward_shifted_kernel<T, W, decltype(block)::value>>(forward_grid(a.rows, a.lanes, sizeof(T), sms),
+                                                                                row_block(a.lanes), columns_bytes(a.lanes), queue, 1, a);
+    });
 }
 
 // Shared memory of a gradient's shifted kernel.
@@ -767,16 +798,14 @@ template <typename T, typename W, bool Q8, bool WHOLE>
 gemm_status_t forward(const RmsForwardArgs<T, W>& a, int sms, Queue queue) {
     if (a.cols > kRowColumns)
         return launch<rms_forward_wide_kernel<T, W, Q8, WHOLE>>(a.rows, kMostRowLanes, 0, queue, 1, a);
-    const int block = row_block(a.lanes);
-    const int64_t blocks = (a.rows + block / a.lanes - 1) / (block / a.lanes);
-    const int64_t most = static_cast<int64_t>(sms) * forward_blocks_an_sm(block, sizeof(T)), grid = blocks < most ? blocks : most;
-    switch (block) {
-        case 128: return launch<rms_forward_kernel<T, W, 128, Q8, WHOLE>>(grid, 128, 0, queue, 1, a);
-        case 256: return launch<rms_forward_kernel<T, W, 256, Q8, WHOLE>>(grid, 256, 0, queue, 1, a);
-        case 512: return launch<rms_forward_kernel<T, W, 512, Q8, WHOLE>>(grid, 512, 0, queue, 1, a);
-        default: return launch<rms_forward_kernel<T, W, 1024, Q8, WHOLE>>(grid, 1024, 0, queue, 1, a);
-    }
+    return with_block(a.lanes, [&](auto block) {
+        return launch<rms_forward_kernel<T, W, decltype(block)::value, Q8, WHOLE>>(forward_grid(a.rows, a.lanes, sizeof(T), sms),
+                                                                                   row_block(a.lanes), 0, queue, 1, a);
+    });
 }
+
+// Shared memory of the weight's gradient of a block's threads.
+constexpr size_t sums_bytes(int block) { return static_cast<size_t>(block) * kLaneColumns * sizeof(float); }
 
 // Blocks of a backward launch: enough for every row, at most what the SMs hold at once.
 int64_t backward_grid(int64_t rows, int lanes, int sms) {
@@ -787,27 +816,19 @@ int64_t backward_grid(int64_t rows, int lanes, int sms) {
 
 template <typename T, typename W, bool WHOLE>
 gemm_status_t backward(const RmsBackwardArgs<T, W>& a, int64_t grid, Queue queue) {
-    const int block = row_block(a.lanes);
-    const bool shared = block > a.lanes || block == kMostRowLanes || sizeof(T) == 4;
-    const size_t smem = shared ? static_cast<size_t>(block) * kLaneColumns * sizeof(float) : 0;
-    switch (block) {
-        case 128: return launch<rms_backward_kernel<T, W, 128, WHOLE>>(grid, 128, smem, queue, 1, a);
-        case 256: return launch<rms_backward_kernel<T, W, 256, WHOLE>>(grid, 256, smem, queue, 1, a);
-        case 512: return launch<rms_backward_kernel<T, W, 512, WHOLE>>(grid, 512, smem, queue, 1, a);
-        default: return launch<rms_backward_kernel<T, W, 1024, WHOLE>>(grid, 1024, smem, queue, 1, a);
-    }
+    return with_block(a.lanes, [&](auto block) {
+        constexpr int kBlock = decltype(block)::value;
+        const bool shared = kSharedBlock > a.lanes || !kBackwardRoom<kBlock, T>;
+        return launch<rms_backward_kernel<T, W, kBlock, WHOLE>>(grid, row_block(a.lanes), shared ? sums_bytes(kBlock) : 0, queue, 1, a);
+    });
 }
 
 template <typename T, typename W>
 gemm_status_t backward_shifted(const RmsBackwardArgs<T, W>& a, int64_t grid, Queue queue) {
-    const int block = row_block(a.lanes);
-    const size_t smem = backward_room(a.lanes);
-    switch (block) {
-        case 128: return launch<rms_backward_shifted_kernel<T, W, 128>>(grid, 128, smem, queue, 1, a);
-        case 256: return launch<rms_backward_shifted_kernel<T, W, 256>>(grid, 256, smem, queue, 1, a);
-        case 512: return launch<rms_backward_shifted_kernel<T, W, 512>>(grid, 512, smem, queue, 1, a);
-        default: return launch<rms_backward_shifted_kernel<T, W, 1024>>(grid, 1024, smem, queue, 1, a);
-    }
+    return with_block(a.lanes, [&](auto block) {
+        return launch<rms_backward_shifted_kernel<T, W, decltype(block)::value>>(grid, row_block(a.lanes), backward_room(a.lanes),
+                                                                                 queue, 1, a);
+    });
 }
 
 template <typename F>
@@ -825,16 +846,19 @@ bool allow(size_t bytes) {
 }
 template <typename T, typename W>
 gemm_status_t prepare() {
-    constexpr size_t kBytes = kMostRowLanes * kLaneColumns * sizeof(float);
-    if (allow<rms_backward_kernel<T, W, kMostRowLanes, true>>(kBytes) && allow<rms_backward_kernel<T, W, kMostRowLanes, false>>(kBytes) &&
-        allow<rms_backward_shifted_kernel<T, W, 512>>(backward_room(512)) &&
-        allow<rms_backward_shifted_kernel<T, W, 1024>>(backward_room(1024))) {
-        if constexpr (sizeof(T) == 4) {
-            return GEMM_OK;
-        } else if (allow<rms_forward_shifted_kernel<T, W, 1024>>(columns_bytes(1024))) {
-            return GEMM_OK;
-        }
-    }
+    const auto wide = [](auto block) {
+        constexpr int kBlock = decltype(block)::value;
+        return allow<rms_backward_kernel<T, W, kBlock, true>>(sums_bytes(kBlock)) &&
+               allow<rms_backward_kernel<T, W, kBlock, false>>(sums_bytes(kBlock)) &&
+               allow<rms_backward_shifted_kernel<T, W, kBlock>>(backward_room(kBlock));
+    };
+    bool ok = wide(std::integral_constant<int, 768>()) && wide(std::integral_constant<int, kMostRowLanes>()) &&
+              allow<rms_backward_shifted_kernel<T, W, 384>>(backward_room(384)) &&
+              allow<rms_backward_shifted_kernel<T, W, 512>>(backward_room(512));
+    if constexpr (sizeof(T) == 2)
+        ok = ok && allow<rms_forward_shifted_kernel<T, W, 768>>(columns_bytes(768)) &&
+             allow<rms_forward_shifted_kernel<T, W, kMostRowLanes>>(columns_bytes(kMostRowLanes));
+    if (ok) return GEMM_OK;
     cudaGetLastError();
     return GEMM_ERR_LAUNCH;
 }
@@ -911,7 +935,7 @@ gemm_status_t gemm_rms_forward(gemm_rms_plan_t p, int64_t rows, const void* x, i
         const gbt::RmsForwardArgs<T, W> a{static_cast<const T*>(x), static_cast<const T*>(residual),
                                           static_cast<const W*>(gamma), static_cast<T*>(total), static_cast<T*>(y), nullptr,
                                           nullptr, rstd, ldx, ldr, ldt, ldy, 0, 0, rows, eps, static_cast<int>(p->cols),
-                                          gbt::row_lanes(p->cols), gbt::along(x, ldx, total, ldt, e),
+                                          gbt::row_lanes(p->cols + (shifted && sizeof(T) == 2 ? 7 : 0)), gbt::along(x, ldx, total, ldt, e),
                                           gbt::along(x, ldx, y, ldy, e)};
         const gbt::Queue queue{stream, p->device};
         if constexpr (sizeof(T) == 2) {
@@ -966,7 +990,7 @@ gemm_status_t gemm_rms_backward(gemm_rms_plan_t p, int64_t rows, const void* tot
     return gbt::with_types(p, [&](auto t, auto v) {
         using T = decltype(t);
         using W = decltype(v);
-        const int cols = static_cast<int>(p->cols), lanes = gbt::row_lanes(cols);
+        const int cols = static_cast<int>(p->cols), lanes = gbt::row_lanes(cols + (shifted ? 7 : 0));
         const unsigned tiles = static_cast<unsigned>((p->cols + 31) / 32);
         const gbt::RmsBackwardArgs<T, W> a{static_cast<const T*>(total), static_cast<const W*>(gamma), rstd,
                                            static_cast<const T*>(dy), static_cast<const T*>(dtotal), static_cast<T*>(dx),
