@@ -275,11 +275,23 @@ __device__ __forceinline__ void store_part(const Eight<T>& v, T* p, int first, i
         if (i >= first && i < end) p[i] = reinterpret_cast<const T*>(&v.part[i / Eight<T>::kPer].raw)[i % Eight<T>::kPer];
 }
 
-// The weights (ones where there are none) at their columns' places, zeros at the others.
+// The weights (ones where there are none) at their columns' places, zeros at the others; all loads of a
+// thread are in flight at once.
 template <typename W>
-__device__ __forceinline__ void place_weights(float* room, const Columns& places, const W* gamma, int cols, int lanes) {
-    for (int c = static_cast<int>(threadIdx.x) - 8; c < lanes * kLaneColumns; c += static_cast<int>(blockDim.x))
-        room[places.at(c)] = c < 0 || c >= cols ? 0.f : gamma ? to_f32(gamma[c]) : 1.f;
+__device__ __forceinline__ void place_weights(float* room, const Columns& places, const W* gamma, int cols, int lanes, int threads) {
+    constexpr int kEach = kLaneColumns + 1;          // of 16 columns a lane, and eight in front
+    const int first = static_cast<int>(threadIdx.x) - 8;
+    float v[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        const int c = first + j * threads;
+        v[j] = c < 0 || c >= cols ? 0.f : gamma ? to_f32(gamma[c]) : 1.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        const int c = first + j * threads;
+        if (c < lanes * kLaneColumns) room[places.at(c)] = v[j];
+    }
 }
 
 template <typename T>
@@ -312,7 +324,7 @@ __global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK, sizeof(T)))
     let_next_kernel_start();
     ShiftedInput<T> next;
     if (kAhead) next.load(a, static_cast<int64_t>(blockIdx.x) * groups + group, lane);
-    place_weights(room, places, a.gamma, a.cols, a.lanes);
+    place_weights(room, places, a.gamma, a.cols, a.lanes, at.threads);
     __syncthreads();
     const float* const weights = room + lane;
     int turn = 0;
@@ -598,12 +610,12 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
     const int lane = at.lane, group = at.group, groups = at.groups;
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     float* const dgamma = room + places.size();
+    for (int i = static_cast<int>(threadIdx.x); i < groups * places.size(); i += at.threads) dgamma[i] = 0.f;
     wait_for_previous_kernel();
     let_next_kernel_start();
     ShiftedRow<T, kMore> next;
     if (kAhead) next.load(a, static_cast<int64_t>(blockIdx.x) * groups + group, lane);
-    place_weights(room, places, a.gamma, a.cols, a.lanes);
-    for (int i = static_cast<int>(threadIdx.x); i < groups * places.size(); i += at.threads) dgamma[i] = 0.f;
+    place_weights(room, places, a.gamma, a.cols, a.lanes, at.threads);
     __syncthreads();
     const float* const weights = room + lane;
     float* const sums = dgamma + group * places.size() + lane;
