@@ -143,22 +143,22 @@ __device__ __forceinline__ void finish_eight(const RmsForwardArgs<T, W>& a, int6
 template <typename T, bool WHOLE>
 struct RmsInput {
     Eight<T> x[kRowPacks], r[kRowPacks];
-    template <typename W>
+    template <bool ALONE, typename W>
     __device__ __forceinline__ void load(const RmsForwardArgs<T, W>& a, int64_t row, int lane) {
         const bool there = row < a.rows;
 #pragma unroll
         for (int k = 0; k < kRowPacks; ++k) {
             const int c = first_column<WHOLE>(k * a.lanes + lane);
             x[k].template load<WHOLE>(a.x + row * a.ldx + c, there ? a.cols - c : 0);
-            r[k].template load<WHOLE>(a.residual + row * a.ldr + c, there && a.residual ? a.cols - c : 0);
+            if (!ALONE) r[k].template load<WHOLE>(a.residual + row * a.ldr + c, there && a.residual ? a.cols - c : 0);
         }
     }
 };
 
-// Blocks of a forward kernel that share an SM (its registers: 80 a thread, 128 for fp32 rows, 64 with
-// 1024 threads).
-constexpr int forward_blocks_an_sm(int block, int bytes) {
-    const int threads = bytes == 4 ? 512 : 768;
+// Blocks of a forward kernel that an SM's registers hold (80 a thread at most, 128 for fp32 rows, 64 without
+// a residual).
+constexpr int forward_blocks_an_sm(int block, int bytes, bool alone) {
+    const int threads = bytes == 4 ? 512 : alone ? 1024 : 768;
     return block < threads ? threads / block : 1;
 }
 // Whether a lane's registers hold the next row, too.
@@ -168,9 +168,9 @@ constexpr bool kForwardAhead = BLOCK <= (sizeof(T) == 4 ? 512 : 768);
 // A row is held by `lanes` threads, 16 columns each: it is read once, and its sum of squares
 // and results come from registers.  A block goes over rows blockIdx.x, + gridDim.x, ... (BLOCK /
 // lanes at a time); the next row's loads are in flight during the present one's sum (not with
-// 1024 threads, whose registers do not hold two rows).
-template <typename T, typename W, int BLOCK, bool Q8, bool WHOLE>
-__global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK, sizeof(T))) rms_forward_kernel(const RmsForwardArgs<T, W> a) {
+// 1024 threads, whose registers do not hold two rows).  ALONE: no residual.
+template <typename T, typename W, int BLOCK, bool Q8, bool WHOLE, bool ALONE>
+__global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK, sizeof(T), ALONE)) rms_forward_kernel(const RmsForwardArgs<T, W> a) {
     constexpr bool kAhead = kForwardAhead<BLOCK, T>;
     __shared__ float part[2][BLOCK / 32];
     const RowPlace<BLOCK> at(a.lanes);
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK, sizeof(T)))
     let_next_kernel_start();
     int turn = 0;
     RmsInput<T, WHOLE> next;
-    if (kAhead) next.load(a, static_cast<int64_t>(blockIdx.x) * groups + group, lane);
+    if (kAhead) next.template load<ALONE>(a, static_cast<int64_t>(blockIdx.x) * groups + group, lane);
     Eight<W> gamma[kRowPacks];
 #pragma unroll
     for (int k = 0; k < kRowPacks; ++k) {
@@ -193,14 +193,14 @@ __global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK, sizeof(T)))
         RmsInput<T, WHOLE> now;
         if constexpr (kAhead) {
             now = next;
-            next.load(a, row + step, lane);
+            next.template load<ALONE>(a, row + step, lane);
         } else {
-            now.load(a, row, lane);
+            now.template load<ALONE>(a, row, lane);
         }
         Pair squares(0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < kRowPacks; ++k) {
-            if (a.residual) add_eight(now.x[k], now.r[k]);
+            if (!ALONE && a.residual) add_eight(now.x[k], now.r[k]);
             squares = add_squares(now.x[k], squares);
         }
         if (a.total) {
@@ -312,7 +312,7 @@ struct ShiftedInput {
 
 // As rms_forward_kernel, for results of T.
 template <typename T, typename W, int BLOCK>
-__global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK, sizeof(T))) rms_forward_shifted_kernel(const RmsForwardArgs<T, W> a) {
+__global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK, sizeof(T), false)) rms_forward_shifted_kernel(const RmsForwardArgs<T, W> a) {
     constexpr bool kAhead = kForwardAhead<BLOCK, T>;
     extern __shared__ float room[];              // the weights
     __shared__ float part[2][BLOCK / 32];
@@ -790,16 +790,26 @@ bool along(const void* p, int64_t ldp, const void* q, int64_t ldq, int bytes) {
 // Whether a row of few more lanes (a quarter at most) holds it wherever in an Eight it starts.
 bool shiftable(int64_t cols) { return cols + 7 <= kRowColumns && row_lanes(cols + 7) * 4 <= row_lanes(cols) * 5; }
 
-int64_t forward_grid(int64_t rows, int lanes, int bytes, int sms) {
-    const int block = row_block(lanes), groups = block / lanes;
-    return std::min((rows + groups - 1) / groups, static_cast<int64_t>(sms) * forward_blocks_an_sm(block, bytes));
+// Blocks of a forward launch: enough for every row, at most what the SMs hold at once.  Blocks of whole warps
+// below their kernel's size find more room (896 threads of 72 registers), unless that puts more than 50 KB of
+// rows with residuals on their way: 8192 x 5120 has 41 KB an SM, 16384 x 4096 with 48 KB takes 86 us and with
+// 64 KB 91, 16384 x 2560 with 40 KB 53 and with 50 KB 58, rows of 4099 with 32 KB 117 and with 48 KB 85.
+template <typename T, typename W>
+int64_t forward_grid(const RmsForwardArgs<T, W>& a, bool quick, bool few, bool alone, int sms) {
+    const int block = row_block(a.lanes), groups = block / a.lanes;
+    int64_t most = forward_blocks_an_sm(block, sizeof(T), alone);
+    if (sizeof(T) == 2 && quick && !alone && block > kSharedBlock) {
+        most = std::max(896 / block, 1);
+        if (few && a.residual) most = std::min<int64_t>(most, std::max(50000 / (4 * a.cols), 1));
+    }
+    return std::min((a.rows + groups - 1) / groups, sms * most);
 }
 
 template <typename T, typename W>
 gemm_status_t forward_shifted(const RmsForwardArgs<T, W>& a, int sms, Queue queue) {
     return with_block(a.lanes, [&](auto block) {
-        return launch<rms_forward_shifted_kernel<T, W, decltype(block)::value>>(forward_grid(a.rows, a.lanes, sizeof(T), sms),
-                                                                                row_block(a.lanes), columns_bytes(a.lanes), queue, 1, a);
+        return launch<rms_forward_shifted_kernel<T, W, decltype(block)::value>>(forward_grid(a, true, true, false, sms), row_block(a.lanes),
+                                                                                columns_bytes(a.lanes), queue, 1, a);
     });
 }
 
@@ -811,8 +821,16 @@ gemm_status_t forward(const RmsForwardArgs<T, W>& a, int sms, Queue queue) {
     if (a.cols > kRowColumns)
         return launch<rms_forward_wide_kernel<T, W, Q8, WHOLE>>(a.rows, kMostRowLanes, 0, queue, 1, a);
     return with_block(a.lanes, [&](auto block) {
-        return launch<rms_forward_kernel<T, W, decltype(block)::value, Q8, WHOLE>>(forward_grid(a.rows, a.lanes, sizeof(T), sms),
-                                                                                   row_block(a.lanes), 0, queue, 1, a);
+        constexpr int kBlock = decltype(block)::value;
+        // (without a residual there is not enough on its way: 8192 x 8192 bf16 55 us with 768 threads an SM, 45
+        // with 1024; blocks of 257 to 384 threads fit twice either way)
+        if constexpr (sizeof(T) == 2 && WHOLE && !Q8 && kBlock != 384) {
+            if (!a.residual)
+                return launch<rms_forward_kernel<T, W, kBlock, Q8, WHOLE, true>>(forward_grid(a, WHOLE, !Q8, true, sms),
+                                                                                 row_block(a.lanes), 0, queue, 1, a);
+        }
+        return launch<rms_forward_kernel<T, W, kBlock, Q8, WHOLE, false>>(forward_grid(a, WHOLE, !Q8, false, sms),
+                                                                          row_block(a.lanes), 0, queue, 1, a);
     });
 }
 
