@@ -611,7 +611,9 @@ inline FewChoice choose_kernel(int64_t rows, int64_t few_tiles, double pair_wave
         const int64_t ctas = few_tiles * s, slots = static_cast<int64_t>(resident[k] * num_sms);
         const int64_t waves = (ctas + slots - 1) / slots;
         const double kb = (rows <= 32 ? r.kb_32 : r.kb_128) * (ctas > num_sms ? r.shared : 1.0);
-        const double time = with_memory(2 + 0.7 * k + static_cast<double>(waves) * (per * kb + (s > 1 ? 1.0 : 0.5)));
+        // (each further wave starts its CTAs anew: 5632 x 11264 x 64 gated, 26 waves of one k-block, takes 114 us)
+        const double time = with_memory(2 + 0.7 * k + static_cast<double>(waves) * (per * kb + (s > 1 ? 1.0 : 0.5)) +
+                                        3.4 * static_cast<double>(waves - 1));
         if ((best.slices == 0 && few_only) || time < least) {
             best = FewChoice{s, per};
             least = time;
