@@ -291,9 +291,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             raster_tile_fast(p.m_blocks, p.rd, u, &m_blk, &n_blk);
             const int32_t y = (2 * m_blk + static_cast<int32_t>(rank)) * kBM + quad * 32;
             const int32_t x = n_blk * kBN + which * kCols;
-            // 64 columns of the warp's rows, which `place` writes to a buffer of the warp
+            // 64 columns of the warp's rows, which `place` writes to a buffer of the warp.  With two buffers the
+            // wait lets the newest group go on, so that has to be the other buffer's: columns behind the last
+            // are a group, too, an empty one.
             const auto store = [&](int c, auto place) {
-                if (y >= p.M || x + c >= p.N) return;        // (the whole warp)
+                if (y >= p.M || x + c >= p.N) {              // (the whole warp)
+                    if (L::kStoreBufs > 1 && lane == 0) bulk_commit_group();
+                    return;
+                }
                 const uint32_t buf = buf_at + static_cast<uint32_t>(c / 64 * L::kStoreBuf);
                 if (lane == 0) bulk_wait_group_read<L::kStoreBufs - 1>();
                 __syncwarp();
