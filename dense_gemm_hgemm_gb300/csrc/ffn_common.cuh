@@ -87,6 +87,72 @@ __device__ __forceinline__ void store_bytes(uint8_t* p, int n, uint2 v) {
     }
 }
 
+// ---- results anywhere, of rows on the boundaries: neighbouring lanes hold neighbouring packs of W words, and a lane
+// stores what lies between two boundaries, the end of the lane's pack before it and the start of its own.  The first
+// lane of a warp or row and the last one store the rest of theirs element by element.  (All lanes of a warp come here.)
+//   p: where the pack goes, n: elements of the row from there on (none: <= 0), lanes: of the row
+template <typename E, int W>
+__device__ __forceinline__ void store_between(const uint32_t (&w)[W], E* p, int n, int lanes) {
+    constexpr int kUnit = W * 4 < 16 ? W * 4 : 16, kEach = W * 4 / 8;       // bytes between boundaries, of an element
+    constexpr int kBefore = kUnit / 4;                                      // words of the lane before that may be needed
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & (kUnit - 1)), words = off / 4, bits = off % 4 * 8;
+    const int lane = static_cast<int>(threadIdx.x) & (lanes < 32 ? lanes - 1 : 31);
+    uint32_t v[kBefore + W];
+#pragma unroll
+    for (int i = 0; i < kBefore; ++i) v[i] = __shfl_up_sync(0xffffffffu, w[W - kBefore + i], 1);
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[kBefore + i] = w[i];
+    if (n <= 0) return;
+    const bool first = lane == 0, last = lane == (lanes < 32 ? lanes - 1 : 31) || n <= 8;
+    const int here = W * 4 - off;                                           // bytes of the own pack's part
+    if (!first) {
+        // v moved up by off bytes
+        if constexpr (kEach < 4) {
+#pragma unroll
+            for (int i = kBefore + W - 1; i > 0; --i) v[i] = __funnelshift_l(v[i - 1], v[i], bits);
+        }
+#pragma unroll
+        for (int i = kBefore + W - 1; i > 0; --i) v[i] = words & 1 ? v[i - 1] : v[i];
+        char* to = reinterpret_cast<char*>(p) - off;
+        if constexpr (kUnit == 16) {
+#pragma unroll
+            for (int i = kBefore + W - 1; i > 1; --i) v[i] = words & 2 ? v[i - 2] : v[i];
+#pragma unroll
+            for (int i = 0; i < W; i += 4)
+                *reinterpret_cast<uint4*>(to + i * 4) = make_uint4(v[kBefore + i], v[kBefore + i + 1], v[kBefore + i + 2], v[kBefore + i + 3]);
+        } else {
+            *reinterpret_cast<uint2*>(to) = make_uint2(v[kBefore], v[kBefore + 1]);
+        }
+    }
+    if (first || last) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i * kEach < here ? first : last) p[i] = static_cast<E>(w[i * kEach / 4] >> (i * kEach % 4 * 8));
+    }
+}
+// An Eight or eight bytes of a result, placed as its columns (OFF: anywhere, see above).
+template <bool WHOLE, bool OFF, typename T>
+__device__ __forceinline__ void store_result(const Eight<T>& v, T* p, int n, int lanes) {
+    if constexpr (OFF) {
+        constexpr int kWords = 4 * Eight<T>::kParts;
+        uint32_t w[kWords];
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint32_t*>(&v.part[i / 4].raw)[i % 4];
+        store_between(w, reinterpret_cast<typename RawOf<static_cast<int>(sizeof(T))>::type*>(p), n, lanes);
+    } else {
+        v.template store<WHOLE>(p, n);
+    }
+}
+template <bool WHOLE, bool OFF>
+__device__ __forceinline__ void store_result(uint2 v, uint8_t* p, int n, int lanes) {
+    if constexpr (OFF) {
+        const uint32_t w[2] = {v.x, v.y};
+        store_between(w, p, n, lanes);
+    } else {
+        store_bytes<WHOLE>(p, n, v);
+    }
+}
+
 // The largest size among eight numbers (NaN aside, which fmaxf passes over).
 __device__ __forceinline__ float largest(const Pair (&v)[4]) {
     float m = 0.f;

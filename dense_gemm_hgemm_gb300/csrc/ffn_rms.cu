@@ -41,6 +41,13 @@ gemm_status_t with_block(int lanes, F f) {
     if (lanes <= 768) return f(std::integral_constant<int, 768>());
     return f(std::integral_constant<int, kMostRowLanes>());
 }
+// ... and those of the kernels whose results lie off the boundaries, fewer as they are rare.
+template <typename F>
+gemm_status_t with_block_off(int lanes, F f) {
+    if (lanes <= kSharedBlock) return f(std::integral_constant<int, kSharedBlock>());
+    if (lanes <= 512) return f(std::integral_constant<int, 512>());
+    return f(std::integral_constant<int, kMostRowLanes>());
+}
 // A thread's place in such a block.
 template <int BLOCK>
 struct RowPlace {
@@ -85,7 +92,7 @@ struct RmsForwardArgs {
     int64_t ldx, ldr, ldt, ldy, ldq, lds, rows;
     float eps;
     int cols, lanes;
-    bool total_along, y_along;   // (shifted kernels: at x's distance from the 16-byte boundaries)
+    bool total_along, y_along;   // at x's distance from the 16-byte boundaries
 };
 
 // x + residual as it is kept: an fp32 sum (one rounding), rounded to T.
@@ -116,7 +123,7 @@ __device__ __forceinline__ float both(Pair v) {
 }
 
 // y of eight columns from t, and its conversion where Q8 (all lanes of a warp come here).
-template <typename T, typename W, bool Q8, bool WHOLE>
+template <typename T, typename W, bool Q8, bool WHOLE, bool OFF>
 __device__ __forceinline__ void finish_eight(const RmsForwardArgs<T, W>& a, int64_t row, int c, int n, float rstd,
                                              const Eight<T>& t, const Eight<W>& gamma) {
     Pair y[4], w[4];
@@ -131,11 +138,11 @@ __device__ __forceinline__ void finish_eight(const RmsForwardArgs<T, W>& a, int6
     if constexpr (Q8) {
         const float s = scale_of(largest_of_group(largest(y)));
         if (n > 0 && c % kGroup == 0) a.scales[row * a.lds + c / kGroup] = s;
-        store_bytes<WHOLE>(a.q + row * a.ldq + c, n, e4m3_eight(y, 1.f / s));
+        store_result<WHOLE, OFF>(e4m3_eight(y, 1.f / s), a.q + row * a.ldq + c, n, a.lanes);
     } else {
         Eight<T> out;
         out.set(y);
-        out.template store<WHOLE>(a.y + row * a.ldy + c, n);
+        store_result<WHOLE, OFF>(out, a.y + row * a.ldy + c, n, a.lanes);
     }
 }
 
@@ -168,8 +175,9 @@ constexpr bool kForwardAhead = BLOCK <= (sizeof(T) == 4 ? 512 : 768);
 // A row is held by `lanes` threads, 16 columns each: it is read once, and its sum of squares
 // and results come from registers.  A block goes over rows blockIdx.x, + gridDim.x, ... (BLOCK /
 // lanes at a time); the next row's loads are in flight during the present one's sum (not with
-// 1024 threads, whose registers do not hold two rows).  ALONE: no residual.
-template <typename T, typename W, int BLOCK, bool Q8, bool WHOLE, bool ALONE>
+// 1024 threads, whose registers do not hold two rows).  ALONE: no residual.  OFF: results need not be
+// on the boundaries (with WHOLE, which the inputs decide, so that a row's sum has one order wherever results go).
+template <typename T, typename W, int BLOCK, bool Q8, bool WHOLE, bool ALONE, bool OFF>
 __global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK, sizeof(T), ALONE)) rms_forward_kernel(const RmsForwardArgs<T, W> a) {
     constexpr bool kAhead = kForwardAhead<BLOCK, T>;
     __shared__ float part[2][BLOCK / 32];
@@ -207,7 +215,7 @@ __global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK, sizeof(T), 
 #pragma unroll
             for (int k = 0; k < kRowPacks; ++k) {
                 const int c = first_column<WHOLE>(k * a.lanes + lane);
-                now.x[k].template store<WHOLE>(a.total + row * a.ldt + c, there ? a.cols - c : 0);
+                store_result<WHOLE, OFF>(now.x[k], a.total + row * a.ldt + c, there ? a.cols - c : 0, a.lanes);
             }
         }
         const float sum = row_sum<BLOCK>(both(squares), a.lanes, part[turn]);
@@ -217,7 +225,7 @@ __global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK, sizeof(T), 
 #pragma unroll
         for (int k = 0; k < kRowPacks; ++k) {
             const int c = first_column<WHOLE>(k * a.lanes + lane);
-            finish_eight<T, W, Q8, WHOLE>(a, row, c, there ? a.cols - c : 0, rstd, now.x[k], gamma[k]);
+            finish_eight<T, W, Q8, WHOLE, OFF>(a, row, c, there ? a.cols - c : 0, rstd, now.x[k], gamma[k]);
         }
     }
 }
@@ -370,7 +378,7 @@ __global__ void __launch_bounds__(BLOCK, forward_blocks_an_sm(BLOCK, sizeof(T), 
 }
 
 // Longer rows: a block goes over its row twice.
-template <typename T, typename W, bool Q8, bool WHOLE>
+template <typename T, typename W, bool Q8, bool WHOLE, bool OFF>
 __global__ void __launch_bounds__(kMostRowLanes) rms_forward_wide_kernel(const RmsForwardArgs<T, W> a) {
     __shared__ float part[kMostRowLanes / 32];
     const int64_t row = blockIdx.x;
@@ -386,28 +394,30 @@ __global__ void __launch_bounds__(kMostRowLanes) rms_forward_wide_kernel(const R
         if (residual) add_eight(t, r);
     };
     Pair squares(0.f, 0.f);
-    for (int c = first_column<WHOLE>(static_cast<int>(threadIdx.x)); c < a.cols; c += kMostRowLanes * 8) {
+    for (int c0 = 0; c0 < a.cols; c0 += kMostRowLanes * 8) {
+        const int c = c0 + first_column<WHOLE>(static_cast<int>(threadIdx.x)), n = a.cols - c;
+        if (!OFF && n <= 0) break;
         Eight<T> t;
-        sum_at(c, a.cols - c, t);
+        sum_at(c, n, t);
         squares = add_squares(t, squares);
-        if (total) t.template store<WHOLE>(total + c, a.cols - c);
+        if (total) store_result<WHOLE, OFF>(t, total + c, n, kMostRowLanes);
     }
     const float sum = row_sum<kMostRowLanes>(both(squares), kMostRowLanes, part);
     const float rstd = 1.f / sqrtf(sum / static_cast<float>(a.cols) + a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
-    // (a thread reads back only what it wrote: total may be x or the residual.  All lanes of a
-    // warp go through every step: the largest value of a group is taken among them.)
+    // (a thread reads back only what it wrote: total may be x or the residual, and then lies where they do.  All
+    // lanes of a warp go through every step: the largest value of a group is taken among them.)
     for (int c0 = 0; c0 < a.cols; c0 += kMostRowLanes * 8) {
         const int c = c0 + first_column<WHOLE>(static_cast<int>(threadIdx.x)), n = a.cols - c;
         Eight<T> t;
         Eight<W> gamma;
         gamma.template load<WHOLE>(a.gamma + c, a.gamma ? n : 0);
-        if (total) {
+        if (total && (!OFF || a.total_along)) {
             t.template load<WHOLE>(total + c, n);
         } else {
             sum_at(c, n, t);
         }
-        finish_eight<T, W, Q8, WHOLE>(a, row, c, n, rstd, t, gamma);
+        finish_eight<T, W, Q8, WHOLE, OFF>(a, row, c, n, rstd, t, gamma);
     }
 }
 
@@ -424,7 +434,7 @@ struct RmsBackwardArgs {
     float* partial;             // [grid][cols], or NULL: no gradient of gamma wanted
     int64_t ldt, lddy, lddt, lddx, rows;
     int cols, lanes;
-    bool dx_along;               // (shifted kernels: at total's distance from the 16-byte boundaries)
+    bool dx_along;               // at total's distance from the 16-byte boundaries
 };
 
 // What a lane needs of a row, as it is in memory (MORE: dtotal too).
@@ -446,6 +456,12 @@ struct RmsRow {
     }
 };
 
+// v * rstd + what reaches the sum on its other way, with one rounding: written as a product and a sum, the assembler
+// made one operation of them in some kernels and not in others, and the same row had other bits in each.
+__device__ __forceinline__ Pair along_total(Pair v, float rstd, Pair more, const void* dtotal) {
+    return dtotal ? fma2(v, Pair(rstd, rstd), more) : mul2(v, Pair(rstd, rstd));
+}
+
 // Blocks of a backward kernel that share an SM (its registers: 128 a thread).
 constexpr int backward_blocks_an_sm(int block) { return block < 512 ? 512 / block : 1; }
 // Whether a lane's registers hold the next row, too ...
@@ -462,7 +478,7 @@ constexpr bool kBackwardRoom = BLOCK <= 512 && sizeof(T) == 2;
 // flight during the present one's sum (not with 1024 threads, whose registers do not hold two rows;
 // above 512 dtotal is loaded where it is used).  So are gamma, and the weight's gradient is in shared
 // memory, above 512 threads and with fp32 rows, which take twice the registers.
-template <typename T, typename W, int BLOCK, bool WHOLE>
+template <typename T, typename W, int BLOCK, bool WHOLE, bool OFF>
 __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backward_kernel(const RmsBackwardArgs<T, W> a) {
     constexpr bool kAhead = kBackwardAhead<BLOCK, T>, kMore = kBackwardMore<BLOCK>, kRoom = kBackwardRoom<BLOCK, T>;
     extern __shared__ Pair shared[];             // the weight's gradient: of each thread, or of several groups
@@ -536,12 +552,11 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
             now.more[k].get(d);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                g[i] = mul2(fma2(hat[i], Pair(-mean, -mean), g[i]), Pair(now.rstd, now.rstd));
-                if (a.dtotal) g[i] = add2(g[i], d[i]);
+                g[i] = along_total(fma2(hat[i], Pair(-mean, -mean), g[i]), now.rstd, d[i], a.dtotal);
             }
             Eight<T> out;
             out.set(g);
-            out.template store<WHOLE>(a.dx + row * a.lddx + c, n);
+            store_result<WHOLE, OFF>(out, a.dx + row * a.lddx + c, n, a.lanes);
         }
     }
     if (!a.partial) return;
@@ -673,8 +688,7 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
             now.more[k].get(d);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                g[i] = mul2(fma2(hat[i], Pair(-mean, -mean), g[i]), Pair(now.rstd, now.rstd));
-                if (a.dtotal) g[i] = add2(g[i], d[i]);
+                g[i] = along_total(fma2(hat[i], Pair(-mean, -mean), g[i]), now.rstd, d[i], a.dtotal);
             }
             Eight<T> out;
             out.set(g);
@@ -692,7 +706,7 @@ __global__ void __launch_bounds__(BLOCK, backward_blocks_an_sm(BLOCK)) rms_backw
 }
 
 // Longer rows: dx, a row a block, twice over it.
-template <typename T, typename W, bool WHOLE>
+template <typename T, typename W, bool WHOLE, bool OFF>
 __global__ void __launch_bounds__(kMostRowLanes) rms_dx_wide_kernel(const RmsBackwardArgs<T, W> a) {
     __shared__ float part[kMostRowLanes / 32];
     const int64_t row = blockIdx.x;
@@ -712,13 +726,15 @@ __global__ void __launch_bounds__(kMostRowLanes) rms_dx_wide_kernel(const RmsBac
         for (int i = 0; i < 8; ++i) sum = fmaf(a.gamma ? g.get(i) * w.get(i) : g.get(i), t.get(i) * rstd, sum);
     }
     const float mean = row_sum<kMostRowLanes>(sum, kMostRowLanes, part) / static_cast<float>(a.cols);
-    for (int c = first_column<WHOLE>(static_cast<int>(threadIdx.x)); c < a.cols; c += kMostRowLanes * 8) {
+    for (int c0 = 0; c0 < a.cols; c0 += kMostRowLanes * 8) {
+        const int c = c0 + first_column<WHOLE>(static_cast<int>(threadIdx.x)), n = a.cols - c;
+        if (!OFF && n <= 0) break;
         Eight<T> t, g, more;
         Eight<W> w;
-        t.template load<WHOLE>(total + c, a.cols - c);
-        g.template load<WHOLE>(dy + c, a.cols - c);
-        w.template load<WHOLE>(a.gamma + c, a.gamma ? a.cols - c : 0);
-        more.template load<WHOLE>(a.dtotal + row * a.lddt + c, a.dtotal ? a.cols - c : 0);
+        t.template load<WHOLE>(total + c, n);
+        g.template load<WHOLE>(dy + c, n);
+        w.template load<WHOLE>(a.gamma + c, a.gamma ? n : 0);
+        more.template load<WHOLE>(a.dtotal + row * a.lddt + c, a.dtotal ? n : 0);
         Pair hat[4], v[4], by[4], d[4];
         t.get(hat);
         g.get(v);
@@ -732,7 +748,7 @@ __global__ void __launch_bounds__(kMostRowLanes) rms_dx_wide_kernel(const RmsBac
             if (a.dtotal) v[i] = add2(v[i], d[i]);
         }
         g.set(v);
-        g.template store<WHOLE>(a.dx + row * a.lddx + c, a.cols - c);
+        store_result<WHOLE, OFF>(g, a.dx + row * a.lddx + c, n, kMostRowLanes);
     }
 }
 
@@ -816,22 +832,30 @@ gemm_status_t forward_shifted(const RmsForwardArgs<T, W>& a, int sms, Queue queu
 // Shared memory of a gradient's shifted kernel.
 constexpr size_t backward_room(int lanes) { return columns_bytes(lanes) * (1 + row_block(lanes) / lanes); }
 
-template <typename T, typename W, bool Q8, bool WHOLE>
+template <typename T, typename W, bool Q8, bool WHOLE, bool OFF>
 gemm_status_t forward(const RmsForwardArgs<T, W>& a, int sms, Queue queue) {
     if (a.cols > kRowColumns)
-        return launch<rms_forward_wide_kernel<T, W, Q8, WHOLE>>(a.rows, kMostRowLanes, 0, queue, 1, a);
-    return with_block(a.lanes, [&](auto block) {
+        return launch<rms_forward_wide_kernel<T, W, Q8, WHOLE, OFF>>(a.rows, kMostRowLanes, 0, queue, 1, a);
+    const auto go = [&](auto block) {
         constexpr int kBlock = decltype(block)::value;
         // (without a residual there is not enough on its way: 8192 x 8192 bf16 55 us with 768 threads an SM, 45
         // with 1024; blocks of 257 to 384 threads fit twice either way)
-        if constexpr (sizeof(T) == 2 && WHOLE && !Q8 && kBlock != 384) {
+        if constexpr (sizeof(T) == 2 && WHOLE && !Q8 && !OFF && kBlock != 384) {
             if (!a.residual)
-                return launch<rms_forward_kernel<T, W, kBlock, Q8, WHOLE, true>>(forward_grid(a, WHOLE, !Q8, true, sms),
-                                                                                 row_block(a.lanes), 0, queue, 1, a);
+                return launch<rms_forward_kernel<T, W, kBlock, Q8, WHOLE, true, OFF>>(forward_grid(a, WHOLE, !Q8, true, sms),
+                                                                                      row_block(a.lanes), 0, queue, 1, a);
         }
-        return launch<rms_forward_kernel<T, W, kBlock, Q8, WHOLE, false>>(forward_grid(a, WHOLE, !Q8, false, sms),
-                                                                          row_block(a.lanes), 0, queue, 1, a);
-    });
+        return launch<rms_forward_kernel<T, W, kBlock, Q8, WHOLE, false, OFF>>(forward_grid(a, WHOLE, !Q8, false, sms),
+                                                                               row_block(a.lanes), 0, queue, 1, a);
+    };
+    if constexpr (OFF) return with_block_off(a.lanes, go);
+    return with_block(a.lanes, go);
+}
+// whole: the inputs' rows (all on the boundaries, whole packs), off: a result's are not.
+template <typename T, typename W, bool Q8>
+gemm_status_t forward(const RmsForwardArgs<T, W>& a, bool whole, bool off, int sms, Queue queue) {
+    if (!whole) return forward<T, W, Q8, false, false>(a, sms, queue);
+    return off ? forward<T, W, Q8, true, true>(a, sms, queue) : forward<T, W, Q8, true, false>(a, sms, queue);
 }
 
 // Shared memory of the weight's gradient of a block's threads.
@@ -844,13 +868,15 @@ int64_t backward_grid(int64_t rows, int lanes, int sms) {
     return blocks < most ? blocks : most;
 }
 
-template <typename T, typename W, bool WHOLE>
+template <typename T, typename W, bool WHOLE, bool OFF>
 gemm_status_t backward(const RmsBackwardArgs<T, W>& a, int64_t grid, Queue queue) {
-    return with_block(a.lanes, [&](auto block) {
+    const auto go = [&](auto block) {
         constexpr int kBlock = decltype(block)::value;
         const bool shared = kSharedBlock > a.lanes || !kBackwardRoom<kBlock, T>;
-        return launch<rms_backward_kernel<T, W, kBlock, WHOLE>>(grid, row_block(a.lanes), shared ? sums_bytes(kBlock) : 0, queue, 1, a);
-    });
+        return launch<rms_backward_kernel<T, W, kBlock, WHOLE, OFF>>(grid, row_block(a.lanes), shared ? sums_bytes(kBlock) : 0, queue, 1, a);
+    };
+    if constexpr (OFF) return with_block_off(a.lanes, go);
+    return with_block(a.lanes, go);
 }
 
 template <typename T, typename W>
@@ -878,11 +904,12 @@ template <typename T, typename W>
 gemm_status_t prepare() {
     const auto wide = [](auto block) {
         constexpr int kBlock = decltype(block)::value;
-        return allow<rms_backward_kernel<T, W, kBlock, true>>(sums_bytes(kBlock)) &&
-               allow<rms_backward_kernel<T, W, kBlock, false>>(sums_bytes(kBlock)) &&
+        return allow<rms_backward_kernel<T, W, kBlock, true, false>>(sums_bytes(kBlock)) &&
+               allow<rms_backward_kernel<T, W, kBlock, false, false>>(sums_bytes(kBlock)) &&
                allow<rms_backward_shifted_kernel<T, W, kBlock>>(backward_room(kBlock));
     };
     bool ok = wide(std::integral_constant<int, 768>()) && wide(std::integral_constant<int, kMostRowLanes>()) &&
+              allow<rms_backward_kernel<T, W, kMostRowLanes, true, true>>(sums_bytes(kMostRowLanes)) &&
               allow<rms_backward_shifted_kernel<T, W, 384>>(backward_room(384)) &&
               allow<rms_backward_shifted_kernel<T, W, 512>>(backward_room(512));
     if constexpr (sizeof(T) == 2)
@@ -956,8 +983,9 @@ gemm_status_t gemm_rms_forward(gemm_rms_plan_t p, int64_t rows, const void* x, i
     const int e = gbt::elem_bytes(p->elem);
     if (!gbt::aligned(y, e)) return GEMM_ERR_ALIGNMENT;
     if (rows == 0) return GEMM_OK;
+    // (the inputs alone decide which kernel sums their rows, and in which order: the same numbers wherever results go)
     const bool whole = p->cols % 8 == 0 && gbt::rows_aligned(x, ldx, e) && gbt::packs_aligned(residual, ldr, e) &&
-                       gbt::packs_aligned(total, ldt, e) && gbt::rows_aligned(y, ldy, e) && gbt::aligned(gamma, 16);
+                       gbt::aligned(gamma, 16);
     const bool shifted = !whole && gbt::shiftable(p->cols) && gbt::along(x, ldx, residual, ldr, e);
     return gbt::with_types(p, [&](auto t, auto v) {
         using T = decltype(t);
@@ -971,7 +999,7 @@ gemm_status_t gemm_rms_forward(gemm_rms_plan_t p, int64_t rows, const void* x, i
         if constexpr (sizeof(T) == 2) {
             if (shifted) return gbt::forward_shifted<T, W>(a, p->num_sms, queue);
         }
-        return whole ? gbt::forward<T, W, false, true>(a, p->num_sms, queue) : gbt::forward<T, W, false, false>(a, p->num_sms, queue);
+        return gbt::forward<T, W, false>(a, whole, !a.total_along || !a.y_along, p->num_sms, queue);
     });
 }
 
@@ -985,16 +1013,16 @@ gemm_status_t gemm_rms_forward_fp8(gemm_rms_plan_t p, int64_t rows, const void* 
     if (rows == 0) return GEMM_OK;
     const int e = gbt::elem_bytes(p->elem);
     const bool whole = p->cols % 8 == 0 && gbt::rows_aligned(x, ldx, e) && gbt::packs_aligned(residual, ldr, e) &&
-                       gbt::packs_aligned(total, ldt, e) && gbt::bytes_aligned(q, ldq) && gbt::aligned(gamma, 16);
+                       gbt::aligned(gamma, 16);
     return gbt::with_types(p, [&](auto t, auto v) {
         using T = decltype(t);
         using W = decltype(v);
         const gbt::RmsForwardArgs<T, W> a{static_cast<const T*>(x), static_cast<const T*>(residual),
                                           static_cast<const W*>(gamma), static_cast<T*>(total), nullptr,
                                           static_cast<uint8_t*>(q), scales, rstd, ldx, ldr, ldt, 0, ldq, lds, rows, eps,
-                                          static_cast<int>(p->cols), gbt::row_lanes(p->cols), false, false};
+                                          static_cast<int>(p->cols), gbt::row_lanes(p->cols), gbt::along(x, ldx, total, ldt, e), false};
         const gbt::Queue queue{stream, p->device};
-        return whole ? gbt::forward<T, W, true, true>(a, p->num_sms, queue) : gbt::forward<T, W, true, false>(a, p->num_sms, queue);
+        return gbt::forward<T, W, true>(a, whole, !a.total_along || !gbt::bytes_aligned(q, ldq), p->num_sms, queue);
     });
 }
 
@@ -1012,7 +1040,7 @@ gemm_status_t gemm_rms_backward(gemm_rms_plan_t p, int64_t rows, const void* tot
     const gemm_status_t st = gbt::check_device(p->device);
     if (st != GEMM_OK || (!dx && !dgamma)) return st;
     const bool whole = p->cols % 8 == 0 && gbt::rows_aligned(total, ldt, e) && gbt::rows_aligned(dy, lddy, e) &&
-                       gbt::packs_aligned(dtotal, lddt, e) && gbt::packs_aligned(dx, lddx, e) && gbt::aligned(gamma, 16);
+                       gbt::packs_aligned(dtotal, lddt, e) && gbt::aligned(gamma, 16);
     // (a result's place decides nothing but its stores: the same numbers wherever it goes)
     const bool shifted = !whole && gbt::shiftable(p->cols) && gbt::along(total, ldt, dy, lddy, e) &&
                          gbt::along(total, ldt, dtotal, lddt, e);
@@ -1033,15 +1061,17 @@ gemm_status_t gemm_rms_backward(gemm_rms_plan_t p, int64_t rows, const void* tot
                 s = gbt::launch<gbt::rms_dgamma_wide_kernel<T, W>>(tiles, gbt::kJoinThreads, 0, queue, 1, a,
                                                                     static_cast<W*>(dgamma));
             if (s == GEMM_OK && dx && rows > 0)
-                s = whole ? gbt::launch<gbt::rms_dx_wide_kernel<T, W, true>>(rows, gbt::kMostRowLanes, 0, queue, 1, a)
-                          : gbt::launch<gbt::rms_dx_wide_kernel<T, W, false>>(rows, gbt::kMostRowLanes, 0, queue, 1, a);
+                s = !whole         ? gbt::launch<gbt::rms_dx_wide_kernel<T, W, false, false>>(rows, gbt::kMostRowLanes, 0, queue, 1, a)
+                    : a.dx_along ? gbt::launch<gbt::rms_dx_wide_kernel<T, W, true, false>>(rows, gbt::kMostRowLanes, 0, queue, 1, a)
+                                 : gbt::launch<gbt::rms_dx_wide_kernel<T, W, true, true>>(rows, gbt::kMostRowLanes, 0, queue, 1, a);
             return s;
         }
         const int64_t grid = gbt::backward_grid(rows, lanes, p->num_sms);
         if (grid > 0)
             s = shifted ? gbt::backward_shifted<T, W>(a, grid, queue)
-                : whole ? gbt::backward<T, W, true>(a, grid, queue)
-                        : gbt::backward<T, W, false>(a, grid, queue);
+                : !whole     ? gbt::backward<T, W, false, false>(a, grid, queue)
+                : a.dx_along ? gbt::backward<T, W, true, false>(a, grid, queue)
+                             : gbt::backward<T, W, true, true>(a, grid, queue);
         if (s == GEMM_OK && dgamma)
             s = gbt::launch<gbt::rms_dgamma_join_kernel<W>>(tiles, gbt::kJoinThreads, 0, queue, 1, p->partial,
                                                             static_cast<int>(grid), cols, static_cast<W*>(dgamma));

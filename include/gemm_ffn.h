@@ -21,7 +21,8 @@
  * A plan is used with the device current on which it was made, by one thread and on
  * one stream at a time (graphs captured from one plan are replayed one after another).
  * All sums and statistics are fp32; a result is rounded once, to nearest even.
- * Results do not depend on the schedule: the same inputs give the same bits.
+ * Results do not depend on the schedule, nor on where they go: the same inputs give the same
+ * bits (inputs that lie elsewhere to the 16-byte boundaries may be summed in another order).
  */
 #ifndef GB300_GEMM_FFN_H
 #define GB300_GEMM_FFN_H
