@@ -27,7 +27,8 @@ struct QuantArgs {
 // t / 16 + 16 k, or, transposed, 8 (t / 16) + k, so that a column's eight values are eight
 // bytes of a result's row.  That goes through shared memory, its 8-byte units exchanged
 // within a row by `turn` so that no two lanes of a store or a load meet in a bank.
-// WHOLE: of x and of q (see Eight).
+// WHOLE: of x and of q (see Eight).  (Rows and columns of a tile behind 2^31 - 1 elements stay below 2^31: tiles
+// divide it.)
 template <typename T, bool SQUARE, bool TRANSPOSE, bool WHOLE>
 __global__ void __launch_bounds__(kQuantThreads, (sizeof(T) == 2 ? 3 : 2) + (kHeld<SQUARE, TRANSPOSE> == 4 ? 2 : 0))
     quantize_kernel(const QuantArgs a) {
@@ -136,7 +137,7 @@ extern "C" gemm_status_t gemm_fp8_quantize(int64_t rows, int64_t cols, gemm_elem
                                            int64_t ldq, float* scales, int64_t lds, void* stream) {
     using namespace gbt;
     if (!valid_elem(elem) || (kind != GEMM_SCALE_ROW && kind != GEMM_SCALE_SQUARE)) return GEMM_ERR_UNSUPPORTED;
-    if (rows < 0 || cols < 0 || rows > INT32_MAX - kSide || cols > INT32_MAX - kSide || (transpose != 0 && transpose != 1))
+    if (rows < 0 || cols < 0 || rows > INT32_MAX || cols > INT32_MAX || (transpose != 0 && transpose != 1))
         return GEMM_ERR_INVALID_ARG;
     const int64_t down = groups_of(rows), across = groups_of(cols);
     if (down * across > (int64_t{1} << 29)) return GEMM_ERR_INVALID_ARG;
