@@ -24,8 +24,8 @@ from __future__ import annotations
 import ctypes
 
 from . import ACTIVATIONS, GemmError, _check, _stream, library
-from .train import (_INVALID_ARG, _UNSUPPORTED, GEMM_ELEM_F32, _elem, _elem_of, _matrix, _on_device, _Plan, _torch_types,
-                    _vector)
+from . import train
+from .train import _INVALID_ARG, _UNSUPPORTED, GEMM_ELEM_F32, _elem, _elem_of, _on_device, _Plan, _torch_types, _vector
 
 __all__ = ["GEMM_SCALE_ROW", "GEMM_SCALE_SQUARE", "SCALES", "RmsNormPlan", "fp8_quantize", "Fp8Plan", "GatedPlan"]
 
@@ -84,10 +84,27 @@ def _scale_kind(kind) -> int:
     return int(kind)
 
 
+def _needed(t, what):
+    if t is None:
+        raise GemmError(_INVALID_ARG, "%s: a tensor is needed" % what)
+    return t
+
+
+def _rows(t, what) -> int:
+    """The rows of a call's first matrix."""
+    if _needed(t, what).dim() != 2:
+        raise GemmError(_INVALID_ARG, "%s: a matrix is needed" % what)
+    return t.shape[0]
+
+
+def _matrix(t, rows, cols, elem, what):
+    return train._matrix(_needed(t, what), rows, cols, elem, what)
+
+
 def _bytes_matrix(t, rows, cols, what):
     """(address, row stride) of a rows x cols e4m3 matrix with contiguous rows."""
     import torch
-    if t.dtype != torch.float8_e4m3fn:
+    if _needed(t, what).dtype != torch.float8_e4m3fn:
         raise GemmError(_UNSUPPORTED, "%s: %s" % (what, t.dtype))
     return _matrix(t, rows, cols, None, what)
 
@@ -142,7 +159,7 @@ class RmsNormPlan(_FfnPlan):
                                (_RMS_BACKWARD, "gemm_rms_backward")))
 
     def _inputs(self, x, gamma, residual, total, eps):
-        rows, cols = x.shape[0], self.cols
+        rows, cols = _rows(x, "x"), self.cols
         return (rows, *_matrix(x, rows, cols, self._elem, "x"), *_optional(residual, rows, cols, self._elem, "residual"),
                 _vector(gamma, cols, self._weight, "gamma", True), eps,
                 *_optional(total, rows, cols, self._elem, "total"))
@@ -175,7 +192,7 @@ class RmsNormPlan(_FfnPlan):
         the gradient that reaches the sum on its other way."""
         if self._taken(self._enter_backward, "gemm_rms_backward", (total, gamma, rstd, dy, dx, dgamma, dtotal, stream)):
             return
-        rows, cols = total.shape[0], self.cols
+        rows, cols = _rows(total, "total"), self.cols
         _check(library().gemm_rms_backward(
             self.handle, rows, *_matrix(total, rows, cols, self._elem, "total"),
             _vector(gamma, cols, self._weight, "gamma", True), _vector(rstd, rows, GEMM_ELEM_F32, "rstd"),
@@ -207,7 +224,7 @@ def fp8_quantize(x, q, scales, block="row", transpose: bool = False, stream=None
     if _Plan._taken(_quantize_entry(), "gemm_fp8_quantize", (x, q, scales, kind, transpose, stream)):
         return
     _torch_types()
-    if not _on_device(x) or x.dim() != 2:
+    if not _on_device(_needed(x, "x")) or x.dim() != 2:
         raise GemmError(_INVALID_ARG, "x: a matrix on the current device is needed")
     rows, cols = x.shape
     out = (cols, rows) if transpose else (rows, cols)
@@ -266,8 +283,6 @@ class GatedPlan(_ProductPlan):
     def _matrix(self, t, rows, cols, what, may_be_none=False):
         if t is None and may_be_none:
             return None
-        if t is None:
-            raise GemmError(_INVALID_ARG, "%s: a tensor is needed" % what)
         return _whole(t, rows, cols, self._elem, what)
 
     def forward(self, X, W, H, gate_up=None, stream=None) -> None:
