@@ -238,7 +238,9 @@ def fp8_quantize(x, q, scales, block="row", transpose: bool = False, stream=None
 
 class Fp8Plan(_ProductPlan):
     """C = A B^T of e4m3 matrices (A M x K, B N x K) with scales, C of `dtype` ("f16" or "bf16").  A's scales go
-    by rows, B's by squares (`b_scales` "square") or by rows ("row")."""
+    by rows, B's by squares (`b_scales` "square") or by rows ("row").  K is a multiple of 16: a weight gradient over any
+    other number of tokens takes matrices of the next one with zeros behind the tokens, q[:, :tokens] for fp8_quantize
+    (their scales are as many)."""
 
     _destroy, _kind = "gemm_fp8_plan_destroy", "fp8"
 

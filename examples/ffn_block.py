@@ -85,19 +85,24 @@ class Projection:
         def held(rows, cols, square=False):
             return (torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device="cuda"),
                     torch.empty(groups(rows) if square else rows, groups(cols), device="cuda"))
+
+        def along_tokens(rows):
+            # (the product's K is a multiple of 16: zeros stand behind the last token)
+            whole = torch.zeros(rows, -(-tokens // 16) * 16, device="cuda").to(torch.float8_e4m3fn)
+            return whole, whole[:, :tokens], torch.empty(rows, groups(tokens), device="cuda")
         self.gamma = torch.ones(dim, device="cuda")
         self.w, self.w_turned = held(out, dim, True), held(dim, out, True)
         g.fp8_quantize(weight, *self.w, block="square")
         g.fp8_quantize(weight, *self.w_turned, block="square", transpose=True)
-        self.y, self.y_turned = held(tokens, dim), held(dim, tokens)
-        self.d, self.d_turned = held(tokens, out), held(out, tokens)
+        self.y, self.d = held(tokens, dim), held(tokens, out)
+        self.y_turned, self.d_turned = along_tokens(dim), along_tokens(out)
         self.total, self.normed, self.d_normed = (torch.empty(tokens, dim, **BF16) for _ in range(3))
         self.rstd, self.c = torch.empty(tokens, device="cuda"), torch.empty(tokens, out, **BF16)
         self.d_weight = torch.empty(out, dim, **BF16)
         self.norm = g.RmsNormPlan(tokens, dim, "bf16", weight="f32")
         self.product = g.Fp8Plan(tokens, out, dim, "bf16")
         self.to_input = g.Fp8Plan(tokens, dim, out, "bf16")
-        self.to_weight = g.Fp8Plan(out, dim, tokens, "bf16", b_scales="row")
+        self.to_weight = g.Fp8Plan(out, dim, self.d_turned[0].shape[1], "bf16", b_scales="row")
 
     def forward(self, x, residual):
         self.norm.forward_fp8(x, self.gamma, *self.y, self.rstd, residual=residual, total=self.total)
@@ -109,9 +114,10 @@ class Projection:
         g.fp8_quantize(d_c, *self.d)
         self.to_input.run(*self.d, *self.w_turned, self.d_normed)
         self.norm.forward(self.total, self.gamma, self.normed)
-        g.fp8_quantize(d_c, *self.d_turned, transpose=True)
-        g.fp8_quantize(self.normed, *self.y_turned, transpose=True)
-        self.to_weight.run(*self.d_turned, *self.y_turned, self.d_weight)
+        (d, d_tokens, d_scales), (y, y_tokens, y_scales) = self.d_turned, self.y_turned
+        g.fp8_quantize(d_c, d_tokens, d_scales, transpose=True)
+        g.fp8_quantize(self.normed, y_tokens, y_scales, transpose=True)
+        self.to_weight.run(d, d_scales, y, y_scales, self.d_weight)
 
     def check(self):
         for plan in (self.product, self.to_input, self.to_weight):

@@ -129,7 +129,9 @@ typedef struct gemm_fp8_plan *gemm_fp8_plan_t;
  * (GEMM_ELEM_F16 or GEMM_ELEM_BF16).  A's scales go by rows, B's by b_scales: squares
  * (weights) or rows (where both are activations).  K has to be a multiple of 16 and N of
  * 8 (GEMM_ERR_ALIGNMENT); M, N <= 2^31 - 257, K <= 2^31 - 129, and at most 2^27 tiles of
- * 128 x 128 of C.
+ * 128 x 128 of C.  Any other K (a weight gradient's tokens): rows of the next multiple of 16
+ * bytes, zeros behind the K elements in both operands, to whose front gemm_fp8_quantize
+ * converts (ldq); the scales of K elements are as many.
  */
 gemm_status_t gemm_fp8_plan_create(int64_t M, int64_t N, int64_t K, gemm_elem_t out,
                                    gemm_scale_t b_scales, gemm_fp8_plan_t *plan);
