@@ -132,6 +132,8 @@ typedef struct gemm_fp8_plan *gemm_fp8_plan_t;
  * 128 x 128 of C.  Any other K (a weight gradient's tokens): rows of the next multiple of 16
  * bytes, zeros behind the K elements in both operands, to whose front gemm_fp8_quantize
  * converts (ldq); the scales of K elements are as many.
+ * The scales of a group are multiplied in fp32 with each other (squares), or one after the other
+ * with the group's sum (rows): what leaves that type's range on the way is lost.
  */
 gemm_status_t gemm_fp8_plan_create(int64_t M, int64_t N, int64_t K, gemm_elem_t out,
                                    gemm_scale_t b_scales, gemm_fp8_plan_t *plan);
