@@ -517,6 +517,8 @@ gemm_status_t gemm_gated_backward(gemm_gated_plan_t p, const void* X, const void
     if ((dX && some && p->K > 0 && !W) || (dW && some && p->K > 0 && !X)) return GEMM_ERR_INVALID_ARG;
     if (misaligned(X, W, gate_up, dH) || misaligned(dgate_up, dX, dW, nullptr)) return GEMM_ERR_ALIGNMENT;
     const gbt::Queue queue{stream, p->base.device};
+    // (dgate_up is rounded to the type before its two products, whose operands have 16 bits: in bf16 at 4096 x 8192 x
+    // 4096 dX and dW are 2.4e-3 from 64 bits in the norm, 1.7e-3 with 32-bit operands, which would halve the rate or more)
     if (some)
         st = p->elem == GEMM_ELEM_F16 ? gate_grad<__half>(p, gate_up, dH, dgate_up, queue)
                                       : gate_grad<__nv_bfloat16>(p, gate_up, dH, dgate_up, queue);

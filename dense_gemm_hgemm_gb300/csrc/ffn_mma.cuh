@@ -99,7 +99,8 @@ __device__ __forceinline__ bool await(uint32_t bar, uint32_t parity, const Watch
     return wait_phase(bar, parity, w, site);
 }
 
-// sigmoid(g), to fp32 accuracy in relative terms on both sides of zero.
+// sigmoid(g), relative to its value on both sides of zero: within 3.5e-7 for g from -4 up, then with __expf's error,
+// which grows with the argument (1e-6 at -20, 4e-6 at -80; from -87 down its results leave the normal range).
 __device__ __forceinline__ float sigmoid(float g) {
     const float e = __expf(-fabsf(g));
     const float s = __fdividef(1.f, 1.f + e);
@@ -114,7 +115,8 @@ __device__ __forceinline__ float bell(float g) {
 // |g| / sqrt 2 the upper tail is erfc(z) / 2 = exp(-z^2) t Q(t) / 2 with t = 1 / (1 + 0.45 z): a smooth
 // function of t in (0, 1], here a polynomial of degree 7 fitted to erfc(z) exp(z^2) / t for z up to 10
 // (weighted least squares, the weights moved to the largest relative errors; 3.1e-7 at most).
-// With the exponential's rounding 1e-6 for |g| up to 4 and 1.2e-5 at 12.  erfcf took 6 us more of
+// With the exponential's rounding the lower tail is within 1.2e-6 for |g| up to 4, 5.2e-6 up to 8 and 1.3e-5 at 13
+// (below 2^-126 it is zero), which 16-bit results do not show.  erfcf took 6 us more of
 // 1024 x 4096 x 2048 (23 us with SiLU).
 __device__ __forceinline__ float normal_cdf(float g, float e) {
     const float t = __fdividef(1.f, fmaf(0.45f * 0.70710678f, fabsf(g), 1.f));
@@ -128,7 +130,7 @@ __device__ __forceinline__ float normal_cdf(float g, float e) {
     q *= 0.5f * t * e;
     return g < 0.f ? q : 1.f - q;
 }
-// act(g) of gemm_activation_t, with the lower tails to relative accuracy.
+// act(g) of gemm_activation_t, with the lower tails relative to their values (see above).
 template <int ACT>
 __device__ __forceinline__ float gate_fn(float g) {
     if constexpr (ACT == GEMM_ACT_RELU) return fmaxf(g, 0.f) + (g != g ? g : 0.f);
