@@ -97,8 +97,9 @@ static_assert(sizeof(Fp8Ctl<7>) <= 256, "control block");
 //   squares: tiles of 256 columns, two accumulators, or of 128, four.  Four warps take half of the
 //            columns (of one square of scales); a thread has a row, with one factor for them.  A step
 //            of 128 columns is 0.25 us, of 256 it is 512 cycles
-//            of the tensor cores and 128 reads of TMEM and 64 double multiply-adds of a thread:
-//            0.42 us, 2.8 PFLOP/s over one wave (0.34 where the MMAs do not wait for the warps).
+//            of the tensor cores and 128 reads of TMEM and 64 double multiply-adds of a thread: 0.40 to
+//            0.43 us (2048 x 2304 x 16384, one wave of 72 pairs: 54 to 59 us, 2.6 to 2.9 PFLOP/s), 0.45 over 14
+//            waves at the power limit (8192 x 8192 x 8192: 404 us), 0.34 where the MMAs do not wait for the warps.
 //            Accumulators of 128 columns, 32 instead of 16 columns a read and single instead of
 //            double multiply-adds all gave the same.  Nothing may spill: what is stored to local memory
 //            right after its load makes the thread wait for it (0.7 to 1.2 us a step).
@@ -444,8 +445,8 @@ bool prepare() {
 }
 
 // The kernel and, by squares, its tiles' columns: a step of 128 takes 0.6 of one of 256, so they are taken
-// where they make less than 1.6 times the waves (512 x 4096 x 4096: 64 tiles or 32 for 76 pairs, 11.0 and
-// 15.3 us; 1024 x 4096 x 4096: 128 or 64, 18.3 and 16.2; 8192 x 8192 x 8192: 461 and 358).
+// where they make less than 1.6 times the waves (512 x 4096 x 4096: 64 tiles or 32 for 76 pairs, 11.3 and
+// 16.0 us; 1024 x 4096 x 4096: 128 or 64, 19.3 and 17.1; 8192 x 8192 x 8192: 465 and 405).
 void choose(gemm_fp8_plan* p) {
     constexpr FewRates kRates{0.29, 0.33, 1.6, 0.38, 0.5};
     p->choice = FewChoice{0, 0};

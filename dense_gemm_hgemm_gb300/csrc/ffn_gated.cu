@@ -415,7 +415,7 @@ gemm_status_t forward(const gemm_gated_plan* p, const void* X, const void* W, vo
 // The width of the tiles of the kernel of many rows, 64 to 128 columns of H: the one whose waves over the SM
 // pairs take the least, where a tile of width w takes 0.35 + 0.65 w / 128 of a full one (1000 x 3000 x 1000 17.8 us
 // with 128, 15.0 with 80; 1024 x 4096 x 2048 22.7 with 128, 21.1 with 112; from some waves on 128 is best:
-// 4096 x 8192 x 4096 277 against 286).  *waves: what they take, in waves of full tiles.
+// 4096 x 8192 x 4096 277 against 286; inputs in L2 where they fit).  *waves: what they take, in waves of full tiles.
 int tile_width(int64_t M, int64_t F, int num_sms, double* waves) {
     const int64_t pairs = num_sms / 2, rows = (M + 2 * kBM - 1) / (2 * kBM);
     int best = kTileF;

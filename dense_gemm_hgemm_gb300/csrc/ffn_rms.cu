@@ -41,7 +41,8 @@ gemm_status_t with_block(int lanes, F f) {
     if (lanes <= 768) return f(std::integral_constant<int, 768>());
     return f(std::integral_constant<int, kMostRowLanes>());
 }
-// ... and those of the kernels whose results lie off the boundaries, fewer as they are rare.
+// ... and those of the kernels whose results lie off the boundaries, fewer as they are rare (those of 1024 threads
+// spill 8 bytes).
 template <typename F>
 gemm_status_t with_block_off(int lanes, F f) {
     if (lanes <= kSharedBlock) return f(std::integral_constant<int, kSharedBlock>());
@@ -163,7 +164,8 @@ struct RmsInput {
 };
 
 // Blocks of a forward kernel that an SM's registers hold (80 a thread at most, 128 for fp32 rows, 64 without
-// a residual).
+// a residual).  The aligned and the shifted kernels fit them; element by element addresses and masks do not: those
+// kernels spill 32 to 64 bytes a thread, the gradient's 20 to 92.
 constexpr int forward_blocks_an_sm(int block, int bytes, bool alone) {
     const int threads = bytes == 4 ? 512 : alone ? 1024 : 768;
     return block < threads ? threads / block : 1;
